@@ -16,6 +16,8 @@ from ._binding import (  # noqa: F401
     Stack, si_stack_create, si_stack_plan, si_sparse_ffn_decode_stack,
     spax_encode, spax_dense_act, spax_tiered_down, spax_ffn_decode, spax_select_decode,
     spax_encode_rows, spax_gate_up, spax_all_decode,
+    KV, Rope, KvDesc, si_kv_create, si_rope_create, si_kv_append, si_tree_attention, si_kv_accumulate, si_kv_evict,
+    SI_BF16, SI_FP16, SI_DEVERR_WAIT_TIMEOUT, SI_DEVERR_COUNT, SI_DEVERR_RANGE, SI_DEVERR_CACHE,
     SI_OK, SI_ERR_INVALID_ARG, SI_ERR_CUDA, SI_ERR_OOM, SI_ERR_UNSUPPORTED, SI_ERR_DEVICE,
 )
 

@@ -13,7 +13,7 @@ import os
 from . import _build
 
 SI_OK, SI_ERR_INVALID_ARG, SI_ERR_CUDA, SI_ERR_OOM, SI_ERR_UNSUPPORTED, SI_ERR_DEVICE = range(6)
-SI_DEVERR_WAIT_TIMEOUT, SI_DEVERR_COUNT, SI_DEVERR_RANGE = 1, 2, 4
+SI_DEVERR_WAIT_TIMEOUT, SI_DEVERR_COUNT, SI_DEVERR_RANGE, SI_DEVERR_CACHE = 1, 2, 4, 8
 
 # every symbol include/si.h declares, with (restype, argtypes)
 _vp, _i, _d, _ll, _u32p = C.c_void_p, C.c_int, C.c_double, C.c_longlong, C.POINTER(C.c_uint32)
@@ -60,7 +60,24 @@ SIGNATURES = {
     "spax_select_decode": (_i, [_vp, _vp, _vp, _vp, _i, _vp, _d, _d, _vp, _vp, _vp]),
     "spax_gate_up": (_i, [_vp, _vp, _vp, _d, _d, _vp, _vp, _vp, _vp]),
     "spax_all_decode": (_i, [_vp, _vp, _vp, _vp, _d, _d, _d, _d, _vp, _vp, _vp]),
+    "si_kv_create": (_i, [_vp, C.POINTER(_vp)]),
+    "si_kv_destroy": (_i, [_vp]),
+    "si_rope_create": (_i, [_i, C.POINTER(_d), C.POINTER(C.c_uint8), _i, _i, C.POINTER(_vp)]),
+    "si_rope_destroy": (_i, [_vp]),
+    "si_kv_append": (_i, [_vp, _i, _vp, _i, _i, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
+    "si_tree_attention": (_i, [_vp, _i, _i, _i, _vp, _vp, _vp, C.c_float, _vp, _vp, _vp]),
+    "si_kv_accumulate": (_i, [_vp, _i, _i, _i, _vp, _vp, _vp, _vp, _vp, C.c_float, _vp, _vp]),
+    "si_kv_evict": (_i, [_vp, _i, _i, _vp, _vp, _i, _i, _i, _vp, _vp, _vp]),
 }
+
+SI_BF16, SI_FP16 = 0, 1
+
+
+class KvDesc(C.Structure):
+    """si_kv_desc of include/si.h."""
+    _fields_ = [("dtype", _i), ("L", _i), ("B", _i), ("Hkv", _i), ("D", _i), ("cap", _i), ("n_slots", _ll),
+                ("k", _vp), ("v", _vp), ("k_stride", _ll * 4), ("v_stride", _ll * 4),
+                ("table", _vp), ("table_stride", _ll * 3), ("len", _vp), ("acc", _vp), ("acc_stride", _ll * 3)]
 
 _lib = None
 
@@ -486,3 +503,216 @@ def spax_all_decode(down: SpaxLayer, gate: SpaxLayer, up: SpaxLayer, x, in_top, 
                                   float(top_frac), float(mid_frac), _ptr(y, torch.float32, "y"),
                                   _ptr(a_out, torch.float32, "a_out"), _stream(stream)))
     return y
+
+
+# ------------------------------------------------------------------ key/value cache
+
+
+class Rope:
+    """Rotary positions (owns the library handle): n_pairs pairs over n_axes axes."""
+
+    def __init__(self, handle, n_pairs, n_axes):
+        self._h, self.n_pairs, self.n_axes = handle, n_pairs, n_axes
+
+    @property
+    def handle(self):
+        return self._h
+
+    def close(self):
+        if self._h:
+            load().si_rope_destroy(self._h)
+            self._h = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+def si_rope_create(D, base=10000.0, sections=None, interleaved=False, inv_freq=None, axis=None) -> Rope:
+    """Rotary positions for heads of D elements.
+
+    By default all D / 2 pairs turn, pair i by pos * base ** (-2 i / D).
+    `sections` (pairs of each axis, in order; one section by default) says
+    which axis of the positions a pair follows; `axis` (an axis index per
+    pair) says it pair by pair. `inv_freq` (radians per position, one per
+    pair) replaces the default frequencies, and fewer than D / 2 of them leave
+    the elements past the pairs unrotated."""
+    freq = [float(base) ** (-2.0 * i / D) for i in range(D // 2)] if inv_freq is None else [float(f) for f in inv_freq]
+    n = len(freq)
+    if axis is None:
+        sections = [n] if sections is None else [int(c) for c in sections]
+        if sum(sections) != n or min(sections) < 0:
+            raise ValueError("sections must add up to the number of pairs (%d)" % n)
+        axis, n_axes = [a for a, c in enumerate(sections) for _ in range(c)], len(sections)
+    else:
+        axis = [int(a) for a in axis]
+        if len(axis) != n or min(axis) < 0 or max(axis) > 255:
+            raise ValueError("axis needs an index for each of the %d pairs" % n)
+        n_axes = max(axis) + 1
+    if 2 * n > D:
+        raise ValueError("%d pairs exceed D = %d" % (n, D))
+    h = C.c_void_p()
+    _check(load().si_rope_create(n, (C.c_double * n)(*freq), (C.c_uint8 * n)(*axis), n_axes, 1 if interleaved else 0,
+                                 C.byref(h)))
+    return Rope(h, n, n_axes)
+
+
+class KV:
+    """A key/value cache over the caller's tensors (owns the library handle
+    and keeps references to the tensors)."""
+
+    def __init__(self, handle, K, V, table, lens, acc):
+        self._h = handle
+        self.K, self.V, self.table, self.lens, self.acc = K, V, table, lens, acc
+        self.L, self.B, self.Hkv, self.n_slots, self.D = K.shape
+        self.cap = table.shape[3] if table is not None else self.n_slots
+        self.dtype = K.dtype
+
+    @property
+    def handle(self):
+        return self._h
+
+    def close(self):
+        if self._h:
+            load().si_kv_destroy(self._h)
+            self._h = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+def _dev(t, dtype, name, shape=None, ndim=None):
+    """A CUDA tensor of this type (and shape) whose last dimension is contiguous."""
+    if not t.is_cuda:
+        raise ValueError("%s must be a CUDA tensor" % name)
+    if t.dtype != dtype:
+        raise ValueError("%s must have dtype %s, got %s" % (name, dtype, t.dtype))
+    if shape is not None and t.shape != shape:
+        raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
+    if ndim is not None and t.dim() != ndim:
+        raise ValueError("%s must have %d dimensions, got %d" % (name, ndim, t.dim()))
+    if t.stride(-1) != 1 and t.shape[-1] != 1:
+        raise ValueError("the last dimension of %s must be contiguous" % name)
+    return t.data_ptr()
+
+
+def _whole(t, dtype, name, shape):
+    """The same, contiguous throughout; None passes."""
+    if t is None:
+        return None
+    if not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % name)
+    return _dev(t, dtype, name, shape)
+
+
+_Stride3 = _ll * 3
+
+
+def _rows(t, dtype, name, B, T, D):
+    """(pointer, strides, heads) of a [B][T][heads][D] tensor."""
+    p = _dev(t, dtype, name, None, 4)
+    b, n, heads, d = t.shape
+    if b != B or n != T or d != D:
+        raise ValueError("%s must have shape (%d, %d, heads, %d), got %s" % (name, B, T, D, tuple(t.shape)))
+    return p, _Stride3(*t.stride()[:3]), heads
+
+
+def si_kv_create(K, V, table, lens, acc=None) -> KV:
+    """A cache over K, V [L][B][Hkv][n_slots][D] (bf16 or fp16), table int32
+    [L][B][Hkv][cap] (None: entry i is slot i), lens int32 [L][B] and acc fp32
+    [L][B][Hkv][n_slots] (None: no eviction)."""
+    torch = _torch()
+    if K.dtype not in (torch.bfloat16, torch.float16):
+        raise ValueError("K must be bf16 or fp16")
+    d = KvDesc()
+    d.dtype = SI_FP16 if K.dtype == torch.float16 else SI_BF16
+    d.k = _dev(K, K.dtype, "K", None, 5)
+    d.v = _dev(V, K.dtype, "V", K.shape)
+    d.L, d.B, d.Hkv, d.n_slots, d.D = K.shape
+    d.k_stride[:], d.v_stride[:] = K.stride()[:4], V.stride()[:4]
+    d.cap = min(d.n_slots, 2 ** 31 - 1)
+    if table is not None:
+        d.table = _dev(table, torch.int32, "table", None, 4)
+        if table.shape[:3] != K.shape[:3]:
+            raise ValueError("table must have shape (L, B, Hkv, cap), got %s" % (tuple(table.shape),))
+        d.cap = table.shape[3]
+        d.table_stride[:] = table.stride()[:3]
+    d.len = _whole(lens, torch.int32, "lens", K.shape[:2])
+    if acc is not None:
+        d.acc = _dev(acc, torch.float32, "acc", K.shape[:4])
+        d.acc_stride[:] = acc.stride()[:3]
+    h = C.c_void_p()
+    _check(load().si_kv_create(C.byref(d), C.byref(h)))
+    return KV(h, K, V, table, lens, acc)
+
+
+def si_kv_append(kv: KV, rope: Rope, q, k, v, pos, q_out, layer=0, stream=None):
+    """Rotates q [B][T][Hq][D] into q_out and k [B][T][Hkv][D] into the
+    cache, with v, at the first T free slots of every list. pos int32
+    [B][T][n_axes]. q and q_out may be None."""
+    torch = _torch()
+    B, T, D = kv.B, k.shape[1], kv.D
+    kp, ks, hk = _rows(k, kv.dtype, "k", B, T, D)
+    vp, vs, hv = _rows(v, kv.dtype, "v", B, T, D)
+    if hk != kv.Hkv or hv != kv.Hkv:
+        raise ValueError("k and v must have %d heads" % kv.Hkv)
+    qp, qs, hq, op = None, None, 0, None
+    if q is not None:
+        qp, qs, hq = _rows(q, kv.dtype, "q", B, T, D)
+        op = _whole(q_out, kv.dtype, "q_out", q.shape)
+    _check(_lib.si_kv_append(kv._h, layer, rope._h, T, hq, qp, qs, kp, ks, vp, vs,
+                             _whole(pos, torch.int32, "pos", (B, T, rope.n_axes)), op, _stream(stream)))
+    return q_out
+
+
+def si_tree_attention(kv: KV, q, out, mask=None, lse=None, scale=None, layer=0, stream=None):
+    """Attention of the T new tokens q [B][T][Hq][D] over the cache and each
+    other. mask int64 [B][T]: bit j of a node's word says that it sees node j
+    (0: padding; None: a chain). out as q, contiguous; lse fp32 [B][T][Hq]
+    (optional). scale defaults to D ** -0.5."""
+    torch = _torch()
+    B, T, D = kv.B, q.shape[1], kv.D
+    qp, qs, hq = _rows(q, kv.dtype, "q", B, T, D)
+    _check(_lib.si_tree_attention(kv._h, layer, T, hq, qp, qs, _whole(mask, torch.int64, "mask", (B, T)),
+                                  D ** -0.5 if scale is None else scale, _whole(out, kv.dtype, "out", q.shape),
+                                  _whole(lse, torch.float32, "lse", (B, T, hq)), _stream(stream)))
+    return out
+
+
+def si_kv_accumulate(kv: KV, q, lse, mask=None, rows=None, scale=None, acc_out=None, layer=0, stream=None):
+    """Adds to every key's accumulated weight what it received from the
+    counted nodes of q (rows int64 [B], bit t counts node t; None: all), with
+    the lse of si_tree_attention. acc_out fp32 [B][Hkv][n_slots] with the
+    cache's strides, or [1][B][Hkv][n_slots] (None: the cache's acc)."""
+    torch = _torch()
+    B, T, D = kv.B, q.shape[1], kv.D
+    qp, qs, hq = _rows(q, kv.dtype, "q", B, T, D)
+    ap = None
+    if acc_out is not None:
+        ap = _dev(acc_out, torch.float32, "acc_out")
+        if kv.acc is None or acc_out.shape[-3:] != kv.acc.shape[1:] or acc_out.stride()[-3:] != kv.acc.stride()[1:] \
+                or acc_out.numel() != B * kv.Hkv * kv.n_slots:
+            raise ValueError("acc_out must have the shape and strides of one layer of the cache's acc")
+    _check(_lib.si_kv_accumulate(kv._h, layer, T, hq, qp, qs, _whole(lse, torch.float32, "lse", (B, T, hq)),
+                                 _whole(mask, torch.int64, "mask", (B, T)), _whole(rows, torch.int64, "rows", (B,)),
+                                 D ** -0.5 if scale is None else scale, ap, _stream(stream)))
+
+
+def si_kv_evict(kv: KV, T, budget, sinks=0, recent=0, path=None, n_path=None, table_out=None, len_out=None,
+                layer=None, stream=None):
+    """Takes the accepted ones of the T new nodes into the lists and drops the
+    keys with the least accumulated weight beyond `budget` (0: none), but for
+    the first `sinks` and the last `recent`. path int32 [B][T] and n_path int32
+    [B] name the accepted nodes (path None: the first n_path; n_path None:
+    all). All layers, or one. In place unless table_out and len_out are given."""
+    torch = _torch()
+    B = kv.B
+    _check(_lib.si_kv_evict(kv._h, -1 if layer is None else layer, T, _whole(path, torch.int32, "path", (B, T)),
+                            _whole(n_path, torch.int32, "n_path", (B,)), budget, sinks, recent,
+                            _whole(table_out, torch.int32, "table_out", (kv.L, B, kv.Hkv, kv.cap)),
+                            _whole(len_out, torch.int32, "len_out", (kv.L, B)), _stream(stream)))

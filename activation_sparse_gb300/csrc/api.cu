@@ -100,6 +100,7 @@ bool ratios_ok(double delta, double phi, double gamma) {
 
 namespace si {
 void set_error_message(const char* msg) { g_msg = msg; }
+int device_error_word(unsigned** out) { return err_word(out); }
 }  // namespace si
 
 struct si_layer {

@@ -1,0 +1,951 @@
+// attend.cu -- attention of a tree of new tokens over a key/value cache, and
+// the attention weight each cached key receives.
+//
+// A list of keys (one sequence, one cache head) is cut into tiles of 64; the
+// tiles of all lists, in order, are dealt out evenly to the CTAs of one
+// resident grid, so a long context of one sequence and a batch of ragged
+// ones load every SM alike. A CTA walks its tiles with the keys and values
+// of the next ones in flight (16-byte asynchronous copies, gathered through
+// the slot table), and keeps the running maximum and sum of the softmax and
+// the output rows in registers. A list that ends up in one CTA is finished
+// there; the others leave partial rows that a second kernel joins in a fixed
+// order, so results do not depend on timing.
+#include <cuda_fp16.h>
+
+#include <cmath>
+#include <cstring>
+
+#include "common.cuh"
+#include "internal.h"
+
+namespace si {
+
+namespace {
+
+constexpr int KT = 64;             // keys per tile
+constexpr int kThreads = 128;      // four warps
+constexpr float kLog2e = 1.4426950408889634f;
+
+// ------------------------------------------------------------- primitives
+
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool on) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr));
+}
+__device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr));
+}
+
+// d += a (16 x 16) * b (16 x 8), fp32 accumulators
+template <bool FP16>
+__device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    if (FP16)
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+            "{%0, %1, %2, %3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    else
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+            "{%0, %1, %2, %3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+template <bool FP16>
+__device__ __forceinline__ uint32_t pack(float a, float b) {
+    uint32_t w;
+    if (FP16) {
+        const __half2 h = __floats2half2_rn(a, b);
+        w = *reinterpret_cast<const uint32_t*>(&h);
+    } else {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+        w = *reinterpret_cast<const uint32_t*>(&h);
+    }
+    return w;
+}
+
+template <bool FP16>
+__device__ __forceinline__ bool not_finite(uint16_t w) {
+    return FP16 ? (w & 0x7C00u) == 0x7C00u : (w & 0x7F80u) == 0x7F80u;
+}
+
+template <bool FP16>
+__device__ __forceinline__ float widen(uint16_t w) {
+    if (FP16) return __half2float(*reinterpret_cast<const __half*>(&w));
+    return __uint_as_float((uint32_t)w << 16);
+}
+
+// Byte offset of 16-byte unit `unit` of row `row` in a tile of rows of DP
+// 16-bit elements; the unit index is XORed with the row's low bits so that
+// the eight rows of an ldmatrix lie in different banks.
+template <int DP>
+__device__ __forceinline__ uint32_t tile_at(int row, int unit) {
+    return (uint32_t)(row * (DP * 2) + ((unit ^ (row & 7)) * 16));
+}
+
+// --------------------------------------------------------------- schedule
+
+// The lists of one launch: `groups` lists a sequence (cache heads x row
+// blocks), each of ntile(b) tiles.
+struct Plan {
+    int* len;         // [B] live keys (0 where the sequence is out of bounds)
+    int* tot;         // [B] live keys + new nodes (0 likewise)
+    int* first;       // [B + 1] flat index of the sequence's first tile
+};
+
+__device__ __forceinline__ int tiles_of(int tot) { return tot > KT ? (tot + KT - 1) / KT : 1; }
+
+// Fills the plan (all threads; ends with a barrier). Lengths are read once.
+template <int THREADS>
+__device__ void make_plan(const KvView& C, int T, int groups, const Plan& p, unsigned* err, bool report) {
+    for (int b = threadIdx.x; b < C.B; b += THREADS) {
+        const int len = C.len[b];
+        const bool ok = len >= 0 && len <= C.cap - T;
+        if (!ok && report) atomicOr(err, SI_DEVERR_CACHE);
+        p.len[b] = ok ? len : 0;
+        p.tot[b] = ok ? len + T : 0;
+    }
+    __syncthreads();
+    if (threadIdx.x < 32) {
+        int base = 0;
+        for (int b0 = 0; b0 < C.B; b0 += 32) {
+            const int b = b0 + (int)threadIdx.x;
+            const int mine = b < C.B ? tiles_of(p.tot[b]) * groups : 0;
+            int incl = mine;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int v = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+                if ((int)threadIdx.x >= o) incl += v;
+            }
+            if (b < C.B) p.first[b] = base + incl - mine;
+            base += __shfl_sync(0xFFFFFFFFu, incl, 31);
+        }
+        if (threadIdx.x == 0) p.first[C.B] = base;
+    }
+    __syncthreads();
+}
+
+__device__ __forceinline__ int share(int total, int part, int parts) {
+    return (int)((long long)total * part / parts);
+}
+
+// A position in the flat order of tiles.
+struct At {
+    int b, group, tile, ntile;
+};
+
+__device__ __forceinline__ At locate(const Plan& p, int B, int x) {
+    int lo = 0, hi = B - 1;  // last b with first[b] <= x
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (p.first[mid] <= x) lo = mid;
+        else hi = mid - 1;
+    }
+    At a;
+    a.b = lo;
+    a.ntile = tiles_of(p.tot[lo]);
+    const int in = x - p.first[lo];
+    a.group = in / a.ntile;
+    a.tile = in - a.group * a.ntile;
+    return a;
+}
+
+__device__ __forceinline__ void step(const Plan& p, int B, int groups, At& a) {
+    if (++a.tile < a.ntile) return;
+    a.tile = 0;
+    if (++a.group < groups) return;
+    a.group = 0;
+    if (++a.b < B) a.ntile = tiles_of(p.tot[a.b]);
+}
+
+// Ancestor word of node t (mask NULL: a chain).
+__device__ __forceinline__ unsigned long long word_of(const unsigned long long* mask, int T, int b, int t) {
+    return mask ? mask[(long long)b * T + t] : (t >= 63 ? ~0ull : (2ull << t) - 1);
+}
+
+// Slot of list entry i, or -1 where nothing is to be read.
+__device__ __forceinline__ int slot_of(const KvView& C, const int32_t* list, int i, int len, int tot,
+                                       unsigned long long seen, unsigned* err) {
+    if (i >= tot || (i >= len && !(seen >> (i - len) & 1))) return -1;
+    const int slot = list ? list[i] : i;
+    if (slot < 0 || slot >= C.n_slots) {
+        atomicOr(err, SI_DEVERR_CACHE);
+        return -1;
+    }
+    return slot;
+}
+
+// ------------------------------------------------------------- attention
+
+template <int DP>
+struct AttendCfg {
+    static constexpr int kTile = KT * DP * 2;             // bytes of a K or V tile
+    static constexpr int kStages = 3;
+    static constexpr int kRows = DP <= 128 ? 64 : 32;     // query rows a block has at most
+    static constexpr int kQBytes = kRows * DP * 2;
+    static constexpr int kOffQ = kStages * 2 * kTile;
+    static constexpr int kOffPlan = kOffQ + kQBytes;
+    static constexpr int kOffOdd = kOffPlan;              // new nodes whose value row is not finite (a word)
+    static constexpr int smem(int B) { return kOffPlan + 16 + (3 * B + 1) * 4; }
+};
+
+// Floats of one partial: RB rows of output, then their maxima and sums.
+constexpr int part_floats(int rb, int dp) { return rb * (dp + 2); }
+
+// MW row warps x KW key warps = 4: a block of RB = 16 * MW rows; each key
+// warp takes KT / KW keys of every tile with its own softmax state, joined at
+// the end of a list.
+template <int DP, int MW, bool FP16>
+__global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1)
+    k_tree_attention(const __grid_constant__ AttendParams P, int row_blocks) {
+    using Cfg = AttendCfg<DP>;
+    constexpr int KW = 4 / MW;
+    constexpr int RB = 16 * MW;
+    constexpr int WK = KT / KW;          // keys of a tile per warp
+    constexpr int NS = WK / 8;           // n8 score tiles
+    constexpr int KD = DP / 16;          // k steps over D
+    constexpr int UNITS = DP / 8;        // 16-byte units of a row
+    constexpr int ROWS_PER = kThreads / UNITS;  // rows one sweep of the threads copies
+    constexpr int SWEEPS = KT / ROWS_PER;
+    constexpr int S = Cfg::kStages;
+
+    extern __shared__ __align__(128) uint8_t smem[];
+    uint8_t* const tiles = smem;
+    uint8_t* const q_s = smem + Cfg::kOffQ;
+    Plan plan;
+    plan.len = reinterpret_cast<int*>(smem + Cfg::kOffPlan + 16);
+    plan.tot = plan.len + P.c.B;
+    plan.first = plan.tot + P.c.B;
+    unsigned long long* odd_s = reinterpret_cast<unsigned long long*>(smem + Cfg::kOffOdd);
+
+    const KvView& C = P.c;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int mw = warp % MW, kw = warp / MW;
+    const int T = P.T, G = P.G, R = T * G, D = C.D;
+    const int groups = C.Hkv * row_blocks;
+
+    grid_launch_dependents();
+    grid_dependency_wait();
+    make_plan<kThreads>(C, T, groups, plan, P.err, blockIdx.x == 0);
+    const int total = plan.first[C.B];
+    const int x0 = share(total, blockIdx.x, gridDim.x), x1 = share(total, blockIdx.x + 1, gridDim.x);
+    if (x0 >= x1) return;
+
+    const float c2 = P.scale * kLog2e;
+    const int unit = tid % UNITS, row0 = tid / UNITS;
+    const bool unit_on = unit * 8 < D;
+
+    // producer state: slots of the tile to be issued next
+    At pa = locate(plan, C.B, x0);
+    int px = x0;
+    int next_slot[SWEEPS];
+    unsigned long long p_seen = 0;
+    int p_seen_b = -1;
+    auto fetch_slots = [&]() {
+        if (px >= x1) return;
+        const int h = pa.group / row_blocks;
+        const int32_t* list = C.table ? C.table + pa.b * C.tb + h * C.th : nullptr;
+        const int len = plan.len[pa.b], tot = plan.tot[pa.b];
+        const int i0 = pa.tile * KT;
+        if (i0 + KT > len && p_seen_b != pa.b) {  // the tile meets the new nodes: which of them does any row see
+            unsigned long long mine = lane < T ? word_of(P.mask, T, pa.b, lane) : 0;
+            if (lane + 32 < T) mine |= word_of(P.mask, T, pa.b, lane + 32);
+            p_seen = (unsigned long long)__reduce_or_sync(0xFFFFFFFFu, (unsigned)(mine >> 32)) << 32 |
+                     __reduce_or_sync(0xFFFFFFFFu, (unsigned)mine);
+            p_seen_b = pa.b;
+        }
+#pragma unroll
+        for (int j = 0; j < SWEEPS; ++j)
+            next_slot[j] = slot_of(C, list, i0 + row0 + j * ROWS_PER, len, tot, p_seen, P.err);
+    };
+    auto issue = [&]() {
+        if (px < x1) {
+            const int h = pa.group / row_blocks;
+            const uint16_t* kp = static_cast<const uint16_t*>(C.k) + pa.b * C.kb + h * C.kh + unit * 8;
+            const uint16_t* vp = static_cast<const uint16_t*>(C.v) + pa.b * C.vb + h * C.vh + unit * 8;
+            const uint32_t dst = smem_u32(tiles + (px - x0) % S * 2 * Cfg::kTile);
+#pragma unroll
+            for (int j = 0; j < SWEEPS; ++j) {
+                const bool on = unit_on && next_slot[j] >= 0;
+                const long long slot = on ? next_slot[j] : 0;
+                const uint32_t at = tile_at<DP>(row0 + j * ROWS_PER, unit);
+                cp16(dst + at, on ? kp + slot * C.ks : kp - unit * 8, on);
+                cp16(dst + Cfg::kTile + at, on ? vp + slot * C.vs : vp - unit * 8, on);
+            }
+            ++px;
+            step(plan, C.B, groups, pa);
+        }
+        cp_commit();
+        fetch_slots();
+    };
+    fetch_slots();
+    for (int s = 0; s < S - 1; ++s) issue();
+
+    At a = locate(plan, C.B, x0);
+    int segment = 0;
+    for (int x = x0; x < x1; ++segment) {
+        // one list, or the part of it that this CTA has
+        const int b = a.b, h = a.group / row_blocks, rb = a.group % row_blocks;
+        const int len = plan.len[b], tot = plan.tot[b];
+        const int seg_end = min(x1, x + a.ntile - a.tile);
+        const bool whole = a.tile == 0 && seg_end - x == a.ntile;
+
+        // query rows of this block into shared memory (rows past R are zero)
+        __syncthreads();  // the previous list's joins and reads of q_s are over
+        if (tid == 0) *odd_s = 0;
+        for (int i = tid; i < RB * UNITS; i += kThreads) {
+            const int r = i / UNITS, u = i % UNITS, row = rb * RB + r;
+            uint4 val = make_uint4(0, 0, 0, 0);
+            if (row < R && u * 8 < D) {
+                const int t = row / G, g = row - t * G;
+                val = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(P.q) + b * P.qb + t * P.qt +
+                                                      (long long)(h * G + g) * P.qh + u * 8);
+            }
+            *reinterpret_cast<uint4*>(q_s + tile_at<DP>(r, u)) = val;
+        }
+        unsigned long long word[2] = {0, 0};
+        int row[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            row[e] = rb * RB + mw * 16 + e * 8 + (lane >> 2);
+            if (row[e] < R && tot > 0) word[e] = word_of(P.mask, T, b, row[e] / G);
+        }
+        float o[DP / 8][4];
+        float mx[2] = {-INFINITY, -INFINITY}, sum[2] = {0.0f, 0.0f};
+#pragma unroll
+        for (int i = 0; i < DP / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.0f;
+        __syncthreads();
+        uint32_t qf[DP <= 128 ? KD : 1][4];
+        const uint32_t q_addr = smem_u32(q_s);
+        if (DP <= 128) {
+#pragma unroll
+            for (int k = 0; k < KD; ++k)
+                ldsm4(qf[DP <= 128 ? k : 0], q_addr + tile_at<DP>(mw * 16 + (lane & 15), 2 * k + (lane >> 4)));
+        }
+
+        for (; x < seg_end; ++x, ++a.tile) {
+            cp_wait<S - 2>();
+            uint8_t* const stage = tiles + (x - x0) % S * 2 * Cfg::kTile;
+            const bool meets_new = a.tile * KT + KT > len;
+            if (meets_new) {
+                // A node's value row may hold infinities or NaN that only its descendants may
+                // see, and 0 * NaN is NaN: such elements leave the product here (each thread
+                // looks at what it copied itself) and come back below for the rows that see them.
+#pragma unroll 1
+                for (int j = 0; j < SWEEPS; ++j) {
+                    const int node = a.tile * KT + row0 + j * ROWS_PER - len;
+                    if (node < 0 || node >= T) continue;
+                    uint16_t* e = reinterpret_cast<uint16_t*>(stage + Cfg::kTile + tile_at<DP>(row0 + j * ROWS_PER, unit));
+                    bool odd = false;
+                    for (int i = 0; i < 8; ++i)
+                        if (not_finite<FP16>(e[i])) e[i] = 0, odd = true;
+                    if (odd) atomicOr(odd_s, 1ull << node);
+                }
+            }
+            __syncthreads();
+            issue();
+            const uint32_t k_s = smem_u32(stage);
+            const uint32_t v_s = k_s + Cfg::kTile;
+            const int key0 = kw * WK;
+            float s[NS][4];
+#pragma unroll
+            for (int n = 0; n < NS; ++n) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.0f;
+#pragma unroll
+            for (int k = 0; k < KD; ++k) {
+                uint32_t qk[4];
+                if (DP > 128) ldsm4(qk, q_addr + tile_at<DP>(mw * 16 + (lane & 15), 2 * k + (lane >> 4)));
+                const uint32_t(&qa)[4] = DP <= 128 ? qf[DP <= 128 ? k : 0] : qk;
+#pragma unroll
+                for (int n = 0; n < NS; n += 2) {
+                    // keys n*8 .. +15: matrices (keys 0-7, d 0-7), (keys 0-7, d 8-15), (keys 8-15, ...)
+                    uint32_t kf[4];
+                    ldsm4(kf, k_s + tile_at<DP>(key0 + n * 8 + (lane & 7) + ((lane >> 4) << 3), 2 * k + ((lane >> 3) & 1)));
+                    mma<FP16>(s[n], qa, kf[0], kf[1]);
+                    mma<FP16>(s[n + 1], qa, kf[2], kf[3]);
+                }
+            }
+            const int i0 = a.tile * KT + key0;
+            if (i0 + WK > len) {  // the tile meets the new nodes or the list's end
+#pragma unroll
+                for (int n = 0; n < NS; ++n)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int j = i0 + n * 8 + (lane & 3) * 2 + (e & 1) - len;
+                        const bool sees = j < 0 || (j < T && (word[e >> 1] >> (j & 63) & 1));
+                        if (!sees) s[n][e] = -INFINITY;
+                    }
+            }
+            float top[2] = {mx[0], mx[1]};
+#pragma unroll
+            for (int n = 0; n < NS; ++n) {
+                top[0] = fmaxf(top[0], fmaxf(s[n][0], s[n][1]));
+                top[1] = fmaxf(top[1], fmaxf(s[n][2], s[n][3]));
+            }
+            float shift[2], keep[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                top[e] = fmaxf(top[e], __shfl_xor_sync(0xFFFFFFFFu, top[e], 1));
+                top[e] = fmaxf(top[e], __shfl_xor_sync(0xFFFFFFFFu, top[e], 2));
+                // The difference is taken before the scale: scores of the type's lowest value
+                // differ by 0 from their maximum, where a fused s * c2 - top * c2 would be off by the
+                // product's rounding, which at that size is a number of any size.
+                shift[e] = top[e] == -INFINITY ? 0.0f : top[e];  // a row that has seen nothing yet
+                keep[e] = ex2((mx[e] - shift[e]) * c2);
+                mx[e] = top[e];
+                sum[e] *= keep[e];
+            }
+#pragma unroll
+            for (int i = 0; i < DP / 8; ++i) {
+                o[i][0] *= keep[0];
+                o[i][1] *= keep[0];
+                o[i][2] *= keep[1];
+                o[i][3] *= keep[1];
+            }
+#pragma unroll
+            for (int n = 0; n < NS; ++n) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    s[n][e] = ex2((s[n][e] - shift[e >> 1]) * c2);
+                    sum[e >> 1] += s[n][e];
+                }
+            }
+#pragma unroll
+            for (int n = 0; n < NS; n += 2) {
+                // the weights are rounded to the cache's type here: the matrix product takes both sides in one type
+                const uint32_t pf[4] = {pack<FP16>(s[n][0], s[n][1]), pack<FP16>(s[n][2], s[n][3]),
+                                        pack<FP16>(s[n + 1][0], s[n + 1][1]), pack<FP16>(s[n + 1][2], s[n + 1][3])};
+#pragma unroll
+                for (int i = 0; i < DP / 8; i += 2) {
+                    uint32_t vf[4];
+                    ldsm4t(vf, v_s + tile_at<DP>(key0 + n * 8 + (lane & 15), i + (lane >> 4)));
+                    mma<FP16>(o[i], pf, vf[0], vf[1]);
+                    mma<FP16>(o[i + 1], pf, vf[2], vf[3]);
+                }
+            }
+            if (meets_new && *odd_s) {
+                // the value elements taken out above: not finite, so their weight does not matter
+                const int32_t* list = C.table ? C.table + b * C.tb + h * C.th : nullptr;
+                for (int key = 0; key < WK; ++key) {
+                    const int node = i0 + key - len;
+                    if (node < 0 || node >= T || !(*odd_s >> node & 1)) continue;
+                    const long long slot = list ? list[len + node] : len + node;
+                    if (slot < 0 || slot >= C.n_slots) continue;
+                    const uint16_t* src = static_cast<const uint16_t*>(C.v) + b * C.vb + h * C.vh + slot * C.vs;
+#pragma unroll
+                    for (int i = 0; i < DP / 8; ++i) {
+                        const int d = i * 8 + (lane & 3) * 2;
+                        if (d >= D) continue;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const uint16_t w = src[d + (e & 1)];
+                            if (not_finite<FP16>(w) && (word[e >> 1] >> node & 1)) o[i][e] += widen<FP16>(w);
+                        }
+                    }
+                }
+            }
+        }
+        if (a.tile == a.ntile) {
+            a.tile = a.ntile - 1;
+            step(plan, C.B, groups, a);
+        }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            sum[e] += __shfl_xor_sync(0xFFFFFFFFu, sum[e], 1);
+            sum[e] += __shfl_xor_sync(0xFFFFFFFFu, sum[e], 2);
+        }
+
+        // join the key warps: pairwise through the stage that the next copies do not touch yet
+        if (KW > 1) {
+            // q_s holds this list's queries, no longer needed; maxima and sums go there
+            __syncthreads();
+            float* ms = reinterpret_cast<float*>(q_s);  // [KW][RB][2]
+            if ((lane & 3) == 0) {
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int r = mw * 16 + e * 8 + (lane >> 2);
+                    ms[(kw * RB + r) * 2] = mx[e];
+                    ms[(kw * RB + r) * 2 + 1] = sum[e];
+                }
+            }
+            __syncthreads();
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int r = mw * 16 + e * 8 + (lane >> 2);
+                float top = -INFINITY, all = 0.0f;
+                for (int w = 0; w < KW; ++w) top = fmaxf(top, ms[(w * RB + r) * 2]);
+                const float sh = top == -INFINITY ? 0.0f : top;
+                for (int w = 0; w < KW; ++w) all += ms[(w * RB + r) * 2 + 1] * ex2((ms[(w * RB + r) * 2] - sh) * c2);
+                const float f = ex2((mx[e] - sh) * c2);
+#pragma unroll
+                for (int i = 0; i < DP / 8; ++i) o[i][2 * e] *= f, o[i][2 * e + 1] *= f;
+                mx[e] = top;
+                sum[e] = all;
+            }
+            // the output rows, summed in key-warp order through shared memory (the queries' place)
+            float* acc = reinterpret_cast<float*>(q_s);
+            constexpr int kHalf = Cfg::kQBytes / 4 / RB;  // columns that fit at once
+            constexpr int COLS = kHalf < DP ? kHalf : DP;
+            for (int col = 0; col < DP; col += COLS) {
+                for (int w = 1; w < KW; ++w) {
+                    __syncthreads();
+                    if (kw == w) {
+#pragma unroll
+                        for (int i = 0; i < DP / 8; ++i) {
+                            const int cc = i * 8 + (lane & 3) * 2 - col;
+                            if (cc < 0 || cc >= COLS) continue;
+                            const int r = mw * 16 + (lane >> 2);
+                            *reinterpret_cast<float2*>(acc + r * COLS + cc) = make_float2(o[i][0], o[i][1]);
+                            *reinterpret_cast<float2*>(acc + (r + 8) * COLS + cc) = make_float2(o[i][2], o[i][3]);
+                        }
+                    }
+                    __syncthreads();
+                    if (kw == 0) {
+#pragma unroll
+                        for (int i = 0; i < DP / 8; ++i) {
+                            const int cc = i * 8 + (lane & 3) * 2 - col;
+                            if (cc < 0 || cc >= COLS) continue;
+                            const int r = mw * 16 + (lane >> 2);
+                            const float2 u0 = *reinterpret_cast<const float2*>(acc + r * COLS + cc);
+                            const float2 u1 = *reinterpret_cast<const float2*>(acc + (r + 8) * COLS + cc);
+                            o[i][0] += u0.x, o[i][1] += u0.y, o[i][2] += u1.x, o[i][3] += u1.y;
+                        }
+                    }
+                }
+            }
+        }
+        if (kw == 0) {
+            if (whole) {
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    if (row[e] >= R) continue;
+                    const bool empty = word[e] == 0 || sum[e] == 0.0f;
+                    const float inv = empty ? 0.0f : 1.0f / sum[e];
+                    const int t = row[e] / G, g = row[e] - t * G;
+                    const long long at = ((long long)b * T + t) * P.Hq + h * G + g;
+                    uint16_t* dst = static_cast<uint16_t*>(P.out) + at * D;
+#pragma unroll
+                    for (int i = 0; i < DP / 8; ++i) {
+                        const int d = i * 8 + (lane & 3) * 2;
+                        if (d < D)
+                            *reinterpret_cast<uint32_t*>(dst + d) =
+                                empty ? 0u : pack<FP16>(o[i][2 * e] * inv, o[i][2 * e + 1] * inv);
+                    }
+                    if (P.lse && (lane & 3) == 0)
+                        P.lse[at] = empty ? -INFINITY : fmaf(mx[e], P.scale, logf(sum[e]));
+                }
+            } else {
+                float* part = P.part + ((long long)blockIdx.x * 2 + (segment ? 1 : 0)) * part_floats(RB, DP);
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int r = mw * 16 + e * 8 + (lane >> 2);
+#pragma unroll
+                    for (int i = 0; i < DP / 8; ++i)
+                        *reinterpret_cast<float2*>(part + r * DP + i * 8 + (lane & 3) * 2) =
+                            make_float2(o[i][2 * e], o[i][2 * e + 1]);
+                    if ((lane & 3) == 0) {
+                        part[RB * DP + r] = mx[e];
+                        part[RB * DP + RB + r] = sum[e];
+                    }
+                }
+            }
+        }
+    }
+    cp_wait<0>();
+}
+
+// Joins the partial rows of the lists that more than one CTA worked on: one
+// warp per row, the CTAs' parts in order.
+template <int DP, int MW, bool FP16>
+__global__ void __launch_bounds__(128) k_tree_attention_join(const __grid_constant__ AttendParams P, int row_blocks, int parts) {
+    constexpr int RB = 16 * MW;
+    constexpr int E = DP / 32;  // columns a lane
+    extern __shared__ __align__(128) uint8_t smem[];
+    const KvView& C = P.c;
+    Plan plan;
+    plan.len = reinterpret_cast<int*>(smem);
+    plan.tot = plan.len + C.B;
+    plan.first = plan.tot + C.B;
+    const int T = P.T, G = P.G, R = T * G, D = C.D;
+    const int groups = C.Hkv * row_blocks;
+    grid_launch_dependents();
+    grid_dependency_wait();
+    make_plan<128>(C, T, groups, plan, P.err, false);
+    const int total = plan.first[C.B];
+    const int fours = (min(R, RB) + 3) / 4;  // blocks of four rows per list
+    const int list_id = blockIdx.x / fours;
+    const int b = list_id / groups, group = list_id % groups;
+    const int r = blockIdx.x % fours * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    const int h = group / row_blocks, row = group % row_blocks * RB + r;
+    const int n = tiles_of(plan.tot[b]);
+    const int y0 = plan.first[b] + group * n, y1 = y0 + n;  // this list's tiles
+    // the CTA that has tile y: the last one whose share starts at or before it
+    auto owner = [&](int y) {
+        int c = (int)((long long)y * parts / total);
+        while (c + 1 < parts && share(total, c + 1, parts) <= y) ++c;
+        while (share(total, c, parts) > y) --c;
+        return c;
+    };
+    const int first = owner(y0), last = owner(y1 - 1);
+    if (first == last || row >= R || r >= RB) return;
+    const float c2 = P.scale * kLog2e;
+    auto part_of = [&](int c) {
+        const int second = share(total, c, parts) < y0;  // only the first part can follow another list in its CTA
+        return P.part + ((long long)c * 2 + second) * part_floats(RB, DP);
+    };
+    float top = -INFINITY;
+    for (int c = first + lane; c <= last; c += 32) {
+        if (share(total, c, parts) == share(total, c + 1, parts)) continue;
+        top = fmaxf(top, part_of(c)[RB * DP + r]);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+    const float shift = top == -INFINITY ? 0.0f : top;
+    float acc[E] = {}, sum = 0.0f;
+#pragma unroll 4
+    for (int c = first; c <= last; ++c) {
+        if (share(total, c, parts) == share(total, c + 1, parts)) continue;
+        const float* p = part_of(c);
+        const float f = ex2((p[RB * DP + r] - shift) * c2);
+        sum += f * p[RB * DP + RB + r];
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] += f * p[r * DP + e * 32 + lane];
+    }
+    const int t = row / G, g = row - t * G;
+    const bool empty = plan.tot[b] == 0 || word_of(P.mask, T, b, t) == 0 || sum == 0.0f;
+    const float inv = empty ? 0.0f : 1.0f / sum;
+    const long long at = ((long long)b * T + t) * P.Hq + h * G + g;
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+        const int d = e * 32 + lane;
+        if (d >= D) continue;
+        const float v = empty ? 0.0f : acc[e] * inv;
+        uint16_t w;
+        if (FP16) {
+            const __half hv = __float2half_rn(v);
+            w = *reinterpret_cast<const uint16_t*>(&hv);
+        } else {
+            const __nv_bfloat16 hv = __float2bfloat16_rn(v);
+            w = *reinterpret_cast<const uint16_t*>(&hv);
+        }
+        static_cast<uint16_t*>(P.out)[at * D + d] = w;
+    }
+    if (P.lse && lane == 0) P.lse[at] = empty ? -INFINITY : fmaf(top, P.scale, logf(sum));
+}
+
+// ---------------------------------------------------------------- weights
+
+// Rows kept in shared memory at once.
+constexpr int kWeighRows = 64;
+
+template <int DP>
+struct WeighCfg {
+    static constexpr int kTile = KT * DP * 2;
+    static constexpr int kStages = 4;
+    static constexpr int kOffQ = kStages * kTile;
+    static constexpr int kOffRow = kOffQ + kWeighRows * DP * 2;      // lse2 [64], word [64]
+    static constexpr int kOffPlan = kOffRow + kWeighRows * 4 + kWeighRows * 8 + 64 * 4 + 16;
+    static constexpr int smem(int B) { return kOffPlan + (3 * B + 1) * 4; }
+};
+
+// acc_out[slot] = acc[slot] + sum over counted rows of exp(scale * q.k - lse).
+// Keys are the m side of the matrix product and rows the n side, so that a
+// thread sums its keys' weights over the rows in registers. Reads K once;
+// each key belongs to one warp of one CTA, so nothing is joined.
+template <int DP, bool FP16>
+__global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) k_kv_accumulate(const __grid_constant__ AttendParams P) {
+    using Cfg = WeighCfg<DP>;
+    constexpr int KD = DP / 16;
+    constexpr int UNITS = DP / 8;
+    constexpr int ROWS_PER = kThreads / UNITS;
+    constexpr int SWEEPS = KT / ROWS_PER;
+    constexpr int S = Cfg::kStages;
+    extern __shared__ __align__(128) uint8_t smem[];
+    uint8_t* const q_s = smem + Cfg::kOffQ;
+    unsigned long long* word_s = reinterpret_cast<unsigned long long*>(smem + Cfg::kOffRow);
+    float* lse_s = reinterpret_cast<float*>(word_s + kWeighRows);
+    int* node_s = reinterpret_cast<int*>(lse_s + kWeighRows);  // counted nodes, ascending
+    Plan plan;
+    plan.len = reinterpret_cast<int*>(smem + Cfg::kOffPlan);
+    plan.tot = plan.len + P.c.B;
+    plan.first = plan.tot + P.c.B;
+
+    const KvView& C = P.c;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int T = P.T, G = P.G, D = C.D;
+
+    grid_launch_dependents();
+    grid_dependency_wait();
+    make_plan<kThreads>(C, T, C.Hkv, plan, P.err, blockIdx.x == 0);
+    const int total = plan.first[C.B];
+    const int x0 = share(total, blockIdx.x, gridDim.x), x1 = share(total, blockIdx.x + 1, gridDim.x);
+    if (x0 >= x1) return;
+    const float c2 = P.scale * kLog2e;
+    const int unit = tid % UNITS, row0 = tid / UNITS;
+    const bool unit_on = unit * 8 < D;
+
+    At pa = locate(plan, C.B, x0);
+    int px = x0;
+    int next_slot[SWEEPS];
+    auto fetch_slots = [&]() {
+        if (px >= x1) return;
+        const int32_t* list = C.table ? C.table + pa.b * C.tb + pa.group * C.th : nullptr;
+#pragma unroll
+        for (int j = 0; j < SWEEPS; ++j)
+            next_slot[j] = slot_of(C, list, pa.tile * KT + row0 + j * ROWS_PER, plan.tot[pa.b], plan.tot[pa.b], 0, P.err);
+    };
+    auto issue = [&]() {
+        if (px < x1) {
+            const uint16_t* kp = static_cast<const uint16_t*>(C.k) + pa.b * C.kb + pa.group * C.kh + unit * 8;
+            const uint32_t dst = smem_u32(smem + (px - x0) % S * Cfg::kTile);
+#pragma unroll
+            for (int j = 0; j < SWEEPS; ++j) {
+                const bool on = unit_on && next_slot[j] >= 0;
+                cp16(dst + tile_at<DP>(row0 + j * ROWS_PER, unit), on ? kp + next_slot[j] * C.ks : kp - unit * 8, on);
+            }
+            ++px;
+            step(plan, C.B, C.Hkv, pa);
+        }
+        cp_commit();
+        fetch_slots();
+    };
+    fetch_slots();
+    for (int s = 0; s < S - 1; ++s) issue();
+
+    At a = locate(plan, C.B, x0);
+    int have_b = -1, have_h = -1, have_block = -1, n_rows = 0;
+    for (int x = x0; x < x1; ++x, step(plan, C.B, C.Hkv, a)) {
+        cp_wait<S - 2>();
+        __syncthreads();
+        issue();
+        const int b = a.b, h = a.group, len = plan.len[b], tot = plan.tot[b];
+        if (have_b != b) {
+            // counted nodes of this sequence
+            if (warp == 0) {
+                const unsigned long long want = P.rows ? P.rows[b] : ~0ull;
+                int n = 0;
+                for (int t0 = 0; t0 < T; t0 += 32) {
+                    const int t = t0 + lane;
+                    const bool on = t < T && (want >> (t & 63) & 1) && word_of(P.mask, T, b, t) != 0 && tot > 0;
+                    const unsigned who = __ballot_sync(0xFFFFFFFFu, on);
+                    if (on) node_s[n + __popc(who & lanemask_lt())] = t;
+                    n += __popc(who);
+                }
+                if (lane == 0) node_s[64] = n;
+            }
+            __syncthreads();
+            n_rows = node_s[64] * G;
+            have_b = b;
+            have_h = -1;
+        }
+        const uint32_t k_s = smem_u32(smem + (x - x0) % S * Cfg::kTile);
+        uint32_t kf[DP <= 128 ? KD : 1][4];
+        if (DP <= 128) {
+#pragma unroll
+            for (int k = 0; k < KD; ++k)
+                ldsm4(kf[DP <= 128 ? k : 0], k_s + tile_at<DP>(warp * 16 + (lane & 15), 2 * k + (lane >> 4)));
+        }
+        float w[2] = {0.0f, 0.0f};  // keys lane/4 and lane/4 + 8 of the warp's sixteen
+        const int i0 = a.tile * KT + warp * 16 + (lane >> 2);
+        for (int r0 = 0; r0 < n_rows; r0 += kWeighRows) {
+            const int nr = min(kWeighRows, n_rows - r0);
+            if (have_h != h || have_block != r0) {
+                __syncthreads();
+                const int padded = (nr + 7) & ~7;
+                for (int i = tid; i < padded * UNITS; i += kThreads) {
+                    const int r = i / UNITS, u = i % UNITS;
+                    uint4 val = make_uint4(0, 0, 0, 0);
+                    if (r < nr && u * 8 < D) {
+                        const int t = node_s[(r0 + r) / G], g = (r0 + r) % G;
+                        val = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(P.q) + b * P.qb + t * P.qt +
+                                                              (long long)(h * G + g) * P.qh + u * 8);
+                    }
+                    *reinterpret_cast<uint4*>(q_s + tile_at<DP>(r, u)) = val;
+                }
+                for (int r = tid; r < padded; r += kThreads) {
+                    float lse = INFINITY;  // a padding row: exp(-inf) = 0
+                    unsigned long long word = 0;
+                    if (r < nr) {
+                        const int t = node_s[(r0 + r) / G], g = (r0 + r) % G;
+                        lse = P.lse[((long long)b * T + t) * P.Hq + h * G + g];
+                        word = word_of(P.mask, T, b, t);
+                    }
+                    // a row that saw nothing gives nothing
+                    lse_s[r] = lse == -INFINITY ? INFINITY : lse * kLog2e;
+                    word_s[r] = word;
+                }
+                have_h = h;
+                have_block = r0;
+                __syncthreads();
+            }
+            const bool edge = a.tile * KT + warp * 16 + 16 > len;
+            for (int n = 0; n < nr; n += 8) {
+                float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                for (int k = 0; k < KD; k += 2) {
+                    // rows n .. n+7, d 32 wide: two k steps
+                    uint32_t qf[4];
+                    ldsm4(qf, smem_u32(q_s) + tile_at<DP>(n + (lane & 7), 2 * k + (lane >> 3)));
+#pragma unroll
+                    for (int kk = 0; kk < 2; ++kk) {
+                        if (DP > 128) {
+                            uint32_t kx[4];
+                            ldsm4(kx, k_s + tile_at<DP>(warp * 16 + (lane & 15), 2 * (k + kk) + (lane >> 4)));
+                            mma<FP16>(s, kx, qf[2 * kk], qf[2 * kk + 1]);
+                        } else {
+                            mma<FP16>(s, kf[DP <= 128 ? k + kk : 0], qf[2 * kk], qf[2 * kk + 1]);
+                        }
+                    }
+                }
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int r = n + (lane & 3) * 2 + (e & 1);
+                    const int j = i0 + (e >> 1) * 8 - len;
+                    const bool sees = r < nr && (!edge || j < 0 || (j < T && (word_s[r] >> (j & 63) & 1)));
+                    const float p = ex2(fmaf(s[e], c2, -lse_s[r]));
+                    w[e >> 1] += sees ? p : 0.0f;
+                }
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            w[e] += __shfl_xor_sync(0xFFFFFFFFu, w[e], 1);
+            w[e] += __shfl_xor_sync(0xFFFFFFFFu, w[e], 2);
+            const int i = i0 + e * 8;
+            if ((lane & 3) == 0 && i < tot) {
+                const long long slot = C.table ? C.table[b * C.tb + h * C.th + i] : i;
+                if (slot >= 0 && slot < C.n_slots) {
+                    const long long at = b * C.ab + h * C.ah + slot;
+                    P.acc_out[at] = C.acc[at] + w[e];
+                }
+            }
+        }
+    }
+    cp_wait<0>();
+}
+
+// ------------------------------------------------------------------ host
+
+int sm_count() {
+    int dev = 0, sms = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+    if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+    return sms;
+}
+
+cudaError_t launch(const void* fn, dim3 grid, int threads, size_t smem, void** args, cudaStream_t st) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelExC(&cfg, fn, args);
+}
+
+int per_sm(int dp) { return dp <= 128 ? 2 : 1; }
+int padded(int D) { return D <= 64 ? 64 : D <= 128 ? 128 : 256; }
+int row_warps(int R, int dp) { return R <= 16 ? 1 : R <= 32 || dp > 128 ? 2 : 4; }
+
+template <int DP, int MW, bool FP16>
+cudaError_t launch_attend(const AttendParams& P, cudaStream_t st) {
+    const int sms = sm_count();
+    if (sms < 1) return cudaErrorInvalidDevice;
+    const int R = P.T * P.G;
+    int row_blocks = (R + 16 * MW - 1) / (16 * MW);
+    int parts = sms * per_sm(DP);
+    const auto kern = k_tree_attention<DP, MW, FP16>;
+    const auto join = k_tree_attention_join<DP, MW, FP16>;
+    cudaError_t e = allow_max_smem(kern);
+    if (e != cudaSuccess) return e;
+    void* args[2] = {const_cast<AttendParams*>(&P), &row_blocks};
+    e = launch(reinterpret_cast<const void*>(kern), dim3(parts, 1, 1), kThreads, AttendCfg<DP>::smem(P.c.B), args, st);
+    if (e != cudaSuccess) return e;
+    void* jargs[3] = {const_cast<AttendParams*>(&P), &row_blocks, &parts};
+    const int rows = R < 16 * MW ? R : 16 * MW;
+    const long long blocks = (long long)P.c.B * P.c.Hkv * row_blocks * ((rows + 3) / 4);
+    if (blocks > 0x7FFFFFFFLL) return cudaErrorInvalidValue;
+    return launch(reinterpret_cast<const void*>(join), dim3((unsigned)blocks, 1, 1), 128, (3 * P.c.B + 1) * 4, jargs,
+                  st);
+}
+
+template <int DP, bool FP16>
+cudaError_t launch_attend_rows(const AttendParams& P, cudaStream_t st) {
+    switch (row_warps(P.T * P.G, DP)) {
+        case 1: return launch_attend<DP, 1, FP16>(P, st);
+        case 2: return launch_attend<DP, 2, FP16>(P, st);
+        default:
+            if constexpr (DP <= 128) return launch_attend<DP, 4, FP16>(P, st);
+            else return cudaErrorInvalidValue;
+    }
+}
+
+template <bool FP16>
+cudaError_t launch_attend_type(const AttendParams& P, cudaStream_t st) {
+    switch (padded(P.c.D)) {
+        case 64: return launch_attend_rows<64, FP16>(P, st);
+        case 128: return launch_attend_rows<128, FP16>(P, st);
+        default: return launch_attend_rows<256, FP16>(P, st);
+    }
+}
+
+template <int DP, bool FP16>
+cudaError_t launch_weigh(const AttendParams& P, cudaStream_t st) {
+    const int sms = sm_count();
+    if (sms < 1) return cudaErrorInvalidDevice;
+    const auto kern = k_kv_accumulate<DP, FP16>;
+    cudaError_t e = allow_max_smem(kern);
+    if (e != cudaSuccess) return e;
+    void* args[1] = {const_cast<AttendParams*>(&P)};
+    return launch(reinterpret_cast<const void*>(kern), dim3(sms * per_sm(DP), 1, 1), kThreads,
+                  WeighCfg<DP>::smem(P.c.B), args, st);
+}
+
+template <bool FP16>
+cudaError_t launch_weigh_type(const AttendParams& P, cudaStream_t st) {
+    switch (padded(P.c.D)) {
+        case 64: return launch_weigh<64, FP16>(P, st);
+        case 128: return launch_weigh<128, FP16>(P, st);
+        default: return launch_weigh<256, FP16>(P, st);
+    }
+}
+
+}  // namespace
+
+long long attend_partial_floats(int D, int T, int G) {
+    const int sms = sm_count();
+    return 2ll * sms * per_sm(padded(D)) * part_floats(16 * row_warps(T * G, padded(D)), padded(D));
+}
+
+cudaError_t launch_tree_attention(const AttendParams& P, cudaStream_t st) {
+    return P.c.fp16 ? launch_attend_type<true>(P, st) : launch_attend_type<false>(P, st);
+}
+
+cudaError_t launch_kv_accumulate(const AttendParams& P, cudaStream_t st) {
+    return P.c.fp16 ? launch_weigh_type<true>(P, st) : launch_weigh_type<false>(P, st);
+}
+
+}  // namespace si

@@ -108,6 +108,7 @@ int si_sparse_layers(int L, int first, int last, uint8_t *sparse, int *n_sparse)
 #define SI_DEVERR_WAIT_TIMEOUT 1u   /* a bounded mbarrier wait ran out */
 #define SI_DEVERR_COUNT 2u          /* an index or count check failed (bad S / tier list, count mismatch) */
 #define SI_DEVERR_RANGE 4u          /* a decode partial exceeded a fixed-point accumulator's range (|y| >= 2^23) */
+#define SI_DEVERR_CACHE 8u          /* a cache list left its bounds (len + T > cap, a slot outside the pool) */
 /* With SI_DEVERR_WAIT_TIMEOUT, bits 8-15 name the kernel whose wait ran out
  * (1 sparse decode, 2 dense activation pass, 3 tiered down-projection,
  * 4 activation GEMM, 5 decode stack) and bits 16-19 the barrier (1 stage
@@ -486,6 +487,148 @@ int spax_gate_up(const spax_layer *gate, const spax_layer *up, const uint16_t *x
 int spax_all_decode(spax_layer *down, const spax_layer *gate, const spax_layer *up, const uint16_t *x,
                     double in_top_frac, double in_mid_frac, double top_frac, double mid_frac, float *y,
                     float *a_out, void *stream);
+
+/* ------------------------------------- key/value cache and its attention */
+
+/* The other half of a decoder layer: attention over a key/value cache, in
+ * the manner of the FFN's computed set. What a sequence's head attends to is
+ * an index list, the order of the keys in memory is free, and dropping a key
+ * edits the list alone.
+ *
+ * A cache holds, for L layers, B sequences and Hkv heads,
+ *   k, v    [L][B][Hkv][n_slots][D] bf16 or fp16: slot s of a head;
+ *   table   int32 [L][B][Hkv][cap], a permutation of slots per list: its
+ *           first len[l][b] entries are the live keys in the order they were
+ *           added, the rest are free slots;
+ *   len     int32 [L][B];
+ *   acc     (optional) fp32 [L][B][Hkv][n_slots]: the attention weight the
+ *           key in a slot has received so far.
+ * One step with T new (or drafted) tokens is
+ *   si_kv_append       rotates q and k, writes k and v into the first T free
+ *                      slots (list entries len .. len + T - 1);
+ *   si_tree_attention  the T tokens over the live keys and each other;
+ *   si_kv_accumulate   adds the weight that each key received from the
+ *                      tokens that count (the accepted ones) to acc;
+ *   si_kv_evict        takes the accepted path into the live list and drops
+ *                      the keys with the least weight beyond a budget.
+ * The lists and lengths live on the device: a step reads nothing back. */
+#define SI_BF16 0
+#define SI_FP16 1
+
+typedef struct si_kv si_kv;
+typedef struct si_rope si_rope;
+
+/* Memory of a cache (the caller's, kept alive as long as the handle).
+ * Strides are in elements; the last dimension of every array is contiguous.
+ *   k_stride / v_stride  {layer, sequence, head, slot}, multiples of 8; k and
+ *     v 16-byte aligned. A sequence stride of 0 with tables that share no
+ *     slot makes one pool for all sequences.
+ *   table_stride {layer, sequence, head}. table NULL: entry i is slot i (a
+ *     cache that never evicts; needs cap <= n_slots).
+ *   acc_stride {layer, sequence, head} (acc may be NULL).
+ *   len int32 [L][B] contiguous.
+ * 8 <= D <= 256, D % 8 == 0; 1 <= B <= 1024; L, Hkv, cap, n_slots >= 1. */
+typedef struct si_kv_desc {
+    int dtype;                /* SI_BF16 or SI_FP16 */
+    int L, B, Hkv, D;
+    int cap;                  /* entries per list */
+    long long n_slots;        /* slots per head: every table entry is below it */
+    void *k, *v;
+    long long k_stride[4], v_stride[4];
+    int32_t *table;
+    long long table_stride[3];
+    int32_t *len;
+    float *acc;
+    long long acc_stride[3];
+} si_kv_desc;
+
+/* A handle over the caller's cache. It owns the scratch of the calls below,
+ * made on their first use (run a call once before capturing it; a larger
+ * call may need more). si_kv_destroy synchronises the device first. */
+int si_kv_create(const si_kv_desc *desc, si_kv **out);
+int si_kv_destroy(si_kv *kv);
+
+/* Rotary positions with several axes (text has one, images and video have
+ * time, height, width). Pair i < n_pairs turns by pos[axis[i]] * inv_freq[i]
+ * radians: (a, b) -> (a cos - b sin, b cos + a sin). Elements past
+ * 2 * n_pairs are not rotated. Pairs are (i, i + n_pairs), or with
+ * interleaved != 0 (2i, 2i + 1).
+ *   inv_freq (host) [n_pairs], |inv_freq| <= 2^20; axis (host) [n_pairs], each < n_axes.
+ * The angle is reduced in 64-bit fixed point, so a far position (any int32)
+ * is as exact as a near one. Requires n_pairs % 8 == 0, 8 <= n_pairs <= 128,
+ * 1 <= n_axes <= 4. Host only: no CUDA call. */
+int si_rope_create(int n_pairs, const double *inv_freq, const uint8_t *axis, int n_axes,
+                   int interleaved, si_rope **out);
+int si_rope_destroy(si_rope *rope);
+
+/* Rotates the new tokens' queries and keys and writes keys and values into
+ * the first T free slots of each list: token t of sequence b goes to slot
+ * table[l][b][h][len[l][b] + t]; acc of that slot (if any) becomes 0; len
+ * stays. q [B][T][Hq][D], k and v [B][T][Hkv][D] with strides {sequence,
+ * token, head} in elements (multiples of 8, 16-byte aligned bases: slices of
+ * one fused projection are fine); pos int32 [B][T][n_axes]; q_out
+ * [B][T][Hq][D] contiguous receives the rotated queries (may be q itself when q
+ * is contiguous). All in the cache's type, computed in fp32, rounded once.
+ * Hq = 0 (q, q_out NULL) writes keys and values only. T >= 1. A sequence
+ * with len + T > cap, or a table entry outside [0, n_slots), sets
+ * SI_DEVERR_CACHE and is not written. Requires 2 * n_pairs <= D. */
+int si_kv_append(si_kv *kv, int layer, const si_rope *rope, int T, int Hq,
+                 const void *q, const long long *q_stride, const void *k, const long long *k_stride,
+                 const void *v, const long long *v_stride, const int32_t *pos, void *q_out,
+                 void *stream);
+
+/* Attention of T <= 64 new tokens, the nodes of a tree of drafted tokens
+ * (T = 1: plain decoding), over a cache that si_kv_append has written them
+ * to. Node t of sequence b sees every live key (entries below len) and node
+ * j (entry len + j) if bit j of mask[b][t] is set; a node's word holds its
+ * ancestors and itself. A word of 0 marks a padding node: its output is 0 and
+ * its lse -inf, and what its key and value hold never matters. mask NULL: a
+ * chain (node t sees nodes 0..t). Query head h reads cache head
+ * h / (Hq / Hkv).
+ *   q [B][T][Hq][D], strides {sequence, token, head} as for si_kv_append;
+ *   scale > 0 multiplies the products; out [B][T][Hq][D] contiguous, in the
+ *   cache's type (may not be q); lse (optional) fp32 [B][T][Hq]: the log of
+ *   the sum of exp(scale * q.k) over the keys seen.
+ * Products and sums in fp32 on the tensor cores; the softmax weights are
+ * rounded to the cache's type for the product with v. Results do not depend
+ * on timing. Requires Hq % Hkv == 0, 1 <= T <= 64. A sequence with
+ * len + T > cap sets SI_DEVERR_CACHE and gets zeros. */
+int si_tree_attention(si_kv *kv, int layer, int T, int Hq, const void *q, const long long *q_stride,
+                      const uint64_t *mask, float scale, void *out, float *lse, void *stream);
+
+/* Attention weight per key: for every list entry i < len + T of every head,
+ *   acc_out[slot] = acc[slot] + sum over counted nodes t and the head's query
+ *   heads g of exp(scale * q_tg . k_i - lse_tg), over nodes that see the key.
+ * rows (uint64 [B]): bit t set counts node t (the accepted path, known after
+ * verification); NULL counts all. q, mask, scale as given to
+ * si_tree_attention, lse fp32 [B][T][Hq] as it returned. acc_out: same
+ * layout as the cache's acc of one layer ([B][Hkv][n_slots], the cache's
+ * strides), NULL: the cache's acc itself. Requires a cache with acc. */
+int si_kv_accumulate(si_kv *kv, int layer, int T, int Hq, const void *q, const long long *q_stride,
+                     const float *lse, const uint64_t *mask, const uint64_t *rows, float scale,
+                     float *acc_out, void *stream);
+
+/* Acceptance and eviction, every layer (layer = -1) or one. The candidates
+ * of a list are its live entries, then the accepted ones of the T nodes that
+ * si_kv_append added: nodes path[b][0 .. n_path[b]) in that order (path
+ * NULL: the first n_path[b] nodes; n_path NULL: all T). With n candidates and
+ * budget > 0, n > budget, the first `sinks` and the last `recent` are kept,
+ * and of the rest the ones with the largest acc (ties to the earlier
+ * candidate; NaN counts as the smallest) until `budget` are kept. budget = 0
+ * keeps all. The list then holds the kept candidates in candidate order
+ * (their number is the new len), the evicted ones, the nodes that were not
+ * accepted, and the free slots as before. No key or value moves.
+ *   path int32 [B][T] (distinct, in [0, T); needs T <= 64), n_path int32 [B]
+ *   (0 .. T); T may be 0 (no new nodes);
+ *   table_out, len_out: the cache's table and len when NULL (in place), else
+ *   contiguous int32 [L][B][Hkv][cap] and [L][B] (one layer: that layer's
+ *   place in them), written in full; neither may overlap the cache's own.
+ * Requires a table; acc when budget > 0; 0 <= sinks, recent and
+ * sinks + recent <= budget when budget > 0; cap <= 196608. A sequence whose
+ * path or n_path is not valid accepts nothing and sets SI_DEVERR_COUNT; one
+ * with len + T > cap is left as it is and sets SI_DEVERR_CACHE. */
+int si_kv_evict(si_kv *kv, int layer, int T, const int32_t *path, const int32_t *n_path, int budget,
+                int sinks, int recent, int32_t *table_out, int32_t *len_out, void *stream);
 
 #ifdef __cplusplus
 }

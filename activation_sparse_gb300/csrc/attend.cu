@@ -12,6 +12,7 @@
 // order, so results do not depend on timing.
 #include <cuda_fp16.h>
 
+#include <climits>
 #include <cmath>
 #include <cstring>
 
@@ -183,16 +184,21 @@ __device__ __forceinline__ unsigned long long word_of(const unsigned long long* 
     return mask ? mask[(long long)b * T + t] : (t >= 63 ? ~0ull : (2ull << t) - 1);
 }
 
-// Slot of list entry i, or -1 where nothing is to be read.
-__device__ __forceinline__ int slot_of(const KvView& C, const int32_t* list, int i, int len, int tot,
-                                       unsigned long long seen, unsigned* err) {
-    if (i >= tot || (i >= len && !(seen >> (i - len) & 1))) return -1;
-    const int slot = list ? list[i] : i;
-    if (slot < 0 || slot >= C.n_slots) {
-        atomicOr(err, SI_DEVERR_CACHE);
-        return -1;
-    }
-    return slot;
+constexpr int kNoSlot = INT_MIN;
+
+// Slot of list entry i, or kNoSlot where nothing is to be read. The value is not
+// looked at here: it is used a tile later, so the load's latency is hidden.
+__device__ __forceinline__ int slot_of(const int32_t* list, int i, int len, int tot, unsigned long long seen) {
+    const bool on = i < len || (i < tot && (seen >> ((i - len) & 63) & 1));
+    if (!on) return kNoSlot;
+    return list ? list[i] : i;
+}
+
+// A slot outside the pool is reported and not read.
+__device__ __forceinline__ bool slot_ok(int slot, int n_slots, unsigned* err) {
+    if ((unsigned)slot < (unsigned)n_slots) return true;
+    if (slot != kNoSlot) atomicOr(err, SI_DEVERR_CACHE);
+    return false;
 }
 
 // ------------------------------------------------------------- attention
@@ -276,7 +282,7 @@ __global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1)
         }
 #pragma unroll
         for (int j = 0; j < SWEEPS; ++j)
-            next_slot[j] = slot_of(C, list, i0 + row0 + j * ROWS_PER, len, tot, p_seen, P.err);
+            next_slot[j] = slot_of(list, i0 + row0 + j * ROWS_PER, len, tot, p_seen);
     };
     auto issue = [&]() {
         if (px < x1) {
@@ -286,7 +292,7 @@ __global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1)
             const uint32_t dst = smem_u32(tiles + (px - x0) % S * 2 * Cfg::kTile);
 #pragma unroll
             for (int j = 0; j < SWEEPS; ++j) {
-                const bool on = unit_on && next_slot[j] >= 0;
+                const bool on = slot_ok(next_slot[j], (int)C.n_slots, P.err) && unit_on;
                 const long long slot = on ? next_slot[j] : 0;
                 const uint32_t at = tile_at<DP>(row0 + j * ROWS_PER, unit);
                 cp16(dst + at, on ? kp + slot * C.ks : kp - unit * 8, on);
@@ -711,7 +717,7 @@ __global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) k_kv_accumulate(c
         const int32_t* list = C.table ? C.table + pa.b * C.tb + pa.group * C.th : nullptr;
 #pragma unroll
         for (int j = 0; j < SWEEPS; ++j)
-            next_slot[j] = slot_of(C, list, pa.tile * KT + row0 + j * ROWS_PER, plan.tot[pa.b], plan.tot[pa.b], 0, P.err);
+            next_slot[j] = slot_of(list, pa.tile * KT + row0 + j * ROWS_PER, plan.tot[pa.b], plan.tot[pa.b], 0);
     };
     auto issue = [&]() {
         if (px < x1) {
@@ -719,7 +725,7 @@ __global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) k_kv_accumulate(c
             const uint32_t dst = smem_u32(smem + (px - x0) % S * Cfg::kTile);
 #pragma unroll
             for (int j = 0; j < SWEEPS; ++j) {
-                const bool on = unit_on && next_slot[j] >= 0;
+                const bool on = slot_ok(next_slot[j], (int)C.n_slots, P.err) && unit_on;
                 cp16(dst + tile_at<DP>(row0 + j * ROWS_PER, unit), on ? kp + next_slot[j] * C.ks : kp - unit * 8, on);
             }
             ++px;

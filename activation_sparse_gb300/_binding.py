@@ -116,9 +116,15 @@ def _check(rc):
 
 # ------------------------------------------------------------------ helpers
 
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 def _ptr(t, dtype=None, name="tensor"):
@@ -134,10 +140,21 @@ def _ptr(t, dtype=None, name="tensor"):
     return C.c_void_p(t.data_ptr())
 
 
+_raw_stream = None
+
+
 def _stream(stream=None):
-    torch = _torch()
-    s = torch.cuda.current_stream() if stream is None else stream
-    return C.c_void_p(s.cuda_stream)
+    """The given stream's handle, or that of torch's current stream on the current device."""
+    global _raw_stream
+    if stream is not None:
+        return C.c_void_p(stream.cuda_stream)
+    if _raw_stream is None:
+        cuda = _torch().cuda
+        cuda.init()
+        get, dev = (getattr(_torch()._C, n, None) for n in ("_cuda_getCurrentRawStream", "_cuda_getDevice"))
+        # torch.cuda.current_stream() builds a stream object (4 us); the raw handle is all that is needed
+        _raw_stream = (lambda: get(dev())) if get and dev else (lambda: cuda.current_stream().cuda_stream)
+    return _raw_stream()
 
 
 def _bf16(t, name):
@@ -602,24 +619,29 @@ def _dev(t, dtype, name, shape=None, ndim=None):
 
 
 def _whole(t, dtype, name, shape):
-    """The same, contiguous throughout; None passes."""
+    """The pointer of a contiguous CUDA tensor of this type and shape; None passes."""
     if t is None:
         return None
-    if not t.is_contiguous():
+    # one look at what a decode step has right; _dev says what is wrong
+    if not (t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.is_cuda):
+        _dev(t, dtype, name, shape)
         raise ValueError("%s must be contiguous" % name)
-    return _dev(t, dtype, name, shape)
+    return t.data_ptr()
 
 
 _Stride3 = _ll * 3
 
 
-def _rows(t, dtype, name, B, T, D):
-    """(pointer, strides, heads) of a [B][T][heads][D] tensor."""
-    p = _dev(t, dtype, name, None, 4)
+def _rows(t, kv, name, T):
+    """(pointer, strides, heads) of a [B][T][heads][D] tensor of the cache's type."""
+    if t.dim() != 4 or not (t.dtype is kv.dtype and t.is_cuda):
+        _dev(t, kv.dtype, name, None, 4)
     b, n, heads, d = t.shape
-    if b != B or n != T or d != D:
-        raise ValueError("%s must have shape (%d, %d, heads, %d), got %s" % (name, B, T, D, tuple(t.shape)))
-    return p, _Stride3(*t.stride()[:3]), heads
+    sb, st, sh, one = t.stride()
+    if b != kv.B or n != T or d != kv.D or one != 1:
+        raise ValueError("%s must have shape (%d, %d, heads, %d) with contiguous heads, got %s with strides %s"
+                         % (name, kv.B, T, kv.D, tuple(t.shape), t.stride()))
+    return t.data_ptr(), _Stride3(sb, st, sh), heads
 
 
 def si_kv_create(K, V, table, lens, acc=None) -> KV:
@@ -656,17 +678,17 @@ def si_kv_append(kv: KV, rope: Rope, q, k, v, pos, q_out, layer=0, stream=None):
     cache, with v, at the first T free slots of every list. pos int32
     [B][T][n_axes]. q and q_out may be None."""
     torch = _torch()
-    B, T, D = kv.B, k.shape[1], kv.D
-    kp, ks, hk = _rows(k, kv.dtype, "k", B, T, D)
-    vp, vs, hv = _rows(v, kv.dtype, "v", B, T, D)
+    T = k.shape[1]
+    kp, ks, hk = _rows(k, kv, "k", T)
+    vp, vs, hv = _rows(v, kv, "v", T)
     if hk != kv.Hkv or hv != kv.Hkv:
         raise ValueError("k and v must have %d heads" % kv.Hkv)
     qp, qs, hq, op = None, None, 0, None
     if q is not None:
-        qp, qs, hq = _rows(q, kv.dtype, "q", B, T, D)
+        qp, qs, hq = _rows(q, kv, "q", T)
         op = _whole(q_out, kv.dtype, "q_out", q.shape)
     _check(_lib.si_kv_append(kv._h, layer, rope._h, T, hq, qp, qs, kp, ks, vp, vs,
-                             _whole(pos, torch.int32, "pos", (B, T, rope.n_axes)), op, _stream(stream)))
+                             _whole(pos, torch.int32, "pos", (kv.B, T, rope.n_axes)), op, _stream(stream)))
     return q_out
 
 
@@ -676,10 +698,10 @@ def si_tree_attention(kv: KV, q, out, mask=None, lse=None, scale=None, layer=0, 
     (0: padding; None: a chain). out as q, contiguous; lse fp32 [B][T][Hq]
     (optional). scale defaults to D ** -0.5."""
     torch = _torch()
-    B, T, D = kv.B, q.shape[1], kv.D
-    qp, qs, hq = _rows(q, kv.dtype, "q", B, T, D)
+    B, T = kv.B, q.shape[1]
+    qp, qs, hq = _rows(q, kv, "q", T)
     _check(_lib.si_tree_attention(kv._h, layer, T, hq, qp, qs, _whole(mask, torch.int64, "mask", (B, T)),
-                                  D ** -0.5 if scale is None else scale, _whole(out, kv.dtype, "out", q.shape),
+                                  kv.D ** -0.5 if scale is None else scale, _whole(out, kv.dtype, "out", q.shape),
                                   _whole(lse, torch.float32, "lse", (B, T, hq)), _stream(stream)))
     return out
 
@@ -690,8 +712,8 @@ def si_kv_accumulate(kv: KV, q, lse, mask=None, rows=None, scale=None, acc_out=N
     the lse of si_tree_attention. acc_out fp32 [B][Hkv][n_slots] with the
     cache's strides, or [1][B][Hkv][n_slots] (None: the cache's acc)."""
     torch = _torch()
-    B, T, D = kv.B, q.shape[1], kv.D
-    qp, qs, hq = _rows(q, kv.dtype, "q", B, T, D)
+    B, T = kv.B, q.shape[1]
+    qp, qs, hq = _rows(q, kv, "q", T)
     ap = None
     if acc_out is not None:
         ap = _dev(acc_out, torch.float32, "acc_out")
@@ -700,7 +722,7 @@ def si_kv_accumulate(kv: KV, q, lse, mask=None, rows=None, scale=None, acc_out=N
             raise ValueError("acc_out must have the shape and strides of one layer of the cache's acc")
     _check(_lib.si_kv_accumulate(kv._h, layer, T, hq, qp, qs, _whole(lse, torch.float32, "lse", (B, T, hq)),
                                  _whole(mask, torch.int64, "mask", (B, T)), _whole(rows, torch.int64, "rows", (B,)),
-                                 D ** -0.5 if scale is None else scale, ap, _stream(stream)))
+                                 kv.D ** -0.5 if scale is None else scale, ap, _stream(stream)))
 
 
 def si_kv_evict(kv: KV, T, budget, sinks=0, recent=0, path=None, n_path=None, table_out=None, len_out=None,

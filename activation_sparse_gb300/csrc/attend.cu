@@ -146,9 +146,22 @@ __device__ void make_plan(const KvView& C, int T, int groups, const Plan& p, uns
     __syncthreads();
 }
 
-__device__ __forceinline__ int share(int total, int part, int parts) {
-    return (int)((long long)total * part / parts);
-}
+// The tiles are dealt out in parts of n / parts or one more; the first n %
+// parts CTAs have the longer ones. All in 32 bits: these run once per part of
+// every list when rows are joined.
+struct Deal {
+    unsigned base, rem;
+    __device__ __forceinline__ Deal(int total, int parts) {
+        base = (unsigned)total / (unsigned)parts;
+        rem = (unsigned)total - base * (unsigned)parts;
+    }
+    __device__ __forceinline__ int start(int part) const { return (int)(part * base + min((unsigned)part, rem)); }
+    // the part that has tile x
+    __device__ __forceinline__ int owner(int x) const {
+        const unsigned longer = rem * (base + 1);
+        return (int)((unsigned)x < longer ? (unsigned)x / (base + 1) : rem + ((unsigned)x - longer) / base);
+    }
+};
 
 // A position in the flat order of tiles.
 struct At {
@@ -218,6 +231,24 @@ struct AttendCfg {
 // Floats of one partial: RB rows of output, then their maxima and sums.
 constexpr int part_floats(int rb, int dp) { return rb * (dp + 2); }
 
+// A CTA's copies. The MW warps that share a set of keys (a group: 16 * MW keys
+// of every tile) copy them for themselves, sixteen rows a warp, so a group
+// waits for nobody else.
+template <int DP>
+struct Copy {
+    static constexpr int UNITS = DP / 8;            // 16-byte units of a row
+    static constexpr int AT_ONCE = 32 / UNITS;      // rows one sweep of a warp copies
+    static constexpr int SWEEPS = 16 / AT_ONCE;
+    // row (of the warp's sixteen) that this lane copies in sweep j
+    static __device__ __forceinline__ int row(int lane, int j) { return (lane / UNITS) * SWEEPS + j; }
+};
+
+template <int THREADS>
+__device__ __forceinline__ void group_sync(int id) {
+    if (THREADS == 32) __syncwarp();
+    else named_bar_sync(id, THREADS);
+}
+
 // MW row warps x KW key warps = 4: a block of RB = 16 * MW rows; each key
 // warp takes KT / KW keys of every tile with its own softmax state, joined at
 // the end of a list.
@@ -225,15 +256,15 @@ template <int DP, int MW, bool FP16>
 __global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1)
     k_tree_attention(const __grid_constant__ AttendParams P, int row_blocks) {
     using Cfg = AttendCfg<DP>;
+    using Cp = Copy<DP>;
     constexpr int KW = 4 / MW;
     constexpr int RB = 16 * MW;
     constexpr int WK = KT / KW;          // keys of a tile per warp
     constexpr int NS = WK / 8;           // n8 score tiles
     constexpr int KD = DP / 16;          // k steps over D
-    constexpr int UNITS = DP / 8;        // 16-byte units of a row
-    constexpr int ROWS_PER = kThreads / UNITS;  // rows one sweep of the threads copies
-    constexpr int SWEEPS = KT / ROWS_PER;
+    constexpr int UNITS = Cp::UNITS;
     constexpr int S = Cfg::kStages;
+    static_assert(WK == 16 * MW, "a group's warps copy sixteen keys each");
 
     extern __shared__ __align__(128) uint8_t smem[];
     uint8_t* const tiles = smem;
@@ -253,18 +284,20 @@ __global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1)
     grid_launch_dependents();
     grid_dependency_wait();
     make_plan<kThreads>(C, T, groups, plan, P.err, blockIdx.x == 0);
-    const int total = plan.first[C.B];
-    const int x0 = share(total, blockIdx.x, gridDim.x), x1 = share(total, blockIdx.x + 1, gridDim.x);
+    const Deal deal(plan.first[C.B], gridDim.x);
+    const int x0 = deal.start(blockIdx.x), x1 = deal.start(blockIdx.x + 1);
     if (x0 >= x1) return;
 
     const float c2 = P.scale * kLog2e;
-    const int unit = tid % UNITS, row0 = tid / UNITS;
+    const int unit = lane % UNITS;
     const bool unit_on = unit * 8 < D;
+    const int own0 = kw * WK + mw * 16;  // this warp copies keys own0 .. own0 + 15 of a tile
+    const int n_slots = (int)C.n_slots, k_step = (int)C.ks, v_step = (int)C.vs;
 
-    // producer state: slots of the tile to be issued next
+    // producer state: lane i < 16 holds the slot of key own0 + i of the tile to be issued next
     At pa = locate(plan, C.B, x0);
-    int px = x0;
-    int next_slot[SWEEPS];
+    int px = x0, stage_in = 0;
+    int next_slot = kNoSlot;
     unsigned long long p_seen = 0;
     int p_seen_b = -1;
     auto fetch_slots = [&]() {
@@ -280,25 +313,27 @@ __global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1)
                      __reduce_or_sync(0xFFFFFFFFu, (unsigned)mine);
             p_seen_b = pa.b;
         }
-#pragma unroll
-        for (int j = 0; j < SWEEPS; ++j)
-            next_slot[j] = slot_of(list, i0 + row0 + j * ROWS_PER, len, tot, p_seen);
+        next_slot = slot_of(list, i0 + own0 + (lane & 15), len, tot, p_seen);
     };
     auto issue = [&]() {
         if (px < x1) {
             const int h = pa.group / row_blocks;
             const uint16_t* kp = static_cast<const uint16_t*>(C.k) + pa.b * C.kb + h * C.kh + unit * 8;
             const uint16_t* vp = static_cast<const uint16_t*>(C.v) + pa.b * C.vb + h * C.vh + unit * 8;
-            const uint32_t dst = smem_u32(tiles + (px - x0) % S * 2 * Cfg::kTile);
+            const uint32_t dst = smem_u32(tiles + stage_in * 2 * Cfg::kTile);
+            const int slot = slot_ok(next_slot, n_slots, P.err) ? next_slot : -1;
 #pragma unroll
-            for (int j = 0; j < SWEEPS; ++j) {
-                const bool on = slot_ok(next_slot[j], (int)C.n_slots, P.err) && unit_on;
-                const long long slot = on ? next_slot[j] : 0;
-                const uint32_t at = tile_at<DP>(row0 + j * ROWS_PER, unit);
-                cp16(dst + at, on ? kp + slot * C.ks : kp - unit * 8, on);
-                cp16(dst + Cfg::kTile + at, on ? vp + slot * C.vs : vp - unit * 8, on);
+            for (int j = 0; j < Cp::SWEEPS; ++j) {
+                const int r = Cp::row(lane, j);
+                const int at_slot = __shfl_sync(0xFFFFFFFFu, slot, r);
+                const bool on = at_slot >= 0 && unit_on;
+                const long long from = on ? at_slot : 0;
+                const uint32_t at = tile_at<DP>(own0 + r, unit);
+                cp16(dst + at, on ? kp + from * k_step : kp - unit * 8, on);
+                cp16(dst + Cfg::kTile + at, on ? vp + from * v_step : vp - unit * 8, on);
             }
             ++px;
+            if (++stage_in == S) stage_in = 0;
             step(plan, C.B, groups, pa);
         }
         cp_commit();
@@ -308,7 +343,7 @@ __global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1)
     for (int s = 0; s < S - 1; ++s) issue();
 
     At a = locate(plan, C.B, x0);
-    int segment = 0;
+    int segment = 0, stage_out = 0;
     for (int x = x0; x < x1; ++segment) {
         // one list, or the part of it that this CTA has
         const int b = a.b, h = a.group / row_blocks, rb = a.group % row_blocks;
@@ -351,24 +386,25 @@ __global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1)
 
         for (; x < seg_end; ++x, ++a.tile) {
             cp_wait<S - 2>();
-            uint8_t* const stage = tiles + (x - x0) % S * 2 * Cfg::kTile;
+            uint8_t* const stage = tiles + stage_out * 2 * Cfg::kTile;
+            if (++stage_out == S) stage_out = 0;
             const bool meets_new = a.tile * KT + KT > len;
             if (meets_new) {
                 // A node's value row may hold infinities or NaN that only its descendants may
-                // see, and 0 * NaN is NaN: such elements leave the product here (each thread
+                // see, and 0 * NaN is NaN: such elements leave the product here (each lane
                 // looks at what it copied itself) and come back below for the rows that see them.
 #pragma unroll 1
-                for (int j = 0; j < SWEEPS; ++j) {
-                    const int node = a.tile * KT + row0 + j * ROWS_PER - len;
+                for (int j = 0; j < Cp::SWEEPS; ++j) {
+                    const int key = own0 + Cp::row(lane, j), node = a.tile * KT + key - len;
                     if (node < 0 || node >= T) continue;
-                    uint16_t* e = reinterpret_cast<uint16_t*>(stage + Cfg::kTile + tile_at<DP>(row0 + j * ROWS_PER, unit));
+                    uint16_t* e = reinterpret_cast<uint16_t*>(stage + Cfg::kTile + tile_at<DP>(key, unit));
                     bool odd = false;
                     for (int i = 0; i < 8; ++i)
                         if (not_finite<FP16>(e[i])) e[i] = 0, odd = true;
                     if (odd) atomicOr(odd_s, 1ull << node);
                 }
             }
-            __syncthreads();
+            group_sync<32 * MW>(1 + kw);
             issue();
             const uint32_t k_s = smem_u32(stage);
             const uint32_t v_s = k_s + Cfg::kTile;
@@ -420,12 +456,15 @@ __global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1)
                 mx[e] = top[e];
                 sum[e] *= keep[e];
             }
+            // a new maximum is rare after the first tiles: the output rows are rescaled only then
+            if (__any_sync(0xFFFFFFFFu, keep[0] != 1.0f || keep[1] != 1.0f)) {
 #pragma unroll
-            for (int i = 0; i < DP / 8; ++i) {
-                o[i][0] *= keep[0];
-                o[i][1] *= keep[0];
-                o[i][2] *= keep[1];
-                o[i][3] *= keep[1];
+                for (int i = 0; i < DP / 8; ++i) {
+                    o[i][0] *= keep[0];
+                    o[i][1] *= keep[0];
+                    o[i][2] *= keep[1];
+                    o[i][3] *= keep[1];
+                }
             }
 #pragma unroll
             for (int n = 0; n < NS; ++n) {
@@ -579,12 +618,20 @@ __global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1)
     cp_wait<0>();
 }
 
-// Joins the partial rows of the lists that more than one CTA worked on: one
-// warp per row, the CTAs' parts in order.
-template <int DP, int MW, bool FP16>
-__global__ void __launch_bounds__(128) k_tree_attention_join(const __grid_constant__ AttendParams P, int row_blocks, int parts) {
+// Joins the partial rows of the lists that more than one CTA worked on. A row
+// belongs to JW warps of one block: warp w takes parts w, w + JW, ..., and
+// the warps' sums are added in their order, so the result does not depend on
+// timing. JW = 8 where lists have many parts (few lists), 1 where they have few.
+constexpr int kJoinWarps = 8;
+
+template <int DP, int MW, int JW, bool FP16>
+__global__ void __launch_bounds__(kJoinWarps * 32)
+    k_tree_attention_join(const __grid_constant__ AttendParams P, int row_blocks, int parts) {
     constexpr int RB = 16 * MW;
     constexpr int E = DP / 32;  // columns a lane
+    constexpr int ROWS = kJoinWarps / JW;  // rows a block
+    __shared__ float acc_s[JW > 1 ? JW : 1][DP];
+    __shared__ float sum_s[kJoinWarps];
     extern __shared__ __align__(128) uint8_t smem[];
     const KvView& C = P.c;
     Plan plan;
@@ -595,47 +642,56 @@ __global__ void __launch_bounds__(128) k_tree_attention_join(const __grid_consta
     const int groups = C.Hkv * row_blocks;
     grid_launch_dependents();
     grid_dependency_wait();
-    make_plan<128>(C, T, groups, plan, P.err, false);
-    const int total = plan.first[C.B];
-    const int fours = (min(R, RB) + 3) / 4;  // blocks of four rows per list
-    const int list_id = blockIdx.x / fours;
+    make_plan<kJoinWarps * 32>(C, T, groups, plan, P.err, false);
+    const Deal deal(plan.first[C.B], parts);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int row_sets = (min(R, RB) + ROWS - 1) / ROWS;
+    const int list_id = blockIdx.x / row_sets;
     const int b = list_id / groups, group = list_id % groups;
-    const int r = blockIdx.x % fours * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    const int r = blockIdx.x % row_sets * ROWS + warp / JW;
     const int h = group / row_blocks, row = group % row_blocks * RB + r;
     const int n = tiles_of(plan.tot[b]);
-    const int y0 = plan.first[b] + group * n, y1 = y0 + n;  // this list's tiles
-    // the CTA that has tile y: the last one whose share starts at or before it
-    auto owner = [&](int y) {
-        int c = (int)((long long)y * parts / total);
-        while (c + 1 < parts && share(total, c + 1, parts) <= y) ++c;
-        while (share(total, c, parts) > y) --c;
-        return c;
-    };
-    const int first = owner(y0), last = owner(y1 - 1);
-    if (first == last || row >= R || r >= RB) return;
+    const int y0 = plan.first[b] + group * n;  // this list's tiles: y0 .. y0 + n - 1
+    const int first = deal.owner(y0), last = deal.owner(y0 + n - 1);
+    if (first == last) return;  // finished by its CTA
+    const bool on = row < R && r < RB;
     const float c2 = P.scale * kLog2e;
+    const int w = warp % JW;
+    // only the first part can follow another list in its CTA
     auto part_of = [&](int c) {
-        const int second = share(total, c, parts) < y0;  // only the first part can follow another list in its CTA
+        const int second = c == first && deal.start(c) < y0;
         return P.part + ((long long)c * 2 + second) * part_floats(RB, DP);
     };
-    float top = -INFINITY;
-    for (int c = first + lane; c <= last; c += 32) {
-        if (share(total, c, parts) == share(total, c + 1, parts)) continue;
-        top = fmaxf(top, part_of(c)[RB * DP + r]);
+    float top = -INFINITY, sum = 0.0f, acc[E] = {};
+    if (on) {
+        for (int c = first + lane; c <= last; c += 32) top = fmaxf(top, part_of(c)[RB * DP + r]);
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
     const float shift = top == -INFINITY ? 0.0f : top;
-    float acc[E] = {}, sum = 0.0f;
+    if (on) {
 #pragma unroll 4
-    for (int c = first; c <= last; ++c) {
-        if (share(total, c, parts) == share(total, c + 1, parts)) continue;
-        const float* p = part_of(c);
-        const float f = ex2((p[RB * DP + r] - shift) * c2);
-        sum += f * p[RB * DP + RB + r];
+        for (int c = first + w; c <= last; c += JW) {
+            const float* p = part_of(c);
+            const float f = ex2((p[RB * DP + r] - shift) * c2);
+            sum += f * p[RB * DP + RB + r];
 #pragma unroll
-        for (int e = 0; e < E; ++e) acc[e] += f * p[r * DP + e * 32 + lane];
+            for (int e = 0; e < E; ++e) acc[e] += f * p[r * DP + e * 32 + lane];
+        }
     }
+    if (JW > 1) {
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc_s[JW > 1 ? w : 0][e * 32 + lane] = acc[e];
+        if (lane == 0) sum_s[w] = sum;
+        __syncthreads();
+        if (w > 0) return;
+        for (int i = 1; i < JW; ++i) {
+            sum += sum_s[i];
+#pragma unroll
+            for (int e = 0; e < E; ++e) acc[e] += acc_s[JW > 1 ? i : 0][e * 32 + lane];
+        }
+    }
+    if (!on) return;
     const int t = row / G, g = row - t * G;
     const bool empty = plan.tot[b] == 0 || word_of(P.mask, T, b, t) == 0 || sum == 0.0f;
     const float inv = empty ? 0.0f : 1.0f / sum;
@@ -645,15 +701,15 @@ __global__ void __launch_bounds__(128) k_tree_attention_join(const __grid_consta
         const int d = e * 32 + lane;
         if (d >= D) continue;
         const float v = empty ? 0.0f : acc[e] * inv;
-        uint16_t w;
+        uint16_t bits;
         if (FP16) {
             const __half hv = __float2half_rn(v);
-            w = *reinterpret_cast<const uint16_t*>(&hv);
+            bits = *reinterpret_cast<const uint16_t*>(&hv);
         } else {
             const __nv_bfloat16 hv = __float2bfloat16_rn(v);
-            w = *reinterpret_cast<const uint16_t*>(&hv);
+            bits = *reinterpret_cast<const uint16_t*>(&hv);
         }
-        static_cast<uint16_t*>(P.out)[at * D + d] = w;
+        static_cast<uint16_t*>(P.out)[at * D + d] = bits;
     }
     if (P.lse && lane == 0) P.lse[at] = empty ? -INFINITY : fmaf(top, P.scale, logf(sum));
 }
@@ -666,30 +722,33 @@ constexpr int kWeighRows = 64;
 template <int DP>
 struct WeighCfg {
     static constexpr int kTile = KT * DP * 2;
-    static constexpr int kStages = 4;
+    static constexpr int kStages = DP <= 128 ? 5 : 4;
     static constexpr int kOffQ = kStages * kTile;
-    static constexpr int kOffRow = kOffQ + kWeighRows * DP * 2;      // lse2 [64], word [64]
-    static constexpr int kOffPlan = kOffRow + kWeighRows * 4 + kWeighRows * 8 + 64 * 4 + 16;
+    static constexpr int kOffRow = kOffQ + kWeighRows * DP * 2;      // per row: ancestor word, lse; the counted nodes
+    static constexpr int kOffKey = kOffRow + kWeighRows * (8 + 4 + 4) + 16;  // per stage and key: slot, acc
+    static constexpr int kOffPlan = kOffKey + kStages * KT * 8;
     static constexpr int smem(int B) { return kOffPlan + (3 * B + 1) * 4; }
 };
 
 // acc_out[slot] = acc[slot] + sum over counted rows of exp(scale * q.k - lse).
 // Keys are the m side of the matrix product and rows the n side, so that a
-// thread sums its keys' weights over the rows in registers. Reads K once;
-// each key belongs to one warp of one CTA, so nothing is joined.
+// thread sums its keys' weights over the rows in registers. Reads K once; a
+// key belongs to one warp, which also copies it and its old weight, so warps
+// only meet when the list (and with it the queries) changes.
 template <int DP, bool FP16>
 __global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) k_kv_accumulate(const __grid_constant__ AttendParams P) {
     using Cfg = WeighCfg<DP>;
+    using Cp = Copy<DP>;
     constexpr int KD = DP / 16;
-    constexpr int UNITS = DP / 8;
-    constexpr int ROWS_PER = kThreads / UNITS;
-    constexpr int SWEEPS = KT / ROWS_PER;
+    constexpr int UNITS = Cp::UNITS;
     constexpr int S = Cfg::kStages;
     extern __shared__ __align__(128) uint8_t smem[];
     uint8_t* const q_s = smem + Cfg::kOffQ;
     unsigned long long* word_s = reinterpret_cast<unsigned long long*>(smem + Cfg::kOffRow);
     float* lse_s = reinterpret_cast<float*>(word_s + kWeighRows);
-    int* node_s = reinterpret_cast<int*>(lse_s + kWeighRows);  // counted nodes, ascending
+    int* node_s = reinterpret_cast<int*>(lse_s + kWeighRows);  // counted nodes, ascending; then their number
+    int* slot_s = reinterpret_cast<int*>(smem + Cfg::kOffKey);  // [stage][key]
+    float* old_s = reinterpret_cast<float*>(slot_s + S * KT);
     Plan plan;
     plan.len = reinterpret_cast<int*>(smem + Cfg::kOffPlan);
     plan.tot = plan.len + P.c.B;
@@ -702,33 +761,46 @@ __global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) k_kv_accumulate(c
     grid_launch_dependents();
     grid_dependency_wait();
     make_plan<kThreads>(C, T, C.Hkv, plan, P.err, blockIdx.x == 0);
-    const int total = plan.first[C.B];
-    const int x0 = share(total, blockIdx.x, gridDim.x), x1 = share(total, blockIdx.x + 1, gridDim.x);
+    const Deal deal(plan.first[C.B], gridDim.x);
+    const int x0 = deal.start(blockIdx.x), x1 = deal.start(blockIdx.x + 1);
     if (x0 >= x1) return;
     const float c2 = P.scale * kLog2e;
-    const int unit = tid % UNITS, row0 = tid / UNITS;
+    const int unit = lane % UNITS;
     const bool unit_on = unit * 8 < D;
+    const int n_slots = (int)C.n_slots, k_step = (int)C.ks;
 
     At pa = locate(plan, C.B, x0);
-    int px = x0;
-    int next_slot[SWEEPS];
+    int px = x0, stage_in = 0;
+    int next_slot = kNoSlot;
     auto fetch_slots = [&]() {
         if (px >= x1) return;
         const int32_t* list = C.table ? C.table + pa.b * C.tb + pa.group * C.th : nullptr;
-#pragma unroll
-        for (int j = 0; j < SWEEPS; ++j)
-            next_slot[j] = slot_of(list, pa.tile * KT + row0 + j * ROWS_PER, plan.tot[pa.b], plan.tot[pa.b], 0);
+        const int tot = plan.tot[pa.b];
+        next_slot = slot_of(list, pa.tile * KT + warp * 16 + (lane & 15), tot, tot, 0);
     };
     auto issue = [&]() {
         if (px < x1) {
             const uint16_t* kp = static_cast<const uint16_t*>(C.k) + pa.b * C.kb + pa.group * C.kh + unit * 8;
-            const uint32_t dst = smem_u32(smem + (px - x0) % S * Cfg::kTile);
+            const float* ap = C.acc + pa.b * C.ab + pa.group * C.ah;
+            const uint32_t dst = smem_u32(smem + stage_in * Cfg::kTile);
+            const int slot = slot_ok(next_slot, n_slots, P.err) ? next_slot : -1;
+            if (lane < 16) {
+                const int at = stage_in * KT + warp * 16 + lane;
+                slot_s[at] = slot;
+                asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(old_s + at)),
+                             "l"(ap + (slot >= 0 ? slot : 0)), "r"(slot >= 0 ? 4 : 0)
+                             : "memory");
+            }
 #pragma unroll
-            for (int j = 0; j < SWEEPS; ++j) {
-                const bool on = slot_ok(next_slot[j], (int)C.n_slots, P.err) && unit_on;
-                cp16(dst + tile_at<DP>(row0 + j * ROWS_PER, unit), on ? kp + next_slot[j] * C.ks : kp - unit * 8, on);
+            for (int j = 0; j < Cp::SWEEPS; ++j) {
+                const int r = Cp::row(lane, j);
+                const int at_slot = __shfl_sync(0xFFFFFFFFu, slot, r);
+                const bool on = at_slot >= 0 && unit_on;
+                const long long from = on ? at_slot : 0;
+                cp16(dst + tile_at<DP>(warp * 16 + r, unit), on ? kp + from * k_step : kp - unit * 8, on);
             }
             ++px;
+            if (++stage_in == S) stage_in = 0;
             step(plan, C.B, C.Hkv, pa);
         }
         cp_commit();
@@ -738,14 +810,17 @@ __global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) k_kv_accumulate(c
     for (int s = 0; s < S - 1; ++s) issue();
 
     At a = locate(plan, C.B, x0);
-    int have_b = -1, have_h = -1, have_block = -1, n_rows = 0;
+    int have_b = -1, have_h = -1, have_block = -1, n_rows = 0, stage_out = 0;
     for (int x = x0; x < x1; ++x, step(plan, C.B, C.Hkv, a)) {
         cp_wait<S - 2>();
-        __syncthreads();
+        __syncwarp();
         issue();
-        const int b = a.b, h = a.group, len = plan.len[b], tot = plan.tot[b];
+        const int b = a.b, h = a.group, len = plan.len[b], tot = plan.tot[b];  // tot = 0: nothing counts
+        const int stage = stage_out;
+        if (++stage_out == S) stage_out = 0;
         if (have_b != b) {
             // counted nodes of this sequence
+            __syncthreads();
             if (warp == 0) {
                 const unsigned long long want = P.rows ? P.rows[b] : ~0ull;
                 int n = 0;
@@ -763,7 +838,7 @@ __global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) k_kv_accumulate(c
             have_b = b;
             have_h = -1;
         }
-        const uint32_t k_s = smem_u32(smem + (x - x0) % S * Cfg::kTile);
+        const uint32_t k_s = smem_u32(smem + stage * Cfg::kTile);
         uint32_t kf[DP <= 128 ? KD : 1][4];
         if (DP <= 128) {
 #pragma unroll
@@ -836,14 +911,9 @@ __global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) k_kv_accumulate(c
         for (int e = 0; e < 2; ++e) {
             w[e] += __shfl_xor_sync(0xFFFFFFFFu, w[e], 1);
             w[e] += __shfl_xor_sync(0xFFFFFFFFu, w[e], 2);
-            const int i = i0 + e * 8;
-            if ((lane & 3) == 0 && i < tot) {
-                const long long slot = C.table ? C.table[b * C.tb + h * C.th + i] : i;
-                if (slot >= 0 && slot < C.n_slots) {
-                    const long long at = b * C.ab + h * C.ah + slot;
-                    P.acc_out[at] = C.acc[at] + w[e];
-                }
-            }
+            const int key = stage * KT + warp * 16 + (lane >> 2) + e * 8;
+            const int slot = slot_s[key];
+            if ((lane & 3) == 0 && slot >= 0) P.acc_out[b * C.ab + h * C.ah + slot] = old_s[key] + w[e];
         }
     }
     cp_wait<0>();
@@ -884,18 +954,21 @@ cudaError_t launch_attend(const AttendParams& P, cudaStream_t st) {
     int row_blocks = (R + 16 * MW - 1) / (16 * MW);
     int parts = sms * per_sm(DP);
     const auto kern = k_tree_attention<DP, MW, FP16>;
-    const auto join = k_tree_attention_join<DP, MW, FP16>;
     cudaError_t e = allow_max_smem(kern);
     if (e != cudaSuccess) return e;
     void* args[2] = {const_cast<AttendParams*>(&P), &row_blocks};
     e = launch(reinterpret_cast<const void*>(kern), dim3(parts, 1, 1), kThreads, AttendCfg<DP>::smem(P.c.B), args, st);
     if (e != cudaSuccess) return e;
     void* jargs[3] = {const_cast<AttendParams*>(&P), &row_blocks, &parts};
+    const long long lists = (long long)P.c.B * P.c.Hkv * row_blocks;
     const int rows = R < 16 * MW ? R : 16 * MW;
-    const long long blocks = (long long)P.c.B * P.c.Hkv * row_blocks * ((rows + 3) / 4);
+    const bool many = parts >= 4 * lists;  // parts of a list: about parts / lists
+    const int per_block = many ? 1 : kJoinWarps;
+    const long long blocks = lists * ((rows + per_block - 1) / per_block);
     if (blocks > 0x7FFFFFFFLL) return cudaErrorInvalidValue;
-    return launch(reinterpret_cast<const void*>(join), dim3((unsigned)blocks, 1, 1), 128, (3 * P.c.B + 1) * 4, jargs,
-                  st);
+    const void* join = many ? reinterpret_cast<const void*>(&k_tree_attention_join<DP, MW, kJoinWarps, FP16>)
+                            : reinterpret_cast<const void*>(&k_tree_attention_join<DP, MW, 1, FP16>);
+    return launch(join, dim3((unsigned)blocks, 1, 1), kJoinWarps * 32, (3 * P.c.B + 1) * 4, jargs, st);
 }
 
 template <int DP, bool FP16>

@@ -144,14 +144,13 @@ __global__ void __launch_bounds__(kAppendThreads)
 
 // ------------------------------------------------------------------- evict
 
-constexpr int kEvictThreads = 512;
-constexpr int kEvictWarps = kEvictThreads / 32;
 constexpr int kEvictBins = 2048;
 constexpr int kEvictChunk = 24576;  // entries a CTA holds at most: 8 bytes each in shared memory
+constexpr int kEvictBatch = 8;      // entries a thread loads at once: two dependent loads each
 
 struct EvictShared {
     unsigned hist[3][kEvictBins];  // one per radix pass: peers read them while the next is filled
-    unsigned warp_a[kEvictWarps], warp_b[kEvictWarps];
+    unsigned warp_a[32], warp_b[32];
     unsigned total_a, total_b;     // this CTA's strict and tied counts, read by the peers
     unsigned bin, left, whole;
     int last;
@@ -166,15 +165,23 @@ __device__ __forceinline__ uint32_t weight_key(float w) { return w != w ? 0u : v
 // through distributed shared memory), and writes the stable partition.
 // Everything is read before the first cluster barrier and written after it,
 // so the list may be edited in place.
-__global__ void __launch_bounds__(kEvictThreads) k_kv_evict(const __grid_constant__ KvEvictParams P, int chunk_cap) {
+template <int kEvictThreads>
+__global__ void __launch_bounds__(kEvictThreads, 1024 / kEvictThreads) k_kv_evict(const __grid_constant__ KvEvictParams P, int chunk_cap) {
     extern __shared__ __align__(16) uint8_t smem_raw[];
     EvictShared& S = *reinterpret_cast<EvictShared*>(smem_raw);
     int32_t* slots = reinterpret_cast<int32_t*>(smem_raw + sizeof(EvictShared));
     uint32_t* keys = reinterpret_cast<uint32_t*>(slots + chunk_cap);
     cg::cluster_group cluster = cg::this_cluster();
     const int CS = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+    constexpr int kEvictWarps = kEvictThreads / 32;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    for (int i = tid; i < 3 * kEvictBins; i += kEvictThreads) (&S.hist[0][0])[i] = 0;
+    for (int i = tid; i < 3 * kEvictBins / 4; i += kEvictThreads)
+        reinterpret_cast<uint4*>(&S.hist[0][0])[i] = make_uint4(0, 0, 0, 0);
+    __syncthreads();
+    // what the warps before this one have counted (warp sums in v[0 .. warps - 1])
+    auto before_warp = [&](const unsigned* v) {
+        return __reduce_add_sync(0xFFFFFFFFu, lane < warp ? v[lane] : 0u);
+    };
     grid_launch_dependents();
     grid_dependency_wait();
 
@@ -215,18 +222,36 @@ __global__ void __launch_bounds__(kEvictThreads) k_kv_evict(const __grid_constan
     // this CTA's candidates [c0, c1)
     const int chunk = ((n + CS - 1) / CS + 31) & ~31;
     const int c0 = min(n, rank * chunk), c1 = min(n, c0 + chunk), m = c1 - c0;
+    const int lo_c = P.sinks, hi_c = n - P.recent;  // candidates outside [lo_c, hi_c) are safe
+    unsigned need = evict ? (unsigned)(P.budget - P.sinks - P.recent) : 0u;
     bool bad_slot = false;
-    for (int i = tid; i < m; i += kEvictThreads) {
-        const int c = c0 + i;
-        int at = c;
-        if (c >= len && named) at = len + P.path[(long long)b * T + c - len];
-        const int slot = table[at];
-        slots[i] = slot;
+    for (int i0 = tid; i0 < m; i0 += kEvictThreads * kEvictBatch) {
+        int slot[kEvictBatch];
+        float w[kEvictBatch];
+#pragma unroll
+        for (int j = 0; j < kEvictBatch; ++j) {
+            const int c = c0 + i0 + j * kEvictThreads;
+            int at = c;
+            if (c >= len && c < c1 && named) at = len + P.path[(long long)b * T + c - len];
+            slot[j] = c < c1 ? table[at] : 0;
+        }
         if (evict) {
-            uint32_t key = 0;
-            if (slot >= 0 && slot < P.n_slots) key = weight_key(acc[slot]);
-            else bad_slot = true;
+#pragma unroll
+            for (int j = 0; j < kEvictBatch; ++j) {
+                const bool ok = slot[j] >= 0 && slot[j] < P.n_slots;
+                bad_slot |= !ok;
+                w[j] = ok ? acc[slot[j]] : __int_as_float(0x7FC00000);
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < kEvictBatch; ++j) {
+            const int i = i0 + j * kEvictThreads, c = c0 + i;
+            if (i >= m) continue;
+            slots[i] = slot[j];
+            if (!evict) continue;
+            const uint32_t key = weight_key(w[j]);
             keys[i] = key;
+            if (need > 0 && c >= lo_c && c < hi_c) atomicAdd(&S.hist[0][key >> 21], 1u);
         }
     }
     if (bad_slot) atomicOr(P.err, SI_DEVERR_CACHE);
@@ -238,8 +263,6 @@ __global__ void __launch_bounds__(kEvictThreads) k_kv_evict(const __grid_constan
         for (int i = tid; i < m; i += kEvictThreads)
             if (!P.in_place || c0 + i >= len) out[c0 + i] = slots[i];
     } else {
-        const int lo_c = P.sinks, hi_c = n - P.recent;  // candidates outside [lo_c, hi_c) are safe
-        unsigned need = (unsigned)(P.budget - P.sinks - P.recent);
         uint32_t prefix = 0xFFFFFFFFu, tie_need = 0;  // need = 0: no key lies above, no tie is taken
         if (need > 0) {
             prefix = 0;
@@ -249,22 +272,16 @@ __global__ void __launch_bounds__(kEvictThreads) k_kv_evict(const __grid_constan
             for (int pass = 0; pass < 3; ++pass) {
                 unsigned* hist = S.hist[pass];
                 const int bins = 1 << width;
-                for (int i0 = warp * 32; i0 < m; i0 += kEvictThreads) {
-                    const int i = i0 + lane, c = c0 + i;
-                    const bool in = i < m && c >= lo_c && c < hi_c && ((keys[min(i, m - 1)] ^ prefix) & done) == 0;
-                    const unsigned who = __ballot_sync(0xFFFFFFFFu, in);
-                    if (!in) continue;
-                    const unsigned bin = keys[i] >> shift & (bins - 1);
-                    int same = 0;
-                    __match_all_sync(who, bin, &same);  // equal weights are common (fresh keys have 0)
-                    if (same) {
-                        if (lane == __ffs(who) - 1) atomicAdd(&hist[bin], (unsigned)__popc(who));
-                    } else {
-                        atomicAdd(&hist[bin], 1u);
+                if (pass > 0) {  // the first was counted as the weights came in
+                    for (int i = tid; i < m; i += kEvictThreads) {
+                        const int c = c0 + i;
+                        const uint32_t key = keys[i];
+                        if (((key ^ prefix) & done) == 0 && c >= lo_c && c < hi_c)
+                            atomicAdd(&hist[key >> shift & (bins - 1)], 1u);
                     }
+                    cluster.sync();
                 }
-                cluster.sync();
-                // every CTA sums all histograms: four (or two) bins a thread, highest bin first
+                // every CTA sums all histograms: a few bins a thread, highest bin first
                 constexpr int kMaxPer = kEvictBins / kEvictThreads;
                 const int per = bins / kEvictThreads;
                 unsigned cnt[kMaxPer] = {};
@@ -285,8 +302,7 @@ __global__ void __launch_bounds__(kEvictThreads) k_kv_evict(const __grid_constan
                 }
                 if (lane == 31) S.warp_a[warp] = incl;
                 __syncthreads();
-                unsigned before = incl - mine;
-                for (int w = 0; w < warp; ++w) before += S.warp_a[w];
+                const unsigned before = incl - mine + before_warp(S.warp_a);
                 if (before < need && before + mine >= need) {
                     unsigned above = before;
 #pragma unroll
@@ -327,18 +343,15 @@ __global__ void __launch_bounds__(kEvictThreads) k_kv_evict(const __grid_constan
         __syncthreads();
         if (lane == 0) S.warp_a[warp] = n_strict, S.warp_b[warp] = n_tie;
         __syncthreads();
-        if (tid == 0) {
-            unsigned a = 0, t2 = 0;
-            for (int w = 0; w < kEvictWarps; ++w) a += S.warp_a[w], t2 += S.warp_b[w];
-            S.total_a = a, S.total_b = t2;
-        }
+        const unsigned warps_a = before_warp(S.warp_a), warps_b = before_warp(S.warp_b);
+        if (warp == kEvictWarps - 1 && lane == 0) S.total_a = warps_a + n_strict, S.total_b = warps_b + n_tie;
         cluster.sync();
         unsigned strict = 0, tie = 0;
         for (int r = 0; r < rank; ++r) {
             strict += *cluster.map_shared_rank(&S.total_a, r);
             tie += *cluster.map_shared_rank(&S.total_b, r);
         }
-        for (int w = 0; w < warp; ++w) strict += S.warp_a[w], tie += S.warp_b[w];
+        strict += warps_a, tie += warps_b;
         unsigned kept = strict + min(tie, tie_need);  // survivors before this warp's segment
         for (int i0 = s0; i0 < s1; i0 += 32) {
             const int i = i0 + lane, c = c0 + i;
@@ -410,14 +423,17 @@ cudaError_t launch_kv_evict(const KvEvictParams& P, cudaStream_t st) {
     const long long rows = (long long)P.L * P.B * P.Hkv;
     int cs = 1;
     while ((P.cap + cs - 1) / cs > kEvictChunk) cs *= 2;
+    // few lists: more CTAs a list, down to 2048 entries each
     while (cs < 8 && (P.cap + cs - 1) / cs > 2048 && rows * cs < 304) cs *= 2;
     int chunk = (((P.cap + cs - 1) / cs) + 31) & ~31;
-    size_t smem = sizeof(EvictShared) + (size_t)chunk * 8;
-    cudaError_t e = allow_max_smem(k_kv_evict);
+    const bool wide = chunk > 6144;
+    const size_t smem = sizeof(EvictShared) + (size_t)chunk * 8;
+    cudaError_t e = wide ? allow_max_smem(k_kv_evict<1024>) : allow_max_smem(k_kv_evict<256>);
     if (e != cudaSuccess) return e;
     void* args[2] = {const_cast<KvEvictParams*>(&P), &chunk};
-    return launch(reinterpret_cast<const void*>(&k_kv_evict), dim3((unsigned)(rows * cs), 1, 1), kEvictThreads, smem,
-                  cs, args, st);
+    const void* fn = wide ? reinterpret_cast<const void*>(&k_kv_evict<1024>)
+                          : reinterpret_cast<const void*>(&k_kv_evict<256>);
+    return launch(fn, dim3((unsigned)(rows * cs), 1, 1), wide ? 1024 : 256, smem, cs, args, st);
 }
 
 }  // namespace si

@@ -181,6 +181,8 @@ int si_kv_create(const si_kv_desc* desc, si_kv** out) {
     if (d.n_slots > 0x7FFFFFFFLL) return fail(SI_ERR_INVALID_ARG, "slots are int32: n_slots is too large");
     if (!aligned16(d.k) || !aligned16(d.v) || !strides_ok(d.k_stride, 4) || !strides_ok(d.v_stride, 4))
         return fail(SI_ERR_INVALID_ARG, "k and v must be 16-byte aligned with strides that are multiples of 8");
+    if (d.k_stride[3] > 0x7FFFFFFFLL || d.v_stride[3] > 0x7FFFFFFFLL)
+        return fail(SI_ERR_UNSUPPORTED, "a slot stride exceeds 2^31 - 1 elements");
     if (!d.table && d.cap > d.n_slots) return fail(SI_ERR_INVALID_ARG, "without a table cap must not exceed n_slots");
     for (int i = 0; i < 3; ++i)
         if (d.table_stride[i] < 0 || d.acc_stride[i] < 0) return fail(SI_ERR_INVALID_ARG, "negative stride");

@@ -520,8 +520,8 @@ typedef struct si_rope si_rope;
 
 /* Memory of a cache (the caller's, kept alive as long as the handle).
  * Strides are in elements; the last dimension of every array is contiguous.
- *   k_stride / v_stride  {layer, sequence, head, slot}, multiples of 8; k and
- *     v 16-byte aligned. A sequence stride of 0 with tables that share no
+ *   k_stride / v_stride  {layer, sequence, head, slot}, multiples of 8 (the
+ *     slot's below 2^31); k and v 16-byte aligned. A sequence stride of 0 with tables that share no
  *     slot makes one pool for all sequences.
  *   table_stride {layer, sequence, head}. table NULL: entry i is slot i (a
  *     cache that never evicts; needs cap <= n_slots).

@@ -145,43 +145,58 @@ __global__ void __launch_bounds__(kAppendThreads)
 // ------------------------------------------------------------------- evict
 
 constexpr int kEvictBins = 2048;
-constexpr int kEvictChunk = 24576;  // entries a CTA holds at most: 8 bytes each in shared memory
+constexpr int kEvictChunk = 24576;  // candidates a CTA holds at most: 8 bytes each in shared memory
 constexpr int kEvictBatch = 8;      // entries a thread loads at once: two dependent loads each
 
-struct EvictShared {
-    unsigned hist[3][kEvictBins];  // one per radix pass: peers read them while the next is filled
+struct alignas(16) EvictShared {
+    unsigned hist[kEvictBins];
     unsigned warp_a[32], warp_b[32];
     unsigned total_a, total_b;     // this CTA's strict and tied counts, read by the peers
-    unsigned bin, left, whole;
+    unsigned found[3][3];          // per pass: bin, how many of it survive, whether that is all of it
     int last;
 };
 
-// Larger weight <=> larger key, -0 and +0 alike, NaN below everything.
-__device__ __forceinline__ uint32_t weight_key(float w) { return w != w ? 0u : value_key(w); }
+// Larger weight <=> larger key, -0 and +0 alike, NaN below everything. Keys
+// of weights lie strictly between kKeyNone (no candidate) and kKeySafe (kept
+// whatever its weight).
+constexpr uint32_t kKeyNone = 0u, kKeyNaN = 1u, kKeySafe = 0xFFFFFFFFu;
+__device__ __forceinline__ uint32_t weight_key(float w) { return w != w ? kKeyNaN : value_key(w); }
 
-// One cluster per list: it holds the whole candidate list (slot and key) in
-// the shared memory of its CTAs, finds the key of the last survivor by a
-// radix selection over 11 + 11 + 10 bits (each pass sums the CTAs' histograms
-// through distributed shared memory), and writes the stable partition.
-// Everything is read before the first cluster barrier and written after it,
-// so the list may be edited in place.
-template <int kEvictThreads>
-__global__ void __launch_bounds__(kEvictThreads, 1024 / kEvictThreads) k_kv_evict(const __grid_constant__ KvEvictParams P, int chunk_cap) {
+// One cluster per list. It holds the candidates (slot and key) in the shared
+// memory of its CTAs, finds the key of the last survivor by a radix selection
+// over 11 + 11 + 10 bits, and writes the stable partition. In each pass the
+// CTAs add their non-empty bins to the first CTA's histogram (a list's
+// weights fall into few bins: a few hundred words, where reading every
+// peer's histogram moved 8 KB a peer); the first CTA finds the bin and tells
+// the others. Everything is read before the first cluster barrier and written
+// after it, so the list may be edited in place. Bound by latency: a chain of
+// three loads (length, slot, weight), then barriers, so two or more CTAs
+// share an SM.
+template <int THREADS>
+__global__ void __launch_bounds__(THREADS, 1024 / THREADS)
+    k_kv_evict(const __grid_constant__ KvEvictParams P, int chunk_cap) {
+    constexpr int WARPS = THREADS / 32;
     extern __shared__ __align__(16) uint8_t smem_raw[];
     EvictShared& S = *reinterpret_cast<EvictShared*>(smem_raw);
     int32_t* slots = reinterpret_cast<int32_t*>(smem_raw + sizeof(EvictShared));
     uint32_t* keys = reinterpret_cast<uint32_t*>(slots + chunk_cap);
     cg::cluster_group cluster = cg::this_cluster();
     const int CS = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
-    constexpr int kEvictWarps = kEvictThreads / 32;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    for (int i = tid; i < 3 * kEvictBins / 4; i += kEvictThreads)
-        reinterpret_cast<uint4*>(&S.hist[0][0])[i] = make_uint4(0, 0, 0, 0);
-    __syncthreads();
-    // what the warps before this one have counted (warp sums in v[0 .. warps - 1])
+    auto clear = [&]() {
+        for (int i = tid; i < kEvictBins / 4; i += THREADS)
+            reinterpret_cast<uint4*>(S.hist)[i] = make_uint4(0, 0, 0, 0);
+    };
+    auto all_sync = [&]() {
+        if (CS > 1) cluster.sync();
+        else __syncthreads();
+    };
+    // what the warps before this one have counted (warp sums in v[0 .. WARPS - 1])
     auto before_warp = [&](const unsigned* v) {
         return __reduce_add_sync(0xFFFFFFFFu, lane < warp ? v[lane] : 0u);
     };
+    clear();
+    all_sync();  // the first CTA's histogram is clear before a peer adds to it
     grid_launch_dependents();
     grid_dependency_wait();
 
@@ -219,81 +234,102 @@ __global__ void __launch_bounds__(kEvictThreads, 1024 / kEvictThreads) k_kv_evic
     const bool evict = P.budget > 0 && n > P.budget;
     const int n_new = bad ? len : (evict ? P.budget : n);
 
-    // this CTA's candidates [c0, c1)
-    const int chunk = ((n + CS - 1) / CS + 31) & ~31;
+    // this CTA's candidates [c0, c1); the chunk is padded to whole sets of 128
+    const int chunk = ((n + CS - 1) / CS + 127) & ~127;
     const int c0 = min(n, rank * chunk), c1 = min(n, c0 + chunk), m = c1 - c0;
     const int lo_c = P.sinks, hi_c = n - P.recent;  // candidates outside [lo_c, hi_c) are safe
-    unsigned need = evict ? (unsigned)(P.budget - P.sinks - P.recent) : 0u;
+    const unsigned n_slots = (unsigned)P.n_slots;
     bool bad_slot = false;
-    for (int i0 = tid; i0 < m; i0 += kEvictThreads * kEvictBatch) {
+    const int by_table = max(0, min(c1, named ? len : n) - c0);  // candidates whose entry is their own index
+    for (int i0 = tid; i0 < by_table; i0 += THREADS * kEvictBatch) {
         int slot[kEvictBatch];
         float w[kEvictBatch];
 #pragma unroll
         for (int j = 0; j < kEvictBatch; ++j) {
-            const int c = c0 + i0 + j * kEvictThreads;
-            int at = c;
-            if (c >= len && c < c1 && named) at = len + P.path[(long long)b * T + c - len];
-            slot[j] = c < c1 ? table[at] : 0;
+            const int i = i0 + j * THREADS;
+            slot[j] = i < by_table ? table[c0 + i] : 0;
         }
         if (evict) {
 #pragma unroll
             for (int j = 0; j < kEvictBatch; ++j) {
-                const bool ok = slot[j] >= 0 && slot[j] < P.n_slots;
+                const bool ok = (unsigned)slot[j] < n_slots;
                 bad_slot |= !ok;
-                w[j] = ok ? acc[slot[j]] : __int_as_float(0x7FC00000);
+                w[j] = acc[ok ? slot[j] : 0];
             }
         }
 #pragma unroll
         for (int j = 0; j < kEvictBatch; ++j) {
-            const int i = i0 + j * kEvictThreads, c = c0 + i;
-            if (i >= m) continue;
+            const int i = i0 + j * THREADS;
+            if (i >= by_table) break;
             slots[i] = slot[j];
-            if (!evict) continue;
-            const uint32_t key = weight_key(w[j]);
-            keys[i] = key;
-            if (need > 0 && c >= lo_c && c < hi_c) atomicAdd(&S.hist[0][key >> 21], 1u);
+            if (evict) {
+                const uint32_t key = c0 + i < lo_c || c0 + i >= hi_c ? kKeySafe : weight_key(w[j]);
+                keys[i] = key;
+                atomicAdd(&S.hist[key >> 21], 1u);
+            }
         }
+    }
+    for (int i = by_table + tid; i < ((m + 127) & ~127); i += THREADS) {
+        uint32_t key = kKeyNone;
+        if (i < m) {  // accepted nodes, in path order
+            const int slot = table[len + P.path[(long long)b * T + c0 + i - len]];
+            slots[i] = slot;
+            if (evict) {
+                const bool ok = (unsigned)slot < n_slots;
+                bad_slot |= !ok;
+                key = c0 + i < lo_c || c0 + i >= hi_c ? kKeySafe : weight_key(acc[ok ? slot : 0]);
+                atomicAdd(&S.hist[key >> 21], 1u);
+            }
+        }
+        if (evict) keys[i] = key;
     }
     if (bad_slot) atomicOr(P.err, SI_DEVERR_CACHE);
     int rejected = -1;  // slot of the node that this thread puts behind the candidates
     if (rank == 0 && named && tid < T && !(taken >> tid & 1)) rejected = bad ? -1 : table[len + tid];
-    cluster.sync();
 
     if (!evict) {
-        for (int i = tid; i < m; i += kEvictThreads)
+        all_sync();
+        for (int i = tid; i < m; i += THREADS)
             if (!P.in_place || c0 + i >= len) out[c0 + i] = slots[i];
     } else {
-        uint32_t prefix = 0xFFFFFFFFu, tie_need = 0;  // need = 0: no key lies above, no tie is taken
-        if (need > 0) {
-            prefix = 0;
-            tie_need = 0xFFFFFFFFu;
-            int shift = 21, width = 11;
-            uint32_t done = 0;  // mask of the bits fixed so far
-            for (int pass = 0; pass < 3; ++pass) {
-                unsigned* hist = S.hist[pass];
-                const int bins = 1 << width;
-                if (pass > 0) {  // the first was counted as the weights came in
-                    for (int i = tid; i < m; i += kEvictThreads) {
-                        const int c = c0 + i;
-                        const uint32_t key = keys[i];
-                        if (((key ^ prefix) & done) == 0 && c >= lo_c && c < hi_c)
-                            atomicAdd(&hist[key >> shift & (bins - 1)], 1u);
-                    }
-                    cluster.sync();
+        const int quads = ((m + 127) & ~127) / 4;
+        const uint4* keys4 = reinterpret_cast<const uint4*>(keys);
+        unsigned need = (unsigned)P.budget;
+        uint32_t prefix = 0, tie_need = 0xFFFFFFFFu;
+        uint32_t done = 0;  // mask of the bits fixed so far
+        for (int pass = 0; pass < 3; ++pass) {
+            const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
+            const int bins = pass < 2 ? 2048 : 1024;
+            if (pass > 0) {  // the first was counted as the weights came in
+                clear();
+                __syncthreads();
+                if (CS > 1) cluster.barrier_arrive();  // clear: peers may add to it
+                for (int i = tid; i < quads; i += THREADS) {
+                    const uint4 k = keys4[i];
+                    if (((k.x ^ prefix) & done) == 0) atomicAdd(&S.hist[k.x >> shift & (bins - 1)], 1u);
+                    if (((k.y ^ prefix) & done) == 0) atomicAdd(&S.hist[k.y >> shift & (bins - 1)], 1u);
+                    if (((k.z ^ prefix) & done) == 0) atomicAdd(&S.hist[k.z >> shift & (bins - 1)], 1u);
+                    if (((k.w ^ prefix) & done) == 0) atomicAdd(&S.hist[k.w >> shift & (bins - 1)], 1u);
                 }
-                // every CTA sums all histograms: a few bins a thread, highest bin first
-                constexpr int kMaxPer = kEvictBins / kEvictThreads;
-                const int per = bins / kEvictThreads;
-                unsigned cnt[kMaxPer] = {};
-                for (int r = 0; r < CS; ++r) {
-                    const unsigned* peer = cluster.map_shared_rank(hist, r);
+                if (CS > 1) cluster.barrier_wait();
+            }
+            if (rank > 0) {
+                __syncthreads();
+                unsigned* lead = cluster.map_shared_rank(S.hist, 0);
+                for (int i = tid; i < bins; i += THREADS)
+                    if (const unsigned c = S.hist[i]) atomicAdd(lead + i, c);
+            }
+            all_sync();
+            if (rank == 0) {
+                // a few bins a thread, highest first: the one where the count from the top reaches need
+                constexpr int kMaxPer = kEvictBins / THREADS;
+                const int per = bins / THREADS;
+                unsigned cnt[kMaxPer], mine = 0;
 #pragma unroll
-                    for (int j = 0; j < kMaxPer; ++j)
-                        if (j < per) cnt[j] += peer[bins - 1 - (tid * per + j)];
+                for (int j = 0; j < kMaxPer; ++j) {
+                    cnt[j] = j < per ? S.hist[bins - 1 - (tid * per + j)] : 0;
+                    mine += cnt[j];
                 }
-                unsigned mine = 0;
-#pragma unroll
-                for (int j = 0; j < kMaxPer; ++j) mine += cnt[j];
                 unsigned incl = mine;
 #pragma unroll
                 for (int o = 1; o < 32; o <<= 1) {
@@ -302,77 +338,93 @@ __global__ void __launch_bounds__(kEvictThreads, 1024 / kEvictThreads) k_kv_evic
                 }
                 if (lane == 31) S.warp_a[warp] = incl;
                 __syncthreads();
-                const unsigned before = incl - mine + before_warp(S.warp_a);
-                if (before < need && before + mine >= need) {
-                    unsigned above = before;
+                unsigned above = incl - mine + before_warp(S.warp_a);
+                if (above < need && above + mine >= need) {
 #pragma unroll
                     for (int j = 0; j < kMaxPer; ++j) {
                         if (above < need && above + cnt[j] >= need) {
-                            S.bin = bins - 1 - (tid * per + j);
-                            S.left = need - above;
-                            S.whole = cnt[j] == need - above;
-                            above = 0xFFFFFFFFu;
-                        } else if (above != 0xFFFFFFFFu) {
+                            for (int r = 0; r < CS; ++r) {
+                                unsigned* f = cluster.map_shared_rank(S.found[pass], r);
+                                f[0] = bins - 1 - (tid * per + j);
+                                f[1] = need - above;
+                                f[2] = cnt[j] == need - above;
+                            }
+                            above = need;
+                        } else {
                             above += cnt[j];
                         }
                     }
                 }
-                __syncthreads();
-                prefix |= S.bin << shift;
-                done |= (uint32_t)(bins - 1) << shift;
-                need = S.left;
-                if (S.whole) break;  // the bin is taken whole: every key >= prefix survives
-                if (pass == 2) tie_need = need;
-                width = pass == 0 ? 11 : 10;
-                shift -= width;
-                __syncthreads();
             }
+            all_sync();
+            prefix |= S.found[pass][0] << shift;
+            done |= (uint32_t)(bins - 1) << shift;
+            need = S.found[pass][1];
+            if (S.found[pass][2]) break;  // the bin is taken whole: every key >= prefix survives
+            if (pass == 2) tie_need = need;
         }
-        // strict survivors and ties per warp segment, then per CTA
-        const int seg = (((m + kEvictWarps - 1) / kEvictWarps) + 31) & ~31;
-        const int s0 = min(m, warp * seg), s1 = min(m, s0 + seg);
-        unsigned n_strict = 0, n_tie = 0;
-        for (int i0 = s0; i0 < s1; i0 += 32) {
-            const int i = i0 + lane, c = c0 + i;
-            const bool in = i < s1;
-            const uint32_t key = in ? keys[i] : 0u;
-            const bool safe = in && (c < lo_c || c >= hi_c);
-            n_strict += __popc(__ballot_sync(0xFFFFFFFFu, safe || (in && key > prefix)));
-            n_tie += __popc(__ballot_sync(0xFFFFFFFFu, in && !safe && key == prefix));
-        }
-        __syncthreads();
+        // Keys above the prefix survive, keys equal to it while tie_need lasts. Counts of both per warp
+        // segment (whole sets of 128 candidates, four a lane), then per CTA; packed as strict | ties << 16.
+        const int sets = quads / 32, per_warp = (sets + WARPS - 1) / WARPS;
+        const int s0 = min(sets, warp * per_warp), s1 = min(sets, s0 + per_warp);
+        auto classes = [&](const uint4& k) {
+            return (unsigned)((k.x > prefix) + (k.y > prefix) + (k.z > prefix) + (k.w > prefix)) |
+                   (unsigned)((k.x == prefix) + (k.y == prefix) + (k.z == prefix) + (k.w == prefix)) << 16;
+        };
+        unsigned both = 0;
+        for (int q = s0; q < s1; ++q) both += classes(keys4[q * 32 + lane]);
+        const unsigned n_strict = __reduce_add_sync(0xFFFFFFFFu, both & 0xFFFFu);
+        const unsigned n_tie = __reduce_add_sync(0xFFFFFFFFu, both >> 16);
         if (lane == 0) S.warp_a[warp] = n_strict, S.warp_b[warp] = n_tie;
         __syncthreads();
         const unsigned warps_a = before_warp(S.warp_a), warps_b = before_warp(S.warp_b);
-        if (warp == kEvictWarps - 1 && lane == 0) S.total_a = warps_a + n_strict, S.total_b = warps_b + n_tie;
-        cluster.sync();
-        unsigned strict = 0, tie = 0;
-        for (int r = 0; r < rank; ++r) {
-            strict += *cluster.map_shared_rank(&S.total_a, r);
-            tie += *cluster.map_shared_rank(&S.total_b, r);
+        unsigned strict = warps_a, tie = warps_b;
+        if (CS > 1) {
+            if (warp == WARPS - 1 && lane == 0) S.total_a = warps_a + n_strict, S.total_b = warps_b + n_tie;
+            cluster.sync();
+            unsigned a = 0, t2 = 0;
+            if (lane < rank) {
+                a = *cluster.map_shared_rank(&S.total_a, lane);
+                t2 = *cluster.map_shared_rank(&S.total_b, lane);
+            }
+            strict += __reduce_add_sync(0xFFFFFFFFu, a);
+            tie += __reduce_add_sync(0xFFFFFFFFu, t2);
         }
-        strict += warps_a, tie += warps_b;
-        unsigned kept = strict + min(tie, tie_need);  // survivors before this warp's segment
-        for (int i0 = s0; i0 < s1; i0 += 32) {
-            const int i = i0 + lane, c = c0 + i;
-            const bool in = i < s1;
-            const uint32_t key = in ? keys[i] : 0u;
-            const bool safe = in && (c < lo_c || c >= hi_c);
-            const bool tied = in && !safe && key == prefix;
-            const unsigned ties = __ballot_sync(0xFFFFFFFFu, tied);
-            const bool keep = safe || (in && key > prefix) || (tied && tie + __popc(ties & lanemask_lt()) < tie_need);
-            const unsigned keeps = __ballot_sync(0xFFFFFFFFu, keep);
-            const int pos = (int)(kept + __popc(keeps & lanemask_lt()));
-            if (in) out[keep ? pos : P.budget + (c - pos)] = slots[i];
-            tie += __popc(ties);
-            kept += __popc(keeps);
+        for (int q = s0; q < s1; ++q) {
+            const uint4 k = keys4[q * 32 + lane];
+            const int4 v = reinterpret_cast<const int4*>(slots)[q * 32 + lane];
+            const unsigned mine = classes(k);
+            unsigned incl = mine;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const unsigned u = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+                if (lane >= o) incl += u;
+            }
+            unsigned my_strict = strict + ((incl - mine) & 0xFFFFu), my_tie = tie + ((incl - mine) >> 16);
+            int c = c0 + q * 128 + lane * 4;
+            auto put = [&](uint32_t key, int slot) {
+                const bool tied = key == prefix;
+                const int pos = (int)(my_strict + min(my_tie, tie_need));  // survivors before this candidate
+                const bool keep = key > prefix || (tied && my_tie < tie_need);
+                if (c < c1) out[keep ? pos : P.budget + (c - pos)] = slot;
+                my_strict += key > prefix;
+                my_tie += tied;
+                ++c;
+            };
+            put(k.x, v.x);
+            put(k.y, v.y);
+            put(k.z, v.z);
+            put(k.w, v.w);
+            const unsigned all = __shfl_sync(0xFFFFFFFFu, incl, 31);
+            strict += all & 0xFFFFu;
+            tie += all >> 16;
         }
     }
     if (rejected >= 0) out[n + tid - __popcll(taken & ((1ull << tid) - 1))] = rejected;
     if (!P.in_place) {
         // what this call does not reorder: unaccepted nodes that stay behind the candidates, free slots
         const int from = named ? used : n;
-        for (int i = from + rank * kEvictThreads + tid; i < P.cap; i += CS * kEvictThreads) out[i] = table[i];
+        for (int i = from + rank * THREADS + tid; i < P.cap; i += CS * THREADS) out[i] = table[i];
         if (h == 0 && rank == 0 && tid == 0) P.len_out[lb] = n_new;
     } else if (rank == 0) {
         // the other heads' clusters still read len: the last cluster of the grid writes the new ones
@@ -385,11 +437,11 @@ __global__ void __launch_bounds__(kEvictThreads, 1024 / kEvictThreads) k_kv_evic
         __syncthreads();
         if (S.last) {
             __threadfence();
-            for (int i = tid; i < P.L * P.B; i += kEvictThreads) P.len_out[i] = (int)__ldcg(len_new + i);
+            for (int i = tid; i < P.L * P.B; i += THREADS) P.len_out[i] = (int)__ldcg(len_new + i);
             if (tid == 0) *P.ticket = 0;
         }
     }
-    cluster.sync();  // peers may still read this CTA's totals
+    if (CS > 1) cluster.sync();  // peers may still read this CTA's totals
 }
 
 cudaError_t launch(const void* fn, dim3 grid, int threads, size_t smem, int cluster, void** args, cudaStream_t st) {
@@ -421,19 +473,21 @@ cudaError_t launch_kv_append(const KvAppendParams& P, const RopeTable& R, cudaSt
 
 cudaError_t launch_kv_evict(const KvEvictParams& P, cudaStream_t st) {
     const long long rows = (long long)P.L * P.B * P.Hkv;
+    // CTAs a list (at most eight, the portable cluster): few enough candidates each that two CTAs share an
+    // SM where eight CTAs can do that; down to 2048 each where the lists alone do not fill the GPU
     int cs = 1;
-    while ((P.cap + cs - 1) / cs > kEvictChunk) cs *= 2;
-    // few lists: more CTAs a list, down to 2048 entries each
-    while (cs < 8 && (P.cap + cs - 1) / cs > 2048 && rows * cs < 304) cs *= 2;
-    int chunk = (((P.cap + cs - 1) / cs) + 31) & ~31;
-    const bool wide = chunk > 6144;
+    auto each = [&]() { return ((P.cap + cs - 1) / cs + 127) & ~127; };
+    while (cs < 8 && (each() > 12544 || (each() > 2048 && rows * cs < 304))) cs *= 2;
+    int chunk = each();
+    if (chunk > kEvictChunk) return cudaErrorInvalidValue;
+    const bool wide = chunk > 5120;
     const size_t smem = sizeof(EvictShared) + (size_t)chunk * 8;
-    cudaError_t e = wide ? allow_max_smem(k_kv_evict<1024>) : allow_max_smem(k_kv_evict<256>);
+    const cudaError_t e = wide ? allow_max_smem(k_kv_evict<512>) : allow_max_smem(k_kv_evict<256>);
     if (e != cudaSuccess) return e;
-    void* args[2] = {const_cast<KvEvictParams*>(&P), &chunk};
-    const void* fn = wide ? reinterpret_cast<const void*>(&k_kv_evict<1024>)
+    const void* fn = wide ? reinterpret_cast<const void*>(&k_kv_evict<512>)
                           : reinterpret_cast<const void*>(&k_kv_evict<256>);
-    return launch(fn, dim3((unsigned)(rows * cs), 1, 1), wide ? 1024 : 256, smem, cs, args, st);
+    void* args[2] = {const_cast<KvEvictParams*>(&P), &chunk};
+    return launch(fn, dim3((unsigned)(rows * cs), 1, 1), wide ? 512 : 256, smem, cs, args, st);
 }
 
 }  // namespace si

@@ -10,209 +10,13 @@
 // the output rows in registers. A list that ends up in one CTA is finished
 // there; the others leave partial rows that a second kernel joins in a fixed
 // order, so results do not depend on timing.
-#include <cuda_fp16.h>
-
-#include <climits>
-#include <cmath>
-#include <cstring>
-
-#include "common.cuh"
-#include "internal.h"
+#include "attend.cuh"
 
 namespace si {
 
 namespace {
 
-constexpr int KT = 64;             // keys per tile
-constexpr int kThreads = 128;      // four warps
-constexpr float kLog2e = 1.4426950408889634f;
-
-// ------------------------------------------------------------- primitives
-
-__device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool on) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0) : "memory");
-}
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
-__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-                 : "r"(addr));
-}
-__device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr) {
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-                 : "r"(addr));
-}
-
-// d += a (16 x 16) * b (16 x 8), fp32 accumulators
-template <bool FP16>
-__device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    if (FP16)
-        asm volatile(
-            "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-            "{%0, %1, %2, %3};"
-            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-    else
-        asm volatile(
-            "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-            "{%0, %1, %2, %3};"
-            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
-template <bool FP16>
-__device__ __forceinline__ uint32_t pack(float a, float b) {
-    uint32_t w;
-    if (FP16) {
-        const __half2 h = __floats2half2_rn(a, b);
-        w = *reinterpret_cast<const uint32_t*>(&h);
-    } else {
-        const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-        w = *reinterpret_cast<const uint32_t*>(&h);
-    }
-    return w;
-}
-
-template <bool FP16>
-__device__ __forceinline__ bool not_finite(uint16_t w) {
-    return FP16 ? (w & 0x7C00u) == 0x7C00u : (w & 0x7F80u) == 0x7F80u;
-}
-
-template <bool FP16>
-__device__ __forceinline__ float widen(uint16_t w) {
-    if (FP16) return __half2float(*reinterpret_cast<const __half*>(&w));
-    return __uint_as_float((uint32_t)w << 16);
-}
-
-// Byte offset of 16-byte unit `unit` of row `row` in a tile of rows of DP
-// 16-bit elements; the unit index is XORed with the row's low bits so that
-// the eight rows of an ldmatrix lie in different banks.
-template <int DP>
-__device__ __forceinline__ uint32_t tile_at(int row, int unit) {
-    return (uint32_t)(row * (DP * 2) + ((unit ^ (row & 7)) * 16));
-}
-
-// --------------------------------------------------------------- schedule
-
-// The lists of one launch: `groups` lists a sequence (cache heads x row
-// blocks), each of ntile(b) tiles.
-struct Plan {
-    int* len;         // [B] live keys (0 where the sequence is out of bounds)
-    int* tot;         // [B] live keys + new nodes (0 likewise)
-    int* first;       // [B + 1] flat index of the sequence's first tile
-};
-
-__device__ __forceinline__ int tiles_of(int tot) { return tot > KT ? (tot + KT - 1) / KT : 1; }
-
-// Fills the plan (all threads; ends with a barrier). Lengths are read once.
-template <int THREADS>
-__device__ void make_plan(const KvView& C, int T, int groups, const Plan& p, unsigned* err, bool report) {
-    for (int b = threadIdx.x; b < C.B; b += THREADS) {
-        const int len = C.len[b];
-        const bool ok = len >= 0 && len <= C.cap - T;
-        if (!ok && report) atomicOr(err, SI_DEVERR_CACHE);
-        p.len[b] = ok ? len : 0;
-        p.tot[b] = ok ? len + T : 0;
-    }
-    __syncthreads();
-    if (threadIdx.x < 32) {
-        int base = 0;
-        for (int b0 = 0; b0 < C.B; b0 += 32) {
-            const int b = b0 + (int)threadIdx.x;
-            const int mine = b < C.B ? tiles_of(p.tot[b]) * groups : 0;
-            int incl = mine;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int v = __shfl_up_sync(0xFFFFFFFFu, incl, o);
-                if ((int)threadIdx.x >= o) incl += v;
-            }
-            if (b < C.B) p.first[b] = base + incl - mine;
-            base += __shfl_sync(0xFFFFFFFFu, incl, 31);
-        }
-        if (threadIdx.x == 0) p.first[C.B] = base;
-    }
-    __syncthreads();
-}
-
-// The tiles are dealt out in parts of n / parts or one more; the first n %
-// parts CTAs have the longer ones. All in 32 bits: these run once per part of
-// every list when rows are joined.
-struct Deal {
-    unsigned base, rem;
-    __device__ __forceinline__ Deal(int total, int parts) {
-        base = (unsigned)total / (unsigned)parts;
-        rem = (unsigned)total - base * (unsigned)parts;
-    }
-    __device__ __forceinline__ int start(int part) const { return (int)(part * base + min((unsigned)part, rem)); }
-    // the part that has tile x
-    __device__ __forceinline__ int owner(int x) const {
-        const unsigned longer = rem * (base + 1);
-        return (int)((unsigned)x < longer ? (unsigned)x / (base + 1) : rem + ((unsigned)x - longer) / base);
-    }
-};
-
-// A position in the flat order of tiles.
-struct At {
-    int b, group, tile, ntile;
-};
-
-__device__ __forceinline__ At locate(const Plan& p, int B, int x) {
-    int lo = 0, hi = B - 1;  // last b with first[b] <= x
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (p.first[mid] <= x) lo = mid;
-        else hi = mid - 1;
-    }
-    At a;
-    a.b = lo;
-    a.ntile = tiles_of(p.tot[lo]);
-    const int in = x - p.first[lo];
-    a.group = in / a.ntile;
-    a.tile = in - a.group * a.ntile;
-    return a;
-}
-
-__device__ __forceinline__ void step(const Plan& p, int B, int groups, At& a) {
-    if (++a.tile < a.ntile) return;
-    a.tile = 0;
-    if (++a.group < groups) return;
-    a.group = 0;
-    if (++a.b < B) a.ntile = tiles_of(p.tot[a.b]);
-}
-
-// Ancestor word of node t (mask NULL: a chain).
-__device__ __forceinline__ unsigned long long word_of(const unsigned long long* mask, int T, int b, int t) {
-    return mask ? mask[(long long)b * T + t] : (t >= 63 ? ~0ull : (2ull << t) - 1);
-}
-
-constexpr int kNoSlot = INT_MIN;
-
-// Slot of list entry i, or kNoSlot where nothing is to be read. The value is not
-// looked at here: it is used a tile later, so the load's latency is hidden.
-__device__ __forceinline__ int slot_of(const int32_t* list, int i, int len, int tot, unsigned long long seen) {
-    const bool on = i < len || (i < tot && (seen >> ((i - len) & 63) & 1));
-    if (!on) return kNoSlot;
-    return list ? list[i] : i;
-}
-
-// A slot outside the pool is reported and not read.
-__device__ __forceinline__ bool slot_ok(int slot, int n_slots, unsigned* err) {
-    if ((unsigned)slot < (unsigned)n_slots) return true;
-    if (slot != kNoSlot) atomicOr(err, SI_DEVERR_CACHE);
-    return false;
-}
+constexpr int kThreads = 128;  // four warps
 
 // ------------------------------------------------------------- attention
 
@@ -226,21 +30,6 @@ struct AttendCfg {
     static constexpr int kOffPlan = kOffQ + kQBytes;
     static constexpr int kOffOdd = kOffPlan;              // new nodes whose value row is not finite (a word)
     static constexpr int smem(int B) { return kOffPlan + 16 + (3 * B + 1) * 4; }
-};
-
-// Floats of one partial: RB rows of output, then their maxima and sums.
-constexpr int part_floats(int rb, int dp) { return rb * (dp + 2); }
-
-// A CTA's copies. The MW warps that share a set of keys (a group: 16 * MW keys
-// of every tile) copy them for themselves, sixteen rows a warp, so a group
-// waits for nobody else.
-template <int DP>
-struct Copy {
-    static constexpr int UNITS = DP / 8;            // 16-byte units of a row
-    static constexpr int AT_ONCE = 32 / UNITS;      // rows one sweep of a warp copies
-    static constexpr int SWEEPS = 16 / AT_ONCE;
-    // row (of the warp's sixteen) that this lane copies in sweep j
-    static __device__ __forceinline__ int row(int lane, int j) { return (lane / UNITS) * SWEEPS + j; }
 };
 
 template <int THREADS>
@@ -624,10 +413,9 @@ __global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1)
 // timing. JW = 8 where lists have many parts (few lists), 1 where they have few.
 constexpr int kJoinWarps = 8;
 
-template <int DP, int MW, int JW, bool FP16>
+template <int DP, int RB, int JW, bool FP16>
 __global__ void __launch_bounds__(kJoinWarps * 32)
     k_tree_attention_join(const __grid_constant__ AttendParams P, int row_blocks, int parts) {
-    constexpr int RB = 16 * MW;
     constexpr int E = DP / 32;  // columns a lane
     constexpr int ROWS = kJoinWarps / JW;  // rows a block
     __shared__ float acc_s[JW > 1 ? JW : 1][DP];
@@ -714,237 +502,30 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
     if (P.lse && lane == 0) P.lse[at] = empty ? -INFINITY : fmaf(top, P.scale, logf(sum));
 }
 
-// ---------------------------------------------------------------- weights
-
-// Rows kept in shared memory at once.
-constexpr int kWeighRows = 64;
-
-template <int DP>
-struct WeighCfg {
-    static constexpr int kTile = KT * DP * 2;
-    static constexpr int kStages = DP <= 128 ? 5 : 4;
-    static constexpr int kOffQ = kStages * kTile;
-    static constexpr int kOffRow = kOffQ + kWeighRows * DP * 2;      // per row: ancestor word, lse; the counted nodes
-    static constexpr int kOffKey = kOffRow + kWeighRows * (8 + 4 + 4) + 16;  // per stage and key: slot, acc
-    static constexpr int kOffPlan = kOffKey + kStages * KT * 8;
-    static constexpr int smem(int B) { return kOffPlan + (3 * B + 1) * 4; }
-};
-
-// acc_out[slot] = acc[slot] + sum over counted rows of exp(scale * q.k - lse).
-// Keys are the m side of the matrix product and rows the n side, so that a
-// thread sums its keys' weights over the rows in registers. Reads K once; a
-// key belongs to one warp, which also copies it and its old weight, so warps
-// only meet when the list (and with it the queries) changes.
-template <int DP, bool FP16>
-__global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) k_kv_accumulate(const __grid_constant__ AttendParams P) {
-    using Cfg = WeighCfg<DP>;
-    using Cp = Copy<DP>;
-    constexpr int KD = DP / 16;
-    constexpr int UNITS = Cp::UNITS;
-    constexpr int S = Cfg::kStages;
-    extern __shared__ __align__(128) uint8_t smem[];
-    uint8_t* const q_s = smem + Cfg::kOffQ;
-    unsigned long long* word_s = reinterpret_cast<unsigned long long*>(smem + Cfg::kOffRow);
-    float* lse_s = reinterpret_cast<float*>(word_s + kWeighRows);
-    int* node_s = reinterpret_cast<int*>(lse_s + kWeighRows);  // counted nodes, ascending; then their number
-    int* slot_s = reinterpret_cast<int*>(smem + Cfg::kOffKey);  // [stage][key]
-    float* old_s = reinterpret_cast<float*>(slot_s + S * KT);
-    Plan plan;
-    plan.len = reinterpret_cast<int*>(smem + Cfg::kOffPlan);
-    plan.tot = plan.len + P.c.B;
-    plan.first = plan.tot + P.c.B;
-
-    const KvView& C = P.c;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int T = P.T, G = P.G, D = C.D;
-
-    grid_launch_dependents();
-    grid_dependency_wait();
-    make_plan<kThreads>(C, T, C.Hkv, plan, P.err, blockIdx.x == 0);
-    const Deal deal(plan.first[C.B], gridDim.x);
-    const int x0 = deal.start(blockIdx.x), x1 = deal.start(blockIdx.x + 1);
-    if (x0 >= x1) return;
-    const float c2 = P.scale * kLog2e;
-    const int unit = lane % UNITS;
-    const bool unit_on = unit * 8 < D;
-    const int n_slots = (int)C.n_slots, k_step = (int)C.ks;
-
-    At pa = locate(plan, C.B, x0);
-    int px = x0, stage_in = 0;
-    int next_slot = kNoSlot;
-    auto fetch_slots = [&]() {
-        if (px >= x1) return;
-        const int32_t* list = C.table ? C.table + pa.b * C.tb + pa.group * C.th : nullptr;
-        const int tot = plan.tot[pa.b];
-        next_slot = slot_of(list, pa.tile * KT + warp * 16 + (lane & 15), tot, tot, 0);
-    };
-    auto issue = [&]() {
-        if (px < x1) {
-            const uint16_t* kp = static_cast<const uint16_t*>(C.k) + pa.b * C.kb + pa.group * C.kh + unit * 8;
-            const float* ap = C.acc + pa.b * C.ab + pa.group * C.ah;
-            const uint32_t dst = smem_u32(smem + stage_in * Cfg::kTile);
-            const int slot = slot_ok(next_slot, n_slots, P.err) ? next_slot : -1;
-            if (lane < 16) {
-                const int at = stage_in * KT + warp * 16 + lane;
-                slot_s[at] = slot;
-                asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(old_s + at)),
-                             "l"(ap + (slot >= 0 ? slot : 0)), "r"(slot >= 0 ? 4 : 0)
-                             : "memory");
-            }
-#pragma unroll
-            for (int j = 0; j < Cp::SWEEPS; ++j) {
-                const int r = Cp::row(lane, j);
-                const int at_slot = __shfl_sync(0xFFFFFFFFu, slot, r);
-                const bool on = at_slot >= 0 && unit_on;
-                const long long from = on ? at_slot : 0;
-                cp16(dst + tile_at<DP>(warp * 16 + r, unit), on ? kp + from * k_step : kp - unit * 8, on);
-            }
-            ++px;
-            if (++stage_in == S) stage_in = 0;
-            step(plan, C.B, C.Hkv, pa);
-        }
-        cp_commit();
-        fetch_slots();
-    };
-    fetch_slots();
-    for (int s = 0; s < S - 1; ++s) issue();
-
-    At a = locate(plan, C.B, x0);
-    int have_b = -1, have_h = -1, have_block = -1, n_rows = 0, stage_out = 0;
-    for (int x = x0; x < x1; ++x, step(plan, C.B, C.Hkv, a)) {
-        cp_wait<S - 2>();
-        __syncwarp();
-        issue();
-        const int b = a.b, h = a.group, len = plan.len[b], tot = plan.tot[b];  // tot = 0: nothing counts
-        const int stage = stage_out;
-        if (++stage_out == S) stage_out = 0;
-        if (have_b != b) {
-            // counted nodes of this sequence
-            __syncthreads();
-            if (warp == 0) {
-                const unsigned long long want = P.rows ? P.rows[b] : ~0ull;
-                int n = 0;
-                for (int t0 = 0; t0 < T; t0 += 32) {
-                    const int t = t0 + lane;
-                    const bool on = t < T && (want >> (t & 63) & 1) && word_of(P.mask, T, b, t) != 0 && tot > 0;
-                    const unsigned who = __ballot_sync(0xFFFFFFFFu, on);
-                    if (on) node_s[n + __popc(who & lanemask_lt())] = t;
-                    n += __popc(who);
-                }
-                if (lane == 0) node_s[64] = n;
-            }
-            __syncthreads();
-            n_rows = node_s[64] * G;
-            have_b = b;
-            have_h = -1;
-        }
-        const uint32_t k_s = smem_u32(smem + stage * Cfg::kTile);
-        uint32_t kf[DP <= 128 ? KD : 1][4];
-        if (DP <= 128) {
-#pragma unroll
-            for (int k = 0; k < KD; ++k)
-                ldsm4(kf[DP <= 128 ? k : 0], k_s + tile_at<DP>(warp * 16 + (lane & 15), 2 * k + (lane >> 4)));
-        }
-        float w[2] = {0.0f, 0.0f};  // keys lane/4 and lane/4 + 8 of the warp's sixteen
-        const int i0 = a.tile * KT + warp * 16 + (lane >> 2);
-        for (int r0 = 0; r0 < n_rows; r0 += kWeighRows) {
-            const int nr = min(kWeighRows, n_rows - r0);
-            if (have_h != h || have_block != r0) {
-                __syncthreads();
-                const int padded = (nr + 7) & ~7;
-                for (int i = tid; i < padded * UNITS; i += kThreads) {
-                    const int r = i / UNITS, u = i % UNITS;
-                    uint4 val = make_uint4(0, 0, 0, 0);
-                    if (r < nr && u * 8 < D) {
-                        const int t = node_s[(r0 + r) / G], g = (r0 + r) % G;
-                        val = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(P.q) + b * P.qb + t * P.qt +
-                                                              (long long)(h * G + g) * P.qh + u * 8);
-                    }
-                    *reinterpret_cast<uint4*>(q_s + tile_at<DP>(r, u)) = val;
-                }
-                for (int r = tid; r < padded; r += kThreads) {
-                    float lse = INFINITY;  // a padding row: exp(-inf) = 0
-                    unsigned long long word = 0;
-                    if (r < nr) {
-                        const int t = node_s[(r0 + r) / G], g = (r0 + r) % G;
-                        lse = P.lse[((long long)b * T + t) * P.Hq + h * G + g];
-                        word = word_of(P.mask, T, b, t);
-                    }
-                    // a row that saw nothing gives nothing
-                    lse_s[r] = lse == -INFINITY ? INFINITY : lse * kLog2e;
-                    word_s[r] = word;
-                }
-                have_h = h;
-                have_block = r0;
-                __syncthreads();
-            }
-            const bool edge = a.tile * KT + warp * 16 + 16 > len;
-            for (int n = 0; n < nr; n += 8) {
-                float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-                for (int k = 0; k < KD; k += 2) {
-                    // rows n .. n+7, d 32 wide: two k steps
-                    uint32_t qf[4];
-                    ldsm4(qf, smem_u32(q_s) + tile_at<DP>(n + (lane & 7), 2 * k + (lane >> 3)));
-#pragma unroll
-                    for (int kk = 0; kk < 2; ++kk) {
-                        if (DP > 128) {
-                            uint32_t kx[4];
-                            ldsm4(kx, k_s + tile_at<DP>(warp * 16 + (lane & 15), 2 * (k + kk) + (lane >> 4)));
-                            mma<FP16>(s, kx, qf[2 * kk], qf[2 * kk + 1]);
-                        } else {
-                            mma<FP16>(s, kf[DP <= 128 ? k + kk : 0], qf[2 * kk], qf[2 * kk + 1]);
-                        }
-                    }
-                }
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int r = n + (lane & 3) * 2 + (e & 1);
-                    const int j = i0 + (e >> 1) * 8 - len;
-                    const bool sees = r < nr && (!edge || j < 0 || (j < T && (word_s[r] >> (j & 63) & 1)));
-                    const float p = ex2(fmaf(s[e], c2, -lse_s[r]));
-                    w[e >> 1] += sees ? p : 0.0f;
-                }
-            }
-        }
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            w[e] += __shfl_xor_sync(0xFFFFFFFFu, w[e], 1);
-            w[e] += __shfl_xor_sync(0xFFFFFFFFu, w[e], 2);
-            const int key = stage * KT + warp * 16 + (lane >> 2) + e * 8;
-            const int slot = slot_s[key];
-            if ((lane & 3) == 0 && slot >= 0) P.acc_out[b * C.ab + h * C.ah + slot] = old_s[key] + w[e];
-        }
-    }
-    cp_wait<0>();
-}
-
 // ------------------------------------------------------------------ host
-
-int sm_count() {
-    int dev = 0, sms = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return 0;
-    if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
-    return sms;
-}
-
-cudaError_t launch(const void* fn, dim3 grid, int threads, size_t smem, void** args, cudaStream_t st) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3(threads, 1, 1);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelExC(&cfg, fn, args);
-}
 
 int per_sm(int dp) { return dp <= 128 ? 2 : 1; }
 int padded(int D) { return D <= 64 ? 64 : D <= 128 ? 128 : 256; }
-int row_warps(int R, int dp) { return R <= 16 ? 1 : R <= 32 || dp > 128 ? 2 : 4; }
+int row_warps(int R) { return R <= 16 ? 1 : 2; }  // more rows than 32 go in further row blocks
+
+// Up to 16 rows a key: the tiles above, bound by memory. More rows: 128-row
+// tiles on the tensor memory path, whose cost a key does not depend on the
+// rows (heads of more than 128 elements do not fit there).
+bool wide_rows(int D, int R) { return R > 16 && D <= 128; }
+
+template <int DP, int RB, bool FP16>
+cudaError_t launch_join(const AttendParams& P, int row_blocks, int parts, cudaStream_t st) {
+    void* args[3] = {const_cast<AttendParams*>(&P), &row_blocks, &parts};
+    const long long lists = (long long)P.c.B * P.c.Hkv * row_blocks;
+    const int rows = P.T * P.G < RB ? P.T * P.G : RB;
+    const bool many = parts >= 4 * lists;  // parts of a list: about parts / lists
+    const int per_block = many ? 1 : kJoinWarps;
+    const long long blocks = lists * ((rows + per_block - 1) / per_block);
+    if (blocks > 0x7FFFFFFFLL) return cudaErrorInvalidValue;
+    const void* join = many ? reinterpret_cast<const void*>(&k_tree_attention_join<DP, RB, kJoinWarps, FP16>)
+                            : reinterpret_cast<const void*>(&k_tree_attention_join<DP, RB, 1, FP16>);
+    return launch(join, dim3((unsigned)blocks, 1, 1), kJoinWarps * 32, (3 * P.c.B + 1) * 4, args, st);
+}
 
 template <int DP, int MW, bool FP16>
 cudaError_t launch_attend(const AttendParams& P, cudaStream_t st) {
@@ -959,72 +540,39 @@ cudaError_t launch_attend(const AttendParams& P, cudaStream_t st) {
     void* args[2] = {const_cast<AttendParams*>(&P), &row_blocks};
     e = launch(reinterpret_cast<const void*>(kern), dim3(parts, 1, 1), kThreads, AttendCfg<DP>::smem(P.c.B), args, st);
     if (e != cudaSuccess) return e;
-    void* jargs[3] = {const_cast<AttendParams*>(&P), &row_blocks, &parts};
-    const long long lists = (long long)P.c.B * P.c.Hkv * row_blocks;
-    const int rows = R < 16 * MW ? R : 16 * MW;
-    const bool many = parts >= 4 * lists;  // parts of a list: about parts / lists
-    const int per_block = many ? 1 : kJoinWarps;
-    const long long blocks = lists * ((rows + per_block - 1) / per_block);
-    if (blocks > 0x7FFFFFFFLL) return cudaErrorInvalidValue;
-    const void* join = many ? reinterpret_cast<const void*>(&k_tree_attention_join<DP, MW, kJoinWarps, FP16>)
-                            : reinterpret_cast<const void*>(&k_tree_attention_join<DP, MW, 1, FP16>);
-    return launch(join, dim3((unsigned)blocks, 1, 1), kJoinWarps * 32, (3 * P.c.B + 1) * 4, jargs, st);
-}
-
-template <int DP, bool FP16>
-cudaError_t launch_attend_rows(const AttendParams& P, cudaStream_t st) {
-    switch (row_warps(P.T * P.G, DP)) {
-        case 1: return launch_attend<DP, 1, FP16>(P, st);
-        case 2: return launch_attend<DP, 2, FP16>(P, st);
-        default:
-            if constexpr (DP <= 128) return launch_attend<DP, 4, FP16>(P, st);
-            else return cudaErrorInvalidValue;
-    }
+    return launch_join<DP, 16 * MW, FP16>(P, row_blocks, parts, st);
 }
 
 template <bool FP16>
 cudaError_t launch_attend_type(const AttendParams& P, cudaStream_t st) {
+    const int R = P.T * P.G;
     switch (padded(P.c.D)) {
-        case 64: return launch_attend_rows<64, FP16>(P, st);
-        case 128: return launch_attend_rows<128, FP16>(P, st);
-        default: return launch_attend_rows<256, FP16>(P, st);
+        case 64: return launch_attend<64, 1, FP16>(P, st);
+        case 128: return launch_attend<128, 1, FP16>(P, st);
+        default: return row_warps(R) == 1 ? launch_attend<256, 1, FP16>(P, st) : launch_attend<256, 2, FP16>(P, st);
     }
 }
 
-template <int DP, bool FP16>
-cudaError_t launch_weigh(const AttendParams& P, cudaStream_t st) {
-    const int sms = sm_count();
-    if (sms < 1) return cudaErrorInvalidDevice;
-    const auto kern = k_kv_accumulate<DP, FP16>;
-    cudaError_t e = allow_max_smem(kern);
+template <int DP>
+cudaError_t launch_wide(const AttendParams& P, cudaStream_t st) {
+    int row_blocks = 0, parts = 0;
+    const cudaError_t e = launch_tree_attention_wide(P, &row_blocks, &parts, st);
     if (e != cudaSuccess) return e;
-    void* args[1] = {const_cast<AttendParams*>(&P)};
-    return launch(reinterpret_cast<const void*>(kern), dim3(sms * per_sm(DP), 1, 1), kThreads,
-                  WeighCfg<DP>::smem(P.c.B), args, st);
-}
-
-template <bool FP16>
-cudaError_t launch_weigh_type(const AttendParams& P, cudaStream_t st) {
-    switch (padded(P.c.D)) {
-        case 64: return launch_weigh<64, FP16>(P, st);
-        case 128: return launch_weigh<128, FP16>(P, st);
-        default: return launch_weigh<256, FP16>(P, st);
-    }
+    return P.c.fp16 ? launch_join<DP, kWideRows, true>(P, row_blocks, parts, st)
+                    : launch_join<DP, kWideRows, false>(P, row_blocks, parts, st);
 }
 
 }  // namespace
 
 long long attend_partial_floats(int D, int T, int G) {
-    const int sms = sm_count();
-    return 2ll * sms * per_sm(padded(D)) * part_floats(16 * row_warps(T * G, padded(D)), padded(D));
+    const int dp = padded(D), R = T * G;
+    const int rows = wide_rows(D, R) ? kWideRows : 16 * row_warps(R);
+    return 2ll * sm_count() * per_sm(dp) * part_floats(rows, dp);
 }
 
 cudaError_t launch_tree_attention(const AttendParams& P, cudaStream_t st) {
+    if (wide_rows(P.c.D, P.T * P.G)) return P.c.D <= 64 ? launch_wide<64>(P, st) : launch_wide<128>(P, st);
     return P.c.fp16 ? launch_attend_type<true>(P, st) : launch_attend_type<false>(P, st);
-}
-
-cudaError_t launch_kv_accumulate(const AttendParams& P, cudaStream_t st) {
-    return P.c.fp16 ? launch_weigh_type<true>(P, st) : launch_weigh_type<false>(P, st);
 }
 
 }  // namespace si

@@ -1,0 +1,245 @@
+// attend.cuh -- what the cache attention's kernels share: the schedule that
+// deals a launch's tiles of keys to its CTAs, the gathered copies, and the
+// warp-level matrix instructions.
+#pragma once
+
+#include <cuda_fp16.h>
+
+#include <climits>
+#include <cmath>
+
+#include "common.cuh"
+#include "internal.h"
+
+namespace si {
+namespace {
+
+constexpr int KT = 64;             // keys per tile
+constexpr float kLog2e = 1.4426950408889634f;
+
+// ------------------------------------------------------------- primitives
+
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool on) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr));
+}
+__device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr));
+}
+
+// d += a (16 x 16) * b (16 x 8), fp32 accumulators
+template <bool FP16>
+__device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    if (FP16)
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+            "{%0, %1, %2, %3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    else
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+            "{%0, %1, %2, %3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+template <bool FP16>
+__device__ __forceinline__ uint32_t pack(float a, float b) {
+    uint32_t w;
+    if (FP16) {
+        const __half2 h = __floats2half2_rn(a, b);
+        w = *reinterpret_cast<const uint32_t*>(&h);
+    } else {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+        w = *reinterpret_cast<const uint32_t*>(&h);
+    }
+    return w;
+}
+
+template <bool FP16>
+__device__ __forceinline__ bool not_finite(uint16_t w) {
+    return FP16 ? (w & 0x7C00u) == 0x7C00u : (w & 0x7F80u) == 0x7F80u;
+}
+
+template <bool FP16>
+__device__ __forceinline__ float widen(uint16_t w) {
+    if (FP16) return __half2float(*reinterpret_cast<const __half*>(&w));
+    return __uint_as_float((uint32_t)w << 16);
+}
+
+// Byte offset of 16-byte unit `unit` of row `row` in a tile of rows of DP
+// 16-bit elements; the unit index is XORed with the row's low bits so that
+// the eight rows of an ldmatrix lie in different banks.
+template <int DP>
+__device__ __forceinline__ uint32_t tile_at(int row, int unit) {
+    return (uint32_t)(row * (DP * 2) + ((unit ^ (row & 7)) * 16));
+}
+
+// --------------------------------------------------------------- schedule
+
+// The lists of one launch: `groups` lists a sequence (cache heads x row
+// blocks), each of ntile(b) tiles.
+struct Plan {
+    int* len;         // [B] live keys (0 where the sequence is out of bounds)
+    int* tot;         // [B] live keys + new nodes (0 likewise)
+    int* first;       // [B + 1] flat index of the sequence's first tile
+};
+
+__device__ __forceinline__ int tiles_of(int tot) { return tot > KT ? (tot + KT - 1) / KT : 1; }
+
+// Fills the plan (all threads; ends with a barrier). Lengths are read once.
+template <int THREADS>
+__device__ void make_plan(const KvView& C, int T, int groups, const Plan& p, unsigned* err, bool report) {
+    for (int b = threadIdx.x; b < C.B; b += THREADS) {
+        const int len = C.len[b];
+        const bool ok = len >= 0 && len <= C.cap - T;
+        if (!ok && report) atomicOr(err, SI_DEVERR_CACHE);
+        p.len[b] = ok ? len : 0;
+        p.tot[b] = ok ? len + T : 0;
+    }
+    __syncthreads();
+    if (threadIdx.x < 32) {
+        int base = 0;
+        for (int b0 = 0; b0 < C.B; b0 += 32) {
+            const int b = b0 + (int)threadIdx.x;
+            const int mine = b < C.B ? tiles_of(p.tot[b]) * groups : 0;
+            int incl = mine;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int v = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+                if ((int)threadIdx.x >= o) incl += v;
+            }
+            if (b < C.B) p.first[b] = base + incl - mine;
+            base += __shfl_sync(0xFFFFFFFFu, incl, 31);
+        }
+        if (threadIdx.x == 0) p.first[C.B] = base;
+    }
+    __syncthreads();
+}
+
+// The tiles are dealt out in parts of n / parts or one more; the first n %
+// parts CTAs have the longer ones. All in 32 bits: these run once per part of
+// every list when rows are joined.
+struct Deal {
+    unsigned base, rem;
+    __device__ __forceinline__ Deal(int total, int parts) {
+        base = (unsigned)total / (unsigned)parts;
+        rem = (unsigned)total - base * (unsigned)parts;
+    }
+    __device__ __forceinline__ int start(int part) const { return (int)(part * base + min((unsigned)part, rem)); }
+    // the part that has tile x
+    __device__ __forceinline__ int owner(int x) const {
+        const unsigned longer = rem * (base + 1);
+        return (int)((unsigned)x < longer ? (unsigned)x / (base + 1) : rem + ((unsigned)x - longer) / base);
+    }
+};
+
+// A position in the flat order of tiles.
+struct At {
+    int b, group, tile, ntile;
+};
+
+__device__ __forceinline__ At locate(const Plan& p, int B, int x) {
+    int lo = 0, hi = B - 1;  // last b with first[b] <= x
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (p.first[mid] <= x) lo = mid;
+        else hi = mid - 1;
+    }
+    At a;
+    a.b = lo;
+    a.ntile = tiles_of(p.tot[lo]);
+    const int in = x - p.first[lo];
+    a.group = in / a.ntile;
+    a.tile = in - a.group * a.ntile;
+    return a;
+}
+
+__device__ __forceinline__ void step(const Plan& p, int B, int groups, At& a) {
+    if (++a.tile < a.ntile) return;
+    a.tile = 0;
+    if (++a.group < groups) return;
+    a.group = 0;
+    if (++a.b < B) a.ntile = tiles_of(p.tot[a.b]);
+}
+
+// Ancestor word of node t (mask NULL: a chain).
+__device__ __forceinline__ unsigned long long word_of(const unsigned long long* mask, int T, int b, int t) {
+    return mask ? mask[(long long)b * T + t] : (t >= 63 ? ~0ull : (2ull << t) - 1);
+}
+
+constexpr int kNoSlot = INT_MIN;
+
+// Slot of list entry i, or kNoSlot where nothing is to be read. The value is not
+// looked at here: it is used a tile later, so the load's latency is hidden.
+__device__ __forceinline__ int slot_of(const int32_t* list, int i, int len, int tot, unsigned long long seen) {
+    const bool on = i < len || (i < tot && (seen >> ((i - len) & 63) & 1));
+    if (!on) return kNoSlot;
+    return list ? list[i] : i;
+}
+
+// A slot outside the pool is reported and not read.
+__device__ __forceinline__ bool slot_ok(int slot, int n_slots, unsigned* err) {
+    if ((unsigned)slot < (unsigned)n_slots) return true;
+    if (slot != kNoSlot) atomicOr(err, SI_DEVERR_CACHE);
+    return false;
+}
+
+// Floats of one partial: RB rows of output, then their maxima and sums.
+constexpr int part_floats(int rb, int dp) { return rb * (dp + 2); }
+
+constexpr int kWideRows = 128;     // query rows a block of the tensor-memory kernel has
+
+// Who copies what: a warp copies KEYS keys of every tile, lane i < KEYS
+// holding the slot of its key i.
+template <int DP, int KEYS = 16>
+struct Copy {
+    static constexpr int UNITS = DP / 8;            // 16-byte units of a row
+    static constexpr int AT_ONCE = 32 / UNITS;      // rows one sweep of a warp copies
+    static constexpr int SWEEPS = KEYS / AT_ONCE;
+    // row (of the warp's) that this lane copies in sweep j
+    static __device__ __forceinline__ int row(int lane, int j) { return (lane / UNITS) * SWEEPS + j; }
+};
+
+inline int sm_count() {
+    int dev = 0, sms = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+    if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+    return sms;
+}
+
+inline cudaError_t launch(const void* fn, dim3 grid, int threads, size_t smem, void** args, cudaStream_t st) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelExC(&cfg, fn, args);
+}
+
+}  // namespace
+}  // namespace si

@@ -1,0 +1,500 @@
+// attend_wide.cu -- tree attention for many rows a key (wide trees, shared
+// heads) on the 5th-generation tensor cores.
+//
+// A block of 128 query rows of one list meets tiles of 64 keys:
+//   S = Q K^T   tcgen05.mma M = 128, N = 64, K = D    (accumulator in TMEM)
+//   P = exp(scale (S - m))                            (one thread a row)
+//   O += P V    tcgen05.mma M = 128, N = D, K = 64    (accumulator in TMEM)
+// The value tile serves as it lies, [key][d], as an operand with d contiguous.
+// The reference m of a row moves only when the maximum outgrows it by a
+// factor of 2^8: weights up to 256 are as exact in 16 bits as weights up to
+// 1, and the sums are in 32 bits, so the output is rescaled a few times a
+// list instead of once a tile.
+//
+// Warps: 0-3 softmax and output (TMEM lanes 32 w ..), 4 issues the matrix
+// instructions, 5 and 6 copy keys and values through the slot table (16-byte
+// asynchronous copies into the 128-byte swizzle the tensor cores read). Two
+// CTAs share an SM, so one's softmax runs under the other's products.
+// All waits are bounded; TMEM is always released.
+#include "attend.cuh"
+
+namespace si {
+
+namespace {
+
+constexpr int kThreads = 7 * 32;
+constexpr int kSoftmaxThreads = 128, kCopyThreads = 64;
+constexpr int kMaxSlots = 4;       // ring slots: a key or a value tile each
+
+template <int DP>
+struct WideCfg {
+    static constexpr int kTile = KT * DP * 2;
+    static constexpr int kQ = kWideRows * DP * 2;
+    static constexpr int kP = kWideRows * KT * 2;
+    static constexpr int kOffP = kQ, kOffRing = kQ + kP;
+    static constexpr int kTmemCols = DP == 128 ? 256 : 128;    // S at 0, O at 64
+    static constexpr int fixed(int B) { return 16 * 8 + kMaxSlots * 8 + 16 + (3 * B + 1) * 4; }
+    static constexpr int smem(int B, int slots) { return kOffRing + slots * kTile + fixed(B); }
+};
+
+// 128-byte swizzled tile of rows of 64 elements: byte offset of 16-byte unit
+// c (0..7) of row r.
+__device__ __forceinline__ uint32_t sw128(int r, int c) { return (uint32_t)(r * 128 + ((c ^ (r & 7)) << 4)); }
+
+// Shared-memory matrix descriptor, 128-byte swizzle: start address >> 4 (bits
+// 0-13), leading offset >> 4 (16-29), stride offset >> 4 (32-45), version 1
+// (46-47), swizzle mode 2 (61-63). Stride: 1024 bytes between groups of eight
+// 128-byte rows. Leading: between sub-tiles of 64 elements where the rows are
+// the reduced dimension (the value tile), unused otherwise.
+__device__ __forceinline__ uint64_t desc128(uint32_t saddr, uint32_t lead) {
+    return (uint64_t)((saddr >> 4) & 0x3FFFu) | ((uint64_t)(lead >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
+           ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+
+__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+
+__device__ __forceinline__ void tc_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate)
+        : "memory");
+}
+
+__device__ __forceinline__ void tc_commit(uint64_t* bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
+                 : "memory");
+}
+
+// 32 fp32 columns of this thread's TMEM lane
+__device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t* r) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(addr));
+}
+__device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t* r) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(addr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+        "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+        "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+        : "memory");
+}
+__device__ __forceinline__ void tmem_ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+}  // namespace
+
+template <int DP, bool FP16>
+__global__ void __launch_bounds__(kThreads, 2)
+    k_tree_attention_wide(const __grid_constant__ AttendParams P, int row_blocks, int slots) {
+    using Cfg = WideCfg<DP>;
+    using Cp = Copy<DP, 32>;
+    extern __shared__ __align__(1024) uint8_t smem[];  // the swizzle needs tiles on 1024-byte boundaries
+    uint8_t* const q_s = smem;
+    uint8_t* const p_s = smem + Cfg::kOffP;
+    uint8_t* const ring = smem + Cfg::kOffRing;
+    uint64_t* const full = reinterpret_cast<uint64_t*>(ring + slots * Cfg::kTile);
+    uint64_t* const empty = full + kMaxSlots;
+    uint64_t* const q_full = empty + kMaxSlots;  // this list's queries are in shared memory
+    uint64_t* const s_full = q_full + 1;         // S of a tile is in TMEM
+    uint64_t* const s_free = q_full + 2;         // and has been read
+    uint64_t* const p_full = q_full + 3;         // P of a tile is in shared memory
+    uint64_t* const o_done = q_full + 4;         // O includes the tile
+    unsigned* const odd = reinterpret_cast<unsigned*>(full + 16);  // [slot][2]: keys of a value tile that are not finite
+    uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(odd + kMaxSlots * 2);
+    Plan plan;
+    plan.len = reinterpret_cast<int*>(tmem_slot + 4);
+    plan.tot = plan.len + P.c.B;
+    plan.first = plan.tot + P.c.B;
+
+    const KvView& C = P.c;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int T = P.T, G = P.G, R = T * G, D = C.D;
+    const int groups = C.Hkv * row_blocks;
+
+    if (smem_u32(smem) & 1023u) {  // never seen: dynamic shared memory starts on such a boundary
+        if (tid == 0) atomicOr(P.err, SI_DEVERR_COUNT);
+        return;
+    }
+    if (tid == 0) {
+        for (int s = 0; s < kMaxSlots; ++s) {
+            mbar_init(&full[s], kCopyThreads);
+            mbar_init(&empty[s], 1);
+        }
+        mbar_init(q_full, kSoftmaxThreads);
+        mbar_init(s_full, 1);
+        mbar_init(s_free, kSoftmaxThreads);
+        mbar_init(p_full, kSoftmaxThreads);
+        mbar_init(o_done, 1);
+        fence_mbar_init();
+    }
+    if (warp == 4) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
+                     "r"(Cfg::kTmemCols)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+        tc_fence_before();
+    }
+    grid_launch_dependents();
+    grid_dependency_wait();
+    make_plan<kThreads>(C, T, groups, plan, P.err, blockIdx.x == 0);  // ends with a barrier
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    const Deal deal(plan.first[C.B], gridDim.x);
+    const int x0 = deal.start(blockIdx.x), x1 = deal.start(blockIdx.x + 1);
+
+    if (x0 >= x1) {
+        // more CTAs than tiles: nothing to do
+    } else if (warp >= 5) {
+        // ---------------------------------------------------------- copies
+        const int own0 = (warp - 5) * 32, unit = lane % Cp::UNITS;
+        const bool unit_on = unit * 8 < D;
+        const int n_slots = (int)C.n_slots, k_step = (int)C.ks, v_step = (int)C.vs;
+        const uint32_t col = (uint32_t)(unit >> 3) * (KT * 128);  // sub-tile of this lane's unit
+        At a = locate(plan, C.B, x0);
+        unsigned long long seen = 0;
+        int seen_b = -1;
+        auto fetch = [&]() {
+            const int h = a.group / row_blocks;
+            const int32_t* list = C.table ? C.table + a.b * C.tb + h * C.th : nullptr;
+            const int len = plan.len[a.b], i0 = a.tile * KT;
+            if (i0 + KT > len && seen_b != a.b) {
+                unsigned long long mine = lane < T ? word_of(P.mask, T, a.b, lane) : 0;
+                if (lane + 32 < T) mine |= word_of(P.mask, T, a.b, lane + 32);
+                seen = (unsigned long long)__reduce_or_sync(0xFFFFFFFFu, (unsigned)(mine >> 32)) << 32 |
+                       __reduce_or_sync(0xFFFFFFFFu, (unsigned)mine);
+                seen_b = a.b;
+            }
+            return slot_of(list, i0 + own0 + lane, len, plan.tot[a.b], seen);
+        };
+        auto copy = [&](uint32_t dst, const uint16_t* base, int step_, int slot) {
+#pragma unroll
+            for (int j = 0; j < Cp::SWEEPS; ++j) {
+                const int r = Cp::row(lane, j);
+                const int at_slot = __shfl_sync(0xFFFFFFFFu, slot, r);
+                const bool on = at_slot >= 0 && unit_on;
+                const long long from = on ? at_slot : 0;
+                cp16(dst + col + sw128(own0 + r, unit & 7), on ? base + from * step_ : base - unit * 8, on);
+            }
+            cp_commit();
+        };
+        // The copy two groups back has landed: make it visible to the tensor cores.
+        auto finish = [&](int slot_at) {
+            fence_proxy_async_smem();
+            mbar_arrive(&full[slot_at]);
+        };
+        // New nodes' value rows that are not finite leave the tile (0 * NaN is NaN) and are
+        // reported, so that the rows that see them get them back at the end.
+        auto clean = [&](int slot_at, int i0, int len) {
+            uint8_t* tile = ring + slot_at * Cfg::kTile;
+            unsigned bad = 0;
+#pragma unroll 1
+            for (int j = 0; j < Cp::SWEEPS; ++j) {
+                const int r = Cp::row(lane, j), node = i0 + own0 + r - len;
+                if (node < 0 || node >= T) continue;
+                uint16_t* e = reinterpret_cast<uint16_t*>(tile + col + sw128(own0 + r, unit & 7));
+                for (int i = 0; i < 8; ++i)
+                    if (not_finite<FP16>(e[i])) e[i] = 0, bad |= 1u << r;
+            }
+            bad = __reduce_or_sync(0xFFFFFFFFu, bad);
+            if (lane == 0) odd[slot_at * 2 + (warp - 5)] = bad;
+        };
+        int next = fetch();
+        int at = 0, fill = 0;               // ring slot of the next group and how often the ring has been round
+        int k_prev = -1, v_prev = -1;       // slots of the previous tile's copies
+        int i0_prev = 0, len_prev = 0;
+        auto take = [&]() {
+            if (fill > 0) mbar_wait(&empty[at], (uint32_t)((fill - 1) & 1), P.err, kSiteAttend | kSiteEmpty);
+            __syncwarp();
+            const int mine = at;
+            if (++at == slots) at = 0, ++fill;
+            return mine;
+        };
+        for (int x = x0; x < x1; ++x) {
+            const int h = a.group / row_blocks, i0 = a.tile * KT, len = plan.len[a.b];
+            const uint16_t* kp = static_cast<const uint16_t*>(C.k) + a.b * C.kb + h * C.kh + unit * 8;
+            const uint16_t* vp = static_cast<const uint16_t*>(C.v) + a.b * C.vb + h * C.vh + unit * 8;
+            const int slot = slot_ok(next, n_slots, P.err) ? next : -1;
+            const int k_at = take();
+            copy(smem_u32(ring + k_at * Cfg::kTile), kp, k_step, slot);
+            step(plan, C.B, groups, a);
+            if (x + 1 < x1) next = fetch();
+            if (k_prev >= 0) {
+                cp_wait<2>();
+                finish(k_prev);
+            }
+            const int v_at = take();
+            copy(smem_u32(ring + v_at * Cfg::kTile), vp, v_step, slot);
+            if (v_prev >= 0) {
+                cp_wait<2>();
+                if (i0_prev + KT > len_prev) clean(v_prev, i0_prev, len_prev);
+                finish(v_prev);
+            }
+            k_prev = k_at, v_prev = v_at, i0_prev = i0, len_prev = len;
+        }
+        cp_wait<1>();
+        finish(k_prev);
+        cp_wait<0>();
+        if (i0_prev + KT > len_prev) clean(v_prev, i0_prev, len_prev);
+        finish(v_prev);
+    } else if (warp == 4) {
+        // ------------------------------------------------- matrix products
+        if (lane == 0) {
+            constexpr uint32_t kType = FP16 ? 0u : (1u << 7) | (1u << 10);
+            constexpr uint32_t kCommon = (1u << 4) | kType | ((uint32_t)(kWideRows >> 4) << 24);
+            constexpr uint32_t kDescS = kCommon | ((uint32_t)(KT >> 3) << 17);
+            constexpr uint32_t kDescO = kCommon | (1u << 16) | ((uint32_t)(DP >> 3) << 17);  // V: d contiguous
+            const uint32_t q_addr = smem_u32(q_s), p_addr = smem_u32(p_s);
+            At a = locate(plan, C.B, x0);
+            int at = 0, round = 0, lists = 0;
+            bool fresh = false;              // the tile whose product with V is pending starts its list's O
+            int v_at = 0, v_round = 0;
+            auto take = [&](int& slot_at, int& slot_round) {
+                slot_at = at, slot_round = round;
+                if (++at == slots) at = 0, ++round;
+            };
+            auto pv = [&](int n) {
+                mbar_wait(p_full, (uint32_t)(n & 1), P.err, kSiteAttend | kSiteAccum);
+                mbar_wait(&full[v_at], (uint32_t)(v_round & 1), P.err, kSiteAttend | kSiteFull);
+                tc_fence_after();
+                const uint32_t v_addr = smem_u32(ring + v_at * Cfg::kTile);
+#pragma unroll
+                for (int k = 0; k < KT / 16; ++k)
+                    tc_mma(tmem + 64, desc128(p_addr + k * 32, 16), desc128(v_addr + k * 16 * 128, KT * 128), kDescO,
+                           !fresh || k > 0);
+                tc_commit(&empty[v_at]);
+                tc_commit(o_done);
+            };
+            for (int n = 0; n < x1 - x0; ++n) {
+                const bool first = n == 0 || a.tile == 0;
+                if (first) {
+                    // the softmax warps load the next list's queries once they have the last list's O
+                    if (n > 0) pv(n - 1);
+                    mbar_wait(q_full, (uint32_t)(lists++ & 1), P.err, kSiteAttend | kSiteFull);
+                }
+                int k_at, k_round;
+                take(k_at, k_round);
+                mbar_wait(&full[k_at], (uint32_t)(k_round & 1), P.err, kSiteAttend | kSiteFull);
+                if (n > 0) mbar_wait(s_free, (uint32_t)((n - 1) & 1), P.err, kSiteAttend | kSiteAccum);
+                tc_fence_after();
+                const uint32_t k_addr = smem_u32(ring + k_at * Cfg::kTile);
+#pragma unroll
+                for (int k = 0; k < DP / 16; ++k)
+                    tc_mma(tmem, desc128(q_addr + (k >> 2) * (kWideRows * 128) + (k & 3) * 32, 16),
+                           desc128(k_addr + (k >> 2) * (KT * 128) + (k & 3) * 32, 16), kDescS, k > 0);
+                tc_commit(&empty[k_at]);
+                tc_commit(s_full);
+                if (n > 0 && !first) pv(n - 1);
+                take(v_at, v_round);
+                fresh = first;
+                step(plan, C.B, groups, a);
+            }
+            pv(x1 - x0 - 1);
+        }
+        __syncwarp();
+    } else {
+        // --------------------------------------------- softmax and output
+        const float c2 = P.scale * kLog2e;
+        const uint32_t t_s = tmem + ((uint32_t)(warp * 32) << 16), t_o = t_s + 64;
+        const int r = warp * 32 + lane;  // this thread's row of the block
+        At a = locate(plan, C.B, x0);
+        int n = 0, segment = 0, v_at = 0, v_round = 0;  // ring position of the value tile of tile n
+        auto advance = [&]() {
+            if (++v_at == slots) v_at = 0, ++v_round;
+        };
+        for (int x = x0; x < x1; ++segment) {
+            const int b = a.b, h = a.group / row_blocks, rb = a.group % row_blocks;
+            const int len = plan.len[b], tot = plan.tot[b];
+            const int seg_end = min(x1, x + a.ntile - a.tile);
+            const bool whole = a.tile == 0 && seg_end - x == a.ntile;
+            const int row = rb * kWideRows + r;
+            const int t = row / G, g = row - t * G;
+            const bool real = row < R;
+            {
+                const uint16_t* src = static_cast<const uint16_t*>(P.q) + b * P.qb + t * P.qt + (long long)(h * G + g) * P.qh;
+#pragma unroll
+                for (int u = 0; u < DP / 8; ++u) {
+                    uint4 val = make_uint4(0, 0, 0, 0);
+                    if (real && u * 8 < D) val = *reinterpret_cast<const uint4*>(src + u * 8);
+                    *reinterpret_cast<uint4*>(q_s + (u >> 3) * (kWideRows * 128) + sw128(r, u & 7)) = val;
+                }
+                fence_proxy_async_smem();
+                mbar_arrive(q_full);
+            }
+            const unsigned long long word = real && tot > 0 ? word_of(P.mask, T, b, t) : 0;
+            float ref = -INFINITY, sum = 0.0f;
+            unsigned long long odd_nodes = 0;  // new nodes whose values were taken out and that this row sees
+            const int n_first = n;
+            for (; x < seg_end; ++x, ++n, ++a.tile) {
+                advance();  // past the key tile
+                mbar_wait(s_full, (uint32_t)(n & 1), P.err, kSiteAttend | kSiteAccum);
+                __syncwarp();
+                tc_fence_after();
+                uint32_t s[KT];
+                tmem_ld32(t_s, s);
+                tmem_ld32(t_s + 32, s + 32);
+                tmem_ld_wait();
+                tc_fence_before();
+                mbar_arrive(s_free);
+                const int i0 = a.tile * KT;
+                if (i0 + KT > len) {  // the tile meets the new nodes or the list's end
+                    // which of the 64 keys this row sees
+                    const int cut = len - i0;  // keys before it are cached ones
+                    unsigned long long vis = 0;
+                    if (cut > 0) vis = (1ull << cut) - 1;  // cut < 64 here
+                    const unsigned long long nodes = T >= 64 ? word : word & ((1ull << T) - 1);
+                    if (cut >= 0) vis |= nodes << cut;
+                    else if (cut > -64) vis |= nodes >> -cut;
+#pragma unroll
+                    for (int i = 0; i < KT; ++i)
+                        if (!(vis >> i & 1)) s[i] = 0xFF800000u;  // -inf
+                    mbar_wait(&full[v_at], (uint32_t)(v_round & 1), P.err, kSiteAttend | kSiteFull);
+                    unsigned long long bad = *reinterpret_cast<const unsigned long long*>(odd + v_at * 2) & vis;
+                    if (bad) odd_nodes |= cut >= 0 ? bad >> cut : bad << -cut;
+                }
+                float top = __uint_as_float(s[0]);
+#pragma unroll
+                for (int i = 1; i < KT; ++i) top = fmaxf(top, __uint_as_float(s[i]));
+                float keep = 1.0f;
+                if (ref == -INFINITY) {
+                    ref = top;  // nothing seen so far, O's row is 0
+                } else if ((top - ref) * c2 > 8.0f) {
+                    keep = ex2((ref - top) * c2);
+                    ref = top;
+                    sum *= keep;
+                }
+                if (n > n_first) mbar_wait(o_done, (uint32_t)((n - 1) & 1), P.err, kSiteAttend | kSiteAccum);
+                if (__any_sync(0xFFFFFFFFu, keep != 1.0f) && n > n_first) {
+                    tc_fence_after();
+#pragma unroll 1
+                    for (int c = 0; c < DP; c += 32) {
+                        uint32_t o[32];
+                        tmem_ld32(t_o + c, o);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * keep);
+                        tmem_st32(t_o + c, o);
+                    }
+                    tmem_st_wait();
+                    tc_fence_before();
+                }
+                const float shift = ref == -INFINITY ? 0.0f : ref;
+#pragma unroll
+                for (int u = 0; u < KT / 8; ++u) {
+                    uint32_t w[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float p0 = ex2((__uint_as_float(s[u * 8 + 2 * i]) - shift) * c2);
+                        const float p1 = ex2((__uint_as_float(s[u * 8 + 2 * i + 1]) - shift) * c2);
+                        sum += p0 + p1;
+                        w[i] = pack<FP16>(p0, p1);  // rounded to the cache's type for the product with V
+                    }
+                    *reinterpret_cast<uint4*>(p_s + sw128(r, u)) = make_uint4(w[0], w[1], w[2], w[3]);
+                }
+                fence_proxy_async_smem();
+                mbar_arrive(p_full);
+                advance();  // past the value tile
+            }
+            if (a.tile == a.ntile) {
+                a.tile = a.ntile - 1;
+                step(plan, C.B, groups, a);
+            }
+            // the list's O, or this CTA's part of it
+            mbar_wait(o_done, (uint32_t)((n - 1) & 1), P.err, kSiteAttend | kSiteAccum);
+            __syncwarp();
+            tc_fence_after();
+            const bool empty_row = word == 0 || sum == 0.0f;
+            const float inv = !whole ? 1.0f : empty_row ? 0.0f : 1.0f / sum;
+            const long long at = ((long long)b * T + t) * P.Hq + h * G + g;
+            uint16_t* out = static_cast<uint16_t*>(P.out) + at * D;
+            float* part = P.part + ((long long)blockIdx.x * 2 + (segment ? 1 : 0)) * part_floats(kWideRows, DP);
+            const int32_t* list = C.table ? C.table + b * C.tb + h * C.th : nullptr;
+#pragma unroll 1
+            for (int c = 0; c < DP; c += 32) {
+                uint32_t o[32];
+                tmem_ld32(t_o + c, o);
+                tmem_ld_wait();
+                for (unsigned long long left = odd_nodes; left; left &= left - 1) {
+                    const int node = __ffsll((long long)left) - 1;
+                    const long long slot = list ? list[len + node] : len + node;
+                    const uint16_t* src = static_cast<const uint16_t*>(C.v) + b * C.vb + h * C.vh + slot * C.vs;
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        if (c + i < D && not_finite<FP16>(src[c + i]))
+                            o[i] = __float_as_uint(__uint_as_float(o[i]) + widen<FP16>(src[c + i]));
+                }
+                if (!real) continue;
+                if (whole) {
+#pragma unroll
+                    for (int i = 0; i < 32; i += 8) {
+                        uint32_t w[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            w[e] = empty_row ? 0u
+                                             : pack<FP16>(__uint_as_float(o[i + 2 * e]) * inv,
+                                                          __uint_as_float(o[i + 2 * e + 1]) * inv);
+                        if (c + i < D) *reinterpret_cast<uint4*>(out + c + i) = make_uint4(w[0], w[1], w[2], w[3]);
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 32; i += 4)
+                        *reinterpret_cast<uint4*>(part + r * DP + c + i) = make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+                }
+            }
+            tc_fence_before();
+            if (real) {
+                if (!whole) {
+                    part[kWideRows * DP + r] = ref;
+                    part[kWideRows * DP + kWideRows + r] = sum;
+                } else if (P.lse) {
+                    P.lse[at] = empty_row ? -INFINITY : fmaf(ref, P.scale, logf(sum));
+                }
+            }
+        }
+    }
+    __syncthreads();
+    if (warp == 4) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(Cfg::kTmemCols) : "memory");
+    }
+}
+
+// ------------------------------------------------------------------ host
+
+namespace {
+
+template <int DP, bool FP16>
+cudaError_t launch_dp(const AttendParams& P, int row_blocks, int parts, cudaStream_t st) {
+    const auto kern = k_tree_attention_wide<DP, FP16>;
+    cudaError_t e = allow_max_smem(kern);
+    if (e != cudaSuccess) return e;
+    // as many ring slots as leave room for two CTAs an SM (228 KB, 1 KB of each CTA's is the system's)
+    int slots = kMaxSlots;
+    while (slots > 3 && WideCfg<DP>::smem(P.c.B, slots) > 113 * 1024) --slots;
+    void* args[3] = {const_cast<AttendParams*>(&P), &row_blocks, &slots};
+    return launch(reinterpret_cast<const void*>(kern), dim3(parts, 1, 1), kThreads, WideCfg<DP>::smem(P.c.B, slots), args,
+                  st);
+}
+
+}  // namespace
+
+cudaError_t launch_tree_attention_wide(const AttendParams& P, int* row_blocks, int* parts, cudaStream_t st) {
+    *row_blocks = (P.T * P.G + kWideRows - 1) / kWideRows;
+    *parts = 2 * sm_count();
+    if (*parts < 1) return cudaErrorInvalidDevice;
+    if (P.c.D <= 64)
+        return P.c.fp16 ? launch_dp<64, true>(P, *row_blocks, *parts, st) : launch_dp<64, false>(P, *row_blocks, *parts, st);
+    return P.c.fp16 ? launch_dp<128, true>(P, *row_blocks, *parts, st) : launch_dp<128, false>(P, *row_blocks, *parts, st);
+}
+
+}  // namespace si

@@ -83,6 +83,7 @@ __device__ __forceinline__ bool mbar_test_wait(uint64_t* bar, uint32_t parity) {
 // bits 16-19 (see si.h).
 enum : unsigned {
     kSiteDecode = 1u << 8, kSiteDenseAct = 2u << 8, kSiteTiered = 3u << 8, kSiteGemm = 4u << 8,
+    kSiteAttend = 6u << 8,
     kSiteFull = 1u << 16, kSiteEmpty = 2u << 16, kSiteFullB = 3u << 16, kSiteAccum = 4u << 16,
 };
 

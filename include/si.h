@@ -111,7 +111,7 @@ int si_sparse_layers(int L, int first, int last, uint8_t *sparse, int *n_sparse)
 #define SI_DEVERR_CACHE 8u          /* a cache list left its bounds (len + T > cap, a slot outside the pool) */
 /* With SI_DEVERR_WAIT_TIMEOUT, bits 8-15 name the kernel whose wait ran out
  * (1 sparse decode, 2 dense activation pass, 3 tiered down-projection,
- * 4 activation GEMM, 5 decode stack) and bits 16-19 the barrier (1 stage
+ * 4 activation GEMM, 5 decode stack, 6 tree attention) and bits 16-19 the barrier (1 stage
  * full, 2 stage empty, 3 stage full in the down-projection phase,
  * 4 accumulator ready, 5 grid barrier between layers). */
 int si_device_error(uint32_t *code, int clear);

@@ -110,13 +110,13 @@ __global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1)
             const uint16_t* kp = static_cast<const uint16_t*>(C.k) + pa.b * C.kb + h * C.kh + unit * 8;
             const uint16_t* vp = static_cast<const uint16_t*>(C.v) + pa.b * C.vb + h * C.vh + unit * 8;
             const uint32_t dst = smem_u32(tiles + stage_in * 2 * Cfg::kTile);
-            const int slot = slot_ok(next_slot, n_slots, P.err) ? next_slot : -1;
+            int slot[Cp::SWEEPS];
+            Cp::slots(slot_ok(next_slot, n_slots, P.err) ? next_slot : -1, lane, slot);
 #pragma unroll
             for (int j = 0; j < Cp::SWEEPS; ++j) {
                 const int r = Cp::row(lane, j);
-                const int at_slot = __shfl_sync(0xFFFFFFFFu, slot, r);
-                const bool on = at_slot >= 0 && unit_on;
-                const long long from = on ? at_slot : 0;
+                const bool on = slot[j] >= 0 && unit_on;
+                const long long from = on ? slot[j] : 0;
                 const uint32_t at = tile_at<DP>(own0 + r, unit);
                 cp16(dst + at, on ? kp + from * k_step : kp - unit * 8, on);
                 cp16(dst + Cfg::kTile + at, on ? vp + from * v_step : vp - unit * 8, on);

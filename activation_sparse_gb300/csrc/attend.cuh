@@ -218,6 +218,12 @@ struct Copy {
     static constexpr int SWEEPS = KEYS / AT_ONCE;
     // row (of the warp's) that this lane copies in sweep j
     static __device__ __forceinline__ int row(int lane, int j) { return (lane / UNITS) * SWEEPS + j; }
+    // Slots of the rows this lane copies, from the lanes that hold them. All at once, ahead of the copies:
+    // a shuffle between two copies would put its latency between them.
+    static __device__ __forceinline__ void slots(int held, int lane, int (&slot)[SWEEPS]) {
+#pragma unroll
+        for (int j = 0; j < SWEEPS; ++j) slot[j] = __shfl_sync(0xFFFFFFFFu, held, row(lane, j));
+    }
 };
 
 inline int sm_count() {

@@ -14,7 +14,9 @@
 // Warps: 0-3 softmax and output (TMEM lanes 32 w ..), 4 issues the matrix
 // instructions, 5 and 6 copy keys and values through the slot table (16-byte
 // asynchronous copies into the 128-byte swizzle the tensor cores read). Two
-// CTAs share an SM, so one's softmax runs under the other's products.
+// CTAs share an SM, so one's softmax runs under the other's products. Every
+// write to shared memory is an ordinary one; the issuing thread's proxy fence,
+// after the barrier that announces it, lets the tensor cores see it.
 // All waits are bounded; TMEM is always released.
 #include "attend.cuh"
 
@@ -177,21 +179,18 @@ __global__ void __launch_bounds__(kThreads, 2)
             }
             return slot_of(list, i0 + own0 + lane, len, plan.tot[a.b], seen);
         };
-        auto copy = [&](uint32_t dst, const uint16_t* base, int step_, int slot) {
+        auto copy = [&](uint32_t dst, const uint16_t* base, int step_, const int (&slot)[Cp::SWEEPS]) {
 #pragma unroll
             for (int j = 0; j < Cp::SWEEPS; ++j) {
-                const int r = Cp::row(lane, j);
-                const int at_slot = __shfl_sync(0xFFFFFFFFu, slot, r);
-                const bool on = at_slot >= 0 && unit_on;
-                const long long from = on ? at_slot : 0;
-                cp16(dst + col + sw128(own0 + r, unit & 7), on ? base + from * step_ : base - unit * 8, on);
+                const bool on = slot[j] >= 0 && unit_on;
+                const long long from = on ? slot[j] : 0;
+                cp16(dst + col + sw128(own0 + Cp::row(lane, j), unit & 7), on ? base + from * step_ : base - unit * 8, on);
             }
-            cp_commit();
         };
-        // The copy two groups back has landed: make it visible to the tensor cores.
-        auto finish = [&](int slot_at) {
-            fence_proxy_async_smem();
-            mbar_arrive(&full[slot_at]);
+        // The barrier hears of this thread's copies when they land. The thread that issues the products
+        // makes them visible to the tensor cores: a proxy fence here would wait for every copy in flight.
+        auto arrive_landed = [&](int slot_at) {
+            asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(&full[slot_at])) : "memory");
         };
         // New nodes' value rows that are not finite leave the tile (0 * NaN is NaN) and are
         // reported, so that the rows that see them get them back at the end.
@@ -211,8 +210,6 @@ __global__ void __launch_bounds__(kThreads, 2)
         };
         int next = fetch();
         int at = 0, fill = 0;               // ring slot of the next group and how often the ring has been round
-        int k_prev = -1, v_prev = -1;       // slots of the previous tile's copies
-        int i0_prev = 0, len_prev = 0;
         auto take = [&]() {
             if (fill > 0) mbar_wait(&empty[at], (uint32_t)((fill - 1) & 1), P.err, kSiteAttend | kSiteEmpty);
             __syncwarp();
@@ -224,29 +221,23 @@ __global__ void __launch_bounds__(kThreads, 2)
             const int h = a.group / row_blocks, i0 = a.tile * KT, len = plan.len[a.b];
             const uint16_t* kp = static_cast<const uint16_t*>(C.k) + a.b * C.kb + h * C.kh + unit * 8;
             const uint16_t* vp = static_cast<const uint16_t*>(C.v) + a.b * C.vb + h * C.vh + unit * 8;
-            const int slot = slot_ok(next, n_slots, P.err) ? next : -1;
+            int slot[Cp::SWEEPS];
+            Cp::slots(slot_ok(next, n_slots, P.err) ? next : -1, lane, slot);
             const int k_at = take();
             copy(smem_u32(ring + k_at * Cfg::kTile), kp, k_step, slot);
+            arrive_landed(k_at);
             step(plan, C.B, groups, a);
             if (x + 1 < x1) next = fetch();
-            if (k_prev >= 0) {
-                cp_wait<2>();
-                finish(k_prev);
-            }
             const int v_at = take();
             copy(smem_u32(ring + v_at * Cfg::kTile), vp, v_step, slot);
-            if (v_prev >= 0) {
-                cp_wait<2>();
-                if (i0_prev + KT > len_prev) clean(v_prev, i0_prev, len_prev);
-                finish(v_prev);
+            if (i0 + KT > len) {
+                asm volatile("cp.async.wait_all;" ::: "memory");
+                clean(v_at, i0, len);
+                mbar_arrive(&full[v_at]);
+            } else {
+                arrive_landed(v_at);
             }
-            k_prev = k_at, v_prev = v_at, i0_prev = i0, len_prev = len;
         }
-        cp_wait<1>();
-        finish(k_prev);
-        cp_wait<0>();
-        if (i0_prev + KT > len_prev) clean(v_prev, i0_prev, len_prev);
-        finish(v_prev);
     } else if (warp == 4) {
         // ------------------------------------------------- matrix products
         if (lane == 0) {
@@ -266,6 +257,7 @@ __global__ void __launch_bounds__(kThreads, 2)
             auto pv = [&](int n) {
                 mbar_wait(p_full, (uint32_t)(n & 1), P.err, kSiteAttend | kSiteAccum);
                 mbar_wait(&full[v_at], (uint32_t)(v_round & 1), P.err, kSiteAttend | kSiteFull);
+                fence_proxy_async_smem();
                 tc_fence_after();
                 const uint32_t v_addr = smem_u32(ring + v_at * Cfg::kTile);
 #pragma unroll
@@ -286,6 +278,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                 take(k_at, k_round);
                 mbar_wait(&full[k_at], (uint32_t)(k_round & 1), P.err, kSiteAttend | kSiteFull);
                 if (n > 0) mbar_wait(s_free, (uint32_t)((n - 1) & 1), P.err, kSiteAttend | kSiteAccum);
+                fence_proxy_async_smem();
                 tc_fence_after();
                 const uint32_t k_addr = smem_u32(ring + k_at * Cfg::kTile);
 #pragma unroll
@@ -322,13 +315,15 @@ __global__ void __launch_bounds__(kThreads, 2)
             const bool real = row < R;
             {
                 const uint16_t* src = static_cast<const uint16_t*>(P.q) + b * P.qb + t * P.qt + (long long)(h * G + g) * P.qh;
+                uint4 val[DP / 8];  // all loads ahead of the stores: they could not pass them
 #pragma unroll
                 for (int u = 0; u < DP / 8; ++u) {
-                    uint4 val = make_uint4(0, 0, 0, 0);
-                    if (real && u * 8 < D) val = *reinterpret_cast<const uint4*>(src + u * 8);
-                    *reinterpret_cast<uint4*>(q_s + (u >> 3) * (kWideRows * 128) + sw128(r, u & 7)) = val;
+                    val[u] = make_uint4(0, 0, 0, 0);
+                    if (real && u * 8 < D) val[u] = *reinterpret_cast<const uint4*>(src + u * 8);
                 }
-                fence_proxy_async_smem();
+#pragma unroll
+                for (int u = 0; u < DP / 8; ++u)
+                    *reinterpret_cast<uint4*>(q_s + (u >> 3) * (kWideRows * 128) + sw128(r, u & 7)) = val[u];
                 mbar_arrive(q_full);
             }
             const unsigned long long word = real && tot > 0 ? word_of(P.mask, T, b, t) : 0;
@@ -401,7 +396,6 @@ __global__ void __launch_bounds__(kThreads, 2)
                     }
                     *reinterpret_cast<uint4*>(p_s + sw128(r, u)) = make_uint4(w[0], w[1], w[2], w[3]);
                 }
-                fence_proxy_async_smem();
                 mbar_arrive(p_full);
                 advance();  // past the value tile
             }

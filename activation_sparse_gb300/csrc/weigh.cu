@@ -85,12 +85,13 @@ __global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) k_kv_accumulate(c
                              "l"(ap + (slot >= 0 ? slot : 0)), "r"(slot >= 0 ? 4 : 0)
                              : "memory");
             }
+            int slots[Cp::SWEEPS];
+            Cp::slots(slot, lane, slots);
 #pragma unroll
             for (int j = 0; j < Cp::SWEEPS; ++j) {
                 const int r = Cp::row(lane, j);
-                const int at_slot = __shfl_sync(0xFFFFFFFFu, slot, r);
-                const bool on = at_slot >= 0 && unit_on;
-                const long long from = on ? at_slot : 0;
+                const bool on = slots[j] >= 0 && unit_on;
+                const long long from = on ? slots[j] : 0;
                 cp16(dst + tile_at<DP>(warp * 16 + r, unit), on ? kp + from * k_step : kp - unit * 8, on);
             }
             ++px;

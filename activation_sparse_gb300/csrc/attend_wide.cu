@@ -12,7 +12,7 @@
 // list instead of once a tile.
 //
 // Warps: 0-3 softmax and output (TMEM lanes 32 w ..), 4 issues the matrix
-// instructions, 5 and 6 copy keys and values through the slot table (16-byte
+// instructions, 5-8 copy keys and values through the slot table (16-byte
 // asynchronous copies into the 128-byte swizzle the tensor cores read). Two
 // CTAs share an SM, so one's softmax runs under the other's products. Every
 // write to shared memory is an ordinary one; the issuing thread's proxy fence,
@@ -24,8 +24,8 @@ namespace si {
 
 namespace {
 
-constexpr int kThreads = 7 * 32;
-constexpr int kSoftmaxThreads = 128, kCopyThreads = 64;
+constexpr int kThreads = 9 * 32;
+constexpr int kSoftmaxThreads = 128, kCopyThreads = 128;
 constexpr int kMaxSlots = 4;       // ring slots: a key or a value tile each
 
 template <int DP>
@@ -100,7 +100,7 @@ template <int DP, bool FP16>
 __global__ void __launch_bounds__(kThreads, 2)
     k_tree_attention_wide(const __grid_constant__ AttendParams P, int row_blocks, int slots) {
     using Cfg = WideCfg<DP>;
-    using Cp = Copy<DP, 32>;
+    using Cp = Copy<DP>;
     extern __shared__ __align__(1024) uint8_t smem[];  // the swizzle needs tiles on 1024-byte boundaries
     uint8_t* const q_s = smem;
     uint8_t* const p_s = smem + Cfg::kOffP;
@@ -112,8 +112,8 @@ __global__ void __launch_bounds__(kThreads, 2)
     uint64_t* const s_free = q_full + 2;         // and has been read
     uint64_t* const p_full = q_full + 3;         // P of a tile is in shared memory
     uint64_t* const o_done = q_full + 4;         // O includes the tile
-    unsigned* const odd = reinterpret_cast<unsigned*>(full + 16);  // [slot][2]: keys of a value tile that are not finite
-    uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(odd + kMaxSlots * 2);
+    uint16_t* const odd = reinterpret_cast<uint16_t*>(full + 16);  // [slot][4]: keys of a value tile that are not finite
+    uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(odd + kMaxSlots * 4);
     Plan plan;
     plan.len = reinterpret_cast<int*>(tmem_slot + 4);
     plan.tot = plan.len + P.c.B;
@@ -159,7 +159,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         // more CTAs than tiles: nothing to do
     } else if (warp >= 5) {
         // ---------------------------------------------------------- copies
-        const int own0 = (warp - 5) * 32, unit = lane % Cp::UNITS;
+        const int own0 = (warp - 5) * 16, unit = lane % Cp::UNITS;
         const bool unit_on = unit * 8 < D;
         const int n_slots = (int)C.n_slots, k_step = (int)C.ks, v_step = (int)C.vs;
         const uint32_t col = (uint32_t)(unit >> 3) * (KT * 128);  // sub-tile of this lane's unit
@@ -177,7 +177,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                        __reduce_or_sync(0xFFFFFFFFu, (unsigned)mine);
                 seen_b = a.b;
             }
-            return slot_of(list, i0 + own0 + lane, len, plan.tot[a.b], seen);
+            return slot_of(list, i0 + own0 + (lane & 15), len, plan.tot[a.b], seen);
         };
         auto copy = [&](uint32_t dst, const uint16_t* base, int step_, const int (&slot)[Cp::SWEEPS]) {
 #pragma unroll
@@ -206,7 +206,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                     if (not_finite<FP16>(e[i])) e[i] = 0, bad |= 1u << r;
             }
             bad = __reduce_or_sync(0xFFFFFFFFu, bad);
-            if (lane == 0) odd[slot_at * 2 + (warp - 5)] = bad;
+            if (lane == 0) odd[slot_at * 4 + (warp - 5)] = (uint16_t)bad;
         };
         int next = fetch();
         int at = 0, fill = 0;               // ring slot of the next group and how often the ring has been round
@@ -335,31 +335,36 @@ __global__ void __launch_bounds__(kThreads, 2)
                 mbar_wait(s_full, (uint32_t)(n & 1), P.err, kSiteAttend | kSiteAccum);
                 __syncwarp();
                 tc_fence_after();
-                uint32_t s[KT];
-                tmem_ld32(t_s, s);
-                tmem_ld32(t_s + 32, s + 32);
-                tmem_ld_wait();
-                tc_fence_before();
-                mbar_arrive(s_free);
+                // which of the 64 keys this row sees
                 const int i0 = a.tile * KT;
+                unsigned long long vis = ~0ull;
                 if (i0 + KT > len) {  // the tile meets the new nodes or the list's end
-                    // which of the 64 keys this row sees
-                    const int cut = len - i0;  // keys before it are cached ones
-                    unsigned long long vis = 0;
-                    if (cut > 0) vis = (1ull << cut) - 1;  // cut < 64 here
+                    const int cut = len - i0;  // keys before it are cached ones; < 64
+                    vis = cut > 0 ? (1ull << cut) - 1 : 0;
                     const unsigned long long nodes = T >= 64 ? word : word & ((1ull << T) - 1);
                     if (cut >= 0) vis |= nodes << cut;
                     else if (cut > -64) vis |= nodes >> -cut;
-#pragma unroll
-                    for (int i = 0; i < KT; ++i)
-                        if (!(vis >> i & 1)) s[i] = 0xFF800000u;  // -inf
                     mbar_wait(&full[v_at], (uint32_t)(v_round & 1), P.err, kSiteAttend | kSiteFull);
-                    unsigned long long bad = *reinterpret_cast<const unsigned long long*>(odd + v_at * 2) & vis;
+                    const unsigned long long bad = *reinterpret_cast<const unsigned long long*>(odd + v_at * 4) & vis;
                     if (bad) odd_nodes |= cut >= 0 ? bad >> cut : bad << -cut;
+                    __syncwarp();
                 }
-                float top = __uint_as_float(s[0]);
+                // the scores are read twice, 32 at a time: registers for all 64 would cost the second CTA
+                uint32_t s[32];
+                float top = -INFINITY;
 #pragma unroll
-                for (int i = 1; i < KT; ++i) top = fmaxf(top, __uint_as_float(s[i]));
+                for (int half = 0; half < 2; ++half) {
+                    tmem_ld32(t_s + half * 32, s);
+                    tmem_ld_wait();
+                    const unsigned in = (unsigned)(vis >> (half * 32));
+                    if (__any_sync(0xFFFFFFFFu, in != 0xFFFFFFFFu)) {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            if (!(in >> i & 1)) s[i] = 0xFF800000u;  // -inf
+                    }
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) top = fmaxf(top, __uint_as_float(s[i]));
+                }
                 float keep = 1.0f;
                 if (ref == -INFINITY) {
                     ref = top;  // nothing seen so far, O's row is 0
@@ -385,16 +390,31 @@ __global__ void __launch_bounds__(kThreads, 2)
                 }
                 const float shift = ref == -INFINITY ? 0.0f : ref;
 #pragma unroll
-                for (int u = 0; u < KT / 8; ++u) {
-                    uint32_t w[4];
+                for (int half = 1; half >= 0; --half) {  // the second half is still in registers
+                    if (half == 0) {
+                        tmem_ld32(t_s, s);
+                        tmem_ld_wait();
+                        tc_fence_before();
+                        mbar_arrive(s_free);
+                        const unsigned in = (unsigned)vis;
+                        if (__any_sync(0xFFFFFFFFu, in != 0xFFFFFFFFu)) {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float p0 = ex2((__uint_as_float(s[u * 8 + 2 * i]) - shift) * c2);
-                        const float p1 = ex2((__uint_as_float(s[u * 8 + 2 * i + 1]) - shift) * c2);
-                        sum += p0 + p1;
-                        w[i] = pack<FP16>(p0, p1);  // rounded to the cache's type for the product with V
+                            for (int i = 0; i < 32; ++i)
+                                if (!(in >> i & 1)) s[i] = 0xFF800000u;
+                        }
                     }
-                    *reinterpret_cast<uint4*>(p_s + sw128(r, u)) = make_uint4(w[0], w[1], w[2], w[3]);
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) {
+                        uint32_t w[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const float p0 = ex2((__uint_as_float(s[u * 8 + 2 * i]) - shift) * c2);
+                            const float p1 = ex2((__uint_as_float(s[u * 8 + 2 * i + 1]) - shift) * c2);
+                            sum += p0 + p1;
+                            w[i] = pack<FP16>(p0, p1);  // rounded to the cache's type for the product with V
+                        }
+                        *reinterpret_cast<uint4*>(p_s + sw128(r, half * 4 + u)) = make_uint4(w[0], w[1], w[2], w[3]);
+                    }
                 }
                 mbar_arrive(p_full);
                 advance();  // past the value tile

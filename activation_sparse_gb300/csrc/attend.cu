@@ -73,7 +73,7 @@ __global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1)
     grid_launch_dependents();
     grid_dependency_wait();
     make_plan<kThreads>(C, T, groups, plan, P.err, blockIdx.x == 0);
-    const Deal deal(plan.first[C.B], gridDim.x);
+    const Deal deal(plan.first[C.B], gridDim.x, 1);
     const int x0 = deal.start(blockIdx.x), x1 = deal.start(blockIdx.x + 1);
     if (x0 >= x1) return;
 
@@ -431,7 +431,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
     grid_launch_dependents();
     grid_dependency_wait();
     make_plan<kJoinWarps * 32>(C, T, groups, plan, P.err, false);
-    const Deal deal(plan.first[C.B], parts);
+    const Deal deal(plan.first[C.B], parts, RB == kWideRows ? kWideLeast : 1);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int row_sets = (min(R, RB) + ROWS - 1) / ROWS;
     const int list_id = blockIdx.x / row_sets;

@@ -137,15 +137,19 @@ __device__ void make_plan(const KvView& C, int T, int groups, const Plan& p, uns
 }
 
 // The tiles are dealt out in parts of n / parts or one more; the first n %
-// parts CTAs have the longer ones. All in 32 bits: these run once per part of
-// every list when rows are joined.
+// parts CTAs have the longer ones. Few tiles go to fewer CTAs (at least
+// `least` each: a part costs its start and its join whatever it holds). All in
+// 32 bits: these run once per part of every list when rows are joined.
 struct Deal {
     unsigned base, rem;
-    __device__ __forceinline__ Deal(int total, int parts) {
-        base = (unsigned)total / (unsigned)parts;
-        rem = (unsigned)total - base * (unsigned)parts;
+    __device__ __forceinline__ Deal(int total, int ctas, int least) {
+        const unsigned parts = max(1u, min((unsigned)ctas, (unsigned)total / (unsigned)least));
+        base = (unsigned)total / parts;
+        rem = (unsigned)total - base * parts;
+        end = total;
     }
-    __device__ __forceinline__ int start(int part) const { return (int)(part * base + min((unsigned)part, rem)); }
+    int end;
+    __device__ __forceinline__ int start(int part) const { return min(end, (int)(part * base + min((unsigned)part, rem))); }
     // the part that has tile x
     __device__ __forceinline__ int owner(int x) const {
         const unsigned longer = rem * (base + 1);
@@ -208,6 +212,7 @@ __device__ __forceinline__ bool slot_ok(int slot, int n_slots, unsigned* err) {
 constexpr int part_floats(int rb, int dp) { return rb * (dp + 2); }
 
 constexpr int kWideRows = 128;     // query rows a block of the tensor-memory kernel has
+constexpr int kWideLeast = 4;      // and the tiles a part of its lists has at least
 
 // Who copies what: a warp copies KEYS keys of every tile, lane i < KEYS
 // holding the slot of its key i.

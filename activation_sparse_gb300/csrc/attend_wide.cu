@@ -152,7 +152,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     make_plan<kThreads>(C, T, groups, plan, P.err, blockIdx.x == 0);  // ends with a barrier
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    const Deal deal(plan.first[C.B], gridDim.x);
+    const Deal deal(plan.first[C.B], gridDim.x, kWideLeast);
     const int x0 = deal.start(blockIdx.x), x1 = deal.start(blockIdx.x + 1);
 
     if (x0 >= x1) {
@@ -314,16 +314,26 @@ __global__ void __launch_bounds__(kThreads, 2)
             const int t = row / G, g = row - t * G;
             const bool real = row < R;
             {
-                const uint16_t* src = static_cast<const uint16_t*>(P.q) + b * P.qb + t * P.qt + (long long)(h * G + g) * P.qh;
-                uint4 val[DP / 8];  // all loads ahead of the stores: they could not pass them
+                // Queries: this warp's 32 rows, whole rows at a time (a row a lane would touch 32 lines with every
+                // load); loads ahead of the stores, which they could not pass.
+                const long long off = real ? b * P.qb + t * P.qt + (long long)(h * G + g) * P.qh : -1;
+                constexpr int UNITS = DP / 8, AT_ONCE = 32 / UNITS, LOADS = 32 / AT_ONCE;
+                const int u = lane % UNITS;
 #pragma unroll
-                for (int u = 0; u < DP / 8; ++u) {
-                    val[u] = make_uint4(0, 0, 0, 0);
-                    if (real && u * 8 < D) val[u] = *reinterpret_cast<const uint4*>(src + u * 8);
+                for (int j0 = 0; j0 < LOADS; j0 += 8) {
+                    uint4 val[8];
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const long long from = __shfl_sync(0xFFFFFFFFu, off, (j0 + j) * AT_ONCE + lane / UNITS);
+                        val[j] = make_uint4(0, 0, 0, 0);
+                        if (from >= 0 && u * 8 < D)
+                            val[j] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(P.q) + from + u * 8);
+                    }
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        *reinterpret_cast<uint4*>(q_s + (u >> 3) * (kWideRows * 128) +
+                                                  sw128(warp * 32 + (j0 + j) * AT_ONCE + lane / UNITS, u & 7)) = val[j];
                 }
-#pragma unroll
-                for (int u = 0; u < DP / 8; ++u)
-                    *reinterpret_cast<uint4*>(q_s + (u >> 3) * (kWideRows * 128) + sw128(r, u & 7)) = val[u];
                 mbar_arrive(q_full);
             }
             const unsigned long long word = real && tot > 0 ? word_of(P.mask, T, b, t) : 0;
@@ -430,9 +440,9 @@ __global__ void __launch_bounds__(kThreads, 2)
             const bool empty_row = word == 0 || sum == 0.0f;
             const float inv = !whole ? 1.0f : empty_row ? 0.0f : 1.0f / sum;
             const long long at = ((long long)b * T + t) * P.Hq + h * G + g;
-            uint16_t* out = static_cast<uint16_t*>(P.out) + at * D;
             float* part = P.part + ((long long)blockIdx.x * 2 + (segment ? 1 : 0)) * part_floats(kWideRows, DP);
             const int32_t* list = C.table ? C.table + b * C.tb + h * C.th : nullptr;
+            uint8_t* const stage = p_s;  // P has been read; a warp's rows of it are its own 4 KB
 #pragma unroll 1
             for (int c = 0; c < DP; c += 32) {
                 uint32_t o[32];
@@ -447,7 +457,8 @@ __global__ void __launch_bounds__(kThreads, 2)
                         if (c + i < D && not_finite<FP16>(src[c + i]))
                             o[i] = __float_as_uint(__uint_as_float(o[i]) + widen<FP16>(src[c + i]));
                 }
-                if (!real) continue;
+                // 32 columns of the warp's 32 rows through shared memory, so that a store covers whole lines
+                __syncwarp();
                 if (whole) {
 #pragma unroll
                     for (int i = 0; i < 32; i += 8) {
@@ -457,14 +468,34 @@ __global__ void __launch_bounds__(kThreads, 2)
                             w[e] = empty_row ? 0u
                                              : pack<FP16>(__uint_as_float(o[i + 2 * e]) * inv,
                                                           __uint_as_float(o[i + 2 * e + 1]) * inv);
-                        if (c + i < D) *reinterpret_cast<uint4*>(out + c + i) = make_uint4(w[0], w[1], w[2], w[3]);
+                        *reinterpret_cast<uint4*>(stage + sw128(r, i / 8)) = make_uint4(w[0], w[1], w[2], w[3]);
+                    }
+                    __syncwarp();
+                    const int u = lane & 3;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const int rr = j * 8 + (lane >> 2);
+                        const long long to = __shfl_sync(0xFFFFFFFFu, real ? at : -1ll, rr);
+                        const uint4 v = *reinterpret_cast<const uint4*>(stage + sw128(warp * 32 + rr, u));
+                        if (to >= 0 && c + u * 8 < D)
+                            *reinterpret_cast<uint4*>(static_cast<uint16_t*>(P.out) + to * D + c + u * 8) = v;
                     }
                 } else {
 #pragma unroll
                     for (int i = 0; i < 32; i += 4)
-                        *reinterpret_cast<uint4*>(part + r * DP + c + i) = make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+                        *reinterpret_cast<uint4*>(stage + sw128(r, i / 4)) = make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+                    __syncwarp();
+                    const int u = lane & 7;
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const int rr = warp * 32 + j * 4 + (lane >> 3);
+                        if (rb * kWideRows + rr < R)
+                            *reinterpret_cast<uint4*>(part + rr * DP + c + u * 4) =
+                                *reinterpret_cast<const uint4*>(stage + sw128(rr, u));
+                    }
                 }
             }
+            __syncwarp();
             tc_fence_before();
             if (real) {
                 if (!whole) {

@@ -55,7 +55,7 @@ __global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) k_kv_accumulate(c
     grid_launch_dependents();
     grid_dependency_wait();
     make_plan<kThreads>(C, T, C.Hkv, plan, P.err, blockIdx.x == 0);
-    const Deal deal(plan.first[C.B], gridDim.x);
+    const Deal deal(plan.first[C.B], gridDim.x, 1);
     const int x0 = deal.start(blockIdx.x), x1 = deal.start(blockIdx.x + 1);
     if (x0 >= x1) return;
     const float c2 = P.scale * kLog2e;

@@ -12,12 +12,21 @@
 // list instead of once a tile.
 //
 // Warps: 0-3 softmax and output (TMEM lanes 32 w ..), 4 issues the matrix
-// instructions, 5-8 copy keys and values through the slot table (16-byte
-// asynchronous copies into the 128-byte swizzle the tensor cores read). Two
+// instructions, 5-8 copy keys and values through the slot table into the
+// 128-byte swizzle the tensor cores read: tiles of cached keys by the TMA's
+// four-row gather (a warp's instruction moves 4 KB), tiles that meet the new
+// nodes, and caches whose strides or D do not fit a tensor map, by 16-byte
+// asynchronous copies (512 bytes an instruction: they took half of the issue
+// slots, and a tile 1570 cycles of an SM). Two
 // CTAs share an SM, so one's softmax runs under the other's products. Every
 // write to shared memory is an ordinary one; the issuing thread's proxy fence,
 // after the barrier that announces it, lets the tensor cores see it.
 // All waits are bounded; TMEM is always released.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include <mutex>
+
 #include "attend.cuh"
 
 namespace si {
@@ -91,6 +100,51 @@ __device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t* r) {
         "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
         : "memory");
 }
+// Bounded wait that an earlier failure does not cut short.
+__device__ __forceinline__ void mbar_drain(uint64_t* bar, uint32_t parity) {
+    const long long t0 = cycles();
+    while (!mbar_try_wait(bar, parity)) {
+        if (cycles() - t0 > kDrainLimitCycles) return;
+    }
+}
+
+// Four rows of 64 elements (from element `col`) into 512 bytes of a swizzled tile.
+__device__ __forceinline__ void tma_gather4(uint32_t dst, const CUtensorMap* map, int col, const int (&row)[4],
+                                            uint64_t* bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cta.global.tile::gather4.mbarrier::complete_tx::bytes [%0], "
+        "[%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(col), "r"(row[0]), "r"(row[1]), "r"(row[2]), "r"(row[3]),
+        "r"(smem_u32(bar))
+        : "memory");
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
+// Two fp32 lanes at once.
+__device__ __forceinline__ uint64_t both(float a, float b) {
+    uint64_t d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(a), "f"(b));
+    return d;
+}
+__device__ __forceinline__ void split(uint64_t v, float& a, float& b) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
 __device__ __forceinline__ void tmem_ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
@@ -98,7 +152,8 @@ __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.
 
 template <int DP, bool FP16>
 __global__ void __launch_bounds__(kThreads, 2)
-    k_tree_attention_wide(const __grid_constant__ AttendParams P, int row_blocks, int slots) {
+    k_tree_attention_wide(const __grid_constant__ AttendParams P, const __grid_constant__ CUtensorMap map_k,
+                          const __grid_constant__ CUtensorMap map_v, int by_tma, int row_blocks, int slots) {
     using Cfg = WideCfg<DP>;
     using Cp = Copy<DP>;
     extern __shared__ __align__(1024) uint8_t smem[];  // the swizzle needs tiles on 1024-byte boundaries
@@ -208,6 +263,28 @@ __global__ void __launch_bounds__(kThreads, 2)
             bad = __reduce_or_sync(0xFFFFFFFFu, bad);
             if (lane == 0) odd[slot_at * 4 + (warp - 5)] = (uint16_t)bad;
         };
+        // Row and first element of a list's slot 0 in the maps' rows of a slot stride each.
+        int list_b = -1, list_h = -1, k_row = 0, k_col = 0, v_row = 0, v_col = 0;
+        auto find_list = [&](int b, int h) {
+            list_b = b, list_h = h;
+            const long long ko = b * C.kb + h * C.kh, vo = b * C.vb + h * C.vh;
+            k_row = (int)(ko / k_step), k_col = (int)(ko - (long long)k_row * k_step);
+            v_row = (int)(vo / v_step), v_col = (int)(vo - (long long)v_row * v_step);
+        };
+        // This warp's sixteen keys of a full tile: lane i issues group i / (DP / 64), half i % (DP / 64).
+        constexpr int HALVES = DP / 64;
+        auto gather = [&](int slot_at, const CUtensorMap* map, int row0, int col0, const int (&slot)[4]) {
+            uint64_t* bar = &full[slot_at];
+            if (lane == 0) mbar_arrive_expect_tx(bar, 16 * DP * 2);
+            else mbar_arrive(bar);
+            __syncwarp();
+            if (lane < 4 * HALVES) {
+                const int rows[4] = {row0 + slot[0], row0 + slot[1], row0 + slot[2], row0 + slot[3]};
+                const int half = lane % HALVES, r = own0 + lane / HALVES * 4;
+                tma_gather4(smem_u32(ring + slot_at * Cfg::kTile) + half * (KT * 128) + r * 128, map, col0 + half * 64,
+                            rows, bar);
+            }
+        };
         int next = fetch();
         int at = 0, fill = 0;               // ring slot of the next group and how often the ring has been round
         auto take = [&]() {
@@ -221,8 +298,21 @@ __global__ void __launch_bounds__(kThreads, 2)
             const int h = a.group / row_blocks, i0 = a.tile * KT, len = plan.len[a.b];
             const uint16_t* kp = static_cast<const uint16_t*>(C.k) + a.b * C.kb + h * C.kh + unit * 8;
             const uint16_t* vp = static_cast<const uint16_t*>(C.v) + a.b * C.vb + h * C.vh + unit * 8;
+            const bool ok = slot_ok(next, n_slots, P.err);
+            if (by_tma && i0 + KT <= len) {
+                if (a.b != list_b || h != list_h) find_list(a.b, h);
+                int four[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    four[e] = __shfl_sync(0xFFFFFFFFu, ok ? next : 0, (lane / HALVES * 4 + e) & 15);
+                gather(take(), &map_k, k_row, k_col, four);
+                step(plan, C.B, groups, a);
+                if (x + 1 < x1) next = fetch();
+                gather(take(), &map_v, v_row, v_col, four);
+                continue;
+            }
             int slot[Cp::SWEEPS];
-            Cp::slots(slot_ok(next, n_slots, P.err) ? next : -1, lane, slot);
+            Cp::slots(ok ? next : -1, lane, slot);
             const int k_at = take();
             copy(smem_u32(ring + k_at * Cfg::kTile), kp, k_step, slot);
             arrive_landed(k_at);
@@ -238,6 +328,11 @@ __global__ void __launch_bounds__(kThreads, 2)
                 arrive_landed(v_at);
             }
         }
+        // No copy is in flight when the CTA ends, even after a wait that ran out.
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        const int groups_in = 2 * (x1 - x0);
+        for (int s = 0; s < slots && s < groups_in; ++s)
+            mbar_drain(&full[s], (uint32_t)((groups_in - s + slots - 1) / slots - 1) & 1u);
     } else if (warp == 4) {
         // ------------------------------------------------- matrix products
         if (lane == 0) {
@@ -373,7 +468,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                             if (!(in >> i & 1)) s[i] = 0xFF800000u;  // -inf
                     }
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) top = fmaxf(top, __uint_as_float(s[i]));
+                    for (int i = 0; i < 32; i += 2) top = max3(top, __uint_as_float(s[i]), __uint_as_float(s[i + 1]));
                 }
                 float keep = 1.0f;
                 if (ref == -INFINITY) {
@@ -399,6 +494,8 @@ __global__ void __launch_bounds__(kThreads, 2)
                     tc_fence_before();
                 }
                 const float shift = ref == -INFINITY ? 0.0f : ref;
+                const uint64_t shift2 = both(-shift, -shift), scale2 = both(c2, c2);
+                uint64_t sum2 = 0;
 #pragma unroll
                 for (int half = 1; half >= 0; --half) {  // the second half is still in registers
                     if (half == 0) {
@@ -418,13 +515,20 @@ __global__ void __launch_bounds__(kThreads, 2)
                         uint32_t w[4];
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
-                            const float p0 = ex2((__uint_as_float(s[u * 8 + 2 * i]) - shift) * c2);
-                            const float p1 = ex2((__uint_as_float(s[u * 8 + 2 * i + 1]) - shift) * c2);
-                            sum += p0 + p1;
+                            float p0, p1;
+                            split(mul2(add2(both(__uint_as_float(s[u * 8 + 2 * i]), __uint_as_float(s[u * 8 + 2 * i + 1])),
+                                            shift2), scale2), p0, p1);
+                            p0 = ex2(p0), p1 = ex2(p1);
+                            sum2 = add2(sum2, both(p0, p1));
                             w[i] = pack<FP16>(p0, p1);  // rounded to the cache's type for the product with V
                         }
                         *reinterpret_cast<uint4*>(p_s + sw128(r, half * 4 + u)) = make_uint4(w[0], w[1], w[2], w[3]);
                     }
+                }
+                {
+                    float s0, s1;
+                    split(sum2, s0, s1);
+                    sum += s0 + s1;
                 }
                 mbar_arrive(p_full);
                 advance();  // past the value tile
@@ -518,6 +622,37 @@ __global__ void __launch_bounds__(kThreads, 2)
 
 namespace {
 
+PFN_cuTensorMapEncodeTiled_v12000 encoder() {
+    static std::mutex mu;
+    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+    std::lock_guard<std::mutex> lk(mu);
+    if (!fn) {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+    }
+    return fn;
+}
+
+// The cache's slots as rows of one slot stride each, 64 elements of a row a
+// box. False where that does not describe it: D not whole boxes (elements of
+// the next slot or head would come along), slots that overlap, row numbers
+// past int32, a head that crosses from one row into the next.
+bool slot_map(CUtensorMap* map, const KvView& C, const void* base, long long sb, long long sh, long long ss) {
+    if (C.D % 64 || ss < C.D || sb % ss || (C.Hkv - 1) * (sh % ss) + C.D > ss) return false;
+    const long long rows = ((C.B - 1) * sb + (C.Hkv - 1) * sh) / ss + C.n_slots + 1;
+    const auto encode = encoder();
+    if (rows > 0x7FFFFFFFLL || !encode) return false;
+    const cuuint64_t dims[2] = {(cuuint64_t)ss, (cuuint64_t)rows};
+    const cuuint64_t strides[1] = {(cuuint64_t)ss * 2};
+    const cuuint32_t box[2] = {64, 1}, each[2] = {1, 1};
+    return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, const_cast<void*>(base), dims, strides, box, each,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <int DP, bool FP16>
 cudaError_t launch_dp(const AttendParams& P, int row_blocks, int parts, cudaStream_t st) {
     const auto kern = k_tree_attention_wide<DP, FP16>;
@@ -526,7 +661,10 @@ cudaError_t launch_dp(const AttendParams& P, int row_blocks, int parts, cudaStre
     // as many ring slots as leave room for two CTAs an SM (228 KB, 1 KB of each CTA's is the system's)
     int slots = kMaxSlots;
     while (slots > 3 && WideCfg<DP>::smem(P.c.B, slots) > 113 * 1024) --slots;
-    void* args[3] = {const_cast<AttendParams*>(&P), &row_blocks, &slots};
+    CUtensorMap map_k = {}, map_v = {};
+    const KvView& C = P.c;
+    int by_tma = slot_map(&map_k, C, C.k, C.kb, C.kh, C.ks) && slot_map(&map_v, C, C.v, C.vb, C.vh, C.vs);
+    void* args[6] = {const_cast<AttendParams*>(&P), &map_k, &map_v, &by_tma, &row_blocks, &slots};
     return launch(reinterpret_cast<const void*>(kern), dim3(parts, 1, 1), kThreads, WideCfg<DP>::smem(P.c.B, slots), args,
                   st);
 }

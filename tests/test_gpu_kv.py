@@ -209,6 +209,9 @@ CASES = [
     ([40], 2, 2, 1, 8, "bf16", True, "tree"),
     ([17] * 30, 2, 4, 2, 64, "fp16", True, "tree"),
     ([3000, 1], 64, 16, 2, 128, "bf16", True, "pad"),
+    ([0, 63, 64, 128], 9, 8, 2, 128, "bf16", True, "tree"),
+    ([4000], 40, 5, 1, 64, "fp16", True, "pad"),
+    ([1500], 17, 3, 3, 128, "fp16", False, "tree"),
 ]
 
 
@@ -322,6 +325,26 @@ def test_attention_strides(si):
     want = t.empty_like(out)
     si.si_tree_attention(plain, q.contiguous(), want)
     assert t.equal(out, want)
+
+
+@pytest.mark.parametrize("D,pad", [(64, 0), (64, 8), (128, 0), (128, 64), (96, 0)])
+def test_attention_strides_many_rows(si, D, pad):
+    """The same with trees of many rows: heads side by side in a slot, with and without room between them."""
+    t = torch()
+    rng = np.random.default_rng(28)
+    B, Hkv, n, T, Hq = 2, 3, 200, 12, 12
+    pool = gpu(rng.standard_normal((B, n + T, 2, Hkv, D + pad)), t.bfloat16)
+    K, V = (pool[:, :, i, :, :D].permute(0, 2, 1, 3)[None] for i in (0, 1))
+    q = gpu(rng.standard_normal((B, T, Hq + 5, D)), t.bfloat16)[:, :, 2:2 + Hq]
+    lens = [n, n - 77]
+    table = ref.tables(rng, (1, B, Hkv), n + T, n + T)
+    kv = si.si_kv_create(K, V, gpu(table), gpu(np.array([lens], np.int32)))
+    out, lse = t.empty(B, T, Hq, D, dtype=t.bfloat16, device="cuda"), t.empty(B, T, Hq, device="cuda")
+    words = ref.trees(rng, B, T)
+    si.si_tree_attention(kv, q, out, mask=gpu(words.view(np.int64)), lse=lse)
+    want, lse_w, mag = ref.attend(host(q), host(K[0]), host(V[0]), table[0], lens, words, D ** -0.5)
+    assert (np.abs(host(out) - want) <= 2.0 ** -8 * (mag + np.abs(want)) * 1.01 + 1e-5).all()
+    assert np.abs(host(lse) - lse_w).max() < 1e-5
 
 
 def test_attention_shared_pool(si):

@@ -2,10 +2,12 @@
 // heads) on the 5th-generation tensor cores.
 //
 // A block of 128 query rows of one list meets tiles of 64 keys:
-//   S = Q K^T   tcgen05.mma M = 128, N = 64, K = D    (accumulator in TMEM)
+//   S = Q K^T   tcgen05.mma M = 128, N = 64, K = D    (accumulator and Q in TMEM)
 //   P = exp(scale (S - m))                            (one thread a row)
 //   O += P V    tcgen05.mma M = 128, N = D, K = 64    (accumulator in TMEM)
-// The value tile serves as it lies, [key][d], as an operand with d contiguous.
+// Q lies in TMEM because the products of a tile would read it again from
+// shared memory, 32 KB beside the key tile's 16: 635 cycles a tile for what
+// takes 256 of arithmetic. The value tile serves as it lies, [key][d], as an operand with d contiguous.
 // The reference m of a row moves only when the maximum outgrows it by a
 // factor of 2^8: weights up to 256 are as exact in 16 bits as weights up to
 // 1, and the sums are in 32 bits, so the output is rescaled a few times a
@@ -35,16 +37,16 @@ namespace {
 
 constexpr int kThreads = 9 * 32;
 constexpr int kSoftmaxThreads = 128, kCopyThreads = 128;
-constexpr int kMaxSlots = 4;       // ring slots: a key or a value tile each
+constexpr int kMaxSlots = 6;       // ring slots: a key or a value tile each
 
 template <int DP>
 struct WideCfg {
     static constexpr int kTile = KT * DP * 2;
-    static constexpr int kQ = kWideRows * DP * 2;
-    static constexpr int kP = kWideRows * KT * 2;
-    static constexpr int kOffP = kQ, kOffRing = kQ + kP;
-    static constexpr int kTmemCols = DP == 128 ? 256 : 128;    // S at 0, O at 64
-    static constexpr int fixed(int B) { return 16 * 8 + kMaxSlots * 8 + 16 + (3 * B + 1) * 4; }
+    static constexpr int kOffRing = kWideRows * KT * 2;        // after P
+    static constexpr int kColO = 64, kColQ = 64 + DP;          // TMEM columns: S, O, Q (two elements a column)
+    static constexpr int kTmemCols = 256;
+    static constexpr int kBars = 2 * kMaxSlots + 5;
+    static constexpr int fixed(int B) { return (kBars + 1) * 8 + kMaxSlots * 8 + 16 + (3 * B + 1) * 4; }
     static constexpr int smem(int B, int slots) { return kOffRing + slots * kTile + fixed(B); }
 };
 
@@ -71,6 +73,16 @@ __device__ __forceinline__ void tc_mma(uint32_t d, uint64_t a, uint64_t b, uint3
         "setp.ne.b32 p, %4, 0;\n\t"
         "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
         "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate)
+        : "memory");
+}
+
+// The same with A in TMEM: a row a lane, two elements a column.
+__device__ __forceinline__ void tc_mma_ta(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate)
         : "memory");
 }
 
@@ -157,17 +169,16 @@ __global__ void __launch_bounds__(kThreads, 2)
     using Cfg = WideCfg<DP>;
     using Cp = Copy<DP>;
     extern __shared__ __align__(1024) uint8_t smem[];  // the swizzle needs tiles on 1024-byte boundaries
-    uint8_t* const q_s = smem;
-    uint8_t* const p_s = smem + Cfg::kOffP;
+    uint8_t* const p_s = smem;
     uint8_t* const ring = smem + Cfg::kOffRing;
     uint64_t* const full = reinterpret_cast<uint64_t*>(ring + slots * Cfg::kTile);
     uint64_t* const empty = full + kMaxSlots;
-    uint64_t* const q_full = empty + kMaxSlots;  // this list's queries are in shared memory
+    uint64_t* const q_full = empty + kMaxSlots;  // this list's queries are in TMEM
     uint64_t* const s_full = q_full + 1;         // S of a tile is in TMEM
     uint64_t* const s_free = q_full + 2;         // and has been read
     uint64_t* const p_full = q_full + 3;         // P of a tile is in shared memory
     uint64_t* const o_done = q_full + 4;         // O includes the tile
-    uint16_t* const odd = reinterpret_cast<uint16_t*>(full + 16);  // [slot][4]: keys of a value tile that are not finite
+    uint16_t* const odd = reinterpret_cast<uint16_t*>(full + Cfg::kBars + 1);  // [slot][4]: keys of a value tile that are not finite
     uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(odd + kMaxSlots * 4);
     Plan plan;
     plan.len = reinterpret_cast<int*>(tmem_slot + 4);
@@ -340,7 +351,7 @@ __global__ void __launch_bounds__(kThreads, 2)
             constexpr uint32_t kCommon = (1u << 4) | kType | ((uint32_t)(kWideRows >> 4) << 24);
             constexpr uint32_t kDescS = kCommon | ((uint32_t)(KT >> 3) << 17);
             constexpr uint32_t kDescO = kCommon | (1u << 16) | ((uint32_t)(DP >> 3) << 17);  // V: d contiguous
-            const uint32_t q_addr = smem_u32(q_s), p_addr = smem_u32(p_s);
+            const uint32_t p_addr = smem_u32(p_s);
             At a = locate(plan, C.B, x0);
             int at = 0, round = 0, lists = 0;
             bool fresh = false;              // the tile whose product with V is pending starts its list's O
@@ -357,7 +368,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                 const uint32_t v_addr = smem_u32(ring + v_at * Cfg::kTile);
 #pragma unroll
                 for (int k = 0; k < KT / 16; ++k)
-                    tc_mma(tmem + 64, desc128(p_addr + k * 32, 16), desc128(v_addr + k * 16 * 128, KT * 128), kDescO,
+                    tc_mma(tmem + Cfg::kColO, desc128(p_addr + k * 32, 16), desc128(v_addr + k * 16 * 128, KT * 128), kDescO,
                            !fresh || k > 0);
                 tc_commit(&empty[v_at]);
                 tc_commit(o_done);
@@ -378,8 +389,8 @@ __global__ void __launch_bounds__(kThreads, 2)
                 const uint32_t k_addr = smem_u32(ring + k_at * Cfg::kTile);
 #pragma unroll
                 for (int k = 0; k < DP / 16; ++k)
-                    tc_mma(tmem, desc128(q_addr + (k >> 2) * (kWideRows * 128) + (k & 3) * 32, 16),
-                           desc128(k_addr + (k >> 2) * (KT * 128) + (k & 3) * 32, 16), kDescS, k > 0);
+                    tc_mma_ta(tmem, tmem + Cfg::kColQ + k * 8, desc128(k_addr + (k >> 2) * (KT * 128) + (k & 3) * 32, 16),
+                              kDescS, k > 0);
                 tc_commit(&empty[k_at]);
                 tc_commit(s_full);
                 if (n > 0 && !first) pv(n - 1);
@@ -393,7 +404,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     } else {
         // --------------------------------------------- softmax and output
         const float c2 = P.scale * kLog2e;
-        const uint32_t t_s = tmem + ((uint32_t)(warp * 32) << 16), t_o = t_s + 64;
+        const uint32_t t_s = tmem + ((uint32_t)(warp * 32) << 16), t_o = t_s + Cfg::kColO;
         const int r = warp * 32 + lane;  // this thread's row of the block
         At a = locate(plan, C.B, x0);
         int n = 0, segment = 0, v_at = 0, v_round = 0;  // ring position of the value tile of tile n
@@ -409,26 +420,39 @@ __global__ void __launch_bounds__(kThreads, 2)
             const int t = row / G, g = row - t * G;
             const bool real = row < R;
             {
-                // Queries: this warp's 32 rows, whole rows at a time (a row a lane would touch 32 lines with every
-                // load); loads ahead of the stores, which they could not pass.
+                // Queries: whole lines at a time (a row a lane would touch 32 lines with every load); all loads ahead
+                // of the stores, which they could not pass.
                 const long long off = real ? b * P.qb + t * P.qt + (long long)(h * G + g) * P.qh : -1;
-                constexpr int UNITS = DP / 8, AT_ONCE = 32 / UNITS, LOADS = 32 / AT_ONCE;
-                const int u = lane % UNITS;
+                // They go through the warp's 4 KB of P's place, 64 elements of a row at a time, to the lanes that
+                // own the rows, and from there to TMEM.
+                const int u = lane & 7;
+                uint4 val[DP / 64][8];
 #pragma unroll
-                for (int j0 = 0; j0 < LOADS; j0 += 8) {
-                    uint4 val[8];
+                for (int half = 0; half < DP / 64; ++half)
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
-                        const long long from = __shfl_sync(0xFFFFFFFFu, off, (j0 + j) * AT_ONCE + lane / UNITS);
-                        val[j] = make_uint4(0, 0, 0, 0);
-                        if (from >= 0 && u * 8 < D)
-                            val[j] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(P.q) + from + u * 8);
+                        const long long from = __shfl_sync(0xFFFFFFFFu, off, j * 4 + (lane >> 3));
+                        const int d = half * 64 + u * 8;
+                        val[half][j] = make_uint4(0, 0, 0, 0);
+                        if (from >= 0 && d < D)
+                            val[half][j] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(P.q) + from + d);
                     }
 #pragma unroll
+                for (int half = 0; half < DP / 64; ++half) {
+                    __syncwarp();
+#pragma unroll
                     for (int j = 0; j < 8; ++j)
-                        *reinterpret_cast<uint4*>(q_s + (u >> 3) * (kWideRows * 128) +
-                                                  sw128(warp * 32 + (j0 + j) * AT_ONCE + lane / UNITS, u & 7)) = val[j];
+                        *reinterpret_cast<uint4*>(p_s + sw128(warp * 32 + j * 4 + (lane >> 3), u)) = val[half][j];
+                    __syncwarp();
+                    uint32_t mine[32];
+#pragma unroll
+                    for (int c = 0; c < 8; ++c)
+                        *reinterpret_cast<uint4*>(mine + c * 4) = *reinterpret_cast<const uint4*>(p_s + sw128(r, c));
+                    tmem_st32(t_s + Cfg::kColQ + half * 32, mine);
                 }
+                tmem_st_wait();
+                __syncwarp();
+                tc_fence_before();
                 mbar_arrive(q_full);
             }
             const unsigned long long word = real && tot > 0 ? word_of(P.mask, T, b, t) : 0;

@@ -83,26 +83,25 @@ __global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1)
     const int own0 = kw * WK + mw * 16;  // this warp copies keys own0 .. own0 + 15 of a tile
     const int n_slots = (int)C.n_slots, k_step = (int)C.ks, v_step = (int)C.vs;
 
-    // producer state: lane i < 16 holds the slot of key own0 + i of the tile to be issued next
-    At pa = locate(plan, C.B, x0);
-    int px = x0, stage_in = 0;
-    int next_slot = kNoSlot;
+    // producer state: lane i < 16 holds the slots of key own0 + i of the next tiles (a load one tile ahead
+    // would be waited for every tile)
+    At pa = locate(plan, C.B, x0), ahead = pa;
+    int px = x0, fetched = x0, stage_in = 0;
+    int queue[kAhead];
     unsigned long long p_seen = 0;
     int p_seen_b = -1;
-    auto fetch_slots = [&]() {
-        if (px >= x1) return;
-        const int h = pa.group / row_blocks;
-        const int32_t* list = C.table ? C.table + pa.b * C.tb + h * C.th : nullptr;
-        const int len = plan.len[pa.b], tot = plan.tot[pa.b];
-        const int i0 = pa.tile * KT;
-        if (i0 + KT > len && p_seen_b != pa.b) {  // the tile meets the new nodes: which of them does any row see
-            unsigned long long mine = lane < T ? word_of(P.mask, T, pa.b, lane) : 0;
-            if (lane + 32 < T) mine |= word_of(P.mask, T, pa.b, lane + 32);
-            p_seen = (unsigned long long)__reduce_or_sync(0xFFFFFFFFu, (unsigned)(mine >> 32)) << 32 |
-                     __reduce_or_sync(0xFFFFFFFFu, (unsigned)mine);
-            p_seen_b = pa.b;
+    auto fetch = [&]() {
+        if (fetched >= x1) return kNoSlot;
+        const int b = ahead.b, h = ahead.group / row_blocks;
+        const int32_t* list = C.table ? C.table + b * C.tb + h * C.th : nullptr;
+        const int len = plan.len[b], i0 = ahead.tile * KT;
+        if (i0 + KT > len && p_seen_b != b) {  // the tile meets the new nodes: which of them does any row see
+            p_seen = seen_nodes(P.mask, T, b, lane);
+            p_seen_b = b;
         }
-        next_slot = slot_of(list, i0 + own0 + (lane & 15), len, tot, p_seen);
+        ++fetched;
+        step(plan, C.B, groups, ahead);
+        return slot_of(list, i0 + own0 + (lane & 15), len, plan.tot[b], p_seen);
     };
     auto issue = [&]() {
         if (px < x1) {
@@ -111,7 +110,10 @@ __global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1)
             const uint16_t* vp = static_cast<const uint16_t*>(C.v) + pa.b * C.vb + h * C.vh + unit * 8;
             const uint32_t dst = smem_u32(tiles + stage_in * 2 * Cfg::kTile);
             int slot[Cp::SWEEPS];
-            Cp::slots(slot_ok(next_slot, n_slots, P.err) ? next_slot : -1, lane, slot);
+            Cp::slots(slot_ok(queue[0], n_slots, P.err) ? queue[0] : -1, lane, slot);
+#pragma unroll
+            for (int i = 0; i + 1 < kAhead; ++i) queue[i] = queue[i + 1];
+            queue[kAhead - 1] = fetch();
 #pragma unroll
             for (int j = 0; j < Cp::SWEEPS; ++j) {
                 const int r = Cp::row(lane, j);
@@ -126,9 +128,9 @@ __global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1)
             step(plan, C.B, groups, pa);
         }
         cp_commit();
-        fetch_slots();
     };
-    fetch_slots();
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) queue[i] = fetch();
     for (int s = 0; s < S - 1; ++s) issue();
 
     At a = locate(plan, C.B, x0);

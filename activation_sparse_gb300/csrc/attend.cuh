@@ -192,6 +192,15 @@ __device__ __forceinline__ unsigned long long word_of(const unsigned long long* 
 }
 
 constexpr int kNoSlot = INT_MIN;
+constexpr int kAhead = 4;          // tiles whose slots are on their way while one is copied
+
+// Nodes of sequence b that any of its nodes sees (all lanes of a warp).
+__device__ __forceinline__ unsigned long long seen_nodes(const unsigned long long* mask, int T, int b, int lane) {
+    unsigned long long mine = lane < T ? word_of(mask, T, b, lane) : 0;
+    if (lane + 32 < T) mine |= word_of(mask, T, b, lane + 32);
+    return (unsigned long long)__reduce_or_sync(0xFFFFFFFFu, (unsigned)(mine >> 32)) << 32 |
+           __reduce_or_sync(0xFFFFFFFFu, (unsigned)mine);
+}
 
 // Slot of list entry i, or kNoSlot where nothing is to be read. The value is not
 // looked at here: it is used a tile later, so the load's latency is hidden.

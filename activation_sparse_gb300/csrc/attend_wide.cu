@@ -229,21 +229,21 @@ __global__ void __launch_bounds__(kThreads, 2)
         const bool unit_on = unit * 8 < D;
         const int n_slots = (int)C.n_slots, k_step = (int)C.ks, v_step = (int)C.vs;
         const uint32_t col = (uint32_t)(unit >> 3) * (KT * 128);  // sub-tile of this lane's unit
-        At a = locate(plan, C.B, x0);
+        At a = locate(plan, C.B, x0), ahead = a;
         unsigned long long seen = 0;
-        int seen_b = -1;
+        int seen_b = -1, fetched = x0;
         auto fetch = [&]() {
-            const int h = a.group / row_blocks;
-            const int32_t* list = C.table ? C.table + a.b * C.tb + h * C.th : nullptr;
-            const int len = plan.len[a.b], i0 = a.tile * KT;
-            if (i0 + KT > len && seen_b != a.b) {
-                unsigned long long mine = lane < T ? word_of(P.mask, T, a.b, lane) : 0;
-                if (lane + 32 < T) mine |= word_of(P.mask, T, a.b, lane + 32);
-                seen = (unsigned long long)__reduce_or_sync(0xFFFFFFFFu, (unsigned)(mine >> 32)) << 32 |
-                       __reduce_or_sync(0xFFFFFFFFu, (unsigned)mine);
-                seen_b = a.b;
+            if (fetched >= x1) return kNoSlot;
+            const int b = ahead.b, h = ahead.group / row_blocks;
+            const int32_t* list = C.table ? C.table + b * C.tb + h * C.th : nullptr;
+            const int len = plan.len[b], i0 = ahead.tile * KT;
+            if (i0 + KT > len && seen_b != b) {
+                seen = seen_nodes(P.mask, T, b, lane);
+                seen_b = b;
             }
-            return slot_of(list, i0 + own0 + (lane & 15), len, plan.tot[a.b], seen);
+            ++fetched;
+            step(plan, C.B, groups, ahead);
+            return slot_of(list, i0 + own0 + (lane & 15), len, plan.tot[b], seen);
         };
         auto copy = [&](uint32_t dst, const uint16_t* base, int step_, const int (&slot)[Cp::SWEEPS]) {
 #pragma unroll
@@ -296,7 +296,10 @@ __global__ void __launch_bounds__(kThreads, 2)
                             rows, bar);
             }
         };
-        int next = fetch();
+        // slots of the next tiles: a load a tile ahead would be waited for every tile
+        int queue[kAhead];
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) queue[i] = fetch();
         int at = 0, fill = 0;               // ring slot of the next group and how often the ring has been round
         auto take = [&]() {
             if (fill > 0) mbar_wait(&empty[at], (uint32_t)((fill - 1) & 1), P.err, kSiteAttend | kSiteEmpty);
@@ -309,6 +312,10 @@ __global__ void __launch_bounds__(kThreads, 2)
             const int h = a.group / row_blocks, i0 = a.tile * KT, len = plan.len[a.b];
             const uint16_t* kp = static_cast<const uint16_t*>(C.k) + a.b * C.kb + h * C.kh + unit * 8;
             const uint16_t* vp = static_cast<const uint16_t*>(C.v) + a.b * C.vb + h * C.vh + unit * 8;
+            const int next = queue[0];
+#pragma unroll
+            for (int i = 0; i + 1 < kAhead; ++i) queue[i] = queue[i + 1];
+            queue[kAhead - 1] = fetch();
             const bool ok = slot_ok(next, n_slots, P.err);
             if (by_tma && i0 + KT <= len) {
                 if (a.b != list_b || h != list_h) find_list(a.b, h);
@@ -318,7 +325,6 @@ __global__ void __launch_bounds__(kThreads, 2)
                     four[e] = __shfl_sync(0xFFFFFFFFu, ok ? next : 0, (lane / HALVES * 4 + e) & 15);
                 gather(take(), &map_k, k_row, k_col, four);
                 step(plan, C.B, groups, a);
-                if (x + 1 < x1) next = fetch();
                 gather(take(), &map_v, v_row, v_col, four);
                 continue;
             }
@@ -328,7 +334,6 @@ __global__ void __launch_bounds__(kThreads, 2)
             copy(smem_u32(ring + k_at * Cfg::kTile), kp, k_step, slot);
             arrive_landed(k_at);
             step(plan, C.B, groups, a);
-            if (x + 1 < x1) next = fetch();
             const int v_at = take();
             copy(smem_u32(ring + v_at * Cfg::kTile), vp, v_step, slot);
             if (i0 + KT > len) {

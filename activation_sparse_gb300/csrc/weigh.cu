@@ -63,21 +63,26 @@ __global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) k_kv_accumulate(c
     const bool unit_on = unit * 8 < D;
     const int n_slots = (int)C.n_slots, k_step = (int)C.ks;
 
-    At pa = locate(plan, C.B, x0);
-    int px = x0, stage_in = 0;
-    int next_slot = kNoSlot;
-    auto fetch_slots = [&]() {
-        if (px >= x1) return;
-        const int32_t* list = C.table ? C.table + pa.b * C.tb + pa.group * C.th : nullptr;
-        const int tot = plan.tot[pa.b];
-        next_slot = slot_of(list, pa.tile * KT + warp * 16 + (lane & 15), tot, tot, 0);
+    At pa = locate(plan, C.B, x0), ahead = pa;
+    int px = x0, fetched = x0, stage_in = 0;
+    int queue[kAhead];  // lane i < 16: the slots of the warp's key i of the next tiles
+    auto fetch = [&]() {
+        if (fetched >= x1) return kNoSlot;
+        const int32_t* list = C.table ? C.table + ahead.b * C.tb + ahead.group * C.th : nullptr;
+        const int tot = plan.tot[ahead.b], i = ahead.tile * KT + warp * 16 + (lane & 15);
+        ++fetched;
+        step(plan, C.B, C.Hkv, ahead);
+        return slot_of(list, i, tot, tot, 0);
     };
     auto issue = [&]() {
         if (px < x1) {
             const uint16_t* kp = static_cast<const uint16_t*>(C.k) + pa.b * C.kb + pa.group * C.kh + unit * 8;
             const float* ap = C.acc + pa.b * C.ab + pa.group * C.ah;
             const uint32_t dst = smem_u32(smem + stage_in * Cfg::kTile);
-            const int slot = slot_ok(next_slot, n_slots, P.err) ? next_slot : -1;
+            const int slot = slot_ok(queue[0], n_slots, P.err) ? queue[0] : -1;
+#pragma unroll
+            for (int i = 0; i + 1 < kAhead; ++i) queue[i] = queue[i + 1];
+            queue[kAhead - 1] = fetch();
             if (lane < 16) {
                 const int at = stage_in * KT + warp * 16 + lane;
                 slot_s[at] = slot;
@@ -99,9 +104,9 @@ __global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) k_kv_accumulate(c
             step(plan, C.B, C.Hkv, pa);
         }
         cp_commit();
-        fetch_slots();
     };
-    fetch_slots();
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) queue[i] = fetch();
     for (int s = 0; s < S - 1; ++s) issue();
 
     At a = locate(plan, C.B, x0);

@@ -83,54 +83,54 @@ __global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1)
     const int own0 = kw * WK + mw * 16;  // this warp copies keys own0 .. own0 + 15 of a tile
     const int n_slots = (int)C.n_slots, k_step = (int)C.ks, v_step = (int)C.vs;
 
-    // producer state: lane i < 16 holds the slots of key own0 + i of the next tiles (a load one tile ahead
-    // would be waited for every tile)
-    At pa = locate(plan, C.B, x0), ahead = pa;
-    int px = x0, fetched = x0, stage_in = 0;
-    int queue[kAhead];
-    unsigned long long p_seen = 0;
-    int p_seen_b = -1;
+    // producer state: lane i < 16 holds the slot of key own0 + i of the tile to be issued next
+    Source src;
+    src.start(plan, C.B, x0, x1);
+    const bool whole_rows = D == DP;
+    const uint32_t ring = smem_u32(tiles);
+    uint32_t stage_in = ring;
+    int held = kNoSlot, seen_b = -1;
     auto fetch = [&]() {
-        if (fetched >= x1) return kNoSlot;
-        const int b = ahead.b, h = ahead.group / row_blocks;
-        const int32_t* list = C.table ? C.table + b * C.tb + h * C.th : nullptr;
-        const int len = plan.len[b], i0 = ahead.tile * KT;
-        if (i0 + KT > len && p_seen_b != b) {  // the tile meets the new nodes: which of them does any row see
-            p_seen = seen_nodes(P.mask, T, b, lane);
-            p_seen_b = b;
+        const int i0 = src.at.tile * KT;
+        if (i0 + KT > src.len && seen_b != src.at.b) {  // the tile meets the new nodes
+            src.seen = seen_nodes(P.mask, T, src.at.b, lane);
+            seen_b = src.at.b;
         }
-        ++fetched;
-        step(plan, C.B, groups, ahead);
-        return slot_of(list, i0 + own0 + (lane & 15), len, plan.tot[b], p_seen);
+        held = slot_of(src.list, i0 + own0 + (lane & 15), src.len, src.tot, src.seen);
     };
     auto issue = [&]() {
-        if (px < x1) {
-            const int h = pa.group / row_blocks;
-            const uint16_t* kp = static_cast<const uint16_t*>(C.k) + pa.b * C.kb + h * C.kh + unit * 8;
-            const uint16_t* vp = static_cast<const uint16_t*>(C.v) + pa.b * C.vb + h * C.vh + unit * 8;
-            const uint32_t dst = smem_u32(tiles + stage_in * 2 * Cfg::kTile);
+        if (src.x < x1) {
             int slot[Cp::SWEEPS];
-            Cp::slots(slot_ok(queue[0], n_slots, P.err) ? queue[0] : -1, lane, slot);
+            const uint16_t *kp = src.k + unit * 8, *vp = src.v + unit * 8;
+            const bool ok = slot_ok(held, n_slots, P.err);
+            if (whole_rows && src.at.tile * KT + KT <= src.len) {
+                // cached keys: nothing to leave out (a slot outside the pool has been reported; slot 0 is read)
+                Cp::slots(ok ? held : 0, lane, slot);
 #pragma unroll
-            for (int i = 0; i + 1 < kAhead; ++i) queue[i] = queue[i + 1];
-            queue[kAhead - 1] = fetch();
+                for (int j = 0; j < Cp::SWEEPS; ++j) {
+                    const uint32_t at = stage_in + tile_at<DP>(own0 + Cp::row(lane, j), unit);
+                    cp16(at, kp + (long long)slot[j] * k_step);
+                    cp16(at + Cfg::kTile, vp + (long long)slot[j] * v_step);
+                }
+            } else {
+                Cp::slots(ok ? held : -1, lane, slot);
 #pragma unroll
-            for (int j = 0; j < Cp::SWEEPS; ++j) {
-                const int r = Cp::row(lane, j);
-                const bool on = slot[j] >= 0 && unit_on;
-                const long long from = on ? slot[j] : 0;
-                const uint32_t at = tile_at<DP>(own0 + r, unit);
-                cp16(dst + at, on ? kp + from * k_step : kp - unit * 8, on);
-                cp16(dst + Cfg::kTile + at, on ? vp + from * v_step : vp - unit * 8, on);
+                for (int j = 0; j < Cp::SWEEPS; ++j) {
+                    const bool on = slot[j] >= 0 && unit_on;
+                    const long long from = on ? slot[j] : 0;
+                    const uint32_t at = stage_in + tile_at<DP>(own0 + Cp::row(lane, j), unit);
+                    cp16(at, on ? kp + from * k_step : src.k, on);
+                    cp16(at + Cfg::kTile, on ? vp + from * v_step : src.v, on);
+                }
             }
-            ++px;
-            if (++stage_in == S) stage_in = 0;
-            step(plan, C.B, groups, pa);
+            stage_in = stage_in + 2 * Cfg::kTile == ring + S * 2 * Cfg::kTile ? ring : stage_in + 2 * Cfg::kTile;
+            if (src.next(plan, C.B, groups) && src.x < x1) src.enter(C, plan, row_blocks);
+            if (src.x < x1) fetch();
         }
         cp_commit();
     };
-#pragma unroll
-    for (int i = 0; i < kAhead; ++i) queue[i] = fetch();
+    src.enter(C, plan, row_blocks);
+    fetch();
     for (int s = 0; s < S - 1; ++s) issue();
 
     At a = locate(plan, C.B, x0);

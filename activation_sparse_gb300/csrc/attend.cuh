@@ -22,6 +22,10 @@ constexpr float kLog2e = 1.4426950408889634f;
 __device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool on) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0) : "memory");
 }
+// the same without the choice
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void cp_wait() {
@@ -223,20 +227,54 @@ constexpr int part_floats(int rb, int dp) { return rb * (dp + 2); }
 constexpr int kWideRows = 128;     // query rows a block of the tensor-memory kernel has
 constexpr int kWideLeast = 4;      // and the tiles a part of its lists has at least
 
-// Who copies what: a warp copies KEYS keys of every tile, lane i < KEYS
+// Who copies what: a warp copies sixteen keys of every tile, lane i < 16
 // holding the slot of its key i.
-template <int DP, int KEYS = 16>
+template <int DP>
 struct Copy {
     static constexpr int UNITS = DP / 8;            // 16-byte units of a row
     static constexpr int AT_ONCE = 32 / UNITS;      // rows one sweep of a warp copies
-    static constexpr int SWEEPS = KEYS / AT_ONCE;
-    // row (of the warp's) that this lane copies in sweep j
+    static constexpr int SWEEPS = 16 / AT_ONCE;
+    // row (of the warp's sixteen) that this lane copies in sweep j
     static __device__ __forceinline__ int row(int lane, int j) { return (lane / UNITS) * SWEEPS + j; }
     // Slots of the rows this lane copies, from the lanes that hold them. All at once, ahead of the copies:
     // a shuffle between two copies would put its latency between them.
     static __device__ __forceinline__ void slots(int held, int lane, int (&slot)[SWEEPS]) {
 #pragma unroll
         for (int j = 0; j < SWEEPS; ++j) slot[j] = __shfl_sync(0xFFFFFFFFu, held, row(lane, j));
+    }
+};
+
+// The copying side of a CTA's walk over its tiles: where the next tile's rows
+// are. What depends on the list alone is worked out when the list changes.
+struct Source {
+    At at;
+    int x, x1;                 // flat index of the next tile, and of the first one that is not ours
+    const int32_t* list;
+    const uint16_t* k;
+    const uint16_t* v;
+    const float* acc;
+    int len, tot;
+    unsigned long long seen;   // nodes that any row sees (all of them where the caller says so)
+
+    __device__ __forceinline__ void start(const Plan& p, int B, int first, int end) {
+        at = locate(p, B, first);
+        x = first, x1 = end;
+    }
+    __device__ __forceinline__ void enter(const KvView& C, const Plan& p, int row_blocks) {
+        const int h = at.group / row_blocks;
+        list = C.table ? C.table + at.b * C.tb + h * C.th : nullptr;
+        k = static_cast<const uint16_t*>(C.k) + at.b * C.kb + h * C.kh;
+        v = static_cast<const uint16_t*>(C.v) + at.b * C.vb + h * C.vh;
+        acc = C.acc + at.b * C.ab + h * C.ah;
+        len = p.len[at.b], tot = p.tot[at.b];
+    }
+    // True where the next tile is of another list.
+    __device__ __forceinline__ bool next(const Plan& p, int B, int groups) {
+        ++x;
+        if (++at.tile < at.ntile) return false;
+        at.tile = at.ntile - 1;
+        step(p, B, groups, at);
+        return true;
     }
 };
 

@@ -63,54 +63,51 @@ __global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) k_kv_accumulate(c
     const bool unit_on = unit * 8 < D;
     const int n_slots = (int)C.n_slots, k_step = (int)C.ks;
 
-    At pa = locate(plan, C.B, x0), ahead = pa;
-    int px = x0, fetched = x0, stage_in = 0;
-    int queue[kAhead];  // lane i < 16: the slots of the warp's key i of the next tiles
+    Source src;
+    src.start(plan, C.B, x0, x1);
+    const bool whole_rows = D == DP;
+    const uint32_t ring = smem_u32(smem);
+    int stage_in = 0, held = kNoSlot;  // lane i < 16: the slot of the warp's key i of the tile to be issued next
     auto fetch = [&]() {
-        if (fetched >= x1) return kNoSlot;
-        const int32_t* list = C.table ? C.table + ahead.b * C.tb + ahead.group * C.th : nullptr;
-        const int tot = plan.tot[ahead.b], i = ahead.tile * KT + warp * 16 + (lane & 15);
-        ++fetched;
-        step(plan, C.B, C.Hkv, ahead);
-        return slot_of(list, i, tot, tot, 0);
+        held = slot_of(src.list, src.at.tile * KT + warp * 16 + (lane & 15), src.tot, src.tot, 0);
     };
     auto issue = [&]() {
-        if (px < x1) {
-            const uint16_t* kp = static_cast<const uint16_t*>(C.k) + pa.b * C.kb + pa.group * C.kh + unit * 8;
-            const float* ap = C.acc + pa.b * C.ab + pa.group * C.ah;
-            const uint32_t dst = smem_u32(smem + stage_in * Cfg::kTile);
-            const int slot = slot_ok(queue[0], n_slots, P.err) ? queue[0] : -1;
-#pragma unroll
-            for (int i = 0; i + 1 < kAhead; ++i) queue[i] = queue[i + 1];
-            queue[kAhead - 1] = fetch();
+        if (src.x < x1) {
+            const uint16_t* kp = src.k + unit * 8;
+            const uint32_t dst = ring + stage_in * Cfg::kTile;
+            const bool ok = slot_ok(held, n_slots, P.err);
             if (lane < 16) {
                 const int at = stage_in * KT + warp * 16 + lane;
-                slot_s[at] = slot;
+                slot_s[at] = ok ? held : -1;
                 asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(old_s + at)),
-                             "l"(ap + (slot >= 0 ? slot : 0)), "r"(slot >= 0 ? 4 : 0)
+                             "l"(src.acc + (ok ? held : 0)), "r"(ok ? 4 : 0)
                              : "memory");
             }
-            int slots[Cp::SWEEPS];
-            Cp::slots(slot, lane, slots);
+            int slot[Cp::SWEEPS];
+            Cp::slots(ok ? held : 0, lane, slot);  // keys past the end are read from slot 0 and not counted
+            if (whole_rows) {
 #pragma unroll
-            for (int j = 0; j < Cp::SWEEPS; ++j) {
-                const int r = Cp::row(lane, j);
-                const bool on = slots[j] >= 0 && unit_on;
-                const long long from = on ? slots[j] : 0;
-                cp16(dst + tile_at<DP>(warp * 16 + r, unit), on ? kp + from * k_step : kp - unit * 8, on);
+                for (int j = 0; j < Cp::SWEEPS; ++j)
+                    cp16(dst + tile_at<DP>(warp * 16 + Cp::row(lane, j), unit), kp + (long long)slot[j] * k_step);
+            } else {
+#pragma unroll
+                for (int j = 0; j < Cp::SWEEPS; ++j)
+                    cp16(dst + tile_at<DP>(warp * 16 + Cp::row(lane, j), unit),
+                         unit_on ? kp + (long long)slot[j] * k_step : src.k, unit_on);
             }
-            ++px;
             if (++stage_in == S) stage_in = 0;
-            step(plan, C.B, C.Hkv, pa);
+            if (src.next(plan, C.B, C.Hkv) && src.x < x1) src.enter(C, plan, 1);
+            if (src.x < x1) fetch();
         }
         cp_commit();
     };
-#pragma unroll
-    for (int i = 0; i < kAhead; ++i) queue[i] = fetch();
+    src.enter(C, plan, 1);
+    fetch();
     for (int s = 0; s < S - 1; ++s) issue();
 
     At a = locate(plan, C.B, x0);
-    int have_b = -1, have_h = -1, have_block = -1, n_rows = 0, stage_out = 0;
+    int have_b = -1, have_h = -1, have_block = -1, out_h = -1, n_rows = 0, stage_out = 0;
+    float* out = nullptr;
     for (int x = x0; x < x1; ++x, step(plan, C.B, C.Hkv, a)) {
         cp_wait<S - 2>();
         __syncwarp();
@@ -136,9 +133,13 @@ __global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) k_kv_accumulate(c
             __syncthreads();
             n_rows = node_s[64] * G;
             have_b = b;
-            have_h = -1;
+            have_h = out_h = -1;
         }
-        const uint32_t k_s = smem_u32(smem + stage * Cfg::kTile);
+        if (out_h != h) {
+            out = P.acc_out + b * C.ab + h * C.ah;
+            out_h = h;
+        }
+        const uint32_t k_s = ring + stage * Cfg::kTile, q_addr = smem_u32(q_s);
         uint32_t kf[DP <= 128 ? KD : 1][4];
         if (DP <= 128) {
 #pragma unroll
@@ -151,7 +152,7 @@ __global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) k_kv_accumulate(c
             const int nr = min(kWeighRows, n_rows - r0);
             if (have_h != h || have_block != r0) {
                 __syncthreads();
-                const int padded = (nr + 7) & ~7;
+                const int padded = (nr + 15) & ~15;
                 for (int i = tid; i < padded * UNITS; i += kThreads) {
                     const int r = i / UNITS, u = i % UNITS;
                     uint4 val = make_uint4(0, 0, 0, 0);
@@ -179,31 +180,38 @@ __global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) k_kv_accumulate(c
                 __syncthreads();
             }
             const bool edge = a.tile * KT + warp * 16 + 16 > len;
-            for (int n = 0; n < nr; n += 8) {
-                float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            for (int n = 0; n < nr; n += 16) {  // two chains of products
+                float s[2][4] = {};
 #pragma unroll
                 for (int k = 0; k < KD; k += 2) {
-                    // rows n .. n+7, d 32 wide: two k steps
-                    uint32_t qf[4];
-                    ldsm4(qf, smem_u32(q_s) + tile_at<DP>(n + (lane & 7), 2 * k + (lane >> 3)));
+                    // rows n .. n+7 and n+8 .. n+15, d 32 wide: two k steps
+                    uint32_t qa[4], qb[4];
+                    ldsm4(qa, q_addr + tile_at<DP>(n + (lane & 7), 2 * k + (lane >> 3)));
+                    ldsm4(qb, q_addr + tile_at<DP>(n + 8 + (lane & 7), 2 * k + (lane >> 3)));
 #pragma unroll
                     for (int kk = 0; kk < 2; ++kk) {
-                        if (DP > 128) {
-                            uint32_t kx[4];
-                            ldsm4(kx, k_s + tile_at<DP>(warp * 16 + (lane & 15), 2 * (k + kk) + (lane >> 4)));
-                            mma<FP16>(s, kx, qf[2 * kk], qf[2 * kk + 1]);
-                        } else {
-                            mma<FP16>(s, kf[DP <= 128 ? k + kk : 0], qf[2 * kk], qf[2 * kk + 1]);
-                        }
+                        uint32_t kx[4];
+                        if (DP > 128) ldsm4(kx, k_s + tile_at<DP>(warp * 16 + (lane & 15), 2 * (k + kk) + (lane >> 4)));
+                        const uint32_t(&ka)[4] = DP > 128 ? kx : kf[DP <= 128 ? k + kk : 0];
+                        mma<FP16>(s[0], ka, qa[2 * kk], qa[2 * kk + 1]);
+                        mma<FP16>(s[1], ka, qb[2 * kk], qb[2 * kk + 1]);
                     }
                 }
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int r = n + (lane & 3) * 2 + (e & 1);
-                    const int j = i0 + (e >> 1) * 8 - len;
-                    const bool sees = r < nr && (!edge || j < 0 || (j < T && (word_s[r] >> (j & 63) & 1)));
-                    const float p = ex2(fmaf(s[e], c2, -lse_s[r]));
-                    w[e >> 1] += sees ? p : 0.0f;
+                for (int c = 0; c < 2; ++c) {
+                    const int r = n + c * 8 + (lane & 3) * 2;
+                    const float2 lse = *reinterpret_cast<const float2*>(lse_s + r);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        float p = ex2(fmaf(s[c][e], c2, e & 1 ? -lse.y : -lse.x));
+                        // a padding row's zeros meet what a key holds, and 0 * infinity is NaN
+                        if (n + 16 > nr && r + (e & 1) >= nr) p = 0.0f;
+                        if (edge) {
+                            const int j = i0 + (e >> 1) * 8 - len;
+                            if (!(j < 0 || (j < T && (word_s[r + (e & 1)] >> (j & 63) & 1)))) p = 0.0f;
+                        }
+                        w[e >> 1] += p;
+                    }
                 }
             }
         }
@@ -213,7 +221,7 @@ __global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) k_kv_accumulate(c
             w[e] += __shfl_xor_sync(0xFFFFFFFFu, w[e], 2);
             const int key = stage * KT + warp * 16 + (lane >> 2) + e * 8;
             const int slot = slot_s[key];
-            if ((lane & 3) == 0 && slot >= 0) P.acc_out[b * C.ab + h * C.ah + slot] = old_s[key] + w[e];
+            if ((lane & 3) == 0 && slot >= 0) out[slot] = old_s[key] + w[e];
         }
     }
     cp_wait<0>();

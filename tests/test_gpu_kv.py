@@ -447,6 +447,22 @@ def test_accumulate(si, lens, T, Hq, Hkv, D, dtype, table, mask, rows):
     assert t.equal(c.acc[1][w], out.t[w]) and t.equal(c.acc[1][~w], acc0[1][~w]) and t.equal(c.acc[0], acc0[0])
 
 
+def test_accumulate_infinite_keys(si):
+    """A key with an infinity weighs nothing where its score is minus infinity; rows that are not there do not change that."""
+    t = torch()
+    K = t.zeros(1, 1, 1, 70, 64, dtype=t.bfloat16, device="cuda")
+    K[0, 0, 0, 3, 0] = -math.inf
+    acc = t.zeros(1, 1, 1, 70, device="cuda")
+    kv = si.si_kv_create(K, K, None, t.full((1, 1), 69, dtype=t.int32, device="cuda"), acc)
+    q = t.ones(1, 1, 3, 64, dtype=t.bfloat16, device="cuda")
+    out, lse = t.empty_like(q), t.empty(1, 1, 3, device="cuda")
+    si.si_tree_attention(kv, q, out, lse=lse)
+    si.si_kv_accumulate(kv, q, lse)
+    want = t.full((70,), 3 / 69, device="cuda")
+    want[3] = 0
+    assert t.allclose(acc[0, 0, 0], want, rtol=1e-5, atol=0)
+
+
 def test_attention_weights_sum_to_rows(si):
     """The weights of one call's own lse add up to the number of its rows."""
     c = Cache(si, 32, [777], 9, 2, 128, "bf16")

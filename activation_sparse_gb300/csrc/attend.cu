@@ -24,7 +24,8 @@ template <int DP>
 struct AttendCfg {
     static constexpr int kTile = KT * DP * 2;             // bytes of a K or V tile
     static constexpr int kStages = 3;
-    static constexpr int kRows = DP <= 128 ? 64 : 32;     // query rows a block has at most
+    static constexpr int kCtas = DP <= 128 ? 2 : 1;       // an SM
+    static constexpr int kRows = DP <= 128 ? 16 : 32;     // query rows a block has at most
     static constexpr int kQBytes = kRows * DP * 2;
     static constexpr int kOffQ = kStages * 2 * kTile;
     static constexpr int kOffPlan = kOffQ + kQBytes;
@@ -42,7 +43,7 @@ __device__ __forceinline__ void group_sync(int id) {
 // warp takes KT / KW keys of every tile with its own softmax state, joined at
 // the end of a list.
 template <int DP, int MW, bool FP16>
-__global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1)
+__global__ void __launch_bounds__(kThreads, AttendCfg<DP>::kCtas)
     k_tree_attention(const __grid_constant__ AttendParams P, int row_blocks) {
     using Cfg = AttendCfg<DP>;
     using Cp = Copy<DP>;

@@ -7,7 +7,7 @@ namespace {
 
 constexpr int kThreads = 128;  // four warps
 
-int per_sm(int dp) { return dp <= 128 ? 2 : 1; }
+int per_sm(int dp) { return dp <= 128 ? 3 : 1; }
 int padded(int D) { return D <= 64 ? 64 : D <= 128 ? 128 : 256; }
 
 // Rows kept in shared memory at once.
@@ -16,7 +16,7 @@ constexpr int kWeighRows = 64;
 template <int DP>
 struct WeighCfg {
     static constexpr int kTile = KT * DP * 2;
-    static constexpr int kStages = DP <= 128 ? 5 : 4;
+    static constexpr int kStages = DP <= 128 ? 3 : 4;
     static constexpr int kOffQ = kStages * kTile;
     static constexpr int kOffRow = kOffQ + kWeighRows * DP * 2;      // per row: ancestor word, lse; the counted nodes
     static constexpr int kOffKey = kOffRow + kWeighRows * (8 + 4 + 4) + 16;  // per stage and key: slot, acc
@@ -30,7 +30,7 @@ struct WeighCfg {
 // key belongs to one warp, which also copies it and its old weight, so warps
 // only meet when the list (and with it the queries) changes.
 template <int DP, bool FP16>
-__global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) k_kv_accumulate(const __grid_constant__ AttendParams P) {
+__global__ void __launch_bounds__(kThreads, DP <= 128 ? 3 : 1) k_kv_accumulate(const __grid_constant__ AttendParams P) {
     using Cfg = WeighCfg<DP>;
     using Cp = Copy<DP>;
     constexpr int KD = DP / 16;

@@ -145,7 +145,7 @@ __global__ void __launch_bounds__(kAppendThreads)
 // ------------------------------------------------------------------- evict
 
 constexpr int kEvictBins = 2048;
-constexpr int kEvictChunk = 24576;  // candidates a CTA holds at most: 8 bytes each in shared memory
+constexpr int kEvictChunk = 24576;  // candidates a CTA holds at most: a key each in shared memory
 constexpr int kEvictBatch = 8;      // entries a thread loads at once: two dependent loads each
 
 struct alignas(16) EvictShared {
@@ -162,24 +162,24 @@ struct alignas(16) EvictShared {
 constexpr uint32_t kKeyNone = 0u, kKeyNaN = 1u, kKeySafe = 0xFFFFFFFFu;
 __device__ __forceinline__ uint32_t weight_key(float w) { return w != w ? kKeyNaN : value_key(w); }
 
-// One cluster per list. It holds the candidates (slot and key) in the shared
-// memory of its CTAs, finds the key of the last survivor by a radix selection
-// over 11 + 11 + 10 bits, and writes the stable partition. In each pass the
-// CTAs add their non-empty bins to the first CTA's histogram (a list's
-// weights fall into few bins: a few hundred words, where reading every
-// peer's histogram moved 8 KB a peer); the first CTA finds the bin and tells
-// the others. Everything is read before the first cluster barrier and written
-// after it, so the list may be edited in place. Bound by latency: a chain of
-// three loads (length, slot, weight), then barriers, so two or more CTAs
-// share an SM.
-template <int THREADS>
-__global__ void __launch_bounds__(THREADS, 1024 / THREADS)
-    k_kv_evict(const __grid_constant__ KvEvictParams P, int chunk_cap) {
+// One cluster per list. It holds the candidates' keys in the shared memory of
+// its CTAs, finds the key of the last survivor by a radix selection over 11 +
+// 11 + 10 bits, and writes the stable partition. In each pass the CTAs add
+// their non-empty bins to the first CTA's histogram (a list's weights fall
+// into few bins: a few hundred words, where reading every peer's histogram
+// moved 8 KB a peer); the first CTA finds the bin and tells the others. The
+// slots are read again for the partition, so that more CTAs share an SM; in
+// place they are all read before the last cluster barrier and written after
+// it. Bound by latency (a chain of three loads: length, slot, weight; then
+// barriers) and for long lists by the weights' gather: four bytes of every
+// 32-byte sector, 0.6 sectors a cycle and SM.
+template <int THREADS, bool IN_PLACE>
+__global__ void __launch_bounds__(THREADS, (IN_PLACE ? 512 : 1536) / THREADS > 0 ? (IN_PLACE ? 512 : 1536) / THREADS : 1)
+    k_kv_evict(const __grid_constant__ KvEvictParams P) {
     constexpr int WARPS = THREADS / 32;
     extern __shared__ __align__(16) uint8_t smem_raw[];
     EvictShared& S = *reinterpret_cast<EvictShared*>(smem_raw);
-    int32_t* slots = reinterpret_cast<int32_t*>(smem_raw + sizeof(EvictShared));
-    uint32_t* keys = reinterpret_cast<uint32_t*>(slots + chunk_cap);
+    uint32_t* keys = reinterpret_cast<uint32_t*>(smem_raw + sizeof(EvictShared));
     cg::cluster_group cluster = cg::this_cluster();
     const int CS = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -239,58 +239,62 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
     const int c0 = min(n, rank * chunk), c1 = min(n, c0 + chunk), m = c1 - c0;
     const int lo_c = P.sinks, hi_c = n - P.recent;  // candidates outside [lo_c, hi_c) are safe
     const unsigned n_slots = (unsigned)P.n_slots;
+    auto entry_of = [&](int c) {  // list entry of candidate c
+        return named && c >= len ? len + P.path[(long long)b * T + c - len] : c;
+    };
     bool bad_slot = false;
-    const int by_table = max(0, min(c1, named ? len : n) - c0);  // candidates whose entry is their own index
-    for (int i0 = tid; i0 < by_table; i0 += THREADS * kEvictBatch) {
-        int slot[kEvictBatch];
-        float w[kEvictBatch];
+    if (evict) {
+        const int by_table = max(0, min(c1, named ? len : n) - c0);  // candidates whose entry is their own index
+        for (int i0 = tid; i0 < by_table; i0 += THREADS * kEvictBatch) {
+            int slot[kEvictBatch];
+            float w[kEvictBatch];
 #pragma unroll
-        for (int j = 0; j < kEvictBatch; ++j) {
-            const int i = i0 + j * THREADS;
-            slot[j] = i < by_table ? table[c0 + i] : 0;
-        }
-        if (evict) {
+            for (int j = 0; j < kEvictBatch; ++j) {
+                const int i = i0 + j * THREADS;
+                slot[j] = i < by_table ? table[c0 + i] : 0;
+            }
 #pragma unroll
             for (int j = 0; j < kEvictBatch; ++j) {
                 const bool ok = (unsigned)slot[j] < n_slots;
                 bad_slot |= !ok;
                 w[j] = acc[ok ? slot[j] : 0];
             }
-        }
 #pragma unroll
-        for (int j = 0; j < kEvictBatch; ++j) {
-            const int i = i0 + j * THREADS;
-            if (i >= by_table) break;
-            slots[i] = slot[j];
-            if (evict) {
+            for (int j = 0; j < kEvictBatch; ++j) {
+                const int i = i0 + j * THREADS;
+                if (i >= by_table) break;
                 const uint32_t key = c0 + i < lo_c || c0 + i >= hi_c ? kKeySafe : weight_key(w[j]);
                 keys[i] = key;
                 atomicAdd(&S.hist[key >> 21], 1u);
             }
         }
-    }
-    for (int i = by_table + tid; i < ((m + 127) & ~127); i += THREADS) {
-        uint32_t key = kKeyNone;
-        if (i < m) {  // accepted nodes, in path order
-            const int slot = table[len + P.path[(long long)b * T + c0 + i - len]];
-            slots[i] = slot;
-            if (evict) {
+        for (int i = by_table + tid; i < ((m + 127) & ~127); i += THREADS) {
+            uint32_t key = kKeyNone;
+            if (i < m) {  // accepted nodes, in path order
+                const int slot = table[entry_of(c0 + i)];
                 const bool ok = (unsigned)slot < n_slots;
                 bad_slot |= !ok;
                 key = c0 + i < lo_c || c0 + i >= hi_c ? kKeySafe : weight_key(acc[ok ? slot : 0]);
                 atomicAdd(&S.hist[key >> 21], 1u);
             }
+            keys[i] = key;
         }
-        if (evict) keys[i] = key;
     }
     if (bad_slot) atomicOr(P.err, SI_DEVERR_CACHE);
     int rejected = -1;  // slot of the node that this thread puts behind the candidates
     if (rank == 0 && named && tid < T && !(taken >> tid & 1)) rejected = bad ? -1 : table[len + tid];
 
     if (!evict) {
-        all_sync();
-        for (int i = tid; i < m; i += THREADS)
-            if (!P.in_place || c0 + i >= len) out[c0 + i] = slots[i];
+        if (IN_PLACE) {
+            // live entries stay; accepted nodes (at most 64) may change places
+            const int c = len + tid;
+            const bool moves = rank == 0 && named && c < n;
+            const int slot = moves ? table[entry_of(c)] : 0;
+            all_sync();
+            if (moves) out[c] = slot;
+        } else {
+            for (int c = c0 + tid; c < c1; c += THREADS) out[c] = table[entry_of(c)];
+        }
     } else {
         const int quads = ((m + 127) & ~127) / 4;
         const uint4* keys4 = reinterpret_cast<const uint4*>(keys);
@@ -390,9 +394,8 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
             strict += __reduce_add_sync(0xFFFFFFFFu, a);
             tie += __reduce_add_sync(0xFFFFFFFFu, t2);
         }
-        for (int q = s0; q < s1; ++q) {
+        auto write_set = [&](int q, const int (&slot)[4]) {
             const uint4 k = keys4[q * 32 + lane];
-            const int4 v = reinterpret_cast<const int4*>(slots)[q * 32 + lane];
             const unsigned mine = classes(k);
             unsigned incl = mine;
 #pragma unroll
@@ -402,26 +405,48 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
             }
             unsigned my_strict = strict + ((incl - mine) & 0xFFFFu), my_tie = tie + ((incl - mine) >> 16);
             int c = c0 + q * 128 + lane * 4;
-            auto put = [&](uint32_t key, int slot) {
+            auto put = [&](uint32_t key, int value) {
                 const bool tied = key == prefix;
                 const int pos = (int)(my_strict + min(my_tie, tie_need));  // survivors before this candidate
                 const bool keep = key > prefix || (tied && my_tie < tie_need);
-                if (c < c1) out[keep ? pos : P.budget + (c - pos)] = slot;
+                if (c < c1) out[keep ? pos : P.budget + (c - pos)] = value;
                 my_strict += key > prefix;
                 my_tie += tied;
                 ++c;
             };
-            put(k.x, v.x);
-            put(k.y, v.y);
-            put(k.z, v.z);
-            put(k.w, v.w);
+            put(k.x, slot[0]);
+            put(k.y, slot[1]);
+            put(k.z, slot[2]);
+            put(k.w, slot[3]);
             const unsigned all = __shfl_sync(0xFFFFFFFFu, incl, 31);
             strict += all & 0xFFFFu;
             tie += all >> 16;
+        };
+        auto read_set = [&](int q, int (&slot)[4]) {
+            const int c = c0 + q * 128 + lane * 4;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) slot[e] = c + e < c1 ? table[entry_of(c + e)] : 0;
+        };
+        if (IN_PLACE) {
+            constexpr int kMost = kEvictChunk / 128 / (512 / 32);  // sets a warp has at most
+            int slot[kMost][4];
+#pragma unroll
+            for (int q = 0; q < kMost; ++q)
+                if (s0 + q < s1) read_set(s0 + q, slot[q]);
+            all_sync();
+#pragma unroll
+            for (int q = 0; q < kMost; ++q)
+                if (s0 + q < s1) write_set(s0 + q, slot[q]);
+        } else {
+            for (int q = s0; q < s1; ++q) {
+                int slot[4];
+                read_set(q, slot);
+                write_set(q, slot);
+            }
         }
     }
     if (rejected >= 0) out[n + tid - __popcll(taken & ((1ull << tid) - 1))] = rejected;
-    if (!P.in_place) {
+    if (!IN_PLACE) {
         // what this call does not reorder: unaccepted nodes that stay behind the candidates, free slots
         const int from = named ? used : n;
         for (int i = from + rank * THREADS + tid; i < P.cap; i += CS * THREADS) out[i] = table[i];
@@ -462,6 +487,15 @@ cudaError_t launch(const void* fn, dim3 grid, int threads, size_t smem, int clus
     return cudaLaunchKernelExC(&cfg, fn, args);
 }
 
+template <int THREADS, bool IN_PLACE>
+cudaError_t launch_evict(const KvEvictParams& P, unsigned ctas, int cs, size_t smem, cudaStream_t st) {
+    const auto kern = k_kv_evict<THREADS, IN_PLACE>;
+    const cudaError_t e = allow_max_smem(kern);
+    if (e != cudaSuccess) return e;
+    void* args[1] = {const_cast<KvEvictParams*>(&P)};
+    return launch(reinterpret_cast<const void*>(kern), dim3(ctas, 1, 1), THREADS, smem, cs, args, st);
+}
+
 }  // namespace
 
 cudaError_t launch_kv_append(const KvAppendParams& P, const RopeTable& R, cudaStream_t st) {
@@ -473,21 +507,20 @@ cudaError_t launch_kv_append(const KvAppendParams& P, const RopeTable& R, cudaSt
 
 cudaError_t launch_kv_evict(const KvEvictParams& P, cudaStream_t st) {
     const long long rows = (long long)P.L * P.B * P.Hkv;
-    // CTAs a list (at most eight, the portable cluster): few enough candidates each that two CTAs share an
+    // CTAs a list (at most eight, the portable cluster): few enough candidates each that three CTAs share an
     // SM where eight CTAs can do that; down to 2048 each where the lists alone do not fill the GPU
     int cs = 1;
     auto each = [&]() { return ((P.cap + cs - 1) / cs + 127) & ~127; };
     while (cs < 8 && (each() > 12544 || (each() > 2048 && rows * cs < 304))) cs *= 2;
-    int chunk = each();
+    const int chunk = each();
     if (chunk > kEvictChunk) return cudaErrorInvalidValue;
     const bool wide = chunk > 5120;
-    const size_t smem = sizeof(EvictShared) + (size_t)chunk * 8;
-    const cudaError_t e = wide ? allow_max_smem(k_kv_evict<512>) : allow_max_smem(k_kv_evict<256>);
-    if (e != cudaSuccess) return e;
-    const void* fn = wide ? reinterpret_cast<const void*>(&k_kv_evict<512>)
-                          : reinterpret_cast<const void*>(&k_kv_evict<256>);
-    void* args[2] = {const_cast<KvEvictParams*>(&P), &chunk};
-    return launch(fn, dim3((unsigned)(rows * cs), 1, 1), wide ? 512 : 256, smem, cs, args, st);
+    const size_t smem = sizeof(EvictShared) + (size_t)chunk * 4;
+    if (P.in_place)
+        return wide ? launch_evict<512, true>(P, (unsigned)(rows * cs), cs, smem, st)
+                    : launch_evict<256, true>(P, (unsigned)(rows * cs), cs, smem, st);
+    return wide ? launch_evict<512, false>(P, (unsigned)(rows * cs), cs, smem, st)
+                : launch_evict<256, false>(P, (unsigned)(rows * cs), cs, smem, st);
 }
 
 }  // namespace si

@@ -394,38 +394,28 @@ __global__ void __launch_bounds__(THREADS, (IN_PLACE ? 512 : 1536) / THREADS > 0
             strict += __reduce_add_sync(0xFFFFFFFFu, a);
             tie += __reduce_add_sync(0xFFFFFFFFu, t2);
         }
-        auto write_set = [&](int q, const int (&slot)[4]) {
-            const uint4 k = keys4[q * 32 + lane];
-            const unsigned mine = classes(k);
-            unsigned incl = mine;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const unsigned u = __shfl_up_sync(0xFFFFFFFFu, incl, o);
-                if (lane >= o) incl += u;
-            }
-            unsigned my_strict = strict + ((incl - mine) & 0xFFFFu), my_tie = tie + ((incl - mine) >> 16);
-            int c = c0 + q * 128 + lane * 4;
-            auto put = [&](uint32_t key, int value) {
-                const bool tied = key == prefix;
-                const int pos = (int)(my_strict + min(my_tie, tie_need));  // survivors before this candidate
-                const bool keep = key > prefix || (tied && my_tie < tie_need);
-                if (c < c1) out[keep ? pos : P.budget + (c - pos)] = value;
-                my_strict += key > prefix;
-                my_tie += tied;
-                ++c;
-            };
-            put(k.x, slot[0]);
-            put(k.y, slot[1]);
-            put(k.z, slot[2]);
-            put(k.w, slot[3]);
-            const unsigned all = __shfl_sync(0xFFFFFFFFu, incl, 31);
-            strict += all & 0xFFFFu;
-            tie += all >> 16;
-        };
+        // A set again, now a candidate a lane four times over: the writes of a warp are runs of the output.
         auto read_set = [&](int q, int (&slot)[4]) {
-            const int c = c0 + q * 128 + lane * 4;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) slot[e] = c + e < c1 ? table[entry_of(c + e)] : 0;
+            for (int e = 0; e < 4; ++e) {
+                const int c = c0 + q * 128 + e * 32 + lane;
+                slot[e] = c < c1 ? table[entry_of(c)] : 0;
+            }
+        };
+        unsigned kept = strict + min(tie, tie_need);  // survivors before the next 32 candidates
+        auto write_set = [&](int q, const int (&slot)[4]) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int i = q * 128 + e * 32 + lane, c = c0 + i;
+                const uint32_t key = keys[i];
+                const unsigned ties = __ballot_sync(0xFFFFFFFFu, key == prefix);
+                const bool keep = key > prefix || (key == prefix && tie + __popc(ties & lanemask_lt()) < tie_need);
+                const unsigned keeps = __ballot_sync(0xFFFFFFFFu, keep && c < c1);
+                const int pos = (int)(kept + __popc(keeps & lanemask_lt()));
+                if (c < c1) out[keep ? pos : P.budget + (c - pos)] = slot[e];
+                tie += __popc(ties);
+                kept += __popc(keeps);
+            }
         };
         if (IN_PLACE) {
             constexpr int kMost = kEvictChunk / 128 / (512 / 32);  // sets a warp has at most

@@ -422,7 +422,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
     constexpr int E = DP / 32;  // columns a lane
     constexpr int ROWS = kJoinWarps / JW;  // rows a block
     __shared__ float acc_s[JW > 1 ? JW : 1][DP];
-    __shared__ float sum_s[kJoinWarps];
+    __shared__ float sum_s[kJoinWarps], top_s[kJoinWarps];
     extern __shared__ __align__(128) uint8_t smem[];
     const KvView& C = P.c;
     Plan plan;
@@ -453,33 +453,58 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
         const int second = c == first && deal.start(c) < y0;
         return P.part + ((long long)c * 2 + second) * part_floats(RB, DP);
     };
+    // Four parts at a time, maxima, sums and rows together: one trip to memory each.
     float top = -INFINITY, sum = 0.0f, acc[E] = {};
+    auto shift_of = [](float m) { return m == -INFINITY ? 0.0f : m; };
     if (on) {
-        for (int c = first + lane; c <= last; c += 32) top = fmaxf(top, part_of(c)[RB * DP + r]);
-    }
+        for (int c0 = first + w; c0 <= last; c0 += 4 * JW) {
+            float m[4], l[4], o[4][E];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-    const float shift = top == -INFINITY ? 0.0f : top;
-    if (on) {
-#pragma unroll 4
-        for (int c = first + w; c <= last; c += JW) {
-            const float* p = part_of(c);
-            const float f = ex2((p[RB * DP + r] - shift) * c2);
-            sum += f * p[RB * DP + RB + r];
+            for (int i = 0; i < 4; ++i) {
+                const int c = c0 + i * JW;
+                m[i] = -INFINITY, l[i] = 0.0f;
 #pragma unroll
-            for (int e = 0; e < E; ++e) acc[e] += f * p[r * DP + e * 32 + lane];
+                for (int e = 0; e < E; ++e) o[i][e] = 0.0f;
+                if (c <= last) {
+                    const float* p = part_of(c);
+                    m[i] = p[RB * DP + r];
+                    l[i] = p[RB * DP + RB + r];
+#pragma unroll
+                    for (int e = 0; e < E; ++e) o[i][e] = p[r * DP + e * 32 + lane];
+                }
+            }
+            const float high = fmaxf(fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])), top);
+            const float shift = shift_of(high), keep = ex2((top - shift) * c2);
+            top = high;
+            sum *= keep;
+#pragma unroll
+            for (int e = 0; e < E; ++e) acc[e] *= keep;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float f = ex2((m[i] - shift) * c2);
+                sum += f * l[i];
+#pragma unroll
+                for (int e = 0; e < E; ++e) acc[e] += f * o[i][e];
+            }
         }
     }
     if (JW > 1) {
 #pragma unroll
         for (int e = 0; e < E; ++e) acc_s[JW > 1 ? w : 0][e * 32 + lane] = acc[e];
-        if (lane == 0) sum_s[w] = sum;
+        if (lane == 0) top_s[w] = top, sum_s[w] = sum;
         __syncthreads();
         if (w > 0) return;
-        for (int i = 1; i < JW; ++i) {
-            sum += sum_s[i];
+        for (int i = 1; i < JW; ++i) top = fmaxf(top, top_s[i]);
+        const float shift = shift_of(top);
+        sum = 0.0f;
 #pragma unroll
-            for (int e = 0; e < E; ++e) acc[e] += acc_s[JW > 1 ? i : 0][e * 32 + lane];
+        for (int e = 0; e < E; ++e) acc[e] = 0.0f;
+#pragma unroll
+        for (int i = 0; i < JW; ++i) {
+            const float f = ex2((top_s[i] - shift) * c2);
+            sum += f * sum_s[i];
+#pragma unroll
+            for (int e = 0; e < E; ++e) acc[e] += f * acc_s[JW > 1 ? i : 0][e * 32 + lane];
         }
     }
     if (!on) return;

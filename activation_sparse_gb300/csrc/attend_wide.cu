@@ -2,33 +2,29 @@
 // heads) on the 5th-generation tensor cores.
 //
 // A block of 128 query rows of one list meets tiles of 64 keys:
-//   S = Q K^T   tcgen05.mma M = 128, N = 64, K = D    (accumulator and Q in TMEM)
+//   S = Q K^T   tcgen05.mma M = 128, N = 64, K = D    (accumulator in TMEM)
 //   P = exp(scale (S - m))                            (one thread a row)
-//   O += P V    tcgen05.mma M = 128, N = D, K = 64    (accumulator in TMEM)
-// Q lies in TMEM because the products of a tile would read it again from
-// shared memory, 32 KB beside the key tile's 16: 635 cycles a tile for what
-// takes 256 of arithmetic. The value tile serves as it lies, [key][d], as an operand with d contiguous.
+//   O += P V    tcgen05.mma M = 128, N = D, K = 64    (P and the accumulator in TMEM)
+// There are two S, and P is written over the half of its S that has been
+// read, so the softmax of a tile waits for nothing but its own S: with one S
+// and P in shared memory every tile was a chain of waits (softmax, product,
+// product), 1.1 us a tile with all work taken out. The value tile serves as
+// it lies, [key][d], as an operand with d contiguous.
 // The reference m of a row moves only when the maximum outgrows it by a
 // factor of 2^8: weights up to 256 are as exact in 16 bits as weights up to
 // 1, and the sums are in 32 bits, so the output is rescaled a few times a
 // list instead of once a tile.
 //
 // Warps: 0-3 softmax and output (TMEM lanes 32 w ..), 4 issues the matrix
-// instructions, 5-8 copy keys and values through the slot table into the
-// 128-byte swizzle the tensor cores read: tiles of cached keys by the TMA's
-// four-row gather (a warp's instruction moves 4 KB), tiles that meet the new
-// nodes, and caches whose strides or D do not fit a tensor map, by 16-byte
-// asynchronous copies (512 bytes an instruction: they took half of the issue
-// slots, and a tile 1570 cycles of an SM). Two
+// instructions, 5-8 copy keys and values through the slot table (16-byte
+// asynchronous copies into the 128-byte swizzle the tensor cores read; the
+// TMA's four-row gather moves as much an instruction but takes its operands
+// from uniform registers, some twenty instructions a gather where a copy
+// takes four, and was no faster). Two
 // CTAs share an SM, so one's softmax runs under the other's products. Every
 // write to shared memory is an ordinary one; the issuing thread's proxy fence,
 // after the barrier that announces it, lets the tensor cores see it.
 // All waits are bounded; TMEM is always released.
-#include <cuda.h>
-#include <cudaTypedefs.h>
-
-#include <mutex>
-
 #include "attend.cuh"
 
 namespace si {
@@ -37,13 +33,13 @@ namespace {
 
 constexpr int kThreads = 9 * 32;
 constexpr int kSoftmaxThreads = 128, kCopyThreads = 128;
-constexpr int kMaxSlots = 6;       // ring slots: a key or a value tile each
+constexpr int kMaxSlots = 5;       // ring slots: a key or a value tile each
 
 template <int DP>
 struct WideCfg {
     static constexpr int kTile = KT * DP * 2;
-    static constexpr int kOffRing = kWideRows * KT * 2;        // after P
-    static constexpr int kColO = 64, kColQ = 64 + DP;          // TMEM columns: S, O, Q (two elements a column)
+    static constexpr int kOffRing = kWideRows * DP * 2;        // after Q
+    static constexpr int kColP = KT / 2, kColO = 2 * KT;       // TMEM columns: two S (P in the second half), O
     static constexpr int kTmemCols = 256;
     static constexpr int kBars = 2 * kMaxSlots + 5;
     static constexpr int fixed(int B) { return (kBars + 1) * 8 + kMaxSlots * 8 + 16 + (3 * B + 1) * 4; }
@@ -102,14 +98,20 @@ __device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t* r) {
           "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
         : "r"(addr));
 }
-__device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t* r) {
+__device__ __forceinline__ void tmem_ld16(uint32_t addr, uint32_t* r) {
     asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(addr),
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, "
+        "[%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(addr));
+}
+__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t* r) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16};" ::"r"(addr),
         "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
-        "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
-        "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
         : "memory");
 }
 // Bounded wait that an earlier failure does not cut short.
@@ -118,17 +120,6 @@ __device__ __forceinline__ void mbar_drain(uint64_t* bar, uint32_t parity) {
     while (!mbar_try_wait(bar, parity)) {
         if (cycles() - t0 > kDrainLimitCycles) return;
     }
-}
-
-// Four rows of 64 elements (from element `col`) into 512 bytes of a swizzled tile.
-__device__ __forceinline__ void tma_gather4(uint32_t dst, const CUtensorMap* map, int col, const int (&row)[4],
-                                            uint64_t* bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cta.global.tile::gather4.mbarrier::complete_tx::bytes [%0], "
-        "[%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(col), "r"(row[0]), "r"(row[1]), "r"(row[2]), "r"(row[3]),
-        "r"(smem_u32(bar))
-        : "memory");
 }
 
 __device__ __forceinline__ float max3(float a, float b, float c) {
@@ -164,20 +155,18 @@ __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.
 
 template <int DP, bool FP16>
 __global__ void __launch_bounds__(kThreads, 2)
-    k_tree_attention_wide(const __grid_constant__ AttendParams P, const __grid_constant__ CUtensorMap map_k,
-                          const __grid_constant__ CUtensorMap map_v, int by_tma, int row_blocks, int slots) {
+    k_tree_attention_wide(const __grid_constant__ AttendParams P, int row_blocks, int slots) {
     using Cfg = WideCfg<DP>;
     using Cp = Copy<DP>;
     extern __shared__ __align__(1024) uint8_t smem[];  // the swizzle needs tiles on 1024-byte boundaries
-    uint8_t* const p_s = smem;
+    uint8_t* const q_s = smem;
     uint8_t* const ring = smem + Cfg::kOffRing;
     uint64_t* const full = reinterpret_cast<uint64_t*>(ring + slots * Cfg::kTile);
     uint64_t* const empty = full + kMaxSlots;
-    uint64_t* const q_full = empty + kMaxSlots;  // this list's queries are in TMEM
-    uint64_t* const s_full = q_full + 1;         // S of a tile is in TMEM
-    uint64_t* const s_free = q_full + 2;         // and has been read
-    uint64_t* const p_full = q_full + 3;         // P of a tile is in shared memory
-    uint64_t* const o_done = q_full + 4;         // O includes the tile
+    uint64_t* const q_full = empty + kMaxSlots;  // this list's queries are in shared memory
+    uint64_t* const s_full = q_full + 1;         // [2] S of a tile is in TMEM
+    uint64_t* const p_full = q_full + 3;         // P of a tile is in TMEM
+    uint64_t* const o_done = q_full + 4;         // O includes the tile; its S and P are free
     uint16_t* const odd = reinterpret_cast<uint16_t*>(full + Cfg::kBars + 1);  // [slot][4]: keys of a value tile that are not finite
     uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(odd + kMaxSlots * 4);
     Plan plan;
@@ -200,8 +189,8 @@ __global__ void __launch_bounds__(kThreads, 2)
             mbar_init(&empty[s], 1);
         }
         mbar_init(q_full, kSoftmaxThreads);
-        mbar_init(s_full, 1);
-        mbar_init(s_free, kSoftmaxThreads);
+        mbar_init(&s_full[0], 1);
+        mbar_init(&s_full[1], 1);
         mbar_init(p_full, kSoftmaxThreads);
         mbar_init(o_done, 1);
         fence_mbar_init();
@@ -226,32 +215,19 @@ __global__ void __launch_bounds__(kThreads, 2)
     } else if (warp >= 5) {
         // ---------------------------------------------------------- copies
         const int own0 = (warp - 5) * 16, unit = lane % Cp::UNITS;
-        const bool unit_on = unit * 8 < D;
+        const bool unit_on = unit * 8 < D, whole_rows = D == DP;
         const int n_slots = (int)C.n_slots, k_step = (int)C.ks, v_step = (int)C.vs;
-        const uint32_t col = (uint32_t)(unit >> 3) * (KT * 128);  // sub-tile of this lane's unit
-        At a = locate(plan, C.B, x0), ahead = a;
-        unsigned long long seen = 0;
-        int seen_b = -1, fetched = x0;
+        const uint32_t ring_addr = smem_u32(ring) + (uint32_t)(unit >> 3) * (KT * 128);  // this lane's sub-tile
+        Source src;
+        src.start(plan, C.B, x0, x1);
+        int held = kNoSlot, seen_b = -1;
         auto fetch = [&]() {
-            if (fetched >= x1) return kNoSlot;
-            const int b = ahead.b, h = ahead.group / row_blocks;
-            const int32_t* list = C.table ? C.table + b * C.tb + h * C.th : nullptr;
-            const int len = plan.len[b], i0 = ahead.tile * KT;
-            if (i0 + KT > len && seen_b != b) {
-                seen = seen_nodes(P.mask, T, b, lane);
-                seen_b = b;
+            const int i0 = src.at.tile * KT;
+            if (i0 + KT > src.len && seen_b != src.at.b) {
+                src.seen = seen_nodes(P.mask, T, src.at.b, lane);
+                seen_b = src.at.b;
             }
-            ++fetched;
-            step(plan, C.B, groups, ahead);
-            return slot_of(list, i0 + own0 + (lane & 15), len, plan.tot[b], seen);
-        };
-        auto copy = [&](uint32_t dst, const uint16_t* base, int step_, const int (&slot)[Cp::SWEEPS]) {
-#pragma unroll
-            for (int j = 0; j < Cp::SWEEPS; ++j) {
-                const bool on = slot[j] >= 0 && unit_on;
-                const long long from = on ? slot[j] : 0;
-                cp16(dst + col + sw128(own0 + Cp::row(lane, j), unit & 7), on ? base + from * step_ : base - unit * 8, on);
-            }
+            held = slot_of(src.list, i0 + own0 + (lane & 15), src.len, src.tot, src.seen);
         };
         // The barrier hears of this thread's copies when they land. The thread that issues the products
         // makes them visible to the tensor cores: a proxy fence here would wait for every copy in flight.
@@ -261,45 +237,19 @@ __global__ void __launch_bounds__(kThreads, 2)
         // New nodes' value rows that are not finite leave the tile (0 * NaN is NaN) and are
         // reported, so that the rows that see them get them back at the end.
         auto clean = [&](int slot_at, int i0, int len) {
-            uint8_t* tile = ring + slot_at * Cfg::kTile;
+            uint8_t* tile = ring + slot_at * Cfg::kTile + (unit >> 3) * (KT * 128);
             unsigned bad = 0;
 #pragma unroll 1
             for (int j = 0; j < Cp::SWEEPS; ++j) {
                 const int r = Cp::row(lane, j), node = i0 + own0 + r - len;
                 if (node < 0 || node >= T) continue;
-                uint16_t* e = reinterpret_cast<uint16_t*>(tile + col + sw128(own0 + r, unit & 7));
+                uint16_t* e = reinterpret_cast<uint16_t*>(tile + sw128(own0 + r, unit & 7));
                 for (int i = 0; i < 8; ++i)
                     if (not_finite<FP16>(e[i])) e[i] = 0, bad |= 1u << r;
             }
             bad = __reduce_or_sync(0xFFFFFFFFu, bad);
-            if (lane == 0) odd[slot_at * 4 + (warp - 5)] = (uint16_t)bad;
+            if (lane == 0) odd[slot_at * 4 + own0 / 16] = (uint16_t)bad;
         };
-        // Row and first element of a list's slot 0 in the maps' rows of a slot stride each.
-        int list_b = -1, list_h = -1, k_row = 0, k_col = 0, v_row = 0, v_col = 0;
-        auto find_list = [&](int b, int h) {
-            list_b = b, list_h = h;
-            const long long ko = b * C.kb + h * C.kh, vo = b * C.vb + h * C.vh;
-            k_row = (int)(ko / k_step), k_col = (int)(ko - (long long)k_row * k_step);
-            v_row = (int)(vo / v_step), v_col = (int)(vo - (long long)v_row * v_step);
-        };
-        // This warp's sixteen keys of a full tile: lane i issues group i / (DP / 64), half i % (DP / 64).
-        constexpr int HALVES = DP / 64;
-        auto gather = [&](int slot_at, const CUtensorMap* map, int row0, int col0, const int (&slot)[4]) {
-            uint64_t* bar = &full[slot_at];
-            if (lane == 0) mbar_arrive_expect_tx(bar, 16 * DP * 2);
-            else mbar_arrive(bar);
-            __syncwarp();
-            if (lane < 4 * HALVES) {
-                const int rows[4] = {row0 + slot[0], row0 + slot[1], row0 + slot[2], row0 + slot[3]};
-                const int half = lane % HALVES, r = own0 + lane / HALVES * 4;
-                tma_gather4(smem_u32(ring + slot_at * Cfg::kTile) + half * (KT * 128) + r * 128, map, col0 + half * 64,
-                            rows, bar);
-            }
-        };
-        // slots of the next tiles: a load a tile ahead would be waited for every tile
-        int queue[kAhead];
-#pragma unroll
-        for (int i = 0; i < kAhead; ++i) queue[i] = fetch();
         int at = 0, fill = 0;               // ring slot of the next group and how often the ring has been round
         auto take = [&]() {
             if (fill > 0) mbar_wait(&empty[at], (uint32_t)((fill - 1) & 1), P.err, kSiteAttend | kSiteEmpty);
@@ -308,35 +258,38 @@ __global__ void __launch_bounds__(kThreads, 2)
             if (++at == slots) at = 0, ++fill;
             return mine;
         };
-        for (int x = x0; x < x1; ++x) {
-            const int h = a.group / row_blocks, i0 = a.tile * KT, len = plan.len[a.b];
-            const uint16_t* kp = static_cast<const uint16_t*>(C.k) + a.b * C.kb + h * C.kh + unit * 8;
-            const uint16_t* vp = static_cast<const uint16_t*>(C.v) + a.b * C.vb + h * C.vh + unit * 8;
-            const int next = queue[0];
-#pragma unroll
-            for (int i = 0; i + 1 < kAhead; ++i) queue[i] = queue[i + 1];
-            queue[kAhead - 1] = fetch();
-            const bool ok = slot_ok(next, n_slots, P.err);
-            if (by_tma && i0 + KT <= len) {
-                if (a.b != list_b || h != list_h) find_list(a.b, h);
-                int four[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    four[e] = __shfl_sync(0xFFFFFFFFu, ok ? next : 0, (lane / HALVES * 4 + e) & 15);
-                gather(take(), &map_k, k_row, k_col, four);
-                step(plan, C.B, groups, a);
-                gather(take(), &map_v, v_row, v_col, four);
-                continue;
-            }
+        src.enter(C, plan, row_blocks);
+        fetch();
+        while (src.x < x1) {
+            const int i0 = src.at.tile * KT, len = src.len;
+            const bool cached = i0 + KT <= len, ok = slot_ok(held, n_slots, P.err);
             int slot[Cp::SWEEPS];
-            Cp::slots(ok ? next : -1, lane, slot);
+            // cached keys: nothing to leave out (a slot outside the pool has been reported; slot 0 is read)
+            Cp::slots(ok ? held : cached ? 0 : -1, lane, slot);
+            const uint16_t *kp = src.k + unit * 8, *vp = src.v + unit * 8;
+            auto copy = [&](uint32_t dst, const uint16_t* from, const uint16_t* nowhere, int step_) {
+                if (cached && whole_rows) {
+#pragma unroll
+                    for (int j = 0; j < Cp::SWEEPS; ++j)
+                        cp16(dst + sw128(own0 + Cp::row(lane, j), unit & 7), from + (long long)slot[j] * step_);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < Cp::SWEEPS; ++j) {
+                        const bool on = slot[j] >= 0 && unit_on;
+                        cp16(dst + sw128(own0 + Cp::row(lane, j), unit & 7),
+                             on ? from + (long long)slot[j] * step_ : nowhere, on);
+                    }
+                }
+            };
             const int k_at = take();
-            copy(smem_u32(ring + k_at * Cfg::kTile), kp, k_step, slot);
+            copy(ring_addr + k_at * Cfg::kTile, kp, src.k, k_step);
             arrive_landed(k_at);
-            step(plan, C.B, groups, a);
+            const uint16_t* v_nowhere = src.v;
+            if (src.next(plan, C.B, groups) && src.x < x1) src.enter(C, plan, row_blocks);
+            if (src.x < x1) fetch();
             const int v_at = take();
-            copy(smem_u32(ring + v_at * Cfg::kTile), vp, v_step, slot);
-            if (i0 + KT > len) {
+            copy(ring_addr + v_at * Cfg::kTile, vp, v_nowhere, v_step);
+            if (!cached) {
                 asm volatile("cp.async.wait_all;" ::: "memory");
                 clean(v_at, i0, len);
                 mbar_arrive(&full[v_at]);
@@ -356,7 +309,7 @@ __global__ void __launch_bounds__(kThreads, 2)
             constexpr uint32_t kCommon = (1u << 4) | kType | ((uint32_t)(kWideRows >> 4) << 24);
             constexpr uint32_t kDescS = kCommon | ((uint32_t)(KT >> 3) << 17);
             constexpr uint32_t kDescO = kCommon | (1u << 16) | ((uint32_t)(DP >> 3) << 17);  // V: d contiguous
-            const uint32_t p_addr = smem_u32(p_s);
+            const uint32_t q_addr = smem_u32(q_s);
             At a = locate(plan, C.B, x0);
             int at = 0, round = 0, lists = 0;
             bool fresh = false;              // the tile whose product with V is pending starts its list's O
@@ -370,11 +323,11 @@ __global__ void __launch_bounds__(kThreads, 2)
                 mbar_wait(&full[v_at], (uint32_t)(v_round & 1), P.err, kSiteAttend | kSiteFull);
                 fence_proxy_async_smem();
                 tc_fence_after();
-                const uint32_t v_addr = smem_u32(ring + v_at * Cfg::kTile);
+                const uint64_t v_desc = desc128(smem_u32(ring + v_at * Cfg::kTile), KT * 128);
+                const uint32_t p_col = tmem + (n & 1) * KT + Cfg::kColP;
 #pragma unroll
                 for (int k = 0; k < KT / 16; ++k)
-                    tc_mma(tmem + Cfg::kColO, desc128(p_addr + k * 32, 16), desc128(v_addr + k * 16 * 128, KT * 128), kDescO,
-                           !fresh || k > 0);
+                    tc_mma_ta(tmem + Cfg::kColO, p_col + k * 8, v_desc + (k * 16 * 128 >> 4), kDescO, !fresh || k > 0);
                 tc_commit(&empty[v_at]);
                 tc_commit(o_done);
             };
@@ -388,16 +341,18 @@ __global__ void __launch_bounds__(kThreads, 2)
                 int k_at, k_round;
                 take(k_at, k_round);
                 mbar_wait(&full[k_at], (uint32_t)(k_round & 1), P.err, kSiteAttend | kSiteFull);
-                if (n > 0) mbar_wait(s_free, (uint32_t)((n - 1) & 1), P.err, kSiteAttend | kSiteAccum);
+                // the S this tile takes was tile n - 2's (where n - 1's product is out already, that one's phase)
+                if (n > 1 || (first && n > 0))
+                    mbar_wait(o_done, (uint32_t)((first ? n - 1 : n - 2) & 1), P.err, kSiteAttend | kSiteAccum);
                 fence_proxy_async_smem();
                 tc_fence_after();
-                const uint32_t k_addr = smem_u32(ring + k_at * Cfg::kTile);
+                const uint64_t q_desc = desc128(q_addr, 16), k_desc = desc128(smem_u32(ring + k_at * Cfg::kTile), 16);
 #pragma unroll
                 for (int k = 0; k < DP / 16; ++k)
-                    tc_mma_ta(tmem, tmem + Cfg::kColQ + k * 8, desc128(k_addr + (k >> 2) * (KT * 128) + (k & 3) * 32, 16),
-                              kDescS, k > 0);
+                    tc_mma(tmem + (n & 1) * KT, q_desc + ((k >> 2) * (kWideRows * 128) + (k & 3) * 32 >> 4),
+                           k_desc + ((k >> 2) * (KT * 128) + (k & 3) * 32 >> 4), kDescS, k > 0);
                 tc_commit(&empty[k_at]);
-                tc_commit(s_full);
+                tc_commit(&s_full[n & 1]);
                 if (n > 0 && !first) pv(n - 1);
                 take(v_at, v_round);
                 fresh = first;
@@ -428,36 +383,23 @@ __global__ void __launch_bounds__(kThreads, 2)
                 // Queries: whole lines at a time (a row a lane would touch 32 lines with every load); all loads ahead
                 // of the stores, which they could not pass.
                 const long long off = real ? b * P.qb + t * P.qt + (long long)(h * G + g) * P.qh : -1;
-                // They go through the warp's 4 KB of P's place, 64 elements of a row at a time, to the lanes that
-                // own the rows, and from there to TMEM.
-                const int u = lane & 7;
-                uint4 val[DP / 64][8];
+                constexpr int UNITS = DP / 8, AT_ONCE = 32 / UNITS, LOADS = 32 / AT_ONCE;
+                const int u = lane % UNITS;
 #pragma unroll
-                for (int half = 0; half < DP / 64; ++half)
+                for (int j0 = 0; j0 < LOADS; j0 += 8) {
+                    uint4 val[8];
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
-                        const long long from = __shfl_sync(0xFFFFFFFFu, off, j * 4 + (lane >> 3));
-                        const int d = half * 64 + u * 8;
-                        val[half][j] = make_uint4(0, 0, 0, 0);
-                        if (from >= 0 && d < D)
-                            val[half][j] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(P.q) + from + d);
+                        const long long from = __shfl_sync(0xFFFFFFFFu, off, (j0 + j) * AT_ONCE + lane / UNITS);
+                        val[j] = make_uint4(0, 0, 0, 0);
+                        if (from >= 0 && u * 8 < D)
+                            val[j] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(P.q) + from + u * 8);
                     }
 #pragma unroll
-                for (int half = 0; half < DP / 64; ++half) {
-                    __syncwarp();
-#pragma unroll
                     for (int j = 0; j < 8; ++j)
-                        *reinterpret_cast<uint4*>(p_s + sw128(warp * 32 + j * 4 + (lane >> 3), u)) = val[half][j];
-                    __syncwarp();
-                    uint32_t mine[32];
-#pragma unroll
-                    for (int c = 0; c < 8; ++c)
-                        *reinterpret_cast<uint4*>(mine + c * 4) = *reinterpret_cast<const uint4*>(p_s + sw128(r, c));
-                    tmem_st32(t_s + Cfg::kColQ + half * 32, mine);
+                        *reinterpret_cast<uint4*>(q_s + (u >> 3) * (kWideRows * 128) +
+                                                  sw128(warp * 32 + (j0 + j) * AT_ONCE + lane / UNITS, u & 7)) = val[j];
                 }
-                tmem_st_wait();
-                __syncwarp();
-                tc_fence_before();
                 mbar_arrive(q_full);
             }
             const unsigned long long word = real && tot > 0 ? word_of(P.mask, T, b, t) : 0;
@@ -466,9 +408,10 @@ __global__ void __launch_bounds__(kThreads, 2)
             const int n_first = n;
             for (; x < seg_end; ++x, ++n, ++a.tile) {
                 advance();  // past the key tile
-                mbar_wait(s_full, (uint32_t)(n & 1), P.err, kSiteAttend | kSiteAccum);
+                mbar_wait(&s_full[n & 1], (uint32_t)((n >> 1) & 1), P.err, kSiteAttend | kSiteAccum);
                 __syncwarp();
                 tc_fence_after();
+                const uint32_t t_tile = t_s + (n & 1) * KT;
                 // which of the 64 keys this row sees
                 const int i0 = a.tile * KT;
                 unsigned long long vis = ~0ull;
@@ -488,7 +431,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                 float top = -INFINITY;
 #pragma unroll
                 for (int half = 0; half < 2; ++half) {
-                    tmem_ld32(t_s + half * 32, s);
+                    tmem_ld32(t_tile + half * 32, s);
                     tmem_ld_wait();
                     const unsigned in = (unsigned)(vis >> (half * 32));
                     if (__any_sync(0xFFFFFFFFu, in != 0xFFFFFFFFu)) {
@@ -507,17 +450,18 @@ __global__ void __launch_bounds__(kThreads, 2)
                     ref = top;
                     sum *= keep;
                 }
-                if (n > n_first) mbar_wait(o_done, (uint32_t)((n - 1) & 1), P.err, kSiteAttend | kSiteAccum);
                 if (__any_sync(0xFFFFFFFFu, keep != 1.0f) && n > n_first) {
+                    mbar_wait(o_done, (uint32_t)((n - 1) & 1), P.err, kSiteAttend | kSiteAccum);
+                    __syncwarp();
                     tc_fence_after();
 #pragma unroll 1
-                    for (int c = 0; c < DP; c += 32) {
-                        uint32_t o[32];
-                        tmem_ld32(t_o + c, o);
+                    for (int c = 0; c < DP; c += 16) {
+                        uint32_t o[16];
+                        tmem_ld16(t_o + c, o);
                         tmem_ld_wait();
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * keep);
-                        tmem_st32(t_o + c, o);
+                        for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * keep);
+                        tmem_st16(t_o + c, o);
                     }
                     tmem_st_wait();
                     tc_fence_before();
@@ -528,10 +472,8 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
                 for (int half = 1; half >= 0; --half) {  // the second half is still in registers
                     if (half == 0) {
-                        tmem_ld32(t_s, s);
+                        tmem_ld32(t_tile, s);
                         tmem_ld_wait();
-                        tc_fence_before();
-                        mbar_arrive(s_free);
                         const unsigned in = (unsigned)vis;
                         if (__any_sync(0xFFFFFFFFu, in != 0xFFFFFFFFu)) {
 #pragma unroll
@@ -539,21 +481,20 @@ __global__ void __launch_bounds__(kThreads, 2)
                                 if (!(in >> i & 1)) s[i] = 0xFF800000u;
                         }
                     }
+                    uint32_t w[16];
 #pragma unroll
-                    for (int u = 0; u < 4; ++u) {
-                        uint32_t w[4];
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            float p0, p1;
-                            split(mul2(add2(both(__uint_as_float(s[u * 8 + 2 * i]), __uint_as_float(s[u * 8 + 2 * i + 1])),
-                                            shift2), scale2), p0, p1);
-                            p0 = ex2(p0), p1 = ex2(p1);
-                            sum2 = add2(sum2, both(p0, p1));
-                            w[i] = pack<FP16>(p0, p1);  // rounded to the cache's type for the product with V
-                        }
-                        *reinterpret_cast<uint4*>(p_s + sw128(r, half * 4 + u)) = make_uint4(w[0], w[1], w[2], w[3]);
+                    for (int i = 0; i < 16; ++i) {
+                        float p0, p1;
+                        split(mul2(add2(both(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), shift2), scale2),
+                              p0, p1);
+                        p0 = ex2(p0), p1 = ex2(p1);
+                        sum2 = add2(sum2, both(p0, p1));
+                        w[i] = pack<FP16>(p0, p1);  // rounded to the cache's type for the product with V
                     }
+                    tmem_st16(t_tile + Cfg::kColP + half * 16, w);
                 }
+                tmem_st_wait();
+                tc_fence_before();
                 {
                     float s0, s1;
                     split(sum2, s0, s1);
@@ -575,7 +516,7 @@ __global__ void __launch_bounds__(kThreads, 2)
             const long long at = ((long long)b * T + t) * P.Hq + h * G + g;
             float* part = P.part + ((long long)blockIdx.x * 2 + (segment ? 1 : 0)) * part_floats(kWideRows, DP);
             const int32_t* list = C.table ? C.table + b * C.tb + h * C.th : nullptr;
-            uint8_t* const stage = p_s;  // P has been read; a warp's rows of it are its own 4 KB
+            uint8_t* const stage = q_s;  // Q has been read; a warp's rows of its first half are its own 4 KB
 #pragma unroll 1
             for (int c = 0; c < DP; c += 32) {
                 uint32_t o[32];
@@ -651,37 +592,6 @@ __global__ void __launch_bounds__(kThreads, 2)
 
 namespace {
 
-PFN_cuTensorMapEncodeTiled_v12000 encoder() {
-    static std::mutex mu;
-    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-    std::lock_guard<std::mutex> lk(mu);
-    if (!fn) {
-        void* p = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) == cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-    }
-    return fn;
-}
-
-// The cache's slots as rows of one slot stride each, 64 elements of a row a
-// box. False where that does not describe it: D not whole boxes (elements of
-// the next slot or head would come along), slots that overlap, row numbers
-// past int32, a head that crosses from one row into the next.
-bool slot_map(CUtensorMap* map, const KvView& C, const void* base, long long sb, long long sh, long long ss) {
-    if (C.D % 64 || ss < C.D || sb % ss || (C.Hkv - 1) * (sh % ss) + C.D > ss) return false;
-    const long long rows = ((C.B - 1) * sb + (C.Hkv - 1) * sh) / ss + C.n_slots + 1;
-    const auto encode = encoder();
-    if (rows > 0x7FFFFFFFLL || !encode) return false;
-    const cuuint64_t dims[2] = {(cuuint64_t)ss, (cuuint64_t)rows};
-    const cuuint64_t strides[1] = {(cuuint64_t)ss * 2};
-    const cuuint32_t box[2] = {64, 1}, each[2] = {1, 1};
-    return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, const_cast<void*>(base), dims, strides, box, each,
-                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 template <int DP, bool FP16>
 cudaError_t launch_dp(const AttendParams& P, int row_blocks, int parts, cudaStream_t st) {
     const auto kern = k_tree_attention_wide<DP, FP16>;
@@ -690,10 +600,7 @@ cudaError_t launch_dp(const AttendParams& P, int row_blocks, int parts, cudaStre
     // as many ring slots as leave room for two CTAs an SM (228 KB, 1 KB of each CTA's is the system's)
     int slots = kMaxSlots;
     while (slots > 3 && WideCfg<DP>::smem(P.c.B, slots) > 113 * 1024) --slots;
-    CUtensorMap map_k = {}, map_v = {};
-    const KvView& C = P.c;
-    int by_tma = slot_map(&map_k, C, C.k, C.kb, C.kh, C.ks) && slot_map(&map_v, C, C.v, C.vb, C.vh, C.vs);
-    void* args[6] = {const_cast<AttendParams*>(&P), &map_k, &map_v, &by_tma, &row_blocks, &slots};
+    void* args[3] = {const_cast<AttendParams*>(&P), &row_blocks, &slots};
     return launch(reinterpret_cast<const void*>(kern), dim3(parts, 1, 1), kThreads, WideCfg<DP>::smem(P.c.B, slots), args,
                   st);
 }

@@ -63,28 +63,50 @@ __device__ __forceinline__ uint64_t desc128(uint32_t saddr, uint32_t lead) {
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 
-__device__ __forceinline__ void tc_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate) {
+// The products are issued by one lane of a warp that runs the surrounding
+// code as a whole: what they take then lies in uniform registers. (A branch for
+// the one lane costs some ninety cycles an instruction in moves, where a
+// product takes 32 to 64.)
+__device__ __forceinline__ void tc_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate, uint32_t leader) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
+        "{\n\t.reg .pred p, q;\n\t"
         "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate)
+        "setp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate), "r"(leader)
         : "memory");
 }
 
 // The same with A in TMEM: a row a lane, two elements a column.
-__device__ __forceinline__ void tc_mma_ta(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool accumulate) {
+__device__ __forceinline__ void tc_mma_ta(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool accumulate,
+                                          uint32_t leader) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
+        "{\n\t.reg .pred p, q;\n\t"
         "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-        "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate)
+        "setp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate), "r"(leader)
         : "memory");
 }
 
-__device__ __forceinline__ void tc_commit(uint64_t* bar) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
-                 : "memory");
+__device__ __forceinline__ void tc_commit(uint64_t* bar, uint32_t leader) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\t"
+        "setp.ne.b32 q, %1, 0;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)),
+        "r"(leader)
+        : "memory");
+}
+
+// One lane of the warp: 1 there, 0 elsewhere.
+__device__ __forceinline__ uint32_t elect_lane() {
+    uint32_t one;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xFFFFFFFF;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(one));
+    return one;
 }
 
 // 32 fp32 columns of this thread's TMEM lane
@@ -304,7 +326,9 @@ __global__ void __launch_bounds__(kThreads, 2)
             mbar_drain(&full[s], (uint32_t)((groups_in - s + slots - 1) / slots - 1) & 1u);
     } else if (warp == 4) {
         // ------------------------------------------------- matrix products
-        if (lane == 0) {
+        {
+            const uint32_t leader = elect_lane();
+            const int count = __reduce_max_sync(0xFFFFFFFFu, x1 - x0);  // uniform, and known to be
             constexpr uint32_t kType = FP16 ? 0u : (1u << 7) | (1u << 10);
             constexpr uint32_t kCommon = (1u << 4) | kType | ((uint32_t)(kWideRows >> 4) << 24);
             constexpr uint32_t kDescS = kCommon | ((uint32_t)(KT >> 3) << 17);
@@ -327,11 +351,11 @@ __global__ void __launch_bounds__(kThreads, 2)
                 const uint32_t p_col = tmem + (n & 1) * KT + Cfg::kColP;
 #pragma unroll
                 for (int k = 0; k < KT / 16; ++k)
-                    tc_mma_ta(tmem + Cfg::kColO, p_col + k * 8, v_desc + (k * 16 * 128 >> 4), kDescO, !fresh || k > 0);
-                tc_commit(&empty[v_at]);
-                tc_commit(o_done);
+                    tc_mma_ta(tmem + Cfg::kColO, p_col + k * 8, v_desc + (k * 16 * 128 >> 4), kDescO, !fresh || k > 0, leader);
+                tc_commit(&empty[v_at], leader);
+                tc_commit(o_done, leader);
             };
-            for (int n = 0; n < x1 - x0; ++n) {
+            for (int n = 0; n < count; ++n) {
                 const bool first = n == 0 || a.tile == 0;
                 if (first) {
                     // the softmax warps load the next list's queries once they have the last list's O
@@ -350,15 +374,15 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
                 for (int k = 0; k < DP / 16; ++k)
                     tc_mma(tmem + (n & 1) * KT, q_desc + ((k >> 2) * (kWideRows * 128) + (k & 3) * 32 >> 4),
-                           k_desc + ((k >> 2) * (KT * 128) + (k & 3) * 32 >> 4), kDescS, k > 0);
-                tc_commit(&empty[k_at]);
-                tc_commit(&s_full[n & 1]);
+                           k_desc + ((k >> 2) * (KT * 128) + (k & 3) * 32 >> 4), kDescS, k > 0, leader);
+                tc_commit(&empty[k_at], leader);
+                tc_commit(&s_full[n & 1], leader);
                 if (n > 0 && !first) pv(n - 1);
                 take(v_at, v_round);
                 fresh = first;
                 step(plan, C.B, groups, a);
             }
-            pv(x1 - x0 - 1);
+            pv(count - 1);
         }
         __syncwarp();
     } else {

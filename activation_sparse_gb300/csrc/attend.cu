@@ -434,7 +434,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
     grid_launch_dependents();
     grid_dependency_wait();
     make_plan<kJoinWarps * 32>(C, T, groups, plan, P.err, false);
-    const Deal deal(plan.first[C.B], parts, RB == kWideRows ? kWideLeast : 1);
+    const Deal deal(plan.first[C.B], parts, RB >= 128 ? kWideLeast : 1);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int row_sets = (min(R, RB) + ROWS - 1) / ROWS;
     const int list_id = blockIdx.x / row_sets;
@@ -539,7 +539,7 @@ int row_warps(int R) { return R <= 16 ? 1 : 2; }  // more rows than 32 go in fur
 // Up to 16 rows a key: the tiles above, bound by memory. More rows: 128-row
 // tiles on the tensor memory path, whose cost a key does not depend on the
 // rows (heads of more than 128 elements do not fit there).
-bool wide_rows(int D, int R) { return R > 16 && D <= 128; }
+bool many_rows(int D, int R) { return R > 16 && D <= 128; }
 
 template <int DP, int RB, bool FP16>
 cudaError_t launch_join(const AttendParams& P, int row_blocks, int parts, cudaStream_t st) {
@@ -581,25 +581,32 @@ cudaError_t launch_attend_type(const AttendParams& P, cudaStream_t st) {
     }
 }
 
-template <int DP>
+template <int DP, int RB>
+cudaError_t launch_wide_join(const AttendParams& P, int row_blocks, int parts, cudaStream_t st) {
+    return P.c.fp16 ? launch_join<DP, RB, true>(P, row_blocks, parts, st) : launch_join<DP, RB, false>(P, row_blocks, parts, st);
+}
+
 cudaError_t launch_wide(const AttendParams& P, cudaStream_t st) {
     int row_blocks = 0, parts = 0;
     const cudaError_t e = launch_tree_attention_wide(P, &row_blocks, &parts, st);
     if (e != cudaSuccess) return e;
-    return P.c.fp16 ? launch_join<DP, kWideRows, true>(P, row_blocks, parts, st)
-                    : launch_join<DP, kWideRows, false>(P, row_blocks, parts, st);
+    if (wide_rows(P.T * P.G) == 128)
+        return P.c.D <= 64 ? launch_wide_join<64, 128>(P, row_blocks, parts, st)
+                           : launch_wide_join<128, 128>(P, row_blocks, parts, st);
+    return P.c.D <= 64 ? launch_wide_join<64, 256>(P, row_blocks, parts, st)
+                       : launch_wide_join<128, 256>(P, row_blocks, parts, st);
 }
 
 }  // namespace
 
 long long attend_partial_floats(int D, int T, int G) {
     const int dp = padded(D), R = T * G;
-    const int rows = wide_rows(D, R) ? kWideRows : 16 * row_warps(R);
-    return 2ll * sm_count() * per_sm(dp) * part_floats(rows, dp);
+    if (many_rows(D, R)) return 2ll * sm_count() * 2 * part_floats(128, dp);  // two CTAs an SM, or one with twice the rows
+    return 2ll * sm_count() * per_sm(dp) * part_floats(16 * row_warps(R), dp);
 }
 
 cudaError_t launch_tree_attention(const AttendParams& P, cudaStream_t st) {
-    if (wide_rows(P.c.D, P.T * P.G)) return P.c.D <= 64 ? launch_wide<64>(P, st) : launch_wide<128>(P, st);
+    if (many_rows(P.c.D, P.T * P.G)) return launch_wide(P, st);
     return P.c.fp16 ? launch_attend_type<true>(P, st) : launch_attend_type<false>(P, st);
 }
 

@@ -224,8 +224,9 @@ __device__ __forceinline__ bool slot_ok(int slot, int n_slots, unsigned* err) {
 // Floats of one partial: RB rows of output, then their maxima and sums.
 constexpr int part_floats(int rb, int dp) { return rb * (dp + 2); }
 
-constexpr int kWideRows = 128;     // query rows a block of the tensor-memory kernel has
-constexpr int kWideLeast = 4;      // and the tiles a part of its lists has at least
+// Query rows a CTA of the tensor-memory kernel takes, and the tiles a part of its lists has at least.
+inline int wide_rows(int R) { return R <= 128 ? 128 : 256; }
+constexpr int kWideLeast = 4;
 
 // Who copies what: a warp copies sixteen keys of every tile, lane i < 16
 // holding the slot of its key i.

@@ -1,7 +1,8 @@
 // attend_wide.cu -- tree attention for many rows a key (wide trees, shared
 // heads) on the 5th-generation tensor cores.
 //
-// A block of 128 query rows of one list meets tiles of 64 keys:
+// One or two blocks of 128 query rows of one list meet tiles of 64 keys, each
+// with products of its own:
 //   S = Q K^T   tcgen05.mma M = 128, N = 64, K = D    (accumulator in TMEM)
 //   P = exp(scale (S - m))                            (one thread a row)
 //   O += P V    tcgen05.mma M = 128, N = D, K = 64    (P and the accumulator in TMEM)
@@ -15,35 +16,45 @@
 // 1, and the sums are in 32 bits, so the output is rescaled a few times a
 // list instead of once a tile.
 //
-// Warps: 0-3 softmax and output (TMEM lanes 32 w ..), 4 issues the matrix
-// instructions, 5-8 copy keys and values through the slot table (16-byte
-// asynchronous copies into the 128-byte swizzle the tensor cores read; the
-// TMA's four-row gather moves as much an instruction but takes its operands
-// from uniform registers, some twenty instructions a gather where a copy
-// takes four, and was no faster). Two
-// CTAs share an SM, so one's softmax runs under the other's products. Every
-// write to shared memory is an ordinary one; the issuing thread's proxy fence,
-// after the barrier that announces it, lets the tensor cores see it.
-// All waits are bounded; TMEM is always released.
+// Four warps a block do its softmax and output (TMEM lanes 32 w ..), one warp
+// issues the matrix instructions, four copy keys and values through the slot
+// table (16-byte asynchronous copies into the 128-byte swizzle the tensor
+// cores read; the TMA's four-row gather moves as much an instruction but takes
+// its operands from uniform registers, some twenty instructions a gather
+// where a copy takes four, and was no faster). Copies out of L2 are what bounds
+// it, about 24 bytes a cycle and SM by either way, so more than 128 rows go
+// through one CTA an SM with two blocks, which copies a tile once; with one
+// block two CTAs share the SM. Every write to shared memory is an ordinary
+// one; the issuing warp's proxy fence, after the barrier that announces it,
+// lets the tensor cores see it. All waits are bounded; TMEM is always released.
 #include "attend.cuh"
 
 namespace si {
 
 namespace {
 
-constexpr int kThreads = 9 * 32;
-constexpr int kSoftmaxThreads = 128, kCopyThreads = 128;
-constexpr int kMaxSlots = 5;       // ring slots: a key or a value tile each
+constexpr int kBlock = 128;        // query rows of one product: a TMEM lane each
+constexpr int kCopyWarps = 4, kCopyThreads = 32 * kCopyWarps;
 
-template <int DP>
+// NB row blocks a CTA meet every key tile it copies.
+template <int DP, int NB>
 struct WideCfg {
+    static constexpr int kRows = kBlock * NB;
+    static constexpr int kSoftmaxWarps = 4 * NB;
+    static constexpr int kMmaWarp = kSoftmaxWarps, kCopyWarp = kMmaWarp + 1;
+    static constexpr int kThreads = 32 * (kCopyWarp + kCopyWarps);
+    static constexpr int kCtas = NB == 1 ? 2 : 1;              // an SM
+    static constexpr int kMaxSlots = NB == 1 ? 5 : 9;          // ring slots: a key or a value tile each
     static constexpr int kTile = KT * DP * 2;
-    static constexpr int kOffRing = kWideRows * DP * 2;        // after Q
-    static constexpr int kColP = KT / 2, kColO = 2 * KT;       // TMEM columns: two S (P in the second half), O
-    static constexpr int kTmemCols = 256;
-    static constexpr int kBars = 2 * kMaxSlots + 5;
-    static constexpr int fixed(int B) { return (kBars + 1) * 8 + kMaxSlots * 8 + 16 + (3 * B + 1) * 4; }
+    static constexpr int kQ = kBlock * DP * 2;                 // of one block
+    static constexpr int kOffRing = NB * kQ;
+    static constexpr int kColP = KT / 2, kColO = 2 * KT;       // TMEM columns of a block: two S (P in the second half), O
+    static constexpr int kCols = kColO + DP;
+    static constexpr int kTmemCols = NB * kCols <= 256 ? 256 : 512;
+    static constexpr int kBars = 2 * kMaxSlots + 5 * NB;
+    static constexpr int fixed(int B) { return (kBars + 1) * 8 + (kMaxSlots + 1) * 8 + 16 + (3 * B + 1) * 4; }
     static constexpr int smem(int B, int slots) { return kOffRing + slots * kTile + fixed(B); }
+    static constexpr int kSmemLimit = NB == 1 ? 113 * 1024 : 227 * 1024;  // of the SM's 228 KB, 1 KB a CTA is the system's
 };
 
 // 128-byte swizzled tile of rows of 64 elements: byte offset of 16-byte unit
@@ -175,20 +186,21 @@ __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.
 
 }  // namespace
 
-template <int DP, bool FP16>
-__global__ void __launch_bounds__(kThreads, 2)
+template <int DP, int NB, bool FP16>
+__global__ void __launch_bounds__(WideCfg<DP, NB>::kThreads, WideCfg<DP, NB>::kCtas)
     k_tree_attention_wide(const __grid_constant__ AttendParams P, int row_blocks, int slots) {
-    using Cfg = WideCfg<DP>;
+    using Cfg = WideCfg<DP, NB>;
+    constexpr int kThreads = Cfg::kThreads, kMaxSlots = Cfg::kMaxSlots;
     using Cp = Copy<DP>;
     extern __shared__ __align__(1024) uint8_t smem[];  // the swizzle needs tiles on 1024-byte boundaries
     uint8_t* const q_s = smem;
     uint8_t* const ring = smem + Cfg::kOffRing;
     uint64_t* const full = reinterpret_cast<uint64_t*>(ring + slots * Cfg::kTile);
     uint64_t* const empty = full + kMaxSlots;
-    uint64_t* const q_full = empty + kMaxSlots;  // this list's queries are in shared memory
-    uint64_t* const s_full = q_full + 1;         // [2] S of a tile is in TMEM
-    uint64_t* const p_full = q_full + 3;         // P of a tile is in TMEM
-    uint64_t* const o_done = q_full + 4;         // O includes the tile; its S and P are free
+    uint64_t* const q_full = empty + kMaxSlots;  // [block] this list's queries are in shared memory
+    uint64_t* const s_full = q_full + NB;        // [block][2] S of a tile is in TMEM
+    uint64_t* const p_full = s_full + 2 * NB;    // [block] P of a tile is in TMEM
+    uint64_t* const o_done = p_full + NB;        // [block] O includes the tile; its S and P are free
     uint16_t* const odd = reinterpret_cast<uint16_t*>(full + Cfg::kBars + 1);  // [slot][4]: keys of a value tile that are not finite
     uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(odd + kMaxSlots * 4);
     Plan plan;
@@ -210,14 +222,16 @@ __global__ void __launch_bounds__(kThreads, 2)
             mbar_init(&full[s], kCopyThreads);
             mbar_init(&empty[s], 1);
         }
-        mbar_init(q_full, kSoftmaxThreads);
-        mbar_init(&s_full[0], 1);
-        mbar_init(&s_full[1], 1);
-        mbar_init(p_full, kSoftmaxThreads);
-        mbar_init(o_done, 1);
+        for (int k = 0; k < NB; ++k) {
+            mbar_init(&q_full[k], kBlock);
+            mbar_init(&s_full[2 * k], 1);
+            mbar_init(&s_full[2 * k + 1], 1);
+            mbar_init(&p_full[k], kBlock);
+            mbar_init(&o_done[k], 1);
+        }
         fence_mbar_init();
     }
-    if (warp == 4) {
+    if (warp == Cfg::kMmaWarp) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
                      "r"(Cfg::kTmemCols)
                      : "memory");
@@ -234,9 +248,9 @@ __global__ void __launch_bounds__(kThreads, 2)
 
     if (x0 >= x1) {
         // more CTAs than tiles: nothing to do
-    } else if (warp >= 5) {
+    } else if (warp >= Cfg::kCopyWarp) {
         // ---------------------------------------------------------- copies
-        const int own0 = (warp - 5) * 16, unit = lane % Cp::UNITS;
+        const int own0 = (warp - Cfg::kCopyWarp) * 16, unit = lane % Cp::UNITS;
         const bool unit_on = unit * 8 < D, whole_rows = D == DP;
         const int n_slots = (int)C.n_slots, k_step = (int)C.ks, v_step = (int)C.vs;
         const uint32_t ring_addr = smem_u32(ring) + (uint32_t)(unit >> 3) * (KT * 128);  // this lane's sub-tile
@@ -324,13 +338,13 @@ __global__ void __launch_bounds__(kThreads, 2)
         const int groups_in = 2 * (x1 - x0);
         for (int s = 0; s < slots && s < groups_in; ++s)
             mbar_drain(&full[s], (uint32_t)((groups_in - s + slots - 1) / slots - 1) & 1u);
-    } else if (warp == 4) {
+    } else if (warp == Cfg::kMmaWarp) {
         // ------------------------------------------------- matrix products
         {
             const uint32_t leader = elect_lane();
             const int count = __reduce_max_sync(0xFFFFFFFFu, x1 - x0);  // uniform, and known to be
             constexpr uint32_t kType = FP16 ? 0u : (1u << 7) | (1u << 10);
-            constexpr uint32_t kCommon = (1u << 4) | kType | ((uint32_t)(kWideRows >> 4) << 24);
+            constexpr uint32_t kCommon = (1u << 4) | kType | ((uint32_t)(kBlock >> 4) << 24);
             constexpr uint32_t kDescS = kCommon | ((uint32_t)(KT >> 3) << 17);
             constexpr uint32_t kDescO = kCommon | (1u << 16) | ((uint32_t)(DP >> 3) << 17);  // V: d contiguous
             const uint32_t q_addr = smem_u32(q_s);
@@ -343,40 +357,46 @@ __global__ void __launch_bounds__(kThreads, 2)
                 if (++at == slots) at = 0, ++round;
             };
             auto pv = [&](int n) {
-                mbar_wait(p_full, (uint32_t)(n & 1), P.err, kSiteAttend | kSiteAccum);
                 mbar_wait(&full[v_at], (uint32_t)(v_round & 1), P.err, kSiteAttend | kSiteFull);
-                fence_proxy_async_smem();
-                tc_fence_after();
                 const uint64_t v_desc = desc128(smem_u32(ring + v_at * Cfg::kTile), KT * 128);
-                const uint32_t p_col = tmem + (n & 1) * KT + Cfg::kColP;
 #pragma unroll
-                for (int k = 0; k < KT / 16; ++k)
-                    tc_mma_ta(tmem + Cfg::kColO, p_col + k * 8, v_desc + (k * 16 * 128 >> 4), kDescO, !fresh || k > 0, leader);
+                for (int k = 0; k < NB; ++k) {
+                    mbar_wait(&p_full[k], (uint32_t)(n & 1), P.err, kSiteAttend | kSiteAccum);
+                    if (k == 0) fence_proxy_async_smem();
+                    tc_fence_after();
+                    const uint32_t block = tmem + k * Cfg::kCols, p_col = block + (n & 1) * KT + Cfg::kColP;
+#pragma unroll
+                    for (int i = 0; i < KT / 16; ++i)
+                        tc_mma_ta(block + Cfg::kColO, p_col + i * 8, v_desc + (i * 16 * 128 >> 4), kDescO,
+                                  !fresh || i > 0, leader);
+                    tc_commit(&o_done[k], leader);
+                }
                 tc_commit(&empty[v_at], leader);
-                tc_commit(o_done, leader);
             };
             for (int n = 0; n < count; ++n) {
                 const bool first = n == 0 || a.tile == 0;
-                if (first) {
-                    // the softmax warps load the next list's queries once they have the last list's O
-                    if (n > 0) pv(n - 1);
-                    mbar_wait(q_full, (uint32_t)(lists++ & 1), P.err, kSiteAttend | kSiteFull);
-                }
+                if (first && n > 0) pv(n - 1);  // the softmax warps load the next list's queries once they have the last one's O
                 int k_at, k_round;
                 take(k_at, k_round);
                 mbar_wait(&full[k_at], (uint32_t)(k_round & 1), P.err, kSiteAttend | kSiteFull);
-                // the S this tile takes was tile n - 2's (where n - 1's product is out already, that one's phase)
-                if (n > 1 || (first && n > 0))
-                    mbar_wait(o_done, (uint32_t)((first ? n - 1 : n - 2) & 1), P.err, kSiteAttend | kSiteAccum);
-                fence_proxy_async_smem();
-                tc_fence_after();
-                const uint64_t q_desc = desc128(q_addr, 16), k_desc = desc128(smem_u32(ring + k_at * Cfg::kTile), 16);
+                const uint64_t k_desc = desc128(smem_u32(ring + k_at * Cfg::kTile), 16);
 #pragma unroll
-                for (int k = 0; k < DP / 16; ++k)
-                    tc_mma(tmem + (n & 1) * KT, q_desc + ((k >> 2) * (kWideRows * 128) + (k & 3) * 32 >> 4),
-                           k_desc + ((k >> 2) * (KT * 128) + (k & 3) * 32 >> 4), kDescS, k > 0, leader);
+                for (int k = 0; k < NB; ++k) {
+                    if (first) mbar_wait(&q_full[k], (uint32_t)(lists & 1), P.err, kSiteAttend | kSiteFull);
+                    // the S this tile takes was tile n - 2's (where n - 1's product is out already, that one's phase)
+                    if (n > 1 || (first && n > 0))
+                        mbar_wait(&o_done[k], (uint32_t)((first ? n - 1 : n - 2) & 1), P.err, kSiteAttend | kSiteAccum);
+                    if (k == 0 || first) fence_proxy_async_smem();
+                    tc_fence_after();
+                    const uint64_t q_desc = desc128(q_addr + k * Cfg::kQ, 16);
+#pragma unroll
+                    for (int i = 0; i < DP / 16; ++i)
+                        tc_mma(tmem + k * Cfg::kCols + (n & 1) * KT, q_desc + ((i >> 2) * (kBlock * 128) + (i & 3) * 32 >> 4),
+                               k_desc + ((i >> 2) * (KT * 128) + (i & 3) * 32 >> 4), kDescS, i > 0, leader);
+                    tc_commit(&s_full[2 * k + (n & 1)], leader);
+                }
                 tc_commit(&empty[k_at], leader);
-                tc_commit(&s_full[n & 1], leader);
+                if (first) ++lists;
                 if (n > 0 && !first) pv(n - 1);
                 take(v_at, v_round);
                 fresh = first;
@@ -388,8 +408,10 @@ __global__ void __launch_bounds__(kThreads, 2)
     } else {
         // --------------------------------------------- softmax and output
         const float c2 = P.scale * kLog2e;
-        const uint32_t t_s = tmem + ((uint32_t)(warp * 32) << 16), t_o = t_s + Cfg::kColO;
-        const int r = warp * 32 + lane;  // this thread's row of the block
+        const int block = warp >> 2, quarter = warp & 3;
+        const uint32_t t_s = tmem + ((uint32_t)(quarter * 32) << 16) + block * Cfg::kCols, t_o = t_s + Cfg::kColO;
+        const int r = warp * 32 + lane;  // this thread's row of the blocks
+        uint8_t* const my_q = q_s + block * Cfg::kQ;
         At a = locate(plan, C.B, x0);
         int n = 0, segment = 0, v_at = 0, v_round = 0;  // ring position of the value tile of tile n
         auto advance = [&]() {
@@ -400,7 +422,7 @@ __global__ void __launch_bounds__(kThreads, 2)
             const int len = plan.len[b], tot = plan.tot[b];
             const int seg_end = min(x1, x + a.ntile - a.tile);
             const bool whole = a.tile == 0 && seg_end - x == a.ntile;
-            const int row = rb * kWideRows + r;
+            const int row = rb * Cfg::kRows + r;
             const int t = row / G, g = row - t * G;
             const bool real = row < R;
             {
@@ -421,10 +443,10 @@ __global__ void __launch_bounds__(kThreads, 2)
                     }
 #pragma unroll
                     for (int j = 0; j < 8; ++j)
-                        *reinterpret_cast<uint4*>(q_s + (u >> 3) * (kWideRows * 128) +
-                                                  sw128(warp * 32 + (j0 + j) * AT_ONCE + lane / UNITS, u & 7)) = val[j];
+                        *reinterpret_cast<uint4*>(my_q + (u >> 3) * (kBlock * 128) +
+                                                  sw128(quarter * 32 + (j0 + j) * AT_ONCE + lane / UNITS, u & 7)) = val[j];
                 }
-                mbar_arrive(q_full);
+                mbar_arrive(&q_full[block]);
             }
             const unsigned long long word = real && tot > 0 ? word_of(P.mask, T, b, t) : 0;
             float ref = -INFINITY, sum = 0.0f;
@@ -432,7 +454,7 @@ __global__ void __launch_bounds__(kThreads, 2)
             const int n_first = n;
             for (; x < seg_end; ++x, ++n, ++a.tile) {
                 advance();  // past the key tile
-                mbar_wait(&s_full[n & 1], (uint32_t)((n >> 1) & 1), P.err, kSiteAttend | kSiteAccum);
+                mbar_wait(&s_full[2 * block + (n & 1)], (uint32_t)((n >> 1) & 1), P.err, kSiteAttend | kSiteAccum);
                 __syncwarp();
                 tc_fence_after();
                 const uint32_t t_tile = t_s + (n & 1) * KT;
@@ -475,7 +497,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                     sum *= keep;
                 }
                 if (__any_sync(0xFFFFFFFFu, keep != 1.0f) && n > n_first) {
-                    mbar_wait(o_done, (uint32_t)((n - 1) & 1), P.err, kSiteAttend | kSiteAccum);
+                    mbar_wait(&o_done[block], (uint32_t)((n - 1) & 1), P.err, kSiteAttend | kSiteAccum);
                     __syncwarp();
                     tc_fence_after();
 #pragma unroll 1
@@ -524,7 +546,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                     split(sum2, s0, s1);
                     sum += s0 + s1;
                 }
-                mbar_arrive(p_full);
+                mbar_arrive(&p_full[block]);
                 advance();  // past the value tile
             }
             if (a.tile == a.ntile) {
@@ -532,15 +554,15 @@ __global__ void __launch_bounds__(kThreads, 2)
                 step(plan, C.B, groups, a);
             }
             // the list's O, or this CTA's part of it
-            mbar_wait(o_done, (uint32_t)((n - 1) & 1), P.err, kSiteAttend | kSiteAccum);
+            mbar_wait(&o_done[block], (uint32_t)((n - 1) & 1), P.err, kSiteAttend | kSiteAccum);
             __syncwarp();
             tc_fence_after();
             const bool empty_row = word == 0 || sum == 0.0f;
             const float inv = !whole ? 1.0f : empty_row ? 0.0f : 1.0f / sum;
             const long long at = ((long long)b * T + t) * P.Hq + h * G + g;
-            float* part = P.part + ((long long)blockIdx.x * 2 + (segment ? 1 : 0)) * part_floats(kWideRows, DP);
+            float* part = P.part + ((long long)blockIdx.x * 2 + (segment ? 1 : 0)) * part_floats(Cfg::kRows, DP);
             const int32_t* list = C.table ? C.table + b * C.tb + h * C.th : nullptr;
-            uint8_t* const stage = q_s;  // Q has been read; a warp's rows of its first half are its own 4 KB
+            uint8_t* const stage = my_q + quarter * 4096;  // Q has been read; a warp's rows of its first half are its own 4 KB
 #pragma unroll 1
             for (int c = 0; c < DP; c += 32) {
                 uint32_t o[32];
@@ -566,7 +588,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                             w[e] = empty_row ? 0u
                                              : pack<FP16>(__uint_as_float(o[i + 2 * e]) * inv,
                                                           __uint_as_float(o[i + 2 * e + 1]) * inv);
-                        *reinterpret_cast<uint4*>(stage + sw128(r, i / 8)) = make_uint4(w[0], w[1], w[2], w[3]);
+                        *reinterpret_cast<uint4*>(stage + sw128(lane, i / 8)) = make_uint4(w[0], w[1], w[2], w[3]);
                     }
                     __syncwarp();
                     const int u = lane & 3;
@@ -574,21 +596,21 @@ __global__ void __launch_bounds__(kThreads, 2)
                     for (int j = 0; j < 4; ++j) {
                         const int rr = j * 8 + (lane >> 2);
                         const long long to = __shfl_sync(0xFFFFFFFFu, real ? at : -1ll, rr);
-                        const uint4 v = *reinterpret_cast<const uint4*>(stage + sw128(warp * 32 + rr, u));
+                        const uint4 v = *reinterpret_cast<const uint4*>(stage + sw128(rr, u));
                         if (to >= 0 && c + u * 8 < D)
                             *reinterpret_cast<uint4*>(static_cast<uint16_t*>(P.out) + to * D + c + u * 8) = v;
                     }
                 } else {
 #pragma unroll
                     for (int i = 0; i < 32; i += 4)
-                        *reinterpret_cast<uint4*>(stage + sw128(r, i / 4)) = make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+                        *reinterpret_cast<uint4*>(stage + sw128(lane, i / 4)) = make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
                     __syncwarp();
                     const int u = lane & 7;
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
-                        const int rr = warp * 32 + j * 4 + (lane >> 3);
-                        if (rb * kWideRows + rr < R)
-                            *reinterpret_cast<uint4*>(part + rr * DP + c + u * 4) =
+                        const int rr = j * 4 + (lane >> 3);
+                        if (rb * Cfg::kRows + warp * 32 + rr < R)
+                            *reinterpret_cast<uint4*>(part + (warp * 32 + rr) * DP + c + u * 4) =
                                 *reinterpret_cast<const uint4*>(stage + sw128(rr, u));
                     }
                 }
@@ -597,8 +619,8 @@ __global__ void __launch_bounds__(kThreads, 2)
             tc_fence_before();
             if (real) {
                 if (!whole) {
-                    part[kWideRows * DP + r] = ref;
-                    part[kWideRows * DP + kWideRows + r] = sum;
+                    part[Cfg::kRows * DP + r] = ref;
+                    part[Cfg::kRows * DP + Cfg::kRows + r] = sum;
                 } else if (P.lse) {
                     P.lse[at] = empty_row ? -INFINITY : fmaf(ref, P.scale, logf(sum));
                 }
@@ -606,7 +628,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         }
     }
     __syncthreads();
-    if (warp == 4) {
+    if (warp == Cfg::kMmaWarp) {
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(Cfg::kTmemCols) : "memory");
     }
@@ -616,28 +638,36 @@ __global__ void __launch_bounds__(kThreads, 2)
 
 namespace {
 
-template <int DP, bool FP16>
-cudaError_t launch_dp(const AttendParams& P, int row_blocks, int parts, cudaStream_t st) {
-    const auto kern = k_tree_attention_wide<DP, FP16>;
-    cudaError_t e = allow_max_smem(kern);
+template <int DP, int NB, bool FP16>
+cudaError_t launch_wide(const AttendParams& P, int row_blocks, int parts, cudaStream_t st) {
+    using Cfg = WideCfg<DP, NB>;
+    const auto kern = k_tree_attention_wide<DP, NB, FP16>;
+    const cudaError_t e = allow_max_smem(kern);
     if (e != cudaSuccess) return e;
-    // as many ring slots as leave room for two CTAs an SM (228 KB, 1 KB of each CTA's is the system's)
-    int slots = kMaxSlots;
-    while (slots > 3 && WideCfg<DP>::smem(P.c.B, slots) > 113 * 1024) --slots;
+    int slots = Cfg::kMaxSlots;
+    while (slots > 3 && Cfg::smem(P.c.B, slots) > Cfg::kSmemLimit) --slots;
     void* args[3] = {const_cast<AttendParams*>(&P), &row_blocks, &slots};
-    return launch(reinterpret_cast<const void*>(kern), dim3(parts, 1, 1), kThreads, WideCfg<DP>::smem(P.c.B, slots), args,
-                  st);
+    return launch(reinterpret_cast<const void*>(kern), dim3(parts, 1, 1), Cfg::kThreads, Cfg::smem(P.c.B, slots), args, st);
+}
+
+template <int DP, bool FP16>
+cudaError_t launch_rows(const AttendParams& P, int rows, int row_blocks, int parts, cudaStream_t st) {
+    return rows == kBlock ? launch_wide<DP, 1, FP16>(P, row_blocks, parts, st)
+                          : launch_wide<DP, 2, FP16>(P, row_blocks, parts, st);
 }
 
 }  // namespace
 
 cudaError_t launch_tree_attention_wide(const AttendParams& P, int* row_blocks, int* parts, cudaStream_t st) {
-    *row_blocks = (P.T * P.G + kWideRows - 1) / kWideRows;
-    *parts = 2 * sm_count();
+    const int rows = wide_rows(P.T * P.G);
+    *row_blocks = (P.T * P.G + rows - 1) / rows;
+    *parts = sm_count() * (rows == kBlock ? 2 : 1);
     if (*parts < 1) return cudaErrorInvalidDevice;
     if (P.c.D <= 64)
-        return P.c.fp16 ? launch_dp<64, true>(P, *row_blocks, *parts, st) : launch_dp<64, false>(P, *row_blocks, *parts, st);
-    return P.c.fp16 ? launch_dp<128, true>(P, *row_blocks, *parts, st) : launch_dp<128, false>(P, *row_blocks, *parts, st);
+        return P.c.fp16 ? launch_rows<64, true>(P, rows, *row_blocks, *parts, st)
+                        : launch_rows<64, false>(P, rows, *row_blocks, *parts, st);
+    return P.c.fp16 ? launch_rows<128, true>(P, rows, *row_blocks, *parts, st)
+                    : launch_rows<128, false>(P, rows, *row_blocks, *parts, st);
 }
 
 }  // namespace si

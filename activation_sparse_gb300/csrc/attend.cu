@@ -30,7 +30,7 @@ struct AttendCfg {
     static constexpr int kOffQ = kStages * 2 * kTile;
     static constexpr int kOffPlan = kOffQ + kQBytes;
     static constexpr int kOffOdd = kOffPlan;              // new nodes whose value row is not finite (a word)
-    static constexpr int smem(int B) { return kOffPlan + 16 + (3 * B + 1) * 4; }
+    static constexpr int smem(int B) { return kOffPlan + 16 + Plan::words(B) * 4; }
 };
 
 template <int THREADS>
@@ -59,10 +59,7 @@ __global__ void __launch_bounds__(kThreads, AttendCfg<DP>::kCtas)
     extern __shared__ __align__(128) uint8_t smem[];
     uint8_t* const tiles = smem;
     uint8_t* const q_s = smem + Cfg::kOffQ;
-    Plan plan;
-    plan.len = reinterpret_cast<int*>(smem + Cfg::kOffPlan + 16);
-    plan.tot = plan.len + P.c.B;
-    plan.first = plan.tot + P.c.B;
+    const Plan plan(reinterpret_cast<int*>(smem + Cfg::kOffPlan + 16), P.c.B);
     unsigned long long* odd_s = reinterpret_cast<unsigned long long*>(smem + Cfg::kOffOdd);
 
     const KvView& C = P.c;
@@ -73,9 +70,11 @@ __global__ void __launch_bounds__(kThreads, AttendCfg<DP>::kCtas)
 
     grid_launch_dependents();
     grid_dependency_wait();
-    make_plan<kThreads>(C, T, groups, plan, P.err, blockIdx.x == 0);
-    const Deal deal(plan.first[C.B], gridDim.x, 1);
-    const int x0 = deal.start(blockIdx.x), x1 = deal.start(blockIdx.x + 1);
+    make_plan<kThreads, kNarrowLeast, kNarrowPiece>(C, T, groups, gridDim.x, plan, P.err, blockIdx.x == 0);
+    if (blockIdx.x == 0 && tid == 0) *P.cut = *plan.cut;
+    const Deal deal(plan, C.B, gridDim.x, kNarrowLeast);
+    int x0, x1;
+    deal.range(blockIdx.x, x0, x1);
     if (x0 >= x1) return;
 
     const float c2 = P.scale * kLog2e;
@@ -425,33 +424,29 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
     __shared__ float sum_s[kJoinWarps], top_s[kJoinWarps];
     extern __shared__ __align__(128) uint8_t smem[];
     const KvView& C = P.c;
-    Plan plan;
-    plan.len = reinterpret_cast<int*>(smem);
-    plan.tot = plan.len + C.B;
-    plan.first = plan.tot + C.B;
+    const Plan plan(reinterpret_cast<int*>(smem), P.c.B);
     const int T = P.T, G = P.G, R = T * G, D = C.D;
     const int groups = C.Hkv * row_blocks;
     grid_launch_dependents();
     grid_dependency_wait();
-    make_plan<kJoinWarps * 32>(C, T, groups, plan, P.err, false);
-    const Deal deal(plan.first[C.B], parts, RB >= 128 ? kWideLeast : 1);
+    constexpr int LEAST = RB >= 128 ? kWideLeast : kNarrowLeast, PIECE = RB >= 128 ? kWidePiece : kNarrowPiece;
+    make_plan<kJoinWarps * 32, LEAST, PIECE>(C, T, groups, parts, plan, P.err, false, P.cut);
+    const Deal deal(plan, C.B, parts, LEAST);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int row_sets = (min(R, RB) + ROWS - 1) / ROWS;
     const int list_id = blockIdx.x / row_sets;
     const int b = list_id / groups, group = list_id % groups;
     const int r = blockIdx.x % row_sets * ROWS + warp / JW;
     const int h = group / row_blocks, row = group % row_blocks * RB + r;
-    const int n = tiles_of(plan.tot[b]);
-    const int y0 = plan.first[b] + group * n;  // this list's tiles: y0 .. y0 + n - 1
-    const int first = deal.owner(y0), last = deal.owner(y0 + n - 1);
+    int first, last;
+    bool behind;  // only the first part can follow another list in its CTA
+    deal.ctas_of(b, group, first, last, behind);
     if (first == last) return;  // finished by its CTA
     const bool on = row < R && r < RB;
     const float c2 = P.scale * kLog2e;
     const int w = warp % JW;
-    // only the first part can follow another list in its CTA
     auto part_of = [&](int c) {
-        const int second = c == first && deal.start(c) < y0;
-        return P.part + ((long long)c * 2 + second) * part_floats(RB, DP);
+        return P.part + ((long long)c * 2 + (c == first && behind)) * part_floats(RB, DP);
     };
     // Four parts at a time, maxima, sums and rows together: one trip to memory each.
     float top = -INFINITY, sum = 0.0f, acc[E] = {};
@@ -552,7 +547,7 @@ cudaError_t launch_join(const AttendParams& P, int row_blocks, int parts, cudaSt
     if (blocks > 0x7FFFFFFFLL) return cudaErrorInvalidValue;
     const void* join = many ? reinterpret_cast<const void*>(&k_tree_attention_join<DP, RB, kJoinWarps, FP16>)
                             : reinterpret_cast<const void*>(&k_tree_attention_join<DP, RB, 1, FP16>);
-    return launch(join, dim3((unsigned)blocks, 1, 1), kJoinWarps * 32, (3 * P.c.B + 1) * 4, args, st);
+    return launch(join, dim3((unsigned)blocks, 1, 1), kJoinWarps * 32, Plan::words(P.c.B) * 4, args, st);
 }
 
 template <int DP, int MW, bool FP16>
@@ -599,6 +594,7 @@ cudaError_t launch_wide(const AttendParams& P, cudaStream_t st) {
 
 }  // namespace
 
+// Partial rows of every CTA (two pieces of lists each).
 long long attend_partial_floats(int D, int T, int G) {
     const int dp = padded(D), R = T * G;
     if (many_rows(D, R)) return 2ll * sm_count() * 2 * part_floats(128, dp);  // two CTAs an SM, or one with twice the rows

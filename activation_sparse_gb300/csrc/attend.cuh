@@ -101,18 +101,34 @@ __device__ __forceinline__ uint32_t tile_at(int row, int unit) {
 // --------------------------------------------------------------- schedule
 
 // The lists of one launch: `groups` lists a sequence (cache heads x row
-// blocks), each of ntile(b) tiles.
+// blocks), each of tiles_of(tot[b]) tiles, in flat order.
 struct Plan {
     int* len;         // [B] live keys (0 where the sequence is out of bounds)
     int* tot;         // [B] live keys + new nodes (0 likewise)
     int* first;       // [B + 1] flat index of the sequence's first tile
+    int* part;        // [B + 1] first part of the sequence, where lists are cut by themselves
+    int* cut;         // [1] tiles a part has at most there; 0: CTAs' shares run across lists
+
+    static constexpr int words(int B) { return 4 * B + 3; }
+    __device__ __forceinline__ Plan(int* at, int B)
+        : len(at), tot(at + B), first(at + 2 * B), part(at + 3 * B + 1), cut(at + 4 * B + 2) {}
 };
 
 __device__ __forceinline__ int tiles_of(int tot) { return tot > KT ? (tot + KT - 1) / KT : 1; }
 
-// Fills the plan (all threads; ends with a barrier). Lengths are read once.
-template <int THREADS>
-__device__ void make_plan(const KvView& C, int T, int groups, const Plan& p, unsigned* err, bool report) {
+// Fills the plan for `ctas` CTAs (all threads; ends with a barrier). Lengths
+// are read once.
+//
+// A list is cut into parts, one CTA each, or the CTAs' shares run across the
+// lists' ends. Running across balances any set of lists, but a CTA then
+// finishes two lists, and every piece of a list costs it about PIECE tiles'
+// time (queries in, partial rows out). So lists are cut by themselves where
+// the longest part and one piece take less than an even share and two. A part
+// has at least LEAST tiles. `known`: where an earlier launch left its *cut.
+template <int THREADS, int LEAST, int PIECE>
+__device__ void make_plan(const KvView& C, int T, int groups, int ctas, const Plan& p, unsigned* err, bool report,
+                          const int* known = nullptr) {
+    const int cut = known ? *known : -1;
     for (int b = threadIdx.x; b < C.B; b += THREADS) {
         const int len = C.len[b];
         const bool ok = len >= 0 && len <= C.cap - T;
@@ -122,42 +138,103 @@ __device__ void make_plan(const KvView& C, int T, int groups, const Plan& p, uns
     }
     __syncthreads();
     if (threadIdx.x < 32) {
-        int base = 0;
-        for (int b0 = 0; b0 < C.B; b0 += 32) {
-            const int b = b0 + (int)threadIdx.x;
-            const int mine = b < C.B ? tiles_of(p.tot[b]) * groups : 0;
-            int incl = mine;
+        const int lane = threadIdx.x;
+        // out[b]: sum of value(n tiles) * groups over the sequences before b
+        auto scan = [&](int* out, auto value) {
+            int base = 0;
+            for (int b0 = 0; b0 < C.B; b0 += 32) {
+                const int b = b0 + lane;
+                const int mine = b < C.B ? value(tiles_of(p.tot[b])) * groups : 0;
+                int incl = mine;
 #pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int v = __shfl_up_sync(0xFFFFFFFFu, incl, o);
-                if ((int)threadIdx.x >= o) incl += v;
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int v = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+                    if (lane >= o) incl += v;
+                }
+                if (b < C.B) out[b] = base + incl - mine;
+                base += __shfl_sync(0xFFFFFFFFu, incl, 31);
             }
-            if (b < C.B) p.first[b] = base + incl - mine;
-            base += __shfl_sync(0xFFFFFFFFu, incl, 31);
+            if (lane == 0) out[C.B] = base;
+            return base;
+        };
+        const int total = scan(p.first, [](int n) { return n; });
+        int q = max(cut, 0);
+        if (PIECE > 0 && cut < 0 && C.B * groups <= ctas) {
+            // the least number of tiles a part, from the even share up, that needs no more than ctas parts
+            const int even = max(LEAST, (total + ctas - 1) / ctas);
+            if (C.B == 1) {
+                const int m = ctas / groups, n = tiles_of(p.tot[0]);
+                q = max(even, (n + m - 1) / m);
+                if (q > even + PIECE) q = 0;
+            } else {
+                int parts = 0;  // lane i tries even + i
+                for (int b = 0; b < C.B; ++b) parts += (tiles_of(p.tot[b]) + even + lane - 1) / (even + lane);
+                const unsigned fits = __ballot_sync(0xFFFFFFFFu, lane <= PIECE && parts * groups <= ctas);
+                if (fits) q = even + __ffs(fits) - 1;
+            }
         }
-        if (threadIdx.x == 0) p.first[C.B] = base;
+        if (q) scan(p.part, [q](int n) { return (n + q - 1) / q; });
+        if (lane == 0) *p.cut = q;
     }
     __syncthreads();
 }
 
-// The tiles are dealt out in parts of n / parts or one more; the first n %
-// parts CTAs have the longer ones. Few tiles go to fewer CTAs (at least
-// `least` each: a part costs its start and its join whatever it holds). All in
-// 32 bits: these run once per part of every list when rows are joined.
+// Which tiles a CTA has, and which CTAs a list has. All in 32 bits: this runs
+// for every row that is joined.
 struct Deal {
-    unsigned base, rem;
-    __device__ __forceinline__ Deal(int total, int ctas, int least) {
-        const unsigned parts = max(1u, min((unsigned)ctas, (unsigned)total / (unsigned)least));
-        base = (unsigned)total / parts;
-        rem = (unsigned)total - base * parts;
-        end = total;
+    const Plan& p;
+    int B, q, end;
+    unsigned base, rem;  // shares across lists: rem CTAs of base + 1 tiles, then base each
+
+    __device__ __forceinline__ Deal(const Plan& plan, int seqs, int ctas, int least) : p(plan), B(seqs) {
+        q = *plan.cut;
+        end = plan.first[seqs];
+        const unsigned n = max(1u, min((unsigned)ctas, (unsigned)end / (unsigned)least));
+        base = (unsigned)end / n;
+        rem = (unsigned)end - base * n;
     }
-    int end;
-    __device__ __forceinline__ int start(int part) const { return min(end, (int)(part * base + min((unsigned)part, rem))); }
-    // the part that has tile x
+    __device__ __forceinline__ int start(int cta) const { return min(end, (int)(cta * base + min((unsigned)cta, rem))); }
     __device__ __forceinline__ int owner(int x) const {
         const unsigned longer = rem * (base + 1);
         return (int)((unsigned)x < longer ? (unsigned)x / (base + 1) : rem + ((unsigned)x - longer) / base);
+    }
+    // first tile of part k of m of a list of n
+    static __device__ __forceinline__ int part_start(int n, int m, int k) {
+        const int each = n / m;
+        return k * each + min(k, n - each * m);
+    }
+    __device__ __forceinline__ void range(int cta, int& x0, int& x1) const {
+        if (!q) {
+            x0 = start(cta), x1 = start(cta + 1);
+            return;
+        }
+        x0 = x1 = 0;
+        if (cta >= p.part[B]) return;
+        int lo = 0, hi = B - 1;  // last b with part[b] <= cta
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (p.part[mid] <= cta) lo = mid;
+            else hi = mid - 1;
+        }
+        const int n = tiles_of(p.tot[lo]), m = (n + q - 1) / q;
+        const int group = (cta - p.part[lo]) / m, k = cta - p.part[lo] - group * m;
+        x0 = p.first[lo] + group * n + part_start(n, m, k);
+        x1 = p.first[lo] + group * n + part_start(n, m, k + 1);
+    }
+    // The CTAs of a list, and whether the first of them has another list before it.
+    __device__ __forceinline__ void ctas_of(int b, int group, int& first, int& last, bool& second) const {
+        const int n = tiles_of(p.tot[b]);
+        if (q) {
+            const int m = (n + q - 1) / q;
+            first = p.part[b] + group * m;
+            last = first + m - 1;
+            second = false;
+            return;
+        }
+        const int y0 = p.first[b] + group * n;
+        first = owner(y0);
+        last = owner(y0 + n - 1);
+        second = start(first) < y0;
     }
 };
 
@@ -224,9 +301,11 @@ __device__ __forceinline__ bool slot_ok(int slot, int n_slots, unsigned* err) {
 // Floats of one partial: RB rows of output, then their maxima and sums.
 constexpr int part_floats(int rb, int dp) { return rb * (dp + 2); }
 
-// Query rows a CTA of the tensor-memory kernel takes, and the tiles a part of its lists has at least.
+// Query rows a CTA of the tensor-memory kernel takes; for it and the narrow kernel, the tiles a part of a
+// list has at least and what a piece of a list costs beside its tiles, in tiles.
 inline int wide_rows(int R) { return R <= 128 ? 128 : 256; }
-constexpr int kWideLeast = 4;
+constexpr int kWideLeast = 4, kWidePiece = 6;
+constexpr int kNarrowLeast = 1, kNarrowPiece = 4;
 
 // Who copies what: a warp copies sixteen keys of every tile, lane i < 16
 // holding the slot of its key i.

@@ -51,8 +51,8 @@ struct WideCfg {
     static constexpr int kColP = KT / 2, kColO = 2 * KT;       // TMEM columns of a block: two S (P in the second half), O
     static constexpr int kCols = kColO + DP;
     static constexpr int kTmemCols = NB * kCols <= 256 ? 256 : 512;
-    static constexpr int kBars = 2 * kMaxSlots + 5 * NB;
-    static constexpr int fixed(int B) { return (kBars + 1) * 8 + (kMaxSlots + 1) * 8 + 16 + (3 * B + 1) * 4; }
+    static constexpr int kBars = 2 * kMaxSlots + 6 * NB;
+    static constexpr int fixed(int B) { return (kBars + 1) * 8 + (kMaxSlots + 1) * 8 + 16 + Plan::words(B) * 4; }
     static constexpr int smem(int B, int slots) { return kOffRing + slots * kTile + fixed(B); }
     static constexpr int kSmemLimit = NB == 1 ? 113 * 1024 : 227 * 1024;  // of the SM's 228 KB, 1 KB a CTA is the system's
 };
@@ -199,14 +199,14 @@ __global__ void __launch_bounds__(WideCfg<DP, NB>::kThreads, WideCfg<DP, NB>::kC
     uint64_t* const empty = full + kMaxSlots;
     uint64_t* const q_full = empty + kMaxSlots;  // [block] this list's queries are in shared memory
     uint64_t* const s_full = q_full + NB;        // [block][2] S of a tile is in TMEM
-    uint64_t* const p_full = s_full + 2 * NB;    // [block] P of a tile is in TMEM
-    uint64_t* const o_done = p_full + NB;        // [block] O includes the tile; its S and P are free
+    // [block][2] P of a tile is in TMEM. Two barriers: a late value tile can hold its product back until the
+    // softmax has written the next P too, and one barrier would then be two phases on, which its parity
+    // cannot tell from none.
+    uint64_t* const p_full = s_full + 2 * NB;
+    uint64_t* const o_done = p_full + 2 * NB;    // [block] O includes the tile; its S and P are free
     uint16_t* const odd = reinterpret_cast<uint16_t*>(full + Cfg::kBars + 1);  // [slot][4]: keys of a value tile that are not finite
     uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(odd + kMaxSlots * 4);
-    Plan plan;
-    plan.len = reinterpret_cast<int*>(tmem_slot + 4);
-    plan.tot = plan.len + P.c.B;
-    plan.first = plan.tot + P.c.B;
+    const Plan plan(reinterpret_cast<int*>(tmem_slot + 4), P.c.B);
 
     const KvView& C = P.c;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -226,7 +226,8 @@ __global__ void __launch_bounds__(WideCfg<DP, NB>::kThreads, WideCfg<DP, NB>::kC
             mbar_init(&q_full[k], kBlock);
             mbar_init(&s_full[2 * k], 1);
             mbar_init(&s_full[2 * k + 1], 1);
-            mbar_init(&p_full[k], kBlock);
+            mbar_init(&p_full[2 * k], kBlock);
+            mbar_init(&p_full[2 * k + 1], kBlock);
             mbar_init(&o_done[k], 1);
         }
         fence_mbar_init();
@@ -240,11 +241,13 @@ __global__ void __launch_bounds__(WideCfg<DP, NB>::kThreads, WideCfg<DP, NB>::kC
     }
     grid_launch_dependents();
     grid_dependency_wait();
-    make_plan<kThreads>(C, T, groups, plan, P.err, blockIdx.x == 0);  // ends with a barrier
+    make_plan<kThreads, kWideLeast, kWidePiece>(C, T, groups, gridDim.x, plan, P.err, blockIdx.x == 0);  // ends with a barrier
+    if (blockIdx.x == 0 && tid == 0) *P.cut = *plan.cut;
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    const Deal deal(plan.first[C.B], gridDim.x, kWideLeast);
-    const int x0 = deal.start(blockIdx.x), x1 = deal.start(blockIdx.x + 1);
+    const Deal deal(plan, C.B, gridDim.x, kWideLeast);
+    int x0, x1;
+    deal.range(blockIdx.x, x0, x1);
 
     if (x0 >= x1) {
         // more CTAs than tiles: nothing to do
@@ -361,7 +364,7 @@ __global__ void __launch_bounds__(WideCfg<DP, NB>::kThreads, WideCfg<DP, NB>::kC
                 const uint64_t v_desc = desc128(smem_u32(ring + v_at * Cfg::kTile), KT * 128);
 #pragma unroll
                 for (int k = 0; k < NB; ++k) {
-                    mbar_wait(&p_full[k], (uint32_t)(n & 1), P.err, kSiteAttend | kSiteAccum);
+                    mbar_wait(&p_full[2 * k + (n & 1)], (uint32_t)((n >> 1) & 1), P.err, kSiteAttend | kSiteAccum);
                     if (k == 0) fence_proxy_async_smem();
                     tc_fence_after();
                     const uint32_t block = tmem + k * Cfg::kCols, p_col = block + (n & 1) * KT + Cfg::kColP;
@@ -546,7 +549,7 @@ __global__ void __launch_bounds__(WideCfg<DP, NB>::kThreads, WideCfg<DP, NB>::kC
                     split(sum2, s0, s1);
                     sum += s0 + s1;
                 }
-                mbar_arrive(&p_full[block]);
+                mbar_arrive(&p_full[2 * block + (n & 1)]);
                 advance();  // past the value tile
             }
             if (a.tile == a.ntile) {

@@ -21,7 +21,7 @@ struct WeighCfg {
     static constexpr int kOffRow = kOffQ + kWeighRows * DP * 2;      // per row: ancestor word, lse; the counted nodes
     static constexpr int kOffKey = kOffRow + kWeighRows * (8 + 4 + 4) + 16;  // per stage and key: slot, acc
     static constexpr int kOffPlan = kOffKey + kStages * KT * 8;
-    static constexpr int smem(int B) { return kOffPlan + (3 * B + 1) * 4; }
+    static constexpr int smem(int B) { return kOffPlan + Plan::words(B) * 4; }
 };
 
 // acc_out[slot] = acc[slot] + sum over counted rows of exp(scale * q.k - lse).
@@ -43,10 +43,7 @@ __global__ void __launch_bounds__(kThreads, DP <= 128 ? 3 : 1) k_kv_accumulate(c
     int* node_s = reinterpret_cast<int*>(lse_s + kWeighRows);  // counted nodes, ascending; then their number
     int* slot_s = reinterpret_cast<int*>(smem + Cfg::kOffKey);  // [stage][key]
     float* old_s = reinterpret_cast<float*>(slot_s + S * KT);
-    Plan plan;
-    plan.len = reinterpret_cast<int*>(smem + Cfg::kOffPlan);
-    plan.tot = plan.len + P.c.B;
-    plan.first = plan.tot + P.c.B;
+    const Plan plan(reinterpret_cast<int*>(smem + Cfg::kOffPlan), P.c.B);
 
     const KvView& C = P.c;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -54,9 +51,10 @@ __global__ void __launch_bounds__(kThreads, DP <= 128 ? 3 : 1) k_kv_accumulate(c
 
     grid_launch_dependents();
     grid_dependency_wait();
-    make_plan<kThreads>(C, T, C.Hkv, plan, P.err, blockIdx.x == 0);
-    const Deal deal(plan.first[C.B], gridDim.x, 1);
-    const int x0 = deal.start(blockIdx.x), x1 = deal.start(blockIdx.x + 1);
+    make_plan<kThreads, 1, 0>(C, T, C.Hkv, gridDim.x, plan, P.err, blockIdx.x == 0);
+    const Deal deal(plan, C.B, gridDim.x, 1);
+    int x0, x1;
+    deal.range(blockIdx.x, x0, x1);
     if (x0 >= x1) return;
     const float c2 = P.scale * kLog2e;
     const int unit = lane % UNITS;

@@ -131,6 +131,7 @@ __global__ void __launch_bounds__(kThreads, AttendCfg<DP>::kCtas)
     };
     src.enter(C, plan, row_blocks);
     fetch();
+#pragma unroll 1
     for (int s = 0; s < S - 1; ++s) issue();
 
     At a = locate(plan, C.B, x0);

@@ -114,6 +114,16 @@ struct Plan {
         : len(at), tot(at + B), first(at + 2 * B), part(at + 3 * B + 1), cut(at + 4 * B + 2) {}
 };
 
+// a / b for 0 <= a, 0 < b, exact: a float quotient and its correction, a third of an integer division's
+// instructions (these stand in front of every launch's first load).
+__device__ __forceinline__ int div_of(int a, int b) {
+    int q = (int)__fdividef((float)a, (float)b);
+    int r = a - q * b;
+    while (r < 0) r += b, --q;
+    while (r >= b) r -= b, ++q;
+    return q;
+}
+
 __device__ __forceinline__ int tiles_of(int tot) { return tot > KT ? (tot + KT - 1) / KT : 1; }
 
 // Fills the plan for `ctas` CTAs (all threads; ends with a barrier). Lengths
@@ -129,6 +139,30 @@ template <int THREADS, int LEAST, int PIECE>
 __device__ void make_plan(const KvView& C, int T, int groups, int ctas, const Plan& p, unsigned* err, bool report,
                           const int* known = nullptr) {
     const int cut = known ? *known : -1;
+    if (C.B == 1) {
+        // The same for one sequence, by one thread: the general way's code alone, cold in the instruction
+        // cache at every launch, takes 1.3 us of a short call.
+        if (threadIdx.x == 0) {
+            const int len = C.len[0];
+            const bool ok = len >= 0 && len <= C.cap - T;
+            if (!ok && report) atomicOr(err, SI_DEVERR_CACHE);
+            const int tot = ok ? len + T : 0, n = tiles_of(tot), total = n * groups;
+            int q = max(cut, 0);
+            if (PIECE > 0 && cut < 0 && groups <= ctas) {
+                const int even = max(LEAST, div_of(total + ctas - 1, ctas)), m = div_of(ctas, groups);
+                q = max(even, div_of(n + m - 1, m));
+                if (q > even + PIECE) q = 0;
+            }
+            p.len[0] = ok ? len : 0;
+            p.tot[0] = tot;
+            p.first[0] = p.part[0] = 0;
+            p.first[1] = total;
+            p.part[1] = q ? div_of(n + q - 1, q) * groups : 0;
+            *p.cut = q;
+        }
+        __syncthreads();
+        return;
+    }
     for (int b = threadIdx.x; b < C.B; b += THREADS) {
         const int len = C.len[b];
         const bool ok = len >= 0 && len <= C.cap - T;
@@ -142,6 +176,7 @@ __device__ void make_plan(const KvView& C, int T, int groups, int ctas, const Pl
         // out[b]: sum of value(n tiles) * groups over the sequences before b
         auto scan = [&](int* out, auto value) {
             int base = 0;
+#pragma unroll 1
             for (int b0 = 0; b0 < C.B; b0 += 32) {
                 const int b = b0 + lane;
                 const int mine = b < C.B ? value(tiles_of(p.tot[b])) * groups : 0;
@@ -161,19 +196,14 @@ __device__ void make_plan(const KvView& C, int T, int groups, int ctas, const Pl
         int q = max(cut, 0);
         if (PIECE > 0 && cut < 0 && C.B * groups <= ctas) {
             // the least number of tiles a part, from the even share up, that needs no more than ctas parts
-            const int even = max(LEAST, (total + ctas - 1) / ctas);
-            if (C.B == 1) {
-                const int m = ctas / groups, n = tiles_of(p.tot[0]);
-                q = max(even, (n + m - 1) / m);
-                if (q > even + PIECE) q = 0;
-            } else {
-                int parts = 0;  // lane i tries even + i
-                for (int b = 0; b < C.B; ++b) parts += (tiles_of(p.tot[b]) + even + lane - 1) / (even + lane);
-                const unsigned fits = __ballot_sync(0xFFFFFFFFu, lane <= PIECE && parts * groups <= ctas);
-                if (fits) q = even + __ffs(fits) - 1;
-            }
+            const int even = max(LEAST, div_of(total + ctas - 1, ctas));
+            int parts = 0;  // lane i tries even + i
+#pragma unroll 1
+            for (int b = 0; b < C.B; ++b) parts += div_of(tiles_of(p.tot[b]) + even + lane - 1, even + lane);
+            const unsigned fits = __ballot_sync(0xFFFFFFFFu, lane <= PIECE && parts * groups <= ctas);
+            if (fits) q = even + __ffs(fits) - 1;
         }
-        if (q) scan(p.part, [q](int n) { return (n + q - 1) / q; });
+        if (q) scan(p.part, [q](int n) { return div_of(n + q - 1, q); });
         if (lane == 0) *p.cut = q;
     }
     __syncthreads();
@@ -189,6 +219,8 @@ struct Deal {
     __device__ __forceinline__ Deal(const Plan& plan, int seqs, int ctas, int least) : p(plan), B(seqs) {
         q = *plan.cut;
         end = plan.first[seqs];
+        base = rem = 0;
+        if (q) return;
         const unsigned n = max(1u, min((unsigned)ctas, (unsigned)end / (unsigned)least));
         base = (unsigned)end / n;
         rem = (unsigned)end - base * n;
@@ -200,7 +232,7 @@ struct Deal {
     }
     // first tile of part k of m of a list of n
     static __device__ __forceinline__ int part_start(int n, int m, int k) {
-        const int each = n / m;
+        const int each = div_of(n, m);
         return k * each + min(k, n - each * m);
     }
     __device__ __forceinline__ void range(int cta, int& x0, int& x1) const {
@@ -216,8 +248,8 @@ struct Deal {
             if (p.part[mid] <= cta) lo = mid;
             else hi = mid - 1;
         }
-        const int n = tiles_of(p.tot[lo]), m = (n + q - 1) / q;
-        const int group = (cta - p.part[lo]) / m, k = cta - p.part[lo] - group * m;
+        const int n = tiles_of(p.tot[lo]), m = div_of(n + q - 1, q);
+        const int group = div_of(cta - p.part[lo], m), k = cta - p.part[lo] - group * m;
         x0 = p.first[lo] + group * n + part_start(n, m, k);
         x1 = p.first[lo] + group * n + part_start(n, m, k + 1);
     }
@@ -225,7 +257,7 @@ struct Deal {
     __device__ __forceinline__ void ctas_of(int b, int group, int& first, int& last, bool& second) const {
         const int n = tiles_of(p.tot[b]);
         if (q) {
-            const int m = (n + q - 1) / q;
+            const int m = div_of(n + q - 1, q);
             first = p.part[b] + group * m;
             last = first + m - 1;
             second = false;
@@ -254,7 +286,7 @@ __device__ __forceinline__ At locate(const Plan& p, int B, int x) {
     a.b = lo;
     a.ntile = tiles_of(p.tot[lo]);
     const int in = x - p.first[lo];
-    a.group = in / a.ntile;
+    a.group = div_of(in, a.ntile);
     a.tile = in - a.group * a.ntile;
     return a;
 }

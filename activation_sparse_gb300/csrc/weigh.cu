@@ -101,6 +101,7 @@ __global__ void __launch_bounds__(kThreads, DP <= 128 ? 3 : 1) k_kv_accumulate(c
     };
     src.enter(C, plan, 1);
     fetch();
+#pragma unroll 1
     for (int s = 0; s < S - 1; ++s) issue();
 
     At a = locate(plan, C.B, x0);

@@ -114,16 +114,6 @@ struct Plan {
         : len(at), tot(at + B), first(at + 2 * B), part(at + 3 * B + 1), cut(at + 4 * B + 2) {}
 };
 
-// a / b for 0 <= a, 0 < b, exact: a float quotient and its correction, a third of an integer division's
-// instructions (these stand in front of every launch's first load).
-__device__ __forceinline__ int div_of(int a, int b) {
-    int q = (int)__fdividef((float)a, (float)b);
-    int r = a - q * b;
-    while (r < 0) r += b, --q;
-    while (r >= b) r -= b, ++q;
-    return q;
-}
-
 __device__ __forceinline__ int tiles_of(int tot) { return tot > KT ? (tot + KT - 1) / KT : 1; }
 
 // Fills the plan for `ctas` CTAs (all threads; ends with a barrier). Lengths

@@ -197,6 +197,16 @@ __device__ __forceinline__ float warp_sum(float v) {
     return v;
 }
 
+// a / b for 0 <= a, 0 < b, exact: a float quotient and its correction, a
+// third of an integer division's instructions.
+__device__ __forceinline__ int div_of(int a, int b) {
+    int q = (int)__fdividef((float)a, (float)b);
+    int r = a - q * b;
+    while (r < 0) r += b, --q;
+    while (r >= b) r -= b, ++q;
+    return q;
+}
+
 // ------------------------------------------------------------ ordering keys
 
 // Magnitude key: larger |f| <=> larger key (-0 and +0 equal). NaN ranks above inf.

@@ -71,7 +71,7 @@ __global__ void __launch_bounds__(kAppendThreads)
     grid_launch_dependents();
     grid_dependency_wait();
     const long long tok = blockIdx.x;
-    const int b = (int)(tok / P.T), t = (int)(tok % P.T);
+    const int b = (int)(blockIdx.x / (unsigned)P.T), t = (int)(blockIdx.x - (unsigned)b * (unsigned)P.T);
     const int np = R.n_pairs;
     for (int i = threadIdx.x; i < np; i += kAppendThreads) {
         const long long pos = P.pos[tok * R.n_axes + R.axis[i]];
@@ -110,7 +110,7 @@ __global__ void __launch_bounds__(kAppendThreads)
         uint16_t* dst;
         int part;
         const bool is_v = u >= n_qk;
-        int head = is_v ? (u - n_qk) / per_v : u / per_qk;
+        int head = is_v ? div_of(u - n_qk, per_v) : div_of(u, per_qk);
         part = is_v ? (u - n_qk) - head * per_v : u - head * per_qk;
         if (!is_v && head < P.Hq) {
             src = q + head * P.qh;

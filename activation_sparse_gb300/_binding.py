@@ -629,7 +629,18 @@ def _whole(t, dtype, name, shape):
     return t.data_ptr()
 
 
-_Stride3 = _ll * 3
+_stride_arrays = {}  # the C array of {sequence, token, head} strides, by a tensor's strides
+
+
+def _strides(t, name):
+    a = _stride_arrays.get(t.stride())
+    if a is None:
+        if t.stride(-1) != 1 and t.shape[-1] != 1:
+            raise ValueError("the last dimension of %s must be contiguous" % name)
+        if len(_stride_arrays) >= 1024:
+            _stride_arrays.clear()
+        a = _stride_arrays[t.stride()] = (_ll * 3)(*t.stride()[:3])
+    return a
 
 
 def _rows(t, kv, name, T):
@@ -637,11 +648,9 @@ def _rows(t, kv, name, T):
     if t.dim() != 4 or not (t.dtype is kv.dtype and t.is_cuda):
         _dev(t, kv.dtype, name, None, 4)
     b, n, heads, d = t.shape
-    sb, st, sh, one = t.stride()
-    if b != kv.B or n != T or d != kv.D or one != 1:
-        raise ValueError("%s must have shape (%d, %d, heads, %d) with contiguous heads, got %s with strides %s"
-                         % (name, kv.B, T, kv.D, tuple(t.shape), t.stride()))
-    return t.data_ptr(), _Stride3(sb, st, sh), heads
+    if b != kv.B or n != T or d != kv.D:
+        raise ValueError("%s must have shape (%d, %d, heads, %d), got %s" % (name, kv.B, T, kv.D, tuple(t.shape)))
+    return t.data_ptr(), _strides(t, name), heads
 
 
 def si_kv_create(K, V, table, lens, acc=None) -> KV:
@@ -687,8 +696,10 @@ def si_kv_append(kv: KV, rope: Rope, q, k, v, pos, q_out, layer=0, stream=None):
     if q is not None:
         qp, qs, hq = _rows(q, kv, "q", T)
         op = _whole(q_out, kv.dtype, "q_out", q.shape)
-    _check(_lib.si_kv_append(kv._h, layer, rope._h, T, hq, qp, qs, kp, ks, vp, vs,
-                             _whole(pos, torch.int32, "pos", (kv.B, T, rope.n_axes)), op, _stream(stream)))
+    rc = _lib.si_kv_append(kv._h, layer, rope._h, T, hq, qp, qs, kp, ks, vp, vs,
+                           _whole(pos, torch.int32, "pos", (kv.B, T, rope.n_axes)), op, _stream(stream))
+    if rc:
+        _check(rc)
     return q_out
 
 
@@ -700,9 +711,11 @@ def si_tree_attention(kv: KV, q, out, mask=None, lse=None, scale=None, layer=0, 
     torch = _torch()
     B, T = kv.B, q.shape[1]
     qp, qs, hq = _rows(q, kv, "q", T)
-    _check(_lib.si_tree_attention(kv._h, layer, T, hq, qp, qs, _whole(mask, torch.int64, "mask", (B, T)),
-                                  kv.D ** -0.5 if scale is None else scale, _whole(out, kv.dtype, "out", q.shape),
-                                  _whole(lse, torch.float32, "lse", (B, T, hq)), _stream(stream)))
+    rc = _lib.si_tree_attention(kv._h, layer, T, hq, qp, qs, _whole(mask, torch.int64, "mask", (B, T)),
+                                kv.D ** -0.5 if scale is None else scale, _whole(out, kv.dtype, "out", q.shape),
+                                _whole(lse, torch.float32, "lse", (B, T, hq)), _stream(stream))
+    if rc:
+        _check(rc)
     return out
 
 
@@ -720,9 +733,11 @@ def si_kv_accumulate(kv: KV, q, lse, mask=None, rows=None, scale=None, acc_out=N
         if kv.acc is None or acc_out.shape[-3:] != kv.acc.shape[1:] or acc_out.stride()[-3:] != kv.acc.stride()[1:] \
                 or acc_out.numel() != B * kv.Hkv * kv.n_slots:
             raise ValueError("acc_out must have the shape and strides of one layer of the cache's acc")
-    _check(_lib.si_kv_accumulate(kv._h, layer, T, hq, qp, qs, _whole(lse, torch.float32, "lse", (B, T, hq)),
-                                 _whole(mask, torch.int64, "mask", (B, T)), _whole(rows, torch.int64, "rows", (B,)),
-                                 kv.D ** -0.5 if scale is None else scale, ap, _stream(stream)))
+    rc = _lib.si_kv_accumulate(kv._h, layer, T, hq, qp, qs, _whole(lse, torch.float32, "lse", (B, T, hq)),
+                               _whole(mask, torch.int64, "mask", (B, T)), _whole(rows, torch.int64, "rows", (B,)),
+                               kv.D ** -0.5 if scale is None else scale, ap, _stream(stream))
+    if rc:
+        _check(rc)
 
 
 def si_kv_evict(kv: KV, T, budget, sinks=0, recent=0, path=None, n_path=None, table_out=None, len_out=None,
@@ -734,7 +749,9 @@ def si_kv_evict(kv: KV, T, budget, sinks=0, recent=0, path=None, n_path=None, ta
     all). All layers, or one. In place unless table_out and len_out are given."""
     torch = _torch()
     B = kv.B
-    _check(_lib.si_kv_evict(kv._h, -1 if layer is None else layer, T, _whole(path, torch.int32, "path", (B, T)),
-                            _whole(n_path, torch.int32, "n_path", (B,)), budget, sinks, recent,
-                            _whole(table_out, torch.int32, "table_out", (kv.L, B, kv.Hkv, kv.cap)),
-                            _whole(len_out, torch.int32, "len_out", (kv.L, B)), _stream(stream)))
+    rc = _lib.si_kv_evict(kv._h, -1 if layer is None else layer, T, _whole(path, torch.int32, "path", (B, T)),
+                          _whole(n_path, torch.int32, "n_path", (B,)), budget, sinks, recent,
+                          _whole(table_out, torch.int32, "table_out", (kv.L, B, kv.Hkv, kv.cap)),
+                          _whole(len_out, torch.int32, "len_out", (kv.L, B)), _stream(stream))
+    if rc:
+        _check(rc)

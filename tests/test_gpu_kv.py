@@ -212,6 +212,9 @@ CASES = [
     ([0, 63, 64, 128], 9, 8, 2, 128, "bf16", True, "tree"),
     ([4000], 40, 5, 1, 64, "fp16", True, "pad"),
     ([1500], 17, 3, 3, 128, "fp16", False, "tree"),
+    ([5, 70] * 100, 1, 4, 2, 64, "bf16", True, "none"),       # more lists than CTAs
+    ([3, 130] * 100, 5, 8, 2, 64, "fp16", True, "pad"),
+    ([9000, 1, 64, 7000, 20], 40, 8, 2, 128, "bf16", False, "tree"),
 ]
 
 
@@ -247,6 +250,28 @@ def test_attention(si, lens, T, Hq, Hkv, D, dtype, table, mask):
     again = torch().empty_like(q)
     si.si_tree_attention(c.kv, q, again, mask=mask_t, scale=scale, layer=1)
     assert torch().equal(again, out.t)  # no lse asked for, and the same bits
+
+
+@pytest.mark.parametrize("T,Hq,Hkv", [(64, 32, 8), (16, 16, 4), (1, 8, 2)])
+def test_attention_back_to_back(si, T, Hq, Hkv):
+    """Launches that overlap their neighbours' ends, by the hundred: the same bits and no wait that runs out."""
+    t = torch()
+    c = Cache(si, 29, [3000, 1900, 700], T, Hkv, 128, "bf16")
+    q, words, mask = make_rows(c, T, Hq, 128, "bf16", "tree" if T > 1 else "none")
+    want, outs = t.empty_like(q), [t.empty_like(q) for _ in range(4)]
+    si.si_tree_attention(c.kv, q, want, mask=mask)
+    for _ in range(100):
+        for o in outs:
+            si.si_tree_attention(c.kv, q, o, mask=mask)
+    g = t.cuda.CUDAGraph()
+    with t.cuda.graph(g):
+        for _ in range(25):
+            for o in outs:
+                si.si_tree_attention(c.kv, q, o, mask=mask)
+    for _ in range(4):
+        g.replay()
+    t.cuda.synchronize()
+    assert all(t.equal(o, want) for o in outs)
 
 
 def test_attention_peaked_and_flat_rows(si):

@@ -10,6 +10,7 @@
 
 #include "../../include/si.h"
 #include "internal.h"
+#include "kv.h"
 #include <nvtx3/nvToolsExt.h>
 
 namespace {

@@ -8,8 +8,7 @@
 #include <climits>
 #include <cmath>
 
-#include "common.cuh"
-#include "internal.h"
+#include "kv.cuh"
 
 namespace si {
 namespace {

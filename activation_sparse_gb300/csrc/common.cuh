@@ -83,7 +83,6 @@ __device__ __forceinline__ bool mbar_test_wait(uint64_t* bar, uint32_t parity) {
 // bits 16-19 (see si.h).
 enum : unsigned {
     kSiteDecode = 1u << 8, kSiteDenseAct = 2u << 8, kSiteTiered = 3u << 8, kSiteGemm = 4u << 8,
-    kSiteAttend = 6u << 8,
     kSiteFull = 1u << 16, kSiteEmpty = 2u << 16, kSiteFullB = 3u << 16, kSiteAccum = 4u << 16,
 };
 
@@ -195,16 +194,6 @@ __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
     return v;
-}
-
-// a / b for 0 <= a, 0 < b, exact: a float quotient and its correction, a
-// third of an integer division's instructions.
-__device__ __forceinline__ int div_of(int a, int b) {
-    int q = (int)__fdividef((float)a, (float)b);
-    int r = a - q * b;
-    while (r < 0) r += b, --q;
-    while (r >= b) r -= b, ++q;
-    return q;
 }
 
 // ------------------------------------------------------------ ordering keys

@@ -5,8 +5,7 @@
 
 #include <cstring>
 
-#include "common.cuh"
-#include "internal.h"
+#include "kv.cuh"
 
 namespace cg = cooperative_groups;
 

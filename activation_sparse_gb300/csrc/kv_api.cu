@@ -7,7 +7,7 @@
 #include <string>
 
 #include "../../include/si.h"
-#include "internal.h"
+#include "kv.h"
 #include <nvtx3/nvToolsExt.h>
 
 namespace {

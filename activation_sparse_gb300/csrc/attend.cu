@@ -68,10 +68,9 @@ __global__ void __launch_bounds__(kThreads, AttendCfg<DP>::kCtas)
     const int T = P.T, G = P.G, R = T * G, D = C.D;
     const int groups = C.Hkv * row_blocks;
 
-    grid_launch_dependents();
     grid_dependency_wait();
+    grid_launch_dependents();  // after the wait: the join reads the lengths before its own
     make_plan<kThreads, kNarrowLeast, kNarrowPiece>(C, T, groups, gridDim.x, plan, P.err, blockIdx.x == 0);
-    if (blockIdx.x == 0 && tid == 0) *P.cut = *plan.cut;
     const Deal deal(plan, C.B, gridDim.x, kNarrowLeast);
     int x0, x1;
     deal.range(blockIdx.x, x0, x1);
@@ -428,10 +427,12 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
     const Plan plan(reinterpret_cast<int*>(smem), P.c.B);
     const int T = P.T, G = P.G, R = T * G, D = C.D;
     const int groups = C.Hkv * row_blocks;
+    // The first kernel lets this one start once everything before it is complete, and does not change the
+    // lengths: the plan is made under its last tiles.
+    constexpr int LEAST = RB >= 128 ? kWideLeast : kNarrowLeast, PIECE = RB >= 128 ? kWidePiece : kNarrowPiece;
+    make_plan<kJoinWarps * 32, LEAST, PIECE>(C, T, groups, parts, plan, P.err, false);
     grid_launch_dependents();
     grid_dependency_wait();
-    constexpr int LEAST = RB >= 128 ? kWideLeast : kNarrowLeast, PIECE = RB >= 128 ? kWidePiece : kNarrowPiece;
-    make_plan<kJoinWarps * 32, LEAST, PIECE>(C, T, groups, parts, plan, P.err, false, P.cut);
     const Deal deal(plan, C.B, parts, LEAST);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int row_sets = (min(R, RB) + ROWS - 1) / ROWS;

@@ -123,11 +123,9 @@ __device__ __forceinline__ int tiles_of(int tot) { return tot > KT ? (tot + KT -
 // finishes two lists, and every piece of a list costs it about PIECE tiles'
 // time (queries in, partial rows out). So lists are cut by themselves where
 // the longest part and one piece take less than an even share and two. A part
-// has at least LEAST tiles. `known`: where an earlier launch left its *cut.
+// has at least LEAST tiles.
 template <int THREADS, int LEAST, int PIECE>
-__device__ void make_plan(const KvView& C, int T, int groups, int ctas, const Plan& p, unsigned* err, bool report,
-                          const int* known = nullptr) {
-    const int cut = known ? *known : -1;
+__device__ void make_plan(const KvView& C, int T, int groups, int ctas, const Plan& p, unsigned* err, bool report) {
     if (C.B == 1) {
         // The same for one sequence, by one thread: the general way's code alone, cold in the instruction
         // cache at every launch, takes 1.3 us of a short call.
@@ -136,8 +134,8 @@ __device__ void make_plan(const KvView& C, int T, int groups, int ctas, const Pl
             const bool ok = len >= 0 && len <= C.cap - T;
             if (!ok && report) atomicOr(err, SI_DEVERR_CACHE);
             const int tot = ok ? len + T : 0, n = tiles_of(tot), total = n * groups;
-            int q = max(cut, 0);
-            if (PIECE > 0 && cut < 0 && groups <= ctas) {
+            int q = 0;
+            if (PIECE > 0 && groups <= ctas) {
                 const int even = max(LEAST, div_of(total + ctas - 1, ctas)), m = div_of(ctas, groups);
                 q = max(even, div_of(n + m - 1, m));
                 if (q > even + PIECE) q = 0;
@@ -182,8 +180,8 @@ __device__ void make_plan(const KvView& C, int T, int groups, int ctas, const Pl
             return base;
         };
         const int total = scan(p.first, [](int n) { return n; });
-        int q = max(cut, 0);
-        if (PIECE > 0 && cut < 0 && C.B * groups <= ctas) {
+        int q = 0;
+        if (PIECE > 0 && C.B * groups <= ctas) {
             // the least number of tiles a part, from the even share up, that needs no more than ctas parts
             const int even = max(LEAST, div_of(total + ctas - 1, ctas));
             int parts = 0;  // lane i tries even + i

@@ -239,10 +239,9 @@ __global__ void __launch_bounds__(WideCfg<DP, NB>::kThreads, WideCfg<DP, NB>::kC
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
         tc_fence_before();
     }
-    grid_launch_dependents();
     grid_dependency_wait();
+    grid_launch_dependents();  // after the wait: the join reads the lengths before its own
     make_plan<kThreads, kWideLeast, kWidePiece>(C, T, groups, gridDim.x, plan, P.err, blockIdx.x == 0);  // ends with a barrier
-    if (blockIdx.x == 0 && tid == 0) *P.cut = *plan.cut;
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     const Deal deal(plan, C.B, gridDim.x, kWideLeast);

@@ -74,7 +74,6 @@ struct AttendParams {
     float* lse;               // attention: written (may be null); accumulate: read
     float* acc_out;           // accumulate (the cache's strides)
     float* part;              // attention: partial rows
-    int* cut;                 // attention: how the first kernel cut the lists, for the join
     unsigned* err;
 };
 // Scratch floats that launch_tree_attention needs for these sizes (0: cannot query the device).

@@ -277,11 +277,8 @@ int si_tree_attention(si_kv* kv, int layer, int T, int Hq, const void* q, const 
     if ((rc = on_device(kv))) return rc;
     if ((rc = si::device_error_word(&P.err))) return rc;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    // the scratch: a word for the join (in a line of its own), then the partial rows
-    const long long rows = si::attend_partial_floats(kv->d.D, T, P.G);
-    if ((rc = grow_part(kv, rows > 0 ? rows + 32 : rows, st))) return rc;
-    P.cut = reinterpret_cast<int*>(kv->part);
-    P.part = kv->part + 32;
+    if ((rc = grow_part(kv, si::attend_partial_floats(kv->d.D, T, P.G), st))) return rc;
+    P.part = kv->part;
     const cudaError_t e = si::launch_tree_attention(P, st);
     return e == cudaSuccess ? SI_OK : cuda_fail(e, "si_tree_attention");
 }

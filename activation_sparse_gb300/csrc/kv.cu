@@ -205,6 +205,14 @@ __global__ void __launch_bounds__(THREADS, (IN_PLACE ? 512 : 1536) / THREADS > 0
     int32_t* out = P.table_out + l * P.ol + b * P.ob + h * P.oh;
     const float* acc = P.acc ? P.acc + l * P.al + b * P.ab + h * P.ah : nullptr;
     const int T = P.T;
+    // What does not wait for the length goes out with it: the path, and where one CTA has the whole list its
+    // first entries (a list has cap of them whatever its length).
+    const int path_lo = P.path && lane < T ? P.path[(long long)b * T + lane] : 0;
+    const int path_hi = P.path && lane + 32 < T ? P.path[(long long)b * T + lane + 32] : 0;
+    int early[kEvictBatch];
+#pragma unroll
+    for (int j = 0; j < kEvictBatch; ++j)
+        early[j] = CS == 1 && tid + j * THREADS < P.cap ? table[tid + j * THREADS] : 0;
     const int len = P.len[lb];
     const bool bad = len < 0 || len > P.cap - T;
     int np = P.n_path ? P.n_path[b] : T;
@@ -214,7 +222,7 @@ __global__ void __launch_bounds__(THREADS, (IN_PLACE ? 512 : 1536) / THREADS > 0
         unsigned lo = 0, hi = 0;
         bool out_of_range = false;
         for (int i = lane; i < np; i += 32) {
-            const int node = P.path[(long long)b * T + i];
+            const int node = i < 32 ? path_lo : path_hi;
             if (node < 0 || node >= T) out_of_range = true;
             else if (node < 32) lo |= 1u << node;
             else hi |= 1u << (node - 32);
@@ -250,7 +258,7 @@ __global__ void __launch_bounds__(THREADS, (IN_PLACE ? 512 : 1536) / THREADS > 0
 #pragma unroll
             for (int j = 0; j < kEvictBatch; ++j) {
                 const int i = i0 + j * THREADS;
-                slot[j] = i < by_table ? table[c0 + i] : 0;
+                slot[j] = i >= by_table ? 0 : CS == 1 && i0 == tid ? early[j] : table[c0 + i];
             }
 #pragma unroll
             for (int j = 0; j < kEvictBatch; ++j) {

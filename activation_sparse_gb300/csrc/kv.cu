@@ -206,13 +206,15 @@ __global__ void __launch_bounds__(THREADS, (IN_PLACE ? 512 : 1536) / THREADS > 0
     const float* acc = P.acc ? P.acc + l * P.al + b * P.ab + h * P.ah : nullptr;
     const int T = P.T;
     // What does not wait for the length goes out with it: the path, and where one CTA has the whole list its
-    // first entries (a list has cap of them whatever its length).
-    const int path_lo = P.path && lane < T ? P.path[(long long)b * T + lane] : 0;
-    const int path_hi = P.path && lane + 32 < T ? P.path[(long long)b * T + lane + 32] : 0;
+    // first entries past the sinks (a list has cap entries whatever its length).
     int early[kEvictBatch];
 #pragma unroll
-    for (int j = 0; j < kEvictBatch; ++j)
-        early[j] = CS == 1 && tid + j * THREADS < P.cap ? table[tid + j * THREADS] : 0;
+    for (int j = 0; j < kEvictBatch; ++j) {
+        const unsigned i = (unsigned)P.sinks + tid + j * THREADS;  // any sinks without a budget
+        early[j] = CS == 1 && i < (unsigned)P.cap ? table[i] : 0;
+    }
+    const int path_lo = P.path && lane < T ? P.path[(long long)b * T + lane] : 0;
+    const int path_hi = P.path && lane + 32 < T ? P.path[(long long)b * T + lane + 32] : 0;
     const int len = P.len[lb];
     const bool bad = len < 0 || len > P.cap - T;
     int np = P.n_path ? P.n_path[b] : T;
@@ -251,14 +253,20 @@ __global__ void __launch_bounds__(THREADS, (IN_PLACE ? 512 : 1536) / THREADS > 0
     };
     bool bad_slot = false;
     if (evict) {
-        const int by_table = max(0, min(c1, named ? len : n) - c0);  // candidates whose entry is their own index
-        for (int i0 = tid; i0 < by_table; i0 += THREADS * kEvictBatch) {
+        // The safe ones at either end are kept whatever they weigh: nothing is read for them.
+        const int safe_lo = min(m, max(0, lo_c - c0)), safe_hi = max(safe_lo, min(m, hi_c - c0));
+        for (int i = tid; i < ((m + 127) & ~127); i += THREADS)
+            if (i < safe_lo || i >= safe_hi) keys[i] = i < m ? kKeySafe : kKeyNone;
+        if (tid == 0 && m > safe_hi - safe_lo) atomicAdd(&S.hist[kKeySafe >> 21], (unsigned)(m - (safe_hi - safe_lo)));
+        // candidates whose entry is their own index, then accepted nodes, in path order
+        const int by_table = min(safe_hi, max(safe_lo, (named ? len : n) - c0));
+        for (int i0 = safe_lo + tid; i0 < by_table; i0 += THREADS * kEvictBatch) {
             int slot[kEvictBatch];
             float w[kEvictBatch];
 #pragma unroll
             for (int j = 0; j < kEvictBatch; ++j) {
                 const int i = i0 + j * THREADS;
-                slot[j] = i >= by_table ? 0 : CS == 1 && i0 == tid ? early[j] : table[c0 + i];
+                slot[j] = i >= by_table ? 0 : CS == 1 && i0 == P.sinks + tid ? early[j] : table[c0 + i];
             }
 #pragma unroll
             for (int j = 0; j < kEvictBatch; ++j) {
@@ -270,21 +278,18 @@ __global__ void __launch_bounds__(THREADS, (IN_PLACE ? 512 : 1536) / THREADS > 0
             for (int j = 0; j < kEvictBatch; ++j) {
                 const int i = i0 + j * THREADS;
                 if (i >= by_table) break;
-                const uint32_t key = c0 + i < lo_c || c0 + i >= hi_c ? kKeySafe : weight_key(w[j]);
+                const uint32_t key = weight_key(w[j]);
                 keys[i] = key;
                 atomicAdd(&S.hist[key >> 21], 1u);
             }
         }
-        for (int i = by_table + tid; i < ((m + 127) & ~127); i += THREADS) {
-            uint32_t key = kKeyNone;
-            if (i < m) {  // accepted nodes, in path order
-                const int slot = table[entry_of(c0 + i)];
-                const bool ok = (unsigned)slot < n_slots;
-                bad_slot |= !ok;
-                key = c0 + i < lo_c || c0 + i >= hi_c ? kKeySafe : weight_key(acc[ok ? slot : 0]);
-                atomicAdd(&S.hist[key >> 21], 1u);
-            }
+        for (int i = by_table + tid; i < safe_hi; i += THREADS) {
+            const int slot = table[entry_of(c0 + i)];
+            const bool ok = (unsigned)slot < n_slots;
+            bad_slot |= !ok;
+            const uint32_t key = weight_key(acc[ok ? slot : 0]);
             keys[i] = key;
+            atomicAdd(&S.hist[key >> 21], 1u);
         }
     }
     if (bad_slot) atomicOr(P.err, SI_DEVERR_CACHE);

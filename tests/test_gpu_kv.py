@@ -535,6 +535,9 @@ def run_evict(si, table, lens, acc, T, path, n_path, budget, sinks, recent, in_p
     (1, 1, 1, [190000], 1, False, 100001, 4, 512, "real"),
     (1, 2, 2, [300, 200], 7, True, 0, 0, 0, "real"),            # acceptance alone
     (1, 2, 2, [300, 200], 7, False, 1000, 0, 0, "real"),        # a budget that is not met
+    (1, 2, 2, [300, 200], 7, True, 0, 2147483647, 2147483647, "real"),  # sinks and recent mean nothing without one
+    (2, 1, 2, [900], 7, False, 700, 350, 350, "real"),          # budget taken by sinks and recent
+    (2, 1, 2, [9000], 7, False, 7000, 3000, 3000, "ties"),
     (1, 1, 2, [2500], 1, False, 1200, 0, 3, "odd"),
     (40, 3, 2, [64, 65, 66], 4, True, 64, 1, 4, "ties"),
 ])

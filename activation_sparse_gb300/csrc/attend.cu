@@ -1,15 +1,19 @@
-// attend.cu -- attention of a tree of new tokens over a key/value cache, and
-// the attention weight each cached key receives.
+// attend.cu -- attention of a tree of new tokens over a key/value cache: the
+// kernel for few rows a key, and the join of what several CTAs have of a list.
 //
 // A list of keys (one sequence, one cache head) is cut into tiles of 64; the
-// tiles of all lists, in order, are dealt out evenly to the CTAs of one
-// resident grid, so a long context of one sequence and a batch of ragged
-// ones load every SM alike. A CTA walks its tiles with the keys and values
-// of the next ones in flight (16-byte asynchronous copies, gathered through
-// the slot table), and keeps the running maximum and sum of the softmax and
-// the output rows in registers. A list that ends up in one CTA is finished
-// there; the others leave partial rows that a second kernel joins in a fixed
-// order, so results do not depend on timing.
+// tiles of all lists are dealt out evenly to the CTAs of one resident grid, so
+// a long context of one sequence and a batch of ragged ones load every SM
+// alike. A CTA walks its tiles with the keys and values of the next ones in
+// flight (16-byte asynchronous copies, gathered through the slot table), and
+// keeps the running maximum and sum of the softmax and the output rows in
+// registers. A list that ends up in one CTA is finished there; the others
+// leave partial rows that a second kernel joins in a fixed order, so results
+// do not depend on timing.
+//
+// Bound by memory: one token of 32 heads over 131071 keys of 8 heads of 128
+// takes 90 us, 6.0 TB/s, 0.88 of what a plain copy reaches. Short lists are
+// bound by latency (1000 keys: 9 us with the join).
 #include "attend.cuh"
 
 namespace si {
@@ -534,8 +538,11 @@ int padded(int D) { return D <= 64 ? 64 : D <= 128 ? 128 : 256; }
 int row_warps(int R) { return R <= 16 ? 1 : 2; }  // more rows than 32 go in further row blocks
 
 // Up to 16 rows a key: the tiles above, bound by memory. More rows: 128-row
-// tiles on the tensor memory path, whose cost a key does not depend on the
-// rows (heads of more than 128 elements do not fit there).
+// tiles on the tensor memory path, whose cost a key hardly depends on the
+// rows (heads of more than 128 elements do not fit there). 8 sequences of 8192
+// keys, 8 heads of 128, here / there: 16 rows 62 / 60 us, 20 rows 99 / 61, 64
+// rows 179 / 76; one of 30000 keys, heads of 64: 16 rows 19 / 24 us, 20 rows
+// 29 / 24.
 bool many_rows(int D, int R) { return R > 16 && D <= 128; }
 
 template <int DP, int RB, bool FP16>

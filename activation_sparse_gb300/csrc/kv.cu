@@ -62,7 +62,10 @@ constexpr int kAppendThreads = 256;
 // 64-bit fixed point (the product wraps to the fraction of a turn, exact for
 // any int32 position); cos and sin of the token's pairs are made once, in
 // shared memory, for its Hq + Hkv heads. Bound by memory: every element is
-// read and written once, in 16-byte units.
+// read and written once, in 16-byte units. 8192 tokens of 32 + 8 + 8 heads of
+// 128 take 41 us (a plain copy of the same bytes 33); what carries it is the
+// eight blocks an SM: elements loaded ahead of the angles (48 registers, five
+// blocks) took 54 us, and through shared memory a token ahead 46.
 template <bool FP16>
 __global__ void __launch_bounds__(kAppendThreads)
     k_kv_append(const __grid_constant__ KvAppendParams P, const __grid_constant__ RopeTable R) {

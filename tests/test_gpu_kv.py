@@ -576,6 +576,34 @@ def test_evict(si, in_place, L, B, H, lens, T, path, budget, sinks, recent, weig
     assert (np.sort(got_t, -1) == np.sort(table, -1)).all()
 
 
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("L,B,H,lens,T,budget,sinks,recent,weights", [
+    (40, 4, 3, [40, 7, 0, 64], 5, 32, 2, 4, "real"),
+    (40, 4, 3, [300, 1030, 290, 900], 1, 256, 4, 16, "ties"),
+    (60, 2, 4, [1500, 2100], 16, 1400, 0, 100, "odd"),
+    (60, 1, 8, [4900], 3, 4500, 4, 512, "real"),
+    (20, 2, 2, [6500, 3000], 3, 2500, 4, 512, "ties"),
+])
+def test_evict_many_lists(si, in_place, L, B, H, lens, T, budget, sinks, recent, weights):
+    """More lists than CTAs of one kind run at once, and lists that few CTAs share."""
+    rng = np.random.default_rng(44)
+    cap = max(lens) + T + 3
+    table = ref.tables(rng, (L, B, H), cap, cap)
+    lens = np.broadcast_to(np.array(lens, np.int32), (L, B)).copy()
+    acc = np.exp(2 * rng.standard_normal((L, B, H, cap))).astype(np.float32)
+    if weights == "ties":
+        acc = np.floor(acc)
+    elif weights == "odd":
+        acc[rng.random(acc.shape) < .1] = np.nan
+        acc[rng.random(acc.shape) < .1] = -np.inf
+    path = np.stack([rng.permutation(T) for _ in range(B)])
+    n_path = rng.integers(0, T + 1, B)
+    want_t, want_n = ref.evict(table, lens, acc, T, path, n_path, budget, sinks, recent)
+    got_t, got_n = run_evict(si, table, lens, acc, T, path, n_path, budget, sinks, recent, in_place)
+    assert (got_n == want_n).all()
+    assert (got_t == want_t).all(), np.argwhere(got_t != want_t)[:5]
+
+
 def test_evict_one_layer(si):
     rng = np.random.default_rng(42)
     table = ref.tables(rng, (3, 2, 2), 60, 60)

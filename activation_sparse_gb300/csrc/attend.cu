@@ -416,7 +416,7 @@ __global__ void __launch_bounds__(kThreads, AttendCfg<DP>::kCtas)
 // Joins the partial rows of the lists that more than one CTA worked on. A row
 // belongs to JW warps of one block: warp w takes parts w, w + JW, ..., and
 // the warps' sums are added in their order, so the result does not depend on
-// timing. JW = 8 where lists have many parts (few lists), 1 where they have few.
+// timing. JW = 8 or 1.
 constexpr int kJoinWarps = 8;
 
 template <int DP, int RB, int JW, bool FP16>
@@ -535,7 +535,9 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
 
 int per_sm(int dp) { return dp <= 128 ? 2 : 1; }
 int padded(int D) { return D <= 64 ? 64 : D <= 128 ? 128 : 256; }
-int row_warps(int R) { return R <= 16 ? 1 : 2; }  // more rows than 32 go in further row blocks
+// Row warps of heads of more than 128 elements; more rows than 32 go in further row blocks. Four sequences of
+// 8192 keys, 4 heads of 256, one / two: 16 rows 27.4 / 29.7 us, 20 rows 42 / 31, 64 rows 79 / 57.
+int row_warps(int R) { return R <= 16 ? 1 : 2; }
 
 // Up to 16 rows a key: the tiles above, bound by memory. More rows: 128-row
 // tiles on the tensor memory path, whose cost a key hardly depends on the
@@ -550,7 +552,11 @@ cudaError_t launch_join(const AttendParams& P, int row_blocks, int parts, cudaSt
     void* args[3] = {const_cast<AttendParams*>(&P), &row_blocks, &parts};
     const long long lists = (long long)P.c.B * P.c.Hkv * row_blocks;
     const int rows = P.T * P.G < RB ? P.T * P.G : RB;
-    const bool many = parts >= 4 * lists;  // parts of a list: about parts / lists
+    // A block a row (eight warps share its parts) where lists have eight parts and the rows fit the GPU twice
+    // over; else a warp a row. The whole call by the one / the other: 8 lists of 131071 keys, 4 rows 91 / 97 us; 12
+    // of 9001, 128 rows 23.8 / 27.5; 128 of 8192, 4 rows 68.6 / 68.4; 256 of 4096, 4 rows 95 / 91; 32 of 1000, 256
+    // rows 40 / 18; 64 of 8192, 256 rows 133 / 70.
+    const bool many = parts >= 8 * lists && lists * rows <= 16ll * sm_count();  // parts of a list: about parts / lists
     const int per_block = many ? 1 : kJoinWarps;
     const long long blocks = lists * ((rows + per_block - 1) / per_block);
     if (blocks > 0x7FFFFFFFLL) return cudaErrorInvalidValue;

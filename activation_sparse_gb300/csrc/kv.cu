@@ -514,12 +514,12 @@ cudaError_t launch_kv_evict(const KvEvictParams& P, cudaStream_t st) {
     const long long rows = (long long)P.L * P.B * P.Hkv;
     // CTAs a list (at most eight, the portable cluster). Few enough candidates each that three CTAs share an
     // SM where eight CTAs can do that (64 lists of up to 100001: 78 us, 96 with twice the candidates each). Where
-    // the lists alone do not fill the GPU, lists above 6144 are split down to 3072 each: a cluster's barriers
+    // the lists alone do not fill the GPU, lists above 6144 are split down to 3200 each: a cluster's barriers
     // cost 2 us, a CTA's further thousand candidates 1 (eight lists of 3000, whole / in two: 7.5 / 8.8 us;
     // of 8000, in two / in four: 12.1 / 10.6; 128 lists of 4096, whole / in four: 14.5 / 18.1).
     int cs = 1;
     auto each = [&]() { return ((P.cap + cs - 1) / cs + 127) & ~127; };
-    while (cs < 8 && (each() > 12544 || (P.cap > 6144 && each() > 3072 && rows * cs <= 152))) cs *= 2;
+    while (cs < 8 && (each() > 12544 || (P.cap > 6144 && each() > 3200 && rows * cs <= 152))) cs *= 2;
     const int chunk = each();
     if (chunk > kEvictChunk) return cudaErrorInvalidValue;
     // 512 threads where the CTAs all run at once, three an SM, or hold much each; else 256, of which six fit.

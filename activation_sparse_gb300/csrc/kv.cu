@@ -240,7 +240,7 @@ __global__ void __launch_bounds__(THREADS, (IN_PLACE ? 512 : 1536) / THREADS > 0
     if (path_bad) np = 0, taken = 0;
     if ((bad || path_bad) && rank == 0 && tid == 0)
         atomicOr(P.err, (bad ? SI_DEVERR_CACHE : 0u) | (path_bad ? SI_DEVERR_COUNT : 0u));
-    const bool named = P.path && !path_bad;
+    const bool named = P.path && !path_bad && !bad;  // a list out of bounds is left as it is
     const int n = bad ? 0 : len + np;
     const int used = bad ? 0 : len + T;           // entries this call may reorder
     const bool evict = P.budget > 0 && n > P.budget;
@@ -297,7 +297,7 @@ __global__ void __launch_bounds__(THREADS, (IN_PLACE ? 512 : 1536) / THREADS > 0
     }
     if (bad_slot) atomicOr(P.err, SI_DEVERR_CACHE);
     int rejected = -1;  // slot of the node that this thread puts behind the candidates
-    if (rank == 0 && named && tid < T && !(taken >> tid & 1)) rejected = bad ? -1 : table[len + tid];
+    if (rank == 0 && named && tid < T && !(taken >> tid & 1)) rejected = table[len + tid];
 
     if (!evict) {
         if (IN_PLACE) {

@@ -636,6 +636,32 @@ def test_evict_bad_paths_and_lengths(si, in_place):
     assert (got_t[:, 4:] == table[:, 4:]).all() and (got_n[:, 4:] == lens[:, 4:]).all()
 
 
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("bad", [[-1, -2, -3, -4], [-9, -2147483648, -40, -1], [38, 41, 2147483647, 39]])
+def test_evict_lengths_out_of_bounds_touch_nothing(si, in_place, bad):
+    """Lists out of bounds, between good ones and with paths that are valid and permuted: no entry of any other
+    list changes, and the bad lists and lengths are what they were."""
+    rng = np.random.default_rng(45)
+    B, T, cap = 9, 4, 40
+    table = ref.tables(rng, (1, B, 2), cap, cap)
+    lens = np.full((1, B), 30, np.int32)
+    lens[0, 1::2] = bad
+    acc = rng.random((1, B, 2, cap)).astype(np.float32)
+    path = np.array([[2, 0, 3, 1]] * B)
+    n_path = np.full(B, 3)
+    safe = np.where(np.arange(B) % 2, 0, 30).astype(np.int32)[None]
+    want_t, want_n = ref.evict(table, safe, acc, T, path, n_path, 20, 2, 4)
+    want_t[0, 1::2], want_n[0, 1::2] = table[0, 1::2], lens[0, 1::2]
+    for budget, expect in ((20, (want_t, want_n)), (0, None)):
+        if expect is None:  # acceptance alone
+            expect = ref.evict(table, safe, acc, T, path, n_path, 0, 0, 0)
+            expect[0][0, 1::2], expect[1][0, 1::2] = table[0, 1::2], lens[0, 1::2]
+        got_t, got_n = run_evict(si, table, lens, acc, T, path, n_path, budget, 2, 4, in_place)
+        assert si.si_device_error(clear=True) == si.SI_DEVERR_CACHE
+        assert (got_t == expect[0]).all(), np.argwhere(got_t != expect[0])[:5]
+        assert (got_n == expect[1]).all()
+
+
 # ------------------------------------------------------------ streams, graphs
 
 def test_step_on_another_stream_and_in_a_graph(si):

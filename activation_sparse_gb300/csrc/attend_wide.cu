@@ -54,7 +54,7 @@ struct WideCfg {
     static constexpr int kColP = KT / 2, kColO = 2 * KT;       // TMEM columns of a block: two S (P in the second half), O
     static constexpr int kCols = kColO + DP;
     static constexpr int kTmemCols = NB * kCols <= 256 ? 256 : 512;
-    static constexpr int kBars = 2 * kMaxSlots + 6 * NB;
+    static constexpr int kBars = 2 * kMaxSlots + 7 * NB;
     static constexpr int fixed(int B) { return (kBars + 1) * 8 + (kMaxSlots + 1) * 8 + 16 + Plan::words(B) * 4; }
     static constexpr int smem(int B, int slots) { return kOffRing + slots * kTile + fixed(B); }
     static constexpr int kSmemLimit = NB == 1 ? 113 * 1024 : 227 * 1024;  // of the SM's 228 KB, 1 KB a CTA is the system's
@@ -202,11 +202,12 @@ __global__ void __launch_bounds__(WideCfg<DP, NB>::kThreads, WideCfg<DP, NB>::kC
     uint64_t* const empty = full + kMaxSlots;
     uint64_t* const q_full = empty + kMaxSlots;  // [block] this list's queries are in shared memory
     uint64_t* const s_full = q_full + NB;        // [block][2] S of a tile is in TMEM
-    // [block][2] P of a tile is in TMEM. Two barriers: a late value tile can hold its product back until the
-    // softmax has written the next P too, and one barrier would then be two phases on, which its parity
-    // cannot tell from none.
+    // [block][2] P of a tile is in TMEM, and O includes the tile (its S and P are free). Two barriers of each, for
+    // even and odd tiles: the S of a tile is out before the last tile's product, which waits for the slowest warp and
+    // the other block, so a quick warp is done with its P while that product is still to come. One barrier would
+    // then be waited for two phases ahead, which its parity cannot tell from none.
     uint64_t* const p_full = s_full + 2 * NB;
-    uint64_t* const o_done = p_full + 2 * NB;    // [block] O includes the tile; its S and P are free
+    uint64_t* const o_done = p_full + 2 * NB;
     uint16_t* const odd = reinterpret_cast<uint16_t*>(full + Cfg::kBars + 1);  // [slot][4]: keys of a value tile that are not finite
     uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(odd + kMaxSlots * 4);
     const Plan plan(reinterpret_cast<int*>(tmem_slot + 4), P.c.B);
@@ -231,7 +232,8 @@ __global__ void __launch_bounds__(WideCfg<DP, NB>::kThreads, WideCfg<DP, NB>::kC
             mbar_init(&s_full[2 * k + 1], 1);
             mbar_init(&p_full[2 * k], kBlock);
             mbar_init(&p_full[2 * k + 1], kBlock);
-            mbar_init(&o_done[k], 1);
+            mbar_init(&o_done[2 * k], 1);
+            mbar_init(&o_done[2 * k + 1], 1);
         }
         fence_mbar_init();
     }
@@ -374,7 +376,7 @@ __global__ void __launch_bounds__(WideCfg<DP, NB>::kThreads, WideCfg<DP, NB>::kC
                     for (int i = 0; i < KT / 16; ++i)
                         tc_mma_ta(block + Cfg::kColO, p_col + i * 8, v_desc + (i * 16 * 128 >> 4), kDescO,
                                   !fresh || i > 0, leader);
-                    tc_commit(&o_done[k], leader);
+                    tc_commit(&o_done[2 * k + (n & 1)], leader);
                 }
                 tc_commit(&empty[v_at], leader);
             };
@@ -389,8 +391,10 @@ __global__ void __launch_bounds__(WideCfg<DP, NB>::kThreads, WideCfg<DP, NB>::kC
                 for (int k = 0; k < NB; ++k) {
                     if (first) mbar_wait(&q_full[k], (uint32_t)(lists & 1), P.err, kSiteAttend | kSiteFull);
                     // the S this tile takes was tile n - 2's (where n - 1's product is out already, that one's phase)
-                    if (n > 1 || (first && n > 0))
-                        mbar_wait(&o_done[k], (uint32_t)((first ? n - 1 : n - 2) & 1), P.err, kSiteAttend | kSiteAccum);
+                    if (n > 1 || (first && n > 0)) {
+                        const int done = first ? n - 1 : n - 2;
+                        mbar_wait(&o_done[2 * k + (done & 1)], (uint32_t)((done >> 1) & 1), P.err, kSiteAttend | kSiteAccum);
+                    }
                     if (k == 0 || first) fence_proxy_async_smem();
                     tc_fence_after();
                     const uint64_t q_desc = desc128(q_addr + k * Cfg::kQ, 16);
@@ -421,6 +425,9 @@ __global__ void __launch_bounds__(WideCfg<DP, NB>::kThreads, WideCfg<DP, NB>::kC
         int n = 0, segment = 0, v_at = 0, v_round = 0;  // ring position of the value tile of tile n
         auto advance = [&]() {
             if (++v_at == slots) v_at = 0, ++v_round;
+        };
+        auto wait_o = [&](int tile) {  // O of this block has the tile
+            mbar_wait(&o_done[2 * block + (tile & 1)], (uint32_t)((tile >> 1) & 1), P.err, kSiteAttend | kSiteAccum);
         };
         for (int x = x0; x < x1; ++segment) {
             const int b = a.b, h = a.group / row_blocks, rb = a.group % row_blocks;
@@ -502,7 +509,7 @@ __global__ void __launch_bounds__(WideCfg<DP, NB>::kThreads, WideCfg<DP, NB>::kC
                     sum *= keep;
                 }
                 if (__any_sync(0xFFFFFFFFu, keep != 1.0f) && n > n_first) {
-                    mbar_wait(&o_done[block], (uint32_t)((n - 1) & 1), P.err, kSiteAttend | kSiteAccum);
+                    wait_o(n - 1);
                     __syncwarp();
                     tc_fence_after();
 #pragma unroll 1
@@ -559,7 +566,7 @@ __global__ void __launch_bounds__(WideCfg<DP, NB>::kThreads, WideCfg<DP, NB>::kC
                 step(plan, C.B, groups, a);
             }
             // the list's O, or this CTA's part of it
-            mbar_wait(&o_done[block], (uint32_t)((n - 1) & 1), P.err, kSiteAttend | kSiteAccum);
+            wait_o(n - 1);
             __syncwarp();
             tc_fence_after();
             const bool empty_row = word == 0 || sum == 0.0f;

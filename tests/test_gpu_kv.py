@@ -274,6 +274,58 @@ def test_attention_back_to_back(si, T, Hq, Hkv):
     assert all(t.equal(o, want) for o in outs)
 
 
+def rise_late(c, q, Hkv, D, at_nodes, last=400, slope=0.1):
+    """Scores of the chosen nodes' rows climb by `slope` a key over each list's last `last` keys: maxima that
+    outgrow the ones of the tiles before, in some warps and not in others."""
+    u = np.zeros(D)
+    u[::2] = (2.0 / D) ** 0.5
+    for b, n in enumerate(c.lens_h):
+        climb = slope * D ** 0.5 / 8.0 * np.maximum(0, np.arange(n) - n + last)
+        for h in range(Hkv):
+            slots = gpu(np.arange(n) if c.table_h is None else c.table_h[0, b, h, :n].astype(np.int64))
+            k = host(c.K[0, b, h, slots])
+            k -= np.outer(k @ u, u)
+            c.K[0, b, h, slots] = gpu(k + np.outer(climb, u), c.K.dtype)
+    x = host(q)
+    x -= (x @ u)[..., None] * u
+    x[:, at_nodes] += 8.0 * u
+    q.copy_(gpu(x, q.dtype))
+
+
+@pytest.mark.parametrize("lens,T,Hq,Hkv,D,dtype,table", [
+    ([3000, 1900, 700], 64, 32, 8, 128, "bf16", True),
+    ([3001, 1920, 640, 65], 16, 16, 2, 128, "fp16", True),
+    ([1500, 130, 900], 33, 8, 2, 64, "bf16", False),
+    ([100] * 40, 24, 8, 2, 64, "fp16", True),        # a CTA has lists of two tiles
+])
+def test_attention_every_launch_with_maxima_that_rise_late(si, lens, T, Hq, Hkv, D, dtype, table):
+    """Rows that rescale in a list's last tiles beside rows that do not; every one of many overlapping launches is
+    looked at, not the last into a buffer."""
+    t = torch()
+    c = Cache(si, 61, lens, T, Hkv, D, dtype, table=table)
+    q, words, mask = make_rows(c, T, Hq, D, dtype, "tree")
+    per_warp = max(1, 32 // (Hq // Hkv))
+    rise_late(c, q, Hkv, D, [n for n in range(T) if n // per_warp % 2])
+    want, lse = t.empty_like(q), t.empty(q.shape[:3], device="cuda")
+    si.si_tree_attention(c.kv, q, want, mask=mask, lse=lse)
+    check_attend(c, q, want, lse, words, D ** -0.5, dtype)
+    outs = [t.zeros_like(q) for _ in range(120)]
+    for o in outs:
+        si.si_tree_attention(c.kv, q, o, mask=mask)
+    assert all(t.equal(o, want) for o in outs)
+    for o in outs:
+        o.zero_()
+    g = t.cuda.CUDAGraph()
+    with t.cuda.graph(g):
+        for o in outs:
+            si.si_tree_attention(c.kv, q, o, mask=mask)
+    for _ in range(3):
+        for o in outs:
+            o.zero_()
+        g.replay()
+        assert all(t.equal(o, want) for o in outs)
+
+
 def test_attention_peaked_and_flat_rows(si):
     """Scores far apart (one key takes all) and all equal."""
     c = Cache(si, 22, [700], 1, 1, 64, "bf16", k_scale=8.0)

@@ -245,7 +245,9 @@ __global__ void __launch_bounds__(WideCfg<DP, NB>::kThreads, WideCfg<DP, NB>::kC
         tc_fence_before();
     }
     grid_dependency_wait();
-    grid_launch_dependents();  // after the wait: the join reads the lengths before its own
+    // After the wait: the join reads the lengths before its own. And by the warp that has the tensor memory: a later
+    // grid that takes tensor memory and then waits for this one may only start where this one has its own.
+    if (warp == Cfg::kMmaWarp) grid_launch_dependents();
     make_plan<kThreads, kWideLeast, kWidePiece>(C, T, groups, gridDim.x, plan, P.err, blockIdx.x == 0);  // ends with a barrier
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;

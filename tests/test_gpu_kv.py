@@ -326,6 +326,42 @@ def test_attention_every_launch_with_maxima_that_rise_late(si, lens, T, Hq, Hkv,
         assert all(t.equal(o, want) for o in outs)
 
 
+def test_attention_between_prefill_products(si):
+    """Tree attention and the FFN's prefill product, which both take tensor memory, in turn without a pause: every
+    launch gives its bits and no wait runs out."""
+    t = torch()
+    c = Cache(si, 62, [700, 300], 64, 2, 128, "bf16")
+    q, words, mask = make_rows(c, 64, 8, 128, "bf16", "tree")
+    rng = np.random.default_rng(63)
+    W = [gpu(rng.standard_normal(s) / 16, t.bfloat16) for s in ((1024, 256), (1024, 256), (256, 1024))]
+    score = gpu(rng.random(1024), t.float32)
+    layer = si.si_pack_loaded(*W, score, score, 0.7, 0.4)
+    X = gpu(rng.standard_normal((300, 256)), t.bfloat16)
+    n = si.si_count(0.5, 1024)
+    pairs = [(t.zeros_like(q), t.zeros(1, n, dtype=t.int32, device="cuda"), t.zeros(300, layer.n_pad, device="cuda")) for _ in range(60)]
+
+    def both():
+        for o, S, A in pairs:
+            si.si_select_dynamic(layer, X, 300, 1, 200, 0.5, S, A)
+            si.si_tree_attention(c.kv, q, o, mask=mask)
+
+    both()
+    want, lse = t.empty_like(q), t.empty(q.shape[:3], device="cuda")
+    si.si_tree_attention(c.kv, q, want, mask=mask, lse=lse)
+    check_attend(c, q, want, lse, words, 128 ** -0.5, "bf16")
+    S0, A0 = pairs[0][1].clone(), pairs[0][2].clone()
+    assert all(t.equal(o, want) and t.equal(S, S0) and t.equal(A, A0) for o, S, A in pairs)
+    for x in pairs:
+        for y in x:
+            y.zero_()
+    g = t.cuda.CUDAGraph()
+    with t.cuda.graph(g):
+        both()
+    g.replay()
+    assert all(t.equal(o, want) and t.equal(S, S0) and t.equal(A, A0) for o, S, A in pairs)
+    layer.close()
+
+
 def test_attention_peaked_and_flat_rows(si):
     """Scores far apart (one key takes all) and all equal."""
     c = Cache(si, 22, [700], 1, 1, 64, "bf16", k_scale=8.0)

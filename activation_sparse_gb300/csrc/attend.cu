@@ -609,11 +609,11 @@ cudaError_t launch_wide(const AttendParams& P, cudaStream_t st) {
 
 }  // namespace
 
-// Partial rows of every CTA (two pieces of lists each).
-long long attend_partial_floats(int D, int T, int G) {
-    const int dp = padded(D), R = T * G;
-    if (many_rows(D, R)) return 2ll * sm_count() * 2 * part_floats(128, dp);  // two CTAs an SM, or one with twice the rows
-    return 2ll * sm_count() * per_sm(dp) * part_floats(16 * row_warps(R), dp);
+// Partial rows of every CTA (two pieces of lists each), for as many rows as a call can have: 40 MB for heads of 128.
+long long attend_partial_floats(int D) {
+    const int dp = padded(D);
+    if (many_rows(D, INT_MAX)) return 2ll * sm_count() * 2 * part_floats(128, dp);  // two CTAs an SM, or one with twice the rows
+    return 2ll * sm_count() * per_sm(dp) * part_floats(16 * row_warps(INT_MAX), dp);
 }
 
 cudaError_t launch_tree_attention(const AttendParams& P, cudaStream_t st) {

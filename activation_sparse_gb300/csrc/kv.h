@@ -76,8 +76,8 @@ struct AttendParams {
     float* part;              // attention: partial rows
     unsigned* err;
 };
-// Scratch floats that launch_tree_attention needs for these sizes (0: cannot query the device).
-long long attend_partial_floats(int D, int T, int G);
+// Scratch floats that launch_tree_attention needs at most for heads of D elements (0: cannot query the device).
+long long attend_partial_floats(int D);
 cudaError_t launch_tree_attention(const AttendParams& P, cudaStream_t st);
 // attend_wide.cu: the first of the two kernels for many rows; says how it cut the work for the join.
 cudaError_t launch_tree_attention_wide(const AttendParams& P, int* row_blocks, int* parts, cudaStream_t st);

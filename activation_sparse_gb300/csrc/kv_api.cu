@@ -55,7 +55,6 @@ struct si_kv {
     si_kv_desc d;
     int device = -1;          // of the scratch, set with its first allocation
     float* part = nullptr;    // partial attention rows
-    long long part_floats = 0;
     unsigned* ticket = nullptr;  // eviction: a ticket and L * B lengths
 };
 
@@ -71,23 +70,19 @@ int on_device(si_kv* kv) {
     return SI_OK;
 }
 
-int grow_part(si_kv* kv, long long need, cudaStream_t st) {
+// The attention's scratch, for whatever this handle's calls may need: made once and kept, because a captured graph
+// holds its address.
+int make_part(si_kv* kv, cudaStream_t st) {
+    if (kv->part) return SI_OK;
+    const long long need = si::attend_partial_floats(kv->d.D);
     if (need <= 0) return fail(SI_ERR_CUDA, "cannot query the device for the attention grid");
-    if (kv->part_floats >= need) return SI_OK;
-    if (capturing(st)) return fail(SI_ERR_INVALID_ARG, "attention scratch must grow; call once before capture");
-    if (kv->part) {
-        const cudaError_t e = cudaFree(kv->part);  // waits for the launches that use it
-        kv->part = nullptr;
-        kv->part_floats = 0;
-        if (e != cudaSuccess) return cuda_fail(e, "cudaFree");
-    }
+    if (capturing(st)) return fail(SI_ERR_INVALID_ARG, "attention scratch must be made; call once before capture");
     const cudaError_t e = cudaMalloc(reinterpret_cast<void**>(&kv->part), (size_t)need * sizeof(float));
     if (e != cudaSuccess) {
         (void)cudaGetLastError();
         kv->part = nullptr;
         return fail(SI_ERR_OOM, "cudaMalloc failed for the attention scratch");
     }
-    kv->part_floats = need;
     return SI_OK;
 }
 
@@ -277,7 +272,7 @@ int si_tree_attention(si_kv* kv, int layer, int T, int Hq, const void* q, const 
     if ((rc = on_device(kv))) return rc;
     if ((rc = si::device_error_word(&P.err))) return rc;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if ((rc = grow_part(kv, si::attend_partial_floats(kv->d.D, T, P.G), st))) return rc;
+    if ((rc = make_part(kv, st))) return rc;
     P.part = kv->part;
     const cudaError_t e = si::launch_tree_attention(P, st);
     return e == cudaSuccess ? SI_OK : cuda_fail(e, "si_tree_attention");

@@ -543,8 +543,10 @@ typedef struct si_kv_desc {
 } si_kv_desc;
 
 /* A handle over the caller's cache. It owns the scratch of the calls below,
- * made on their first use (run a call once before capturing it; a larger
- * call may need more). si_kv_destroy synchronises the device first. */
+ * made on their first use (run a call once before capturing it) for calls of
+ * any size, and kept where it is until si_kv_destroy: graphs captured on the
+ * handle stay good whatever is called on it later. si_kv_destroy synchronises
+ * the device first; graphs that use the handle may not run after it. */
 int si_kv_create(const si_kv_desc *desc, si_kv **out);
 int si_kv_destroy(si_kv *kv);
 

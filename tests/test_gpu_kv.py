@@ -817,3 +817,35 @@ def test_scratch_does_not_grow_in_a_capture(si):
             si.si_tree_attention(c.kv, q, t.empty_like(q))
         with pytest.raises(si.SIError, match="before capture"):
             si.si_kv_evict(c.kv, 1, 4)
+
+
+@pytest.mark.parametrize("D,small,large", [(128, (1, 8), (16, 32)), (64, (2, 4), (64, 64)), (256, (1, 2), (40, 8))])
+def test_graphs_outlive_larger_calls(si, D, small, large):
+    """A graph of a small call gives its bits after larger calls on its handle; the larger one needs no more
+    scratch, so that it can be captured at once."""
+    t = torch()
+    c = Cache(si, 54, [4000], 64, 2, D, "bf16")
+
+    def call(T, Hq, seed):
+        q = gpu(np.random.default_rng(seed).standard_normal((1, T, Hq, D)), t.bfloat16)
+        out, lse = t.zeros_like(q), t.zeros(1, T, Hq, device="cuda")
+        return (lambda: si.si_tree_attention(c.kv, q, out, lse=lse)), out, lse
+
+    one, out1, lse1 = call(*small, 55)
+    many, out2, lse2 = call(*large, 56)
+    one()
+    want1 = out1.clone(), lse1.clone()
+    graphs = t.cuda.CUDAGraph(), t.cuda.CUDAGraph()
+    with t.cuda.graph(graphs[0]):
+        one()
+    with t.cuda.graph(graphs[1]):
+        many()
+    many()
+    want2 = out2.clone(), lse2.clone()
+    for o in (out1, lse1, out2, lse2):
+        o.zero_()
+    for _ in range(3):
+        graphs[0].replay()
+        graphs[1].replay()
+    assert t.equal(out1, want1[0]) and t.equal(lse1, want1[1])
+    assert t.equal(out2, want2[0]) and t.equal(lse2, want2[1])

@@ -391,7 +391,7 @@ __global__ void __launch_bounds__(kThreads, AttendCfg<DP>::kCtas)
                                 empty ? 0u : pack<FP16>(o[i][2 * e] * inv, o[i][2 * e + 1] * inv);
                     }
                     if (P.lse && (lane & 3) == 0)
-                        P.lse[at] = empty ? -INFINITY : fmaf(mx[e], P.scale, logf(sum[e]));
+                        P.lse[at] = empty ? -INFINITY : lse_of(mx[e], P.scale, sum[e]);
                 }
             } else {
                 float* part = P.part + ((long long)blockIdx.x * 2 + (segment ? 1 : 0)) * part_floats(RB, DP);
@@ -528,7 +528,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
         }
         static_cast<uint16_t*>(P.out)[at * D + d] = bits;
     }
-    if (P.lse && lane == 0) P.lse[at] = empty ? -INFINITY : fmaf(top, P.scale, logf(sum));
+    if (P.lse && lane == 0) P.lse[at] = empty ? -INFINITY : lse_of(top, P.scale, sum);
 }
 
 // ------------------------------------------------------------------ host

@@ -65,6 +65,12 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
+// log of sum * exp(scale * score). The product is rounded by itself, as where a key's weight is taken: whatever
+// the scores' size, scale * score and lse then differ by log(sum) alone.
+__device__ __forceinline__ float lse_of(float score, float scale, float sum) {
+    return __fadd_rn(__fmul_rn(score, scale), logf(sum));
+}
+
 template <bool FP16>
 __device__ __forceinline__ uint32_t pack(float a, float b) {
     uint32_t w;

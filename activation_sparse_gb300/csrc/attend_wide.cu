@@ -636,7 +636,7 @@ __global__ void __launch_bounds__(WideCfg<DP, NB>::kThreads, WideCfg<DP, NB>::kC
                     part[Cfg::kRows * DP + r] = ref;
                     part[Cfg::kRows * DP + Cfg::kRows + r] = sum;
                 } else if (P.lse) {
-                    P.lse[at] = empty_row ? -INFINITY : fmaf(ref, P.scale, logf(sum));
+                    P.lse[at] = empty_row ? -INFINITY : lse_of(ref, P.scale, sum);
                 }
             }
         }

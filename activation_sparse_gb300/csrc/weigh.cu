@@ -59,7 +59,6 @@ __global__ void __launch_bounds__(kThreads, DP <= 128 ? 3 : 1) k_kv_accumulate(c
     int x0, x1;
     deal.range(blockIdx.x, x0, x1);
     if (x0 >= x1) return;
-    const float c2 = P.scale * kLog2e;
     const int unit = lane % UNITS;
     const bool unit_on = unit * 8 < D;
     const int n_slots = (int)C.n_slots, k_step = (int)C.ks;
@@ -174,7 +173,7 @@ __global__ void __launch_bounds__(kThreads, DP <= 128 ? 3 : 1) k_kv_accumulate(c
                         word = word_of(P.mask, T, b, t);
                     }
                     // a row that saw nothing gives nothing
-                    lse_s[r] = lse == -INFINITY ? INFINITY : lse * kLog2e;
+                    lse_s[r] = lse == -INFINITY ? INFINITY : lse;
                     word_s[r] = word;
                 }
                 have_h = h;
@@ -203,9 +202,12 @@ __global__ void __launch_bounds__(kThreads, DP <= 128 ? 3 : 1) k_kv_accumulate(c
                 for (int c = 0; c < 2; ++c) {
                     const int r = n + c * 8 + (lane & 3) * 2;
                     const float2 lse = *reinterpret_cast<const float2*>(lse_s + r);
+                    // The difference is taken before the base's factor, and of the rounded product, as lse was: scores of
+                    // the type's lowest value then differ from lse by 0, where s * (scale * log2 e) would be off by a
+                    // rounding of that size, and its power of two 0 or infinite.
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        float p = ex2(fmaf(s[c][e], c2, e & 1 ? -lse.y : -lse.x));
+                        float p = ex2(__fadd_rn(__fmul_rn(s[c][e], P.scale), e & 1 ? -lse.y : -lse.x) * kLog2e);
                         // a padding row's zeros meet what a key holds, and 0 * infinity is NaN
                         if (n + 16 > nr && r + (e & 1) >= nr) p = 0.0f;
                         if (edge) {

@@ -577,6 +577,29 @@ def test_accumulate_infinite_keys(si):
     assert t.allclose(acc[0, 0, 0], want, rtol=1e-5, atol=0)
 
 
+@pytest.mark.parametrize("heads", [1, 32])  # lse from the kernel for few rows a key, and for many
+@pytest.mark.parametrize("scale", [0.5, 0.3, 64 ** -0.5 * 1.1])
+def test_accumulate_lowest_values(si, heads, scale):
+    """Weights of keys of the type's lowest value: nothing beside others, finite and alike among themselves (a
+    32-bit lse of that size cannot hold how many they are), nothing in a row of minus infinities."""
+    t = torch()
+    K = t.zeros(1, 3, 1, 4, 64, dtype=t.bfloat16, device="cuda")
+    low = t.finfo(t.bfloat16).min
+    K[0, 0, 0, 0, 0], K[0, 1, 0, :, 0], K[0, 2, 0, :, 0] = low, low, -math.inf
+    acc = t.zeros(1, 3, 1, 4, device="cuda")
+    kv = si.si_kv_create(K, t.ones_like(K), None, t.full((1, 3), 3, dtype=t.int32, device="cuda"), acc)
+    q = t.zeros(3, 1, heads, 64, dtype=t.bfloat16, device="cuda")
+    q[:, :, :, 0] = 1
+    out, lse = t.empty_like(q), t.empty(3, 1, heads, device="cuda")
+    si.si_tree_attention(kv, q, out, lse=lse, scale=scale)
+    si.si_kv_accumulate(kv, q, lse, scale=scale)
+    got = acc[0, :, 0].cpu()
+    assert bool(t.isfinite(got).all())
+    assert got[0, 0] == 0 and bool(((got[0, 1:] - heads / 3).abs() < 1e-5 * heads).all())
+    assert bool((got[1] == got[1, 0]).all()) and heads / 4 <= float(got[1, 0]) <= heads
+    assert bool((got[2] == 0).all())
+
+
 def test_attention_weights_sum_to_rows(si):
     """The weights of one call's own lse add up to the number of its rows."""
     c = Cache(si, 32, [777], 9, 2, 128, "bf16")

@@ -58,6 +58,7 @@ __global__ void __launch_bounds__(kThreads, AttendCfg<DP>::kCtas)
     constexpr int KD = DP / 16;          // k steps over D
     constexpr int UNITS = Cp::UNITS;
     constexpr int S = Cfg::kStages;
+    using Wt = Weights<FP16, false>;
     static_assert(WK == 16 * MW, "a group's warps copy sixteen keys each");
 
     extern __shared__ __align__(128) uint8_t smem[];
@@ -265,7 +266,7 @@ __global__ void __launch_bounds__(kThreads, AttendCfg<DP>::kCtas)
             for (int n = 0; n < NS; ++n) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    s[n][e] = ex2((s[n][e] - shift[e >> 1]) * c2);
+                    s[n][e] = ex2(fmaf(s[n][e] - shift[e >> 1], c2, Wt::kUp));
                     sum[e >> 1] += s[n][e];
                 }
             }
@@ -391,7 +392,7 @@ __global__ void __launch_bounds__(kThreads, AttendCfg<DP>::kCtas)
                                 empty ? 0u : pack<FP16>(o[i][2 * e] * inv, o[i][2 * e + 1] * inv);
                     }
                     if (P.lse && (lane & 3) == 0)
-                        P.lse[at] = empty ? -INFINITY : lse_of(mx[e], P.scale, sum[e]);
+                        P.lse[at] = empty ? -INFINITY : lse_of(mx[e], P.scale, sum[e] * Wt::kDown);
                 }
             } else {
                 float* part = P.part + ((long long)blockIdx.x * 2 + (segment ? 1 : 0)) * part_floats(RB, DP);
@@ -528,7 +529,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
         }
         static_cast<uint16_t*>(P.out)[at * D + d] = bits;
     }
-    if (P.lse && lane == 0) P.lse[at] = empty ? -INFINITY : lse_of(top, P.scale, sum);
+    if (P.lse && lane == 0) P.lse[at] = empty ? -INFINITY : lse_of(top, P.scale, sum * Weights<FP16, (RB >= 128)>::kDown);
 }
 
 // ------------------------------------------------------------------ host

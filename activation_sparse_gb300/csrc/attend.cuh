@@ -65,6 +65,18 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
+// fp16's normal range ends at 2^-14: beside one key that has nearly all of the weight, the others' weights, all of the
+// output where that key's value is small, would keep a few bits each (3000 keys at e^-14 of the largest: 4 % off).
+// So fp16 weights are taken times 2^15, the most that the type holds, and their sums come out the same power
+// larger; the output's quotient does not see it. Where a row's maximum may be outgrown by 2^kLazy before its
+// weights are rescaled, the power is that much less. bf16 has fp32's range.
+template <bool FP16, bool LAZY>
+struct Weights {
+    static constexpr int kLazy = !LAZY ? 0 : FP16 ? 4 : 8;
+    static constexpr float kUp = FP16 ? 15 - kLazy : 0;  // added to the exponent
+    static constexpr float kDown = FP16 ? 1.0f / (1 << (15 - kLazy)) : 1.0f;  // of the sums
+};
+
 // log of sum * exp(scale * score). The product is rounded by itself, as where a key's weight is taken: whatever
 // the scores' size, scale * score and lse then differ by log(sum) alone.
 __device__ __forceinline__ float lse_of(float score, float scale, float sum) {

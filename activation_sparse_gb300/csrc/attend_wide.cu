@@ -12,9 +12,9 @@
 // product), 1.1 us a tile with all work taken out. The value tile serves as
 // it lies, [key][d], as an operand with d contiguous.
 // The reference m of a row moves only when the maximum outgrows it by a
-// factor of 2^8: weights up to 256 are as exact in 16 bits as weights up to
-// 1, and the sums are in 32 bits, so the output is rescaled a few times a
-// list instead of once a tile.
+// factor of 2^8 (fp16: 2^4, see Weights): weights up to 256 are as exact in 16
+// bits as weights up to 1, and the sums are in 32 bits, so the output is
+// rescaled a few times a list instead of once a tile.
 //
 // Four warps a block do its softmax and output (TMEM lanes 32 w ..), one warp
 // issues the matrix instructions, four copy keys and values through the slot
@@ -178,9 +178,9 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
     return d;
 }
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
     uint64_t d;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
     return d;
 }
 
@@ -195,6 +195,7 @@ __global__ void __launch_bounds__(WideCfg<DP, NB>::kThreads, WideCfg<DP, NB>::kC
     using Cfg = WideCfg<DP, NB>;
     constexpr int kThreads = Cfg::kThreads, kMaxSlots = Cfg::kMaxSlots;
     using Cp = Copy<DP>;
+    using Wt = Weights<FP16, true>;
     extern __shared__ __align__(1024) uint8_t smem[];  // the swizzle needs tiles on 1024-byte boundaries
     uint8_t* const q_s = smem;
     uint8_t* const ring = smem + Cfg::kOffRing;
@@ -505,7 +506,7 @@ __global__ void __launch_bounds__(WideCfg<DP, NB>::kThreads, WideCfg<DP, NB>::kC
                 float keep = 1.0f;
                 if (ref == -INFINITY) {
                     ref = top;  // nothing seen so far, O's row is 0
-                } else if ((top - ref) * c2 > 8.0f) {
+                } else if ((top - ref) * c2 > (float)Wt::kLazy) {
                     keep = ex2((ref - top) * c2);
                     ref = top;
                     sum *= keep;
@@ -527,7 +528,7 @@ __global__ void __launch_bounds__(WideCfg<DP, NB>::kThreads, WideCfg<DP, NB>::kC
                     tc_fence_before();
                 }
                 const float shift = ref == -INFINITY ? 0.0f : ref;
-                const uint64_t shift2 = both(-shift, -shift), scale2 = both(c2, c2);
+                const uint64_t shift2 = both(-shift, -shift), scale2 = both(c2, c2), up2 = both(Wt::kUp, Wt::kUp);
                 uint64_t sum2 = 0;
 #pragma unroll
                 for (int half = 1; half >= 0; --half) {  // the second half is still in registers
@@ -545,7 +546,7 @@ __global__ void __launch_bounds__(WideCfg<DP, NB>::kThreads, WideCfg<DP, NB>::kC
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
                         float p0, p1;
-                        split(mul2(add2(both(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), shift2), scale2),
+                        split(fma2(add2(both(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), shift2), scale2, up2),
                               p0, p1);
                         p0 = ex2(p0), p1 = ex2(p1);
                         sum2 = add2(sum2, both(p0, p1));
@@ -636,7 +637,7 @@ __global__ void __launch_bounds__(WideCfg<DP, NB>::kThreads, WideCfg<DP, NB>::kC
                     part[Cfg::kRows * DP + r] = ref;
                     part[Cfg::kRows * DP + Cfg::kRows + r] = sum;
                 } else if (P.lse) {
-                    P.lse[at] = empty_row ? -INFINITY : lse_of(ref, P.scale, sum);
+                    P.lse[at] = empty_row ? -INFINITY : lse_of(ref, P.scale, sum * Wt::kDown);
                 }
             }
         }

@@ -423,6 +423,34 @@ def test_attention_odd_values_stay_with_their_branch(si, dtype, D, T, Hq):
     assert (host(base)[0].transpose(0, 2, 1)[ok] == got[ok]).all()
 
 
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("n,T,G,Hkv,D", [
+    (3000, 1, 4, 1, 64), (3000, 2, 8, 1, 128), (3000, 3, 4, 1, 256), (3000, 8, 4, 1, 128), (3000, 40, 4, 1, 64),
+    (400, 1, 2, 320, 64), (400, 2, 2, 160, 256), (400, 6, 3, 320, 64)])  # whole lists in a block
+@pytest.mark.parametrize("place,above", [(0.0, 9.0), (0.0, 12.3), (0.0, 14.2), (0.5, 14.2), (1.0, 12.3)])
+def test_attention_one_key_takes_nearly_all(si, dtype, n, T, G, Hkv, D, place, above):
+    """One key far above the others and with a value of 0: the output is what the others give, each with a weight
+    far below the largest, as exact as the type."""
+    t = torch()
+    at = int(place * (n - 1))
+    rng = np.random.default_rng(64)
+    K, V = (t.zeros(1, 1, Hkv, n + T, D, dtype=tdtype(dtype), device="cuda") for _ in range(2))
+    V[0, 0, :, :n] = gpu(1 + rng.random((Hkv, n, D)) / 4, V.dtype)
+    K[0, 0, :, at, 0], V[0, 0, :, at] = above, 0
+    kv = si.si_kv_create(K, V, None, t.full((1, 1), n, dtype=t.int32, device="cuda"))
+    q = t.zeros(1, T, Hkv * G, D, dtype=tdtype(dtype), device="cuda")
+    q[..., 0] = gpu(1 - 0.0625 * (np.arange(Hkv * G) % G), q.dtype)
+    out, lse = t.empty_like(q), t.empty(1, T, Hkv * G, device="cuda")
+    si.si_tree_attention(kv, q, out, lse=lse, scale=1.0)
+    want, lse_w, mag = ref.attend(host(q), host(K[0]), host(V[0]), None, [n], ref.chain(1, T), 1.0)
+    e = (D / 16 + 8) * 2.0 ** -23 * above + 2.0 ** -19
+    tol = ref.U[dtype] * (mag + np.abs(want)) + 2 * e * mag + 2.0 ** -30
+    if dtype == "fp16":
+        tol += 2.0 ** -25 * (np.abs(want) < 2.0 ** -13)  # an output below the type's normal range
+    assert (np.abs(host(out) - want) <= tol).all(), (np.abs(host(out) - want) / mag).max()
+    assert (np.abs(host(lse) - lse_w) <= e + 2.0 ** -21 * (1 + np.abs(lse_w))).all()
+
+
 def test_attention_strides(si):
     """Keys and values inside one interleaved pool, queries inside a fused projection."""
     t = torch()

@@ -58,6 +58,7 @@ __global__ void __launch_bounds__(kThreads, AttendCfg<DP>::kCtas)
     constexpr int KD = DP / 16;          // k steps over D
     constexpr int UNITS = Cp::UNITS;
     constexpr int S = Cfg::kStages;
+    constexpr bool TWO = MW == 1;        // terms of a weight
     using Wt = Weights<FP16, false>;
     static_assert(WK == 16 * MW, "a group's warps copy sixteen keys each");
 
@@ -272,15 +273,25 @@ __global__ void __launch_bounds__(kThreads, AttendCfg<DP>::kCtas)
             }
 #pragma unroll
             for (int n = 0; n < NS; n += 2) {
-                // the weights are rounded to the cache's type here: the matrix product takes both sides in one type
-                const uint32_t pf[4] = {pack<FP16>(s[n][0], s[n][1]), pack<FP16>(s[n][2], s[n][3]),
-                                        pack<FP16>(s[n + 1][0], s[n + 1][1]), pack<FP16>(s[n + 1][2], s[n + 1][3])};
+                // The matrix product takes both sides in one type. With up to 16 rows a key, bound by memory, a weight
+                // goes in as two terms of it, the second what the first one's rounding left: good to U^2 for a rounding
+                // of U. (One term / two: 8 sequences of 8192 keys, 8 heads of 128, 16 rows 60.7 / 61.3 us; with more rows
+                // the products bound it, 4 of 8192, 4 heads of 256, 64 rows 79 / 94, and one rounding is left.)
+                uint32_t pf[4], pr[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float a = s[n + (e >> 1)][(e & 1) * 2], b = s[n + (e >> 1)][(e & 1) * 2 + 1];
+                    pf[e] = pack<FP16>(a, b);
+                    if (TWO) pr[e] = pack<FP16>(a - widen<FP16>((uint16_t)pf[e]), b - widen<FP16>((uint16_t)(pf[e] >> 16)));
+                }
 #pragma unroll
                 for (int i = 0; i < DP / 8; i += 2) {
                     uint32_t vf[4];
                     ldsm4t(vf, v_s + tile_at<DP>(key0 + n * 8 + (lane & 15), i + (lane >> 4)));
                     mma<FP16>(o[i], pf, vf[0], vf[1]);
                     mma<FP16>(o[i + 1], pf, vf[2], vf[3]);
+                    if (TWO) mma<FP16>(o[i], pr, vf[0], vf[1]);
+                    if (TWO) mma<FP16>(o[i + 1], pr, vf[2], vf[3]);
                 }
             }
             if (meets_new && *odd_s) {

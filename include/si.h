@@ -591,9 +591,10 @@ int si_kv_append(si_kv *kv, int layer, const si_rope *rope, int T, int Hq,
  *   scale > 0 multiplies the products; out [B][T][Hq][D] contiguous, in the
  *   cache's type (may not be q); lse (optional) fp32 [B][T][Hq]: the log of
  *   the sum of exp(scale * q.k) over the keys seen.
- * Products and sums in fp32 on the tensor cores; the softmax weights are
- * rounded to the cache's type for the product with v. Results do not depend
- * on timing. Requires Hq % Hkv == 0, 1 <= T <= 64. A sequence with
+ * Products and sums in fp32 on the tensor cores. For the product with v the
+ * softmax weights are carried in two terms of the cache's type where a key
+ * meets up to 16 rows (T * Hq / Hkv), and rounded to it once where it meets
+ * more. Results do not depend on timing. Requires Hq % Hkv == 0, 1 <= T <= 64. A sequence with
  * len + T > cap sets SI_DEVERR_CACHE and gets zeros. */
 int si_tree_attention(si_kv *kv, int layer, int T, int Hq, const void *q, const long long *q_stride,
                       const uint64_t *mask, float scale, void *out, float *lse, void *stream);

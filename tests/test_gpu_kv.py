@@ -451,6 +451,32 @@ def test_attention_one_key_takes_nearly_all(si, dtype, n, T, G, Hkv, D, place, a
     assert (np.abs(host(lse) - lse_w) <= e + 2.0 ** -21 * (1 + np.abs(lse_w))).all()
 
 
+@pytest.mark.parametrize("lens,T,Hq,Hkv,D,dtype,table", [
+    ([40], 1, 8, 2, 64, "bf16", True),
+    ([1000], 1, 32, 8, 64, "bf16", True),
+    ([130, 7, 700], 4, 8, 2, 128, "bf16", True),
+    ([20], 16, 2, 2, 128, "bf16", False),
+    ([64], 2, 16, 2, 80, "fp16", True),
+    ([100, 30], 4, 8, 2, 256, "bf16", True),
+    ([5000], 1, 8, 1, 128, "fp16", False),
+])
+def test_attention_few_rows_rounds_the_output_alone(si, lens, T, Hq, Hkv, D, dtype, table):
+    """Up to 16 rows a key: a weight is carried in two terms of the type, so it is good to
+    U^2 and what is left is the output's own rounding. Sums in fp32: an addition a step of sixteen keys."""
+    t = torch()
+    c = Cache(si, 65, lens, T, Hkv, D, dtype, table=table)
+    q, words, mask = make_rows(c, T, Hq, D, dtype, "tree")
+    out = t.empty_like(q)
+    si.si_tree_attention(c.kv, q, out, mask=mask)
+    K, V, tab = c.args()
+    want, _, mag = ref.attend(host(q), K, V, tab, c.lens_h, words, D ** -0.5)
+    u, n = ref.U[dtype], max(lens) + T
+    e = score_error(host(q), K, D, D ** -0.5) + 2.0 ** -19
+    err = (u * u + 2 * e + (n / 16 + 16) * 2.0 ** -23) * mag
+    tol = u * (np.abs(want) + err) + err + 2.0 ** -25
+    assert (np.abs(host(out) - want) <= tol).all(), (np.abs(host(out) - want) - tol).max()
+
+
 def test_attention_strides(si):
     """Keys and values inside one interleaved pool, queries inside a fused projection."""
     t = torch()

@@ -512,6 +512,8 @@ cudaError_t launch_kv_append(const KvAppendParams& P, const RopeTable& R, cudaSt
 
 cudaError_t launch_kv_evict(const KvEvictParams& P, cudaStream_t st) {
     const long long rows = (long long)P.L * P.B * P.Hkv;
+    const int sms = sm_count();
+    if (sms < 1) return cudaErrorInvalidDevice;
     // CTAs a list (at most eight, the portable cluster). Few enough candidates each that three CTAs share an
     // SM where eight CTAs can do that (64 lists of up to 100001: 78 us, 96 with twice the candidates each). Where
     // the lists alone do not fill the GPU, lists above 6144 are split down to 3200 each: a cluster's barriers
@@ -519,13 +521,13 @@ cudaError_t launch_kv_evict(const KvEvictParams& P, cudaStream_t st) {
     // of 8000, in two / in four: 12.1 / 10.6; 128 lists of 4096, whole / in four: 14.5 / 18.1).
     int cs = 1;
     auto each = [&]() { return ((P.cap + cs - 1) / cs + 127) & ~127; };
-    while (cs < 8 && (each() > 12544 || (P.cap > 6144 && each() > 3200 && rows * cs <= 152))) cs *= 2;
+    while (cs < 8 && (each() > 12544 || (P.cap > 6144 && each() > 3200 && rows * cs <= sms))) cs *= 2;
     const int chunk = each();
     if (chunk > kEvictChunk) return cudaErrorInvalidValue;
     // 512 threads where the CTAs all run at once, three an SM, or hold much each; else 256, of which six fit.
     // 512 / 256: eight lists of 1025 5.9 / 6.6 us, 256 of 4096 16.0 / 22.4, 320 of 2000 12.6 / 15.1, 448 of 2000
     // 12.5 / 11.6, 896 of 2000 22.3 / 16.3, of 4096 28.9 / 25.1, of 6000 36.1 / 48.8.
-    const bool wide = chunk > 5120 || rows * cs <= 456;
+    const bool wide = chunk > 5120 || rows * cs <= 3 * sms;
     const size_t smem = sizeof(EvictShared) + (size_t)chunk * 4;
     if (P.in_place)
         return wide ? launch_evict<512, true>(P, (unsigned)(rows * cs), cs, smem, st)

@@ -19,4 +19,12 @@ __device__ __forceinline__ int div_of(int a, int b) {
     return q;
 }
 
+// SMs of the current device (0: cannot be asked).
+inline int sm_count() {
+    int dev = 0, sms = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+    if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+    return sms;
+}
+
 }  // namespace si

@@ -628,6 +628,15 @@ long long attend_partial_floats(int D) {
     return 2ll * sm_count() * per_sm(dp) * part_floats(16 * row_warps(INT_MAX), dp);
 }
 
+bool attend_counts_fit(const AttendParams& P) {
+    constexpr long long kMost = INT_MAX - (1 << 20);  // room for a grid and a tile beside them
+    const int R = P.T * P.G;
+    const int rows = many_rows(P.c.D, R) ? wide_rows(R) : 16 * (padded(P.c.D) > 128 ? row_warps(R) : 1);
+    const long long lists = (long long)P.c.B * P.c.Hkv * ((R + rows - 1) / rows);
+    const long long tiles = (long long)P.c.cap / KT + 1;
+    return P.c.cap <= kMost && lists <= kMost / tiles && lists <= kMost / rows;
+}
+
 cudaError_t launch_tree_attention(const AttendParams& P, cudaStream_t st) {
     if (many_rows(P.c.D, P.T * P.G)) return launch_wide(P, st);
     return P.c.fp16 ? launch_attend_type<true>(P, st) : launch_attend_type<false>(P, st);

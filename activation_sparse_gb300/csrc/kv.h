@@ -78,6 +78,8 @@ struct AttendParams {
 };
 // Scratch floats that launch_tree_attention needs at most for heads of D elements (0: cannot query the device).
 long long attend_partial_floats(int D);
+// Whether the kernels' 32-bit counts hold every tile of 64 keys of every list's row blocks, and the join's blocks.
+bool attend_counts_fit(const AttendParams& P);
 cudaError_t launch_tree_attention(const AttendParams& P, cudaStream_t st);
 // attend_wide.cu: the first of the two kernels for many rows; says how it cut the work for the join.
 cudaError_t launch_tree_attention_wide(const AttendParams& P, int* row_blocks, int* parts, cudaStream_t st);

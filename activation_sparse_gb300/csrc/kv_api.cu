@@ -243,6 +243,8 @@ int si_kv_append(si_kv* kv, int layer, const si_rope* rope, int T, int Hq, const
         (Hq > 0 && (!aligned16(q) || !aligned16(q_out) || !strides_ok(q_stride, 3))))
         return fail(SI_ERR_INVALID_ARG, "q, k, v, q_out must be 16-byte aligned with strides that are multiples of 8");
     if ((long long)d.B * T > 0x7FFFFFFFLL) return fail(SI_ERR_UNSUPPORTED, "B * T exceeds 2^31 - 1");
+    if (((long long)Hq + 2ll * d.Hkv) * (d.D / 8) > 0x7FFF0000LL)
+        return fail(SI_ERR_UNSUPPORTED, "a token's heads exceed 32-bit counts");
     si::KvAppendParams P = {};
     P.c = view_of(d, layer);
     P.T = T, P.Hq = Hq;
@@ -267,6 +269,7 @@ int si_tree_attention(si_kv* kv, int layer, int T, int Hq, const void* q, const 
     if (out == q) return fail(SI_ERR_INVALID_ARG, "out may not be q");
     if (!aligned16(out)) return fail(SI_ERR_INVALID_ARG, "out must be 16-byte aligned");
     si::AttendParams P = rows_of(kv, layer, T, Hq, q, q_stride, mask, scale);
+    if (!si::attend_counts_fit(P)) return fail(SI_ERR_UNSUPPORTED, "lists, row blocks and entries exceed 32-bit counts");
     P.out = out;
     P.lse = lse;
     if ((rc = on_device(kv))) return rc;
@@ -286,6 +289,7 @@ int si_kv_accumulate(si_kv* kv, int layer, int T, int Hq, const void* q, const l
     if (!lse) return fail(SI_ERR_INVALID_ARG, "NULL pointer");
     if (!kv->d.acc) return fail(SI_ERR_INVALID_ARG, "the cache has no acc");
     si::AttendParams P = rows_of(kv, layer, T, Hq, q, q_stride, mask, scale);
+    if (!si::attend_counts_fit(P)) return fail(SI_ERR_UNSUPPORTED, "lists, row blocks and entries exceed 32-bit counts");
     P.lse = const_cast<float*>(lse);
     P.rows = reinterpret_cast<const unsigned long long*>(rows);
     P.acc_out = acc_out ? acc_out : P.c.acc;

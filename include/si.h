@@ -594,8 +594,10 @@ int si_kv_append(si_kv *kv, int layer, const si_rope *rope, int T, int Hq,
  * Products and sums in fp32 on the tensor cores. For the product with v the
  * softmax weights are carried in two terms of the cache's type where a key
  * meets up to 16 rows (T * Hq / Hkv), and rounded to it once where it meets
- * more. Results do not depend on timing. Requires Hq % Hkv == 0, 1 <= T <= 64. A sequence with
- * len + T > cap sets SI_DEVERR_CACHE and gets zeros. */
+ * more. Results do not depend on timing. Requires Hq % Hkv == 0,
+ * 1 <= T <= 64; SI_ERR_UNSUPPORTED where lists (B * Hkv), blocks of 16 to
+ * 256 rows of a list and tiles of 64 entries (cap) multiply past 32 bits. A
+ * sequence with len + T > cap sets SI_DEVERR_CACHE and gets zeros. */
 int si_tree_attention(si_kv *kv, int layer, int T, int Hq, const void *q, const long long *q_stride,
                       const uint64_t *mask, float scale, void *out, float *lse, void *stream);
 

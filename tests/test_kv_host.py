@@ -129,6 +129,27 @@ def test_calls_refuse(si):
         assert lib.si_kv_destroy(h) == si.SI_OK
 
 
+def test_calls_beyond_32_bit_counts_refuse(si):
+    """More tiles, lists or units than the kernels' 32-bit counts hold are refused before anything is launched."""
+    lib = si.load()
+    p, s3 = 1 << 20, (C.c_longlong * 3)(0, 0, 0)
+    none = dict(k_stride=(0, 0, 0, 8), v_stride=(0, 0, 0, 8), table_stride=(0, 0, 0), acc_stride=(0, 0, 0))
+    rope = si.si_rope_create(64)
+    for over, T, G in ((dict(B=1024, Hkv=1024, cap=200000, n_slots=200000), 1, 1),
+                       (dict(B=1024, Hkv=1024, cap=64, n_slots=64, D=256), 64, 256),
+                       (dict(B=1, Hkv=1, cap=(1 << 31) - 1, n_slots=(1 << 31) - 1), 1, 1)):
+        rc, kv = make(si, **over, **none)
+        assert rc == si.SI_OK
+        Hq = over["Hkv"] * G
+        assert lib.si_tree_attention(kv, 0, T, Hq, p, s3, None, 0.1, p + 4096, None, None) == si.SI_ERR_UNSUPPORTED
+        if G == 1:
+            assert lib.si_kv_accumulate(kv, 0, T, Hq, p, s3, p, None, None, 0.1, None, None) == si.SI_ERR_UNSUPPORTED
+        assert lib.si_kv_destroy(kv) == si.SI_OK
+    rc, kv = make(si)
+    assert lib.si_kv_append(kv, 0, rope.handle, 1, (1 << 31) - 1, p, s3, p, s3, p, s3, p, p, None) == si.SI_ERR_UNSUPPORTED
+    assert lib.si_kv_destroy(kv) == si.SI_OK
+
+
 def test_python_checks(si):
     torch = pytest.importorskip("torch")
     K = torch.zeros(1, 1, 2, 8, 64, dtype=torch.bfloat16)

@@ -730,8 +730,8 @@ def si_kv_accumulate(kv: KV, q, lse, mask=None, rows=None, scale=None, acc_out=N
     ap = None
     if acc_out is not None:
         ap = _dev(acc_out, torch.float32, "acc_out")
-        if kv.acc is None or acc_out.shape[-3:] != kv.acc.shape[1:] or acc_out.stride()[-3:] != kv.acc.stride()[1:] \
-                or acc_out.numel() != B * kv.Hkv * kv.n_slots:
+        if kv.acc is None or acc_out.shape[-3:] != kv.acc.shape[1:] or acc_out.numel() != B * kv.Hkv * kv.n_slots \
+                or any(n > 1 and x != y for n, x, y in zip(acc_out.shape[-3:], acc_out.stride()[-3:], kv.acc.stride()[1:])):
             raise ValueError("acc_out must have the shape and strides of one layer of the cache's acc")
     rc = _lib.si_kv_accumulate(kv._h, layer, T, hq, qp, qs, _whole(lse, torch.float32, "lse", (B, T, hq)),
                                _whole(mask, torch.int64, "mask", (B, T)), _whole(rows, torch.int64, "rows", (B,)),

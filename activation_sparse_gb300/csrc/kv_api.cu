@@ -37,11 +37,20 @@ bool capturing(cudaStream_t st) {
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-bool strides_ok(const long long* s, int n) {
-    for (int i = 0; i < n; ++i)
-        if (s[i] < 0 || s[i] % 8) return false;
-    return true;
-}
+// Strides of an array of these extents. What stands at a dimension of one element is not looked at (tensors from
+// elsewhere may hold anything there) and taken as 0.
+struct Strides {
+    long long at[4] = {};
+    template <int N>
+    Strides(const long long* s, const long long (&extents)[N]) {
+        for (int i = 0; i < N; ++i) at[i] = extents[i] == 1 ? 0 : s[i];
+    }
+    bool whole_units() const {
+        for (long long s : at)
+            if (s < 0 || s % 8) return false;
+        return true;
+    }
+};
 
 }  // namespace
 
@@ -140,7 +149,7 @@ int check_rows(const si_kv* kv, int layer, int T, int Hq, const void* q, const l
     if (T > kv->d.cap) return fail(SI_ERR_INVALID_ARG, "T exceeds the cache's entries");
     if (Hq < 1 || Hq % kv->d.Hkv) return fail(SI_ERR_INVALID_ARG, "need Hq a multiple of Hkv");
     if (Hq / kv->d.Hkv > 256) return fail(SI_ERR_UNSUPPORTED, "more than 256 query heads per cache head");
-    if (!aligned16(q) || !strides_ok(q_stride, 3))
+    if (!aligned16(q) || !Strides(q_stride, {kv->d.B, T, Hq}).whole_units())
         return fail(SI_ERR_INVALID_ARG, "q must be 16-byte aligned with strides that are multiples of 8");
     if (!(scale > 0.0f) || !std::isfinite(scale)) return fail(SI_ERR_INVALID_ARG, "need a finite scale > 0");
     return SI_OK;
@@ -152,7 +161,8 @@ si::AttendParams rows_of(const si_kv* kv, int layer, int T, int Hq, const void* 
     P.c = view_of(kv->d, layer);
     P.T = T, P.Hq = Hq, P.G = Hq / kv->d.Hkv;
     P.q = q;
-    P.qb = q_stride[0], P.qt = q_stride[1], P.qh = q_stride[2];
+    const Strides qs(q_stride, {kv->d.B, T, Hq});
+    P.qb = qs.at[0], P.qt = qs.at[1], P.qh = qs.at[2];
     P.mask = reinterpret_cast<const unsigned long long*>(mask);
     P.scale = scale;
     return P;
@@ -174,16 +184,22 @@ int si_kv_create(const si_kv_desc* desc, si_kv** out) {
     if (d.B > 1024) return fail(SI_ERR_UNSUPPORTED, "more than 1024 sequences");
     if (d.Hkv > 1024) return fail(SI_ERR_UNSUPPORTED, "more than 1024 cache heads");
     if (d.n_slots > 0x7FFFFFFFLL) return fail(SI_ERR_INVALID_ARG, "slots are int32: n_slots is too large");
-    if (!aligned16(d.k) || !aligned16(d.v) || !strides_ok(d.k_stride, 4) || !strides_ok(d.v_stride, 4))
+    const long long pool[4] = {d.L, d.B, d.Hkv, d.n_slots}, lists[3] = {d.L, d.B, d.Hkv};
+    const Strides ks(d.k_stride, pool), vs(d.v_stride, pool), ts(d.table_stride, lists), as(d.acc_stride, lists);
+    if (!aligned16(d.k) || !aligned16(d.v) || !ks.whole_units() || !vs.whole_units())
         return fail(SI_ERR_INVALID_ARG, "k and v must be 16-byte aligned with strides that are multiples of 8");
-    if (d.k_stride[3] > 0x7FFFFFFFLL || d.v_stride[3] > 0x7FFFFFFFLL)
+    if (ks.at[3] > 0x7FFFFFFFLL || vs.at[3] > 0x7FFFFFFFLL)
         return fail(SI_ERR_UNSUPPORTED, "a slot stride exceeds 2^31 - 1 elements");
     if (!d.table && d.cap > d.n_slots) return fail(SI_ERR_INVALID_ARG, "without a table cap must not exceed n_slots");
     for (int i = 0; i < 3; ++i)
-        if (d.table_stride[i] < 0 || d.acc_stride[i] < 0) return fail(SI_ERR_INVALID_ARG, "negative stride");
+        if (ts.at[i] < 0 || as.at[i] < 0) return fail(SI_ERR_INVALID_ARG, "negative stride");
     si_kv* kv = new (std::nothrow) si_kv;
     if (!kv) return fail(SI_ERR_OOM, "out of host memory");
     kv->d = d;
+    std::memcpy(kv->d.k_stride, ks.at, sizeof d.k_stride);
+    std::memcpy(kv->d.v_stride, vs.at, sizeof d.v_stride);
+    std::memcpy(kv->d.table_stride, ts.at, sizeof d.table_stride);
+    std::memcpy(kv->d.acc_stride, as.at, sizeof d.acc_stride);
     *out = kv;
     return SI_OK;
 }
@@ -239,8 +255,10 @@ int si_kv_append(si_kv* kv, int layer, const si_rope* rope, int T, int Hq, const
     if (layer < 0 || layer >= d.L) return fail(SI_ERR_INVALID_ARG, "layer outside the cache");
     if (T < 1 || T > d.cap) return fail(SI_ERR_INVALID_ARG, "need 1 <= T <= cap");
     if (2 * rope->t.n_pairs > d.D) return fail(SI_ERR_INVALID_ARG, "the rotary pairs exceed D");
-    if (!aligned16(k) || !aligned16(v) || !strides_ok(k_stride, 3) || !strides_ok(v_stride, 3) ||
-        (Hq > 0 && (!aligned16(q) || !aligned16(q_out) || !strides_ok(q_stride, 3))))
+    static const long long none[3] = {};
+    const Strides qs(Hq > 0 ? q_stride : none, {d.B, T, Hq}), ks(k_stride, {d.B, T, d.Hkv}), vs(v_stride, {d.B, T, d.Hkv});
+    if (!aligned16(k) || !aligned16(v) || !ks.whole_units() || !vs.whole_units() ||
+        (Hq > 0 && (!aligned16(q) || !aligned16(q_out) || !qs.whole_units())))
         return fail(SI_ERR_INVALID_ARG, "q, k, v, q_out must be 16-byte aligned with strides that are multiples of 8");
     if ((long long)d.B * T > 0x7FFFFFFFLL) return fail(SI_ERR_UNSUPPORTED, "B * T exceeds 2^31 - 1");
     if (((long long)Hq + 2ll * d.Hkv) * (d.D / 8) > 0x7FFF0000LL)
@@ -249,9 +267,9 @@ int si_kv_append(si_kv* kv, int layer, const si_rope* rope, int T, int Hq, const
     P.c = view_of(d, layer);
     P.T = T, P.Hq = Hq;
     P.q = q, P.k = k, P.v = v;
-    if (Hq > 0) P.qb = q_stride[0], P.qt = q_stride[1], P.qh = q_stride[2];
-    P.kb = k_stride[0], P.kt = k_stride[1], P.kh = k_stride[2];
-    P.vb = v_stride[0], P.vt = v_stride[1], P.vh = v_stride[2];
+    P.qb = qs.at[0], P.qt = qs.at[1], P.qh = qs.at[2];
+    P.kb = ks.at[0], P.kt = ks.at[1], P.kh = ks.at[2];
+    P.vb = vs.at[0], P.vt = vs.at[1], P.vh = vs.at[2];
     P.pos = pos;
     P.q_out = q_out;
     const int rc = si::device_error_word(&P.err);

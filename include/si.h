@@ -520,6 +520,7 @@ typedef struct si_rope si_rope;
 
 /* Memory of a cache (the caller's, kept alive as long as the handle).
  * Strides are in elements; the last dimension of every array is contiguous.
+ * The stride of a dimension of one element does not matter, here and below.
  *   k_stride / v_stride  {layer, sequence, head, slot}, multiples of 8 (the
  *     slot's below 2^31); k and v 16-byte aligned. A sequence stride of 0 with tables that share no
  *     slot makes one pool for all sequences.

@@ -495,6 +495,37 @@ def test_attention_strides(si):
     assert t.equal(out, want)
 
 
+def test_strides_of_single_elements(si):
+    """One sequence and one token whose strides there mean nothing, as tensors from elsewhere have them: the same bits."""
+    t = torch()
+    D, n = 64, 30
+    rng = np.random.default_rng(66)
+    rope = si.si_rope_create(D)
+
+    def step(odd):
+        """The result with plain strides, or with 1 and 3 in the places that do not matter."""
+        like = lambda x: x.as_strided(x.shape, [(1, 3)[i % 2] if k == 1 else s for i, (k, s) in enumerate(zip(x.shape, x.stride()))]) if odd else x  # noqa: E731
+        K, V = (like(gpu(kv0[i], t.bfloat16)) for i in (0, 1))
+        acc = like(t.zeros(1, 1, 2, n + 1, device="cuda"))
+        table = like(gpu(np.arange(n + 1, dtype=np.int32)[::-1] + np.zeros((1, 1, 2, 1), np.int32)).to(t.int32))
+        lens = gpu(np.array([[n]], np.int32))
+        kv = si.si_kv_create(K, V, table, lens, acc)
+        q, k, v = (like(gpu(x, t.bfloat16)) for x in new)
+        qr, out, lse = t.empty(1, 1, 4, D, dtype=t.bfloat16, device="cuda"), t.empty(1, 1, 4, D, dtype=t.bfloat16, device="cuda"), t.empty(1, 1, 4, device="cuda")
+        si.si_kv_append(kv, rope, q, k, v, t.full((1, 1, 1), 7, dtype=t.int32, device="cuda"), qr)
+        si.si_tree_attention(kv, like(qr), out, lse=lse)
+        more = like(t.zeros(1, 2, n + 1, device="cuda"))
+        si.si_kv_accumulate(kv, like(qr), lse, acc_out=more)
+        si.si_kv_accumulate(kv, like(qr), lse)
+        si.si_kv_evict(kv, 1, 20, sinks=1, recent=2)
+        return [x.contiguous() for x in (K, V, qr, out, lse, more, acc, table, lens)]
+
+    kv0 = rng.standard_normal((2, 1, 1, 2, n + 1, D))
+    new = [rng.standard_normal((1, 1, h, D)) for h in (4, 2, 2)]
+    for a, b in zip(step(False), step(True)):
+        assert t.equal(a, b)
+
+
 @pytest.mark.parametrize("D,pad", [(64, 0), (64, 8), (128, 0), (128, 64), (96, 0)])
 def test_attention_strides_many_rows(si, D, pad):
     """The same with trees of many rows: heads side by side in a slot, with and without room between them."""

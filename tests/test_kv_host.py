@@ -47,6 +47,15 @@ def test_create_refuses(si, over):
     assert si.load().si_last_error_string()
 
 
+def test_strides_of_single_elements_do_not_matter(si):
+    one = dict(L=1, B=1, k_stride=(1, 1, 120 * 64, 64), v_stride=(-3, 1, 120 * 64, 64), table_stride=(1, -1, 100), acc_stride=(-1, 1, 120))
+    rc, h = make(si, **one)
+    assert rc == si.SI_OK and si.load().si_kv_destroy(h) == si.SI_OK
+    assert make(si, **dict(one, B=2))[0] == si.SI_ERR_INVALID_ARG
+    rc, h = make(si, L=1, B=1, Hkv=1, cap=1, n_slots=1, k_stride=(1, 1, 1, 1 << 40), v_stride=(1, 1, 1, 1))
+    assert rc == si.SI_OK and si.load().si_kv_destroy(h) == si.SI_OK
+
+
 def test_create_limits(si):
     assert make(si, B=1025)[0] == si.SI_ERR_UNSUPPORTED
     assert si.load().si_kv_create(None, None) == si.SI_ERR_INVALID_ARG

@@ -359,7 +359,11 @@ int si_kv_evict(si_kv* kv, int layer, int T, const int32_t* path, const int32_t*
         e = cudaMemset(kv->ticket, 0, words * sizeof(unsigned));
         // the memset is on the legacy stream, `stream` may not wait for that one
         if (e == cudaSuccess) e = cudaStreamSynchronize(nullptr);
-        if (e != cudaSuccess) return cuda_fail(e, "cudaMemset");
+        if (e != cudaSuccess) {
+            cudaFree(kv->ticket);  // a ticket that may not be zero is not kept
+            kv->ticket = nullptr;
+            return cuda_fail(e, "cudaMemset");
+        }
     }
     si::KvEvictParams P = {};
     P.table = d.table + first * d.table_stride[0];

@@ -12,8 +12,8 @@
 // do not depend on timing.
 //
 // Bound by memory: one token of 32 heads over 131071 keys of 8 heads of 128
-// takes 90 us, 6.0 TB/s, 0.88 of what a plain copy reaches. Short lists are
-// bound by latency (1000 keys: 9 us with the join).
+// takes 91 us, 6.0 TB/s, 0.88 of what a plain copy reaches. Short lists are
+// bound by latency (1000 keys, heads of 64: 9.5 us with the join).
 #include "attend.cuh"
 
 namespace si {
@@ -326,9 +326,9 @@ __global__ void __launch_bounds__(kThreads, AttendCfg<DP>::kCtas)
             sum[e] += __shfl_xor_sync(0xFFFFFFFFu, sum[e], 2);
         }
 
-        // join the key warps: pairwise through the stage that the next copies do not touch yet
+        // Join the key warps: maxima and sums, then output rows in key-warp order, through the place of this list's
+        // queries, which are no longer needed. (The ring's stages are not touched: the next list's copies are in flight.)
         if (KW > 1) {
-            // q_s holds this list's queries, no longer needed; maxima and sums go there
             __syncthreads();
             float* ms = reinterpret_cast<float*>(q_s);  // [KW][RB][2]
             if ((lane & 3) == 0) {
@@ -353,7 +353,6 @@ __global__ void __launch_bounds__(kThreads, AttendCfg<DP>::kCtas)
                 mx[e] = top;
                 sum[e] = all;
             }
-            // the output rows, summed in key-warp order through shared memory (the queries' place)
             float* acc = reinterpret_cast<float*>(q_s);
             constexpr int kHalf = Cfg::kQBytes / 4 / RB;  // columns that fit at once
             constexpr int COLS = kHalf < DP ? kHalf : DP;
@@ -548,15 +547,15 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
 int per_sm(int dp) { return dp <= 128 ? 2 : 1; }
 int padded(int D) { return D <= 64 ? 64 : D <= 128 ? 128 : 256; }
 // Row warps of heads of more than 128 elements; more rows than 32 go in further row blocks. Four sequences of
-// 8192 keys, 4 heads of 256, one / two: 16 rows 27.4 / 29.7 us, 20 rows 42 / 31, 64 rows 79 / 57.
+// up to 8192 keys, 4 heads of 256, one / two: 16 rows 28.6 / 30.1 us, 20 rows 45 / 31, 64 rows 84 / 54.
 int row_warps(int R) { return R <= 16 ? 1 : 2; }
 
 // Up to 16 rows a key: the tiles above, bound by memory. More rows: 128-row
 // tiles on the tensor memory path, whose cost a key hardly depends on the
-// rows (heads of more than 128 elements do not fit there). 8 sequences of 8192
-// keys, 8 heads of 128, here / there: 16 rows 62 / 60 us, 20 rows 99 / 61, 64
-// rows 179 / 76; one of 30000 keys, heads of 64: 16 rows 19 / 24 us, 20 rows
-// 29 / 24.
+// rows (it is not built for heads of more than 128 elements). 8 sequences of up
+// to 8192 keys, 8 heads of 128, here / there: 16 rows 42.8 / 39.8 us, 20 rows 63
+// / 40, 64 rows 114 / 43; one of 30000 keys, heads of 64: 16 rows 20.0 / 23.3 us,
+// 20 rows 30 / 24.
 bool many_rows(int D, int R) { return R > 16 && D <= 128; }
 
 template <int DP, int RB, bool FP16>
@@ -565,9 +564,9 @@ cudaError_t launch_join(const AttendParams& P, int row_blocks, int parts, cudaSt
     const long long lists = (long long)P.c.B * P.c.Hkv * row_blocks;
     const int rows = P.T * P.G < RB ? P.T * P.G : RB;
     // A block a row (eight warps share its parts) where lists have eight parts and the rows fit the GPU twice
-    // over; else a warp a row. The whole call by the one / the other: 8 lists of 131071 keys, 4 rows 91 / 97 us; 12
-    // of 9001, 128 rows 23.8 / 27.5; 128 of 8192, 4 rows 68.6 / 68.4; 256 of 4096, 4 rows 95 / 91; 32 of 1000, 256
-    // rows 40 / 18; 64 of 8192, 256 rows 133 / 70.
+    // over; else a warp a row. The whole call by the one / the other: 8 lists of 131071 keys, 4 rows 94 / 97 us; 12
+    // of up to 9001, 128 rows 23.7 / 27.3; 128 of 8192, 4 rows 70.0 / 69.7; 256 of 4096, 4 rows 98 / 93; 32 of 1000,
+    // 256 rows 41 / 18; 64 of 8192, 256 rows 134 / 70.
     const bool many = parts >= 8 * lists && lists * rows <= 16ll * sm_count();  // parts of a list: about parts / lists
     const int per_block = many ? 1 : kJoinWarps;
     const long long blocks = lists * ((rows + per_block - 1) / per_block);

@@ -339,11 +339,11 @@ constexpr int part_floats(int rb, int dp) { return rb * (dp + 2); }
 
 // Query rows a CTA of the tensor-memory kernel takes: two blocks of 128 in one CTA an SM copy a tile once, one
 // block leaves room for two CTAs, which copy it twice (64 lists of up to 8192 keys of 128 elements, two blocks /
-// one: 132 rows 60 / 70 us, 256 rows 70 / 78; 8 lists of 2000, 256 rows 21.0 / 20.6).
+// one: 132 rows 61 / 71 us, 256 rows 71 / 79; 8 lists of 2000, 256 rows 21.1 / 20.7).
 inline int wide_rows(int R) { return R <= 128 ? 128 : 256; }
 
 // For it and the narrow kernel, the tiles a part of a list has at least and what a piece of a list costs beside its
-// tiles, in tiles: 128 lists of up to 300 keys, 32 rows, take 19 us, 30 with the shares always across the lists.
+// tiles, in tiles: 128 lists of up to 300 keys, 32 rows, take 18 us, 30 with the shares always across the lists.
 constexpr int kWideLeast = 4, kWidePiece = 6;
 constexpr int kNarrowLeast = 1, kNarrowPiece = 4;
 

@@ -24,12 +24,18 @@
 // where a copy takes four, and was no faster). More than 128 rows go through
 // one CTA an SM with two blocks, which copies a tile once; with one block two
 // CTAs share the SM. 8 trees of 64 nodes x 32 heads over up to 8192 keys of 8
-// heads of 128: 70 us with two blocks, 560 TFLOP/s (78 with one block and every
-// tile copied twice); the tensor pipe is 34 % busy, what bounds it is the
+// heads of 128: 72 us with two blocks, 540 TFLOP/s (79 with one block and every
+// tile copied twice); the tensor pipe is 33 % busy, what bounds it is the
 // softmax's instructions and the waits between the roles. 64 keys take 1.7 us;
-// a list costs some 6 us beside (queries in, rows out). Every write to shared memory is an ordinary
-// one; the issuing warp's proxy fence, after the barrier that announces it,
-// lets the tensor cores see it. All waits are bounded; TMEM is always released.
+// a list costs some 6 us beside (queries in, rows out).
+// P is rounded once to the cache's type: in two terms of it, as the kernel for
+// few rows takes its weights, the output's error against 64 bits would be the
+// output's own rounding alone (fp16 0.00021 instead of 0.00028), but the
+// second terms' instructions lie in the chain that bounds this kernel (72 / 80 us
+// above; 6 trees of 16 nodes, 9001 keys 27.5 / 28.6).
+// Every write to shared memory is an ordinary one; the issuing warp's proxy
+// fence, after the barrier that announces it, lets the tensor cores see it. All
+// waits are bounded; TMEM is always released.
 #include "attend.cuh"
 
 namespace si {
@@ -550,7 +556,7 @@ __global__ void __launch_bounds__(WideCfg<DP, NB>::kThreads, WideCfg<DP, NB>::kC
                               p0, p1);
                         p0 = ex2(p0), p1 = ex2(p1);
                         sum2 = add2(sum2, both(p0, p1));
-                        w[i] = pack<FP16>(p0, p1);  // rounded to the cache's type for the product with V
+                        w[i] = pack<FP16>(p0, p1);  // rounded once, see above
                     }
                     tmem_st16(t_tile + Cfg::kColP + half * 16, w);
                 }

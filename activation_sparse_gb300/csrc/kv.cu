@@ -515,7 +515,7 @@ cudaError_t launch_kv_evict(const KvEvictParams& P, cudaStream_t st) {
     const int sms = sm_count();
     if (sms < 1) return cudaErrorInvalidDevice;
     // CTAs a list (at most eight, the portable cluster). Few enough candidates each that three CTAs share an
-    // SM where eight CTAs can do that (64 lists of up to 100001: 78 us, 96 with twice the candidates each). Where
+    // SM where eight CTAs can do that (64 lists of up to 100001: 73 us, 96 with twice the candidates each). Where
     // the lists alone do not fill the GPU, lists above 6144 are split down to 3200 each: a cluster's barriers
     // cost 2 us, a CTA's further thousand candidates 1 (eight lists of 3000, whole / in two: 7.5 / 8.8 us;
     // of 8000, in two / in four: 12.1 / 10.6; 128 lists of 4096, whole / in four: 14.5 / 18.1).

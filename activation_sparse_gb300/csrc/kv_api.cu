@@ -1,6 +1,6 @@
 // kv_api.cu -- the C ABI of the key/value cache (declared in include/si.h):
 // handles, argument validation and launches. The kernels are in kv.cu (append,
-// evict) and attend.cu (tree attention, weights).
+// evict), attend.cu and attend_wide.cu (tree attention), and weigh.cu (weights).
 #include <cmath>
 #include <cstring>
 #include <new>

@@ -30,8 +30,10 @@ struct WeighCfg {
 // key belongs to one warp, which also copies it and its old weight, so warps
 // only meet when the list (and with it the queries) changes. 8 sequences of up
 // to 16384 keys, 8 heads of 128, four nodes of 32 heads: 36 us, 4.4 TB/s, 0.65
-// of what a plain copy reaches; bound by issue (46 % of the slots with the 12
-// warps that fit an SM; 42 us with eight).
+// of what a plain copy reaches; bound by issue (47 % of the slots with the 12
+// warps that fit an SM; 42 us with eight). Above 64 counted rows a key the
+// queries take turns in shared memory, a block of 64 after another for every
+// tile (the same lists: 64 rows 62 us, 128 rows 210).
 template <int DP, bool FP16>
 __global__ void __launch_bounds__(kThreads, DP <= 128 ? 3 : 1) k_kv_accumulate(const __grid_constant__ AttendParams P) {
     using Cfg = WeighCfg<DP>;

@@ -632,7 +632,7 @@ int si_kv_accumulate(si_kv *kv, int layer, int T, int Hq, const void *q, const l
  * Requires a table; acc when budget > 0; 0 <= sinks, recent and
  * sinks + recent <= budget when budget > 0; cap <= 196608. A sequence whose
  * path or n_path is not valid accepts nothing and sets SI_DEVERR_COUNT; one
- * with len + T > cap is left as it is and sets SI_DEVERR_CACHE. */
+ * with len < 0 or len + T > cap is left as it is and sets SI_DEVERR_CACHE. */
 int si_kv_evict(si_kv *kv, int layer, int T, const int32_t *path, const int32_t *n_path, int budget,
                 int sinks, int recent, int32_t *table_out, int32_t *len_out, void *stream);
 

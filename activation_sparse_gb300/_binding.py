@@ -61,6 +61,7 @@ SIGNATURES = {
     "spax_gate_up": (_i, [_vp, _vp, _vp, _d, _d, _vp, _vp, _vp, _vp]),
     "spax_all_decode": (_i, [_vp, _vp, _vp, _vp, _d, _d, _d, _d, _vp, _vp, _vp]),
     "si_kv_create": (_i, [_vp, C.POINTER(_vp)]),
+    "si_kv_create_e4m3": (_i, [_vp, _vp, C.POINTER(_vp)]),
     "si_kv_destroy": (_i, [_vp]),
     "si_rope_create": (_i, [_i, C.POINTER(_d), C.POINTER(C.c_uint8), _i, _i, C.POINTER(_vp)]),
     "si_rope_destroy": (_i, [_vp]),
@@ -68,9 +69,10 @@ SIGNATURES = {
     "si_tree_attention": (_i, [_vp, _i, _i, _i, _vp, _vp, _vp, C.c_float, _vp, _vp, _vp]),
     "si_kv_accumulate": (_i, [_vp, _i, _i, _i, _vp, _vp, _vp, _vp, _vp, C.c_float, _vp, _vp]),
     "si_kv_evict": (_i, [_vp, _i, _i, _vp, _vp, _i, _i, _i, _vp, _vp, _vp]),
+    "si_token_logprobs": (_i, [_i, _vp, _ll, _i, _i, C.c_float, _vp, _i, _vp, _vp, _i, _vp, _vp, _vp]),
 }
 
-SI_BF16, SI_FP16 = 0, 1
+SI_BF16, SI_FP16, SI_FP32 = 0, 1, 2
 
 
 class KvDesc(C.Structure):
@@ -78,6 +80,12 @@ class KvDesc(C.Structure):
     _fields_ = [("dtype", _i), ("L", _i), ("B", _i), ("Hkv", _i), ("D", _i), ("cap", _i), ("n_slots", _ll),
                 ("k", _vp), ("v", _vp), ("k_stride", _ll * 4), ("v_stride", _ll * 4),
                 ("table", _vp), ("table_stride", _ll * 3), ("len", _vp), ("acc", _vp), ("acc_stride", _ll * 3)]
+
+
+class KvScales(C.Structure):
+    """si_kv_scales of include/si.h."""
+    _fields_ = [("block", _i), ("k", _vp), ("v", _vp), ("k_stride", _ll * 3), ("v_stride", _ll * 3)]
+
 
 _lib = None
 
@@ -580,12 +588,13 @@ class KV:
     """A key/value cache over the caller's tensors (owns the library handle
     and keeps references to the tensors)."""
 
-    def __init__(self, handle, K, V, table, lens, acc):
+    def __init__(self, handle, K, V, table, lens, acc, dtype, k_scale=None, v_scale=None, block=1):
         self._h = handle
         self.K, self.V, self.table, self.lens, self.acc = K, V, table, lens, acc
+        self.k_scale, self.v_scale, self.block = k_scale, v_scale, block
         self.L, self.B, self.Hkv, self.n_slots, self.D = K.shape
         self.cap = table.shape[3] if table is not None else self.n_slots
-        self.dtype = K.dtype
+        self.dtype = dtype  # of q, k, v and out in the calls; of K and V too, where they are not codes
 
     @property
     def handle(self):
@@ -653,15 +662,33 @@ def _rows(t, kv, name, T):
     return t.data_ptr(), _strides(t, name), heads
 
 
-def si_kv_create(K, V, table, lens, acc=None) -> KV:
+def si_kv_create(K, V, table, lens, acc=None, k_scale=None, v_scale=None, block=1, dtype=None) -> KV:
     """A cache over K, V [L][B][Hkv][n_slots][D] (bf16 or fp16), table int32
     [L][B][Hkv][cap] (None: entry i is slot i), lens int32 [L][B] and acc fp32
-    [L][B][Hkv][n_slots] (None: no eviction)."""
+    [L][B][Hkv][n_slots] (None: no eviction).
+
+    K and V of float8_e4m3fn make a cache in 8 bits: k_scale and v_scale
+    [L][B][Hkv][ceil(n_slots / block)] (uint8 or float8_e8m0fnu) are the biased
+    exponents of the blocks' scales, and dtype (bf16 by default, or fp16) is
+    the type of q, k, v and out in the calls. With block = 1 si_kv_append
+    writes a slot's scale, with larger blocks (powers of two) it rounds with
+    the one that is there."""
     torch = _torch()
-    if K.dtype not in (torch.bfloat16, torch.float16):
-        raise ValueError("K must be bf16 or fp16")
+    coded = K.dtype == torch.float8_e4m3fn
+    if coded:
+        dtype = torch.bfloat16 if dtype is None else dtype
+        if dtype not in (torch.bfloat16, torch.float16):
+            raise ValueError("dtype must be bf16 or fp16")
+        if k_scale is None or v_scale is None:
+            raise ValueError("e4m3 codes need k_scale and v_scale")
+    else:
+        if K.dtype not in (torch.bfloat16, torch.float16):
+            raise ValueError("K must be bf16 or fp16, or float8_e4m3fn")
+        if k_scale is not None or v_scale is not None or block != 1 or dtype not in (None, K.dtype):
+            raise ValueError("scales, block and dtype go with K and V of float8_e4m3fn")
+        dtype = K.dtype
     d = KvDesc()
-    d.dtype = SI_FP16 if K.dtype == torch.float16 else SI_BF16
+    d.dtype = SI_FP16 if dtype == torch.float16 else SI_BF16
     d.k = _dev(K, K.dtype, "K", None, 5)
     d.v = _dev(V, K.dtype, "V", K.shape)
     d.L, d.B, d.Hkv, d.n_slots, d.D = K.shape
@@ -678,8 +705,25 @@ def si_kv_create(K, V, table, lens, acc=None) -> KV:
         d.acc = _dev(acc, torch.float32, "acc", K.shape[:4])
         d.acc_stride[:] = acc.stride()[:3]
     h = C.c_void_p()
-    _check(load().si_kv_create(C.byref(d), C.byref(h)))
-    return KV(h, K, V, table, lens, acc)
+    if coded:
+        if block < 1 or block > 2 ** 30 or block & (block - 1):
+            raise ValueError("block must be a power of two, 1 to 2 ** 30")
+        sc = KvScales()
+        sc.block = block
+        blocks = K.shape[:3] + ((K.shape[3] + block - 1) // block,)
+        sc.k, sc.v = _scale(k_scale, "k_scale", blocks), _scale(v_scale, "v_scale", blocks)
+        sc.k_stride[:], sc.v_stride[:] = k_scale.stride()[:3], v_scale.stride()[:3]
+        _check(load().si_kv_create_e4m3(C.byref(d), C.byref(sc), C.byref(h)))
+    else:
+        _check(load().si_kv_create(C.byref(d), C.byref(h)))
+    return KV(h, K, V, table, lens, acc, dtype, k_scale, v_scale, block)
+
+
+def _scale(t, name, shape):
+    torch = _torch()
+    if t.dtype not in (torch.uint8, torch.float8_e8m0fnu):
+        raise ValueError("%s must be uint8 or float8_e8m0fnu" % name)
+    return _dev(t, t.dtype, name, shape)
 
 
 def si_kv_append(kv: KV, rope: Rope, q, k, v, pos, q_out, layer=0, stream=None):
@@ -753,5 +797,43 @@ def si_kv_evict(kv: KV, T, budget, sinks=0, recent=0, path=None, n_path=None, ta
                           _whole(n_path, torch.int32, "n_path", (B,)), budget, sinks, recent,
                           _whole(table_out, torch.int32, "table_out", (kv.L, B, kv.Hkv, kv.cap)),
                           _whole(len_out, torch.int32, "len_out", (kv.L, B)), _stream(stream))
+    if rc:
+        _check(rc)
+
+
+# ------------------------------------------------------- what a step answers with
+
+
+def si_token_logprobs(logits, targets=None, logp=None, entropy=None, top_logp=None, top_ids=None, temperature=1.0,
+                      stream=None):
+    """Log probabilities under logits [N][V] / temperature (bf16, fp16 or
+    fp32; rows may be strided): of targets int32 [N][M] into logp fp32 [N][M]
+    (an id outside the vocabulary: -inf), the rows' entropy fp32 [N], and the
+    K <= 32 best tokens' top_logp fp32 and top_ids int32 [N][K], falling, ties
+    to the lower id. Each output is optional."""
+    torch = _torch()
+    dtype = {torch.bfloat16: SI_BF16, torch.float16: SI_FP16, torch.float32: SI_FP32}.get(logits.dtype)
+    if dtype is None:
+        raise ValueError("logits must be bf16, fp16 or fp32")
+    xp = _dev(logits, logits.dtype, "logits", None, 2)
+    N, V = logits.shape
+    if V < 1:
+        raise ValueError("logits must have at least one column")
+    if (targets is None) != (logp is None) or (top_logp is None) != (top_ids is None):
+        raise ValueError("targets and logp, and top_logp and top_ids, go together")
+    M = K = 0
+    if targets is not None:
+        if targets.dim() != 2:
+            raise ValueError("targets must have shape (N, M)")
+        M = targets.shape[1]
+    if top_ids is not None:
+        if top_ids.dim() != 2:
+            raise ValueError("top_ids must have shape (N, K)")
+        K = top_ids.shape[1]
+    rc = _lib.si_token_logprobs(dtype, xp, logits.stride(0), N, V, temperature,
+                                _whole(targets, torch.int32, "targets", (N, M)), M,
+                                _whole(logp, torch.float32, "logp", (N, M)), _whole(entropy, torch.float32, "entropy", (N,)),
+                                K, _whole(top_logp, torch.float32, "top_logp", (N, K)),
+                                _whole(top_ids, torch.int32, "top_ids", (N, K)), _stream(stream))
     if rc:
         _check(rc)

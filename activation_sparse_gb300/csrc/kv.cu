@@ -15,25 +15,6 @@ namespace {
 
 // ------------------------------------------------------------------ append
 
-template <bool FP16>
-__device__ __forceinline__ float2 unpack2(uint32_t w) {
-    if (FP16) return __half22float2(*reinterpret_cast<const __half2*>(&w));
-    return make_float2(bf_lo(w), bf_hi(w));
-}
-
-template <bool FP16>
-__device__ __forceinline__ uint32_t pack2(float a, float b) {
-    uint32_t w;
-    if (FP16) {
-        const __half2 h = __floats2half2_rn(a, b);
-        w = *reinterpret_cast<const uint32_t*>(&h);
-    } else {
-        const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-        w = *reinterpret_cast<const uint32_t*>(&h);
-    }
-    return w;
-}
-
 // Eight pairs: half-split layout takes a = x[0..7], b = x[n_pairs ..]; the
 // interleaved one has (a, b) alternating through both vectors.
 template <bool FP16>
@@ -77,12 +58,7 @@ __global__ void __launch_bounds__(kAppendThreads)
     const int np = R.n_pairs;
     for (int i = threadIdx.x; i < np; i += kAppendThreads) {
         const long long pos = P.pos[tok * R.n_axes + R.axis[i]];
-        const unsigned long long turn = (unsigned long long)pos * R.turn[i];
-        // signed fraction in half turns: [-1, 1)
-        const float x = (float)(int32_t)(uint32_t)(turn >> 32) * 4.656612873077393e-10f;  // 2^-31
-        float s, c;
-        sincospif(x, &s, &c);
-        cs[i] = make_float2(c, s);
+        cs[i] = turned(pos, R.turn[i]);
     }
     const KvView& C = P.c;
     const int D = C.D, Hkv = C.Hkv;

@@ -1,5 +1,6 @@
 // kv.h -- launcher interface of the key/value cache between its C ABI
-// (kv_api.cu) and its kernels (kv.cu, attend.cu, attend_wide.cu, weigh.cu).
+// (kv_api.cu) and its kernels (kv.cu, attend.cu, attend_wide.cu, weigh.cu; append8.cu,
+// attend8.cu, weigh8.cu for a cache in 8 bits; logprobs.cu).
 // Not installed; not part of the public ABI.
 #pragma once
 
@@ -21,6 +22,12 @@ struct KvView {
     long long ab, ah;
     long long n_slots;
     int B, Hkv, D, cap, fp16;
+    // A cache of e4m3 codes: fp16 is then the type of q and out alone, and slot s has the scale byte s >> block_shift
+    // of its head, taken within [e_lo, e_hi].
+    int e4m3, block_shift, e_lo, e_hi;
+    uint8_t* k_scale;
+    uint8_t* v_scale;
+    long long kcb, kch, vcb, vch;  // sequence, head
 };
 
 constexpr int kRopeMaxPairs = 128;
@@ -41,6 +48,8 @@ struct KvAppendParams {
     unsigned* err;
 };
 cudaError_t launch_kv_append(const KvAppendParams& P, const RopeTable& R, cudaStream_t st);
+// append8.cu: the same into a cache of e4m3 codes
+cudaError_t launch_kv_append8(const KvAppendParams& P, const RopeTable& R, cudaStream_t st);
 
 constexpr int kEvictMaxCap = 196608;
 struct KvEvictParams {
@@ -84,6 +93,23 @@ cudaError_t launch_tree_attention(const AttendParams& P, cudaStream_t st);
 // attend_wide.cu: the first of the two kernels for many rows; says how it cut the work for the join.
 cudaError_t launch_tree_attention_wide(const AttendParams& P, int* row_blocks, int* parts, cudaStream_t st);
 cudaError_t launch_kv_accumulate(const AttendParams& P, cudaStream_t st);
+// attend8.cu, weigh8.cu: the same over a cache of e4m3 codes
+cudaError_t launch_tree_attention8(const AttendParams& P, cudaStream_t st);
+cudaError_t launch_kv_accumulate8(const AttendParams& P, cudaStream_t st);
+
+// logprobs.cu
+struct LogprobsParams {
+    const void* x;            // [N][V], row n at element n * stride
+    long long stride;
+    int dtype, N, V, M, K;
+    float inv_t;              // 1 / temperature
+    const int32_t* targets;   // [N][M] or nullptr
+    float* logp;              // [N][M]
+    float* entropy;           // [N] or nullptr
+    float* top_logp;          // [N][K] or nullptr
+    int32_t* top_ids;
+};
+cudaError_t launch_token_logprobs(const LogprobsParams& P, cudaStream_t st);
 
 // api.cu: the device error word of the current device (allocated on first use)
 int device_error_word(unsigned** out);

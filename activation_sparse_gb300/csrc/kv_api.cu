@@ -1,6 +1,7 @@
 // kv_api.cu -- the C ABI of the key/value cache (declared in include/si.h):
 // handles, argument validation and launches. The kernels are in kv.cu (append,
-// evict), attend.cu and attend_wide.cu (tree attention), and weigh.cu (weights).
+// evict), attend.cu and attend_wide.cu (tree attention), and weigh.cu (weights);
+// append8.cu, attend8.cu and weigh8.cu for a cache in 8 bits; logprobs.cu.
 #include <cmath>
 #include <cstring>
 #include <new>
@@ -45,9 +46,9 @@ struct Strides {
     Strides(const long long* s, const long long (&extents)[N]) {
         for (int i = 0; i < N; ++i) at[i] = extents[i] == 1 ? 0 : s[i];
     }
-    bool whole_units() const {
+    bool whole_units(int unit = 8) const {
         for (long long s : at)
-            if (s < 0 || s % 8) return false;
+            if (s < 0 || s % unit) return false;
         return true;
     }
 };
@@ -62,6 +63,8 @@ struct si_rope {
 
 struct si_kv {
     si_kv_desc d;
+    bool e4m3 = false;
+    si_kv_scales scales = {};
     int device = -1;          // of the scratch, set with its first allocation
     float* part = nullptr;    // partial attention rows
     unsigned* ticket = nullptr;  // eviction: a ticket and L * B lengths
@@ -95,10 +98,12 @@ int make_part(si_kv* kv, cudaStream_t st) {
     return SI_OK;
 }
 
-si::KvView view_of(const si_kv_desc& d, int layer) {
+si::KvView view_of(const si_kv* kv, int layer) {
+    const si_kv_desc& d = kv->d;
     si::KvView c = {};
-    c.k = static_cast<const uint16_t*>(d.k) + layer * d.k_stride[0];
-    c.v = static_cast<const uint16_t*>(d.v) + layer * d.v_stride[0];
+    const long long size = kv->e4m3 ? 1 : 2;
+    c.k = static_cast<const uint8_t*>(d.k) + layer * d.k_stride[0] * size;
+    c.v = static_cast<const uint8_t*>(d.v) + layer * d.v_stride[0] * size;
     c.kb = d.k_stride[1], c.kh = d.k_stride[2], c.ks = d.k_stride[3];
     c.vb = d.v_stride[1], c.vh = d.v_stride[2], c.vs = d.v_stride[3];
     c.table = d.table ? d.table + layer * d.table_stride[0] : nullptr;
@@ -109,6 +114,16 @@ si::KvView view_of(const si_kv_desc& d, int layer) {
     c.n_slots = d.n_slots;
     c.B = d.B, c.Hkv = d.Hkv, c.D = d.D, c.cap = d.cap;
     c.fp16 = d.dtype == SI_FP16;
+    if (kv->e4m3) {
+        const si_kv_scales& s = kv->scales;
+        c.e4m3 = 1;
+        while ((1ll << c.block_shift) < s.block) ++c.block_shift;
+        c.e_lo = 127 + (c.fp16 ? -15 : -124), c.e_hi = 127 + (c.fp16 ? 7 : 119);
+        c.k_scale = s.k + layer * s.k_stride[0];
+        c.v_scale = s.v + layer * s.v_stride[0];
+        c.kcb = s.k_stride[1], c.kch = s.k_stride[2];
+        c.vcb = s.v_stride[1], c.vch = s.v_stride[2];
+    }
     return c;
 }
 
@@ -158,7 +173,7 @@ int check_rows(const si_kv* kv, int layer, int T, int Hq, const void* q, const l
 si::AttendParams rows_of(const si_kv* kv, int layer, int T, int Hq, const void* q, const long long* q_stride,
                          const uint64_t* mask, float scale) {
     si::AttendParams P = {};
-    P.c = view_of(kv->d, layer);
+    P.c = view_of(kv, layer);
     P.T = T, P.Hq = Hq, P.G = Hq / kv->d.Hkv;
     P.q = q;
     const Strides qs(q_stride, {kv->d.B, T, Hq});
@@ -168,31 +183,40 @@ si::AttendParams rows_of(const si_kv* kv, int layer, int T, int Hq, const void* 
     return P;
 }
 
-}  // namespace
-
-extern "C" {
-
-int si_kv_create(const si_kv_desc* desc, si_kv** out) {
+// scales: those of a cache of e4m3 codes, or nullptr.
+int create(const si_kv_desc* desc, const si_kv_scales* scales, si_kv** out) {
     if (!desc || !out) return fail(SI_ERR_INVALID_ARG, "NULL pointer");
     *out = nullptr;
     const si_kv_desc& d = *desc;
-    if (!d.k || !d.v || !d.len) return fail(SI_ERR_INVALID_ARG, "NULL pointer in the cache description");
+    if (!d.k || !d.v || !d.len || (scales && (!scales->k || !scales->v)))
+        return fail(SI_ERR_INVALID_ARG, "NULL pointer in the cache description");
     if (d.dtype != SI_BF16 && d.dtype != SI_FP16) return fail(SI_ERR_INVALID_ARG, "dtype must be SI_BF16 or SI_FP16");
     if (d.L < 1 || d.B < 1 || d.Hkv < 1 || d.cap < 1 || d.n_slots < 1)
         return fail(SI_ERR_INVALID_ARG, "need L, B, Hkv, cap, n_slots >= 1");
-    if (d.D < 8 || d.D > 256 || d.D % 8) return fail(SI_ERR_INVALID_ARG, "need 8 <= D <= 256 and D % 8 == 0");
+    const int unit = scales ? 16 : 8;
+    if (d.D < unit || d.D > 256 || d.D % unit)
+        return fail(SI_ERR_INVALID_ARG, scales ? "need 16 <= D <= 256 and D % 16 == 0" : "need 8 <= D <= 256 and D % 8 == 0");
     if (d.B > 1024) return fail(SI_ERR_UNSUPPORTED, "more than 1024 sequences");
     if (d.Hkv > 1024) return fail(SI_ERR_UNSUPPORTED, "more than 1024 cache heads");
     if (d.n_slots > 0x7FFFFFFFLL) return fail(SI_ERR_INVALID_ARG, "slots are int32: n_slots is too large");
     const long long pool[4] = {d.L, d.B, d.Hkv, d.n_slots}, lists[3] = {d.L, d.B, d.Hkv};
     const Strides ks(d.k_stride, pool), vs(d.v_stride, pool), ts(d.table_stride, lists), as(d.acc_stride, lists);
-    if (!aligned16(d.k) || !aligned16(d.v) || !ks.whole_units() || !vs.whole_units())
-        return fail(SI_ERR_INVALID_ARG, "k and v must be 16-byte aligned with strides that are multiples of 8");
+    if (!aligned16(d.k) || !aligned16(d.v) || !ks.whole_units(unit) || !vs.whole_units(unit))
+        return fail(SI_ERR_INVALID_ARG, scales ? "k and v must be 16-byte aligned with strides that are multiples of 16"
+                                               : "k and v must be 16-byte aligned with strides that are multiples of 8");
     if (ks.at[3] > 0x7FFFFFFFLL || vs.at[3] > 0x7FFFFFFFLL)
         return fail(SI_ERR_UNSUPPORTED, "a slot stride exceeds 2^31 - 1 elements");
     if (!d.table && d.cap > d.n_slots) return fail(SI_ERR_INVALID_ARG, "without a table cap must not exceed n_slots");
     for (int i = 0; i < 3; ++i)
         if (ts.at[i] < 0 || as.at[i] < 0) return fail(SI_ERR_INVALID_ARG, "negative stride");
+    if (scales) {
+        const int block = scales->block;
+        if (block < 1 || block > (1 << 30) || (block & (block - 1)))
+            return fail(SI_ERR_INVALID_ARG, "block must be a power of two, 1 to 2^30");
+        const Strides kc(scales->k_stride, lists), vc(scales->v_stride, lists);
+        for (int i = 0; i < 3; ++i)
+            if (kc.at[i] < 0 || vc.at[i] < 0) return fail(SI_ERR_INVALID_ARG, "negative stride");
+    }
     si_kv* kv = new (std::nothrow) si_kv;
     if (!kv) return fail(SI_ERR_OOM, "out of host memory");
     kv->d = d;
@@ -200,8 +224,25 @@ int si_kv_create(const si_kv_desc* desc, si_kv** out) {
     std::memcpy(kv->d.v_stride, vs.at, sizeof d.v_stride);
     std::memcpy(kv->d.table_stride, ts.at, sizeof d.table_stride);
     std::memcpy(kv->d.acc_stride, as.at, sizeof d.acc_stride);
+    if (scales) {
+        kv->e4m3 = true;
+        kv->scales = *scales;
+        std::memcpy(kv->scales.k_stride, Strides(scales->k_stride, lists).at, sizeof scales->k_stride);
+        std::memcpy(kv->scales.v_stride, Strides(scales->v_stride, lists).at, sizeof scales->v_stride);
+    }
     *out = kv;
     return SI_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int si_kv_create(const si_kv_desc* desc, si_kv** out) { return create(desc, nullptr, out); }
+
+int si_kv_create_e4m3(const si_kv_desc* desc, const si_kv_scales* scales, si_kv** out) {
+    if (!scales) return fail(SI_ERR_INVALID_ARG, "NULL pointer");
+    return create(desc, scales, out);
 }
 
 int si_kv_destroy(si_kv* kv) {
@@ -264,7 +305,7 @@ int si_kv_append(si_kv* kv, int layer, const si_rope* rope, int T, int Hq, const
     if (((long long)Hq + 2ll * d.Hkv) * (d.D / 8) > 0x7FFF0000LL)
         return fail(SI_ERR_UNSUPPORTED, "a token's heads exceed 32-bit counts");
     si::KvAppendParams P = {};
-    P.c = view_of(d, layer);
+    P.c = view_of(kv, layer);
     P.T = T, P.Hq = Hq;
     P.q = q, P.k = k, P.v = v;
     P.qb = qs.at[0], P.qt = qs.at[1], P.qh = qs.at[2];
@@ -274,7 +315,8 @@ int si_kv_append(si_kv* kv, int layer, const si_rope* rope, int T, int Hq, const
     P.q_out = q_out;
     const int rc = si::device_error_word(&P.err);
     if (rc) return rc;
-    const cudaError_t e = si::launch_kv_append(P, rope->t, static_cast<cudaStream_t>(stream));
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const cudaError_t e = kv->e4m3 ? si::launch_kv_append8(P, rope->t, st) : si::launch_kv_append(P, rope->t, st);
     return e == cudaSuccess ? SI_OK : cuda_fail(e, "si_kv_append");
 }
 
@@ -295,7 +337,7 @@ int si_tree_attention(si_kv* kv, int layer, int T, int Hq, const void* q, const 
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if ((rc = make_part(kv, st))) return rc;
     P.part = kv->part;
-    const cudaError_t e = si::launch_tree_attention(P, st);
+    const cudaError_t e = kv->e4m3 ? si::launch_tree_attention8(P, st) : si::launch_tree_attention(P, st);
     return e == cudaSuccess ? SI_OK : cuda_fail(e, "si_tree_attention");
 }
 
@@ -312,7 +354,8 @@ int si_kv_accumulate(si_kv* kv, int layer, int T, int Hq, const void* q, const l
     P.rows = reinterpret_cast<const unsigned long long*>(rows);
     P.acc_out = acc_out ? acc_out : P.c.acc;
     if ((rc = si::device_error_word(&P.err))) return rc;
-    const cudaError_t e = si::launch_kv_accumulate(P, static_cast<cudaStream_t>(stream));
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const cudaError_t e = kv->e4m3 ? si::launch_kv_accumulate8(P, st) : si::launch_kv_accumulate(P, st);
     return e == cudaSuccess ? SI_OK : cuda_fail(e, "si_kv_accumulate");
 }
 
@@ -389,6 +432,34 @@ int si_kv_evict(si_kv* kv, int layer, int T, const int32_t* path, const int32_t*
     if ((rc = si::device_error_word(&P.err))) return rc;
     const cudaError_t e = si::launch_kv_evict(P, st);
     return e == cudaSuccess ? SI_OK : cuda_fail(e, "si_kv_evict");
+}
+
+int si_token_logprobs(int dtype, const void* logits, long long row_stride, int N, int V, float temperature,
+                      const int32_t* targets, int M, float* logp, float* entropy, int K, float* top_logp,
+                      int32_t* top_ids, void* stream) {
+    SI_TRACE("si_token_logprobs");
+    if (dtype != SI_BF16 && dtype != SI_FP16 && dtype != SI_FP32)
+        return fail(SI_ERR_INVALID_ARG, "dtype must be SI_BF16, SI_FP16 or SI_FP32");
+    if (N < 0 || V < 1 || M < 0 || K < 0) return fail(SI_ERR_INVALID_ARG, "need N, M, K >= 0 and V >= 1");
+    if (K > 32 || K > V) return fail(SI_ERR_INVALID_ARG, "need K <= 32 and K <= V");
+    if (!(temperature > 0.0f) || !std::isfinite(temperature) || !std::isfinite(1.0f / temperature))
+        return fail(SI_ERR_INVALID_ARG, "need a finite temperature > 0");
+    if (N == 0) return SI_OK;
+    if (!logits) return fail(SI_ERR_INVALID_ARG, "NULL pointer");
+    if (N > 1 && row_stride < V) return fail(SI_ERR_INVALID_ARG, "row_stride must be at least V");
+    if (M > 0 && (!targets || !logp)) return fail(SI_ERR_INVALID_ARG, "targets and logp go with M");
+    if (K > 0 && (!top_logp || !top_ids)) return fail(SI_ERR_INVALID_ARG, "top_logp and top_ids go with K");
+    if (reinterpret_cast<uintptr_t>(logits) % (dtype == SI_FP32 ? 4 : 2))
+        return fail(SI_ERR_INVALID_ARG, "logits are not aligned to their type");
+    if (M == 0 && K == 0 && !entropy) return SI_OK;
+    si::LogprobsParams P = {};
+    P.x = logits, P.stride = N > 1 ? row_stride : 0;
+    P.dtype = dtype, P.N = N, P.V = V, P.M = M, P.K = K;
+    P.inv_t = 1.0f / temperature;
+    P.targets = targets, P.logp = logp, P.entropy = entropy;
+    P.top_logp = top_logp, P.top_ids = top_ids;
+    const cudaError_t e = si::launch_token_logprobs(P, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? SI_OK : cuda_fail(e, "si_token_logprobs");
 }
 
 }  // extern "C"

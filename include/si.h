@@ -530,7 +530,7 @@ typedef struct si_rope si_rope;
  *   len int32 [L][B] contiguous.
  * 8 <= D <= 256, D % 8 == 0; 1 <= B <= 1024; L, Hkv, cap, n_slots >= 1. */
 typedef struct si_kv_desc {
-    int dtype;                /* SI_BF16 or SI_FP16 */
+    int dtype;                /* SI_BF16 or SI_FP16: of k and v too, but for si_kv_create_e4m3 */
     int L, B, Hkv, D;
     int cap;                  /* entries per list */
     long long n_slots;        /* slots per head: every table entry is below it */
@@ -543,13 +543,40 @@ typedef struct si_kv_desc {
     long long acc_stride[3];
 } si_kv_desc;
 
-/* A handle over the caller's cache. It owns the scratch of the calls below,
+/* A handle over the caller's cache of bf16 or fp16. It owns the scratch of the calls below,
  * made on their first use (run a call once before capturing it) for calls of
  * any size, and kept where it is until si_kv_destroy: graphs captured on the
  * handle stay good whatever is called on it later. si_kv_destroy synchronises
  * the device first; graphs that use the handle may not run after it. */
 int si_kv_create(const si_kv_desc *desc, si_kv **out);
 int si_kv_destroy(si_kv *kv);
+
+/* A cache in 8 bits: k and v hold e4m3 codes (one byte an element, strides in
+ * elements: multiples of 16, D too), and desc->dtype is the type of q, k, v and
+ * out in the calls below, all of which take such a handle as they take one of
+ * si_kv_create (si_kv_evict moves no key and needs no more than the lists).
+ * Every `block` consecutive slots of a head share a scale, one byte that is a
+ * biased exponent (E8M0): slot s holds code * 2^(byte - 127) with the byte
+ * of block s / block, k's and v's apart.
+ *   block = 1: si_kv_append writes a slot's scale, the least power of two
+ *     whose 448-fold reaches the row's largest magnitude;
+ *   block > 1 (a power of two up to 2^30; at least n_slots: one scale a
+ *     head): the scales are the caller's, and si_kv_append rounds with the
+ *     one that is there; what exceeds 448 of it becomes 448 of it.
+ * An exponent is kept in, and a byte outside taken as the nearest of, -124 ..
+ * 119 for bf16 and -15 .. 7 for fp16: every code then stands for a number of
+ * the cache's type. Byte 255 is NaN: it stands for a row of NaN, and
+ * si_kv_append gives it (block = 1, codes 0) to a row with an element that is
+ * not finite. Elements are rounded once, to the nearest code, from the fp32
+ * values of the rotation.
+ *   k, v uint8 [L][B][Hkv][ceil(n_slots / block)], strides {layer, sequence,
+ *   head}. 16 <= D <= 256. */
+typedef struct si_kv_scales {
+    int block;
+    uint8_t *k, *v;
+    long long k_stride[3], v_stride[3];
+} si_kv_scales;
+int si_kv_create_e4m3(const si_kv_desc *desc, const si_kv_scales *scales, si_kv **out);
 
 /* Rotary positions with several axes (text has one, images and video have
  * time, height, width). Pair i < n_pairs turns by pos[axis[i]] * inv_freq[i]
@@ -635,6 +662,29 @@ int si_kv_accumulate(si_kv *kv, int layer, int T, int Hq, const void *q, const l
  * with len < 0 or len + T > cap is left as it is and sets SI_DEVERR_CACHE. */
 int si_kv_evict(si_kv *kv, int layer, int T, const int32_t *path, const int32_t *n_path, int budget,
                 int sinks, int recent, int32_t *table_out, int32_t *len_out, void *stream);
+
+/* ------------------------------------------------ what a step answers with */
+
+/* Log probabilities of N rows of V logits, x = logits / temperature, l = x -
+ * log(sum of exp(x)): of given tokens (a drafted node's children, the prompt's
+ * own next tokens), the rows' entropy, and each row's best alternatives.
+ *   logits  device, dtype SI_BF16, SI_FP16 or SI_FP32, row n at element n *
+ *     row_stride (row_stride >= V, or 0 where N is 1); any alignment of the type.
+ *   targets (optional) int32 [N][M]: logp fp32 [N][M] receives l[target]; an id
+ *     outside [0, V) stands for no token and gets -inf.
+ *   entropy (optional) fp32 [N]: -sum of exp(l) l, in nats; logits of -inf
+ *     (a constrained vocabulary) have no part in it.
+ *   top_logp fp32 and top_ids int32 [N][K] (both or neither; K <= 32, K <= V):
+ *     the K largest logits' l and ids, falling, ties to the lower id (0 and
+ *     -0 tie; NaN counts as larger than all).
+ * A row with a NaN or +inf has NaN for all of its numbers; one of -inf
+ * alone has l = -inf and entropy 0. Sums in fp32, in a fixed order: results do
+ * not depend on timing. N >= 0, 1 <= V < 2^31; temperature and its reciprocal > 0 and finite.
+ * Needs no handle and no scratch. */
+#define SI_FP32 2
+int si_token_logprobs(int dtype, const void *logits, long long row_stride, int N, int V, float temperature,
+                      const int32_t *targets, int M, float *logp, float *entropy,
+                      int K, float *top_logp, int32_t *top_ids, void *stream);
 
 #ifdef __cplusplus
 }

@@ -365,13 +365,17 @@ struct Copy {
 };
 
 // The copying side of a CTA's walk over its tiles: where the next tile's rows
-// are. What depends on the list alone is worked out when the list changes.
-struct Source {
+// are. What depends on the list alone is worked out when the list changes. E: an
+// element of the pools, two bytes or an e4m3 code.
+template <class E>
+struct SourceOf {
     At at;
     int x, x1;                 // flat index of the next tile, and of the first one that is not ours
     const int32_t* list;
-    const uint16_t* k;
-    const uint16_t* v;
+    const E* k;
+    const E* v;
+    const uint8_t* k_scale;    // where E is a code
+    const uint8_t* v_scale;
     const float* acc;
     int len, tot;
     unsigned long long seen;   // nodes that any row sees (all of them where the caller says so)
@@ -383,8 +387,12 @@ struct Source {
     __device__ __forceinline__ void enter(const KvView& C, const Plan& p, int row_blocks) {
         const int h = at.group / row_blocks;
         list = C.table ? C.table + at.b * C.tb + h * C.th : nullptr;
-        k = static_cast<const uint16_t*>(C.k) + at.b * C.kb + h * C.kh;
-        v = static_cast<const uint16_t*>(C.v) + at.b * C.vb + h * C.vh;
+        k = static_cast<const E*>(C.k) + at.b * C.kb + h * C.kh;
+        v = static_cast<const E*>(C.v) + at.b * C.vb + h * C.vh;
+        if (sizeof(E) == 1) {
+            k_scale = C.k_scale + at.b * C.kcb + h * C.kch;
+            v_scale = C.v_scale + at.b * C.vcb + h * C.vch;
+        }
         acc = C.acc + at.b * C.ab + h * C.ah;
         len = p.len[at.b], tot = p.tot[at.b];
     }
@@ -397,6 +405,7 @@ struct Source {
         return true;
     }
 };
+using Source = SourceOf<uint16_t>;
 
 inline cudaError_t launch(const void* fn, dim3 grid, int threads, size_t smem, void** args, cudaStream_t st) {
     cudaLaunchConfig_t cfg = {};

@@ -92,6 +92,9 @@ bool attend_counts_fit(const AttendParams& P);
 cudaError_t launch_tree_attention(const AttendParams& P, cudaStream_t st);
 // attend_wide.cu: the first of the two kernels for many rows; says how it cut the work for the join.
 cudaError_t launch_tree_attention_wide(const AttendParams& P, int* row_blocks, int* parts, cudaStream_t st);
+// attend.cu: joins the partial rows of a first kernel of `parts` CTAs with blocks of 8 or 16 query rows, dealt as the
+// kernel for few rows deals them; maxima, sums and rows as that one writes them for P.c.fp16.
+cudaError_t launch_tree_attention_join(const AttendParams& P, int rows, int row_blocks, int parts, cudaStream_t st);
 cudaError_t launch_kv_accumulate(const AttendParams& P, cudaStream_t st);
 // attend8.cu, weigh8.cu: the same over a cache of e4m3 codes
 cudaError_t launch_tree_attention8(const AttendParams& P, cudaStream_t st);

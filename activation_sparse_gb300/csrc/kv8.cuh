@@ -38,6 +38,71 @@ __device__ __forceinline__ uint32_t halves(uint16_t codes) {
     return w;
 }
 
+// The four codes of a word that lie at bytes 0, 1 and 2, 3.
+__device__ __forceinline__ void halves4(uint32_t w, uint32_t& lo, uint32_t& hi) {
+    lo = halves((uint16_t)w);
+    hi = halves((uint16_t)(w >> 16));
+}
+
+// 1 / x of a power of two within the scales' limits.
+__device__ __forceinline__ float power_inverse(float x) { return __int_as_float((254 << 23) - __float_as_int(x)); }
+
+// Byte offset of 16-byte unit `unit` of row `row` in a tile of rows of DP codes; XORed so that the eight rows of an
+// ldmatrix lie in different banks (two rows of 64 codes share the banks' 128 bytes).
+template <int DP>
+__device__ __forceinline__ uint32_t tile8_at(int row, int unit) {
+    const int swap = DP == 64 ? (row >> 1) & 3 : row & 7;
+    return (uint32_t)(row * DP + ((unit ^ swap) * 16));
+}
+
+// As Copy, for rows of codes.
+template <int DP>
+struct Copy8 {
+    static constexpr int UNITS = DP / 16;
+    static constexpr int AT_ONCE = 32 / UNITS;
+    static constexpr int SWEEPS = 16 / AT_ONCE;
+    static __device__ __forceinline__ int row(int lane, int j) { return (lane / UNITS) * SWEEPS + j; }
+    static __device__ __forceinline__ void slots(int held, int lane, int (&slot)[SWEEPS]) {
+#pragma unroll
+        for (int j = 0; j < SWEEPS; ++j) slot[j] = __shfl_sync(0xFFFFFFFFu, held, row(lane, j));
+    }
+};
+
+// d += a (16 x 16) * b (16 x 8)
+__device__ __forceinline__ void mma16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// This lane's eight elements of a query row (nullptr: zeros) as fp16, where the DP / 8 lanes of a group share a row of D
+// elements. fp16 queries are taken as they are; bf16 ones times the power of two that brings the row's largest into
+// 2^14 .. 2^15, so that all down to 2^-29 of it is exact and what lies below good to 2^-39 of it: `down` undoes it. A
+// row that is not finite stays as it is.
+template <int DP>
+__device__ __forceinline__ uint4 query_unit(const uint16_t* row, int D, bool fp16, int lane, float& down) {
+    constexpr int LANES = DP / 8;
+    const int u = lane % LANES;
+    uint4 val = make_uint4(0, 0, 0, 0);
+    if (row && u * 8 < D) val = *reinterpret_cast<const uint4*>(row + u * 8);
+    down = 1.0f;
+    if (fp16) return val;
+    uint32_t w[4] = {val.x, val.y, val.z, val.w};
+    uint32_t top = 0;  // the largest exponent
+#pragma unroll
+    for (int i = 0; i < 4; ++i) top = max(top, max(w[i] & 0x7F80u, w[i] >> 16 & 0x7F80u));
+#pragma unroll
+    for (int o = 1; o < LANES; o <<= 1) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+    const int e = (int)(top >> 7), f = min(268 - e, 253);
+    const float up = e < 255 ? __int_as_float(f << 23) : 1.0f;
+    if (e < 255) down = __int_as_float((254 - f) << 23);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = pack2<true>(bf_lo(w[i]) * up, bf_hi(w[i]) * up);
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
 __device__ __forceinline__ bool code_nan(uint32_t code) { return (code & 0x7Fu) == 0x7Fu; }
 
 }  // namespace si

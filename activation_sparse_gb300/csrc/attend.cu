@@ -576,20 +576,6 @@ cudaError_t launch_join(const AttendParams& P, int row_blocks, int parts, cudaSt
     return launch(join, dim3((unsigned)blocks, 1, 1), kJoinWarps * 32, Plan::words(P.c.B) * 4, args, st);
 }
 
-template <int DP, bool FP16>
-cudaError_t launch_join_rows(const AttendParams& P, int rows, int row_blocks, int parts, cudaStream_t st) {
-    return rows == 8 ? launch_join<DP, 8, FP16>(P, row_blocks, parts, st) : launch_join<DP, 16, FP16>(P, row_blocks, parts, st);
-}
-
-template <bool FP16>
-cudaError_t launch_join_heads(const AttendParams& P, int rows, int row_blocks, int parts, cudaStream_t st) {
-    switch (padded(P.c.D)) {
-        case 64: return launch_join_rows<64, FP16>(P, rows, row_blocks, parts, st);
-        case 128: return launch_join_rows<128, FP16>(P, rows, row_blocks, parts, st);
-        default: return launch_join_rows<256, FP16>(P, rows, row_blocks, parts, st);
-    }
-}
-
 template <int DP, int MW, bool FP16>
 cudaError_t launch_attend(const AttendParams& P, cudaStream_t st) {
     const int sms = sm_count();
@@ -649,11 +635,6 @@ bool attend_counts_fit(const AttendParams& P) {
     const long long lists = (long long)P.c.B * P.c.Hkv * ((R + rows - 1) / rows);
     const long long tiles = (long long)P.c.cap / KT + 1;
     return P.c.cap <= kMost && lists <= kMost / tiles && lists <= kMost / rows;
-}
-
-cudaError_t launch_tree_attention_join(const AttendParams& P, int rows, int row_blocks, int parts, cudaStream_t st) {
-    return P.c.fp16 ? launch_join_heads<true>(P, rows, row_blocks, parts, st)
-                    : launch_join_heads<false>(P, rows, row_blocks, parts, st);
 }
 
 cudaError_t launch_tree_attention(const AttendParams& P, cudaStream_t st) {

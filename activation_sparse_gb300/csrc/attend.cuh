@@ -131,7 +131,11 @@ struct Plan {
         : len(at), tot(at + B), first(at + 2 * B), part(at + 3 * B + 1), cut(at + 4 * B + 2) {}
 };
 
-__device__ __forceinline__ int tiles_of(int tot) { return tot > KT ? (tot + KT - 1) / KT : 1; }
+// K: keys a tile, here and below.
+template <int K = KT>
+__device__ __forceinline__ int tiles_of(int tot) {
+    return tot > K ? (tot + K - 1) / K : 1;
+}
 
 // Fills the plan for `ctas` CTAs (all threads; ends with a barrier). Lengths
 // are read once.
@@ -142,7 +146,7 @@ __device__ __forceinline__ int tiles_of(int tot) { return tot > KT ? (tot + KT -
 // time (queries in, partial rows out). So lists are cut by themselves where
 // the longest part and one piece take less than an even share and two. A part
 // has at least LEAST tiles.
-template <int THREADS, int LEAST, int PIECE>
+template <int THREADS, int LEAST, int PIECE, int K = KT>
 __device__ void make_plan(const KvView& C, int T, int groups, int ctas, const Plan& p, unsigned* err, bool report) {
     if (C.B == 1) {
         // The same for one sequence, by one thread: the general way's code alone, cold in the instruction
@@ -151,7 +155,7 @@ __device__ void make_plan(const KvView& C, int T, int groups, int ctas, const Pl
             const int len = C.len[0];
             const bool ok = len >= 0 && len <= C.cap - T;
             if (!ok && report) atomicOr(err, SI_DEVERR_CACHE);
-            const int tot = ok ? len + T : 0, n = tiles_of(tot), total = n * groups;
+            const int tot = ok ? len + T : 0, n = tiles_of<K>(tot), total = n * groups;
             int q = 0;
             if (PIECE > 0 && groups <= ctas) {
                 const int even = max(LEAST, div_of(total + ctas - 1, ctas)), m = div_of(ctas, groups);
@@ -184,7 +188,7 @@ __device__ void make_plan(const KvView& C, int T, int groups, int ctas, const Pl
 #pragma unroll 1
             for (int b0 = 0; b0 < C.B; b0 += 32) {
                 const int b = b0 + lane;
-                const int mine = b < C.B ? value(tiles_of(p.tot[b])) * groups : 0;
+                const int mine = b < C.B ? value(tiles_of<K>(p.tot[b])) * groups : 0;
                 int incl = mine;
 #pragma unroll
                 for (int o = 1; o < 32; o <<= 1) {
@@ -204,7 +208,7 @@ __device__ void make_plan(const KvView& C, int T, int groups, int ctas, const Pl
             const int even = max(LEAST, div_of(total + ctas - 1, ctas));
             int parts = 0;  // lane i tries even + i
 #pragma unroll 1
-            for (int b = 0; b < C.B; ++b) parts += div_of(tiles_of(p.tot[b]) + even + lane - 1, even + lane);
+            for (int b = 0; b < C.B; ++b) parts += div_of(tiles_of<K>(p.tot[b]) + even + lane - 1, even + lane);
             const unsigned fits = __ballot_sync(0xFFFFFFFFu, lane <= PIECE && parts * groups <= ctas);
             if (fits) q = even + __ffs(fits) - 1;
         }
@@ -216,12 +220,13 @@ __device__ void make_plan(const KvView& C, int T, int groups, int ctas, const Pl
 
 // Which tiles a CTA has, and which CTAs a list has. All in 32 bits: this runs
 // for every row that is joined.
-struct Deal {
+template <int K>
+struct DealOf {
     const Plan& p;
     int B, q, end;
     unsigned base, rem;  // shares across lists: rem CTAs of base + 1 tiles, then base each
 
-    __device__ __forceinline__ Deal(const Plan& plan, int seqs, int ctas, int least) : p(plan), B(seqs) {
+    __device__ __forceinline__ DealOf(const Plan& plan, int seqs, int ctas, int least) : p(plan), B(seqs) {
         q = *plan.cut;
         end = plan.first[seqs];
         base = rem = 0;
@@ -253,14 +258,14 @@ struct Deal {
             if (p.part[mid] <= cta) lo = mid;
             else hi = mid - 1;
         }
-        const int n = tiles_of(p.tot[lo]), m = div_of(n + q - 1, q);
+        const int n = tiles_of<K>(p.tot[lo]), m = div_of(n + q - 1, q);
         const int group = div_of(cta - p.part[lo], m), k = cta - p.part[lo] - group * m;
         x0 = p.first[lo] + group * n + part_start(n, m, k);
         x1 = p.first[lo] + group * n + part_start(n, m, k + 1);
     }
     // The CTAs of a list, and whether the first of them has another list before it.
     __device__ __forceinline__ void ctas_of(int b, int group, int& first, int& last, bool& second) const {
-        const int n = tiles_of(p.tot[b]);
+        const int n = tiles_of<K>(p.tot[b]);
         if (q) {
             const int m = div_of(n + q - 1, q);
             first = p.part[b] + group * m;
@@ -274,12 +279,14 @@ struct Deal {
         second = start(first) < y0;
     }
 };
+using Deal = DealOf<KT>;
 
 // A position in the flat order of tiles.
 struct At {
     int b, group, tile, ntile;
 };
 
+template <int K = KT>
 __device__ __forceinline__ At locate(const Plan& p, int B, int x) {
     int lo = 0, hi = B - 1;  // last b with first[b] <= x
     while (lo < hi) {
@@ -289,19 +296,20 @@ __device__ __forceinline__ At locate(const Plan& p, int B, int x) {
     }
     At a;
     a.b = lo;
-    a.ntile = tiles_of(p.tot[lo]);
+    a.ntile = tiles_of<K>(p.tot[lo]);
     const int in = x - p.first[lo];
     a.group = div_of(in, a.ntile);
     a.tile = in - a.group * a.ntile;
     return a;
 }
 
+template <int K = KT>
 __device__ __forceinline__ void step(const Plan& p, int B, int groups, At& a) {
     if (++a.tile < a.ntile) return;
     a.tile = 0;
     if (++a.group < groups) return;
     a.group = 0;
-    if (++a.b < B) a.ntile = tiles_of(p.tot[a.b]);
+    if (++a.b < B) a.ntile = tiles_of<K>(p.tot[a.b]);
 }
 
 // Ancestor word of node t (mask NULL: a chain).
@@ -367,7 +375,7 @@ struct Copy {
 // The copying side of a CTA's walk over its tiles: where the next tile's rows
 // are. What depends on the list alone is worked out when the list changes. E: an
 // element of the pools, two bytes or an e4m3 code.
-template <class E>
+template <class E, int K = KT>
 struct SourceOf {
     At at;
     int x, x1;                 // flat index of the next tile, and of the first one that is not ours
@@ -381,7 +389,7 @@ struct SourceOf {
     unsigned long long seen;   // nodes that any row sees (all of them where the caller says so)
 
     __device__ __forceinline__ void start(const Plan& p, int B, int first, int end) {
-        at = locate(p, B, first);
+        at = locate<K>(p, B, first);
         x = first, x1 = end;
     }
     __device__ __forceinline__ void enter(const KvView& C, const Plan& p, int row_blocks) {
@@ -401,7 +409,7 @@ struct SourceOf {
         ++x;
         if (++at.tile < at.ntile) return false;
         at.tile = at.ntile - 1;
-        step(p, B, groups, at);
+        step<K>(p, B, groups, at);
         return true;
     }
 };

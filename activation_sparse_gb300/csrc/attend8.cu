@@ -1,11 +1,13 @@
 // attend8.cu -- tree attention over a cache of e4m3 codes: the kernel for few
-// rows a key. Lists, tiles and the join of several CTAs' parts are those of the
-// cache in 16 bits (attend.cu).
+// rows a key. Lists are cut into tiles and dealt to CTAs as for the cache in 16
+// bits (attend.cu). Where several CTAs have parts of a list, the last of them to
+// be done joins the parts, in their order: the result does not depend on which
+// one that is.
 //
-// A warp takes sixteen keys of every tile and keeps its own softmax state. The
+// A warp takes sixteen keys of a tile, or twice that, and keeps its own softmax state. The
 // products have the keys on the long side, so that up to eight query rows
 // (one token's heads, mostly) fill the short one:
-//   S^T (16 keys x 8 rows) = K (16 x D) Q^T        mma m16n8k16
+//   S^T (16 keys x 8 rows)  = K (16 x D) Q^T        mma m16n8k16
 //   O^T (D x 8 rows)      += V^T (D x 16 keys) P^T
 // Codes become fp16 in registers, two an instruction and exactly, on their way
 // from shared memory to the product; the scales stay out of it. A key's scale
@@ -21,8 +23,7 @@ namespace si {
 
 namespace {
 
-constexpr int kThreads = 128;  // four warps of sixteen keys of a tile
-constexpr int kKeys = 16;
+constexpr int kThreads = 128;  // four warps
 
 // fp16 weights, and a maximum that may be outgrown by 2^kLazy before anything is rescaled.
 using Wt = Weights<true, true>;
@@ -30,21 +31,29 @@ using Wt = Weights<true, true>;
 template <int DP, int NT>
 struct Cfg8 {
     static constexpr int kRows = 8 * NT;                      // query rows of a block
-    static constexpr int kTile = KT * DP;                     // bytes of a K or V tile
+    static constexpr int kMT = DP <= 128 ? 2 : 1;             // sixteens of keys a warp has of a tile
+    static constexpr int kWarpKeys = 16 * kMT;
+    static constexpr int kKeys = 4 * kWarpKeys;               // of a tile
+    static constexpr int kTile = kKeys * DP;                  // bytes of a K or V tile
     static constexpr int kOffScale = 2 * kTile;               // in a stage: {k, v} scales of its keys
-    static constexpr int kStage = 2 * kTile + KT * 8;
-    static constexpr int kStages = 3;
-    static constexpr int kCtas = DP > 128 || (DP == 128 && NT == 2) ? 2 : NT == 1 ? 4 : 3;  // an SM
+    static constexpr int kStage = 2 * kTile + kKeys * 8;
+    static constexpr int kStages = DP == 64 ? 4 : 3;
+    static constexpr int kCtas = DP == 64 ? 3 : 2;            // an SM
     static constexpr int kQRow = DP * 2 + 32;                 // bytes: eight rows' 32-byte pieces lie in different banks
     static constexpr int kJoinRow = DP + 4;                   // floats: likewise
     static constexpr bool kQInRegs = DP * NT <= 256;
     static constexpr int kOffQ = kStages * kStage;            // queries; the join of the warps takes their place
-    static constexpr int kUnion = kRows * kJoinRow * 4;       // >= kRows * kQRow
+    static constexpr int kUnion = 8 * kJoinRow * 4 > kRows * kQRow ? 8 * kJoinRow * 4 : kRows * kQRow;
     static constexpr int kOffFactor = kOffQ + kUnion;         // what a query row was divided by
     static constexpr int kOffState = kOffFactor + kRows * 4;  // [warp][row] {maximum, sum}
-    static constexpr int kOffPlan = kOffState + 4 * kRows * 8;
+    static constexpr int kOffLast = kOffState + 4 * kRows * 8;  // [2] lists that this CTA joins
+    static constexpr int kOffPlan = kOffLast + 2 * 32;
     static constexpr int smem(int B) { return kOffPlan + Plan::words(B) * 4; }
-    static_assert(kRows * kQRow <= kUnion, "the queries fit the join's place");
+};
+
+// A list whose parts this CTA joins.
+struct LastOf {
+    int on, b, group, first, last, behind;
 };
 
 // The transposed 8 x 8 matrix of 16-bit elements that the warp's registers hold.
@@ -66,30 +75,113 @@ __device__ __forceinline__ float column_sum(float v) {
     return v + __shfl_xor_sync(0xFFFFFFFFu, v, 16);
 }
 
+__device__ __forceinline__ float shift_of(float m) { return m == -INFINITY ? 0.0f : m; }
+
+// Joins a list's parts: the CTA's ring is empty and takes the parts' weights.
+template <int DP, int RB>
+__device__ void join_parts(const AttendParams& P, const Plan& plan, int row_blocks, const LastOf& l, uint8_t* smem) {
+    constexpr int CHUNK = 64, QUADS = DP / 4, ITEMS = RB * QUADS / kThreads > 0 ? RB * QUADS / kThreads : 1;
+    float* const weight_s = reinterpret_cast<float*>(smem);             // [part of a chunk][row]
+    float4* const state_s = reinterpret_cast<float4*>(weight_s + CHUNK * RB);  // [row] maximum, sum, what the sums so far are multiplied by
+    const KvView& C = P.c;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int G = P.G, R = P.T * G, D = C.D;
+    const int h = l.group / row_blocks, row0 = l.group % row_blocks * RB, rows = min(RB, R - row0);
+    const float c2 = P.scale * kLog2e;
+    auto part_of = [&](int c) { return P.part + ((long long)c * 2 + (c == l.first && l.behind)) * part_floats(RB, DP); };
+    __syncthreads();
+    if (tid < RB) state_s[tid] = make_float4(-INFINITY, 0.0f, 0.0f, 0.0f);
+    float4 acc[ITEMS];
+#pragma unroll
+    for (int i = 0; i < ITEMS; ++i) acc[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int c0 = l.first; c0 <= l.last; c0 += CHUNK) {
+        const int n = min(CHUNK, l.last - c0 + 1);
+        __syncthreads();
+        for (int r = warp; r < rows; r += 4) {
+            float m[2], s[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                m[i] = -INFINITY, s[i] = 0.0f;
+                if (lane + 32 * i < n) {
+                    const float* p = part_of(c0 + lane + 32 * i) + RB * DP + r;
+                    m[i] = __ldcg(p), s[i] = __ldcg(p + RB);
+                }
+            }
+            const float4 old = state_s[r];
+            float top = fmaxf(m[0], m[1]);
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+            top = fmaxf(top, old.x);
+            const float shift = shift_of(top), keep = ex2((old.x - shift) * c2);
+            float sum = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const float w = ex2((m[i] - shift) * c2);
+                if (lane + 32 * i < n) weight_s[(lane + 32 * i) * RB + r] = w;
+                sum += w * s[i];
+            }
+            sum = warp_sum(sum);
+            if (lane == 0) state_s[r] = make_float4(top, old.y * keep + sum, keep, 0.0f);
+        }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < ITEMS; ++i) {
+            const int item = tid + i * kThreads, r = item / QUADS, q = item % QUADS;
+            if (r >= rows || q * 4 >= D) continue;
+            const float keep = state_s[r].z;
+            acc[i].x *= keep, acc[i].y *= keep, acc[i].z *= keep, acc[i].w *= keep;
+#pragma unroll 16
+            for (int c = 0; c < n; ++c) {
+                const float4 v = __ldcg(reinterpret_cast<const float4*>(part_of(c0 + c) + r * DP) + q);
+                const float w = weight_s[c * RB + r];
+                acc[i].x += w * v.x, acc[i].y += w * v.y, acc[i].z += w * v.z, acc[i].w += w * v.w;
+            }
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < ITEMS; ++i) {
+        const int item = tid + i * kThreads, r = item / QUADS, q = item % QUADS;
+        if (r >= rows || q * 4 >= D) continue;
+        const float4 st = state_s[r];
+        const int t = (row0 + r) / G, g = row0 + r - t * G;
+        const bool empty = plan.tot[l.b] == 0 || word_of(P.mask, P.T, l.b, t) == 0 || st.y == 0.0f;
+        const float inv = empty ? 0.0f : 1.0f / st.y;
+        const long long at = ((long long)l.b * P.T + t) * P.Hq + h * G + g;
+        uint2 w = make_uint2(0, 0);
+        const float4 a = make_float4(acc[i].x * inv, acc[i].y * inv, acc[i].z * inv, acc[i].w * inv);
+        if (!empty) w = C.fp16 ? make_uint2(pack<true>(a.x, a.y), pack<true>(a.z, a.w)) : make_uint2(pack<false>(a.x, a.y), pack<false>(a.z, a.w));
+        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(P.out) + at * D + q * 4) = w;
+        if (P.lse && q == 0) P.lse[at] = empty ? -INFINITY : lse_of(st.x, P.scale, st.y);
+    }
+}
+
 template <int DP, int NT>
 __global__ void __launch_bounds__(kThreads, Cfg8<DP, NT>::kCtas)
     k_tree_attention8(const __grid_constant__ AttendParams P, int row_blocks) {
     using Cfg = Cfg8<DP, NT>;
-    using Cp = Copy8<DP>;
-    constexpr int RB = Cfg::kRows, KD = DP / 16, UNITS = Cp::UNITS, S = Cfg::kStages;
+    using Cp = Copy8<DP, Cfg::kWarpKeys>;
+    constexpr int RB = Cfg::kRows, KD = DP / 16, UNITS = Cp::UNITS, S = Cfg::kStages, MT = Cfg::kMT;
+    constexpr int WK = Cfg::kWarpKeys, KEYS = Cfg::kKeys;
 
     extern __shared__ __align__(128) uint8_t smem[];
     uint8_t* const q_s = smem + Cfg::kOffQ;
     float* const join_s = reinterpret_cast<float*>(q_s);
     float* const factor_s = reinterpret_cast<float*>(smem + Cfg::kOffFactor);
     float2* const state_s = reinterpret_cast<float2*>(smem + Cfg::kOffState);
+    LastOf* const last_s = reinterpret_cast<LastOf*>(smem + Cfg::kOffLast);
     const Plan plan(reinterpret_cast<int*>(smem + Cfg::kOffPlan), P.c.B);
 
     const KvView& C = P.c;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int g = lane >> 2, c = lane & 3;   // keys g, g + 8; rows 2c, 2c + 1 of each eight
+    const int g = lane >> 2, c = lane & 3;   // keys g, g + 8 of sixteen; rows 2c, 2c + 1 of each eight
     const int T = P.T, G = P.G, R = T * G, D = C.D;
     const int groups = C.Hkv * row_blocks;
 
+    if (tid < 2) last_s[tid].on = 0;
     grid_dependency_wait();
-    grid_launch_dependents();  // after the wait: the join reads the lengths before its own
-    make_plan<kThreads, kNarrowLeast, kNarrowPiece>(C, T, groups, gridDim.x, plan, P.err, blockIdx.x == 0);
-    const Deal deal(plan, C.B, gridDim.x, kNarrowLeast);
+    grid_launch_dependents();
+    make_plan<kThreads, kNarrowLeast, kNarrowPiece, KEYS>(C, T, groups, gridDim.x, plan, P.err, blockIdx.x == 0);
+    const DealOf<KEYS> deal(plan, C.B, gridDim.x, kNarrowLeast);
     int x0, x1;
     deal.range(blockIdx.x, x0, x1);
     if (x0 >= x1) return;
@@ -97,35 +189,37 @@ __global__ void __launch_bounds__(kThreads, Cfg8<DP, NT>::kCtas)
     const float c2 = P.scale * kLog2e;
     const int unit = lane % UNITS;
     const bool unit_on = unit * 16 < D, whole_rows = D == DP;
-    const int own0 = warp * kKeys;  // this warp's keys of a tile
+    const int own0 = warp * WK;  // this warp's keys of a tile
     const int n_slots = (int)C.n_slots, k_step = (int)C.ks, v_step = (int)C.vs;
 
-    // producer state: lanes i and i + 16 hold the slot of key own0 + i of the tile to be issued next
-    SourceOf<uint8_t> src;
+    // producer state: lane i holds the slot of key own0 + i (of sixteen: i % 16) of the tile to be issued next
+    SourceOf<uint8_t, KEYS> src;
     src.start(plan, C.B, x0, x1);
     const uint32_t ring = smem_u32(smem);
     int stage_in = 0, held = kNoSlot, seen_b = -1;
-    int pend = -1, pend_byte = 0;   // the stage that waits for its scales, and this lane's (lanes below 16: k's)
+    int pend = -1, pend_k = 0, pend_v = 0;   // the stage that waits for its scales, and this lane's key's
     auto fetch = [&]() {
-        const int i0 = src.at.tile * KT;
-        if (i0 + KT > src.len && seen_b != src.at.b) {  // the tile meets the new nodes
+        const int i0 = src.at.tile * KEYS;
+        if (i0 + KEYS > src.len && seen_b != src.at.b) {  // the tile meets the new nodes
             src.seen = seen_nodes(P.mask, T, src.at.b, lane);
             seen_b = src.at.b;
         }
-        held = slot_of(src.list, i0 + own0 + (lane & 15), src.len, src.tot, src.seen);
+        held = slot_of(src.list, i0 + own0 + lane % WK, src.len, src.tot, src.seen);
     };
     auto issue = [&]() {
         // The scales of the tile before have had a tile's time to arrive. A key that is not there has 0 (byte -1).
         if (pend >= 0) {
-            float* to = reinterpret_cast<float*>(smem + pend * Cfg::kStage + Cfg::kOffScale);
-            to[(own0 + (lane & 15)) * 2 + (lane >> 4)] = pend_byte < 0 ? 0.0f : scale_of(pend_byte, C.e_lo, C.e_hi);
+            float2* to = reinterpret_cast<float2*>(smem + pend * Cfg::kStage + Cfg::kOffScale);
+            if (WK == 32 || lane < WK)
+                to[own0 + lane] = pend_k < 0 ? make_float2(0.0f, 0.0f)
+                                             : make_float2(scale_of(pend_k, C.e_lo, C.e_hi), scale_of(pend_v, C.e_lo, C.e_hi));
             pend = -1;
         }
         if (src.x < x1) {
             int slot[Cp::SWEEPS];
             const uint8_t *kp = src.k + unit * 16, *vp = src.v + unit * 16;
             const bool ok = slot_ok(held, n_slots, P.err);
-            const bool cached = src.at.tile * KT + KT <= src.len;
+            const bool cached = src.at.tile * KEYS + KEYS <= src.len;
             // cached keys: nothing to leave out (a slot outside the pool has been reported; slot 0 is read)
             const int mine = ok ? held : cached ? 0 : -1;
             Cp::slots(mine, lane, slot);
@@ -147,7 +241,8 @@ __global__ void __launch_bounds__(kThreads, Cfg8<DP, NT>::kCtas)
                     cp16(at + Cfg::kTile, on ? vp + from * v_step : src.v, on);
                 }
             }
-            pend_byte = mine < 0 ? -1 : (lane < 16 ? src.k_scale : src.v_scale)[mine >> C.block_shift];
+            pend_k = -1;
+            if (mine >= 0) pend_k = src.k_scale[mine >> C.block_shift], pend_v = src.v_scale[mine >> C.block_shift];
             pend = stage_in;
             if (++stage_in == S) stage_in = 0;
             if (src.next(plan, C.B, groups) && src.x < x1) src.enter(C, plan, row_blocks);
@@ -160,7 +255,7 @@ __global__ void __launch_bounds__(kThreads, Cfg8<DP, NT>::kCtas)
 #pragma unroll 1
     for (int s = 0; s < S - 1; ++s) issue();
 
-    At a = locate(plan, C.B, x0);
+    At a = locate<KEYS>(plan, C.B, x0);
     int segment = 0, stage_out = 0;
     for (int x = x0; x < x1; ++segment) {
         // one list, or the part of it that this CTA has
@@ -221,9 +316,9 @@ __global__ void __launch_bounds__(kThreads, Cfg8<DP, NT>::kCtas)
             cp_wait<S - 2>();
             uint8_t* const stage = smem + stage_out * Cfg::kStage;
             if (++stage_out == S) stage_out = 0;
-            const int i0 = a.tile * KT + own0;
-            const bool edge = i0 + kKeys > len;  // these keys meet the new nodes or the list's end
-            unsigned odd = 0;                    // keys (of the sixteen) with codes of NaN
+            const int i0 = a.tile * KEYS + own0;
+            const bool edge = i0 + WK > len;  // these keys meet the new nodes or the list's end
+            unsigned odd = 0;                 // keys with codes of NaN
             if (edge) {
                 // A node's value row may hold NaN that only its descendants may see, and 0 * NaN is NaN: such codes
                 // leave the product here (each lane looks at what it copied itself) and come back below for the rows
@@ -241,55 +336,80 @@ __global__ void __launch_bounds__(kThreads, Cfg8<DP, NT>::kCtas)
             __syncwarp();
             issue();
             const uint32_t k_s = smem_u32(stage), v_s = k_s + Cfg::kTile;
-            const float2* sc = reinterpret_cast<const float2*>(stage + Cfg::kOffScale) + own0;
-            const float2 sc0 = sc[g], sc1 = sc[g + 8];
+            const float2* sc_s = reinterpret_cast<const float2*>(stage + Cfg::kOffScale) + own0;
             // rows of an ldmatrix: keys 0-7, 8-15 of a unit, then of the next unit
             const int ld_key = own0 + (lane & 15), ld_unit = lane >> 4;
-            float s[NT][4];
+            float s[MT][NT][4];
+            float2 sc[MT][2];
 #pragma unroll
-            for (int n = 0; n < NT; ++n) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.0f;
+            for (int m = 0; m < MT; ++m) {
+                sc[m][0] = sc_s[m * 16 + g], sc[m][1] = sc_s[m * 16 + g + 8];
+#pragma unroll
+                for (int n = 0; n < NT; ++n) s[m][n][0] = s[m][n][1] = s[m][n][2] = s[m][n][3] = 0.0f;
+            }
 #pragma unroll
             for (int u = 0; u < KD; u += 2) {
-                uint32_t r[4];
-                ldsm4(r, k_s + tile8_at<DP>(ld_key, u + ld_unit));
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    uint32_t a0, a1, a2, a3;
-                    halves4(r[2 * i], a0, a2);
-                    halves4(r[2 * i + 1], a1, a3);
+                for (int m = 0; m < MT; ++m) {
+                    uint32_t r[4];
+                    ldsm4(r, k_s + tile8_at<DP>(ld_key + m * 16, u + ld_unit));
 #pragma unroll
-                    for (int n = 0; n < NT; ++n) {
-                        const uint2 q = Cfg::kQInRegs ? qf[Cfg::kQInRegs ? n : 0][Cfg::kQInRegs ? u + i : 0] : query(n, u + i);
-                        mma16(s[n], a0, a1, a2, a3, q.x, q.y);
+                    for (int i = 0; i < 2; ++i) {
+                        uint32_t a0, a1, a2, a3;
+                        halves4(r[2 * i], a0, a2);
+                        halves4(r[2 * i + 1], a1, a3);
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) {
+                            const uint2 q = Cfg::kQInRegs ? qf[Cfg::kQInRegs ? n : 0][Cfg::kQInRegs ? u + i : 0] : query(n, u + i);
+                            mma16(s[m][n], a0, a1, a2, a3, q.x, q.y);
+                        }
                     }
                 }
             }
-            // s[n][0..1]: key g with rows 2c, 2c + 1; s[n][2..3]: key g + 8
-            bool grows = fmaxf(sc0.y, sc1.y) > unit_v;
+            // s[m][n][0..1]: key g with rows 2c, 2c + 1; s[m][n][2..3]: key g + 8
+            float high = 0.0f;  // the largest scale of values
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
+            for (int m = 0; m < MT; ++m) high = fmaxf(high, fmaxf(sc[m][0].y, sc[m][1].y));  // NaN is passed over
+            bool grows = high > unit_v;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    s[n][e] = s[n][e] * qdown[n][e & 1] * (e < 2 ? sc0.x : sc1.x);
-                    if (edge) {
-                        const int j = i0 + g + (e & 2) * 4 - len;
-                        const bool sees = j < 0 || (j < T && (word[n][e & 1] >> (j & 63) & 1));
-                        if (!sees) s[n][e] = -INFINITY;
-                    }
+            for (int n = 0; n < NT; ++n) {
+#pragma unroll
+                for (int m = 0; m < MT; ++m)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) s[m][n][e] = s[m][n][e] * qdown[n][e & 1] * sc[m][e >> 1].x;
+                if (edge) {
+#pragma unroll
+                    for (int m = 0; m < MT; ++m)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int j = i0 + m * 16 + g + (e & 2) * 4 - len;
+                            const bool sees = j < 0 || (j < T && (word[n][e & 1] >> (j & 63) & 1));
+                            if (!sees) s[m][n][e] = -INFINITY;
+                        }
+                }
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    float top = fmaxf(s[0][n][e], s[0][n][e + 2]);
+#pragma unroll
+                    for (int m = 1; m < MT; ++m) top = fmaxf(top, fmaxf(s[m][n][e], s[m][n][e + 2]));
                     // The difference is taken before the scale: scores of the type's lowest value differ by 0 from
                     // their maximum, where a fused s * c2 - ref * c2 would be off by the product's rounding.
-                    grows |= (s[n][e] - ref[n][e & 1]) * c2 > (float)Wt::kLazy;
+                    grows |= (top - ref[n][e]) * c2 > (float)Wt::kLazy;
                 }
+            }
             if (__any_sync(0xFFFFFFFFu, grows)) {
-                const float most = column_max(fmaxf(unit_v, fmaxf(sc0.y, sc1.y)));  // NaN is passed over
-                const float fall = unit_v * (most > 0.0f ? power_inverse(most) : 1.0f);
+                const float most = column_max(fmaxf(unit_v, high));
+                const float fall = most > 0.0f ? unit_v * power_inverse(most) : 1.0f;
                 if (most > 0.0f) unit_v = most, unit_inv = power_inverse(most);
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
                     float keep[2];
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        const float top = column_max(fmaxf(ref[n][e], fmaxf(s[n][e], s[n][e + 2])));
+                        float top = ref[n][e];
+#pragma unroll
+                        for (int m = 0; m < MT; ++m) top = fmaxf(top, fmaxf(s[m][n][e], s[m][n][e + 2]));
+                        top = column_max(top);
                         keep[e] = top == ref[n][e] ? 1.0f : ex2((ref[n][e] - top) * c2);
                         ref[n][e] = top;
                         sum[n][e] *= keep[e];
@@ -302,41 +422,50 @@ __global__ void __launch_bounds__(kThreads, Cfg8<DP, NT>::kCtas)
                     }
                 }
             }
-            const float v0 = sc0.y * unit_inv, v1 = sc1.y * unit_inv;
-            uint32_t ph[NT][2], pl[NT][2];
+            uint32_t ph[MT][NT][2], pl[MT][NT][2];
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
-                float w[4];
+                const float shift[2] = {shift_of(ref[n][0]), shift_of(ref[n][1])};
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float shift = ref[n][e & 1] == -INFINITY ? 0.0f : ref[n][e & 1];
-                    const float p = ex2(fmaf(s[n][e] - shift, c2, Wt::kUp));
-                    sum[n][e & 1] += p;
-                    w[e] = p * (e < 2 ? v0 : v1);
-                    if (edge && s[n][e] == -INFINITY) w[e] = 0.0f;  // whatever scale a key has that the row does not see
-                }
-                // The product takes fp16: a weight goes in as two terms, the second what the first one's rounding left.
+                for (int m = 0; m < MT; ++m) {
+                    float w[4];
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const uint32_t hi = pack<true>(w[2 * i], w[2 * i + 1]);
-                    const uint32_t lo = pack<true>(w[2 * i] - widen<true>((uint16_t)hi), w[2 * i + 1] - widen<true>((uint16_t)(hi >> 16)));
-                    ph[n][i] = transposed(hi), pl[n][i] = transposed(lo);
+                    for (int e = 0; e < 4; ++e) {
+                        const float p = ex2(fmaf(s[m][n][e] - shift[e & 1], c2, Wt::kUp));
+                        sum[n][e & 1] += p;
+                        w[e] = p * (sc[m][e >> 1].y * unit_inv);
+                    }
+                    if (edge) {  // whatever scale a key has that the row does not see
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            if (s[m][n][e] == -INFINITY) w[e] = 0.0f;
+                    }
+                    // The product takes fp16: a weight goes in as two terms, the second what the first one's rounding left.
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const uint32_t hi = pack<true>(w[2 * i], w[2 * i + 1]);
+                        const uint32_t lo = pack<true>(w[2 * i] - widen<true>((uint16_t)hi), w[2 * i + 1] - widen<true>((uint16_t)(hi >> 16)));
+                        ph[m][n][i] = transposed(hi), pl[m][n][i] = transposed(lo);
+                    }
                 }
             }
 #pragma unroll
             for (int u = 0; u < KD; u += 2) {
-                uint32_t r[4];
-                ldsm4t(r, v_s + tile8_at<DP>(ld_key, u + ld_unit));
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    // a register holds two keys' codes of elements 2g, 2g + 1: rows g and g + 8 of the product
-                    uint32_t a0, a1, a2, a3;
-                    halves4(__byte_perm(r[2 * i], 0, 0x3120), a0, a1);
-                    halves4(__byte_perm(r[2 * i + 1], 0, 0x3120), a2, a3);
+                for (int m = 0; m < MT; ++m) {
+                    uint32_t r[4];
+                    ldsm4t(r, v_s + tile8_at<DP>(ld_key + m * 16, u + ld_unit));
 #pragma unroll
-                    for (int n = 0; n < NT; ++n) {
-                        mma16(o[u + i][n], a0, a1, a2, a3, ph[n][0], ph[n][1]);
-                        mma16(o[u + i][n], a0, a1, a2, a3, pl[n][0], pl[n][1]);
+                    for (int i = 0; i < 2; ++i) {
+                        // a register holds two keys' codes of elements 2g, 2g + 1: rows g and g + 8 of the product
+                        uint32_t a0, a1, a2, a3;
+                        halves4(__byte_perm(r[2 * i], 0, 0x3120), a0, a1);
+                        halves4(__byte_perm(r[2 * i + 1], 0, 0x3120), a2, a3);
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) {
+                            mma16(o[u + i][n], a0, a1, a2, a3, ph[m][n][0], ph[m][n][1]);
+                            mma16(o[u + i][n], a0, a1, a2, a3, pl[m][n][0], pl[m][n][1]);
+                        }
                     }
                 }
             }
@@ -364,7 +493,7 @@ __global__ void __launch_bounds__(kThreads, Cfg8<DP, NT>::kCtas)
         }
         if (a.tile == a.ntile) {
             a.tile = a.ntile - 1;
-            step(plan, C.B, groups, a);
+            step<KEYS>(plan, C.B, groups, a);
         }
 
         // Join the warps: maxima and sums, then output rows in warp order, through the place of this list's queries,
@@ -388,7 +517,7 @@ __global__ void __launch_bounds__(kThreads, Cfg8<DP, NT>::kCtas)
                     st[w] = state_s[w * RB + n * 8 + 2 * c + e];
                     top = fmaxf(top, st[w].x);
                 }
-                const float sh = top == -INFINITY ? 0.0f : top;
+                const float sh = shift_of(top);
 #pragma unroll
                 for (int w = 0; w < 4; ++w) all += st[w].y * ex2((st[w].x - sh) * c2);
                 const float f = ex2((ref[n][e] - sh) * c2) * Wt::kDown;
@@ -400,31 +529,30 @@ __global__ void __launch_bounds__(kThreads, Cfg8<DP, NT>::kCtas)
                 ref[n][e] = top;
                 sum[n][e] = all * Wt::kDown;
             }
-        for (int w = 1; w < 4; ++w) {
-            if (w > 1) __syncthreads();
-            if (warp == w) {
 #pragma unroll
-                for (int n = 0; n < NT; ++n)
+        for (int n = 0; n < NT; ++n)
+#pragma unroll 1
+            for (int w = 1; w < 4; ++w) {
+                if (n + w > 1) __syncthreads();
+                if (warp == w) {
 #pragma unroll
                     for (int i = 0; i < KD; ++i)
 #pragma unroll
                         for (int e = 0; e < 2; ++e)
-                            *reinterpret_cast<float2*>(join_s + (n * 8 + 2 * c + e) * Cfg::kJoinRow + i * 16 + 2 * g) =
+                            *reinterpret_cast<float2*>(join_s + (2 * c + e) * Cfg::kJoinRow + i * 16 + 2 * g) =
                                 make_float2(o[i][n][e], o[i][n][e + 2]);
-            }
-            __syncthreads();
-            if (warp == 0) {
-#pragma unroll
-                for (int n = 0; n < NT; ++n)
+                }
+                __syncthreads();
+                if (warp == 0) {
 #pragma unroll
                     for (int i = 0; i < KD; ++i)
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
-                            const float2 v = *reinterpret_cast<const float2*>(join_s + (n * 8 + 2 * c + e) * Cfg::kJoinRow + i * 16 + 2 * g);
+                            const float2 v = *reinterpret_cast<const float2*>(join_s + (2 * c + e) * Cfg::kJoinRow + i * 16 + 2 * g);
                             o[i][n][e] += v.x, o[i][n][e + 2] += v.y;
                         }
+                }
             }
-        }
         if (warp != 0) continue;
         if (whole) {
 #pragma unroll
@@ -447,25 +575,42 @@ __global__ void __launch_bounds__(kThreads, Cfg8<DP, NT>::kCtas)
                     if (P.lse && g == 0) P.lse[at] = empty ? -INFINITY : lse_of(ref[n][e], P.scale, sum[n][e]);
                 }
         } else {
-            // the join takes fp16 caches' rows and sums times 2^15, see Weights
-            const float up = C.fp16 ? 1.0f / Weights<true, false>::kDown : 1.0f;
-            float* part = P.part + ((long long)blockIdx.x * 2 + (segment ? 1 : 0)) * part_floats(RB, DP);
+            const int piece = segment ? 1 : 0;
+            float* part = P.part + ((long long)blockIdx.x * 2 + piece) * part_floats(RB, DP);
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     const int r = n * 8 + 2 * c + e;
+                    if (rb * RB + r >= R) continue;
 #pragma unroll
                     for (int i = 0; i < KD; ++i)
-                        *reinterpret_cast<float2*>(part + r * DP + i * 16 + 2 * g) = make_float2(o[i][n][e] * up, o[i][n][e + 2] * up);
+                        if (i * 16 < D)
+                            *reinterpret_cast<float2*>(part + r * DP + i * 16 + 2 * g) = make_float2(o[i][n][e], o[i][n][e + 2]);
                     if (g == 0) {
                         part[RB * DP + r] = ref[n][e];
-                        part[RB * DP + RB + r] = sum[n][e] * up;
+                        part[RB * DP + RB + r] = sum[n][e];
                     }
                 }
+            __threadfence();
+            __syncwarp();
+            if (lane == 0) {
+                int first, last;
+                bool behind;
+                deal.ctas_of(b, rb + h * row_blocks, first, last, behind);
+                if (atomicAdd(P.done + first, 1u) == (unsigned)(last - first)) {
+                    P.done[first] = 0;  // for the next launch
+                    last_s[piece] = LastOf{1, b, rb + h * row_blocks, first, last, behind};
+                }
+            }
         }
     }
     cp_wait<0>();
+    __syncthreads();
+    __threadfence();
+#pragma unroll 1
+    for (int i = 0; i < 2; ++i)
+        if (last_s[i].on) join_parts<DP, RB>(P, plan, row_blocks, last_s[i], smem);
 }
 
 template <int DP, int NT>
@@ -480,9 +625,7 @@ cudaError_t launch_attend(const AttendParams& P, cudaStream_t st) {
     cudaError_t e = allow_max_smem(kern);
     if (e != cudaSuccess) return e;
     void* args[2] = {const_cast<AttendParams*>(&P), &row_blocks};
-    e = launch(reinterpret_cast<const void*>(kern), dim3(parts, 1, 1), kThreads, Cfg::smem(P.c.B), args, st);
-    if (e != cudaSuccess) return e;
-    return launch_tree_attention_join(P, Cfg::kRows, row_blocks, parts, st);
+    return launch(reinterpret_cast<const void*>(kern), dim3(parts, 1, 1), kThreads, Cfg::smem(P.c.B), args, st);
 }
 
 template <int NT>
@@ -491,7 +634,16 @@ cudaError_t launch_heads(const AttendParams& P, cudaStream_t st) {
     return P.c.D <= 128 ? launch_attend<128, NT>(P, st) : launch_attend<256, NT>(P, st);
 }
 
+constexpr int kMostCtas = 3;  // an SM, of any of the kernels
+
 }  // namespace
+
+int attend8_counters() { return kMostCtas * sm_count(); }
+
+long long attend8_partial_floats(int D) {
+    const long long ctas = (long long)sm_count() * (D <= 64 ? Cfg8<64, 2>::kCtas : D <= 128 ? Cfg8<128, 2>::kCtas : Cfg8<256, 2>::kCtas);
+    return ctas * 2 * part_floats(16, D <= 64 ? 64 : D <= 128 ? 128 : 256);
+}
 
 cudaError_t launch_tree_attention8(const AttendParams& P, cudaStream_t st) {
     return P.T * P.G <= 8 ? launch_heads<1>(P, st) : launch_heads<2>(P, st);

@@ -83,6 +83,7 @@ struct AttendParams {
     float* lse;               // attention: written (may be null); accumulate: read
     float* acc_out;           // accumulate (the cache's strides)
     float* part;              // attention: partial rows
+    unsigned* done;           // attention over codes: parts of a list that are there, by its first CTA; zero between launches
     unsigned* err;
 };
 // Scratch floats that launch_tree_attention needs at most for heads of D elements (0: cannot query the device).
@@ -92,12 +93,11 @@ bool attend_counts_fit(const AttendParams& P);
 cudaError_t launch_tree_attention(const AttendParams& P, cudaStream_t st);
 // attend_wide.cu: the first of the two kernels for many rows; says how it cut the work for the join.
 cudaError_t launch_tree_attention_wide(const AttendParams& P, int* row_blocks, int* parts, cudaStream_t st);
-// attend.cu: joins the partial rows of a first kernel of `parts` CTAs with blocks of 8 or 16 query rows, dealt as the
-// kernel for few rows deals them; maxima, sums and rows as that one writes them for P.c.fp16.
-cudaError_t launch_tree_attention_join(const AttendParams& P, int rows, int row_blocks, int parts, cudaStream_t st);
 cudaError_t launch_kv_accumulate(const AttendParams& P, cudaStream_t st);
 // attend8.cu, weigh8.cu: the same over a cache of e4m3 codes
 cudaError_t launch_tree_attention8(const AttendParams& P, cudaStream_t st);
+long long attend8_partial_floats(int D);
+int attend8_counters();
 cudaError_t launch_kv_accumulate8(const AttendParams& P, cudaStream_t st);
 
 // logprobs.cu

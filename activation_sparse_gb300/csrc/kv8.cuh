@@ -55,12 +55,12 @@ __device__ __forceinline__ uint32_t tile8_at(int row, int unit) {
     return (uint32_t)(row * DP + ((unit ^ swap) * 16));
 }
 
-// As Copy, for rows of codes.
-template <int DP>
+// As Copy, for rows of codes: a warp copies WK keys of every tile, lane i % WK holding the slot of key i.
+template <int DP, int WK = 16>
 struct Copy8 {
     static constexpr int UNITS = DP / 16;
     static constexpr int AT_ONCE = 32 / UNITS;
-    static constexpr int SWEEPS = 16 / AT_ONCE;
+    static constexpr int SWEEPS = WK / AT_ONCE;
     static __device__ __forceinline__ int row(int lane, int j) { return (lane / UNITS) * SWEEPS + j; }
     static __device__ __forceinline__ void slots(int held, int lane, int (&slot)[SWEEPS]) {
 #pragma unroll

@@ -66,7 +66,8 @@ struct si_kv {
     bool e4m3 = false;
     si_kv_scales scales = {};
     int device = -1;          // of the scratch, set with its first allocation
-    float* part = nullptr;    // partial attention rows
+    float* part = nullptr;    // partial attention rows; behind them, over codes, the counters of the lists' parts
+    unsigned* done = nullptr;
     unsigned* ticket = nullptr;  // eviction: a ticket and L * B lengths
 };
 
@@ -86,15 +87,28 @@ int on_device(si_kv* kv) {
 // holds its address.
 int make_part(si_kv* kv, cudaStream_t st) {
     if (kv->part) return SI_OK;
-    const long long need = si::attend_partial_floats(kv->d.D);
-    if (need <= 0) return fail(SI_ERR_CUDA, "cannot query the device for the attention grid");
+    long long need = si::attend_partial_floats(kv->d.D);
+    const int counters = kv->e4m3 ? si::attend8_counters() : 0;
+    if (need <= 0 || (kv->e4m3 && counters <= 0)) return fail(SI_ERR_CUDA, "cannot query the device for the attention grid");
+    if (kv->e4m3 && need < si::attend8_partial_floats(kv->d.D)) need = si::attend8_partial_floats(kv->d.D);
     if (capturing(st)) return fail(SI_ERR_INVALID_ARG, "attention scratch must be made; call once before capture");
-    const cudaError_t e = cudaMalloc(reinterpret_cast<void**>(&kv->part), (size_t)need * sizeof(float));
+    float* part = nullptr;
+    cudaError_t e = cudaMalloc(reinterpret_cast<void**>(&part), (size_t)(need + counters) * sizeof(float));
     if (e != cudaSuccess) {
         (void)cudaGetLastError();
-        kv->part = nullptr;
         return fail(SI_ERR_OOM, "cudaMalloc failed for the attention scratch");
     }
+    if (counters) {
+        e = cudaMemset(part + need, 0, (size_t)counters * sizeof(unsigned));
+        // the memset is on the legacy stream, `st` may not wait for that one
+        if (e == cudaSuccess) e = cudaStreamSynchronize(nullptr);
+        if (e != cudaSuccess) {
+            cudaFree(part);  // counters that may not be zero are not kept
+            return cuda_fail(e, "cudaMemset");
+        }
+        kv->done = reinterpret_cast<unsigned*>(part + need);
+    }
+    kv->part = part;
     return SI_OK;
 }
 
@@ -337,6 +351,7 @@ int si_tree_attention(si_kv* kv, int layer, int T, int Hq, const void* q, const 
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if ((rc = make_part(kv, st))) return rc;
     P.part = kv->part;
+    P.done = kv->done;
     const cudaError_t e = kv->e4m3 ? si::launch_tree_attention8(P, st) : si::launch_tree_attention(P, st);
     return e == cudaSuccess ? SI_OK : cuda_fail(e, "si_tree_attention");
 }

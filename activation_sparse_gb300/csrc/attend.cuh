@@ -206,10 +206,13 @@ __device__ void make_plan(const KvView& C, int T, int groups, int ctas, const Pl
         if (PIECE > 0 && C.B * groups <= ctas) {
             // the least number of tiles a part, from the even share up, that needs no more than ctas parts
             const int even = max(LEAST, div_of(total + ctas - 1, ctas));
-            int parts = 0;  // lane i tries even + i
+            unsigned fits = 0;
 #pragma unroll 1
-            for (int b = 0; b < C.B; ++b) parts += div_of(tiles_of<K>(p.tot[b]) + even + lane - 1, even + lane);
-            const unsigned fits = __ballot_sync(0xFFFFFFFFu, lane <= PIECE && parts * groups <= ctas);
+            for (int i = 0; i <= PIECE && !fits; ++i) {
+                int parts = 0;
+                for (int b = lane; b < C.B; b += 32) parts += div_of(tiles_of<K>(p.tot[b]) + even + i - 1, even + i);
+                if (__reduce_add_sync(0xFFFFFFFFu, parts) * groups <= ctas) fits = 1u << i;
+            }
             if (fits) q = even + __ffs(fits) - 1;
         }
         if (q) scan(p.part, [q](int n) { return div_of(n + q - 1, q); });

@@ -77,36 +77,66 @@ __device__ __forceinline__ float column_sum(float v) {
 
 __device__ __forceinline__ float shift_of(float m) { return m == -INFINITY ? 0.0f : m; }
 
-// Joins a list's parts: the CTA's ring is empty and takes the parts' weights.
+// Where the parts of lists lie: for each of a CTA's two pieces [CTA][row][DP] outputs, then [CTA][row] {maximum, sum},
+// with as many rows as a block can have in this call. A list's parts are neighbours, but for the first one where
+// another list comes before it in its CTA.
 template <int DP, int RB>
-__device__ void join_parts(const AttendParams& P, const Plan& plan, int row_blocks, const LastOf& l, uint8_t* smem) {
+struct Parts {
+    float* const at;
+    const int rows, ctas;
+    __device__ __forceinline__ Parts(const AttendParams& P) : at(P.part), rows(min(RB, P.T * P.G)), ctas(gridDim.x) {}
+    __device__ __forceinline__ float* out(int cta, int piece) const { return at + (long long)(piece * ctas + cta) * rows * DP; }
+    __device__ __forceinline__ float2* state(int cta, int piece) const {
+        return reinterpret_cast<float2*>(at + 2ll * ctas * rows * DP) + (piece * ctas + cta) * rows;
+    }
+};
+
+// Joins a list's parts: the CTA's ring is empty and takes them, as many at once as fit.
+template <int DP, int RB, int BYTES>
+__device__ void join_parts(const AttendParams& P, const Plan& plan, int row_blocks, const LastOf l, uint8_t* smem) {
     constexpr int CHUNK = 64, QUADS = DP / 4, ITEMS = RB * QUADS / kThreads > 0 ? RB * QUADS / kThreads : 1;
-    float* const weight_s = reinterpret_cast<float*>(smem);             // [part of a chunk][row]
+    constexpr int kOffRows = (CHUNK + 4) * RB * 4;
+    float* const weight_s = reinterpret_cast<float*>(smem);                    // [part of a chunk][row]
     float4* const state_s = reinterpret_cast<float4*>(weight_s + CHUNK * RB);  // [row] maximum, sum, what the sums so far are multiplied by
+    float4* const rows_s = reinterpret_cast<float4*>(smem + kOffRows);         // [part of a chunk][row][DP]
     const KvView& C = P.c;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int G = P.G, R = P.T * G, D = C.D;
     const int h = l.group / row_blocks, row0 = l.group % row_blocks * RB, rows = min(RB, R - row0);
+    const int chunk = min(CHUNK, (BYTES - kOffRows) / (rows * DP * 4)), quads = rows * QUADS;
     const float c2 = P.scale * kLog2e;
-    auto part_of = [&](int c) { return P.part + ((long long)c * 2 + (c == l.first && l.behind)) * part_floats(RB, DP); };
+    const Parts<DP, RB> parts(P);
+    auto piece_of = [&](int c) { return c == l.first && l.behind ? 1 : 0; };
     __syncthreads();
     if (tid < RB) state_s[tid] = make_float4(-INFINITY, 0.0f, 0.0f, 0.0f);
     float4 acc[ITEMS];
 #pragma unroll
     for (int i = 0; i < ITEMS; ++i) acc[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    for (int c0 = l.first; c0 <= l.last; c0 += CHUNK) {
-        const int n = min(CHUNK, l.last - c0 + 1);
+    for (int c0 = l.first; c0 <= l.last; c0 += chunk) {
+        const int n = min(chunk, l.last - c0 + 1);
         __syncthreads();
-        for (int r = warp; r < rows; r += 4) {
-            float m[2], s[2];
+        float2 st[2];
+        auto load_state = [&](int r) {
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                m[i] = -INFINITY, s[i] = 0.0f;
-                if (lane + 32 * i < n) {
-                    const float* p = part_of(c0 + lane + 32 * i) + RB * DP + r;
-                    m[i] = __ldcg(p), s[i] = __ldcg(p + RB);
-                }
+                st[i] = make_float2(-INFINITY, 0.0f);
+                const int c = c0 + lane + 32 * i;
+                if (r < rows && lane + 32 * i < n) st[i] = __ldcg(parts.state(c, piece_of(c)) + r);
             }
+        };
+        load_state(warp);  // ahead of the copies, which it would queue behind
+        // a thread copies what it will read: the quads tid, tid + kThreads, ... of every part
+        const uint32_t to = smem_u32(rows_s);
+        for (int q = tid; q < quads; q += kThreads) {
+            const float4* from = reinterpret_cast<const float4*>(parts.out(c0, 0)) + q;
+            const float4* from0 = reinterpret_cast<const float4*>(parts.out(c0, piece_of(c0))) + q;
+#pragma unroll 8
+            for (int c = 0; c < n; ++c) cp16(to + (c * quads + q) * 16, c ? from + (long long)c * (parts.rows * QUADS) : from0);
+        }
+        cp_commit();
+        for (int r = warp; r < rows; r += 4) {
+            if (r != warp) load_state(r);
+            const float m[2] = {st[0].x, st[1].x}, s[2] = {st[0].y, st[1].y};
             const float4 old = state_s[r];
             float top = fmaxf(m[0], m[1]);
 #pragma unroll
@@ -121,18 +151,20 @@ __device__ void join_parts(const AttendParams& P, const Plan& plan, int row_bloc
                 sum += w * s[i];
             }
             sum = warp_sum(sum);
+            __syncwarp();
             if (lane == 0) state_s[r] = make_float4(top, old.y * keep + sum, keep, 0.0f);
         }
+        cp_wait<0>();
         __syncthreads();
 #pragma unroll
         for (int i = 0; i < ITEMS; ++i) {
-            const int item = tid + i * kThreads, r = item / QUADS, q = item % QUADS;
-            if (r >= rows || q * 4 >= D) continue;
+            const int item = tid + i * kThreads, r = item / QUADS;
+            if (item >= quads) continue;
             const float keep = state_s[r].z;
             acc[i].x *= keep, acc[i].y *= keep, acc[i].z *= keep, acc[i].w *= keep;
-#pragma unroll 16
+#pragma unroll 4
             for (int c = 0; c < n; ++c) {
-                const float4 v = __ldcg(reinterpret_cast<const float4*>(part_of(c0 + c) + r * DP) + q);
+                const float4 v = rows_s[c * quads + item];
                 const float w = weight_s[c * RB + r];
                 acc[i].x += w * v.x, acc[i].y += w * v.y, acc[i].z += w * v.z, acc[i].w += w * v.w;
             }
@@ -141,7 +173,7 @@ __device__ void join_parts(const AttendParams& P, const Plan& plan, int row_bloc
 #pragma unroll
     for (int i = 0; i < ITEMS; ++i) {
         const int item = tid + i * kThreads, r = item / QUADS, q = item % QUADS;
-        if (r >= rows || q * 4 >= D) continue;
+        if (item >= quads || q * 4 >= D) continue;
         const float4 st = state_s[r];
         const int t = (row0 + r) / G, g = row0 + r - t * G;
         const bool empty = plan.tot[l.b] == 0 || word_of(P.mask, P.T, l.b, t) == 0 || st.y == 0.0f;
@@ -165,7 +197,6 @@ __global__ void __launch_bounds__(kThreads, Cfg8<DP, NT>::kCtas)
 
     extern __shared__ __align__(128) uint8_t smem[];
     uint8_t* const q_s = smem + Cfg::kOffQ;
-    float* const join_s = reinterpret_cast<float*>(q_s);
     float* const factor_s = reinterpret_cast<float*>(smem + Cfg::kOffFactor);
     float2* const state_s = reinterpret_cast<float2*>(smem + Cfg::kOffState);
     LastOf* const last_s = reinterpret_cast<LastOf*>(smem + Cfg::kOffLast);
@@ -250,12 +281,43 @@ __global__ void __launch_bounds__(kThreads, Cfg8<DP, NT>::kCtas)
         }
         cp_commit();
     };
+    // Query rows of a list's block into shared memory (rows past R are zero).
+    auto stage_queries = [&](const At& at) {
+        const int b = at.b, h = at.group / row_blocks, rb = at.group % row_blocks;
+        constexpr int AT_ONCE = 32 / (DP / 8);  // rows a warp takes at once
+#pragma unroll
+        for (int r0 = 0; r0 < RB; r0 += 4 * AT_ONCE) {
+            const int r = r0 + warp * AT_ONCE + lane / (DP / 8), row = rb * RB + r, t = row / G;
+            const bool on = r < RB && row < R;
+            const uint16_t* from = static_cast<const uint16_t*>(P.q) + b * P.qb + t * P.qt + (long long)(h * G + row - t * G) * P.qh;
+            float down;
+            const uint4 val = query_unit<DP>(on ? from : nullptr, D, C.fp16, lane, down);
+            if (r < RB) {
+                *reinterpret_cast<uint4*>(q_s + r * Cfg::kQRow + lane % (DP / 8) * 16) = val;
+                if (lane % (DP / 8) == 0) factor_s[r] = down;
+            }
+        }
+    };
+    // The first slots, the second tile's with the first's where they are of one list, and the first queries go out
+    // together: each is a trip to memory of its own.
+    At a = locate<KEYS>(plan, C.B, x0);
     src.enter(C, plan, row_blocks);
     fetch();
+    const int first_slot = held;
+    const bool two = x0 + 1 < x1 && a.tile + 1 < a.ntile;
+    if (two) {
+        ++src.at.tile;
+        fetch();
+        --src.at.tile;
+    }
+    const int second_slot = held;
+    held = first_slot;
+    stage_queries(a);
+    issue();
+    if (two) held = second_slot;
 #pragma unroll 1
-    for (int s = 0; s < S - 1; ++s) issue();
+    for (int s = 1; s < S - 1; ++s) issue();
 
-    At a = locate<KEYS>(plan, C.B, x0);
     int segment = 0, stage_out = 0;
     for (int x = x0; x < x1; ++segment) {
         // one list, or the part of it that this CTA has
@@ -264,22 +326,9 @@ __global__ void __launch_bounds__(kThreads, Cfg8<DP, NT>::kCtas)
         const int seg_end = min(x1, x + a.ntile - a.tile);
         const bool whole = a.tile == 0 && seg_end - x == a.ntile;
 
-        // query rows of this block into shared memory (rows past R are zero)
-        __syncthreads();  // the previous list's joins and reads of q_s are over
-        {
-            constexpr int AT_ONCE = 32 / (DP / 8);  // rows a warp takes at once
-#pragma unroll
-            for (int r0 = 0; r0 < RB; r0 += 4 * AT_ONCE) {
-                const int r = r0 + warp * AT_ONCE + lane / (DP / 8), row = rb * RB + r, t = row / G;
-                const bool on = r < RB && row < R;
-                const uint16_t* from = static_cast<const uint16_t*>(P.q) + b * P.qb + t * P.qt + (long long)(h * G + row - t * G) * P.qh;
-                float down;
-                const uint4 val = query_unit<DP>(on ? from : nullptr, D, C.fp16, lane, down);
-                if (r < RB) {
-                    *reinterpret_cast<uint4*>(q_s + r * Cfg::kQRow + lane % (DP / 8) * 16) = val;
-                    if (lane % (DP / 8) == 0) factor_s[r] = down;
-                }
-            }
+        if (segment > 0) {
+            __syncthreads();  // the previous list's joins and reads of q_s are over
+            stage_queries(a);
         }
         unsigned long long word[NT][2];
         float ref[NT][2], sum[NT][2], qdown[NT][2];
@@ -497,7 +546,7 @@ __global__ void __launch_bounds__(kThreads, Cfg8<DP, NT>::kCtas)
         }
 
         // Join the warps: maxima and sums, then output rows in warp order, through the place of this list's queries,
-        // which are no longer needed. (The ring's stages are not touched: the next list's copies are in flight.)
+        // which are no longer needed: in the ring the next list's copies are in flight.
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -529,28 +578,35 @@ __global__ void __launch_bounds__(kThreads, Cfg8<DP, NT>::kCtas)
                 ref[n][e] = top;
                 sum[n][e] = all * Wt::kDown;
             }
+        // (All at once where the ring is idle: after the CTA's last tile.)
+        float* const join_s = reinterpret_cast<float*>(x < x1 ? q_s : smem);
+        const int at_once = x < x1 ? 1 : 3;
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll 1
-            for (int w = 1; w < 4; ++w) {
+            for (int w = 1; w < 4; w += at_once) {
                 if (n + w > 1) __syncthreads();
-                if (warp == w) {
+                float* const place = join_s + 2 * c * Cfg::kJoinRow + 2 * g;
+                constexpr int kArea = 8 * Cfg::kJoinRow;
+                if (warp >= w && warp < w + at_once) {
 #pragma unroll
                     for (int i = 0; i < KD; ++i)
 #pragma unroll
                         for (int e = 0; e < 2; ++e)
-                            *reinterpret_cast<float2*>(join_s + (2 * c + e) * Cfg::kJoinRow + i * 16 + 2 * g) =
+                            *reinterpret_cast<float2*>(place + (warp - w) * kArea + e * Cfg::kJoinRow + i * 16) =
                                 make_float2(o[i][n][e], o[i][n][e + 2]);
                 }
                 __syncthreads();
                 if (warp == 0) {
+#pragma unroll 1
+                    for (int k = 0; k < at_once; ++k)
 #pragma unroll
-                    for (int i = 0; i < KD; ++i)
+                        for (int i = 0; i < KD; ++i)
 #pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const float2 v = *reinterpret_cast<const float2*>(join_s + (2 * c + e) * Cfg::kJoinRow + i * 16 + 2 * g);
-                            o[i][n][e] += v.x, o[i][n][e + 2] += v.y;
-                        }
+                            for (int e = 0; e < 2; ++e) {
+                                const float2 v = *reinterpret_cast<const float2*>(place + k * kArea + e * Cfg::kJoinRow + i * 16);
+                                o[i][n][e] += v.x, o[i][n][e + 2] += v.y;
+                            }
                 }
             }
         if (warp != 0) continue;
@@ -576,7 +632,8 @@ __global__ void __launch_bounds__(kThreads, Cfg8<DP, NT>::kCtas)
                 }
         } else {
             const int piece = segment ? 1 : 0;
-            float* part = P.part + ((long long)blockIdx.x * 2 + piece) * part_floats(RB, DP);
+            const Parts<DP, RB> parts(P);
+            float* part = parts.out(blockIdx.x, piece);
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -587,10 +644,7 @@ __global__ void __launch_bounds__(kThreads, Cfg8<DP, NT>::kCtas)
                     for (int i = 0; i < KD; ++i)
                         if (i * 16 < D)
                             *reinterpret_cast<float2*>(part + r * DP + i * 16 + 2 * g) = make_float2(o[i][n][e], o[i][n][e + 2]);
-                    if (g == 0) {
-                        part[RB * DP + r] = ref[n][e];
-                        part[RB * DP + RB + r] = sum[n][e];
-                    }
+                    if (g == 0) parts.state(blockIdx.x, piece)[r] = make_float2(ref[n][e], sum[n][e]);
                 }
             __threadfence();
             __syncwarp();
@@ -607,10 +661,11 @@ __global__ void __launch_bounds__(kThreads, Cfg8<DP, NT>::kCtas)
     }
     cp_wait<0>();
     __syncthreads();
+    if (!last_s[0].on && !last_s[1].on) return;
     __threadfence();
 #pragma unroll 1
     for (int i = 0; i < 2; ++i)
-        if (last_s[i].on) join_parts<DP, RB>(P, plan, row_blocks, last_s[i], smem);
+        if (last_s[i].on) join_parts<DP, RB, Cfg::kOffQ>(P, plan, row_blocks, last_s[i], smem);
 }
 
 template <int DP, int NT>

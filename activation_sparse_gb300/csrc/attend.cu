@@ -630,8 +630,9 @@ long long attend_partial_floats(int D) {
 bool attend_counts_fit(const AttendParams& P) {
     constexpr long long kMost = INT_MAX - (1 << 20);  // room for a grid and a tile beside them
     const int R = P.T * P.G;
-    const int rows = P.c.e4m3 ? 8  // the least block of its kernels
-                     : many_rows(P.c.D, R) ? wide_rows(R) : 16 * (padded(P.c.D) > 128 ? row_warps(R) : 1);
+    const int rows = many_rows(P.c.D, R) ? wide_rows(R)
+                     : P.c.e4m3          ? (R <= 8 ? 8 : 16)
+                                         : 16 * (padded(P.c.D) > 128 ? row_warps(R) : 1);
     const long long lists = (long long)P.c.B * P.c.Hkv * ((R + rows - 1) / rows);
     const long long tiles = (long long)P.c.cap / KT + 1;
     return P.c.cap <= kMost && lists <= kMost / tiles && lists <= kMost / rows;
@@ -639,6 +640,7 @@ bool attend_counts_fit(const AttendParams& P) {
 
 cudaError_t launch_tree_attention(const AttendParams& P, cudaStream_t st) {
     if (many_rows(P.c.D, P.T * P.G)) return launch_wide(P, st);
+    if (P.c.e4m3) return launch_tree_attention8(P, st);
     return P.c.fp16 ? launch_attend_type<true>(P, st) : launch_attend_type<false>(P, st);
 }
 

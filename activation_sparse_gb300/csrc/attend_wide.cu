@@ -33,10 +33,14 @@
 // output's own rounding alone (fp16 0.00021 instead of 0.00028), but the
 // second terms' instructions lie in the chain that bounds this kernel (72 / 80 us
 // above; 6 trees of 16 nodes, 9001 keys 27.5 / 28.6).
+// Over a cache of e4m3 codes the copying warps load a tile's codes into registers while they
+// turn the tile before into the type of q, its scales in it (exactly, see
+// si_kv_create_e4m3): the rest of the kernel does not know.
 // Every write to shared memory is an ordinary one; the issuing warp's proxy
 // fence, after the barrier that announces it, lets the tensor cores see it. All
 // waits are bounded; TMEM is always released.
 #include "attend.cuh"
+#include "kv8.cuh"
 
 namespace si {
 
@@ -45,16 +49,20 @@ namespace {
 constexpr int kBlock = 128;        // query rows of one product: a TMEM lane each
 constexpr int kCopyWarps = 4, kCopyThreads = 32 * kCopyWarps;
 
-// NB row blocks a CTA meet every key tile it copies.
-template <int DP, int NB>
+// NB row blocks a CTA meet every key tile it copies. E4M3: a cache of codes, which are copied as they are (a key or a
+// value tile each of kRaw places) and then become a ring slot's elements.
+template <int DP, int NB, bool E4M3>
 struct WideCfg {
     static constexpr int kRows = kBlock * NB;
     static constexpr int kSoftmaxWarps = 4 * NB;
     static constexpr int kMmaWarp = kSoftmaxWarps, kCopyWarp = kMmaWarp + 1;
     static constexpr int kThreads = 32 * (kCopyWarp + kCopyWarps);
     static constexpr int kCtas = NB == 1 ? 2 : 1;              // an SM
-    static constexpr int kMaxSlots = NB == 1 ? 5 : 9;          // ring slots: a key or a value tile each
+    static constexpr int kMaxSlots = E4M3 ? (NB == 1 ? 3 : 6) : NB == 1 ? 5 : 9;  // ring slots: a key or a value tile each
     static constexpr int kTile = KT * DP * 2;
+    static constexpr int kRaw = !E4M3 ? 0 : NB == 1 ? 3 : 6;
+    static constexpr int kScaleTiles = 4;                      // whose scales are kept
+    static constexpr int kRawBytes = kRaw * (kTile / 2) + (E4M3 ? kCopyWarps * kScaleTiles * 32 * 4 : 0);
     static constexpr int kQ = kBlock * DP * 2;                 // of one block
     static constexpr int kOffRing = NB * kQ;
     static constexpr int kColP = KT / 2, kColO = 2 * KT;       // TMEM columns of a block: two S (P in the second half), O
@@ -62,7 +70,7 @@ struct WideCfg {
     static constexpr int kTmemCols = NB * kCols <= 256 ? 256 : 512;
     static constexpr int kBars = 2 * kMaxSlots + 7 * NB;
     static constexpr int fixed(int B) { return (kBars + 1) * 8 + (kMaxSlots + 1) * 8 + 16 + Plan::words(B) * 4; }
-    static constexpr int smem(int B, int slots) { return kOffRing + slots * kTile + fixed(B); }
+    static constexpr int smem(int B, int slots) { return kOffRing + slots * kTile + kRawBytes + fixed(B); }
     static constexpr int kSmemLimit = NB == 1 ? 113 * 1024 : 227 * 1024;  // of the SM's 228 KB, 1 KB a CTA is the system's
 };
 
@@ -195,17 +203,175 @@ __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.
 
 }  // namespace
 
+// Sixteen codes times their scale as sixteen elements of the type, exactly.
+template <bool FP16>
+__device__ __forceinline__ void elements16(uint4 codes, float scale, uint4& lo, uint4& hi) {
+    const uint32_t w[4] = {codes.x, codes.y, codes.z, codes.w};
+    uint32_t e[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        uint32_t h[2];
+        halves4(w[i], h[0], h[1]);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const __half2 x = *reinterpret_cast<const __half2*>(&h[j]);
+            if (FP16) {
+                const __half2 y = __hmul2(x, __float2half2_rn(scale));
+                e[2 * i + j] = *reinterpret_cast<const uint32_t*>(&y);
+            } else {
+                const float2 f = __half22float2(x);
+                e[2 * i + j] = pack<false>(f.x * scale, f.y * scale);
+            }
+        }
+    }
+    lo = make_uint4(e[0], e[1], e[2], e[3]), hi = make_uint4(e[4], e[5], e[6], e[7]);
+}
+
+// The copying warps over a cache of codes: every lane copies 16 bytes of DP / 32 of its warp's sixteen keys, several tiles
+// ahead, and turns what it copied itself into elements.
 template <int DP, int NB, bool FP16>
-__global__ void __launch_bounds__(WideCfg<DP, NB>::kThreads, WideCfg<DP, NB>::kCtas)
+__device__ __forceinline__ void copy_codes(const AttendParams& P, const Plan& plan, int row_blocks, int x0, int x1, int slots,
+                                           uint8_t* ring, uint64_t* full, uint64_t* empty, uint16_t* odd) {
+    using Cfg = WideCfg<DP, NB, true>;
+    using Cp = Copy8<DP>;
+    constexpr int RAW = Cfg::kRaw;
+    const KvView& C = P.c;
+    const int T = P.T, D = C.D, groups = C.Hkv * row_blocks;
+    const int warp = (threadIdx.x >> 5) - Cfg::kCopyWarp, lane = threadIdx.x & 31, unit = lane % Cp::UNITS;
+    const int own0 = warp * 16;
+    const bool unit_on = unit * 16 < D;
+    const int n_slots = (int)C.n_slots, k_step = (int)C.ks, v_step = (int)C.vs;
+    uint8_t* const sub_tile = ring + (unit >> 2) * (KT * 128);  // 64 elements are four units of codes
+    uint8_t* const raw = ring + slots * Cfg::kTile + (warp * 32 + lane) * 16;  // [place][row of the lane][thread]
+    float* const scale_s = reinterpret_cast<float*>(ring + slots * Cfg::kTile + RAW * (Cfg::kTile / 2)) + warp * Cfg::kScaleTiles * 32;
+    const uint32_t raw_addr = smem_u32(raw);
+    constexpr int kPlace = Cfg::kTile / 2, kRow = kCopyThreads * 16;
+    SourceOf<uint8_t> src;
+    src.start(plan, C.B, x0, x1);
+    int held = kNoSlot, seen_b = -1;
+    auto fetch = [&]() {
+        const int i0 = src.at.tile * KT;
+        if (i0 + KT > src.len && seen_b != src.at.b) {
+            src.seen = seen_nodes(P.mask, T, src.at.b, lane);
+            seen_b = src.at.b;
+        }
+        held = slot_of(src.list, i0 + own0 + (lane & 15), src.len, src.tot, src.seen);
+    };
+    int slot[Cp::SWEEPS];
+    int in = 0, in_tile = 0, byte = 0;  // place of the next copies; lanes below 16 have their key's scale, the others its value's
+    const uint8_t* v_from = nullptr;
+    bool on = false;                    // whether the values of the tile whose keys went last are still to come
+    auto copy = [&](const uint8_t* from, int step_) {
+#pragma unroll
+        for (int j = 0; j < Cp::SWEEPS; ++j) {
+            const bool there = slot[j] >= 0 && unit_on;
+            cp16(raw_addr + in * kPlace + j * kRow, there ? from + (long long)slot[j] * step_ + unit * 16 : from, there);
+        }
+        if (++in == RAW) in = 0;
+    };
+    // the next key or value tile's copies, in turn
+    auto issue = [&]() {
+        if (on) {
+            copy(v_from, v_step);
+            scale_s[in_tile * 32 + lane] = scale_of(byte, C.e_lo, C.e_hi);
+            if (++in_tile == Cfg::kScaleTiles) in_tile = 0;
+            on = false;
+        } else if (src.x < x1) {
+            const bool ok = slot_ok(held, n_slots, P.err);
+            const int mine = ok ? held : src.at.tile * KT + KT <= src.len ? 0 : -1;  // a bad slot has been reported; slot 0 is read
+            Cp::slots(mine, lane, slot);
+            byte = 127;
+            if (mine >= 0) byte = (lane < 16 ? src.k_scale : src.v_scale)[mine >> C.block_shift];
+            copy(src.k, k_step);
+            v_from = src.v;
+            on = true;
+            if (src.next(plan, C.B, groups) && src.x < x1) src.enter(C, plan, row_blocks);
+            if (src.x < x1) fetch();
+        }
+        cp_commit();
+    };
+    int at = 0, fill = 0;               // ring slot of the next group and how often the ring has been round
+    auto take = [&]() {
+        if (fill > 0) mbar_wait(&empty[at], (uint32_t)((fill - 1) & 1), P.err, kSiteAttend | kSiteEmpty);
+        __syncwarp();
+        const int mine = at;
+        if (++at == slots) at = 0, ++fill;
+        return mine;
+    };
+    int out = 0, out_tile = 0;          // place of the next tile that becomes elements
+    auto load = [&](uint4 (&to)[Cp::SWEEPS]) {
+        cp_wait<RAW - 2>();
+#pragma unroll
+        for (int j = 0; j < Cp::SWEEPS; ++j) to[j] = *reinterpret_cast<const uint4*>(raw + out * kPlace + j * kRow);
+        if (++out == RAW) out = 0;
+        issue();
+    };
+    auto store = [&](int slot_at, const uint4 (&from)[Cp::SWEEPS], float scale, int first_lane) {
+        uint8_t* tile = sub_tile + slot_at * Cfg::kTile;
+#pragma unroll
+        for (int j = 0; j < Cp::SWEEPS; ++j) {
+            const int r = Cp::row(lane, j);
+            uint4 lo, hi;
+            elements16<FP16>(from[j], __shfl_sync(0xFFFFFFFFu, scale, first_lane + r), lo, hi);
+            *reinterpret_cast<uint4*>(tile + sw128(own0 + r, 2 * (unit & 3))) = lo;
+            *reinterpret_cast<uint4*>(tile + sw128(own0 + r, 2 * (unit & 3) + 1)) = hi;
+        }
+    };
+    src.enter(C, plan, row_blocks);
+    fetch();
+#pragma unroll 1
+    for (int i = 0; i < RAW - 1; ++i) issue();
+    At a = locate(plan, C.B, x0);
+    for (int x = x0; x < x1; ++x, step(plan, C.B, groups, a)) {
+        const int i0 = a.tile * KT, len = plan.len[a.b];
+        const bool cached = i0 + KT <= len;
+        uint4 codes[Cp::SWEEPS];
+        load(codes);
+        __syncwarp();
+        float scale = scale_s[out_tile * 32 + lane];  // written with the values' copies, which went out before now
+        if (++out_tile == Cfg::kScaleTiles) out_tile = 0;
+        const int k_at = take();
+        store(k_at, codes, scale, 0);
+        mbar_arrive(&full[k_at]);
+        load(codes);
+        unsigned bad = 0;
+        if (!cached) {
+            // New nodes' value rows that are NaN leave the tile (0 * NaN is NaN) and are reported, so that the rows that
+            // see them get them back at the end.
+            const int node = i0 + own0 + (lane & 15) - len;
+            if (lane >= 16 && node >= 0 && node < T && scale != scale) bad |= 1u << (lane & 15), scale = 0.0f;
+#pragma unroll
+            for (int j = 0; j < Cp::SWEEPS; ++j) {
+                const int r = Cp::row(lane, j), of = i0 + own0 + r - len;
+                if (of < 0 || of >= T) continue;
+                uint32_t* w = reinterpret_cast<uint32_t*>(&codes[j]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int k = 0; k < 32; k += 8)
+                        if (code_nan(w[i] >> k)) w[i] &= ~(0xFFu << k), bad |= 1u << r;
+            }
+            bad = __reduce_or_sync(0xFFFFFFFFu, bad);
+        }
+        const int v_at = take();
+        store(v_at, codes, scale, 16);
+        if (!cached && lane == 0) odd[v_at * 4 + own0 / 16] = (uint16_t)bad;
+        mbar_arrive(&full[v_at]);
+    }
+    cp_wait<0>();
+}
+
+template <int DP, int NB, bool FP16, bool E4M3>
+__global__ void __launch_bounds__(WideCfg<DP, NB, E4M3>::kThreads, WideCfg<DP, NB, E4M3>::kCtas)
     k_tree_attention_wide(const __grid_constant__ AttendParams P, int row_blocks, int slots) {
-    using Cfg = WideCfg<DP, NB>;
+    using Cfg = WideCfg<DP, NB, E4M3>;
     constexpr int kThreads = Cfg::kThreads, kMaxSlots = Cfg::kMaxSlots;
     using Cp = Copy<DP>;
     using Wt = Weights<FP16, true>;
     extern __shared__ __align__(1024) uint8_t smem[];  // the swizzle needs tiles on 1024-byte boundaries
     uint8_t* const q_s = smem;
     uint8_t* const ring = smem + Cfg::kOffRing;
-    uint64_t* const full = reinterpret_cast<uint64_t*>(ring + slots * Cfg::kTile);
+    uint64_t* const full = reinterpret_cast<uint64_t*>(ring + slots * Cfg::kTile + Cfg::kRawBytes);
     uint64_t* const empty = full + kMaxSlots;
     uint64_t* const q_full = empty + kMaxSlots;  // [block] this list's queries are in shared memory
     uint64_t* const s_full = q_full + NB;        // [block][2] S of a tile is in TMEM
@@ -264,7 +430,9 @@ __global__ void __launch_bounds__(WideCfg<DP, NB>::kThreads, WideCfg<DP, NB>::kC
 
     if (x0 >= x1) {
         // more CTAs than tiles: nothing to do
-    } else if (warp >= Cfg::kCopyWarp) {
+    } else if (E4M3 && warp >= Cfg::kCopyWarp) {
+        copy_codes<DP, NB, FP16>(P, plan, row_blocks, x0, x1, slots, ring, full, empty, odd);
+    } else if (!E4M3 && warp >= Cfg::kCopyWarp) {
         // ---------------------------------------------------------- copies
         const int own0 = (warp - Cfg::kCopyWarp) * 16, unit = lane % Cp::UNITS;
         const bool unit_on = unit * 8 < D, whole_rows = D == DP;
@@ -592,11 +760,19 @@ __global__ void __launch_bounds__(WideCfg<DP, NB>::kThreads, WideCfg<DP, NB>::kC
                 for (unsigned long long left = odd_nodes; left; left &= left - 1) {
                     const int node = __ffsll((long long)left) - 1;
                     const long long slot = list ? list[len + node] : len + node;
-                    const uint16_t* src = static_cast<const uint16_t*>(C.v) + b * C.vb + h * C.vh + slot * C.vs;
+                    if (E4M3) {
+                        const uint8_t* src = static_cast<const uint8_t*>(C.v) + b * C.vb + h * C.vh + slot * C.vs;
+                        const bool row = C.v_scale[b * C.vcb + h * C.vch + (slot >> C.block_shift)] == kScaleNaN;
 #pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        if (c + i < D && not_finite<FP16>(src[c + i]))
-                            o[i] = __float_as_uint(__uint_as_float(o[i]) + widen<FP16>(src[c + i]));
+                        for (int i = 0; i < 32; ++i)
+                            if (c + i < D && (row || code_nan(src[c + i]))) o[i] = __float_as_uint(NAN);
+                    } else {
+                        const uint16_t* src = static_cast<const uint16_t*>(C.v) + b * C.vb + h * C.vh + slot * C.vs;
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            if (c + i < D && not_finite<FP16>(src[c + i]))
+                                o[i] = __float_as_uint(__uint_as_float(o[i]) + widen<FP16>(src[c + i]));
+                    }
                 }
                 // 32 columns of the warp's 32 rows through shared memory, so that a store covers whole lines
                 __syncwarp();
@@ -659,10 +835,10 @@ __global__ void __launch_bounds__(WideCfg<DP, NB>::kThreads, WideCfg<DP, NB>::kC
 
 namespace {
 
-template <int DP, int NB, bool FP16>
+template <int DP, int NB, bool FP16, bool E4M3>
 cudaError_t launch_wide(const AttendParams& P, int row_blocks, int parts, cudaStream_t st) {
-    using Cfg = WideCfg<DP, NB>;
-    const auto kern = k_tree_attention_wide<DP, NB, FP16>;
+    using Cfg = WideCfg<DP, NB, E4M3>;
+    const auto kern = k_tree_attention_wide<DP, NB, FP16, E4M3>;
     const cudaError_t e = allow_max_smem(kern);
     if (e != cudaSuccess) return e;
     int slots = Cfg::kMaxSlots;
@@ -671,10 +847,16 @@ cudaError_t launch_wide(const AttendParams& P, int row_blocks, int parts, cudaSt
     return launch(reinterpret_cast<const void*>(kern), dim3(parts, 1, 1), Cfg::kThreads, Cfg::smem(P.c.B, slots), args, st);
 }
 
-template <int DP, bool FP16>
+template <int DP, bool FP16, bool E4M3>
 cudaError_t launch_rows(const AttendParams& P, int rows, int row_blocks, int parts, cudaStream_t st) {
-    return rows == kBlock ? launch_wide<DP, 1, FP16>(P, row_blocks, parts, st)
-                          : launch_wide<DP, 2, FP16>(P, row_blocks, parts, st);
+    return rows == kBlock ? launch_wide<DP, 1, FP16, E4M3>(P, row_blocks, parts, st)
+                          : launch_wide<DP, 2, FP16, E4M3>(P, row_blocks, parts, st);
+}
+
+template <bool FP16, bool E4M3>
+cudaError_t launch_heads(const AttendParams& P, int rows, int row_blocks, int parts, cudaStream_t st) {
+    return P.c.D <= 64 ? launch_rows<64, FP16, E4M3>(P, rows, row_blocks, parts, st)
+                       : launch_rows<128, FP16, E4M3>(P, rows, row_blocks, parts, st);
 }
 
 }  // namespace
@@ -684,11 +866,11 @@ cudaError_t launch_tree_attention_wide(const AttendParams& P, int* row_blocks, i
     *row_blocks = (P.T * P.G + rows - 1) / rows;
     *parts = sm_count() * (rows == kBlock ? 2 : 1);
     if (*parts < 1) return cudaErrorInvalidDevice;
-    if (P.c.D <= 64)
-        return P.c.fp16 ? launch_rows<64, true>(P, rows, *row_blocks, *parts, st)
-                        : launch_rows<64, false>(P, rows, *row_blocks, *parts, st);
-    return P.c.fp16 ? launch_rows<128, true>(P, rows, *row_blocks, *parts, st)
-                    : launch_rows<128, false>(P, rows, *row_blocks, *parts, st);
+    if (P.c.e4m3)
+        return P.c.fp16 ? launch_heads<true, true>(P, rows, *row_blocks, *parts, st)
+                        : launch_heads<false, true>(P, rows, *row_blocks, *parts, st);
+    return P.c.fp16 ? launch_heads<true, false>(P, rows, *row_blocks, *parts, st)
+                    : launch_heads<false, false>(P, rows, *row_blocks, *parts, st);
 }
 
 }  // namespace si

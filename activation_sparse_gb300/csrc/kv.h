@@ -90,11 +90,11 @@ struct AttendParams {
 long long attend_partial_floats(int D);
 // Whether the kernels' 32-bit counts hold every tile of 64 keys of every list's row blocks, and the join's blocks.
 bool attend_counts_fit(const AttendParams& P);
-cudaError_t launch_tree_attention(const AttendParams& P, cudaStream_t st);
+cudaError_t launch_tree_attention(const AttendParams& P, cudaStream_t st);  // of either kind of cache
 // attend_wide.cu: the first of the two kernels for many rows; says how it cut the work for the join.
 cudaError_t launch_tree_attention_wide(const AttendParams& P, int* row_blocks, int* parts, cudaStream_t st);
 cudaError_t launch_kv_accumulate(const AttendParams& P, cudaStream_t st);
-// attend8.cu, weigh8.cu: the same over a cache of e4m3 codes
+// attend8.cu, weigh8.cu: attention of few rows a key, and weights, over a cache of e4m3 codes
 cudaError_t launch_tree_attention8(const AttendParams& P, cudaStream_t st);
 long long attend8_partial_floats(int D);
 int attend8_counters();

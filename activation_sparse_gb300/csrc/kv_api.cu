@@ -352,7 +352,7 @@ int si_tree_attention(si_kv* kv, int layer, int T, int Hq, const void* q, const 
     if ((rc = make_part(kv, st))) return rc;
     P.part = kv->part;
     P.done = kv->done;
-    const cudaError_t e = kv->e4m3 ? si::launch_tree_attention8(P, st) : si::launch_tree_attention(P, st);
+    const cudaError_t e = si::launch_tree_attention(P, st);
     return e == cudaSuccess ? SI_OK : cuda_fail(e, "si_tree_attention");
 }
 

@@ -804,6 +804,9 @@ def si_kv_evict(kv: KV, T, budget, sinks=0, recent=0, path=None, n_path=None, ta
 # ------------------------------------------------------- what a step answers with
 
 
+_logit_types = {}
+
+
 def si_token_logprobs(logits, targets=None, logp=None, entropy=None, top_logp=None, top_ids=None, temperature=1.0,
                       stream=None):
     """Log probabilities under logits [N][V] / temperature (bf16, fp16 or
@@ -811,11 +814,15 @@ def si_token_logprobs(logits, targets=None, logp=None, entropy=None, top_logp=No
     (an id outside the vocabulary: -inf), the rows' entropy fp32 [N], and the
     K <= 32 best tokens' top_logp fp32 and top_ids int32 [N][K], falling, ties
     to the lower id. Each output is optional."""
-    torch = _torch()
-    dtype = {torch.bfloat16: SI_BF16, torch.float16: SI_FP16, torch.float32: SI_FP32}.get(logits.dtype)
+    dtype = _logit_types.get(logits.dtype)
     if dtype is None:
-        raise ValueError("logits must be bf16, fp16 or fp32")
-    xp = _dev(logits, logits.dtype, "logits", None, 2)
+        torch = _torch()
+        _logit_types.update({torch.bfloat16: SI_BF16, torch.float16: SI_FP16, torch.float32: SI_FP32})
+        dtype = _logit_types.get(logits.dtype)
+        if dtype is None:
+            raise ValueError("logits must be bf16, fp16 or fp32")
+    if not (logits.is_cuda and logits.dim() == 2 and logits.stride(1) == 1):
+        _dev(logits, logits.dtype, "logits", None, 2)
     N, V = logits.shape
     if V < 1:
         raise ValueError("logits must have at least one column")
@@ -830,7 +837,8 @@ def si_token_logprobs(logits, targets=None, logp=None, entropy=None, top_logp=No
         if top_ids.dim() != 2:
             raise ValueError("top_ids must have shape (N, K)")
         K = top_ids.shape[1]
-    rc = _lib.si_token_logprobs(dtype, xp, logits.stride(0), N, V, temperature,
+    torch = _torch()
+    rc = _lib.si_token_logprobs(dtype, logits.data_ptr(), logits.stride(0), N, V, temperature,
                                 _whole(targets, torch.int32, "targets", (N, M)), M,
                                 _whole(logp, torch.float32, "logp", (N, M)), _whole(entropy, torch.float32, "entropy", (N,)),
                                 K, _whole(top_logp, torch.float32, "top_logp", (N, K)),

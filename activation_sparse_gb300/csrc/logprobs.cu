@@ -155,7 +155,8 @@ __global__ void __launch_bounds__(kThreads, 4) k_token_logprobs(const __grid_con
 
     Sums a{-INFINITY, 0.0f, 0.0f};
     uint64_t s2 = 0, u2 = 0;  // what belongs to a.s and a.u, in two sums each
-    int best = has_head ? tid : u0 + tid < u1 ? head + (u0 + tid) * U::N : has_tail ? head + units * U::N + tid : -1;
+    // where the largest was first: a logit, or -2 - j of the batch that starts with unit j (-1: the thread has none)
+    int best = has_head ? tid : u0 + tid < u1 ? -2 - (u0 + tid) : has_tail ? head + units * U::N + tid : -1;
     auto grow = [&](float top) {
         if (a.m != -INFINITY) {
             const float d = fmaxf((a.m - top) * c, -1000.0f), f = ex2(d);
@@ -202,21 +203,7 @@ __global__ void __launch_bounds__(kThreads, 4) k_token_logprobs(const __grid_con
             const float2 h = U::pair(hi), l = U::pair(lo);
             top = max_nan(h.x, h.y), low = fminf(l.x, l.y);
         }
-        if (!(top <= a.m) && a.m == a.m) {  // it grows, or is NaN now: the first of them
-#pragma unroll
-            for (int i = 4 * kBatch - 1; i >= 0; --i) {
-                const int id = head + (j + i / 4 * kThreads) * U::N + i % 4 * U::kWord;
-                if (DTYPE == SI_FP32) {
-                    const float x = __uint_as_float(w[i]);
-                    if (x == top || (top != top && x != x)) best = id;
-                } else {
-                    const float2 x = U::pair(w[i]);
-                    if (x.y == top || (top != top && x.y != x.y)) best = id + 1;
-                    if (x.x == top || (top != top && x.x != x.x)) best = id;
-                }
-            }
-            grow(top);
-        }
+        if (!(top <= a.m) && a.m == a.m) best = -2 - j, grow(top);  // it grows, or is NaN now
         const float base = a.m == -INFINITY ? 0.0f : a.m;
         const uint64_t base2 = both(-base, -base), c2 = both(c, c);
         const bool far = !((low - base) * c >= -1000.0f);  // -inf among them, or nearly: e's are bounded, 0 * -inf is NaN
@@ -249,6 +236,26 @@ __global__ void __launch_bounds__(kThreads, 4) k_token_logprobs(const __grid_con
         split(u2, x, y);
         a.u += x + y;
     }
+    if (P.K > 0 && best < -1) {  // the first such logit of that batch
+        const int j = -2 - best;
+        load(j);
+        best = head + j * U::N;  // where all are -inf
+#pragma unroll
+        for (int i = 4 * kBatch - 1; i >= 0; --i) {
+            const uint4 v = next[i / 4];
+            const uint32_t w = i % 4 == 0 ? v.x : i % 4 == 1 ? v.y : i % 4 == 2 ? v.z : v.w;
+            const int id = head + (j + i / 4 * kThreads) * U::N + i % 4 * U::kWord;
+            auto is = [&](float x) { return x == a.m || (a.m != a.m && x != x); };
+            if (j + i / 4 * kThreads >= u1) continue;
+            if (DTYPE == SI_FP32) {
+                if (is(__uint_as_float(w))) best = id;
+            } else {
+                const float2 x = U::pair(w);
+                if (is(x.y)) best = id + 1;
+                if (is(x.x)) best = id;
+            }
+        }
+    }
     const unsigned long long mine = best < 0 ? 0 : order_of(a.m, best);
 
 #pragma unroll
@@ -275,28 +282,46 @@ __global__ void __launch_bounds__(kThreads, 4) k_token_logprobs(const __grid_con
             const unsigned long long least = S.lists[0][P.K - 1];  // 0: fewer threads have any
             if (mine != 0 && mine >= least) S.chosen[atomicAdd(&S.n_chosen, 1)] = tid;
             __syncthreads();
-            unsigned long long list = 0;
+            unsigned long long list = 0, bar = least;
+            // takes what the lanes have that is not below the bar
+            auto insert = [&](unsigned long long v) {
+                for (unsigned who = __ballot_sync(0xFFFFFFFFu, v != 0 && v >= bar); who; who &= who - 1) {
+                    const unsigned long long x = __shfl_sync(0xFFFFFFFFu, v, __ffs(who) - 1);
+                    const int at = __popc(__ballot_sync(0xFFFFFFFFu, list > x));
+                    const unsigned long long before = __shfl_up_sync(0xFFFFFFFFu, list, 1);
+                    list = lane < at ? list : lane == at ? x : before;
+                }
+                const unsigned long long last = __shfl_sync(0xFFFFFFFFu, list, P.K - 1);
+                bar = last > least ? last : least;
+            };
+            const float least_x = least ? logit_of(least) : -INFINITY;
             for (int i = warp; i < S.n_chosen; i += kWarps) {
-                const int t = S.chosen[i];
-                const bool t_head = rank == 0 && t < head, t_tail = rank == 0 && t < tail;
-                const int its = u0 + t < u1 ? (u1 - u0 - t + kThreads - 1) / kThreads : 0;  // units
-                for (int k0 = 0; k0 < its * U::N + 2; k0 += 128) {
-                    unsigned long long v[4];
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        const int k = k0 + r * 32 + lane - 2;  // -2: the logit before the units, -1: the one behind them
-                        int id = -1;
-                        if (k == -2 && t_head) id = t;
-                        if (k == -1 && t_tail) id = head + units * U::N + t;
-                        if (k >= 0 && k < its * U::N) id = head + (u0 + t + k / U::N * kThreads) * U::N + k % U::N;
-                        v[r] = id < 0 ? 0 : order_of(U::logit(row, id), id);
+                const int t = S.chosen[i], its = u0 + t < u1 ? (u1 - u0 - t + kThreads - 1) / kThreads : 0;  // units
+                if (rank == 0 && (t < head || t < tail)) {
+                    const int id = lane == 0 && t < head ? t : lane == 1 && t < tail ? head + units * U::N + t : -1;
+                    insert(id < 0 ? 0 : order_of(U::logit(row, id), id));
+                }
+                for (int k0 = 0; k0 < its; k0 += 32) {
+                    uint4 w = make_uint4(U::kNone, U::kNone, U::kNone, U::kNone);
+                    if (k0 + lane < its) w = __ldg(body + u0 + t + (k0 + lane) * kThreads);
+                    const uint32_t hi = U::larger(U::larger(w.x, w.y), U::larger(w.z, w.w));
+                    float top = __uint_as_float(hi);
+                    if (DTYPE != SI_FP32) {
+                        const float2 h = U::pair(hi);
+                        top = max_nan(h.x, h.y);
                     }
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        if (v[r] < least) v[r] = 0;
-                        if (!__any_sync(0xFFFFFFFFu, v[r] != 0)) continue;
-                        v[r] = sorted(v[r], lane);
-                        list = merged(list, __shfl_xor_sync(0xFFFFFFFFu, v[r], 31), lane);
+                    for (unsigned who = __ballot_sync(0xFFFFFFFFu, k0 + lane < its && !(top < least_x)); who; who &= who - 1) {
+                        const int l = __ffs(who) - 1, e = lane % U::N;
+                        const uint32_t x = __shfl_sync(0xFFFFFFFFu, w.x, l), y = __shfl_sync(0xFFFFFFFFu, w.y, l);
+                        const uint32_t z = __shfl_sync(0xFFFFFFFFu, w.z, l), v = __shfl_sync(0xFFFFFFFFu, w.w, l);
+                        const int at = e / U::kWord;
+                        const uint32_t mine_w = at == 0 ? x : at == 1 ? y : at == 2 ? z : v;
+                        float f = __uint_as_float(mine_w);
+                        if (DTYPE != SI_FP32) {
+                            const float2 p = U::pair(mine_w);
+                            f = e % 2 ? p.y : p.x;
+                        }
+                        insert(lane < U::N ? order_of(f, head + (u0 + t + (k0 + l) * kThreads) * U::N + e) : 0);
                     }
                 }
             }

@@ -228,7 +228,8 @@ __global__ void __launch_bounds__(kThreads, Cfg8<DP, NT>::kCtas)
     src.start(plan, C.B, x0, x1);
     const uint32_t ring = smem_u32(smem);
     int stage_in = 0, held = kNoSlot, seen_b = -1;
-    int pend = -1, pend_k = 0, pend_v = 0;   // the stage that waits for its scales, and this lane's key's
+    // stages that wait for their scales, and this lane's key's: the older one first
+    int pend[2] = {-1, -1}, pend_k[2] = {0, 0}, pend_v[2] = {0, 0};
     auto fetch = [&]() {
         const int i0 = src.at.tile * KEYS;
         if (i0 + KEYS > src.len && seen_b != src.at.b) {  // the tile meets the new nodes
@@ -238,14 +239,14 @@ __global__ void __launch_bounds__(kThreads, Cfg8<DP, NT>::kCtas)
         held = slot_of(src.list, i0 + own0 + lane % WK, src.len, src.tot, src.seen);
     };
     auto issue = [&]() {
-        // The scales of the tile before have had a tile's time to arrive. A key that is not there has 0 (byte -1).
-        if (pend >= 0) {
-            float2* to = reinterpret_cast<float2*>(smem + pend * Cfg::kStage + Cfg::kOffScale);
+        // The scales of the tile before last have had the time to arrive. A key that is not there has 0 (byte -1).
+        if (pend[0] >= 0) {
+            float2* to = reinterpret_cast<float2*>(smem + pend[0] * Cfg::kStage + Cfg::kOffScale);
             if (WK == 32 || lane < WK)
-                to[own0 + lane] = pend_k < 0 ? make_float2(0.0f, 0.0f)
-                                             : make_float2(scale_of(pend_k, C.e_lo, C.e_hi), scale_of(pend_v, C.e_lo, C.e_hi));
-            pend = -1;
+                to[own0 + lane] = pend_k[0] < 0 ? make_float2(0.0f, 0.0f)
+                                                : make_float2(scale_of(pend_k[0], C.e_lo, C.e_hi), scale_of(pend_v[0], C.e_lo, C.e_hi));
         }
+        pend[0] = pend[1], pend_k[0] = pend_k[1], pend_v[0] = pend_v[1], pend[1] = -1;
         if (src.x < x1) {
             int slot[Cp::SWEEPS];
             const uint8_t *kp = src.k + unit * 16, *vp = src.v + unit * 16;
@@ -272,9 +273,9 @@ __global__ void __launch_bounds__(kThreads, Cfg8<DP, NT>::kCtas)
                     cp16(at + Cfg::kTile, on ? vp + from * v_step : src.v, on);
                 }
             }
-            pend_k = -1;
-            if (mine >= 0) pend_k = src.k_scale[mine >> C.block_shift], pend_v = src.v_scale[mine >> C.block_shift];
-            pend = stage_in;
+            pend_k[1] = -1;
+            if (mine >= 0) pend_k[1] = src.k_scale[mine >> C.block_shift], pend_v[1] = src.v_scale[mine >> C.block_shift];
+            pend[1] = stage_in;
             if (++stage_in == S) stage_in = 0;
             if (src.next(plan, C.B, groups) && src.x < x1) src.enter(C, plan, row_blocks);
             if (src.x < x1) fetch();
@@ -382,13 +383,15 @@ __global__ void __launch_bounds__(kThreads, Cfg8<DP, NT>::kCtas)
                 }
                 odd = __reduce_or_sync(0xFFFFFFFFu, odd);
             }
-            __syncwarp();
+            __syncwarp();  // the tile before has been read by every lane
             issue();
+            __syncwarp();
             const uint32_t k_s = smem_u32(stage), v_s = k_s + Cfg::kTile;
             const float2* sc_s = reinterpret_cast<const float2*>(stage + Cfg::kOffScale) + own0;
             // rows of an ldmatrix: keys 0-7, 8-15 of a unit, then of the next unit
             const int ld_key = own0 + (lane & 15), ld_unit = lane >> 4;
-            float s[MT][NT][4];
+            constexpr int CHAINS = MT * NT <= 2 ? 2 : 1;  // of products, for each sixteen keys and eight rows
+            float s[MT][NT][4], s_odd[CHAINS == 2 ? MT : 1][CHAINS == 2 ? NT : 1][4] = {};
             float2 sc[MT][2];
 #pragma unroll
             for (int m = 0; m < MT; ++m) {
@@ -410,7 +413,7 @@ __global__ void __launch_bounds__(kThreads, Cfg8<DP, NT>::kCtas)
 #pragma unroll
                         for (int n = 0; n < NT; ++n) {
                             const uint2 q = Cfg::kQInRegs ? qf[Cfg::kQInRegs ? n : 0][Cfg::kQInRegs ? u + i : 0] : query(n, u + i);
-                            mma16(s[m][n], a0, a1, a2, a3, q.x, q.y);
+                            mma16(CHAINS == 2 && i == 1 ? s_odd[CHAINS == 2 ? m : 0][CHAINS == 2 ? n : 0] : s[m][n], a0, a1, a2, a3, q.x, q.y);
                         }
                     }
                 }
@@ -425,7 +428,10 @@ __global__ void __launch_bounds__(kThreads, Cfg8<DP, NT>::kCtas)
 #pragma unroll
                 for (int m = 0; m < MT; ++m)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) s[m][n][e] = s[m][n][e] * qdown[n][e & 1] * sc[m][e >> 1].x;
+                    for (int e = 0; e < 4; ++e) {
+                        if (CHAINS == 2) s[m][n][e] += s_odd[CHAINS == 2 ? m : 0][CHAINS == 2 ? n : 0][e];
+                        s[m][n][e] = s[m][n][e] * qdown[n][e & 1] * sc[m][e >> 1].x;
+                    }
                 if (edge) {
 #pragma unroll
                     for (int m = 0; m < MT; ++m)

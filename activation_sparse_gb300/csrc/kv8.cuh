@@ -40,8 +40,10 @@ __device__ __forceinline__ uint32_t halves(uint16_t codes) {
 
 // The four codes of a word that lie at bytes 0, 1 and 2, 3.
 __device__ __forceinline__ void halves4(uint32_t w, uint32_t& lo, uint32_t& hi) {
-    lo = halves((uint16_t)w);
-    hi = halves((uint16_t)(w >> 16));
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(w));
 }
 
 // 1 / x of a power of two within the scales' limits.

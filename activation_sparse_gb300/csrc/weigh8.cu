@@ -1,4 +1,6 @@
 // weigh8.cu -- the attention weight that each key of a cache of e4m3 codes received.
+#include <type_traits>
+
 #include "attend.cuh"
 #include "kv8.cuh"
 
@@ -6,16 +8,18 @@ namespace si {
 
 namespace {
 
-constexpr int kThreads = 128;  // four warps of sixteen keys of a tile
-constexpr int kKeys = 16;
+constexpr int kThreads = 128;  // four warps
 constexpr int kRows = 64;      // kept in shared memory at once
 
 template <int DP>
 struct Cfg8 {
-    static constexpr int kTile = KT * DP;
+    static constexpr int kMT = DP <= 128 ? 2 : 1;             // sixteens of keys a warp has of a tile
+    static constexpr int kWarpKeys = 16 * kMT;
+    static constexpr int kKeys = 4 * kWarpKeys;               // of a tile
+    static constexpr int kTile = kKeys * DP;
     static constexpr int kOffKey = kTile;                     // in a stage: slots, old weights, scales of its keys
-    static constexpr int kStage = kTile + KT * 12;
-    static constexpr int kStages = 4;
+    static constexpr int kStage = kTile + kKeys * 12;
+    static constexpr int kStages = 2;
     static constexpr int kCtas = DP <= 128 ? 4 : 2;           // an SM
     static constexpr int kQRow = DP * 2 + 32;
     static constexpr int kOffQ = kStages * kStage;
@@ -32,8 +36,8 @@ struct Cfg8 {
 template <int DP>
 __global__ void __launch_bounds__(kThreads, Cfg8<DP>::kCtas) k_kv_accumulate8(const __grid_constant__ AttendParams P) {
     using Cfg = Cfg8<DP>;
-    using Cp = Copy8<DP>;
-    constexpr int KD = DP / 16, UNITS = Cp::UNITS, S = Cfg::kStages;
+    using Cp = Copy8<DP, Cfg::kWarpKeys>;
+    constexpr int KD = DP / 16, UNITS = Cp::UNITS, S = Cfg::kStages, MT = Cfg::kMT, WK = Cfg::kWarpKeys, KEYS = Cfg::kKeys;
     extern __shared__ __align__(128) uint8_t smem[];
     uint8_t* const q_s = smem + Cfg::kOffQ;
     unsigned long long* const word_s = reinterpret_cast<unsigned long long*>(smem + Cfg::kOffRow);
@@ -44,50 +48,45 @@ __global__ void __launch_bounds__(kThreads, Cfg8<DP>::kCtas) k_kv_accumulate8(co
 
     const KvView& C = P.c;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int g = lane >> 2, c = lane & 3;  // keys g, g + 8; rows 2c, 2c + 1 of each eight
+    const int g = lane >> 2, c = lane & 3;  // keys g, g + 8 of sixteen; rows 2c, 2c + 1 of each eight
     const int T = P.T, G = P.G, D = C.D;
 
     grid_launch_dependents();
     grid_dependency_wait();
-    make_plan<kThreads, 1, 0>(C, T, C.Hkv, gridDim.x, plan, P.err, blockIdx.x == 0);
-    const Deal deal(plan, C.B, gridDim.x, 1);
+    make_plan<kThreads, 1, 0, KEYS>(C, T, C.Hkv, gridDim.x, plan, P.err, blockIdx.x == 0);
+    const DealOf<KEYS> deal(plan, C.B, gridDim.x, 1);
     int x0, x1;
     deal.range(blockIdx.x, x0, x1);
     if (x0 >= x1) return;
-    const int unit = lane % UNITS, own0 = warp * kKeys;
+    const int unit = lane % UNITS, own0 = warp * WK;
     const bool unit_on = unit * 16 < D, whole_rows = D == DP;
     const int n_slots = (int)C.n_slots, k_step = (int)C.ks;
 
-    SourceOf<uint8_t> src;
+    SourceOf<uint8_t, KEYS> src;
     src.start(plan, C.B, x0, x1);
     const uint32_t ring = smem_u32(smem);
-    int stage_in = 0, held = kNoSlot;  // lanes i and i + 16: the slot of the warp's key i of the tile to be issued next
-    int pend = -1, pend_byte = 0;      // the stage that waits for its scales, and this lane's
+    int stage_in = 0, held = kNoSlot;  // lane i: the slot of the warp's key i (of sixteen: i % 16) of the tile to be issued next
+    int pend[S - 1], pend_byte[S - 1];  // stages that wait for their scales, and this lane's: the oldest first
+#pragma unroll
+    for (int i = 0; i < S - 1; ++i) pend[i] = -1, pend_byte[i] = 0;
     auto fetch = [&]() {
-        held = slot_of(src.list, src.at.tile * KT + own0 + (lane & 15), src.tot, src.tot, 0);
+        held = slot_of(src.list, src.at.tile * KEYS + own0 + lane % WK, src.tot, src.tot, 0);
     };
     auto issue = [&]() {
-        if (pend >= 0) {  // the scales of the tile before have had a tile's time to arrive
-            if (lane < 16)
-                reinterpret_cast<float*>(smem + pend * Cfg::kStage + Cfg::kOffKey + KT * 8)[own0 + lane] =
-                    scale_of(pend_byte, C.e_lo, C.e_hi);
-            pend = -1;
-        }
+        // The scales of the tile that is read next, which have had the time of S - 1 tiles to arrive.
+        if (pend[0] >= 0 && (WK == 32 || lane < WK))
+            reinterpret_cast<float*>(smem + pend[0] * Cfg::kStage + Cfg::kOffKey + KEYS * 8)[own0 + lane] =
+                scale_of(pend_byte[0], C.e_lo, C.e_hi);
+#pragma unroll
+        for (int i = 0; i + 1 < S - 1; ++i) pend[i] = pend[i + 1], pend_byte[i] = pend_byte[i + 1];
+        pend[S - 2] = -1;
         if (src.x < x1) {
             const uint8_t* kp = src.k + unit * 16;
             const uint32_t dst = ring + stage_in * Cfg::kStage;
             const bool ok = slot_ok(held, n_slots, P.err);
-            if (lane < 16) {
-                int* at = reinterpret_cast<int*>(smem + stage_in * Cfg::kStage + Cfg::kOffKey) + own0 + lane;
-                *at = ok ? held : -1;
-                asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(at + KT)),
-                             "l"(src.acc + (ok ? held : 0)), "r"(ok ? 4 : 0)
-                             : "memory");
-                pend_byte = src.k_scale[(ok ? held : 0) >> C.block_shift];
-            }
-            pend = stage_in;
+            const int mine = ok ? held : 0;  // keys past the end are read from slot 0 and not counted
             int slot[Cp::SWEEPS];
-            Cp::slots(ok ? held : 0, lane, slot);  // keys past the end are read from slot 0 and not counted
+            Cp::slots(mine, lane, slot);
             if (whole_rows) {
 #pragma unroll
                 for (int j = 0; j < Cp::SWEEPS; ++j)
@@ -98,26 +97,42 @@ __global__ void __launch_bounds__(kThreads, Cfg8<DP>::kCtas) k_kv_accumulate8(co
                     cp16(dst + tile8_at<DP>(own0 + Cp::row(lane, j), unit),
                          unit_on ? kp + (long long)slot[j] * k_step : src.k, unit_on);
             }
+            if (WK == 32 || lane < WK) {
+                int* at = reinterpret_cast<int*>(smem + stage_in * Cfg::kStage + Cfg::kOffKey) + own0 + lane;
+                *at = ok ? held : -1;
+                asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(at + KEYS)),
+                             "l"(src.acc + mine), "r"(ok ? 4 : 0)
+                             : "memory");
+                pend_byte[S - 2] = src.k_scale[mine >> C.block_shift];
+            }
+            pend[S - 2] = stage_in;
             if (++stage_in == S) stage_in = 0;
             if (src.next(plan, C.B, C.Hkv) && src.x < x1) src.enter(C, plan, 1);
             if (src.x < x1) fetch();
         }
         cp_commit();
     };
+    // The first slots, and the second tile's where they are of the same list, go out together.
+    At a = locate<KEYS>(plan, C.B, x0);
     src.enter(C, plan, 1);
     fetch();
+    const int first_slot = held;
+    const bool two = x0 + 1 < x1 && a.tile + 1 < a.ntile;
+    if (two) {
+        ++src.at.tile;
+        fetch();
+        --src.at.tile;
+    }
+    const int second_slot = held;
+    held = first_slot;
+    issue();
+    if (two) held = second_slot;
 #pragma unroll 1
-    for (int s = 0; s < S - 1; ++s) issue();
+    for (int s = 1; s < S - 1; ++s) issue();
 
-    At a = locate(plan, C.B, x0);
     int have_b = -1, have_h = -1, have_block = -1, n_rows = 0, stage_out = 0;
-    for (int x = x0; x < x1; ++x, step(plan, C.B, C.Hkv, a)) {
-        cp_wait<S - 2>();
-        __syncwarp();
-        issue();
+    for (int x = x0; x < x1; ++x, step<KEYS>(plan, C.B, C.Hkv, a)) {
         const int b = a.b, h = a.group, len = plan.len[b], tot = plan.tot[b];  // tot = 0: nothing counts
-        uint8_t* const stage = smem + stage_out * Cfg::kStage;
-        if (++stage_out == S) stage_out = 0;
         if (have_b != b) {
             // counted nodes of this sequence
             __syncthreads();
@@ -138,85 +153,129 @@ __global__ void __launch_bounds__(kThreads, Cfg8<DP>::kCtas) k_kv_accumulate8(co
             have_b = b;
             have_h = -1;
         }
+        // queries r0 .. r0 + nr - 1 of those that count
+        auto stage_rows = [&](int r0, int nr) {
+            if (have_h == h && have_block == r0) return;
+            __syncthreads();
+            const int padded = (nr + 15) & ~15;
+            constexpr int AT_ONCE = 32 / (DP / 8);
+            for (int base = warp * AT_ONCE; base < padded; base += 4 * AT_ONCE) {
+                const int r = base + lane / (DP / 8), u = lane % (DP / 8);
+                const bool on = r < nr;
+                const int t = on ? node_s[(r0 + r) / G] : 0, gq = (r0 + r) % G;
+                const uint16_t* from = static_cast<const uint16_t*>(P.q) + b * P.qb + t * P.qt + (long long)(h * G + gq) * P.qh;
+                float down;
+                const uint4 val = query_unit<DP>(on ? from : nullptr, D, C.fp16, lane, down);
+                if (r < padded) {
+                    *reinterpret_cast<uint4*>(q_s + r * Cfg::kQRow + u * 16) = val;
+                    if (u == 0) {
+                        float lse = INFINITY;  // a padding row: exp(-inf) = 0
+                        if (on) lse = P.lse[((long long)b * T + t) * P.Hq + h * G + gq];
+                        // a row that saw nothing gives nothing
+                        lse_s[r] = lse == -INFINITY ? INFINITY : lse;
+                        word_s[r] = on ? word_of(P.mask, T, b, t) : 0;
+                        factor_s[r] = down;
+                    }
+                }
+            }
+            have_h = h;
+            have_block = r0;
+            __syncthreads();
+        };
+        if (n_rows > 0) stage_rows(0, min(kRows, n_rows));
+        cp_wait<S - 2>();
+        __syncwarp();  // the tile before has been read by every lane
+        issue();
+        __syncwarp();
+        uint8_t* const stage = smem + stage_out * Cfg::kStage;
+        if (++stage_out == S) stage_out = 0;
         const uint32_t k_s = smem_u32(stage);
-        uint32_t kf[KD][4];
+        uint32_t kf[MT][KD][4];
         const float* key_s = reinterpret_cast<const float*>(stage + Cfg::kOffKey);  // slots, old weights, scales
-        const float sk0 = key_s[2 * KT + own0 + g], sk1 = key_s[2 * KT + own0 + g + 8];
+        float sk[MT][2], w[MT][2];  // of keys g and g + 8
 #pragma unroll
-        for (int u = 0; u < KD; u += 2) {
-            uint32_t r[4];
-            ldsm4(r, k_s + tile8_at<DP>(own0 + (lane & 15), u + (lane >> 4)));
+        for (int m = 0; m < MT; ++m) {
+            sk[m][0] = key_s[2 * KEYS + own0 + m * 16 + g], sk[m][1] = key_s[2 * KEYS + own0 + m * 16 + g + 8];
+            w[m][0] = w[m][1] = 0.0f;
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                halves4(r[2 * i], kf[u + i][0], kf[u + i][2]);
-                halves4(r[2 * i + 1], kf[u + i][1], kf[u + i][3]);
+            for (int u = 0; u < KD; u += 2) {
+                uint32_t r[4];
+                ldsm4(r, k_s + tile8_at<DP>(own0 + m * 16 + (lane & 15), u + (lane >> 4)));
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    halves4(r[2 * i], kf[m][u + i][0], kf[m][u + i][2]);
+                    halves4(r[2 * i + 1], kf[m][u + i][1], kf[m][u + i][3]);
+                }
             }
         }
-        float w[2] = {0.0f, 0.0f};  // keys g and g + 8
-        const int i0 = a.tile * KT + own0;
-        const bool edge = i0 + kKeys > len;
+        const int i0 = a.tile * KEYS + own0;
+        const bool edge = i0 + WK > len;
         for (int r0 = 0; r0 < n_rows; r0 += kRows) {
             const int nr = min(kRows, n_rows - r0);
-            if (have_h != h || have_block != r0) {
-                __syncthreads();
-                const int padded = (nr + 7) & ~7;
-                constexpr int AT_ONCE = 32 / (DP / 8);
-                for (int base = warp * AT_ONCE; base < padded; base += 4 * AT_ONCE) {
-                    const int r = base + lane / (DP / 8), u = lane % (DP / 8);
-                    const bool on = r < nr;
-                    const int t = on ? node_s[(r0 + r) / G] : 0, gq = (r0 + r) % G;
-                    const uint16_t* from = static_cast<const uint16_t*>(P.q) + b * P.qb + t * P.qt + (long long)(h * G + gq) * P.qh;
-                    float down;
-                    const uint4 val = query_unit<DP>(on ? from : nullptr, D, C.fp16, lane, down);
-                    if (r < padded) {
-                        *reinterpret_cast<uint4*>(q_s + r * Cfg::kQRow + u * 16) = val;
-                        if (u == 0) {
-                            float lse = INFINITY;  // a padding row: exp(-inf) = 0
-                            if (on) lse = P.lse[((long long)b * T + t) * P.Hq + h * G + gq];
-                            // a row that saw nothing gives nothing
-                            lse_s[r] = lse == -INFINITY ? INFINITY : lse;
-                            word_s[r] = on ? word_of(P.mask, T, b, t) : 0;
-                            factor_s[r] = down;
-                        }
-                    }
-                }
-                have_h = h;
-                have_block = r0;
-                __syncthreads();
-            }
-            for (int n = 0; n < nr; n += 8) {
-                float s[4] = {};
+            if (n_rows > kRows) stage_rows(r0, nr);
+            // 16 rows at a time, or the last 8: several chains of products
+            auto rows = [&](int n, auto tiles) {
+                constexpr int NT = decltype(tiles)::value, CHAINS = NT == 1 ? 2 : 1;
+                float s[CHAINS][MT][NT][4] = {};
                 const uint8_t* q_at = q_s + (n + g) * Cfg::kQRow + c * 8;
 #pragma unroll
-                for (int u = 0; u < KD; ++u) {
-                    const uint2 q = *reinterpret_cast<const uint2*>(q_at + u * 32);
-                    mma16(s, kf[u][0], kf[u][1], kf[u][2], kf[u][3], q.x, q.y);
-                }
-                const int r = n + c * 2;
-                const float2 lse = *reinterpret_cast<const float2*>(lse_s + r), down = *reinterpret_cast<const float2*>(factor_s + r);
-                // The difference is taken before the base's factor, and of the rounded product, as lse was: scores of
-                // the type's lowest value then differ from lse by 0.
+                for (int u = 0; u < KD; ++u)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float z = s[e] * (e & 1 ? down.y : down.x) * (e < 2 ? sk0 : sk1);
-                    float p = ex2(__fadd_rn(__fmul_rn(z, P.scale), e & 1 ? -lse.y : -lse.x) * kLog2e);
-                    // a padding row's zeros meet what a key holds, and 0 * NaN is NaN
-                    if (n + 8 > nr && r + (e & 1) >= nr) p = 0.0f;
-                    if (edge) {
-                        const int j = i0 + g + (e >> 1) * 8 - len;
-                        if (!(j < 0 || (j < T && (word_s[r + (e & 1)] >> (j & 63) & 1)))) p = 0.0f;
+                    for (int t = 0; t < NT; ++t) {
+                        const uint2 q = *reinterpret_cast<const uint2*>(q_at + t * 8 * Cfg::kQRow + u * 32);
+#pragma unroll
+                        for (int m = 0; m < MT; ++m)
+                            mma16(s[u % CHAINS][m][t], kf[m][u][0], kf[m][u][1], kf[m][u][2], kf[m][u][3], q.x, q.y);
                     }
-                    w[e >> 1] += p;
+#pragma unroll
+                for (int t = 0; t < NT; ++t) {
+                    const int r = n + t * 8 + c * 2;
+                    const float2 lse = *reinterpret_cast<const float2*>(lse_s + r), down = *reinterpret_cast<const float2*>(factor_s + r);
+                    // The difference is taken before the base's factor, and of the rounded product, as lse was: scores of
+                    // the type's lowest value then differ from lse by 0.
+#pragma unroll
+                    for (int m = 0; m < MT; ++m) {
+                        float p[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const float sum = CHAINS == 2 ? s[0][m][t][e] + s[CHAINS - 1][m][t][e] : s[0][m][t][e];
+                            const float z = sum * (e & 1 ? down.y : down.x) * sk[m][e >> 1];
+                            p[e] = ex2(__fadd_rn(__fmul_rn(z, P.scale), e & 1 ? -lse.y : -lse.x) * kLog2e);
+                        }
+                        if (n + NT * 8 > nr) {  // a padding row's zeros meet what a key holds, and 0 * NaN is NaN
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                if (r + (e & 1) >= nr) p[e] = 0.0f;
+                        }
+                        if (edge) {
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const int j = i0 + m * 16 + g + (e >> 1) * 8 - len;
+                                if (!(j < 0 || (j < T && (word_s[r + (e & 1)] >> (j & 63) & 1)))) p[e] = 0.0f;
+                            }
+                        }
+                        w[m][0] += p[0] + p[1], w[m][1] += p[2] + p[3];
+                    }
                 }
-            }
+            };
+            int n = 0;
+            for (; n + 8 < nr; n += 16) rows(n, std::integral_constant<int, 2>());
+            if (n < nr) rows(n, std::integral_constant<int, 1>());
         }
         float* out = P.acc_out + b * C.ab + h * C.ah;
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            w[e] += __shfl_xor_sync(0xFFFFFFFFu, w[e], 1);
-            w[e] += __shfl_xor_sync(0xFFFFFFFFu, w[e], 2);
-            const int key = own0 + g + e * 8, slot = reinterpret_cast<const int*>(key_s)[key];
-            if (c == 0 && slot >= 0) out[slot] = key_s[KT + key] + w[e];
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                w[m][e] += __shfl_xor_sync(0xFFFFFFFFu, w[m][e], 1);
+                w[m][e] += __shfl_xor_sync(0xFFFFFFFFu, w[m][e], 2);
+            }
+        // the four lanes that have a key's sum share the keys out
+        if (c < 2 * MT) {
+            const float sum = MT == 1 ? (c & 1 ? w[0][1] : w[0][0])
+                                      : c & 2 ? (c & 1 ? w[MT - 1][1] : w[MT - 1][0]) : (c & 1 ? w[0][1] : w[0][0]);
+            const int key = own0 + (c >> 1) * 16 + (c & 1) * 8 + g, slot = reinterpret_cast<const int*>(key_s)[key];
+            if (slot >= 0) out[slot] = key_s[KEYS + key] + sum;
         }
     }
     cp_wait<0>();

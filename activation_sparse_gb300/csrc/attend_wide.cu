@@ -39,6 +39,8 @@
 // Every write to shared memory is an ordinary one; the issuing warp's proxy
 // fence, after the barrier that announces it, lets the tensor cores see it. All
 // waits are bounded; TMEM is always released.
+#include <type_traits>
+
 #include "attend.cuh"
 #include "kv8.cuh"
 
@@ -47,7 +49,6 @@ namespace si {
 namespace {
 
 constexpr int kBlock = 128;        // query rows of one product: a TMEM lane each
-constexpr int kCopyWarps = 4, kCopyThreads = 32 * kCopyWarps;
 
 // NB row blocks a CTA meet every key tile it copies. E4M3: a cache of codes, which are copied as they are (a key or a
 // value tile each of kRaw places) and then become a ring slot's elements.
@@ -55,6 +56,7 @@ template <int DP, int NB, bool E4M3>
 struct WideCfg {
     static constexpr int kRows = kBlock * NB;
     static constexpr int kSoftmaxWarps = 4 * NB;
+    static constexpr int kCopyWarps = E4M3 && NB == 2 ? 8 : 4, kCopyThreads = 32 * kCopyWarps;
     static constexpr int kMmaWarp = kSoftmaxWarps, kCopyWarp = kMmaWarp + 1;
     static constexpr int kThreads = 32 * (kCopyWarp + kCopyWarps);
     static constexpr int kCtas = NB == 1 ? 2 : 1;              // an SM
@@ -183,11 +185,22 @@ __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.
 
 }  // namespace
 
-// Sixteen codes times their scale as sixteen elements of the type, exactly.
-template <bool FP16>
+// a * b in fp32 of two fp16
+__device__ __forceinline__ float product(uint32_t a, uint32_t b, bool high) {
+    float d;
+    if (high) asm("{\n\t.reg .b16 x, y, s, t;\n\tmov.b32 {x, y}, %1;\n\tmov.b32 {s, t}, %2;\n\tfma.rn.f32.f16 %0, y, s, 0f00000000;\n\t}" : "=f"(d) : "r"(a), "r"(b));
+    else asm("{\n\t.reg .b16 x, y, s, t;\n\tmov.b32 {x, y}, %1;\n\tmov.b32 {s, t}, %2;\n\tfma.rn.f32.f16 %0, x, s, 0f00000000;\n\t}" : "=f"(d) : "r"(a), "r"(b));
+    return d;
+}
+
+// Sixteen codes times their scale as sixteen elements of the type, exactly. IN_HALF: the scale is an fp16 number (all of
+// an fp16 cache's are), which the product takes as it is.
+template <bool FP16, bool IN_HALF>
 __device__ __forceinline__ void elements16(uint4 codes, float scale, uint4& lo, uint4& hi) {
     const uint32_t w[4] = {codes.x, codes.y, codes.z, codes.w};
     uint32_t e[8];
+    const __half2 scale2 = __float2half2_rn(scale);
+    const uint32_t scale_w = *reinterpret_cast<const uint32_t*>(&scale2);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         uint32_t h[2];
@@ -196,8 +209,10 @@ __device__ __forceinline__ void elements16(uint4 codes, float scale, uint4& lo, 
         for (int j = 0; j < 2; ++j) {
             const __half2 x = *reinterpret_cast<const __half2*>(&h[j]);
             if (FP16) {
-                const __half2 y = __hmul2(x, __float2half2_rn(scale));
+                const __half2 y = __hmul2(x, scale2);
                 e[2 * i + j] = *reinterpret_cast<const uint32_t*>(&y);
+            } else if (IN_HALF) {
+                e[2 * i + j] = pack<false>(product(h[j], scale_w, false), product(h[j], scale_w, true));
             } else {
                 const float2 f = __half22float2(x);
                 e[2 * i + j] = pack<false>(f.x * scale, f.y * scale);
@@ -207,25 +222,26 @@ __device__ __forceinline__ void elements16(uint4 codes, float scale, uint4& lo, 
     lo = make_uint4(e[0], e[1], e[2], e[3]), hi = make_uint4(e[4], e[5], e[6], e[7]);
 }
 
-// The copying warps over a cache of codes: every lane copies 16 bytes of DP / 32 of its warp's sixteen keys, several tiles
-// ahead, and turns what it copied itself into elements.
+// The copying warps over a cache of codes: every lane copies 16 bytes of some of its warp's keys, several tiles ahead, and
+// turns what it copied itself into elements.
 template <int DP, int NB, bool FP16>
 __device__ __forceinline__ void copy_codes(const AttendParams& P, const Plan& plan, int row_blocks, int x0, int x1, int slots,
                                            uint8_t* ring, uint64_t* full, uint64_t* empty, uint16_t* odd) {
     using Cfg = WideCfg<DP, NB, true>;
-    using Cp = Copy8<DP>;
     constexpr int RAW = Cfg::kRaw;
+    constexpr int WK = KT / Cfg::kCopyWarps;  // keys a warp has of a tile
+    using Cp = Copy8<DP, WK>;
     const KvView& C = P.c;
     const int T = P.T, D = C.D, groups = C.Hkv * row_blocks;
     const int warp = (threadIdx.x >> 5) - Cfg::kCopyWarp, lane = threadIdx.x & 31, unit = lane % Cp::UNITS;
-    const int own0 = warp * 16;
-    const bool unit_on = unit * 16 < D;
+    const int own0 = warp * WK, of_v = lane / WK & 1;  // lane i % WK has key i: its key's scale or, of the next WK lanes, its value's
+    const bool unit_on = unit * 16 < D, whole_rows = D == DP;
     const int n_slots = (int)C.n_slots, k_step = (int)C.ks, v_step = (int)C.vs;
     uint8_t* const sub_tile = ring + (unit >> 2) * (KT * 128);  // 64 elements are four units of codes
     uint8_t* const raw = ring + slots * Cfg::kTile + (warp * 32 + lane) * 16;  // [place][row of the lane][thread]
     float* const scale_s = reinterpret_cast<float*>(ring + slots * Cfg::kTile + RAW * (Cfg::kTile / 2)) + warp * Cfg::kScaleTiles * 32;
     const uint32_t raw_addr = smem_u32(raw);
-    constexpr int kPlace = Cfg::kTile / 2, kRow = kCopyThreads * 16;
+    constexpr int kPlace = Cfg::kTile / 2, kRow = Cfg::kCopyThreads * 16;
     SourceOf<uint8_t> src;
     src.start(plan, C.B, x0, x1);
     int held = kNoSlot, seen_b = -1;
@@ -235,17 +251,24 @@ __device__ __forceinline__ void copy_codes(const AttendParams& P, const Plan& pl
             src.seen = seen_nodes(P.mask, T, src.at.b, lane);
             seen_b = src.at.b;
         }
-        held = slot_of(src.list, i0 + own0 + (lane & 15), src.len, src.tot, src.seen);
+        held = slot_of(src.list, i0 + own0 + lane % WK, src.len, src.tot, src.seen);
     };
     int slot[Cp::SWEEPS];
-    int in = 0, in_tile = 0, byte = 0;  // place of the next copies; lanes below 16 have their key's scale, the others its value's
+    int in = 0, in_tile = 0, byte = 0;  // place of the next copies; a scale on its way
+    bool all = false;                   // whether they leave nothing out
     const uint8_t* v_from = nullptr;
     bool on = false;                    // whether the values of the tile whose keys went last are still to come
     auto copy = [&](const uint8_t* from, int step_) {
+        if (all) {
+            from += unit * 16;
 #pragma unroll
-        for (int j = 0; j < Cp::SWEEPS; ++j) {
-            const bool there = slot[j] >= 0 && unit_on;
-            cp16(raw_addr + in * kPlace + j * kRow, there ? from + (long long)slot[j] * step_ + unit * 16 : from, there);
+            for (int j = 0; j < Cp::SWEEPS; ++j) cp16(raw_addr + in * kPlace + j * kRow, from + (long long)slot[j] * step_);
+        } else {
+#pragma unroll
+            for (int j = 0; j < Cp::SWEEPS; ++j) {
+                const bool there = slot[j] >= 0 && unit_on;
+                cp16(raw_addr + in * kPlace + j * kRow, there ? from + (long long)slot[j] * step_ + unit * 16 : from, there);
+            }
         }
         if (++in == RAW) in = 0;
     };
@@ -258,10 +281,12 @@ __device__ __forceinline__ void copy_codes(const AttendParams& P, const Plan& pl
             on = false;
         } else if (src.x < x1) {
             const bool ok = slot_ok(held, n_slots, P.err);
-            const int mine = ok ? held : src.at.tile * KT + KT <= src.len ? 0 : -1;  // a bad slot has been reported; slot 0 is read
+            const bool cached = src.at.tile * KT + KT <= src.len;
+            const int mine = ok ? held : cached ? 0 : -1;  // a bad slot has been reported; slot 0 is read
+            all = cached && whole_rows;
             Cp::slots(mine, lane, slot);
             byte = 127;
-            if (mine >= 0) byte = (lane < 16 ? src.k_scale : src.v_scale)[mine >> C.block_shift];
+            if (mine >= 0) byte = (of_v ? src.v_scale : src.k_scale)[mine >> C.block_shift];
             copy(src.k, k_step);
             v_from = src.v;
             on = true;
@@ -286,16 +311,25 @@ __device__ __forceinline__ void copy_codes(const AttendParams& P, const Plan& pl
         if (++out == RAW) out = 0;
         issue();
     };
-    auto store = [&](int slot_at, const uint4 (&from)[Cp::SWEEPS], float scale, int first_lane) {
+    auto store_as = [&](int slot_at, const uint4 (&from)[Cp::SWEEPS], float scale, int first_lane, auto in_half) {
         uint8_t* tile = sub_tile + slot_at * Cfg::kTile;
 #pragma unroll
         for (int j = 0; j < Cp::SWEEPS; ++j) {
             const int r = Cp::row(lane, j);
             uint4 lo, hi;
-            elements16<FP16>(from[j], __shfl_sync(0xFFFFFFFFu, scale, first_lane + r), lo, hi);
+            elements16<FP16, in_half.value>(from[j], __shfl_sync(0xFFFFFFFFu, scale, first_lane + r), lo, hi);
             *reinterpret_cast<uint4*>(tile + sw128(own0 + r, 2 * (unit & 3))) = lo;
             *reinterpret_cast<uint4*>(tile + sw128(own0 + r, 2 * (unit & 3) + 1)) = hi;
         }
+    };
+    // The elements of a key or value tile, and the word that they are there: one arrival a warp.
+    auto store = [&](int slot_at, const uint4 (&from)[Cp::SWEEPS], float scale, int first_lane) {
+        // 2^-14 .. 2^15, 0 or NaN; a cache of bf16 with other scales among the warp's takes the longer way
+        const bool in_half = FP16 || __all_sync(0xFFFFFFFFu, !(scale > 32768.0f) && !(scale < 6.103515625e-5f && scale > 0.0f));
+        if (in_half) store_as(slot_at, from, scale, first_lane, std::true_type());
+        else store_as(slot_at, from, scale, first_lane, std::false_type());
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&full[slot_at]);
     };
     src.enter(C, plan, row_blocks);
     fetch();
@@ -312,14 +346,13 @@ __device__ __forceinline__ void copy_codes(const AttendParams& P, const Plan& pl
         if (++out_tile == Cfg::kScaleTiles) out_tile = 0;
         const int k_at = take();
         store(k_at, codes, scale, 0);
-        mbar_arrive(&full[k_at]);
         load(codes);
         unsigned bad = 0;
         if (!cached) {
             // New nodes' value rows that are NaN leave the tile (0 * NaN is NaN) and are reported, so that the rows that
             // see them get them back at the end.
-            const int node = i0 + own0 + (lane & 15) - len;
-            if (lane >= 16 && node >= 0 && node < T && scale != scale) bad |= 1u << (lane & 15), scale = 0.0f;
+            const int node = i0 + own0 + lane % WK - len;
+            if (of_v && node >= 0 && node < T && scale != scale) bad |= 1u << lane % WK, scale = 0.0f;
 #pragma unroll
             for (int j = 0; j < Cp::SWEEPS; ++j) {
                 const int r = Cp::row(lane, j), of = i0 + own0 + r - len;
@@ -334,9 +367,11 @@ __device__ __forceinline__ void copy_codes(const AttendParams& P, const Plan& pl
             bad = __reduce_or_sync(0xFFFFFFFFu, bad);
         }
         const int v_at = take();
-        store(v_at, codes, scale, 16);
-        if (!cached && lane == 0) odd[v_at * 4 + own0 / 16] = (uint16_t)bad;
-        mbar_arrive(&full[v_at]);
+        if (!cached && lane == 0) {  // the keys' bits of the tile's word
+            if (WK == 16) odd[v_at * 4 + own0 / 16] = (uint16_t)bad;
+            else reinterpret_cast<uint8_t*>(odd)[v_at * 8 + own0 / 8] = (uint8_t)bad;
+        }
+        store(v_at, codes, scale, WK);
     }
     cp_wait<0>();
 }
@@ -376,7 +411,7 @@ __global__ void __launch_bounds__(WideCfg<DP, NB, E4M3>::kThreads, WideCfg<DP, N
     }
     if (tid == 0) {
         for (int s = 0; s < kMaxSlots; ++s) {
-            mbar_init(&full[s], kCopyThreads);
+            mbar_init(&full[s], E4M3 ? Cfg::kCopyWarps : Cfg::kCopyThreads);
             mbar_init(&empty[s], 1);
         }
         for (int k = 0; k < NB; ++k) {

@@ -170,7 +170,8 @@ __device__ __forceinline__ int tiles_of(int tot) {
 // finishes two lists, and every piece of a list costs it about PIECE tiles'
 // time (queries in, partial rows out). So lists are cut by themselves where
 // the longest part and one piece take less than an even share and two. A part
-// has at least LEAST tiles.
+// has at least LEAST tiles. (Where every tile can have a CTA of its own, both ways
+// are the same and the shorter one is taken: 1000 keys of codes 9.7 -> 8.9 us.)
 template <int THREADS, int LEAST, int PIECE, int K = KT>
 __device__ void make_plan(const KvView& C, int T, int groups, int ctas, const Plan& p, unsigned* err, bool report) {
     if (C.B == 1) {
@@ -182,7 +183,7 @@ __device__ void make_plan(const KvView& C, int T, int groups, int ctas, const Pl
             if (!ok && report) atomicOr(err, SI_DEVERR_CACHE);
             const int tot = ok ? len + T : 0, n = tiles_of<K>(tot), total = n * groups;
             int q = 0;
-            if (PIECE > 0 && groups <= ctas) {
+            if (PIECE > 0 && groups <= ctas && (LEAST > 1 || total > ctas)) {
                 const int even = max(LEAST, div_of(total + ctas - 1, ctas)), m = div_of(ctas, groups);
                 q = max(even, div_of(n + m - 1, m));
                 if (q > even + PIECE) q = 0;
@@ -228,7 +229,7 @@ __device__ void make_plan(const KvView& C, int T, int groups, int ctas, const Pl
         };
         const int total = scan(p.first, [](int n) { return n; });
         int q = 0;
-        if (PIECE > 0 && C.B * groups <= ctas) {
+        if (PIECE > 0 && C.B * groups <= ctas && (LEAST > 1 || total > ctas)) {
             // the least number of tiles a part, from the even share up, that needs no more than ctas parts
             const int even = max(LEAST, div_of(total + ctas - 1, ctas));
             unsigned fits = 0;

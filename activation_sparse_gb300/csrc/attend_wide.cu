@@ -49,6 +49,7 @@ namespace si {
 namespace {
 
 constexpr int kBlock = 128;        // query rows of one product: a TMEM lane each
+constexpr int kCopyWarps = 4, kCopyThreads = 32 * kCopyWarps;
 
 // NB row blocks a CTA meet every key tile it copies. E4M3: a cache of codes, which are copied as they are (a key or a
 // value tile each of kRaw places) and then become a ring slot's elements.
@@ -56,13 +57,12 @@ template <int DP, int NB, bool E4M3>
 struct WideCfg {
     static constexpr int kRows = kBlock * NB;
     static constexpr int kSoftmaxWarps = 4 * NB;
-    static constexpr int kCopyWarps = E4M3 && NB == 2 ? 8 : 4, kCopyThreads = 32 * kCopyWarps;
     static constexpr int kMmaWarp = kSoftmaxWarps, kCopyWarp = kMmaWarp + 1;
     static constexpr int kThreads = 32 * (kCopyWarp + kCopyWarps);
     static constexpr int kCtas = NB == 1 ? 2 : 1;              // an SM
-    static constexpr int kMaxSlots = E4M3 ? (NB == 1 ? 3 : 6) : NB == 1 ? 5 : 9;  // ring slots: a key or a value tile each
+    static constexpr int kMaxSlots = E4M3 ? (NB == 1 ? 3 : 8) : NB == 1 ? 5 : 9;  // ring slots: a key or a value tile each
     static constexpr int kTile = KT * DP * 2;
-    static constexpr int kRaw = !E4M3 ? 0 : NB == 1 ? 3 : 6;
+    static constexpr int kRaw = E4M3 ? 3 : 0;
     static constexpr int kScaleTiles = 4;                      // whose scales are kept
     static constexpr int kRawBytes = kRaw * (kTile / 2) + (E4M3 ? kCopyWarps * kScaleTiles * 32 * 4 : 0);
     static constexpr int kQ = kBlock * DP * 2;                 // of one block
@@ -229,7 +229,7 @@ __device__ __forceinline__ void copy_codes(const AttendParams& P, const Plan& pl
                                            uint8_t* ring, uint64_t* full, uint64_t* empty, uint16_t* odd) {
     using Cfg = WideCfg<DP, NB, true>;
     constexpr int RAW = Cfg::kRaw;
-    constexpr int WK = KT / Cfg::kCopyWarps;  // keys a warp has of a tile
+    constexpr int WK = KT / kCopyWarps;  // sixteen keys a warp has of a tile
     using Cp = Copy8<DP, WK>;
     const KvView& C = P.c;
     const int T = P.T, D = C.D, groups = C.Hkv * row_blocks;
@@ -241,7 +241,7 @@ __device__ __forceinline__ void copy_codes(const AttendParams& P, const Plan& pl
     uint8_t* const raw = ring + slots * Cfg::kTile + (warp * 32 + lane) * 16;  // [place][row of the lane][thread]
     float* const scale_s = reinterpret_cast<float*>(ring + slots * Cfg::kTile + RAW * (Cfg::kTile / 2)) + warp * Cfg::kScaleTiles * 32;
     const uint32_t raw_addr = smem_u32(raw);
-    constexpr int kPlace = Cfg::kTile / 2, kRow = Cfg::kCopyThreads * 16;
+    constexpr int kPlace = Cfg::kTile / 2, kRow = kCopyThreads * 16;
     SourceOf<uint8_t> src;
     src.start(plan, C.B, x0, x1);
     int held = kNoSlot, seen_b = -1;
@@ -254,7 +254,7 @@ __device__ __forceinline__ void copy_codes(const AttendParams& P, const Plan& pl
         held = slot_of(src.list, i0 + own0 + lane % WK, src.len, src.tot, src.seen);
     };
     int slot[Cp::SWEEPS];
-    int in = 0, in_tile = 0, byte = 0;  // place of the next copies; a scale on its way
+    int in = 0, in_tile = 0, byte = -1;  // place of the next copies; a scale on its way (-1: none)
     bool all = false;                   // whether they leave nothing out
     const uint8_t* v_from = nullptr;
     bool on = false;                    // whether the values of the tile whose keys went last are still to come
@@ -276,10 +276,16 @@ __device__ __forceinline__ void copy_codes(const AttendParams& P, const Plan& pl
     auto issue = [&]() {
         if (on) {
             copy(v_from, v_step);
+            on = false;
+            cp_commit();
+            return;
+        }
+        if (byte >= 0) {  // the scales of the tile before have had a tile's time to arrive
             scale_s[in_tile * 32 + lane] = scale_of(byte, C.e_lo, C.e_hi);
             if (++in_tile == Cfg::kScaleTiles) in_tile = 0;
-            on = false;
-        } else if (src.x < x1) {
+            byte = -1;
+        }
+        if (src.x < x1) {
             const bool ok = slot_ok(held, n_slots, P.err);
             const bool cached = src.at.tile * KT + KT <= src.len;
             const int mine = ok ? held : cached ? 0 : -1;  // a bad slot has been reported; slot 0 is read
@@ -303,75 +309,65 @@ __device__ __forceinline__ void copy_codes(const AttendParams& P, const Plan& pl
         if (++at == slots) at = 0, ++fill;
         return mine;
     };
-    int out = 0, out_tile = 0;          // place of the next tile that becomes elements
-    auto load = [&](uint4 (&to)[Cp::SWEEPS]) {
-        cp_wait<RAW - 2>();
-#pragma unroll
-        for (int j = 0; j < Cp::SWEEPS; ++j) to[j] = *reinterpret_cast<const uint4*>(raw + out * kPlace + j * kRow);
-        if (++out == RAW) out = 0;
-        issue();
-    };
-    auto store_as = [&](int slot_at, const uint4 (&from)[Cp::SWEEPS], float scale, int first_lane, auto in_half) {
-        uint8_t* tile = sub_tile + slot_at * Cfg::kTile;
-#pragma unroll
-        for (int j = 0; j < Cp::SWEEPS; ++j) {
-            const int r = Cp::row(lane, j);
-            uint4 lo, hi;
-            elements16<FP16, in_half.value>(from[j], __shfl_sync(0xFFFFFFFFu, scale, first_lane + r), lo, hi);
-            *reinterpret_cast<uint4*>(tile + sw128(own0 + r, 2 * (unit & 3))) = lo;
-            *reinterpret_cast<uint4*>(tile + sw128(own0 + r, 2 * (unit & 3) + 1)) = hi;
-        }
-    };
-    // The elements of a key or value tile, and the word that they are there: one arrival a warp.
-    auto store = [&](int slot_at, const uint4 (&from)[Cp::SWEEPS], float scale, int first_lane) {
-        // 2^-14 .. 2^15, 0 or NaN; a cache of bf16 with other scales among the warp's takes the longer way
-        const bool in_half = FP16 || __all_sync(0xFFFFFFFFu, !(scale > 32768.0f) && !(scale < 6.103515625e-5f && scale > 0.0f));
-        if (in_half) store_as(slot_at, from, scale, first_lane, std::true_type());
-        else store_as(slot_at, from, scale, first_lane, std::false_type());
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&full[slot_at]);
-    };
+    // The loops below are short on purpose: the code of all roles together does not fit the instruction caches next to the
+    // warps, and straight code runs at the pace at which it is fetched.
     src.enter(C, plan, row_blocks);
     fetch();
 #pragma unroll 1
     for (int i = 0; i < RAW - 1; ++i) issue();
     At a = locate(plan, C.B, x0);
-    for (int x = x0; x < x1; ++x, step(plan, C.B, groups, a)) {
-        const int i0 = a.tile * KT, len = plan.len[a.b];
-        const bool cached = i0 + KT <= len;
-        uint4 codes[Cp::SWEEPS];
-        load(codes);
+    int out = 0, out_tile = 0;          // place of the next tile that becomes elements
+    float scale = 1.0f;
+    bool in_half = true, cached = true;
+    int i0 = 0, len = 0;
+#pragma unroll 1
+    for (int half = 0; half < 2 * (x1 - x0); ++half) {
+        const bool is_v = half & 1;
+        cp_wait<RAW - 2>();
+        issue();
         __syncwarp();
-        float scale = scale_s[out_tile * 32 + lane];  // written with the values' copies, which went out before now
-        if (++out_tile == Cfg::kScaleTiles) out_tile = 0;
-        const int k_at = take();
-        store(k_at, codes, scale, 0);
-        load(codes);
-        unsigned bad = 0;
-        if (!cached) {
+        if (!is_v) {
+            i0 = a.tile * KT, len = plan.len[a.b];
+            cached = i0 + KT <= len;
+            step(plan, C.B, groups, a);
+            scale = scale_s[out_tile * 32 + lane];  // written when the next tile's keys went out, at the latest just now
+            if (++out_tile == Cfg::kScaleTiles) out_tile = 0;
+            // 2^-14 .. 2^15, 0 or NaN; a cache of bf16 with other scales among the warp's takes the longer way
+            in_half = FP16 || __all_sync(0xFFFFFFFFu, !(scale > 32768.0f) && !(scale < 6.103515625e-5f && scale > 0.0f));
+        }
+        uint8_t* const from = raw + out * kPlace;
+        if (++out == RAW) out = 0;
+        const int to = take();
+        if (is_v && !cached) {
             // New nodes' value rows that are NaN leave the tile (0 * NaN is NaN) and are reported, so that the rows that
-            // see them get them back at the end.
+            // see them get them back at the end. A lane looks at what it copied itself.
+            unsigned bad = 0;
             const int node = i0 + own0 + lane % WK - len;
             if (of_v && node >= 0 && node < T && scale != scale) bad |= 1u << lane % WK, scale = 0.0f;
-#pragma unroll
+#pragma unroll 1
             for (int j = 0; j < Cp::SWEEPS; ++j) {
                 const int r = Cp::row(lane, j), of = i0 + own0 + r - len;
                 if (of < 0 || of >= T) continue;
-                uint32_t* w = reinterpret_cast<uint32_t*>(&codes[j]);
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-#pragma unroll
-                    for (int k = 0; k < 32; k += 8)
-                        if (code_nan(w[i] >> k)) w[i] &= ~(0xFFu << k), bad |= 1u << r;
+                for (int i = 0; i < 16; ++i)
+                    if (code_nan(from[j * kRow + i])) from[j * kRow + i] = 0, bad |= 1u << r;
             }
             bad = __reduce_or_sync(0xFFFFFFFFu, bad);
+            if (lane == 0) odd[to * 4 + own0 / 16] = (uint16_t)bad;
         }
-        const int v_at = take();
-        if (!cached && lane == 0) {  // the keys' bits of the tile's word
-            if (WK == 16) odd[v_at * 4 + own0 / 16] = (uint16_t)bad;
-            else reinterpret_cast<uint8_t*>(odd)[v_at * 8 + own0 / 8] = (uint8_t)bad;
+        uint8_t* const tile = sub_tile + to * Cfg::kTile;
+#pragma unroll 1
+        for (int j = 0; j < Cp::SWEEPS; ++j) {
+            const int r = Cp::row(lane, j);
+            const float by = __shfl_sync(0xFFFFFFFFu, scale, (is_v ? WK : 0) + r);
+            const uint4 codes = *reinterpret_cast<const uint4*>(from + j * kRow);
+            uint4 lo, hi;
+            if (in_half) elements16<FP16, true>(codes, by, lo, hi);
+            else elements16<FP16, false>(codes, by, lo, hi);
+            *reinterpret_cast<uint4*>(tile + sw128(own0 + r, 2 * (unit & 3))) = lo;
+            *reinterpret_cast<uint4*>(tile + sw128(own0 + r, 2 * (unit & 3) + 1)) = hi;
         }
-        store(v_at, codes, scale, WK);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&full[to]);  // one arrival a warp
     }
     cp_wait<0>();
 }
@@ -411,7 +407,7 @@ __global__ void __launch_bounds__(WideCfg<DP, NB, E4M3>::kThreads, WideCfg<DP, N
     }
     if (tid == 0) {
         for (int s = 0; s < kMaxSlots; ++s) {
-            mbar_init(&full[s], E4M3 ? Cfg::kCopyWarps : Cfg::kCopyThreads);
+            mbar_init(&full[s], E4M3 ? kCopyWarps : kCopyThreads);
             mbar_init(&empty[s], 1);
         }
         for (int k = 0; k < NB; ++k) {

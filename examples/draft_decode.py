@@ -5,9 +5,11 @@ A small decoder with random weights: per layer attention over the cache
 computed set (si_sparse_ffn_decode); once a step si_kv_evict takes the
 accepted path into the cache and keeps it within a budget. A step runs the
 pending token and a tree of guesses for what follows it; the guesses that the
-model itself would have taken are accepted.
+model itself would have taken are accepted: si_token_logprobs gives each
+node's best token and what the tokens of its guesses are worth. With --codes
+the cache holds e4m3 codes, half the bytes.
 
-    python examples/draft_decode.py [--steps 64] [--budget 96] [--plain]
+    python examples/draft_decode.py [--steps 64] [--budget 96] [--plain] [--codes]
 """
 import argparse
 import os
@@ -26,7 +28,7 @@ PARENTS = [-1, 0, 0, 0, 1, 2, 3]
 class Model:
     """Random weights, and what a program keeps: packed FFN layers, computed sets, the cache, rotary positions."""
 
-    def __init__(self, seed=0, layers=2, d=256, neurons=1024, heads=4, kv_heads=2, head_dim=64, vocab=24, slots=512):
+    def __init__(self, seed=0, layers=2, d=256, neurons=1024, heads=4, kv_heads=2, head_dim=64, vocab=24, slots=512, codes=False):
         g = torch.Generator(device="cuda").manual_seed(seed)
         bf = torch.bfloat16
         rnd = lambda *shape, scale: (torch.randn(*shape, generator=g, device="cuda") * scale).to(bf)  # noqa: E731
@@ -43,9 +45,13 @@ class Model:
             self.S.append(torch.arange(0, layer.n_loaded, 2, dtype=torch.int32, device="cuda"))  # the computed set
         self.K = torch.zeros(layers, 1, kv_heads, slots, head_dim, dtype=bf, device="cuda")
         self.V = torch.zeros_like(self.K)
+        scales = {}
+        if codes:  # a scale a slot, which the append writes
+            self.K, self.V = self.K.to(torch.float8_e4m3fn), self.V.to(torch.float8_e4m3fn)
+            scales = {name: torch.zeros(layers, 1, kv_heads, slots, dtype=torch.uint8, device="cuda") for name in ("k_scale", "v_scale")}
         table = torch.arange(slots, dtype=torch.int32, device="cuda").expand(layers, 1, kv_heads, slots).contiguous()
         acc = torch.zeros(layers, 1, kv_heads, slots, device="cuda")
-        self.cache = si.si_kv_create(self.K, self.V, table, torch.zeros(layers, 1, dtype=torch.int32, device="cuda"), acc)
+        self.cache = si.si_kv_create(self.K, self.V, table, torch.zeros(layers, 1, dtype=torch.int32, device="cuda"), acc, **scales)
         self.rope = si.si_rope_create(head_dim, base=10000.0)
 
     def _ffn(self, i, x):
@@ -93,8 +99,18 @@ def words_of(parents):
     return torch.tensor([words], dtype=torch.int64, device="cuda")
 
 
-def decode(model, prompt, steps, budget=0, draft=True, seed=1):
-    """`steps` tokens after the prompt, greedily, and how many were accepted a step on average."""
+def judged(logits, targets):
+    """Each node's best token, the log probability of the targets [T][M] (-1: none) behind it, and its entropy."""
+    T, M = targets.shape
+    logp, entropy = torch.empty(T, M, device="cuda"), torch.empty(T, device="cuda")
+    top, ids = torch.empty(T, 1, device="cuda"), torch.empty(T, 1, dtype=torch.int32, device="cuda")
+    si.si_token_logprobs(logits, targets=targets, logp=logp, entropy=entropy, top_logp=top, top_ids=ids)
+    return ids[:, 0].tolist(), logp.tolist(), entropy.tolist()
+
+
+def decode(model, prompt, steps, budget=0, draft=True, seed=1, told=None):
+    """`steps` tokens after the prompt, greedily, and how many were accepted a step on average. `told` (a list) gets the
+    log probability that the model gave each of them, and its entropy there."""
     guess = torch.Generator().manual_seed(seed)
     chain = lambda T: torch.arange(T, device="cuda")  # noqa: E731
     done = 0
@@ -104,24 +120,38 @@ def decode(model, prompt, steps, budget=0, draft=True, seed=1):
         logits, seen = model.forward(part, done + chain(part.numel()), words)
         model.keep(part.numel(), list(range(part.numel())), words, seen, budget)
         done += part.numel()
-    pending, got, runs = int(logits[-1].argmax()), [], 0
+    none = torch.full((1, 1), -1, dtype=torch.int32, device="cuda")
+    (pending,), _, (entropy,) = judged(logits[-1:], none)
+    worth = judged(logits[-1:], none + 1 + pending)[1][0][0], entropy  # of the pending token
+    got, runs = [], 0
     parents = PARENTS if draft else [-1]
     words = words_of(parents)
+    children = [[t for t, p in enumerate(parents) if p == n] for n in range(len(parents))]
+    most = max(1, max(len(c) for c in children))
     depth = torch.tensor([bin(int(w)).count("1") - 1 for w in words[0].tolist()], device="cuda")
     while len(got) < steps:
         guesses = torch.randperm(model.vocab, generator=guess)[:len(parents) - 1].tolist()
         tokens = [pending] + guesses
         logits, seen = model.forward(torch.tensor(tokens, device="cuda"), done + depth, words)
-        wanted = logits.argmax(-1).tolist()
-        path = [0]
+        behind = torch.tensor([[tokens[t] for t in c] + [-1] * (most - len(c)) for c in children], dtype=torch.int32, device="cuda")
+        wanted, logp, entropy = judged(logits, behind)
+        path, worths = [0], [worth]
         while True:  # a guess stands if it is what the model wants after the node before it
-            follow = [t for t, p in enumerate(parents) if p == path[-1] and tokens[t] == wanted[path[-1]]]
+            n = path[-1]
+            follow = [i for i, t in enumerate(children[n]) if tokens[t] == wanted[n]]
             if not follow:
                 break
-            path.append(follow[0])
+            worths.append((logp[n][follow[0]], entropy[n]))
+            path.append(children[n][follow[0]])
         model.keep(len(parents), path, words, seen, budget)
         got += [tokens[t] for t in path]
+        if told is not None:
+            told += worths
         done, pending, runs = done + len(path), wanted[path[-1]], runs + 1
+        last = path[-1]
+        worth = judged(logits[last:last + 1], none + 1 + pending)[1][0][0], entropy[last]
+    if told is not None:
+        del told[steps:]
     return got[:steps], len(got) / runs
 
 
@@ -130,10 +160,13 @@ def main():
     ap.add_argument("--steps", type=int, default=64)
     ap.add_argument("--budget", type=int, default=96)
     ap.add_argument("--plain", action="store_true", help="one token a step")
+    ap.add_argument("--codes", action="store_true", help="a cache of e4m3 codes")
     a = ap.parse_args()
-    model = Model()
-    tokens, a_step = decode(model, [t * 7 % 24 for t in range(40)], a.steps, a.budget, not a.plain)
+    model = Model(codes=a.codes)
+    told = []
+    tokens, a_step = decode(model, [t * 7 % 24 for t in range(40)], a.steps, a.budget, not a.plain, told=told)
     print("tokens", tokens)
+    print("log probability %.3f a token, entropy %.3f" % tuple(sum(x) / len(told) for x in zip(*told)))
     print("%.2f tokens a step, %d keys a list, device error word %#x"
           % (a_step, int(model.cache.lens[0, 0]), si.si_device_error()))
 

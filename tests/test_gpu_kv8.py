@@ -261,6 +261,11 @@ CASES = [
     ([500], 8, 1, 1, 112, "bf16", True, "tree", 1),              # eight rows a key
     ([500], 9, 1, 1, 112, "fp16", True, "tree", 1),              # nine
     ([900, 10], 16, 4, 4, 128, "fp16", True, "pad", 1),          # sixteen
+    ([2, 40, 0, 129] * 200, 1, 2, 1, 128, "bf16", True, "none", 1),   # 800 sequences: the plan beside the ring
+    ([2, 40] * 450, 20, 1, 1, 128, "fp16", True, "tree", 1),
+    ([3, 70, 1] * 300, 2, 2, 1, 256, "bf16", True, "tree", 32),
+    ([150], 4, 64, 1, 256, "fp16", True, "tree", 1),             # 256 rows a key in blocks of 16
+    ([70, 300], 64, 32, 1, 64, "bf16", True, "tree", 1),         # 2048
 ]
 
 
@@ -441,6 +446,8 @@ WEIGH = [
     ([70], 40, 10, 1, 256, "fp16", True, "tree", None, 1),
     ([30, 31], 2, 2, 2, 16, "bf16", True, "tree", None, 1),
     ([5, 70] * 60, 3, 4, 2, 80, "bf16", True, "tree", None, 1),
+    ([2, 40, 0, 129] * 200, 1, 2, 1, 128, "bf16", True, "none", None, 1),
+    ([150], 4, 64, 1, 128, "fp16", True, "tree", [0b1010], 1),
 ]
 
 

@@ -6,6 +6,8 @@ namespace si {
 
 namespace {
 
+// 8192 tokens of 32 + 8 + 8 heads of 128 / of 64 with 64, 96, 128, 192 and 256 threads a token: 42.3, 40.6, 40.1, 42.4, 49.5 /
+// 23.1, 22.7, 26.0, 28.3, 33.5 us.
 constexpr int kAppendThreads = 96;
 
 // Sixteen elements of a row as they were loaded: eight pairs, (x[i], y[i]) where the layout is half-split and (x[0], x[1]),
@@ -40,7 +42,9 @@ __device__ __forceinline__ unsigned size_of(float2 p) {  // NaN above infinity a
 // eight a lane), so that a key's or value's largest magnitude is a few
 // shuffles. Rows are scaled and rounded from the fp32 values, which are made
 // twice, for the magnitude and for the codes: the elements stay as they were
-// loaded meanwhile, half of the registers.
+// loaded meanwhile, half of the registers. Bound by memory and the chain of
+// loads (position, slot, row): 8192 tokens of 32 + 8 + 8 heads of 128 take 40.6
+// us, 4.5 TB/s, 0.68 of what a plain copy reaches.
 template <bool FP16>
 __global__ void __launch_bounds__(kAppendThreads)
     k_kv_append8(const __grid_constant__ KvAppendParams P, const __grid_constant__ RopeTable R, int group) {

@@ -33,9 +33,15 @@
 // output's own rounding alone (fp16 0.00021 instead of 0.00028), but the
 // second terms' instructions lie in the chain that bounds this kernel (72 / 80 us
 // above; 6 trees of 16 nodes, 9001 keys 27.5 / 28.6).
-// Over a cache of e4m3 codes the copying warps load a tile's codes into registers while they
-// turn the tile before into the type of q, its scales in it (exactly, see
-// si_kv_create_e4m3): the rest of the kernel does not know.
+// Over a cache of e4m3 codes the copying warps copy the codes as they are, tiles
+// ahead, and turn what they copied themselves into elements of the type of q,
+// scale and all (exactly, see si_kv_create_e4m3): the rest of the kernel does
+// not know. That work is on the way of every tile: the trees above take 84 us
+// (bf16 93), of which the products wait for keys 13 %; the copying warps are
+// busy nine tenths of a tile's time, with some 400 instructions that the caches
+// of instructions cannot hold next to the softmax's. Eight copying warps instead
+// of four: 87 and 90 us; a tile's codes held in registers instead of shared
+// memory: 85 and 91 with two blocks, but 60 instead of 50 with one (T = 16).
 // Every write to shared memory is an ordinary one; the issuing warp's proxy
 // fence, after the barrier that announces it, lets the tensor cores see it. All
 // waits are bounded; TMEM is always released.

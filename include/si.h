@@ -572,7 +572,7 @@ int si_kv_destroy(si_kv *kv);
  *   k, v uint8 [L][B][Hkv][ceil(n_slots / block)], strides {layer, sequence,
  *   head}. 16 <= D <= 256. */
 typedef struct si_kv_scales {
-    int block;
+    int block;                /* slots that share a scale */
     uint8_t *k, *v;
     long long k_stride[3], v_stride[3];
 } si_kv_scales;
@@ -622,8 +622,12 @@ int si_kv_append(si_kv *kv, int layer, const si_rope *rope, int T, int Hq,
  * Products and sums in fp32 on the tensor cores. For the product with v the
  * softmax weights are carried in two terms of the cache's type where a key
  * meets up to 16 rows (T * Hq / Hkv), and rounded to it once where it meets
- * more. Results do not depend on timing. Requires Hq % Hkv == 0,
- * 1 <= T <= 64; SI_ERR_UNSUPPORTED where lists (B * Hkv), blocks of 16 to
+ * more. Over a cache in 8 bits with up to 16 rows a key, or heads of more than
+ * 128 elements, they are carried in two terms of fp16, and bf16 queries go in
+ * as fp16 times a power of two (exact down to 2^-29 of a row's largest
+ * element, good to 2^-39 of it below).
+ * Results do not depend on timing. Requires Hq % Hkv == 0,
+ * 1 <= T <= 64; SI_ERR_UNSUPPORTED where lists (B * Hkv), blocks of 8 to
  * 256 rows of a list and tiles of 64 entries (cap) multiply past 32 bits. A
  * sequence with len + T > cap sets SI_DEVERR_CACHE and gets zeros. */
 int si_tree_attention(si_kv *kv, int layer, int T, int Hq, const void *q, const long long *q_stride,

@@ -338,8 +338,8 @@ __device__ __forceinline__ void copy_codes(const AttendParams& P, const Plan& pl
             step(plan, C.B, groups, a);
             scale = scale_s[out_tile * 32 + lane];  // written when the next tile's keys went out, at the latest just now
             if (++out_tile == Cfg::kScaleTiles) out_tile = 0;
-            // 2^-14 .. 2^15, 0 or NaN; a cache of bf16 with other scales among the warp's takes the longer way
-            in_half = FP16 || __all_sync(0xFFFFFFFFu, !(scale > 32768.0f) && !(scale < 6.103515625e-5f && scale > 0.0f));
+            // 2^-24 .. 2^15, 0 or NaN; a cache of bf16 with other scales among the warp's takes the longer way
+            in_half = FP16 || __all_sync(0xFFFFFFFFu, !(scale > 32768.0f) && !(scale < 5.9604644775390625e-8f && scale > 0.0f));
         }
         uint8_t* const from = raw + out * kPlace;
         if (++out == RAW) out = 0;

@@ -266,6 +266,9 @@ CASES = [
     ([3, 70, 1] * 300, 2, 2, 1, 256, "bf16", True, "tree", 32),
     ([150], 4, 64, 1, 256, "fp16", True, "tree", 1),             # 256 rows a key in blocks of 16
     ([70, 300], 64, 32, 1, 64, "bf16", True, "tree", 1),         # 2048
+    ([20000], 1, 8, 1, 128, "bf16", True, "none", 1),            # more parts than are joined at once
+    ([12000, 5], 2, 8, 1, 256, "fp16", False, "tree", 16),
+    ([30000], 1, 3, 1, 64, "fp16", True, "none", 1),
 ]
 
 
@@ -364,6 +367,36 @@ def test_attention_rows_that_see_nothing(si):
         si.si_tree_attention(c.kv, q, out, mask=words, lse=lse)
         assert bool((out == 0).all()) and bool(lse.isneginf().all())
         si.si_device_error(clear=True)
+
+
+@pytest.mark.parametrize("T,Hq,D", [(2, 4, 128), (20, 8, 64), (3, 2, 256)])
+def test_strided_operands(si, T, Hq, D):
+    """Pools, scales, tables, weights and queries that are slices of larger arrays give the bits of contiguous ones."""
+    t = torch()
+    c = Cache8(si, 30, [150, 64], T, 2, D, "bf16", slack=5)
+    q, words, mask = make_rows(c, T, Hq, D, "bf16", "tree")
+    want, lse, acc = t.empty_like(q), t.empty(q.shape[:3], device="cuda"), c.acc.clone()
+    si.si_tree_attention(c.kv, q, want, mask=mask, lse=lse)
+    si.si_kv_accumulate(c.kv, q, lse, mask=mask)
+
+    def within(a, pads):
+        """The same array as a slice of a larger one full of other numbers; the last dimension stays whole."""
+        big = t.full([n + p for n, p in zip(a.shape, pads)], 0x7F if a.element_size() == 1 else 7, device="cuda",
+                     dtype=t.uint8 if a.element_size() == 1 else a.dtype)
+        cut = tuple(slice(p // 2 // 16 * 16 if i == len(pads) - 1 else p // 2, p // 2 // 16 * 16 + n if i == len(pads) - 1 else p // 2 + n)
+                    for i, (n, p) in enumerate(zip(a.shape, pads)))
+        part = big[cut]
+        part.copy_(a.view(t.uint8) if a.element_size() == 1 else a)
+        return part.view(a.dtype)
+
+    K, V = within(c.K, (0, 1, 2, 3, 32)), within(c.V, (0, 2, 1, 5, 64))
+    ks, vs = within(c.k_scale, (1, 0, 1, 32)), within(c.v_scale, (0, 1, 1, 64))
+    table, acc2 = within(c.table, (1, 1, 1, 0)), within(acc, (1, 0, 1, 32))
+    kv = si.si_kv_create(K, V, table, c.lens, acc2, k_scale=ks, v_scale=vs)
+    q2, got, lse2 = within(q, (1, 2, 1, 32)), t.empty_like(q), t.empty_like(lse)
+    si.si_tree_attention(kv, q2, got, mask=mask, lse=lse2)
+    si.si_kv_accumulate(kv, q2, lse2, mask=mask)
+    assert t.equal(got, want) and t.equal(lse2, lse) and t.equal(acc2, c.acc)
 
 
 def test_attention_slot_outside_the_pool(si):

@@ -233,6 +233,8 @@ __global__ void __launch_bounds__(kThreads, Cfg8<DP, NT>::kCtas)
     const int unit = lane % UNITS;
     const bool unit_on = unit * 16 < D, whole_rows = D == DP;
     const int own0 = warp * WK;  // this warp's keys of a tile
+    const Cp cp(lane, own0);
+    const Load8<DP> ld(lane, own0);
     const int n_slots = (int)C.n_slots, k_step = (int)C.ks, v_step = (int)C.vs;
 
     // producer state: lane i holds the slot of key own0 + i (of sixteen: i % 16) of the tile to be issued next
@@ -271,7 +273,7 @@ __global__ void __launch_bounds__(kThreads, Cfg8<DP, NT>::kCtas)
             if (whole_rows && cached) {
 #pragma unroll
                 for (int j = 0; j < Cp::SWEEPS; ++j) {
-                    const uint32_t at = dst + tile8_at<DP>(own0 + Cp::row(lane, j), unit);
+                    const uint32_t at = dst + cp.place(j);
                     cp16(at, kp + (long long)slot[j] * k_step);
                     cp16(at + Cfg::kTile, vp + (long long)slot[j] * v_step);
                 }
@@ -280,7 +282,7 @@ __global__ void __launch_bounds__(kThreads, Cfg8<DP, NT>::kCtas)
                 for (int j = 0; j < Cp::SWEEPS; ++j) {
                     const bool on = slot[j] >= 0 && unit_on;
                     const long long from = on ? slot[j] : 0;
-                    const uint32_t at = dst + tile8_at<DP>(own0 + Cp::row(lane, j), unit);
+                    const uint32_t at = dst + cp.place(j);
                     cp16(at, on ? kp + from * k_step : src.k, on);
                     cp16(at + Cfg::kTile, on ? vp + from * v_step : src.v, on);
                 }
@@ -400,8 +402,6 @@ __global__ void __launch_bounds__(kThreads, Cfg8<DP, NT>::kCtas)
             __syncwarp();
             const uint32_t k_s = smem_u32(stage), v_s = k_s + Cfg::kTile;
             const float2* sc_s = reinterpret_cast<const float2*>(stage + Cfg::kOffScale) + own0;
-            // rows of an ldmatrix: keys 0-7, 8-15 of a unit, then of the next unit
-            const int ld_key = own0 + (lane & 15), ld_unit = lane >> 4;
             constexpr int CHAINS = MT * NT <= 2 ? 2 : 1;  // of products, for each sixteen keys and eight rows
             float s[MT][NT][4], s_odd[CHAINS == 2 ? MT : 1][CHAINS == 2 ? NT : 1][4] = {};
             float2 sc[MT][2];
@@ -416,7 +416,7 @@ __global__ void __launch_bounds__(kThreads, Cfg8<DP, NT>::kCtas)
 #pragma unroll
                 for (int m = 0; m < MT; ++m) {
                     uint32_t r[4];
-                    ldsm4(r, k_s + tile8_at<DP>(ld_key + m * 16, u + ld_unit));
+                    ldsm4(r, k_s + ld.place(u, m));
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
                         uint32_t a0, a1, a2, a3;
@@ -521,7 +521,7 @@ __global__ void __launch_bounds__(kThreads, Cfg8<DP, NT>::kCtas)
 #pragma unroll
                 for (int m = 0; m < MT; ++m) {
                     uint32_t r[4];
-                    ldsm4t(r, v_s + tile8_at<DP>(ld_key + m * 16, u + ld_unit));
+                    ldsm4t(r, v_s + ld.place(u, m));
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
                         // a register holds two keys' codes of elements 2g, 2g + 1: rows g and g + 8 of the product

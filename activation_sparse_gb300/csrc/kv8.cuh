@@ -57,17 +57,38 @@ __device__ __forceinline__ uint32_t tile8_at(int row, int unit) {
     return (uint32_t)(row * DP + ((unit ^ swap) * 16));
 }
 
-// As Copy, for rows of codes: a warp copies WK keys of every tile, lane i % WK holding the slot of key i.
+// As Copy, for rows of codes: a warp copies WK keys of every tile, lane i % WK holding the slot of key i. A sweep's rows are
+// neighbours, and PERIOD sweeps are eight rows: their places in the tile then differ by eight rows' bytes alone.
 template <int DP, int WK = 16>
 struct Copy8 {
     static constexpr int UNITS = DP / 16;
     static constexpr int AT_ONCE = 32 / UNITS;
     static constexpr int SWEEPS = WK / AT_ONCE;
-    static __device__ __forceinline__ int row(int lane, int j) { return (lane / UNITS) * SWEEPS + j; }
+    static constexpr int PERIOD = 8 / AT_ONCE;
+    static __device__ __forceinline__ int row(int lane, int j) { return j * AT_ONCE + lane / UNITS; }
     static __device__ __forceinline__ void slots(int held, int lane, int (&slot)[SWEEPS]) {
 #pragma unroll
         for (int j = 0; j < SWEEPS; ++j) slot[j] = __shfl_sync(0xFFFFFFFFu, held, row(lane, j));
     }
+    // Where this lane's unit of the first sweeps' rows lies in the tile, and so that of sweep j.
+    uint32_t at[PERIOD];
+    __device__ __forceinline__ Copy8(int lane, int own0) {
+#pragma unroll
+        for (int j = 0; j < PERIOD; ++j) at[j] = tile8_at<DP>(own0 + row(lane, j), lane % UNITS);
+    }
+    __device__ __forceinline__ uint32_t place(int j) const { return at[j % PERIOD] + j / PERIOD * 8 * DP; }
+};
+
+// Where a lane's row of an ldmatrix of sixteen keys (0-7, 8-15 of a unit, then of the next unit) lies in a tile, for every
+// two units; the next sixteen keys' lie 16 * DP bytes on.
+template <int DP>
+struct Load8 {
+    uint32_t at[DP / 32];
+    __device__ __forceinline__ Load8(int lane, int own0) {
+#pragma unroll
+        for (int i = 0; i < DP / 32; ++i) at[i] = tile8_at<DP>(own0 + (lane & 15), 2 * i + (lane >> 4));
+    }
+    __device__ __forceinline__ uint32_t place(int u, int m) const { return at[u / 2] + m * 16 * DP; }
 };
 
 // d += a (16 x 16) * b (16 x 8)

@@ -65,6 +65,8 @@ __global__ void __launch_bounds__(kThreads, Cfg8<DP>::kCtas) k_kv_accumulate8(co
     if (x0 >= x1) return;
     const int unit = lane % UNITS, own0 = warp * WK;
     const bool unit_on = unit * 16 < D, whole_rows = D == DP;
+    const Cp cp(lane, own0);
+    const Load8<DP> ld(lane, own0);
     const int n_slots = (int)C.n_slots, k_step = (int)C.ks;
 
     SourceOf<uint8_t, KEYS> src;
@@ -95,11 +97,11 @@ __global__ void __launch_bounds__(kThreads, Cfg8<DP>::kCtas) k_kv_accumulate8(co
             if (whole_rows) {
 #pragma unroll
                 for (int j = 0; j < Cp::SWEEPS; ++j)
-                    cp16(dst + tile8_at<DP>(own0 + Cp::row(lane, j), unit), kp + (long long)slot[j] * k_step);
+                    cp16(dst + cp.place(j), kp + (long long)slot[j] * k_step);
             } else {
 #pragma unroll
                 for (int j = 0; j < Cp::SWEEPS; ++j)
-                    cp16(dst + tile8_at<DP>(own0 + Cp::row(lane, j), unit),
+                    cp16(dst + cp.place(j),
                          unit_on ? kp + (long long)slot[j] * k_step : src.k, unit_on);
             }
             if (WK == 32 || lane < WK) {
@@ -205,7 +207,7 @@ __global__ void __launch_bounds__(kThreads, Cfg8<DP>::kCtas) k_kv_accumulate8(co
 #pragma unroll
             for (int u = 0; u < KD; u += 2) {
                 uint32_t r[4];
-                ldsm4(r, k_s + tile8_at<DP>(own0 + m * 16 + (lane & 15), u + (lane >> 4)));
+                ldsm4(r, k_s + ld.place(u, m));
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     halves4(r[2 * i], kf[m][u + i][0], kf[m][u + i][2]);

@@ -27,7 +27,7 @@
 // in pieces: the next call's last CTA did not fit beside the others and ran
 // after them. Sixteen sequences of up to 4097 keys, mixed order: 26 us; the parts
 // are whole tiles of 128 keys, nine or ten where an even share is seven and a half
-// (shares that run across the lists' ends: 29 us, a list's end costs 4).
+// (shares that run across the lists' ends: 28 us; a list's end costs some 3).
 #include "attend.cuh"
 #include "kv8.cuh"
 
@@ -55,7 +55,8 @@ struct Cfg8 {
     static constexpr int kJoinRow = DP + 4;                   // floats: likewise
     static constexpr bool kQInRegs = DP * NT <= 256;
     static constexpr int kOffQ = kStages * kStage;            // queries; the join of the warps takes their place
-    static constexpr int kUnion = 8 * kJoinRow * 4 > kRows * kQRow ? 8 * kJoinRow * 4 : kRows * kQRow;
+    static constexpr int kJoin = (NT == 1 ? 12 : 8) * kJoinRow * 4;  // three warps' rows of up to four, or one's of eight
+    static constexpr int kUnion = kJoin > kRows * kQRow ? kJoin : kRows * kQRow;
     static constexpr int kOffFactor = kOffQ + kUnion;         // what a query row was divided by
     static constexpr int kOffState = kOffFactor + kRows * 4;  // [warp][row] {maximum, sum}
     static constexpr int kOffLast = kOffState + 4 * kRows * 8;  // [2] lists that this CTA joins
@@ -296,17 +297,26 @@ __global__ void __launch_bounds__(kThreads, Cfg8<DP, NT>::kCtas)
         }
         cp_commit();
     };
-    // Query rows of a list's block into shared memory (rows past R are zero).
-    auto stage_queries = [&](const At& at) {
+    // Query rows of a list's block into shared memory (rows past R are zero), in two steps.
+    constexpr int Q_AT_ONCE = 32 / (DP / 8);                             // rows a warp takes at once
+    constexpr int Q_SWEEPS = (RB + 4 * Q_AT_ONCE - 1) / (4 * Q_AT_ONCE);
+    uint4 queries[Q_SWEEPS];
+    auto load_queries = [&](const At& at) {
         const int b = at.b, h = at.group / row_blocks, rb = at.group % row_blocks;
-        constexpr int AT_ONCE = 32 / (DP / 8);  // rows a warp takes at once
 #pragma unroll
-        for (int r0 = 0; r0 < RB; r0 += 4 * AT_ONCE) {
-            const int r = r0 + warp * AT_ONCE + lane / (DP / 8), row = rb * RB + r, t = row / G;
+        for (int i = 0; i < Q_SWEEPS; ++i) {
+            const int r = (i * 4 + warp) * Q_AT_ONCE + lane / (DP / 8), row = rb * RB + r, t = row / G;
             const bool on = r < RB && row < R;
             const uint16_t* from = static_cast<const uint16_t*>(P.q) + b * P.qb + t * P.qt + (long long)(h * G + row - t * G) * P.qh;
+            queries[i] = query_load<DP>(on ? from : nullptr, D, lane);
+        }
+    };
+    auto store_queries = [&]() {
+#pragma unroll
+        for (int i = 0; i < Q_SWEEPS; ++i) {
+            const int r = (i * 4 + warp) * Q_AT_ONCE + lane / (DP / 8);
             float down;
-            const uint4 val = query_unit<DP>(on ? from : nullptr, D, C.fp16, lane, down);
+            const uint4 val = query_half<DP>(queries[i], C.fp16, down);
             if (r < RB) {
                 *reinterpret_cast<uint4*>(q_s + r * Cfg::kQRow + lane % (DP / 8) * 16) = val;
                 if (lane % (DP / 8) == 0) factor_s[r] = down;
@@ -327,11 +337,12 @@ __global__ void __launch_bounds__(kThreads, Cfg8<DP, NT>::kCtas)
     }
     const int second_slot = held;
     held = first_slot;
-    stage_queries(a);
+    load_queries(a);
     issue();
     if (two) held = second_slot;
 #pragma unroll 1
     for (int s = 1; s < S - 1; ++s) issue();
+    store_queries();
 
     int segment = 0, stage_out = 0;
     for (int x = x0; x < x1; ++segment) {
@@ -343,7 +354,7 @@ __global__ void __launch_bounds__(kThreads, Cfg8<DP, NT>::kCtas)
 
         if (segment > 0) {
             __syncthreads();  // the previous list's joins and reads of q_s are over
-            stage_queries(a);
+            store_queries();
         }
         unsigned long long word[NT][2];
         float ref[NT][2], sum[NT][2], qdown[NT][2];
@@ -562,6 +573,7 @@ __global__ void __launch_bounds__(kThreads, Cfg8<DP, NT>::kCtas)
             a.tile = a.ntile - 1;
             step<KEYS>(plan, C.B, groups, a);
         }
+        if (x < x1) load_queries(a);  // of the next list: they come while this one is finished
 
         // Join the warps: maxima and sums, then output rows in warp order, through the place of this list's queries,
         // which are no longer needed: in the ring the next list's copies are in flight.
@@ -596,33 +608,34 @@ __global__ void __launch_bounds__(kThreads, Cfg8<DP, NT>::kCtas)
                 ref[n][e] = top;
                 sum[n][e] = all * Wt::kDown;
             }
-        // (All at once where the ring is idle: after the CTA's last tile.)
+        // (All at once where the rows are few, or the ring is idle: after the CTA's last tile.)
         float* const join_s = reinterpret_cast<float*>(x < x1 ? q_s : smem);
-        const int at_once = x < x1 ? 1 : 3;
+        const int at_once = x == x1 || (NT == 1 && R <= 4) ? 3 : 1;
+        const int area = (NT == 1 && R <= 4 ? 4 : 8) * Cfg::kJoinRow;
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll 1
             for (int w = 1; w < 4; w += at_once) {
                 if (n + w > 1) __syncthreads();
                 float* const place = join_s + 2 * c * Cfg::kJoinRow + 2 * g;
-                constexpr int kArea = 8 * Cfg::kJoinRow;
-                if (warp >= w && warp < w + at_once) {
+                const bool rows_on = NT > 1 || 2 * c < R;  // rows past R are left out
+                if (warp >= w && warp < w + at_once && rows_on) {
 #pragma unroll
                     for (int i = 0; i < KD; ++i)
 #pragma unroll
                         for (int e = 0; e < 2; ++e)
-                            *reinterpret_cast<float2*>(place + (warp - w) * kArea + e * Cfg::kJoinRow + i * 16) =
+                            *reinterpret_cast<float2*>(place + (warp - w) * area + e * Cfg::kJoinRow + i * 16) =
                                 make_float2(o[i][n][e], o[i][n][e + 2]);
                 }
                 __syncthreads();
-                if (warp == 0) {
+                if (warp == 0 && rows_on) {
 #pragma unroll 1
                     for (int k = 0; k < at_once; ++k)
 #pragma unroll
                         for (int i = 0; i < KD; ++i)
 #pragma unroll
                             for (int e = 0; e < 2; ++e) {
-                                const float2 v = *reinterpret_cast<const float2*>(place + k * kArea + e * Cfg::kJoinRow + i * 16);
+                                const float2 v = *reinterpret_cast<const float2*>(place + k * area + e * Cfg::kJoinRow + i * 16);
                                 o[i][n][e] += v.x, o[i][n][e + 2] += v.y;
                             }
                 }

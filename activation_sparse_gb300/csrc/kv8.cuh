@@ -100,16 +100,18 @@ __device__ __forceinline__ void mma16(float (&d)[4], uint32_t a0, uint32_t a1, u
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// This lane's eight elements of a query row (nullptr: zeros) as fp16, where the DP / 8 lanes of a group share a row of D
-// elements. fp16 queries are taken as they are; bf16 ones times the power of two that brings the row's largest into
+// This lane's eight elements of a query row of D elements (nullptr: zeros), which the DP / 8 lanes of a group share.
+template <int DP>
+__device__ __forceinline__ uint4 query_load(const uint16_t* row, int D, int lane) {
+    const int u = lane % (DP / 8);
+    return row && u * 8 < D ? *reinterpret_cast<const uint4*>(row + u * 8) : make_uint4(0, 0, 0, 0);
+}
+
+// The same as fp16. fp16 queries are taken as they are; bf16 ones times the power of two that brings the row's largest into
 // 2^14 .. 2^15, so that all down to 2^-29 of it is exact and what lies below good to 2^-39 of it: `down` undoes it. A
 // row that is not finite stays as it is.
 template <int DP>
-__device__ __forceinline__ uint4 query_unit(const uint16_t* row, int D, bool fp16, int lane, float& down) {
-    constexpr int LANES = DP / 8;
-    const int u = lane % LANES;
-    uint4 val = make_uint4(0, 0, 0, 0);
-    if (row && u * 8 < D) val = *reinterpret_cast<const uint4*>(row + u * 8);
+__device__ __forceinline__ uint4 query_half(uint4 val, bool fp16, float& down) {
     down = 1.0f;
     if (fp16) return val;
     uint32_t w[4] = {val.x, val.y, val.z, val.w};
@@ -117,7 +119,7 @@ __device__ __forceinline__ uint4 query_unit(const uint16_t* row, int D, bool fp1
 #pragma unroll
     for (int i = 0; i < 4; ++i) top = max(top, max(w[i] & 0x7F80u, w[i] >> 16 & 0x7F80u));
 #pragma unroll
-    for (int o = 1; o < LANES; o <<= 1) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+    for (int o = 1; o < DP / 8; o <<= 1) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
     const int e = (int)(top >> 7), f = min(268 - e, 253);
     const float up = e < 255 ? __int_as_float(f << 23) : 1.0f;
     if (e < 255) down = __int_as_float((254 - f) << 23);

@@ -172,7 +172,7 @@ __global__ void __launch_bounds__(kThreads, Cfg8<DP>::kCtas) k_kv_accumulate8(co
                 const int t = on ? node_s[(r0 + r) / G] : 0, gq = (r0 + r) % G;
                 const uint16_t* from = static_cast<const uint16_t*>(P.q) + b * P.qb + t * P.qt + (long long)(h * G + gq) * P.qh;
                 float down;
-                const uint4 val = query_unit<DP>(on ? from : nullptr, D, C.fp16, lane, down);
+                const uint4 val = query_half<DP>(query_load<DP>(on ? from : nullptr, D, lane), C.fp16, down);
                 if (r < padded) {
                     *reinterpret_cast<uint4*>(q_s + r * Cfg::kQRow + u * 16) = val;
                     if (u == 0) {

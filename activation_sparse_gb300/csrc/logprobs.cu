@@ -134,11 +134,12 @@ __device__ __forceinline__ void gather(Shared& S, unsigned long long list, int w
 // largest are the K largest of those; only their logits are looked at again,
 // a warp a thread, so no order of the logits costs more than K threads' share.
 // 2048 rows of 131072 bf16 take 88 us, 6.1 TB/s, 0.91 of what a plain copy
-// reaches (fp32 164, 6.5 TB/s; with eight alternatives 109, with 32 136: every
+// reaches (fp32 164, 6.5 TB/s; with eight alternatives 102, with 32 128: every
 // thread looks for its largest once more, and the candidates); one row of 32768
-// fp32 8, the host call; 128 rows of 50001 with four alternatives 13, of which
-// the alternatives are 5: sorts and merges of a block's threads, and a cluster
-// barrier.
+// fp32 8, the host call; 128 rows of 50001 with four alternatives 12.4, of which
+// the alternatives are 4.6: sorts and merges of a block's threads, and a cluster
+// barrier. (Where the search for the place of a maximum that grew is done at
+// once, in every batch some lane of a warp has one: 124 us for 96.)
 template <int DTYPE>
 __global__ void __launch_bounds__(kThreads, 4) k_token_logprobs(const __grid_constant__ LogprobsParams P) {
     using U = Unit<DTYPE>;
@@ -161,7 +162,7 @@ __global__ void __launch_bounds__(kThreads, 4) k_token_logprobs(const __grid_con
 
     Sums a{-INFINITY, 0.0f, 0.0f};
     uint64_t s2 = 0, u2 = 0;  // what belongs to a.s and a.u, in two sums each
-    // where the largest was first: a logit, or -2 - j of the batch that starts with unit j (-1: the thread has none)
+    // where the largest was first: a logit, or -2 - j of the unit j that has it (-1: the thread has none)
     int best = has_head ? tid : u0 + tid < u1 ? -2 - (u0 + tid) : has_tail ? head + units * U::N + tid : -1;
     auto grow = [&](float top) {
         if (a.m != -INFINITY) {
@@ -199,17 +200,32 @@ __global__ void __launch_bounds__(kThreads, 4) k_token_logprobs(const __grid_con
         for (int i = 0; i < kBatch; ++i)
             w[4 * i] = next[i].x, w[4 * i + 1] = next[i].y, w[4 * i + 2] = next[i].z, w[4 * i + 3] = next[i].w;
         load(j + kBatch * kThreads);
-        uint32_t hi = w[0], lo = w[0];
+        uint32_t unit[kBatch], hi = 0, lo = w[0];
 #pragma unroll
-        for (int i = 1; i < 4 * kBatch; ++i) hi = U::larger(hi, w[i]), lo = U::smaller(lo, w[i]);
-        float top, low;
-        if (DTYPE == SI_FP32) {
-            top = __uint_as_float(hi), low = __uint_as_float(lo);
-        } else {
-            const float2 h = U::pair(hi), l = U::pair(lo);
-            top = max_nan(h.x, h.y), low = fminf(l.x, l.y);
+        for (int i = 0; i < kBatch; ++i) {
+            unit[i] = U::larger(U::larger(w[4 * i], w[4 * i + 1]), U::larger(w[4 * i + 2], w[4 * i + 3]));
+            hi = i ? U::larger(hi, unit[i]) : unit[0];
         }
-        if (!(top <= a.m) && a.m == a.m) best = -2 - j, grow(top);  // it grows, or is NaN now
+#pragma unroll
+        for (int i = 1; i < 4 * kBatch; ++i) lo = U::smaller(lo, w[i]);
+        auto across = [](uint32_t v) {  // a word's largest
+            if (DTYPE == SI_FP32) return __uint_as_float(v);
+            const float2 p = U::pair(v);
+            return max_nan(p.x, p.y);
+        };
+        const float top = across(hi);
+        const float2 l = U::pair(lo);
+        const float low = DTYPE == SI_FP32 ? __uint_as_float(lo) : fminf(l.x, l.y);
+        if (!(top <= a.m) && a.m == a.m) {  // it grows, or is NaN now
+#pragma unroll
+            for (int i = kBatch - 1; i >= 0; --i) {
+                // For one alternative the batch will do: few threads look again.
+                if (P.K < 2 && i > 0) continue;
+                const float x = across(unit[i]);
+                if (P.K < 2 || x == top || x != x) best = -2 - (j + i * kThreads);
+            }
+            grow(top);
+        }
         const float base = a.m == -INFINITY ? 0.0f : a.m;
         const uint64_t base2 = both(-base, -base), c2 = both(c, c);
         const bool far = !((low - base) * c >= -1000.0f);  // -inf among them, or nearly: e's are bounded, 0 * -inf is NaN
@@ -255,23 +271,27 @@ __global__ void __launch_bounds__(kThreads, 4) k_token_logprobs(const __grid_con
         for (int w = 1; w < kWarps; ++w) top = max_nan(top, S.sums[w].m);
         wanted = wanted && (own == top || own != own);
     }
-    if (wanted && best < -1) {  // the first such logit of that batch
-        const int j = -2 - best;
-        load(j);
-        best = head + j * U::N;  // where all are -inf
+    if (wanted && best < -1) {  // the first such logit of that unit, or of its batch
+        const int unit = -2 - best;
+        best = head + unit * U::N;  // where all are -inf
+        bool found = false;
+#pragma unroll 1
+        for (int k = 0; k < kBatch && !found && unit + k * kThreads < u1; ++k) {
+            const uint4 v = __ldg(body + unit + k * kThreads);
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+            const int first = head + (unit + k * kThreads) * U::N;
+            auto is = [&](float x, int i) {
+                if (x == own || (own != own && x != x)) best = first + i, found = true;
+            };
 #pragma unroll
-        for (int i = 4 * kBatch - 1; i >= 0; --i) {
-            const uint4 v = next[i / 4];
-            const uint32_t w = i % 4 == 0 ? v.x : i % 4 == 1 ? v.y : i % 4 == 2 ? v.z : v.w;
-            const int id = head + (j + i / 4 * kThreads) * U::N + i % 4 * U::kWord;
-            auto is = [&](float x) { return x == own || (own != own && x != x); };
-            if (j + i / 4 * kThreads >= u1) continue;
-            if (DTYPE == SI_FP32) {
-                if (is(__uint_as_float(w))) best = id;
-            } else {
-                const float2 x = U::pair(w);
-                if (is(x.y)) best = id + 1;
-                if (is(x.x)) best = id;
+            for (int i = 3; i >= 0; --i) {
+                if (DTYPE == SI_FP32) {
+                    is(__uint_as_float(w[i]), i);
+                } else {
+                    const float2 x = U::pair(w[i]);
+                    is(x.y, 2 * i + 1);
+                    is(x.x, 2 * i);
+                }
             }
         }
     }

@@ -185,7 +185,7 @@ __global__ void __launch_bounds__(kThreads, 4) k_token_logprobs(const __grid_con
 #pragma unroll
         for (int i = 0; i < kBatch; ++i) {
             next[i] = make_uint4(U::kNone, U::kNone, U::kNone, U::kNone);
-            if (j + i * kThreads < u1) next[i] = __ldg(body + j + i * kThreads);
+            if (j + i * kThreads < u1) next[i] = body[j + i * kThreads];
         }
     };
     load(u0 + tid);
@@ -277,7 +277,7 @@ __global__ void __launch_bounds__(kThreads, 4) k_token_logprobs(const __grid_con
         bool found = false;
 #pragma unroll 1
         for (int k = 0; k < kBatch && !found && unit + k * kThreads < u1; ++k) {
-            const uint4 v = __ldg(body + unit + k * kThreads);
+            const uint4 v = body[unit + k * kThreads];
             const uint32_t w[4] = {v.x, v.y, v.z, v.w};
             const int first = head + (unit + k * kThreads) * U::N;
             auto is = [&](float x, int i) {
@@ -337,7 +337,7 @@ __global__ void __launch_bounds__(kThreads, 4) k_token_logprobs(const __grid_con
                 }
                 for (int k0 = 0; k0 < its; k0 += 32) {
                     uint4 w = make_uint4(U::kNone, U::kNone, U::kNone, U::kNone);
-                    if (k0 + lane < its) w = __ldg(body + u0 + t + (k0 + lane) * kThreads);
+                    if (k0 + lane < its) w = body[u0 + t + (k0 + lane) * kThreads];
                     const uint32_t hi = U::larger(U::larger(w.x, w.y), U::larger(w.z, w.w));
                     float top = __uint_as_float(hi);
                     if (DTYPE != SI_FP32) {

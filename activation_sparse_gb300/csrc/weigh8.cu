@@ -244,11 +244,16 @@ __global__ void __launch_bounds__(kThreads, Cfg8<DP>::kCtas) k_kv_accumulate8(co
                     for (int m = 0; m < MT; ++m) {
                         float p[4];
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const float sum = CHAINS == 2 ? s[0][m][t][e] + s[CHAINS - 1][m][t][e] : s[0][m][t][e];
-                            const float z = sum * (e & 1 ? down.y : down.x) * sk[m][e >> 1];
-                            p[e] = ex2(__fadd_rn(__fmul_rn(z, P.scale), e & 1 ? -lse.y : -lse.x) * kLog2e);
+                        for (int e = 0; e < 4; e += 2) {
+                            uint64_t z2 = both(s[0][m][t][e], s[0][m][t][e + 1]);
+                            if (CHAINS == 2) z2 = add2(z2, both(s[CHAINS - 1][m][t][e], s[CHAINS - 1][m][t][e + 1]));
+                            z2 = mul2(mul2(z2, both(down.x, down.y)), both(sk[m][e >> 1], sk[m][e >> 1]));
+                            split(z2, p[e], p[e + 1]);
                         }
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) p[e] = __fadd_rn(__fmul_rn(p[e], P.scale), e & 1 ? -lse.y : -lse.x);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) p[e] = ex2(p[e] * kLog2e);
                         if (n + NT * 8 > nr) {  // a padding row's zeros meet what a key holds, and 0 * NaN is NaN
 #pragma unroll
                             for (int e = 0; e < 4; ++e)

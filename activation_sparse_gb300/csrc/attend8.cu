@@ -188,7 +188,7 @@ __device__ void join_parts(const AttendParams& P, const Plan& plan, int row_bloc
         const int item = tid + i * kThreads, r = item / QUADS, q = item % QUADS;
         if (item >= quads || q * 4 >= D) continue;
         const float4 st = state_s[r];
-        const int t = (row0 + r) / G, g = row0 + r - t * G;
+        const int t = div_of(row0 + r, G), g = row0 + r - t * G;
         const bool empty = plan.tot[l.b] == 0 || word_of(P.mask, P.T, l.b, t) == 0 || st.y == 0.0f;
         const float inv = empty ? 0.0f : 1.0f / st.y;
         const long long at = ((long long)l.b * P.T + t) * P.Hq + h * G + g;
@@ -240,7 +240,8 @@ __global__ void __launch_bounds__(kThreads, Cfg8<DP, NT>::kCtas)
 
     // producer state: lane i holds the slot of key own0 + i (of sixteen: i % 16) of the tile to be issued next
     SourceOf<uint8_t, KEYS> src;
-    src.start(plan, C.B, x0, x1);
+    At a = locate<KEYS>(plan, C.B, x0);
+    src.at = a, src.x = x0, src.x1 = x1;
     const uint32_t ring = smem_u32(smem);
     int stage_in = 0, held = kNoSlot, seen_b = -1;
     // stages that wait for their scales, and this lane's key's: the older one first
@@ -305,7 +306,7 @@ __global__ void __launch_bounds__(kThreads, Cfg8<DP, NT>::kCtas)
         const int b = at.b, h = at.group / row_blocks, rb = at.group % row_blocks;
 #pragma unroll
         for (int i = 0; i < Q_SWEEPS; ++i) {
-            const int r = (i * 4 + warp) * Q_AT_ONCE + lane / (DP / 8), row = rb * RB + r, t = row / G;
+            const int r = (i * 4 + warp) * Q_AT_ONCE + lane / (DP / 8), row = rb * RB + r, t = div_of(row, G);
             const bool on = r < RB && row < R;
             const uint16_t* from = static_cast<const uint16_t*>(P.q) + b * P.qb + t * P.qt + (long long)(h * G + row - t * G) * P.qh;
             queries[i] = query_load<DP>(on ? from : nullptr, D, lane);
@@ -325,7 +326,6 @@ __global__ void __launch_bounds__(kThreads, Cfg8<DP, NT>::kCtas)
     };
     // The first slots, the second tile's with the first's where they are of one list, and the first queries go out
     // together: each is a trip to memory of its own.
-    At a = locate<KEYS>(plan, C.B, x0);
     src.enter(C, plan, row_blocks);
     fetch();
     const int first_slot = held;
@@ -365,7 +365,7 @@ __global__ void __launch_bounds__(kThreads, Cfg8<DP, NT>::kCtas)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const int row = rb * RB + n * 8 + 2 * c + e;
-                word[n][e] = row < R && tot > 0 ? word_of(P.mask, T, b, row / G) : 0;
+                word[n][e] = row < R && tot > 0 ? word_of(P.mask, T, b, div_of(row, G)) : 0;
                 ref[n][e] = -INFINITY, sum[n][e] = 0.0f;
             }
 #pragma unroll
@@ -650,7 +650,7 @@ __global__ void __launch_bounds__(kThreads, Cfg8<DP, NT>::kCtas)
                     if (row >= R) continue;
                     const bool empty = word[n][e] == 0 || sum[n][e] == 0.0f;
                     const float inv = empty ? 0.0f : 1.0f / sum[n][e];
-                    const int t = row / G, gq = row - t * G;
+                    const int t = div_of(row, G), gq = row - t * G;
                     const long long at = ((long long)b * T + t) * P.Hq + h * G + gq;
                     uint16_t* dst = static_cast<uint16_t*>(P.out) + at * D + 2 * g;
 #pragma unroll

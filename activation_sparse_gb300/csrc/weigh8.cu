@@ -70,7 +70,8 @@ __global__ void __launch_bounds__(kThreads, Cfg8<DP>::kCtas) k_kv_accumulate8(co
     const int n_slots = (int)C.n_slots, k_step = (int)C.ks;
 
     SourceOf<uint8_t, KEYS> src;
-    src.start(plan, C.B, x0, x1);
+    At a = locate<KEYS>(plan, C.B, x0);
+    src.at = a, src.x = x0, src.x1 = x1;
     const uint32_t ring = smem_u32(smem);
     int stage_in = 0, held = kNoSlot;  // lane i: the slot of the warp's key i (of sixteen: i % 16) of the tile to be issued next
     int pend[S - 1], pend_byte[S - 1];  // stages that wait for their scales, and this lane's: the oldest first
@@ -120,7 +121,6 @@ __global__ void __launch_bounds__(kThreads, Cfg8<DP>::kCtas) k_kv_accumulate8(co
         cp_commit();
     };
     // The first slots, and the second tile's where they are of the same list, go out together.
-    At a = locate<KEYS>(plan, C.B, x0);
     src.enter(C, plan, 1);
     fetch();
     const int first_slot = held;
@@ -169,7 +169,7 @@ __global__ void __launch_bounds__(kThreads, Cfg8<DP>::kCtas) k_kv_accumulate8(co
             for (int base = warp * AT_ONCE; base < padded; base += 4 * AT_ONCE) {
                 const int r = base + lane / (DP / 8), u = lane % (DP / 8);
                 const bool on = r < nr;
-                const int t = on ? node_s[(r0 + r) / G] : 0, gq = (r0 + r) % G;
+                const int nth = div_of(r0 + r, G), t = on ? node_s[nth] : 0, gq = r0 + r - nth * G;
                 const uint16_t* from = static_cast<const uint16_t*>(P.q) + b * P.qb + t * P.qt + (long long)(h * G + gq) * P.qh;
                 float down;
                 const uint4 val = query_half<DP>(query_load<DP>(on ? from : nullptr, D, lane), C.fp16, down);

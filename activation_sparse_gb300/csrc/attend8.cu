@@ -11,11 +11,15 @@
 //   O^T (D x 8 rows)      += V^T (D x 16 keys) P^T
 // Codes become fp16 in registers, two an instruction and exactly, on their way
 // from shared memory to the product; the scales stay out of it. A key's scale
-// multiplies its scores; a value's goes into the weight, relative to the largest
-// that the warp has met so far, which the output is rescaled by when it grows,
-// as it is by the softmax's maximum. Queries go in as fp16: bf16 rows times the
-// power of two that brings their largest element below 2^15, so that what lies
-// up to 2^29 below it is exact.
+// multiplies its scores; a value's goes into the weight's exponent. What comes
+// out goes into the product as two fp16 terms, so it is taken relative to a power
+// of two of its row's own: the largest weight times scale that the row has met,
+// which the output is rescaled by when it grows, as it is by the softmax's maximum.
+// (A unit for all rows, from the scales alone, lost the keys that a row weighs beside
+// a large scale that it does not. The rows' own cost 2 to 3 % at sixteen rows a key,
+// 34.5 / 35.4 us for sixteen sequences of up to 4097, and less than 1 % up to eight.)
+// Queries go in as fp16: bf16 rows times the power of two that brings their largest
+// element below 2^15, so that what lies up to 2^29 below it is exact.
 //
 // Bound by memory where lists are long: one token of 32 heads over 131071 keys
 // of 8 heads of 128 takes 53 us, 5.2 TB/s, 0.77 of what a plain copy reaches;
@@ -49,7 +53,7 @@ struct Cfg8 {
     static constexpr int kWarpKeys = 16 * kMT;
     static constexpr int kKeys = 4 * kWarpKeys;               // of a tile
     static constexpr int kTile = kKeys * DP;                  // bytes of a K or V tile
-    static constexpr int kOffScale = 2 * kTile;               // in a stage: {k, v} scales of its keys
+    static constexpr int kOffScale = 2 * kTile;               // in a stage: k's scale and the exponent of v's, of its keys
     static constexpr int kStage = 2 * kTile + kKeys * 8;
     static constexpr int kStages = DP == 64 ? 4 : 3;
     static constexpr int kCtas = DP == 64 ? 3 : 2;            // an SM
@@ -257,12 +261,13 @@ __global__ void __launch_bounds__(kThreads, Cfg8<DP, NT>::kCtas)
         held = slot_of(src.list, i0 + own0 + lane % WK, src.len, src.tot, src.seen);
     };
     auto issue = [&]() {
-        // The scales of the tile before last have had the time to arrive. A key that is not there has 0 (byte -1).
+        // The scales of the tile before last have had the time to arrive. A key that is not there (byte -1) is
+        // below all.
         if (pend[0] >= 0) {
             float2* to = reinterpret_cast<float2*>(smem + pend[0] * Cfg::kStage + Cfg::kOffScale);
             if (WK == 32 || lane < WK)
-                to[own0 + lane] = pend_k[0] < 0 ? make_float2(0.0f, 0.0f)
-                                                : make_float2(scale_of(pend_k[0], C.e_lo, C.e_hi), scale_of(pend_v[0], C.e_lo, C.e_hi));
+                to[own0 + lane] = pend_k[0] < 0 ? make_float2(0.0f, -127.0f)
+                                                : make_float2(scale_of(pend_k[0], C.e_lo, C.e_hi), exponent_of(pend_v[0], C.e_lo, C.e_hi));
         }
         pend[0] = pend[1], pend_k[0] = pend_k[1], pend_v[0] = pend_v[1], pend[1] = -1;
         if (src.x < x1) {
@@ -361,14 +366,15 @@ __global__ void __launch_bounds__(kThreads, Cfg8<DP, NT>::kCtas)
         unsigned long long word[NT][2];
         float ref[NT][2], sum[NT][2], qdown[NT][2];
         float o[KD][NT][4];
-        float unit_v = 0.0f, unit_inv = 1.0f;  // the largest scale of values so far
+        // o is over 2^base of its row too: log2 of the largest weight (over ref's) times its value's scale, kLazy below it at most.
+        float base[NT][2];
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const int row = rb * RB + n * 8 + 2 * c + e;
                 word[n][e] = row < R && tot > 0 ? word_of(P.mask, T, b, div_of(row, G)) : 0;
-                ref[n][e] = -INFINITY, sum[n][e] = 0.0f;
+                ref[n][e] = -INFINITY, base[n][e] = sum[n][e] = 0.0f;
             }
 #pragma unroll
         for (int i = 0; i < KD; ++i)
@@ -444,10 +450,10 @@ __global__ void __launch_bounds__(kThreads, Cfg8<DP, NT>::kCtas)
                 }
             }
             // s[m][n][0..1]: key g with rows 2c, 2c + 1; s[m][n][2..3]: key g + 8
-            float high = 0.0f;  // the largest scale of values
+            float high = -127.0f;  // the largest exponent of values
 #pragma unroll
             for (int m = 0; m < MT; ++m) high = fmaxf(high, fmaxf(sc[m][0].y, sc[m][1].y));  // NaN is passed over
-            bool grows = high > unit_v;
+            bool grows = false;
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
 #pragma unroll
@@ -474,26 +480,31 @@ __global__ void __launch_bounds__(kThreads, Cfg8<DP, NT>::kCtas)
                     for (int m = 1; m < MT; ++m) top = fmaxf(top, fmaxf(s[m][n][e], s[m][n][e + 2]));
                     // The difference is taken before the scale: scores of the type's lowest value differ by 0 from
                     // their maximum, where a fused s * c2 - ref * c2 would be off by the product's rounding.
-                    grows |= (top - ref[n][e]) * c2 > (float)Wt::kLazy;
+                    // A weight times its scale is at most the largest of both.
+                    grows |= (top - ref[n][e]) * c2 + fmaxf(high - base[n][e], 0.0f) > (float)Wt::kLazy;
                 }
             }
             if (__any_sync(0xFFFFFFFFu, grows)) {
-                const float most = column_max(fmaxf(unit_v, high));
-                const float fall = most > 0.0f ? unit_v * power_inverse(most) : 1.0f;
-                if (most > 0.0f) unit_v = most, unit_inv = power_inverse(most);
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
                     float keep[2];
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        float top = ref[n][e];
+                        const float old = ref[n][e];
+                        float top = old, most = -INFINITY;
 #pragma unroll
                         for (int m = 0; m < MT; ++m) top = fmaxf(top, fmaxf(s[m][n][e], s[m][n][e + 2]));
-                        top = column_max(top);
-                        keep[e] = top == ref[n][e] ? 1.0f : ex2((ref[n][e] - top) * c2);
-                        ref[n][e] = top;
-                        sum[n][e] *= keep[e];
-                        keep[e] *= fall;
+                        ref[n][e] = top = column_max(top);
+#pragma unroll
+                        for (int m = 0; m < MT; ++m)
+#pragma unroll
+                            for (int i = e; i < 4; i += 2)  // a scale of NaN is passed over: it makes the row NaN by itself
+                                most = fmaxf(most, fmaf(s[m][n][i] - shift_of(top), c2, sc[m][i >> 1].y));
+                        const float fall = top == old ? 0.0f : (old - top) * c2;  // of what there is, in powers of two
+                        const float next = fmaxf(fmaxf(column_max(most), base[n][e] + fall), -126.0f);
+                        sum[n][e] *= ex2(fall);
+                        keep[e] = ex2(fall + (base[n][e] - next));
+                        base[n][e] = next;
                     }
 #pragma unroll
                     for (int i = 0; i < KD; ++i) {
@@ -506,6 +517,7 @@ __global__ void __launch_bounds__(kThreads, Cfg8<DP, NT>::kCtas)
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
                 const float shift[2] = {shift_of(ref[n][0]), shift_of(ref[n][1])};
+                const float below[2] = {base[n][0] - Wt::kUp, base[n][1] - Wt::kUp};
 #pragma unroll
                 for (int m = 0; m < MT; ++m) {
                     float w[4];
@@ -513,7 +525,7 @@ __global__ void __launch_bounds__(kThreads, Cfg8<DP, NT>::kCtas)
                     for (int e = 0; e < 4; ++e) {
                         const float p = ex2(fmaf(s[m][n][e] - shift[e & 1], c2, Wt::kUp));
                         sum[n][e & 1] += p;
-                        w[e] = p * (sc[m][e >> 1].y * unit_inv);
+                        w[e] = ex2(fmaf(s[m][n][e] - shift[e & 1], c2, sc[m][e >> 1].y - below[e & 1]));
                     }
                     if (edge) {  // whatever scale a key has that the row does not see
 #pragma unroll
@@ -601,11 +613,11 @@ __global__ void __launch_bounds__(kThreads, Cfg8<DP, NT>::kCtas)
                 const float sh = shift_of(top);
 #pragma unroll
                 for (int w = 0; w < 4; ++w) all += st[w].y * ex2((st[w].x - sh) * c2);
-                const float f = ex2((ref[n][e] - sh) * c2) * Wt::kDown;
+                const float f = ex2((ref[n][e] - sh) * c2) * Wt::kDown, power = ex2(base[n][e]);
 #pragma unroll
                 for (int i = 0; i < KD; ++i) {
-                    o[i][n][e] = o[i][n][e] * f * unit_v;
-                    o[i][n][e + 2] = o[i][n][e + 2] * f * unit_v;
+                    o[i][n][e] = o[i][n][e] * f * power;
+                    o[i][n][e + 2] = o[i][n][e + 2] * f * power;
                 }
                 ref[n][e] = top;
                 sum[n][e] = all * Wt::kDown;

@@ -16,6 +16,11 @@ __device__ __forceinline__ float scale_of(int byte, int lo, int hi) {
     return byte == kScaleNaN ? __int_as_float(0x7FC00000) : __int_as_float(min(max(byte, lo), hi) << 23);
 }
 
+// The exponent of what a scale byte stands for.
+__device__ __forceinline__ float exponent_of(int byte, int lo, int hi) {
+    return byte == kScaleNaN ? __int_as_float(0x7FC00000) : (float)(min(max(byte, lo), hi) - 127);
+}
+
 // The scale byte of a row whose largest magnitude is top: the least power of two whose 448-fold reaches it.
 __device__ __forceinline__ int scale_byte_for(float top, int lo, int hi) {
     const int bits = __float_as_int(top);  // >= 0
@@ -45,9 +50,6 @@ __device__ __forceinline__ void halves4(uint32_t w, uint32_t& lo, uint32_t& hi) 
         : "=r"(lo), "=r"(hi)
         : "r"(w));
 }
-
-// 1 / x of a power of two within the scales' limits.
-__device__ __forceinline__ float power_inverse(float x) { return __int_as_float((254 << 23) - __float_as_int(x)); }
 
 // Byte offset of 16-byte unit `unit` of row `row` in a tile of rows of DP codes; XORed so that the eight rows of an
 // ldmatrix lie in different banks (two rows of 64 codes share the banks' 128 bytes).

@@ -623,7 +623,9 @@ int si_kv_append(si_kv *kv, int layer, const si_rope *rope, int T, int Hq,
  * softmax weights are carried in two terms of the cache's type where a key
  * meets up to 16 rows (T * Hq / Hkv), and rounded to it once where it meets
  * more. Over a cache in 8 bits with up to 16 rows a key, or heads of more than
- * 128 elements, they are carried in two terms of fp16, and bf16 queries go in
+ * 128 elements, they are carried in two terms of fp16, together with the values'
+ * scales and relative to the row's largest weight times scale (a key whose weight
+ * times scale lies 2^36 below that may be lost); bf16 queries go in
  * as fp16 times a power of two (exact down to 2^-29 of a row's largest
  * element, good to 2^-39 of it below).
  * Results do not depend on timing. Requires Hq % Hkv == 0,

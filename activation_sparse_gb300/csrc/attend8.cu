@@ -390,10 +390,16 @@ __global__ void __launch_bounds__(kThreads, Cfg8<DP, NT>::kCtas)
 #pragma unroll
                 for (int u = 0; u < KD; ++u) qf[Cfg::kQInRegs ? n : 0][Cfg::kQInRegs ? u : 0] = query(n, u);
         }
+        bool steep = false;
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) qdown[n][e] = factor_s[n * 8 + 2 * c + e];
+            for (int e = 0; e < 2; ++e) {
+                const float down = factor_s[n * 8 + 2 * c + e];
+                steep |= down > kSteep;
+                qdown[n][e] = fminf(down, kSteep);
+            }
+        steep = __any_sync(0xFFFFFFFFu, steep);
 
         for (; x < seg_end; ++x, ++a.tile) {
             cp_wait<S - 2>();
@@ -463,6 +469,14 @@ __global__ void __launch_bounds__(kThreads, Cfg8<DP, NT>::kCtas)
                         if (CHAINS == 2) s[m][n][e] += s_odd[CHAINS == 2 ? m : 0][CHAINS == 2 ? n : 0][e];
                         s[m][n][e] = s[m][n][e] * qdown[n][e & 1] * sc[m][e >> 1].x;
                     }
+                if (steep) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float rest = rest_of(factor_s[n * 8 + 2 * c + (e & 1)]);
+#pragma unroll
+                        for (int m = 0; m < MT; ++m) s[m][n][e] *= rest;
+                    }
+                }
                 if (edge) {
 #pragma unroll
                     for (int m = 0; m < MT; ++m)

@@ -130,6 +130,11 @@ __device__ __forceinline__ uint4 query_half(uint4 val, bool fp16, float& down) {
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+// A product's sum, up to 2^32, times a query row's `down` and the key's scale: past 2^64 `down` is taken in two parts, one
+// on either side of the scale, which may bring the score back into fp32's range.
+constexpr float kSteep = 18446744073709551616.0f;
+__device__ __forceinline__ float rest_of(float down) { return fmaxf(down * (1.0f / kSteep), 1.0f); }
+
 __device__ __forceinline__ bool code_nan(uint32_t code) { return (code & 0x7Fu) == 0x7Fu; }
 
 }  // namespace si

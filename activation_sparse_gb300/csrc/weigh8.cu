@@ -138,6 +138,7 @@ __global__ void __launch_bounds__(kThreads, Cfg8<DP>::kCtas) k_kv_accumulate8(co
     for (int s = 1; s < S - 1; ++s) issue();
 
     int have_b = -1, have_h = -1, have_block = -1, n_rows = 0, stage_out = 0;
+    bool steep = false;  // of the rows that are staged
     for (int x = x0; x < x1; ++x, step<KEYS>(plan, C.B, C.Hkv, a)) {
         const int b = a.b, h = a.group, len = plan.len[b], tot = plan.tot[b];  // tot = 0: nothing counts
         if (have_b != b) {
@@ -166,6 +167,7 @@ __global__ void __launch_bounds__(kThreads, Cfg8<DP>::kCtas) k_kv_accumulate8(co
             __syncthreads();
             const int padded = (nr + 15) & ~15;
             constexpr int AT_ONCE = 32 / (DP / 8);
+            bool far = false;
             for (int base = warp * AT_ONCE; base < padded; base += 4 * AT_ONCE) {
                 const int r = base + lane / (DP / 8), u = lane % (DP / 8);
                 const bool on = r < nr;
@@ -182,12 +184,13 @@ __global__ void __launch_bounds__(kThreads, Cfg8<DP>::kCtas) k_kv_accumulate8(co
                         lse_s[r] = lse == -INFINITY ? INFINITY : lse;
                         word_s[r] = on ? word_of(P.mask, T, b, t) : 0;
                         factor_s[r] = down;
+                        far |= down > kSteep;
                     }
                 }
             }
             have_h = h;
             have_block = r0;
-            __syncthreads();
+            steep = __syncthreads_or(far);
         };
         if (n_rows > 0) stage_rows(0, min(kRows, n_rows));
         cp_wait<S - 2>();
@@ -237,7 +240,8 @@ __global__ void __launch_bounds__(kThreads, Cfg8<DP>::kCtas) k_kv_accumulate8(co
 #pragma unroll
                 for (int t = 0; t < NT; ++t) {
                     const int r = n + t * 8 + c * 2;
-                    const float2 lse = *reinterpret_cast<const float2*>(lse_s + r), down = *reinterpret_cast<const float2*>(factor_s + r);
+                    const float2 lse = *reinterpret_cast<const float2*>(lse_s + r), whole = *reinterpret_cast<const float2*>(factor_s + r);
+                    const float2 down = make_float2(fminf(whole.x, kSteep), fminf(whole.y, kSteep));
                     // The difference is taken before the base's factor, and of the rounded product, as lse was: scores of
                     // the type's lowest value then differ from lse by 0.
 #pragma unroll
@@ -249,6 +253,10 @@ __global__ void __launch_bounds__(kThreads, Cfg8<DP>::kCtas) k_kv_accumulate8(co
                             if (CHAINS == 2) z2 = add2(z2, both(s[CHAINS - 1][m][t][e], s[CHAINS - 1][m][t][e + 1]));
                             z2 = mul2(mul2(z2, both(down.x, down.y)), both(sk[m][e >> 1], sk[m][e >> 1]));
                             split(z2, p[e], p[e + 1]);
+                        }
+                        if (steep) {
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) p[e] *= rest_of(factor_s[r + (e & 1)]);
                         }
 #pragma unroll
                         for (int e = 0; e < 4; ++e) p[e] = __fadd_rn(__fmul_rn(p[e], P.scale), e & 1 ? -lse.y : -lse.x);

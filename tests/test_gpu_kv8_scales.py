@@ -142,3 +142,25 @@ def test_values_of_a_node_that_a_row_does_not_see(si, T, Hq, Hkv, D, dtype, n):
     few = T * Hq // Hkv <= 16 or D > 128
     near = 2.0 ** -18 * mag + 2 * ref.U[dtype] * np.abs(want) + (2.0 ** -24 if dtype == "fp16" else 0.0) if few else 0.0
     assert (np.abs(host(out) - host(clean)) <= near)[0, :node].all()
+
+
+@pytest.mark.parametrize("T,Hq,Hkv,D", [(1, 4, 2, 64), (2, 8, 2, 128), (3, 8, 2, 128), (3, 4, 2, 256), (20, 8, 2, 64), (40, 4, 1, 128)])
+def test_queries_near_the_types_largest(si, T, Hq, Hkv, D):
+    """Queries 2^121 times as large over keys 2^-121 as large have the same scores, outputs and weights, to the bit: nothing
+    between the product and the score leaves fp32's range."""
+    t = torch()
+    c = Cache8(si, 64, [400], T, Hkv, D, "bf16", spread=0.0)
+    q, words, mask = make_rows(c, T, Hq, D, "bf16", "tree")
+    q[0, 0, 0, 1:] = 0.0  # an element alone
+    got = []
+    for up in (0, 121):
+        c.k_scale[c.k_scale != 255] = 124 - up  # 2^-3 and 2^-124
+        big = q * 2.0 ** up
+        assert bool(big.isfinite().all())
+        out, lse, acc = t.empty_like(q), t.empty(q.shape[:3], device="cuda"), t.zeros_like(c.acc[0])
+        si.si_tree_attention(c.kv, big, out, mask=mask, lse=lse, scale=0.02)
+        si.si_kv_accumulate(c.kv, big, lse, mask=mask, scale=0.02, acc_out=acc)
+        got.append((out, lse, acc))
+    assert bool(got[0][1].isfinite().all())
+    for x, y in zip(*got):
+        assert t.equal(x, y)

@@ -457,8 +457,9 @@ int si_token_logprobs(int dtype, const void* logits, long long row_stride, int N
         return fail(SI_ERR_INVALID_ARG, "dtype must be SI_BF16, SI_FP16 or SI_FP32");
     if (N < 0 || V < 1 || M < 0 || K < 0) return fail(SI_ERR_INVALID_ARG, "need N, M, K >= 0 and V >= 1");
     if (K > 32 || K > V) return fail(SI_ERR_INVALID_ARG, "need K <= 32 and K <= V");
-    if (!(temperature > 0.0f) || !std::isfinite(temperature) || !std::isfinite(1.0f / temperature))
-        return fail(SI_ERR_INVALID_ARG, "need a finite temperature > 0");
+    // the kernel's factor of the exponents, in powers of two, has to be finite too
+    if (!(temperature > 0.0f) || !std::isfinite(temperature) || !std::isfinite(1.0f / temperature * 1.4426950408889634f))
+        return fail(SI_ERR_INVALID_ARG, "need a finite temperature of at least 4.24e-39");
     if (N == 0) return SI_OK;
     if (!logits) return fail(SI_ERR_INVALID_ARG, "NULL pointer");
     if (N > 1 && row_stride < V) return fail(SI_ERR_INVALID_ARG, "row_stride must be at least V");

@@ -685,7 +685,8 @@ int si_kv_evict(si_kv *kv, int layer, int T, const int32_t *path, const int32_t 
  *     -0 tie; NaN counts as larger than all).
  * A row with a NaN or +inf has NaN for all of its numbers; one of -inf
  * alone has l = -inf and entropy 0. Sums in fp32, in a fixed order: results do
- * not depend on timing. N >= 0, 1 <= V < 2^31; temperature and its reciprocal > 0 and finite.
+ * not depend on timing. N >= 0, 1 <= V < 2^31; temperature finite, at least
+ * 4.24e-39 (log2(e) over it is finite in fp32).
  * Needs no handle and no scratch. */
 #define SI_FP32 2
 int si_token_logprobs(int dtype, const void *logits, long long row_stride, int N, int V, float temperature,

@@ -193,3 +193,16 @@ def test_logprobs_past_32_bits(si):
     x = wide[:, 33:33 + 5000]
     x.copy_(t.randn(3, 5000, device="cuda"))
     check(x.double().cpu().numpy(), None, 5, 1.0, run(si, x, None, 5))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("temperature", [4.3e-39, 1e-38, 3e38])
+def test_logprobs_at_the_ends_of_the_temperature(si, dtype, temperature):
+    """The least temperature that is taken: differences become 0, or as large as fp32 holds; and the largest: all even."""
+    t = torch()
+    rng = np.random.default_rng(8)
+    x = t.from_numpy(rng.standard_normal((4, 3001)) * 0.3).to(tdtype(dtype)).cuda()
+    x[1, 5], x[1, 2900] = 3.0, 3.0   # two largest
+    x[2] = 0.25
+    targets = np.tile(np.array([0, 5, 2900], np.int32), (4, 1))
+    check(x.double().cpu().numpy(), targets, 8, temperature, run(si, x, t.from_numpy(targets).cuda(), 8, temperature))

@@ -99,6 +99,18 @@ def test_logprobs_refuse(si):
     assert call(M=0, K=0, entropy=None) == si.SI_OK
 
 
+@pytest.mark.parametrize("t", [2.9e-39, 2.95e-39, 3.5e-39, 4.2e-39, 4.239e-39])
+def test_logprobs_refuse_a_temperature_whose_exponents_overflow(si, t):
+    """1 / t is finite for most of these, log2(e) / t is not."""
+    rc = si.load().si_token_logprobs(2, 1 << 20, 100, 2, 100, t, None, 0, None, 1 << 20, 0, None, None, None)
+    assert rc == si.SI_ERR_INVALID_ARG and b"temperature" in si.load().si_last_error_string()
+
+
+@pytest.mark.parametrize("t", [4.25e-39, 1e-38, 1.0, 3.4e38])
+def test_logprobs_take_temperatures_to_the_ends(si, t):
+    assert si.load().si_token_logprobs(2, None, 100, 0, 100, t, None, 0, None, 1 << 20, 0, None, None, None) == si.SI_OK  # no rows
+
+
 def test_python_checks(si):
     torch = pytest.importorskip("torch")
     K = torch.zeros(1, 1, 2, 8, 64).to(torch.float8_e4m3fn)

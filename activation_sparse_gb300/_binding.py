@@ -588,13 +588,13 @@ class KV:
     """A key/value cache over the caller's tensors (owns the library handle
     and keeps references to the tensors)."""
 
-    def __init__(self, handle, K, V, table, lens, acc, dtype, k_scale=None, v_scale=None, block=1):
+    def __init__(self, handle, K, V, table, lens, acc, dtype=None, k_scale=None, v_scale=None, block=1):
         self._h = handle
         self.K, self.V, self.table, self.lens, self.acc = K, V, table, lens, acc
         self.k_scale, self.v_scale, self.block = k_scale, v_scale, block
         self.L, self.B, self.Hkv, self.n_slots, self.D = K.shape
         self.cap = table.shape[3] if table is not None else self.n_slots
-        self.dtype = dtype  # of q, k, v and out in the calls; of K and V too, where they are not codes
+        self.dtype = K.dtype if dtype is None else dtype  # of q, k, v and out in the calls; of K and V too, where they are not codes
 
     @property
     def handle(self):

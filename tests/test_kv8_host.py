@@ -130,6 +130,14 @@ def test_python_checks(si):
         si.si_token_logprobs(x.double())
 
 
+def test_a_handle_over_16_bits_needs_no_type(si):
+    """What wraps a handle by itself need not say what a cache in 16 bits is of."""
+    torch = pytest.importorskip("torch")
+    K, lens = torch.zeros(1, 1, 2, 8, 64, dtype=torch.float16), torch.zeros(1, 1, dtype=torch.int32)
+    kv = si.KV(None, K, K, None, lens, None)
+    assert kv.dtype == torch.float16 and kv.block == 1 and kv.k_scale is None and (kv.Hkv, kv.n_slots, kv.cap, kv.D) == (2, 8, 8, 64)
+
+
 # ------------------------------------------------- the definitions themselves
 
 def test_codes_by_hand():

@@ -2,7 +2,10 @@
 // rows a key. Lists are cut into tiles and dealt to CTAs as for the cache in 16
 // bits (attend.cu). Where several CTAs have parts of a list, the last of them to
 // be done joins the parts, in their order: the result does not depend on which
-// one that is.
+// one that is. The counters that say which one it is lie in the handle's scratch.
+// The launches take kCounterSets sets of them in turn and clear the next one's: what
+// a launch leaves in its own (two that ran at the same time, against the rules, or a
+// length that changed under one) does not outlive the call after it.
 //
 // A warp takes 32 keys of a tile (sixteen of heads above 128 elements) and keeps
 // its own softmax state. The products have the keys on the long side, so that up to eight query rows
@@ -66,14 +69,18 @@ struct Cfg8 {
     static constexpr int kOffFactor = kOffQ + kUnion;         // what a query row was divided by
     static constexpr int kOffState = kOffFactor + kRows * 4;  // [warp][row] {maximum, sum}
     static constexpr int kOffLast = kOffState + 4 * kRows * 8;  // [2] lists that this CTA joins
+    static constexpr int kOffCounters = kOffLast + 2 * 24;
     static constexpr int kOffPlan = kOffLast + 2 * 32;
     static constexpr int smem(int B) { return kOffPlan + Plan::words(B) * 4; }
 };
+
+constexpr unsigned kCounterSets = 4;  // a power of two: the launches are counted modulo 2^32
 
 // A list whose parts this CTA joins.
 struct LastOf {
     int on, b, group, first, last, behind;
 };
+static_assert(sizeof(LastOf) == 24);
 
 // The transposed 8 x 8 matrix of 16-bit elements that the warp's registers hold.
 __device__ __forceinline__ uint32_t transposed(uint32_t w) {
@@ -219,6 +226,7 @@ __global__ void __launch_bounds__(kThreads, Cfg8<DP, NT>::kCtas)
     float* const factor_s = reinterpret_cast<float*>(smem + Cfg::kOffFactor);
     float2* const state_s = reinterpret_cast<float2*>(smem + Cfg::kOffState);
     LastOf* const last_s = reinterpret_cast<LastOf*>(smem + Cfg::kOffLast);
+    unsigned* const counters_s = reinterpret_cast<unsigned*>(smem + Cfg::kOffCounters);  // place of this launch's set
     const Plan plan(reinterpret_cast<int*>(smem + Cfg::kOffPlan), P.c.B);
 
     const KvView& C = P.c;
@@ -230,6 +238,12 @@ __global__ void __launch_bounds__(kThreads, Cfg8<DP, NT>::kCtas)
     if (tid < 2) last_s[tid].on = 0;
     grid_dependency_wait();
     grid_launch_dependents();
+    if (tid == 32) {  // while the plan's lengths are on their way: how many launches this CTA has been in
+        const unsigned n = __ldcg(P.done + blockIdx.x);
+        atomicAdd(P.done + blockIdx.x, 1u);
+        *counters_s = (1 + n % kCounterSets) * gridDim.x;
+        P.done[(1 + (n + 1) % kCounterSets) * gridDim.x + blockIdx.x] = 0;
+    }
     make_plan<kThreads, kNarrowLeast, kNarrowPiece, KEYS>(C, T, groups, gridDim.x, plan, P.err, blockIdx.x == 0);
     const DealOf<KEYS> deal(plan, C.B, gridDim.x, kNarrowLeast);
     int x0, x1;
@@ -711,8 +725,9 @@ __global__ void __launch_bounds__(kThreads, Cfg8<DP, NT>::kCtas)
                 int first, last;
                 bool behind;
                 deal.ctas_of(b, rb + h * row_blocks, first, last, behind);
-                if (atomicAdd(P.done + first, 1u) == (unsigned)(last - first)) {
-                    P.done[first] = 0;  // for the next launch
+                unsigned* const there = P.done + *counters_s + first;
+                if (atomicAdd(there, 1u) == (unsigned)(last - first)) {
+                    *there = 0;
                     last_s[piece] = LastOf{1, b, rb + h * row_blocks, first, last, behind};
                 }
             }
@@ -752,7 +767,10 @@ constexpr int kMostCtas = 3;  // an SM, of any of the kernels
 
 }  // namespace
 
-int attend8_counters() { return kMostCtas * sm_count(); }
+int attend8_counters() {
+    const int sms = sm_count();
+    return sms < 1 ? 0 : (1 + kCounterSets) * kMostCtas * sms;
+}
 
 long long attend8_partial_floats(int D) {
     const long long ctas = (long long)sm_count() * (D <= 64 ? Cfg8<64, 2>::kCtas : D <= 128 ? Cfg8<128, 2>::kCtas : Cfg8<256, 2>::kCtas);

@@ -83,7 +83,7 @@ struct AttendParams {
     float* lse;               // attention: written (may be null); accumulate: read
     float* acc_out;           // accumulate (the cache's strides)
     float* part;              // attention: partial rows
-    unsigned* done;           // attention over codes: parts of a list that are there, by its first CTA; zero between launches
+    unsigned* done;           // attention over codes: launches by CTA, then sets of counters of a list's parts by its first CTA; zero at first
     unsigned* err;
 };
 // Scratch floats that launch_tree_attention needs at most for heads of D elements (0: cannot query the device).

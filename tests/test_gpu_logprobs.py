@@ -206,3 +206,68 @@ def test_logprobs_at_the_ends_of_the_temperature(si, dtype, temperature):
     x[2] = 0.25
     targets = np.tile(np.array([0, 5, 2900], np.int32), (4, 1))
     check(x.double().cpu().numpy(), targets, 8, temperature, run(si, x, t.from_numpy(targets).cuda(), 8, temperature))
+
+
+def best_of(x, K):
+    """Ids of the K largest of every row: NaN first, then by size, then by id."""
+    nan = np.isnan(x)
+    return np.stack([np.lexsort((np.arange(x.shape[1]), -np.where(n, 0.0, r), ~n))[:K] for r, n in zip(x, nan)])
+
+
+def check_best(si, g, K):
+    """The ids of K alternatives, and their log probabilities by the definition."""
+    x = g.double().cpu().numpy()
+    top, ids = run(si, g, None, K, entropy=False)[2:]
+    want = best_of(x, K)
+    assert (ids == want).all()
+    check(x, want.astype(np.int32), 0, 1.0, (top, None, None, None))
+    return ids
+
+
+@pytest.mark.parametrize("K", [1, 2])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("V", [9, 3001, 90000])
+def test_few_alternatives_of_odd_rows(si, K, dtype, V):
+    """One alternative has a way of its own: NaN, infinities, ties and signed zeros there, and with two."""
+    t = torch()
+    rng = np.random.default_rng(9)
+    x = rng.standard_normal((13, V)) * 2
+    big = float(t.finfo(tdtype(dtype)).max)
+    x[0, ::2] = -np.inf
+    x[1] = -np.inf
+    x[2] = -np.inf
+    x[2, V // 2] = 1.5
+    x[3, 3] = np.nan
+    x[4, V - 1] = np.inf
+    x[5] = -np.inf
+    x[5, 4] = np.nan
+    x[6] = -big
+    x[7, V - 2], x[7, V - 1] = np.nan, np.nan
+    x[8] = 2.25
+    x[9] = np.where(np.arange(V) % 2 == 0, -0.0, 0.0)
+    x[10] = -big
+    x[10, 1] = big
+    x[11, 2], x[11, V - 2] = np.inf, np.nan
+    x[12, V // 3], x[12, V - 1] = np.inf, np.inf
+    g = t.from_numpy(x).to(tdtype(dtype)).cuda()
+    check_best(si, g, K)
+    for n in (2, 3, 7, 8):  # a row alone: as many CTAs as a row can have
+        check_best(si, g[n:n + 1].contiguous(), K)
+
+
+@pytest.mark.parametrize("K", [1, 2])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_few_alternatives_that_tie(si, K, dtype):
+    """Equal largest logits in other threads, warps, batches and CTAs: the lowest id. Also where they are NaN or -inf."""
+    t = torch()
+    V = 150001
+    for first, step in ((0, 1), (1, 8), (7, 2048), (3, 8192), (18000, 19000), (149990, 1), (5, 512), (16, 16384)):
+        at = t.arange(first, min(V, first + 32 * step), step, device="cuda")
+        x = t.randn(1, V, device="cuda", generator=t.Generator("cuda").manual_seed(first)).clamp(-4, 4).to(tdtype(dtype))
+        for value in (5.0, float("nan"), float("inf")):
+            x[0, at] = value
+            assert check_best(si, x, K)[0].tolist() == at[:K].tolist()
+            for n in (40, 100, 700):  # fewer CTAs a row
+                assert (run(si, x.expand(n, V).contiguous(), None, K)[3] == at[:K].cpu().numpy()).all()
+    x = t.full((1, V), float("-inf"), dtype=tdtype(dtype), device="cuda")
+    assert run(si, x, None, K)[3].tolist() == [list(range(K))]

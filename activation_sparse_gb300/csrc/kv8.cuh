@@ -8,7 +8,6 @@
 
 namespace si {
 
-constexpr float kE4m3Max = 448.0f;  // 1.75 * 2^8
 constexpr int kScaleNaN = 255;
 
 // What a scale byte stands for, within the cache's limits (never a subnormal).
@@ -21,7 +20,7 @@ __device__ __forceinline__ float exponent_of(int byte, int lo, int hi) {
     return byte == kScaleNaN ? __int_as_float(0x7FC00000) : (float)(min(max(byte, lo), hi) - 127);
 }
 
-// The scale byte of a row whose largest magnitude is top: the least power of two whose 448-fold reaches it.
+// The scale byte of a row whose largest magnitude is top: the least power of two whose 448-fold (1.75 * 2^8) reaches it.
 __device__ __forceinline__ int scale_byte_for(float top, int lo, int hi) {
     const int bits = __float_as_int(top);  // >= 0
     if (bits >= 0x7F800000) return kScaleNaN;
@@ -36,14 +35,7 @@ __device__ __forceinline__ uint32_t code2(float a, float b) {
     return w;
 }
 
-// Two codes (the low 16 bits) as two fp16, exactly.
-__device__ __forceinline__ uint32_t halves(uint16_t codes) {
-    uint32_t w;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(w) : "h"(codes));
-    return w;
-}
-
-// The four codes of a word that lie at bytes 0, 1 and 2, 3.
+// The four codes of a word as fp16, exactly: bytes 0, 1 and 2, 3.
 __device__ __forceinline__ void halves4(uint32_t w, uint32_t& lo, uint32_t& hi) {
     asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
         "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"

@@ -555,8 +555,8 @@ int row_warps(int R) { return R <= 16 ? 1 : 2; }
 // rows (it is not built for heads of more than 128 elements). 8 sequences of up
 // to 8192 keys, 8 heads of 128, here / there: 16 rows 42.8 / 39.8 us, 20 rows 63
 // / 40, 64 rows 114 / 43; one of 30000 keys, heads of 64: 16 rows 20.0 / 23.3 us,
-// 20 rows 30 / 24. Codes, 16 rows: 16 sequences of up to 4097 keys, 8 heads of 128, 35.8 / 52.5; 8 of up to 8192 34.8 /
-// 49.7; one of 131071 76 / 137; 20 rows 65 / 52.7 and 51.6 / 49.8.
+// 20 rows 30 / 24. Codes, 16 rows: 16 sequences of up to 4097 keys, 8 heads of 128, 35.9 / 52.2; 8 of up to 8192 35.6 /
+// 49.8; one of 131071 77 / 138; 20 rows 63.0 / 52.3 and 52.1 / 49.6.
 bool many_rows(int D, int R) { return R > 16 && D <= 128; }
 
 template <int DP, int RB, bool FP16>

@@ -25,10 +25,10 @@
 // element below 2^15, so that what lies up to 2^29 below it is exact.
 //
 // Bound by memory where lists are long: one token of 32 heads over 131071 keys
-// of 8 heads of 128 takes 53 us, 5.2 TB/s, 0.77 of what a plain copy reaches;
+// of 8 heads of 128 takes 52 us, 5.3 TB/s, 0.79 of what a plain copy reaches;
 // the tiles themselves go by at 6.5 TB/s, 4 us pass before the first one is
 // there and 5 at the end (slowest CTA, parts out, join). 1000 keys, heads of
-// 64: 8.9 us, latency alone (lengths, slots, keys, parts out, parts in). With
+// 64: 9.2 us, latency alone (lengths, slots, keys, parts out, parts in). With
 // sixteen keys a warp and four CTAs an SM the long list took 75 us, most of it
 // because the join was a launch of its own, whose blocks left the register file
 // in pieces: the next call's last CTA did not fit beside the others and ran
@@ -47,8 +47,8 @@ constexpr int kThreads = 128;  // four warps
 // fp16 weights, and a maximum that may be outgrown by 2^kLazy before anything is rescaled.
 using Wt = Weights<true, true>;
 
-// Two sixteens of keys a warp / one, the rest alike: 131071 keys, heads of 128, 52.8 / 66.9 us, sixteen sequences of up to
-// 4097 26.1 / 31.4; heads of 256, 4 cache heads 62.6 / 70.4, sixteen sequences 53.5 / 40.4 (two leave one CTA an SM).
+// Two sixteens of keys a warp / one, the rest alike: 131071 keys, heads of 128, 51.8 / 66.9 us, sixteen sequences of up to
+// 4097 25.8 / 30.9; heads of 256, 4 cache heads 63.2 / 70.2, sixteen sequences 55.1 / 39.9 (two leave one CTA an SM).
 template <int DP, int NT>
 struct Cfg8 {
     static constexpr int kRows = 8 * NT;                      // query rows of a block
@@ -777,8 +777,8 @@ long long attend8_partial_floats(int D) {
     return ctas * 2 * part_floats(16, D <= 64 ? 64 : D <= 128 ? 128 : 256);
 }
 
-// Blocks of eight rows where a key meets no more, else of sixteen. Four rows in blocks of eight / sixteen: 131071 keys 52.8 /
-// 61.8 us, sixteen sequences 26.1 / 30.9.
+// Blocks of eight rows where a key meets no more, else of sixteen. Four rows in blocks of eight / sixteen: 131071 keys 51.8 /
+// 63.0 us, sixteen sequences 25.8 / 31.6.
 cudaError_t launch_tree_attention8(const AttendParams& P, cudaStream_t st) {
     return P.T * P.G <= 8 ? launch_heads<1>(P, st) : launch_heads<2>(P, st);
 }

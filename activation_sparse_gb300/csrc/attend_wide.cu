@@ -24,7 +24,7 @@
 // where a copy takes four, and was no faster). More than 128 rows go through
 // one CTA an SM with two blocks, which copies a tile once; with one block two
 // CTAs share the SM. 8 trees of 64 nodes x 32 heads over up to 8192 keys of 8
-// heads of 128: 72 us with two blocks, 540 TFLOP/s (79 with one block and every
+// heads of 128: 71 us with two blocks, 550 TFLOP/s (79 with one block and every
 // tile copied twice); the tensor pipe is 33 % busy, what bounds it is the
 // softmax's instructions and the waits between the roles. 64 keys take 1.7 us;
 // a list costs some 6 us beside (queries in, rows out).
@@ -36,12 +36,12 @@
 // Over a cache of e4m3 codes the copying warps copy the codes as they are, tiles
 // ahead, and turn what they copied themselves into elements of the type of q,
 // scale and all (exactly, see si_kv_create_e4m3): the rest of the kernel does
-// not know. That work is on the way of every tile: the trees above take 84 us
-// (bf16 93), of which the products wait for keys 13 %; the copying warps are
+// not know. That work is on the way of every tile: the trees above take 81 us
+// (bf16 90), of which the products wait for keys 13 %; the copying warps are
 // busy nine tenths of a tile's time, with some 400 instructions that the caches
 // of instructions cannot hold next to the softmax's. Eight copying warps instead
-// of four: 87 and 90 us; a tile's codes held in registers instead of shared
-// memory: 85 and 91 with two blocks, but 60 instead of 50 with one (T = 16).
+// of four: 3 us more and 3 less; a tile's codes held in registers instead of shared
+// memory: 1 more and 2 less with two blocks, but 60 instead of 50 us with one (T = 16).
 // Every write to shared memory is an ordinary one; the issuing warp's proxy
 // fence, after the barrier that announces it, lets the tensor cores see it. All
 // waits are bounded; TMEM is always released.

@@ -136,10 +136,11 @@ __device__ __forceinline__ void gather(Shared& S, unsigned long long list, int w
 // 2048 rows of 131072 bf16 take 88 us, 6.1 TB/s, 0.91 of what a plain copy
 // reaches (fp32 164, 6.5 TB/s; with eight alternatives 102, with 32 128: every
 // thread looks for its largest once more, and the candidates); one row of 32768
-// fp32 8, the host call; 128 rows of 50001 with four alternatives 12.4, of which
-// the alternatives are 4.6: sorts and merges of a block's threads, and a cluster
-// barrier. (Where the search for the place of a maximum that grew is done at
-// once, in every batch some lane of a warp has one: 124 us for 96.)
+// fp32 with eight alternatives 5.4 on the GPU (of 262144, 7.8), 7.6 to 9 with the
+// host's call; 128 rows of 50001 with four alternatives 12.4, of which the
+// alternatives are 4.5: sorts and merges of a block's threads, and a cluster
+// barrier. (Where the search for the place of a maximum that grew is done at once,
+// in every batch some lane of a warp has one: 124 us for 96.)
 template <int DTYPE>
 __global__ void __launch_bounds__(kThreads, 4) k_token_logprobs(const __grid_constant__ LogprobsParams P) {
     using U = Unit<DTYPE>;
@@ -405,8 +406,8 @@ cudaError_t launch_token_logprobs(const LogprobsParams& P, cudaStream_t st) {
     if (sms < 1) return cudaErrorInvalidDevice;
     const long long bytes = (long long)P.V * (P.dtype == SI_FP32 ? 4 : 2);
     // CTAs of a row: as many as all rows together fill the GPU with, four an SM, where each has a unit a thread. 128 rows of
-    // 50001 with two / four / eight: 15.2 / 13.2 / 18.9 us; 2048 of 131072 with one / two: 96 / 103. (Eight units a
-    // thread under way and three CTAs an SM: 109; blocks of 128 threads: 92.)
+    // 50001 with one / two / four / eight: 19.4 / 15.0 / 12.4 / 17.7 us; 2048 of 131072 with one / two: 88.3 / 100.3. (Eight
+    // units a thread under way and three CTAs an SM: 14.3 and 132; blocks of 128 threads, eight an SM: 12.3 and 88.8.)
     int cs = 1;
     while (cs < kMostCtas && (long long)P.N * cs * 2 <= 4ll * sms && bytes / (2 * cs) >= 16 * kThreads) cs *= 2;
     cudaLaunchConfig_t cfg = {};

@@ -33,11 +33,14 @@ struct Cfg8 {
 // the short one, a thread sums its keys' weights over the rows in registers,
 // and a key belongs to one warp, which also copies it, its scale and its old
 // weight. A tile's codes become fp16 once, in registers, for all of the rows.
-// 8 sequences of up to 16384 keys, 8 heads of 128, four nodes of 32 heads: 32 us,
-// 2.6 TB/s, 0.39 of what a plain copy reaches (36 us over 16 bits). Bound by issue: a
-// warp has some 690 instructions for its 32 keys and sixteen rows, and 16 warps
-// fit an SM. Two stages and four CTAs an SM / three and three: 32.1 / 35.5 us;
-// sixteen keys a warp, four stages and four CTAs: 36.8.
+// 8 sequences of up to 16384 keys, 8 heads of 128, four nodes of 32 heads: 31 us,
+// 2.6 TB/s, 0.39 of what a plain copy reaches (36 us over 16 bits). Bound by latency:
+// a warp has some 690 instructions for its 32 keys and sixteen rows, most of them in
+// chains (codes in, products, exponentials), and the 16 warps that fit an SM fill 40 %
+// of the issue slots. Two stages and four CTAs an SM / three and three: 32.1 / 35.5
+// us; sixteen keys a warp, four stages and four CTAs: 36.8.
+// More than 64 counted rows are staged anew, in blocks of 64, for every tile: 64
+// rows (16 nodes) of the sequences above take 62 us, 128 173 and 252 315.
 template <int DP>
 __global__ void __launch_bounds__(kThreads, Cfg8<DP>::kCtas) k_kv_accumulate8(const __grid_constant__ AttendParams P) {
     using Cfg = Cfg8<DP>;

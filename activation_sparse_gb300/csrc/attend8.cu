@@ -19,8 +19,10 @@
 // of two of its row's own: the largest weight times scale that the row has met,
 // which the output is rescaled by when it grows, as it is by the softmax's maximum.
 // (A unit for all rows, from the scales alone, lost the keys that a row weighs beside
-// a large scale that it does not. The rows' own cost 2 to 3 % at sixteen rows a key,
-// 34.5 / 35.4 us for sixteen sequences of up to 4097, and less than 1 % up to eight.)
+// a large scale that it does not. The rows' own cost 4 % at sixteen rows a key, 34.5 /
+// 35.9 us for sixteen sequences of up to 4097, and 1 % up to eight.) Warps and parts
+// are joined likewise: a part whose weights are below fp32's range beside another's
+// may have scales that make up for it.
 // Queries go in as fp16: bf16 rows times the power of two that brings their largest
 // element below 2^15, so that what lies up to 2^29 below it is exact.
 //
@@ -67,8 +69,8 @@ struct Cfg8 {
     static constexpr int kJoin = (NT == 1 ? 12 : 8) * kJoinRow * 4;  // three warps' rows of up to four, or one's of eight
     static constexpr int kUnion = kJoin > kRows * kQRow ? kJoin : kRows * kQRow;
     static constexpr int kOffFactor = kOffQ + kUnion;         // what a query row was divided by
-    static constexpr int kOffState = kOffFactor + kRows * 4;  // [warp][row] {maximum, sum}
-    static constexpr int kOffLast = kOffState + 4 * kRows * 8;  // [2] lists that this CTA joins
+    static constexpr int kOffState = kOffFactor + kRows * 4;  // [warp][row] {maximum, sum, base}
+    static constexpr int kOffLast = kOffState + 4 * kRows * 16;  // [2] lists that this CTA joins
     static constexpr int kOffCounters = kOffLast + 2 * 24;
     static constexpr int kOffPlan = kOffLast + 2 * 32;
     static constexpr int smem(int B) { return kOffPlan + Plan::words(B) * 4; }
@@ -89,6 +91,12 @@ __device__ __forceinline__ uint32_t transposed(uint32_t w) {
     return r;
 }
 
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
+    return v;
+}
+
 // over the eight lanes with the same lane % 4
 __device__ __forceinline__ float column_max(float v) {
     v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 4));
@@ -103,8 +111,8 @@ __device__ __forceinline__ float column_sum(float v) {
 
 __device__ __forceinline__ float shift_of(float m) { return m == -INFINITY ? 0.0f : m; }
 
-// Where the parts of lists lie: for each of a CTA's two pieces [CTA][row][DP] outputs, then [CTA][row] {maximum, sum},
-// with as many rows as a block can have in this call. A list's parts are neighbours, but for the first one where
+// Where the parts of lists lie: for each of a CTA's two pieces [CTA][row][DP] outputs, then [CTA][row] {maximum, sum}, then
+// [CTA][row] bases (all three in 16 bytes: 2 us more where lists have sixty parts), with as many rows as a block can have in this call. A list's parts are neighbours, but for the first one where
 // another list comes before it in its CTA.
 template <int DP, int RB>
 struct Parts {
@@ -115,6 +123,9 @@ struct Parts {
     __device__ __forceinline__ float2* state(int cta, int piece) const {
         return reinterpret_cast<float2*>(at + 2ll * ctas * rows * DP) + (piece * ctas + cta) * rows;
     }
+    __device__ __forceinline__ float* base(int cta, int piece) const {
+        return at + 2ll * ctas * rows * (DP + 2) + (piece * ctas + cta) * rows;
+    }
 };
 
 // Joins a list's parts: the CTA's ring is empty and takes them, as many at once as fit.
@@ -123,7 +134,7 @@ __device__ void join_parts(const AttendParams& P, const Plan& plan, int row_bloc
     constexpr int CHUNK = 64, QUADS = DP / 4, ITEMS = RB * QUADS / kThreads > 0 ? RB * QUADS / kThreads : 1;
     constexpr int kOffRows = (CHUNK + 4) * RB * 4;
     float* const weight_s = reinterpret_cast<float*>(smem);                    // [part of a chunk][row]
-    float4* const state_s = reinterpret_cast<float4*>(weight_s + CHUNK * RB);  // [row] maximum, sum, what the sums so far are multiplied by
+    float4* const state_s = reinterpret_cast<float4*>(weight_s + CHUNK * RB);  // [row] maximum, sum, base, what the rows so far are multiplied by
     float4* const rows_s = reinterpret_cast<float4*>(smem + kOffRows);         // [part of a chunk][row][DP]
     const KvView& C = P.c;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -134,7 +145,7 @@ __device__ void join_parts(const AttendParams& P, const Plan& plan, int row_bloc
     const Parts<DP, RB> parts(P);
     auto piece_of = [&](int c) { return c == l.first && l.behind ? 1 : 0; };
     __syncthreads();
-    if (tid < RB) state_s[tid] = make_float4(-INFINITY, 0.0f, 0.0f, 0.0f);
+    if (tid < RB) state_s[tid] = make_float4(-INFINITY, 0.0f, -INFINITY, 0.0f);
     float4 acc[ITEMS];
 #pragma unroll
     for (int i = 0; i < ITEMS; ++i) acc[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
@@ -142,12 +153,16 @@ __device__ void join_parts(const AttendParams& P, const Plan& plan, int row_bloc
         const int n = min(chunk, l.last - c0 + 1);
         __syncthreads();
         float2 st[2];
+        float bs[2];
         auto load_state = [&](int r) {
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                st[i] = make_float2(-INFINITY, 0.0f);
+                st[i] = make_float2(-INFINITY, 0.0f), bs[i] = 0.0f;
                 const int c = c0 + lane + 32 * i;
-                if (r < rows && lane + 32 * i < n) st[i] = __ldcg(parts.state(c, piece_of(c)) + r);
+                if (r < rows && lane + 32 * i < n) {
+                    st[i] = __ldcg(parts.state(c, piece_of(c)) + r);
+                    bs[i] = __ldcg(parts.base(c, piece_of(c)) + r);
+                }
             }
         };
         load_state(warp);  // ahead of the copies, which it would queue behind
@@ -162,23 +177,20 @@ __device__ void join_parts(const AttendParams& P, const Plan& plan, int row_bloc
         cp_commit();
         for (int r = warp; r < rows; r += 4) {
             if (r != warp) load_state(r);
-            const float m[2] = {st[0].x, st[1].x}, s[2] = {st[0].y, st[1].y};
             const float4 old = state_s[r];
-            float top = fmaxf(m[0], m[1]);
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-            top = fmaxf(top, old.x);
-            const float shift = shift_of(top), keep = ex2((old.x - shift) * c2);
+            const float top = fmaxf(warp_max(fmaxf(st[0].x, st[1].x)), old.x), shift = shift_of(top);
+            // The rows are brought to the largest base, beside the maximum: what a part's weights lose the scales may make up for.
+            const float d[2] = {(st[0].x - shift) * c2, (st[1].x - shift) * c2}, d_old = (old.x - shift) * c2;
+            const float base = shift_of(fmaxf(warp_max(fmaxf(d[0] + bs[0], d[1] + bs[1])), d_old + old.z));
             float sum = 0.0f;
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                const float w = ex2((m[i] - shift) * c2);
-                if (lane + 32 * i < n) weight_s[(lane + 32 * i) * RB + r] = w;
-                sum += w * s[i];
+                if (lane + 32 * i < n) weight_s[(lane + 32 * i) * RB + r] = ex2(d[i] + (bs[i] - base));
+                sum += ex2(d[i]) * st[i].y;
             }
             sum = warp_sum(sum);
             __syncwarp();
-            if (lane == 0) state_s[r] = make_float4(top, old.y * keep + sum, keep, 0.0f);
+            if (lane == 0) state_s[r] = make_float4(top, old.y * ex2(d_old) + sum, base, ex2(d_old + (old.z - base)));
         }
         cp_wait<0>();
         __syncthreads();
@@ -186,7 +198,7 @@ __device__ void join_parts(const AttendParams& P, const Plan& plan, int row_bloc
         for (int i = 0; i < ITEMS; ++i) {
             const int item = tid + i * kThreads, r = item / QUADS;
             if (item >= quads) continue;
-            const float keep = state_s[r].z;
+            const float keep = state_s[r].w;
             acc[i].x *= keep, acc[i].y *= keep, acc[i].z *= keep, acc[i].w *= keep;
 #pragma unroll 4
             for (int c = 0; c < n; ++c) {
@@ -203,10 +215,10 @@ __device__ void join_parts(const AttendParams& P, const Plan& plan, int row_bloc
         const float4 st = state_s[r];
         const int t = div_of(row0 + r, G), g = row0 + r - t * G;
         const bool empty = plan.tot[l.b] == 0 || word_of(P.mask, P.T, l.b, t) == 0 || st.y == 0.0f;
-        const float inv = empty ? 0.0f : 1.0f / st.y;
+        const float inv = empty ? 0.0f : 1.0f / st.y, power = ex2(st.z) * Wt::kDown;
         const long long at = ((long long)l.b * P.T + t) * P.Hq + h * G + g;
         uint2 w = make_uint2(0, 0);
-        const float4 a = make_float4(acc[i].x * inv, acc[i].y * inv, acc[i].z * inv, acc[i].w * inv);
+        const float4 a = make_float4(acc[i].x * inv * power, acc[i].y * inv * power, acc[i].z * inv * power, acc[i].w * inv * power);
         if (!empty) w = C.fp16 ? make_uint2(pack<true>(a.x, a.y), pack<true>(a.z, a.w)) : make_uint2(pack<false>(a.x, a.y), pack<false>(a.z, a.w));
         *reinterpret_cast<uint2*>(static_cast<uint16_t*>(P.out) + at * D + q * 4) = w;
         if (P.lse && q == 0) P.lse[at] = empty ? -INFINITY : lse_of(st.x, P.scale, st.y);
@@ -224,7 +236,7 @@ __global__ void __launch_bounds__(kThreads, Cfg8<DP, NT>::kCtas)
     extern __shared__ __align__(128) uint8_t smem[];
     uint8_t* const q_s = smem + Cfg::kOffQ;
     float* const factor_s = reinterpret_cast<float*>(smem + Cfg::kOffFactor);
-    float2* const state_s = reinterpret_cast<float2*>(smem + Cfg::kOffState);
+    float4* const state_s = reinterpret_cast<float4*>(smem + Cfg::kOffState);
     LastOf* const last_s = reinterpret_cast<LastOf*>(smem + Cfg::kOffLast);
     unsigned* const counters_s = reinterpret_cast<unsigned*>(smem + Cfg::kOffCounters);  // place of this launch's set
     const Plan plan(reinterpret_cast<int*>(smem + Cfg::kOffPlan), P.c.B);
@@ -617,38 +629,44 @@ __global__ void __launch_bounds__(kThreads, Cfg8<DP, NT>::kCtas)
         }
         if (x < x1) load_queries(a);  // of the next list: they come while this one is finished
 
-        // Join the warps: maxima and sums, then output rows in warp order, through the place of this list's queries,
+        // Join the warps: maxima, sums and bases, then output rows in warp order, through the place of this list's queries,
         // which are no longer needed: in the ring the next list's copies are in flight.
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 sum[n][e] = column_sum(sum[n][e]);
-                if (g == 0) state_s[warp * RB + n * 8 + 2 * c + e] = make_float2(ref[n][e], sum[n][e]);
+                if (g == 0) state_s[warp * RB + n * 8 + 2 * c + e] = make_float4(ref[n][e], sum[n][e], base[n][e], 0.0f);
             }
+        __syncthreads();
+        if (tid < RB) {  // a thread a row: what the row has, and what each warp's output is multiplied by
+            float4 it[4];
+            float top = -INFINITY, all = 0.0f, most = -INFINITY, d[4];
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+                it[w] = state_s[w * RB + tid];
+                top = fmaxf(top, it[w].x);
+            }
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+                d[w] = (it[w].x - shift_of(top)) * c2;
+                all += it[w].y * ex2(d[w]);
+                most = fmaxf(most, d[w] + it[w].z);
+            }
+            most = shift_of(most);
+#pragma unroll
+            for (int w = 0; w < 4; ++w) state_s[w * RB + tid].w = ex2(d[w] + (it[w].z - most));
+            *reinterpret_cast<float2*>(state_s + tid) = make_float2(top, all * Wt::kDown);
+            state_s[tid].z = most;
+        }
         __syncthreads();
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                float top = -INFINITY, all = 0.0f;
-                float2 st[4];
+                const float f = state_s[warp * RB + n * 8 + 2 * c + e].w;
 #pragma unroll
-                for (int w = 0; w < 4; ++w) {
-                    st[w] = state_s[w * RB + n * 8 + 2 * c + e];
-                    top = fmaxf(top, st[w].x);
-                }
-                const float sh = shift_of(top);
-#pragma unroll
-                for (int w = 0; w < 4; ++w) all += st[w].y * ex2((st[w].x - sh) * c2);
-                const float f = ex2((ref[n][e] - sh) * c2) * Wt::kDown, power = ex2(base[n][e]);
-#pragma unroll
-                for (int i = 0; i < KD; ++i) {
-                    o[i][n][e] = o[i][n][e] * f * power;
-                    o[i][n][e + 2] = o[i][n][e + 2] * f * power;
-                }
-                ref[n][e] = top;
-                sum[n][e] = all * Wt::kDown;
+                for (int i = 0; i < KD; ++i) o[i][n][e] *= f, o[i][n][e + 2] *= f;
             }
         // (All at once where the rows are few, or the ring is idle: after the CTA's last tile.)
         float* const join_s = reinterpret_cast<float*>(x < x1 ? q_s : smem);
@@ -690,18 +708,19 @@ __global__ void __launch_bounds__(kThreads, Cfg8<DP, NT>::kCtas)
                 for (int e = 0; e < 2; ++e) {
                     const int row = rb * RB + n * 8 + 2 * c + e;
                     if (row >= R) continue;
-                    const bool empty = word[n][e] == 0 || sum[n][e] == 0.0f;
-                    const float inv = empty ? 0.0f : 1.0f / sum[n][e];
+                    const float4 it = state_s[n * 8 + 2 * c + e];
+                    const bool empty = word[n][e] == 0 || it.y == 0.0f;
+                    const float inv = empty ? 0.0f : 1.0f / it.y, power = ex2(it.z) * Wt::kDown;
                     const int t = div_of(row, G), gq = row - t * G;
                     const long long at = ((long long)b * T + t) * P.Hq + h * G + gq;
                     uint16_t* dst = static_cast<uint16_t*>(P.out) + at * D + 2 * g;
 #pragma unroll
                     for (int i = 0; i < KD; ++i) {
-                        const float p = o[i][n][e] * inv, q = o[i][n][e + 2] * inv;
+                        const float p = o[i][n][e] * inv * power, q = o[i][n][e + 2] * inv * power;
                         if (i * 16 < D)
                             *reinterpret_cast<uint32_t*>(dst + i * 16) = empty ? 0u : C.fp16 ? pack<true>(p, q) : pack<false>(p, q);
                     }
-                    if (P.lse && g == 0) P.lse[at] = empty ? -INFINITY : lse_of(ref[n][e], P.scale, sum[n][e]);
+                    if (P.lse && g == 0) P.lse[at] = empty ? -INFINITY : lse_of(it.x, P.scale, it.y);
                 }
         } else {
             const int piece = segment ? 1 : 0;
@@ -717,7 +736,11 @@ __global__ void __launch_bounds__(kThreads, Cfg8<DP, NT>::kCtas)
                     for (int i = 0; i < KD; ++i)
                         if (i * 16 < D)
                             *reinterpret_cast<float2*>(part + r * DP + i * 16 + 2 * g) = make_float2(o[i][n][e], o[i][n][e + 2]);
-                    if (g == 0) parts.state(blockIdx.x, piece)[r] = make_float2(ref[n][e], sum[n][e]);
+                    if (g == 0) {
+                        const float4 it = state_s[r];
+                        parts.state(blockIdx.x, piece)[r] = make_float2(it.x, it.y);
+                        parts.base(blockIdx.x, piece)[r] = it.z;
+                    }
                 }
             __threadfence();
             __syncwarp();
@@ -774,7 +797,7 @@ int attend8_counters() {
 
 long long attend8_partial_floats(int D) {
     const long long ctas = (long long)sm_count() * (D <= 64 ? Cfg8<64, 2>::kCtas : D <= 128 ? Cfg8<128, 2>::kCtas : Cfg8<256, 2>::kCtas);
-    return ctas * 2 * part_floats(16, D <= 64 ? 64 : D <= 128 ? 128 : 256);
+    return ctas * 2 * 16 * ((D <= 64 ? 64 : D <= 128 ? 128 : 256) + 3);
 }
 
 // Blocks of eight rows where a key meets no more, else of sixteen. Four rows in blocks of eight / sixteen: 131071 keys 51.8 /

@@ -3,7 +3,8 @@
 Tolerances. With n keys, p_j the softmax weights and 2^e_j the values' scales: up to 16 rows a key, or above 128
 elements, a weight times its value's scale goes into the product as two fp16 terms relative to the largest that its row
 has met: the terms lose 2^-22 of it, or 2^-35 of the largest, times a code of up to 448. Else it is rounded once to the
-type, relative to the weight (fp16: 2^-35 of the largest weight at least). Scores and output as in test_gpu_kv8.py; the
+type, relative to the weight (fp16: 2^-35 of the largest weight at least), an fp32 number relative to the row's largest, so
+that those below 2^-126 of it are 0. Scores and output as in test_gpu_kv8.py; the
 score error is that of the keys which have weight.
 """
 import math
@@ -27,12 +28,13 @@ def si():
 
 
 def weighed(c, q, words, scale):
-    """Of every row: the largest weight times its value's scale, and the largest value among keys that have weight."""
+    """Of every row: the largest weight times its value's scale, the largest value among keys that have weight, and what the
+    weights below fp32's normal range give."""
     qh, (K, V, table) = host(q), c.args()
     B, T, Hq, D = qh.shape
     G = Hq // K.shape[1]
     byte = c.v_scale[c.layer].cpu().numpy()
-    top, size = np.zeros((B, T, Hq, 1)), np.zeros((B, T, Hq, 1))
+    top, size, least = np.zeros((B, T, Hq, 1)), np.zeros((B, T, Hq, 1)), np.zeros((B, T, Hq, D))
     for b in range(B):
         n = int(c.lens_h[b])
         for h in range(K.shape[1]):
@@ -43,10 +45,12 @@ def weighed(c, q, words, scale):
                 for g in range(h * G, h * G + G if vis.any() else 0):
                     z = scale * (K[b, h, at[vis]] @ qh[b, t, g])
                     p = np.exp(z - z.max())
+                    low = p < 2.0 ** -126
                     p /= p.sum()
+                    least[b, t, g] = p[low] @ np.abs(V[b, h, at[vis]][low])
                     top[b, t, g] = (p * unit[vis]).max()
                     size[b, t, g] = np.abs(V[b, h, at[vis]])[p > 2.0 ** -100].max()
-    return top, size
+    return top, size, least
 
 
 def check(c, q, out, lse, words, scale, light=None):
@@ -55,12 +59,12 @@ def check(c, q, out, lse, words, scale, light=None):
     want, lse_w, mag = ref.attend(host(q), K, V, table, c.lens_h, words, scale)
     e = score_error(host(q), K if light is None else np.where(light[..., None], 0, K), q.shape[-1], scale) + 2.0 ** -19
     u, n = ref.U[c.dtype], max(c.lens_h) + c.T
-    top, size = weighed(c, q, words, scale)
+    top, size, least = weighed(c, q, words, scale)
     few = q.shape[1] * q.shape[2] // K.shape[1] <= 16 or q.shape[-1] > 128
     if few:
         weights = 2.0 ** -21 * mag + n * 448 * 2.0 ** -35 * top
     else:
-        weights = u * mag + (n * 2.0 ** -35 * size if c.dtype == "fp16" else 0.0)
+        weights = u * mag + least + (n * 2.0 ** -35 * size if c.dtype == "fp16" else 0.0)
     got, lg, empty = host(out), host(lse), words == 0
     assert np.isfinite(got).all()
     bad = np.abs(got - want) - (u * np.abs(want) + weights + 2 * e * mag + (2.0 ** -24 if c.dtype == "fp16" else 1e-37))
@@ -164,3 +168,31 @@ def test_queries_near_the_types_largest(si, T, Hq, Hkv, D):
     assert bool(got[0][1].isfinite().all())
     for x, y in zip(*got):
         assert t.equal(x, y)
+
+
+@pytest.mark.parametrize("falling", [False, True])
+@pytest.mark.parametrize("T,Hq,Hkv,D", [(1, 4, 2, 64), (2, 8, 2, 128), (4, 8, 2, 128), (2, 4, 2, 256), (20, 8, 2, 128)])
+def test_scores_that_rise_as_scales_fall_along_the_list(si, T, Hq, Hkv, D, falling):
+    """Every few tiles a score outgrows the ones before it by little while the scales fall as much, or the other way round:
+    what has been summed is rescaled over and over, and no key's part is lost."""
+    t = torch()
+    c = Cache8(si, 65, [5200, 900], T, Hkv, D, "bf16", spread=0.0)
+    q, words, mask = make_rows(c, T, Hq, D, "bf16", "none" if T == 1 else "tree")
+    q *= 0.125
+    q[..., 0] = 1.0
+    # scores of 0.5 x, x the codes from -448 to 448 in order, and scales of about 2^-(0.5 x log2(e) / 5): 2^+-65
+    codes = np.sort(ref8.CODES[~np.isnan(ref8.CODES)])
+    c.K.view(t.uint8)[..., 1:] = gpu(ref8.encode(c.rng.standard_normal(c.K.shape[:4] + (D - 1,)) * 0.25))
+    c.V.view(t.uint8).copy_(gpu(ref8.encode(c.rng.standard_normal(c.V.shape) * 100.0)))
+    c.k_scale.fill_(127)
+    x = np.zeros(c.K.shape[:4])
+    for b, n in enumerate(c.lens_h + T):
+        rise = codes[np.linspace(0, len(codes) - 1, n).astype(int)] / 5  # -89.6 .. 89.6
+        for h in range(Hkv):
+            x[0, b, h, c.table_h[0, b, h, :n]] = rise[::-1] if falling else rise
+    x = ref8.CODES[ref8.encode(x)]
+    c.K.view(t.uint8)[..., 0] = gpu(ref8.encode(x))
+    c.v_scale.copy_(gpu((120 - np.round(0.5 * x * math.log2(math.e))).astype(np.uint8)))
+    out, lse = t.empty_like(q), t.empty(q.shape[:3], device="cuda")
+    si.si_tree_attention(c.kv, q, out, mask=mask, lse=lse, scale=0.5)
+    check(c, q, out, lse, words, 0.5)

@@ -19,18 +19,18 @@
 // of two of its row's own: the largest weight times scale that the row has met,
 // which the output is rescaled by when it grows, as it is by the softmax's maximum.
 // (A unit for all rows, from the scales alone, lost the keys that a row weighs beside
-// a large scale that it does not. The rows' own cost 4 % at sixteen rows a key, 34.5 /
-// 35.9 us for sixteen sequences of up to 4097, and 1 % up to eight.) Warps and parts
+// a large scale that it does not. The rows' own cost 5 % at sixteen rows a key, 34.5 /
+// 36.5 us for sixteen sequences of up to 4097, and 1 % up to eight.) Warps and parts
 // are joined likewise: a part whose weights are below fp32's range beside another's
 // may have scales that make up for it.
 // Queries go in as fp16: bf16 rows times the power of two that brings their largest
 // element below 2^15, so that what lies up to 2^29 below it is exact.
 //
 // Bound by memory where lists are long: one token of 32 heads over 131071 keys
-// of 8 heads of 128 takes 52 us, 5.3 TB/s, 0.79 of what a plain copy reaches;
+// of 8 heads of 128 takes 52.5 us, 5.2 TB/s, 0.78 of what a plain copy reaches;
 // the tiles themselves go by at 6.5 TB/s, 4 us pass before the first one is
 // there and 5 at the end (slowest CTA, parts out, join). 1000 keys, heads of
-// 64: 9.2 us, latency alone (lengths, slots, keys, parts out, parts in). With
+// 64: 9.3 us, latency alone (lengths, slots, keys, parts out, parts in). With
 // sixteen keys a warp and four CTAs an SM the long list took 75 us, most of it
 // because the join was a launch of its own, whose blocks left the register file
 // in pieces: the next call's last CTA did not fit beside the others and ran
